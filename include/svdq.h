@@ -1,7 +1,8 @@
 /*
  * svdq.h -- C ABI of libsvdq, an MI355X (gfx950) implementation of the
  * SVDQuant W4A4 linear layer with its 16-bit low-rank branch, and of the
- * AWQ-style W4A16 linear used for modulation layers.
+ * AWQ-style W4A16 linear used for modulation layers; with a 4-bit key/value
+ * cache and its attention, and an expert layer of W4A16 linears.
  *
  * Method.  "Bringing Nunchaku 4-bit diffusion inference to Diffusers"
  * (Vietnamese edition, section "Bối cảnh: SVDQuant và Nunchaku"; Korean
@@ -383,6 +384,66 @@ svdq_status_t svdq_debug_group_sums_codes(const svdq_weights_t *w, const uint8_t
                                           int m0, int mcount, int n0, int ncount, int32_t *P,
                                           void *workspace, size_t ws_bytes, void *hip_stream);
 
+/* ================================================= 4-bit key/value cache
+ * The key/value cache of a language model's attention, held in MXFP4 (the
+ * format of the FP4 variant above: 32 consecutive channels of one token and
+ * head share a power-of-two scale), and the attention of new tokens over it.
+ *
+ * The cache is one device buffer of svdq_kv4_cache_bytes bytes, cut into
+ * `num_pages` pages of `page_size` tokens (16, 32, 64, 128 or 256) for
+ * `kv_heads` heads (1..1024) of `head_dim` channels (64, 128 or 256).  The
+ * bytes' order inside is internal to the library.  Slot s of the cache is token s %
+ * page_size of page s / page_size; num_pages * page_size < 2^31.  The buffer
+ * needs no clearing: attention reads slots that were never written only as
+ * far as its lengths say they were. */
+typedef struct {
+  void *data; /* device, 16-byte aligned */
+  int32_t num_pages, page_size, kv_heads, head_dim;
+} svdq_kv4_cache_t;
+
+/* 0 for a shape outside the limits above. */
+size_t svdq_kv4_cache_bytes(int num_pages, int page_size, int kv_heads, int head_dim);
+
+/* Encodes T rows of keys and values (bf16 or fp16, device) into the slots
+ * slots[T] (device): row t's head h starts at k + t k_row + h k_head elements
+ * (v likewise), its channels next to each other, so rows of a fused
+ * projection are taken where they are.  Pointers are 16-byte aligned and strides
+ * multiples of 8 elements, not negative.  A block's exponent and codes are as
+ * for svdq_mx_linear_forward's activations; a block that holds an infinity or
+ * a NaN gets scale byte 255, for which all its values read as NaN.  A slot outside
+ * the cache is skipped (-1 marks padding rows).  The slots of one call must
+ * differ; one named twice is left with parts of both rows.  One kernel. */
+svdq_status_t svdq_kv4_append(const svdq_kv4_cache_t *cache, const void *k, int64_t k_row, int64_t k_head,
+                              const void *v, int64_t v_row, int64_t v_head, svdq_dtype_t dtype, int T,
+                              const int32_t *slots, void *hip_stream);
+
+/* The values that slots[T] hold: k, v [T, kv_heads, head_dim] of `dtype`
+ * SVDQ_BF16 or SVDQ_FP32, both exact.  Slots outside the cache read as zeros. */
+svdq_status_t svdq_kv4_read(const svdq_kv4_cache_t *cache, const int32_t *slots, int T, void *k, void *v,
+                            svdq_dtype_t dtype, void *hip_stream);
+
+/* Attention of the last Q tokens of each of B sequences over the cache:
+ *   out[b, i, h] = sum_t p_t v[t, h / g] / sum_t p_t,
+ *   p_t = exp(scale q[b, i, h] . k[t, h / g] - max),  0 <= t < seq_lens[b] - Q + i + 1
+ * with g = Hq / kv_heads query heads to a key/value head; token t of sequence b is
+ * in page page_table[b, t / page_size].  seq_lens counts the new tokens, which
+ * are appended first.  A row that sees no token (an empty sequence, or one
+ * shorter than Q) is zero.  q is bf16 or fp16, q[b, i, h] at q + b q_batch + i
+ * q_token + h q_head elements (aligned as for svdq_kv4_append); out [B, Q, Hq,
+ * head_dim] of the same type, dense.  page_table [B, table_width] and
+ * seq_lens [B] are int32 device arrays; a length past the table's end counts
+ * up to it and a negative one as 0, and a page outside the cache hides its
+ * tokens.  B <= 65536, Hq a multiple of kv_heads, Q g <= 1024, B Q Hq <= 2^24.
+ * Scores, softmax statistics and sums are float32; the weights p enter the
+ * product with 16 significant bits.  The result does not depend on the
+ * order in which workgroups run.  Two kernels; the workspace needs no
+ * clearing and keeps nothing from one call for the next. */
+size_t svdq_kv4_attention_workspace_bytes(int B, int Q, int Hq, int kv_heads, int head_dim);
+svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, int64_t q_batch, int64_t q_token,
+                                 int64_t q_head, svdq_dtype_t dtype, int B, int Q, int Hq,
+                                 const int32_t *page_table, int table_width, const int32_t *seq_lens, float scale,
+                                 void *out, void *workspace, size_t ws_bytes, void *hip_stream);
+
 /* ============================================================== AWQ W4A16
  * "Bringing Nunchaku 4-bit diffusion inference to Diffusers" (Russian
  * edition, technical-details section; Korean edition, "Diffusers 내
@@ -413,6 +474,48 @@ svdq_status_t awq_pack_device_weights(const uint8_t *q, const uint16_t *scales_f
 svdq_status_t awq_w4a16_forward(const void *blob, int N, int K, const void *x_fp16,
                                 int M, const void *bias_fp16, void *y_fp16,
                                 void *hip_stream);
+
+/* ------------------------------------------------- mixture of experts
+ * The expert layer of a mixture of experts whose experts are AWQ W4A16
+ * linears, for a few tokens (what a serving step brings), and its router. */
+typedef enum { SVDQ_MOE_SOFTMAX = 0, SVDQ_MOE_SIGMOID = 1 } svdq_moe_score_t;
+typedef enum { SVDQ_MOE_SILU = 0, SVDQ_MOE_GELU_TANH = 1 } svdq_moe_act_t;
+
+/* The experts of each token: logits x w_router^T [T, E], scores their softmax
+ * over the E experts or their sigmoid, and the top_k experts of the largest
+ * score (+ bias), the lower index first where two are equal (a NaN counts as
+ * the smallest).  ids [T, top_k] int32 in that order; weights [T, top_k]
+ * float32 their scores without the bias, divided by their sum if `normalize`.
+ * x [T, K] and w_router [E, K] are bf16 or fp16 (device, 16-byte aligned), bias
+ * [E] float32 or NULL.  Logits and scores are float64, so the choice does not
+ * hang on the order of a sum.  E <= 1024, K a multiple of 8 up to 2^20,
+ * top_k <= min(E, 32), T <= 65535.  Two kernels. */
+size_t svdq_moe_route_workspace_bytes(int T, int E);
+svdq_status_t svdq_moe_route(const void *x, const void *w_router, const float *bias, svdq_dtype_t dtype, int T, int E,
+                             int K, int top_k, svdq_moe_score_t score, int normalize, int32_t *ids, float *weights,
+                             void *workspace, size_t ws_bytes, void *hip_stream);
+
+/* Experts resident in device memory: E blobs of awq_pack_device_weights one
+ * after another, each awq_device_weights_bytes long.  gate_up: [2 I, K] each
+ * (the I gate rows, then the I up rows); down: [K, I] each. */
+typedef struct {
+  const void *gate_up, *down;
+  int32_t E, K, I;
+} awq_moe_weights_t;
+
+/* y[t] = sum_j weights[t, j] Down_e (act(Gate_e x[t]) * (Up_e x[t])),
+ * e = ids[t, j].  x and y [T, K] bf16 or fp16; ids [T, top_k] int32 and
+ * weights [T, top_k] float32 as svdq_moe_route leaves them (device).  An id
+ * outside [0, E) adds nothing (experts held elsewhere, padding rows); one
+ * that a token names twice counts twice.  The gated product is kept to 16
+ * significant bits in float32's range, sums are float32, and y is rounded once.
+ * E <= 1024, K and I multiples of 64 with 2 I K <= 2^31, T top_k <= 4096.
+ * Each expert that some token names is read once per 16 of its rows.  The
+ * workspace needs no clearing and keeps nothing from one call for the next. */
+size_t awq_moe_workspace_bytes(int T, int top_k, int K, int I);
+svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dtype_t dtype, int T, const int32_t *ids,
+                              const float *weights, int top_k, svdq_moe_act_t act, void *y, void *workspace,
+                              size_t ws_bytes, void *hip_stream);
 
 /* ============================================================ measurement
  * Not part of the layer: the practical HBM rate that the bandwidth-bound

@@ -1,0 +1,349 @@
+"""The MXFP4 key/value cache and its attention on the GPU against the float64
+oracle: every value of the cache bit for bit, attention within the bounds of
+its float32 arithmetic."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4 as O
+from tests.conftest import announce
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def S():
+    import w4a4_rank_corrected_smooth_amd as lib
+    lib.device_check()
+    return lib
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rows(r, shape, dtype, scale=1.0):
+    x = r.standard_normal(shape) * scale
+    x[..., ::29] *= 9.0
+    return torch.from_numpy(x).to(DT[dtype]).cuda()
+
+
+# ------------------------------------------------------------ append and read
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,H,D,page", [(1, 1, 64, 16), (37, 3, 128, 16), (70, 2, 256, 64), (129, 5, 64, 256)])
+def test_append_then_read(S, T, H, D, page, dtype):
+    announce(f"kv4 append/read T={T} H={H} D={D} page={page} {dtype}")
+    r = np.random.default_rng(T + D)
+    pages = T // page + 3
+    cache = S.Kv4Cache(pages, page, H, D)
+    k, v = rows(r, (T, H, D), dtype), rows(r, (T, H, D), dtype, 0.01)
+    slots = torch.from_numpy(r.permutation(pages * page)[:T].astype(np.int32)).cuda()
+    S.kv4_append(cache, k, v, slots)
+    for out in (torch.bfloat16, torch.float32):
+        gk, gv = S.kv4_read(cache, slots, dtype=out)
+        assert gk.dtype == out and np.array_equal(f64(gk), O.values(f64(k))) and np.array_equal(f64(gv), O.values(f64(v)))
+    # slots that were not named still hold what a new cache holds
+    rest = np.setdiff1d(np.arange(pages * page), slots.cpu().numpy()).astype(np.int32)
+    gk, gv = S.kv4_read(cache, torch.from_numpy(rest).cuda())
+    assert not gk.any() and not gv.any()
+
+
+@pytest.mark.parametrize("run", [1, 15, 16, 17, 40, 64])
+@pytest.mark.parametrize("first", [0, 5, 16])
+def test_append_runs_of_slots(S, run, first):
+    """Rows that fill units of 16 tokens whole, in part, and from the middle, after others' rows were there."""
+    announce(f"kv4 append of {run} rows from slot {first}")
+    r = np.random.default_rng(run * 100 + first)
+    H, D = 2, 128
+    cache = S.Kv4Cache(6, 16, H, D)
+    k0, v0 = rows(r, (96, H, D), "bf16"), rows(r, (96, H, D), "bf16")
+    S.kv4_append(cache, k0, v0, torch.arange(96, dtype=torch.int32, device="cuda"))
+    k, v = rows(r, (run, H, D), "bf16"), rows(r, (run, H, D), "bf16")
+    S.kv4_append(cache, k, v, torch.arange(first, first + run, dtype=torch.int32, device="cuda"))
+    gk, gv = S.kv4_read(cache, torch.arange(96, dtype=torch.int32, device="cuda"))
+    for got, old, new in ((gk, k0, k), (gv, v0, v)):
+        want = O.values(f64(old))
+        want[first:first + run] = O.values(f64(new))
+        assert np.array_equal(f64(got), want)
+
+
+def test_append_takes_rows_where_they_are_and_skips_slots_outside(S):
+    r = np.random.default_rng(8)
+    T, H, D, page = 21, 2, 64, 16
+    qkv = rows(r, (T, 8, D), "bf16")
+    k, v = qkv[:, 4:6], qkv[:, 6:8]
+    cache = S.Kv4Cache(2, page, H, D)
+    slots = torch.from_numpy(r.permutation(32)[:T].astype(np.int32)).cuda()
+    slots[3], slots[7], slots[9] = -1, 32, 2 ** 31 - 1
+    announce("kv4 append of strided rows, three of them to no slot")
+    S.kv4_append(cache, k, v, slots)
+    gk, gv = S.kv4_read(cache, slots)
+    for got, x in ((gk, k), (gv, v)):
+        want = O.values(f64(x))
+        want[[3, 7, 9]] = 0
+        assert np.array_equal(f64(got), want)
+    # per-head layout [H, T, D]
+    t = k.permute(1, 0, 2).contiguous().permute(1, 0, 2)
+    S.kv4_append(cache, t, v, slots)
+    assert torch.equal(S.kv4_read(cache, slots)[0], gk)
+
+
+def test_append_edge_values(S):
+    """Zeros of both signs, the smallest and largest values, ties, infinities and NaN."""
+    x = np.zeros((8, 1, 64))
+    x[0, 0, :8] = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]
+    x[0, 0, 32:40] = [-0.25, -0.75, -1.25, -1.75, -2.5, -3.5, -5.0, -7.0]
+    x[1, 0, 0], x[1, 0, 33] = -0.0, 2.0 ** -133
+    x[2, 0, :3] = [3.0e38, -1.0e38, 1.0]
+    x[3, 0, 5], x[3, 0, 40] = np.inf, -np.inf
+    x[4, 0, 63] = np.nan
+    x[5, 0, :4] = [2.0 ** -126, 2.0 ** -127, -2.0 ** -128, 2.0 ** -130]
+    x[6, 0, :] = 1.9921875
+    k = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    cache = S.Kv4Cache(1, 16, 1, 64)
+    slots = torch.arange(8, dtype=torch.int32, device="cuda")
+    announce("kv4 append of edge values")
+    S.kv4_append(cache, k, k, slots)
+    for got in S.kv4_read(cache, slots, dtype=torch.float32):
+        want = O.values(f64(k))
+        assert np.array_equal(f64(got), want, equal_nan=True)
+        assert not np.signbit(f64(got)[1]).any()
+
+
+# ------------------------------------------------------------------- attention
+class Batch:
+    """Sequences scattered over a cache whose every other slot holds large values."""
+
+    def __init__(self, S, seed, lens, H, D, page, dtype, spare=2, width_more=0):
+        r = np.random.default_rng(seed)
+        per = [-(-n // page) for n in lens]
+        self.pages = sum(per) + spare
+        order = r.permutation(self.pages).astype(np.int32)
+        width = max(1, max(per)) + width_more
+        table = r.integers(0, self.pages, (len(lens), width)).astype(np.int32)
+        at = 0
+        for b, n in enumerate(per):
+            table[b, :n] = order[at:at + n]
+            at += n
+        self.cache = S.Kv4Cache(self.pages, page, H, D)
+        n = self.pages * page
+        k, v = rows(r, (n, H, D), dtype), rows(r, (n, H, D), dtype)
+        used = np.zeros(n, bool)
+        for b, m in enumerate(lens):
+            t = np.arange(m)
+            used[table[b, t // page] * page + t % page] = True
+        k[torch.from_numpy(~used).cuda()] = float("inf")    # old rows behind a sequence's end
+        v[torch.from_numpy(~used).cuda()] = float("nan")
+        S.kv4_append(self.cache, k, v, torch.arange(n, dtype=torch.int32, device="cuda"))
+        kv, vv = (O.values(f64(t)) for t in (k, v))
+        self.k, self.v = [], []
+        for b, m in enumerate(lens):
+            t = np.arange(m)
+            s = table[b, t // page] * page + t % page
+            self.k.append(kv[s])
+            self.v.append(vv[s])
+        self.lens, self.D, self.dtype = lens, D, dtype
+        self.table = torch.from_numpy(table).cuda()
+        self.seq_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.r = r
+
+    def queries(self, Q, Hq, scale=1.0):
+        return torch.from_numpy(self.r.standard_normal((len(self.lens), Q, Hq, self.D)) * scale).to(DT[self.dtype]).cuda()
+
+
+def check(got, q, b, scale):
+    """|error| <= half a step of the output, plus what float32 does to it: a
+    score is a sum of D products in any order, a scaling and a difference,
+    (D + 4) 2^-24 of its terms, twice (a piece may be joined to another's
+    maximum); exp2 and the joins 2^-20; a weight has 2^-17 of its own; the
+    sum over n tokens n 2^-24.  All of it on sum p |v|, and once more for the
+    denominator."""
+    out, mass, largest, terms = O.attend(f64(q), b.k, b.v, b.lens, scale)
+    D = q.shape[-1]
+    u = 2.0 ** -24
+    rel = 2 * (2 * (D + 4) * u * largest + 2.0 ** -20 + 2.0 ** -17 + terms * u)
+    tol = torch.finfo(q.dtype).eps / 2 * np.abs(out) * (1 + rel) + rel * mass + torch.finfo(q.dtype).tiny
+    err = np.abs(f64(got) - out)
+    assert got.dtype == q.dtype and (err <= tol).all(), f"{(err / np.maximum(tol, 1e-300)).max()} of the bound"
+
+
+CASES = [
+    # lens, Q, Hq, Hkv, D, page, dtype
+    ([1], 1, 1, 1, 64, 16, "bf16"),
+    ([1, 0, 2], 1, 4, 2, 128, 16, "fp16"),
+    ([15, 16, 17, 31, 32, 33, 127, 128, 129], 1, 8, 2, 128, 16, "bf16"),
+    ([15, 16, 17, 31, 32, 33, 127, 128, 129], 1, 8, 2, 128, 128, "fp16"),
+    ([700], 1, 32, 8, 128, 64, "bf16"),
+    ([513, 3, 0, 1000, 64, 90], 1, 5, 1, 64, 32, "fp16"),
+    ([300, 1], 1, 32, 2, 256, 16, "bf16"),
+    ([257, 40], 1, 16, 16, 64, 256, "bf16"),
+    ([3000, 2999], 1, 17, 1, 128, 32, "fp16"),          # 17 rows: two tiles
+    ([640, 5], 3, 10, 5, 128, 16, "bf16"),              # drafted tokens
+    ([100, 2, 0, 1], 5, 8, 1, 64, 32, "fp16"),          # 40 rows: two blocks, sequences shorter than Q
+    ([90], 7, 32, 2, 256, 64, "bf16"),                  # 112 rows
+    ([40] * 150, 1, 2, 1, 64, 16, "bf16"),              # more sequences than lanes
+    ([1, 2000] * 70, 1, 4, 4, 64, 64, "fp16"),
+    ([20000], 1, 8, 1, 128, 256, "bf16"),               # one sequence over many workgroups
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention(S, case):
+    lens, Q, Hq, H, D, page, dtype = CASES[case]
+    announce(f"kv4 attention case {case}: B={len(lens)} max={max(lens)} Q={Q} Hq={Hq}/{H} D={D} page={page} {dtype}")
+    b = Batch(S, case, lens, H, D, page, dtype)
+    q = b.queries(Q, Hq)
+    got = S.kv4_attention(b.cache, q, b.table, b.seq_lens)
+    check(got, q, b, D ** -0.5)
+    again = S.kv4_attention(b.cache, q, b.table, b.seq_lens, out=torch.full_like(got, float("nan")),
+                            workspace=torch.full_like(S.kv4_attention_workspace(b.cache, q), 0xFF))
+    assert torch.equal(got, again)
+
+
+def test_attention_peaked_and_negative_scales(S):
+    b = Batch(S, 50, [400, 77], 2, 128, 16, "fp16")
+    for scale, size in ((0.7, 3.0), (-0.2, 1.0), (0.0, 1.0)):
+        announce(f"kv4 attention scale {scale}")
+        q = b.queries(1, 8, size)
+        check(S.kv4_attention(b.cache, q, b.table, b.seq_lens, scale=scale), q, b, scale)
+
+
+def test_attention_of_strided_queries_and_a_wide_table(S):
+    b = Batch(S, 51, [130, 0, 45], 2, 64, 32, "bf16", width_more=40)
+    qkv = b.queries(2, 12)
+    q = qkv[:, :, 3:7]
+    announce("kv4 attention with strided queries")
+    got = S.kv4_attention(b.cache, q, b.table, b.seq_lens)
+    check(got, q, b, 0.125)
+    assert torch.equal(got, S.kv4_attention(b.cache, q.contiguous(), b.table, b.seq_lens))
+
+
+def test_attention_hides_bad_pages_and_clamps_lengths(S):
+    page = 16
+    b = Batch(S, 52, [100, 64, 48], 1, 64, page, "bf16")
+    q = b.queries(1, 4)
+    width = b.table.shape[1]
+    lens = b.seq_lens.clone()
+    lens[0], lens[2] = 2 ** 31 - 1, -5
+    table = b.table.clone()
+    t = np.arange(width * page)
+    # the long row: as far as the table goes, pages that exist only where the sequence had some
+    table[0, 7:] = -1
+    table[0, 2], table[1, 1] = b.pages, -(2 ** 31)
+    announce("kv4 attention with bad pages, a length past the table and a negative one")
+    got = f64(S.kv4_attention(b.cache, q, table, lens))
+    seen0 = [i for i in t if i // page < 7 and i // page != 2 and i < 100]
+    tail = list(range(100, 112))                # the seventh page's old rows: not finite, so the row is not either
+    assert tail and not np.isfinite(got[0]).any()
+    assert (got[2] == 0).all()
+    k, v = b.k[1], b.v[1]
+    keep = [i for i in range(64) if i // page != 1]
+    bb = type("B", (), dict(k=[k[keep]], v=[v[keep]], lens=[len(keep)]))
+    check(torch.from_numpy(got[1:2]).to(torch.bfloat16), q[1:2], bb, 0.125)
+    lens[0] = 100
+    got = S.kv4_attention(b.cache, q, table, lens)
+    bb = type("B", (), dict(k=[b.k[0][seen0]], v=[b.v[0][seen0]], lens=[len(seen0)]))
+    check(got[:1], q[:1], bb, 0.125)
+    table.fill_(-1)
+    assert not S.kv4_attention(b.cache, q, table, lens).any()
+
+
+def test_attention_carries_nan_and_infinity(S):
+    """A NaN in a sequence's cache, or in one query head, reaches the rows that see it and no others."""
+    b = Batch(S, 53, [50, 50], 2, 64, 16, "bf16")
+    k = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    v[0, 1, 3] = float("nan")
+    slot = (b.table[0, 0] * 16 + 7).reshape(1).to(torch.int32)
+    announce("kv4 attention over a NaN")
+    S.kv4_append(b.cache, k, v, slot)
+    q = b.queries(1, 4)
+    q[1, 0, 0, 5] = float("nan")
+    got = f64(S.kv4_attention(b.cache, q, b.table, b.seq_lens))
+    assert np.isnan(got[0, 0, 2:, :32]).all() and np.isfinite(got[0, 0, :2]).all() and np.isfinite(got[0, 0, 2:, 32:]).all()
+    assert np.isnan(got[1, 0, 0]).all() and np.isfinite(got[1, 0, 1:]).all()
+
+
+def test_attention_slots_past_32_bit_offsets(S):
+    """A cache of more than 4 GiB: pages at its far end."""
+    H, D, page = 8, 128, 256
+    pages = (1 << 32) // (H * page * (D + 8)) + 8
+    announce(f"kv4 cache of {pages} pages, {pages * H * page * (D + 8) / 2 ** 30:.2f} GiB")
+    cache = S.Kv4Cache(pages, page, H, D)
+    r = np.random.default_rng(9)
+    n = 300
+    table = torch.tensor([[pages - 1, pages - 3]], dtype=torch.int32, device="cuda")
+    t = np.arange(n)
+    slots = torch.from_numpy((table.cpu().numpy()[0][t // page].astype(np.int64) * page + t % page).astype(np.int32)).cuda()
+    k, v = rows(r, (n, H, D), "bf16"), rows(r, (n, H, D), "bf16")
+    S.kv4_append(cache, k, v, slots)
+    assert np.array_equal(f64(S.kv4_read(cache, slots)[1]), O.values(f64(v)))
+    q = torch.from_numpy(r.standard_normal((1, 1, 16, D))).to(torch.bfloat16).cuda()
+    got = S.kv4_attention(cache, q, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    bb = type("B", (), dict(k=[O.values(f64(k))], v=[O.values(f64(v))], lens=[n]))
+    check(got, q, bb, D ** -0.5)
+
+
+def test_append_and_attention_in_a_graph(S):
+    """A decode step captured once and replayed as the sequences grow equals the eager calls."""
+    page, H, D, B = 16, 2, 64, 3
+    r = np.random.default_rng(11)
+    lens = torch.tensor([5, 0, 30], dtype=torch.int32, device="cuda")
+    table = torch.from_numpy(r.permutation(12).reshape(B, 4).astype(np.int32)).cuda()
+    caches = [S.Kv4Cache(12, page, H, D) for _ in range(2)]
+    k0, v0 = rows(r, (192, H, D), "bf16"), rows(r, (192, H, D), "bf16")
+    for c in caches:
+        S.kv4_append(c, k0, v0, torch.arange(192, dtype=torch.int32, device="cuda"))
+    q, k, v = (torch.zeros(B, 1, h, D, dtype=torch.bfloat16, device="cuda") for h in (4, H, H))
+    out = torch.empty_like(q)
+    ws = S.kv4_attention_workspace(caches[0], q)
+
+    def step(c, lens, out, ws):
+        at = lens.long()
+        slots = (table.gather(1, (at // page)[:, None])[:, 0] * page + at % page).to(torch.int32)
+        S.kv4_append(c, k[:, 0], v[:, 0], slots)
+        lens += 1
+        return S.kv4_attention(c, q, table, lens, out=out, workspace=ws)
+
+    announce("kv4 decode step: capture")
+    glens = lens.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step(caches[0], glens, out, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    S.kv4_append(caches[0], k0, v0, torch.arange(192, dtype=torch.int32, device="cuda"))
+    glens.copy_(lens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(caches[0], glens, out, ws)
+    glens.copy_(lens)
+    S.kv4_append(caches[0], k0, v0, torch.arange(192, dtype=torch.int32, device="cuda"))
+    elens = lens.clone()
+    for i in range(20):
+        for t in (q, k, v):
+            t.copy_(torch.from_numpy(r.standard_normal(tuple(t.shape))).to(torch.bfloat16))
+        graph.replay()
+        want = step(caches[1], elens, torch.empty_like(q), None)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), f"replay {i}"
+    assert torch.equal(caches[0].data, caches[1].data) and torch.equal(glens, elens)
+
+
+def test_attention_on_two_streams(S):
+    b = Batch(S, 54, [900, 400, 20], 2, 128, 32, "bf16")
+    qs = [b.queries(1, 8) for _ in range(2)]
+    want = [S.kv4_attention(b.cache, q, b.table, b.seq_lens) for q in qs]
+    torch.cuda.synchronize()
+    announce("kv4 attention on two streams")
+    streams = [torch.cuda.Stream() for _ in qs]
+    outs = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(S.kv4_attention(b.cache, qs[i], b.table, b.seq_lens))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])

@@ -1,0 +1,215 @@
+"""The router and the W4A16 expert layer on the GPU against the float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import awq, moe as O
+from tests.conftest import announce
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def S():
+    import w4a4_rank_corrected_smooth_amd as lib
+    lib.device_check()
+    return lib
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ---------------------------------------------------------------------- router
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,E,K,k,score,bias", [
+    (1, 1, 8, 1, "softmax", False), (1, 64, 2048, 6, "softmax", False), (3, 8, 64, 8, "sigmoid", True),
+    (5, 65, 520, 32, "softmax", True), (17, 128, 1000, 8, "sigmoid", False), (4, 257, 264, 3, "softmax", False),
+    (2, 1024, 128, 4, "sigmoid", True), (250, 60, 96, 4, "softmax", False)])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_route(S, T, E, K, k, score, bias, normalize, dtype):
+    announce(f"route T={T} E={E} K={K} k={k} {score} bias={bias} normalize={normalize} {dtype}")
+    r = np.random.default_rng(T * 7 + E)
+    x = torch.from_numpy(r.standard_normal((T, K))).to(DT[dtype]).cuda()
+    w = torch.from_numpy(r.standard_normal((E, K)) / np.sqrt(K)).to(DT[dtype]).cuda()
+    b = torch.from_numpy(r.standard_normal(E) * 0.1).float().cuda() if bias else None
+    ids, wt = S.moe_route(x, w, k, bias=b, score=score, normalize=normalize)
+    rid, rwt = O.route(f64(x), f64(w), k, None if b is None else f64(b), score, normalize)
+    assert ids.dtype == torch.int32 and np.array_equal(ids.cpu().numpy(), rid)
+    # one rounding to float32; the float64 logits, scores and sums are 2^-40 off at the most here
+    assert (np.abs(f64(wt) - rwt) <= (2.0 ** -24 + 2.0 ** -40) * rwt + 2.0 ** -149).all()
+
+
+def test_route_ties_go_to_the_lower_index(S):
+    w = torch.ones(200, 64, dtype=torch.bfloat16, device="cuda")
+    w[[70, 150]] *= 2
+    x = torch.ones(2, 64, dtype=torch.bfloat16, device="cuda")
+    announce("route with ties")
+    assert S.moe_route(x, w, 5)[0].tolist() == [[70, 150, 0, 1, 2]] * 2
+    assert S.moe_route(-x, w, 5)[0].tolist() == [[0, 1, 2, 3, 4]] * 2
+
+
+def test_route_of_rows_that_are_not_finite(S):
+    """NaN and infinite rows keep valid, different ids and leave the other rows alone."""
+    r = np.random.default_rng(2)
+    x = torch.from_numpy(r.standard_normal((4, 64))).bfloat16().cuda()
+    w = torch.from_numpy(r.standard_normal((70, 64))).bfloat16().cuda()
+    want = S.moe_route(x, w, 4)
+    y = x.clone()
+    y[1, 3], y[2, 5] = float("nan"), float("inf")
+    announce("route of rows that are not finite")
+    for score in ("softmax", "sigmoid"):
+        ids, wt = S.moe_route(y, w, 4, score=score)
+        for t in range(4):
+            assert len(set(ids[t].tolist())) == 4 and 0 <= min(ids[t].tolist()) and max(ids[t].tolist()) < 70
+        assert torch.isnan(wt[1]).all()
+        if score == "softmax":
+            assert torch.equal(ids[[0, 3]], want[0][[0, 3]]) and torch.equal(wt[[0, 3]], want[1][[0, 3]])
+
+
+# --------------------------------------------------------------------- experts
+def experts(r, E, K, I):
+    out = []
+    for N, D in ((2 * I, K), (K, I)):
+        q = r.integers(0, 16, (E, N, D), dtype=np.uint8)
+        s = ((0.5 + r.random((E, N, D // 64))) * 0.25 / np.sqrt(D)).astype(np.float16)
+        z = r.integers(0, 16, (E, N, D // 64)).astype(np.float16)
+        out.append((q, s, z))
+    return out
+
+
+def device_layer(S, parts):
+    return S.AwqMoe(*((awq.pack(q), s, z) for q, s, z in parts))
+
+
+def check(got, x, parts, ids, wt, act):
+    per = [[tuple(a[e] for a in p) for e in range(len(p[0]))] for p in parts]
+    y, bound = O.layer(f64(x), *per, ids.cpu().numpy(), f64(wt), act)
+    half = torch.finfo(x.dtype).eps / 2
+    err = np.abs(f64(got) - y)
+    tol = half * (np.abs(y) + bound) + bound + torch.finfo(x.dtype).tiny
+    assert got.dtype == x.dtype and (err <= tol).all(), f"{(err / np.maximum(tol, 1e-300)).max()} of the bound"
+    # the bound is a worst case over the terms' signs; the errors' squares add up to far less: 2^-12
+    # is 16 times what independent roundings of the same terms give
+    assert np.linalg.norm(err) <= (half + 2.0 ** -12) * np.linalg.norm(y) + 1e-30
+
+
+SHAPES = [
+    # T, E, K, I, k
+    (1, 1, 64, 64, 1), (1, 8, 128, 192, 2), (3, 5, 192, 64, 3), (7, 16, 448, 320, 4), (2, 64, 512, 128, 8),
+    (16, 4, 256, 128, 2), (17, 1, 128, 128, 1), (40, 2, 320, 192, 2), (64, 40, 128, 64, 6), (130, 3, 64, 128, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("case", range(len(SHAPES)))
+def test_expert_layer(S, case, act, dtype):
+    T, E, K, I, k = SHAPES[case]
+    announce(f"experts T={T} E={E} K={K} I={I} k={k} {act} {dtype}")
+    r = np.random.default_rng(case)
+    parts = experts(r, E, K, I)
+    layer = device_layer(S, parts)
+    x = torch.from_numpy(r.standard_normal((T, K))).to(DT[dtype]).cuda()
+    ids = torch.from_numpy(np.stack([r.permutation(E)[:k] for _ in range(T)]).astype(np.int32)).cuda()
+    wt = torch.from_numpy(r.random((T, k)) + 0.05).float().cuda()
+    got = S.awq_moe_forward(layer, x, ids, wt, activation=act)
+    check(got, x, parts, ids, wt, act)
+    ws = torch.full_like(layer.new_workspace(T, k), 0xFF)
+    again = S.awq_moe_forward(layer, x, ids, wt, activation=act, out=torch.full_like(got, float("nan")), workspace=ws)
+    assert torch.equal(got, again)
+
+
+def test_expert_layer_ids_outside_and_twice(S):
+    r = np.random.default_rng(30)
+    E, K, I, T, k = 4, 128, 64, 9, 3
+    parts = experts(r, E, K, I)
+    layer = device_layer(S, parts)
+    x = torch.from_numpy(r.standard_normal((T, K))).bfloat16().cuda()
+    ids = torch.from_numpy(r.integers(-1, E + 1, (T, k)).astype(np.int32)).cuda()
+    ids[0] = 2                                   # the same expert three times
+    ids[1] = -1                                  # no expert at all
+    ids[2, 0], ids[2, 1] = 2 ** 31 - 1, -(2 ** 31)
+    wt = torch.from_numpy(r.standard_normal((T, k))).float().cuda()
+    wt[1] = float("nan")                         # weights of choices that do not count
+    announce("experts with ids outside and twice")
+    got = S.awq_moe_forward(layer, x, ids, wt)
+    assert not got[1].any()
+    check(got[[0] + list(range(2, T))], x[[0] + list(range(2, T))], parts, ids[[0] + list(range(2, T))],
+          wt[[0] + list(range(2, T))], "silu")
+    ids.fill_(E)
+    assert not S.awq_moe_forward(layer, x, ids, wt).any()
+
+
+def test_expert_layer_rows_do_not_touch_each_other(S):
+    """A token of NaN or infinities spoils its own row only, and a token's row is the same in any company."""
+    r = np.random.default_rng(31)
+    E, K, I, T, k = 3, 192, 128, 21, 2
+    parts = experts(r, E, K, I)
+    layer = device_layer(S, parts)
+    for dtype in DT.values():
+        x = torch.from_numpy(r.standard_normal((T, K))).to(dtype).cuda()
+        ids = torch.from_numpy(np.stack([r.permutation(E)[:k] for _ in range(T)]).astype(np.int32)).cuda()
+        wt = torch.from_numpy(r.random((T, k))).float().cuda()
+        announce(f"experts: rows apart {dtype}")
+        want = S.awq_moe_forward(layer, x, ids, wt)
+        y = x.clone()
+        y[4, 7], y[11] = float("nan"), float("inf")
+        got = S.awq_moe_forward(layer, y, ids, wt)
+        rest = [t for t in range(T) if t not in (4, 11)]
+        assert torch.isnan(got[4]).all() and torch.equal(got[rest], want[rest])
+        for t in (0, 20):
+            assert torch.equal(S.awq_moe_forward(layer, x[t:t + 1], ids[t:t + 1].contiguous(), wt[t:t + 1].contiguous())[0], want[t])
+
+
+def test_expert_layer_large_gated_products(S):
+    """h beyond fp16's range on its way to an output inside it."""
+    r = np.random.default_rng(32)
+    E, K, I = 2, 64, 64
+    parts = experts(r, E, K, I)
+    parts[0][1][:] *= np.float16(64)
+    parts[1][1][:] *= np.float16(2.0 ** -9)
+    layer = device_layer(S, parts)
+    x = torch.from_numpy(r.standard_normal((2, K)) * 8).half().cuda()
+    ids, wt = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda"), torch.ones(2, 1, device="cuda")
+    announce("experts with large gated products")
+    check(S.awq_moe_forward(layer, x, ids, wt), x, parts, ids, wt, "silu")
+
+
+def test_route_and_experts_in_a_graph(S):
+    """Router and experts captured together and replayed on new tokens equal the eager calls, as do two
+    graphs that share a workspace."""
+    r = np.random.default_rng(33)
+    E, K, I, T, k = 6, 128, 64, 5, 2
+    layer = device_layer(S, experts(r, E, K, I))
+    w = torch.from_numpy(r.standard_normal((E, K))).bfloat16().cuda()
+    ws = layer.new_workspace(T, k)
+    xs = [torch.zeros(T, K, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+
+    def step(x, ws):
+        ids, wt = S.moe_route(x, w, k)
+        return S.awq_moe_forward(layer, x, ids, wt, workspace=ws)
+
+    announce("router and experts: capture")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for x in xs:
+            step(x, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(x, ws))
+        graphs.append(g)
+    for i in range(6):
+        for x in xs:
+            x.copy_(torch.from_numpy(r.standard_normal((T, K))).bfloat16())
+        for g in graphs:
+            g.replay()
+        want = [step(x, None) for x in xs]
+        torch.cuda.synchronize()
+        for o, v in zip(outs, want):
+            assert torch.equal(o, v), f"replay {i}"

@@ -1,5 +1,6 @@
-"""Python binding of libsvdq: the SVDQuant W4A4 + low-rank linear layer and
-the AWQ W4A16 linear on MI355X (gfx950).
+"""Python binding of libsvdq: the SVDQuant W4A4 + low-rank linear layer, the
+AWQ W4A16 linear, the MXFP4 key/value cache with its attention, and the W4A16
+expert layer with its router, on MI355X (gfx950).
 
 This module only marshals arguments into the C ABI declared in
 ``include/svdq.h``: every step of the method runs in the library (host
@@ -35,6 +36,8 @@ STATUS = {0: "SVDQ_OK", 1: "SVDQ_ERR_INVALID_ARGUMENT", 2: "SVDQ_ERR_UNSUPPORTED
           5: "SVDQ_ERR_WORKSPACE_TOO_SMALL", 6: "SVDQ_ERR_NUMERICAL", 7: "SVDQ_ERR_HIP"}
 BF16, FP16, FP32 = 0, 1, 2
 EPILOGUE_NONE, EPILOGUE_GELU_TANH = 0, 1
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+MOE_ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 EXPORTS = [
     "svdq_abi_version", "svdq_status_string", "svdq_last_error", "svdq_device_check",
@@ -50,6 +53,9 @@ EXPORTS = [
     "svdq_mx_pack_device_weights", "svdq_mx_workspace_bytes", "svdq_mx_linear_forward",
     "svdq_mx_linear_quantize", "svdq_mx_linear_gemm", "svdq_mx_quantize_activations",
     "svdq_merge_lora", "svdq_mx_merge_lora", "svdq_measure_stream", "svdq_measure_mfma",
+    "svdq_kv4_cache_bytes", "svdq_kv4_append", "svdq_kv4_read", "svdq_kv4_attention_workspace_bytes",
+    "svdq_kv4_attention", "svdq_moe_route_workspace_bytes", "svdq_moe_route", "awq_moe_workspace_bytes",
+    "awq_moe_forward",
 ]
 
 
@@ -68,6 +74,16 @@ class MxHostWeights(ctypes.Structure):
 class DeviceWeights(ctypes.Structure):
     _fields_ = [("blob", _vp), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
                 ("rank", ctypes.c_int32)]
+
+
+class Kv4CacheStruct(ctypes.Structure):
+    _fields_ = [("data", _vp), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class MoeWeights(ctypes.Structure):
+    _fields_ = [("gate_up", _vp), ("down", _vp), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("I", ctypes.c_int32)]
 
 
 def _sig(name, res, args):
@@ -123,6 +139,19 @@ _sig("svdq_merge_lora", _i, [ctypes.POINTER(HostWeights), _vp, _vp, _i, ctypes.c
                              ctypes.POINTER(HostWeights)])
 _sig("svdq_mx_merge_lora", _i, [ctypes.POINTER(MxHostWeights), _vp, _vp, _i, ctypes.c_float,
                                 ctypes.POINTER(MxHostWeights)])
+
+_i64 = ctypes.c_int64
+_C = ctypes.POINTER(Kv4CacheStruct)
+_sig("svdq_kv4_cache_bytes", _sz, [_i, _i, _i, _i])
+_sig("svdq_kv4_append", _i, [_C, _vp, _i64, _i64, _vp, _i64, _i64, _i, _i, _vp, _vp])
+_sig("svdq_kv4_read", _i, [_C, _vp, _i, _vp, _vp, _i, _vp])
+_sig("svdq_kv4_attention_workspace_bytes", _sz, [_i, _i, _i, _i, _i])
+_sig("svdq_kv4_attention", _i, [_C, _vp, _i64, _i64, _i64, _i, _i, _i, _i, _vp, _i, _vp, ctypes.c_float, _vp, _vp,
+                                _sz, _vp])
+_sig("svdq_moe_route_workspace_bytes", _sz, [_i, _i])
+_sig("svdq_moe_route", _i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp])
+_sig("awq_moe_workspace_bytes", _sz, [_i, _i, _i, _i])
+_sig("awq_moe_forward", _i, [ctypes.POINTER(MoeWeights), _vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp])
 
 
 class SvdqError(RuntimeError):
@@ -665,6 +694,249 @@ def awq_forward(layer: AwqLinear, x: torch.Tensor, bias: Optional[torch.Tensor] 
     _check(_lib.awq_w4a16_forward(layer.blob.data_ptr(), layer.N, layer.K, x.data_ptr(), M,
                                   None if bias is None else bias.data_ptr(), out.data_ptr(),
                                   _stream(x.device)), "awq_w4a16_forward")
+    return out
+
+
+# ------------------------------------------------- 4-bit key/value cache
+_DT16 = {torch.bfloat16: BF16, torch.float16: FP16}
+
+
+def _need(t, name: str, device, dtypes, ndim: int) -> None:
+    """A device operand: a tensor of an accepted dtype and rank on `device`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes or t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions and a dtype of {tuple(dtypes)}, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _need_dense(t, name: str, device, dtypes, shape) -> None:
+    _need(t, name, device, dtypes, len(shape))
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _stride(t: torch.Tensor, i: int) -> int:
+    """The stride of dimension i, 0 where it has one element (torch leaves any value there)."""
+    return t.stride(i) if t.shape[i] > 1 else 0
+
+
+def _call(device, f, *args) -> None:
+    """A device entry point on `device`'s current stream."""
+    if torch.cuda.current_device() == device.index:
+        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != OK:
+        raise SvdqError(status, f.__name__)
+
+
+class Kv4Cache:
+    """A paged key/value cache in MXFP4 on one device.  Slot s is token
+    s % page_size of page s // page_size; what is in which page is the caller's
+    bookkeeping."""
+
+    def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
+        n = _lib.svdq_kv4_cache_bytes(num_pages, page_size, kv_heads, head_dim)
+        if n == 0:
+            raise SvdqError(2, "svdq_kv4_cache_bytes")
+        self.num_pages, self.page_size = num_pages, page_size
+        self.kv_heads, self.head_dim = kv_heads, head_dim
+        self.data = torch.zeros(n, dtype=torch.uint8, device=device)
+        self.device = self.data.device
+        self._c = Kv4CacheStruct(self.data.data_ptr(), num_pages, page_size, kv_heads, head_dim)
+
+
+def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """Encodes key and value rows [T, kv_heads, head_dim] (bf16 or fp16; any row and
+    head strides that are multiples of 8) into the cache's slots [T] (int32, all different; slots
+    outside the cache, such as -1, are skipped)."""
+    for t, name in ((k, "k"), (v, "v")):
+        _need(t, name, cache.device, _DT16, 3)
+        if t.shape[1] != cache.kv_heads or t.shape[2] != cache.head_dim or t.stride(2) != 1:
+            raise ValueError(f"{name} must be [T, {cache.kv_heads}, {cache.head_dim}] with adjacent channels, "
+                             f"got {tuple(t.shape)} with strides {t.stride()}")
+    T = k.shape[0]
+    if v.shape[0] != T or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same rows and dtype")
+    _need_dense(slots, "slots", cache.device, (torch.int32,), (T,))
+    _call(cache.device, _lib.svdq_kv4_append, ctypes.byref(cache._c), k.data_ptr(), _stride(k, 0), _stride(k, 1),
+          v.data_ptr(), _stride(v, 0), _stride(v, 1), _DT16[k.dtype], T, slots.data_ptr())
+
+
+def kv4_read(cache: Kv4Cache, slots: torch.Tensor, dtype=torch.bfloat16):
+    """The values in the cache's slots [T] as (k, v) [T, kv_heads, head_dim], bf16 or float32 (both exact)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"dtype must be bfloat16 or float32, got {dtype}")
+    _need(slots, "slots", cache.device, (torch.int32,), 1)
+    if not slots.is_contiguous():
+        raise ValueError("slots must be contiguous")
+    T = slots.shape[0]
+    k, v = (torch.empty((T, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device) for _ in "kv")
+    _call(cache.device, _lib.svdq_kv4_read, ctypes.byref(cache._c), slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
+          FP32 if dtype == torch.float32 else BF16)
+    return k, v
+
+
+def kv4_attention_workspace(cache: Kv4Cache, q: torch.Tensor) -> torch.Tensor:
+    """A workspace for kv4_attention calls with queries shaped like q [B, Q, Hq, head_dim]."""
+    n = _lib.svdq_kv4_attention_workspace_bytes(q.shape[0], q.shape[1], q.shape[2], cache.kv_heads, cache.head_dim)
+    if n == 0:
+        raise SvdqError(2, "svdq_kv4_attention_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def kv4_attention(cache: Kv4Cache, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of the last Q tokens of each of B sequences over the
+    cache: q [B, Q, Hq, head_dim] (bf16 or fp16; strides multiples of 8), page_table
+    [B, n] and seq_lens [B] int32 on the device (seq_lens counts the new tokens).
+    Returns [B, Q, Hq, head_dim]; rows that see no token are zero.  scale: 1 / sqrt(head_dim) if not given."""
+    dev = cache.device
+    _need(q, "q", dev, _DT16, 4)
+    B, Q, Hq, D = q.shape
+    if D != cache.head_dim or q.stride(3) != 1:
+        raise ValueError(f"q must have {cache.head_dim} adjacent channels, got {tuple(q.shape)} with strides {q.stride()}")
+    _need(page_table, "page_table", dev, (torch.int32,), 2)
+    if page_table.shape[0] != B or not page_table.is_contiguous():
+        raise ValueError(f"page_table must be contiguous with {B} rows, got {tuple(page_table.shape)}")
+    _need_dense(seq_lens, "seq_lens", dev, (torch.int32,), (B,))
+    if out is None:
+        out = torch.empty((B, Q, Hq, D), dtype=q.dtype, device=dev)
+    else:
+        _need_dense(out, "out", dev, (q.dtype,), (B, Q, Hq, D))
+    if workspace is None:
+        workspace = kv4_attention_workspace(cache, q)
+    else:
+        _need_dense(workspace, "workspace", dev, (torch.uint8,), workspace.shape)
+    _call(dev, _lib.svdq_kv4_attention, ctypes.byref(cache._c), q.data_ptr(), _stride(q, 0), _stride(q, 1),
+          _stride(q, 2), _DT16[q.dtype], B, Q, Hq, page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
+          D ** -0.5 if scale is None else float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+# ------------------------------------------------------- mixture of experts
+def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, bias: Optional[torch.Tensor] = None,
+              score: str = "softmax", normalize: bool = True, workspace: Optional[torch.Tensor] = None):
+    """The top_k experts of each row of x [T, K] by the softmax or sigmoid of
+    x w_router^T (w_router [E, K]), plus bias [E] for the choice: (ids int32,
+    weights float32), both [T, top_k], best first, ties to the lower index."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
+    _need(x, "x", dev, _DT16, 2)
+    T, K = x.shape
+    _need(w_router, "w_router", dev, (x.dtype,), 2)
+    E = w_router.shape[0]
+    if not x.is_contiguous() or not w_router.is_contiguous() or w_router.shape[1] != K:
+        raise ValueError(f"x and w_router must be contiguous [T, K] and [E, K], got {tuple(x.shape)} and "
+                         f"{tuple(w_router.shape)}")
+    if score not in MOE_SCORES:
+        raise ValueError(f"score must be one of {tuple(MOE_SCORES)}, got {score!r}")
+    if bias is not None:
+        _need_dense(bias, "bias", dev, (torch.float32,), (E,))
+    if workspace is None:
+        n = _lib.svdq_moe_route_workspace_bytes(T, E)
+        if n == 0:
+            raise SvdqError(2, "svdq_moe_route_workspace_bytes")
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    else:
+        _need_dense(workspace, "workspace", dev, (torch.uint8,), workspace.shape)
+    if not 1 <= top_k <= E:
+        raise ValueError(f"top_k={top_k} outside [1, {E}]")
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    _call(dev, _lib.svdq_moe_route, x.data_ptr(), w_router.data_ptr(), None if bias is None else bias.data_ptr(),
+          _DT16[x.dtype], T, E, K, top_k, MOE_SCORES[score], int(bool(normalize)), ids.data_ptr(), weights.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return ids, weights
+
+
+def _moe_blobs(qsz, N: int, K: int) -> np.ndarray:
+    """E AWQ weights (codes [E, N, K/2], scales and zeros [E, N, K/64]) packed one after another."""
+    from concurrent.futures import ThreadPoolExecutor
+    q, s, z = (np.ascontiguousarray(t.cpu().numpy() if isinstance(t, torch.Tensor) else t) for t in qsz)
+    E = q.shape[0]
+    if q.shape != (E, N, K // 2) or q.dtype != np.uint8 or s.shape != (E, N, K // 64) or s.shape != z.shape \
+            or s.dtype != np.float16 or z.dtype != np.float16:
+        raise ValueError(f"expert weights must be codes uint8 [E, {N}, {K // 2}] with float16 scales and zeros "
+                         f"[E, {N}, {K // 64}], got {q.shape} {q.dtype}, {s.shape} {s.dtype}, {z.shape} {z.dtype}")
+    n = _lib.awq_device_weights_bytes(N, K)
+    if n == 0:
+        raise SvdqError(2, "awq_device_weights_bytes")
+    blobs = np.empty((E, n), np.uint8)
+
+    def pack(e):                         # the library call runs without the interpreter's lock
+        _check(_lib.awq_pack_device_weights(_ptr(q[e]), _ptr(s[e]), _ptr(z[e]), N, K, _ptr(blobs[e]), n),
+               "awq_pack_device_weights")
+
+    with ThreadPoolExecutor(min(len(os.sched_getaffinity(0)), 16)) as pool:
+        list(pool.map(pack, range(E)))
+    return blobs
+
+
+class AwqMoe:
+    """The experts of a mixture-of-experts layer as AWQ W4A16 linears, resident
+    on one device.  gate_up and down are (codes uint8 [E, N, K/2], scales float16
+    [E, N, K/64], zeros float16 [E, N, K/64]), arrays or tensors, as
+    awq_quantize_weights gives them for each expert: gate_up with the I gate rows and
+    then the I up rows over K channels, down with K rows over I channels."""
+
+    def __init__(self, gate_up, down, device="cuda"):
+        self.E, self.K, self.I = gate_up[0].shape[0], gate_up[0].shape[2] * 2, gate_up[0].shape[1] // 2
+        if down[0].shape[0] != self.E or down[0].shape[1] != self.K or down[0].shape[2] * 2 != self.I \
+                or gate_up[0].shape[1] != 2 * self.I:
+            raise ValueError(f"gate_up {tuple(gate_up[0].shape)} and down {tuple(down[0].shape)} do not make an expert layer")
+        if _lib.awq_moe_workspace_bytes(1, 1, self.K, self.I) == 0:
+            raise SvdqError(2, "awq_moe_workspace_bytes")
+        self.gate_up = torch.from_numpy(_moe_blobs(gate_up, 2 * self.I, self.K)).to(device)
+        self.down = torch.from_numpy(_moe_blobs(down, self.K, self.I)).to(device)
+        self.device = self.gate_up.device
+        self._w = MoeWeights(self.gate_up.data_ptr(), self.down.data_ptr(), self.E, self.K, self.I)
+
+    def workspace_bytes(self, T: int, top_k: int) -> int:
+        n = _lib.awq_moe_workspace_bytes(T, top_k, self.K, self.I)
+        if n == 0:
+            raise SvdqError(2, "awq_moe_workspace_bytes")
+        return n
+
+    def new_workspace(self, T: int, top_k: int) -> torch.Tensor:
+        return torch.empty(self.workspace_bytes(T, top_k), dtype=torch.uint8, device=self.device)
+
+
+def awq_moe_forward(layer: AwqMoe, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                    activation: str = "silu", out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[t] = sum_j weights[t, j] Down_e(act(Gate_e x[t]) * Up_e x[t]) with
+    e = ids[t, j]: x [T, K] bf16 or fp16, ids int32 and weights float32 [T, top_k] (from
+    moe_route); ids outside the experts add nothing.  For few tokens (T top_k <= 4096)."""
+    dev = layer.device
+    _need(x, "x", dev, _DT16, 2)
+    T = x.shape[0]
+    if x.shape[1] != layer.K or not x.is_contiguous():
+        raise ValueError(f"x must be contiguous [T, {layer.K}], got {tuple(x.shape)}")
+    _need(ids, "ids", dev, (torch.int32,), 2)
+    top_k = ids.shape[1]
+    if ids.shape[0] != T or not ids.is_contiguous():
+        raise ValueError(f"ids must be contiguous with {T} rows, got {tuple(ids.shape)}")
+    _need_dense(weights, "weights", dev, (torch.float32,), (T, top_k))
+    if activation not in MOE_ACTIVATIONS:
+        raise ValueError(f"activation must be one of {tuple(MOE_ACTIVATIONS)}, got {activation!r}")
+    if out is None:
+        out = torch.empty((T, layer.K), dtype=x.dtype, device=dev)
+    else:
+        _need_dense(out, "out", dev, (x.dtype,), (T, layer.K))
+    if workspace is None:
+        workspace = layer.new_workspace(T, top_k)
+    else:
+        _need_dense(workspace, "workspace", dev, (torch.uint8,), workspace.shape)
+    _call(dev, _lib.awq_moe_forward, ctypes.byref(layer._w), x.data_ptr(), _DT16[x.dtype], T, ids.data_ptr(),
+          weights.data_ptr(), top_k, MOE_ACTIVATIONS[activation], out.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
     return out
 
 

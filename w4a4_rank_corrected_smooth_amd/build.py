@@ -1,5 +1,5 @@
 """Builds libsvdq.so in-tree: host translation units with g++, the device
-translation unit with hipcc for gfx950, linked into one shared library next
+translation units with hipcc for gfx950, linked into one shared library next
 to this file.  Usable without torch or a built library:  python w4a4_rank_corrected_smooth_amd/build.py
 """
 from __future__ import annotations
@@ -27,7 +27,7 @@ HOST_UNITS = {
     "host_threads.cpp": [],
     "host_linalg.cpp": ["-ffp-contract=fast"],
 }
-DEVICE_UNITS = ["device.hip"]
+DEVICE_UNITS = ["device.hip", "kv4.hip", "moe.hip"]
 DEVICE_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
                 "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
                 "-Wno-unused-result", f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -7,7 +7,9 @@
 
 #include "common.h"
 #include "host_prepare.h"
+#include "kv4_layout.h"
 #include "layout.h"
+#include "moe_layout.h"
 
 namespace svdq {
 
@@ -266,6 +268,40 @@ svdq_status_t awq_pack_device_weights(const uint8_t *q, const uint16_t *s, const
   if (!q || !s || !z || !blob) return fail(SVDQ_ERR_INVALID_ARGUMENT, "awq_pack: NULL");
   if (!shape_ok(N, K, 0, "awq_pack_device_weights", &st)) return st;
   return awq_pack(q, s, z, N, K, blob, bytes);
+}
+
+size_t svdq_kv4_cache_bytes(int num_pages, int page_size, int kv_heads, int head_dim) {
+  if (!kv4_shape_ok(num_pages, page_size, kv_heads, head_dim)) {
+    fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_cache_bytes: %d pages of %d tokens, %d heads of %d channels", num_pages,
+         page_size, kv_heads, head_dim);
+    return 0;
+  }
+  return (size_t)Kv4Layout(num_pages, page_size, kv_heads, head_dim).total();
+}
+
+size_t svdq_kv4_attention_workspace_bytes(int B, int Q, int Hq, int kv_heads, int head_dim) {
+  if (!kv4_shape_ok(1, 16, kv_heads, head_dim) || !kv4_query_ok(B, Q, Hq, kv_heads)) {
+    fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_attention_workspace_bytes: B=%d Q=%d Hq=%d over %d heads of %d channels",
+         B, Q, Hq, kv_heads, head_dim);
+    return 0;
+  }
+  return (size_t)kv4_workspace_bytes(Q, Hq, kv_heads, head_dim);
+}
+
+size_t svdq_moe_route_workspace_bytes(int T, int E) {
+  if (!moe_route_ok(T, E, 8, 1)) {
+    fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_moe_route_workspace_bytes: T=%d E=%d", T, E);
+    return 0;
+  }
+  return (size_t)round_up((T > 0 ? T : 1) * (int64_t)E * 8, kAlign);
+}
+
+size_t awq_moe_workspace_bytes(int T, int top_k, int K, int I) {
+  if (!moe_weights_ok(1, K, I) || !moe_call_ok(T, top_k)) {
+    fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "awq_moe_workspace_bytes: T=%d top_k=%d K=%d I=%d", T, top_k, K, I);
+    return 0;
+  }
+  return (size_t)MoeWork(T > 0 ? T : 1, top_k, K, I).total;
 }
 
 }  // extern "C"

@@ -1,0 +1,47 @@
+// Layout and limits of the MXFP4 key/value cache, shared by the host's size
+// queries and the device kernels (kv4.hip describes a unit's bytes).
+#pragma once
+
+#include <stdint.h>
+
+namespace svdq {
+
+// Workgroups of an attention call at most: four for each of the 256 CUs.
+constexpr int kKv4Groups = 1024;
+// Rows (new tokens times query heads of one key/value head) at most.
+constexpr int kKv4MaxRows = 1024;
+
+constexpr bool kv4_shape_ok(int64_t pages, int page_size, int H, int D) {
+  return pages >= 1 && page_size >= 16 && page_size <= 256 && (page_size & (page_size - 1)) == 0 && H >= 1 &&
+         H <= 1024 && (D == 64 || D == 128 || D == 256) && pages * page_size <= 0x7FFFFFFF;
+}
+constexpr bool kv4_query_ok(int64_t B, int64_t Q, int64_t Hq, int64_t H) {
+  return B >= 0 && B <= 65536 && Q >= 1 && Hq >= 1 && Hq % H == 0 && Q * (Hq / H) <= kKv4MaxRows &&
+         B * Q * Hq <= (1 << 24);
+}
+
+// bytes of an attention call's workspace: two running states for each workgroup
+constexpr int64_t kv4_workspace_bytes(int64_t Q, int64_t Hq, int64_t H, int64_t D) {
+  const int64_t rows = Q * (Hq / H), block = rows < 32 ? rows : 32;
+  return 2 * (int64_t)kKv4Groups * block * (D + 2) * 4;
+}
+
+struct Kv4Layout {
+  int pages = 0, page_shift = 0, H = 0, D = 0;
+  constexpr Kv4Layout() = default;
+  constexpr Kv4Layout(int pages_, int page_size_, int H_, int D_) : pages(pages_), H(H_), D(D_) {
+    for (page_shift = 4; (1 << page_shift) < page_size_;) ++page_shift;
+  }
+  constexpr int page_size() const { return 1 << page_shift; }
+  constexpr int64_t unit_bytes() const { return 17 * (int64_t)D; }
+  // byte offset of unit u (16 tokens) of head h in a page
+  constexpr int64_t unit(int64_t page, int h, int u) const {
+    return (((page * H + h) << (page_shift - 4)) + u) * unit_bytes();
+  }
+  constexpr int v_codes() const { return 8 * D; }
+  constexpr int k_scales() const { return 16 * D; }
+  constexpr int v_scales() const { return 16 * D + D / 2; }
+  constexpr int64_t total() const { return unit(pages, 0, 0); }
+};
+
+}  // namespace svdq
