@@ -194,9 +194,11 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(const uint8_t *__restrict
 // Work split: the tokens of each (sequence, head, block of rows) are cut
 // into chunks of 128 (32 for each wavefront at a time); all chunks of the
 // call form one line, of which each workgroup takes an equal piece, so short
-// and long sequences share the machine evenly.  A workgroup that holds all
-// chunks of a (sequence, head) writes the output, otherwise its running
-// state, which kv4_join_kernel joins in order.
+// and long sequences share the machine evenly.  Beginning and ending a
+// (sequence, head) takes about as long as kStart chunks, which stand on the
+// line before its first one.  A workgroup that holds all chunks of a
+// (sequence, head) writes the output, otherwise its running state, which
+// kv4_join_kernel joins in order.
 struct AttendArgs {
   const uint8_t *data;
   Kv4Layout L;
@@ -206,56 +208,62 @@ struct AttendArgs {
   int width;                    // entries of a page-table row
   const int *lens;
   int B, Q, group, rows, row_blocks, block_rows;   // block_rows = min(rows, 16 NT)
-  float scale;                  // softmax scale times log2(e)
+  float scale;                  // |softmax scale| log2(e), positive
+  uint32_t flip;                // sign bits of the queries to turn, for a negative scale
   uint16_t *out;
   float *part;                  // [2 W][block_rows][D], then [2 W][block_rows][2]
   int W;
 };
 
-constexpr int kChunk = 128;
 
 __device__ __forceinline__ int seq_len(const AttendArgs &a, int b) {
   return min(max(a.lens[b], 0), (int)min((int64_t)a.width << a.L.page_shift, (int64_t)1 << 30));
 }
-__device__ __forceinline__ int seq_chunks(int len) { return max(1, (len + kChunk - 1) / kChunk); }
+__device__ __forceinline__ int seq_chunks(int len) { return max(1, (len + kKv4Chunk - 1) / kKv4Chunk); }
 
-// sum of x over the wavefront, and over lanes 0..lane
-__device__ __forceinline__ int64_t wave_sum(int64_t x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+// sum of x over lanes 0..lane, within the vector unit (16 lanes at a time,
+// then the last lane of a row into the next rows)
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);    // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);    // row_bcast:15
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);    // row_bcast:31
   return x;
 }
-__device__ __forceinline__ int64_t wave_scan(int64_t x, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t y = __shfl_up(x, o);
-    if (lane >= o) x += y;
+
+// The line of a call, for one key/value head and block of rows: a sequence
+// takes its chunks and kKv4Start.  The wavefront looks at 64 sequences at a
+// time: their lengths in tokens, and where their parts of the line end.
+struct Line {
+  int base = -64, len = 0, upto = 0;
+  // sequences base.., the line before them being `before` long; returns its length after them
+  __device__ __forceinline__ int look(const AttendArgs &a, int base_, int before, int lane) {
+    base = base_;
+    len = base + lane < a.B ? seq_len(a, base + lane) : 0;
+    upto = before + wave_scan(base + lane < a.B ? seq_chunks(len) + kKv4Start : 0);
+    return __builtin_amdgcn_readlane(upto, 63);
   }
-  return x;
-}
-// chunks of all sequences before `b` (times 1), and of all
-__device__ __forceinline__ void chunks_before(const AttendArgs &a, int b, int lane, int64_t &before, int64_t &all) {
-  int64_t x = 0, y = 0;
-  for (int i = lane; i < a.B; i += 64) {
-    const int n = seq_chunks(seq_len(a, i));
-    y += n;
-    if (i < b) x += n;
-  }
-  before = wave_sum(x);
-  all = wave_sum(y);
+};
+// The whole line's length; `line` is left at the last sequences.
+__device__ __forceinline__ int line_length(const AttendArgs &a, Line &line, int lane) {
+  int all = 0;
+  for (int base = 0; base < a.B; base += 64) all = line.look(a, base, all, lane);
+  return all;
 }
 
 template <int D>
-struct Tile {                       // two units of 16 tokens
-  uint32_t k[2][D / 32], v[2][D / 32], ks[2][(D + 127) / 128], vs[2][D / 32];
-};
+struct Keys { uint32_t k[2][D / 32], s[2][(D + 127) / 128]; };     // two units of 16 tokens
+template <int D>
+struct Values { uint32_t v[2][D / 32], s[2][D / 32]; };
 
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
   if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
+      const v4u u = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(p) + i);
       w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
     }
   } else if constexpr (N == 2) {
@@ -266,21 +274,56 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
   }
 }
 
-// The unit of tokens [t, t + 16) of sequence b; `ok` is false where the page
-// table has no valid page for it (page 0 is read in its place).
+// The pages of a sequence, 64 entries of its page-table row at a time in the
+// lanes of a register, so that a tile's page costs no trip to memory.
+struct Pages {
+  const int *row;
+  int width, pages, first, lanes;   // entries [first, first + 64)
+  // The load is waited for here: left to its use, where the paths with and
+  // without it meet, the wait would also hold up the tiles being copied.
+  __device__ __forceinline__ void load(int at, int lane) {
+    first = at;
+    lanes = row[min(at + lane, width - 1)];
+    __builtin_amdgcn_s_waitcnt(0x0F70);     // vmcnt(0)
+  }
+  // entry `at` (the same in every lane), -1 if it names no page
+  __device__ __forceinline__ int get(int at, int lane) {
+    if (at >= first + 64) load(at, lane);
+    const int p = __builtin_amdgcn_readlane(lanes, at - first);
+    return at < width && p >= 0 && p < pages ? p : -1;
+  }
+};
+
+// The units of tokens [t, t + 16) and [t + 16, t + 32) of a sequence, and
+// whether they have a page (page 0 is read in the place of one that has none).
+struct Place { const uint8_t *unit[2]; bool ok[2]; };
 template <int D>
-__device__ __forceinline__ void load_unit(const AttendArgs &a, const int *row, int h, int t, int lane,
-                                          Tile<D> &x, int u, bool &ok) {
-  const int at = t >> a.L.page_shift;
-  int page = row[min(at, a.width - 1)];
-  ok = at < a.width && page >= 0 && page < a.L.pages;
-  page = __builtin_amdgcn_readfirstlane(ok ? page : 0);
-  const uint8_t *unit = a.data + a.L.unit(page, h, (t & (a.L.page_size() - 1)) >> 4);
-  load_words(x.k[u], unit + lane * (D / 8));
-  load_words(x.v[u], unit + 8 * D + lane * (D / 8));
-  if constexpr (D == 64) x.ks[u][0] = *reinterpret_cast<const uint16_t *>(unit + 16 * D + (lane & 15) * 2);
-  else load_words(x.ks[u], unit + 16 * D + (lane & 15) * (D / 32));
-  load_words(x.vs[u], unit + 16 * D + D / 2 + (lane >> 4) * (D / 8));
+__device__ __forceinline__ Place locate(const AttendArgs &a, Pages &pages, int h, int t, int lane) {
+  Place p;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int page = pages.get((t + 16 * u) >> a.L.page_shift, lane);
+    p.ok[u] = page >= 0;
+    p.unit[u] = a.data + a.L.unit(max(page, 0), h, ((t + 16 * u) & (a.L.page_size() - 1)) >> 4);
+  }
+  return p;
+}
+template <int D>
+__device__ __forceinline__ void load_keys(const Place &p, int lane, Keys<D> &x) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    load_words(x.k[u], p.unit[u] + lane * (D / 8));
+    if constexpr (D == 64) x.s[u][0] = *reinterpret_cast<const uint16_t *>(p.unit[u] + 16 * D + (lane & 15) * 2);
+    else load_words(x.s[u], p.unit[u] + 16 * D + (lane & 15) * (D / 32));
+  }
+}
+template <int D>
+__device__ __forceinline__ void load_values(const Place &p, int lane, Values<D> &x) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    load_words(x.v[u], p.unit[u] + 8 * D + lane * (D / 8));
+    load_words(x.s[u], p.unit[u] + 16 * D + D / 2 + (lane >> 4) * (D / 8));
+  }
 }
 
 // Byte i of `w` as the power of two it stands for.  The conversion reads
@@ -297,8 +340,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v2bf{(__bf16)a, (__bf16)b});
 }
 
+// the largest x of the four lanes of a column (l % 16)
+__device__ __forceinline__ float column_max(float x) {
+  const uint32_t u = __float_as_uint(x);
+  auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  const uint32_t v = __float_as_uint(x);
+  r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Registers: at least two wavefronts a SIMD keeps the matrix accumulators in
+// ordinary registers (with all 512 allowed, the compiler moves them to and from
+// the accumulation registers around every tile).
 template <int D, int NT, bool F16>
-__global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D, NT)))) void kv4_attend_kernel(AttendArgs a) {
   constexpr int NB = D / 32;                       // blocks of 32 channels
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c4 = lane >> 4;
@@ -306,40 +362,41 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
   __shared__ v4f so[2][NT * 2 * NB][64];
 
   const int HR = a.L.H * a.row_blocks;
-  int64_t before, all;
-  chunks_before(a, 0, lane, before, all);
-  const int64_t per = (all * HR + a.W - 1) / a.W;
-  const int64_t u0 = blockIdx.x * per, u1 = min(u0 + per, all * HR);
+  Line line;
+  const int all = line_length(a, line, lane) * HR;
+  const int per = (all + a.W - 1) / a.W;
+  const int u0 = blockIdx.x * per, u1 = min(u0 + per, all);
   if (u0 >= u1) return;
-  // the sequence that holds chunk u0, and the chunks before it
-  int b = 0;
-  int64_t start = 0;
-  for (int base = 0; base < a.B; base += 64) {
-    const int64_t n = base + lane < a.B ? (int64_t)HR * seq_chunks(seq_len(a, base + lane)) : 0;
-    const int64_t upto = start + wave_scan(n, lane);
-    const uint64_t past = __ballot(upto > u0);
+  // the sequence that u0 falls into, and where it begins
+  int b = 0, start = 0;
+  for (int base = 0, before = 0;; base += 64) {
+    if (line.base != base) line.look(a, base, before, lane);
+    const uint64_t past = __ballot(line.upto * HR > u0);
+    before = __builtin_amdgcn_readlane(line.upto, 63);
     if (past) {
       const int i = __builtin_ctzll(past);
       b = base + i;
-      start = __shfl(upto - n, i);
+      start = (__builtin_amdgcn_readlane(line.upto, i) - kKv4Start -
+               seq_chunks(__builtin_amdgcn_readlane(line.len, i))) * HR;
       break;
     }
-    start = __shfl(upto, 63);
   }
 
-  int64_t u = u0;
+  int u = u0;
   while (u < u1) {
-    b = __builtin_amdgcn_readfirstlane(b);
-    const int len = __builtin_amdgcn_readfirstlane(seq_len(a, b));
-    const int n = seq_chunks(len);
-    const int hr = __builtin_amdgcn_readfirstlane((int)((u - start) / n));
-    const int ch0 = __builtin_amdgcn_readfirstlane((int)((u - start) % n));
-    const int ch1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)n, ch0 + (u1 - u)));
+    if (b - line.base >= 64) line.look(a, line.base + 64, 0, lane);
+    const int len = __builtin_amdgcn_readlane(line.len, b - line.base);
+    const int n = seq_chunks(len), span = n + kKv4Start;
+    const int hr = __builtin_amdgcn_readfirstlane((u - start) / span);
+    const int at = u - start - hr * span;                 // place in this (sequence, head)
+    const int ch0 = max(at - kKv4Start, 0), ch1 = min(at - kKv4Start + u1 - u, n);
+    const int next = start + (hr + 1) * span;
+    const int next_b = hr + 1 == HR ? b + 1 : b, next_start = hr + 1 == HR ? next : start;
+    if (ch1 <= 0) break;                                  // the line ends before the first chunk
     const int h = hr / a.row_blocks, r0 = hr % a.row_blocks * (16 * NT);
-    const int *table = a.table + (int64_t)b * a.width;
-
     // queries: row r = i * group + j is new token i, head h * group + j
-    v8bf qh[NT][NB], ql[NT][F16 ? NB : 1];
+    // (asked for before the pages, which are waited for)
+    uint4 qv[NT][NB];
     int limit[NT];                                 // tokens that the lane's row sees
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
@@ -349,8 +406,17 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
       limit[x] = min(len, len - a.Q + i + 1);
       const uint16_t *src = a.q + b * a.q_b + i * a.q_i + (int64_t)(h * a.group + j) * a.q_h + 8 * c4;
 #pragma unroll
+      for (int s = 0; s < NB; ++s)
+        qv[x][s] = real ? *reinterpret_cast<const uint4 *>(src + 32 * s) : make_uint4(0, 0, 0, 0);
+    }
+    Pages pages{a.table + (int64_t)b * a.width, a.width, a.L.pages, 0, 0};
+    pages.load(ch0 * kKv4Chunk >> a.L.page_shift, lane);
+    v8bf qh[NT][NB], ql[NT][F16 ? NB : 1];
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
       for (int s = 0; s < NB; ++s) {
-        uint4 v = real ? *reinterpret_cast<const uint4 *>(src + 32 * s) : make_uint4(0, 0, 0, 0);
+        const uint4 v = make_uint4(qv[x][s].x ^ a.flip, qv[x][s].y ^ a.flip, qv[x][s].z ^ a.flip, qv[x][s].w ^ a.flip);
         if constexpr (F16) {
           const uint32_t in[4] = {v.x, v.y, v.z, v.w};
           uint32_t hi[4], lo[4];
@@ -367,7 +433,6 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
           qh[x][s] = as_v8bf(v);
         }
       }
-    }
 
     float m[NT], l[NT];
     v4f o[NT][2 * NB];
@@ -379,23 +444,26 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
       for (int i = 0; i < 2 * NB; ++i) o[x][i] = v4f{};
     }
 
-    const int t1 = min(ch1 * kChunk, len);
+    const int t1 = min(ch1 * kKv4Chunk, len);
     const int whole = len - a.Q + 1;               // tokens that every row sees
-    int t = ch0 * kChunk + 32 * w;
-    Tile<D> cur;
-    bool ok[2] = {true, true};
-    if (t < t1) {
-      load_unit<D>(a, table, h, t, lane, cur, 0, ok[0]);
-      load_unit<D>(a, table, h, t + 16, lane, cur, 1, ok[1]);
+    // One tile's keys and one tile's values are in registers; the next ones
+    // are asked for as soon as these are used up, so the keys arrive while
+    // the weights and the values are worked on, the values while the keys
+    // are.  The loads are unconditional (past the end, one line of the last
+    // tile), so that the number outstanding is known at every wait.
+    const int tw = ch0 * kKv4Chunk + 32 * w;
+    const int last = tw + (t1 - 1 - tw) / kKv4Chunk * kKv4Chunk;
+    Keys<D> keys;
+    Values<D> vals;
+    Place place;
+    if (tw < t1) {
+      place = locate<D>(a, pages, h, tw, lane);
+      load_keys<D>(place, lane, keys);
+      load_values<D>(place, lane, vals);
     }
-    while (t < t1) {
-      Tile<D> nxt;
-      bool nok[2] = {true, true};
-      if (t + kChunk < t1) {
-        load_unit<D>(a, table, h, t + kChunk, lane, nxt, 0, nok[0]);
-        load_unit<D>(a, table, h, t + kChunk + 16, lane, nxt, 1, nok[1]);
-      }
-      const bool edge = t + 32 > whole || !ok[0] || !ok[1];
+    for (int t = tw; t < t1; t += kKv4Chunk) {
+      const Place next = locate<D>(a, pages, h, min(t + kKv4Chunk, last), lane);
+      const int nlane = t < last ? lane : 0;
       v4f s[NT][2];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -403,8 +471,8 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
         for (int x = 0; x < NT; ++x) s[x][g] = v4f{};
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-          const float sc = scale_of(cur.ks[g][k / 4], k % 4);
-          const uint32_t kw = cur.k[g][k];
+          const float sc = scale_of(keys.s[g][k / 4], k % 4);
+          const uint32_t kw = keys.k[g][k];
           const v8bf ka = as_v8bf(make_uint4(two_values<0>(kw, sc), two_values<1>(kw, sc), two_values<2>(kw, sc),
                                              two_values<3>(kw, sc)));
 #pragma unroll
@@ -414,14 +482,9 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
           }
         }
       }
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[x][g][i] *= a.scale;
-      if (edge) {
-        // after the scale, which may be negative or zero: rows' own limits, and units without a page
+      load_keys<D>(next, nlane, keys);
+      if (t + 32 > whole || !place.ok[0] || !place.ok[1]) {
+        // rows' own limits, and units without a page
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
 #pragma unroll
@@ -429,52 +492,50 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
             const int tok = t + 16 * g + 4 * c4 + i;
 #pragma unroll
             for (int x = 0; x < NT; ++x)
-              if (!ok[g] || tok >= limit[x]) s[x][g][i] = -__builtin_inff();
+              if (!place.ok[g] || tok >= limit[x]) s[x][g][i] = -__builtin_inff();
           }
           // what stands in the cache past the end may be anything, and zero
           // times it must be zero: such tokens' codes and scales are cleared
           uint32_t keep = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (ok[g] && t + 16 * g + 4 * c4 + i < len) keep |= 0xFFu << (8 * i);
+            if (place.ok[g] && t + 16 * g + 4 * c4 + i < len) keep |= 0xFFu << (8 * i);
 #pragma unroll
-          for (int k = 0; k < NB; ++k) cur.v[g][k] &= keep;
+          for (int k = 0; k < NB; ++k) vals.v[g][k] &= keep;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int k = 0; k < NB; ++k)
-              if (!(keep >> (8 * i) & 1u)) cur.vs[g][(i * NB + k) / 4] &= ~(0xFFu << (8 * ((i * NB + k) % 4)));
+              if (!(keep >> (8 * i) & 1u)) vals.s[g][(i * NB + k) / 4] &= ~(0xFFu << (8 * ((i * NB + k) % 4)));
         }
       }
-      // running maximum and weights
+      // running maximum (of the bare products) and weights
       v8bf ph[NT], pl[NT];
 #pragma unroll
       for (int x = 0; x < NT; ++x) {
-        float top = -__builtin_inff();
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, s[x][g][i]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float now = fmaxf(m[x], top);
-        const float ref = now == -__builtin_inff() ? 0.0f : now;
-        if (__ballot(now > m[x])) {
-          const float f = __builtin_amdgcn_exp2f(m[x] - ref);
-          l[x] *= f;
+        const v4f s0 = s[x][0], s1 = s[x][1];
+        const float top = column_max(fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])),
+                                           fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3]))));
+        if (__ballot(top > m[x])) {
+          const float now = fmaxf(m[x], top);
+          const float f = __builtin_amdgcn_exp2f((m[x] - now) * a.scale);
+          m[x] = now;
+          // a row that has seen no token yet keeps nothing (f is not a number there)
+          const float g = now == -__builtin_inff() ? 0.0f : f;
+          l[x] *= g;
 #pragma unroll
           for (int i = 0; i < 2 * NB; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[x][i][e] *= f;
-          m[x] = now;
+            for (int e = 0; e < 4; ++e) o[x][i][e] *= g;
         }
+        const float ref = m[x] == -__builtin_inff() ? 0.0f : m[x] * a.scale;
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float p0 = __builtin_amdgcn_exp2f(s[x][g][2 * i] - ref);
-            const float p1 = __builtin_amdgcn_exp2f(s[x][g][2 * i + 1] - ref);
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][g][2 * i], a.scale, -ref));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][g][2 * i + 1], a.scale, -ref));
             l[x] += p0 + p1;
             const uint32_t pk = pack_bf16(p0, p1);
             hi[2 * g + i] = pk;
@@ -488,11 +549,11 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
         uint32_t lo[4], hi[4];                     // channels 32 k + col, and 16 above
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const uint32_t vw = cur.v[g][k];
-          const uint32_t x0 = two_values<0>(vw, scale_of(cur.vs[g][k / 4], k % 4));
-          const uint32_t x1 = two_values<1>(vw, scale_of(cur.vs[g][(NB + k) / 4], (NB + k) % 4));
-          const uint32_t x2 = two_values<2>(vw, scale_of(cur.vs[g][(2 * NB + k) / 4], (2 * NB + k) % 4));
-          const uint32_t x3 = two_values<3>(vw, scale_of(cur.vs[g][(3 * NB + k) / 4], (3 * NB + k) % 4));
+          const uint32_t vw = vals.v[g][k];
+          const uint32_t x0 = two_values<0>(vw, scale_of(vals.s[g][k / 4], k % 4));
+          const uint32_t x1 = two_values<1>(vw, scale_of(vals.s[g][(NB + k) / 4], (NB + k) % 4));
+          const uint32_t x2 = two_values<2>(vw, scale_of(vals.s[g][(2 * NB + k) / 4], (2 * NB + k) % 4));
+          const uint32_t x3 = two_values<3>(vw, scale_of(vals.s[g][(3 * NB + k) / 4], (3 * NB + k) % 4));
           lo[2 * g] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
           hi[2 * g] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
           lo[2 * g + 1] = __builtin_amdgcn_perm(x3, x2, 0x05040100u);
@@ -508,10 +569,8 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
           o[x][2 * k + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pl[x], o[x][2 * k + 1], 0, 0, 0);
         }
       }
-      cur = nxt;
-      ok[0] = nok[0];
-      ok[1] = nok[1];
-      t += kChunk;
+      load_values<D>(next, nlane, vals);
+      place = next;
     }
 
     // the four wavefronts' states meet: everything relative to the largest
@@ -520,6 +579,7 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
     for (int x = 0; x < NT; ++x) {
       l[x] += __shfl_xor(l[x], 16);
       l[x] += __shfl_xor(l[x], 32);
+      m[x] = m[x] * a.scale;
       if (c4 == 0) {
         sm[w][16 * x + col] = m[x];
         sl[w][16 * x + col] = l[x];
@@ -599,64 +659,82 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(AttendArgs a) {
       }
     }
     __syncthreads();
-    u += ch1 - ch0;
-    if (u >= start + (int64_t)HR * n) {
-      start += (int64_t)HR * n;
-      ++b;
-    }
+    u = next;
+    b = next_b;
+    start = next_start;
   }
 }
 
-// One workgroup per (sequence, new token, query head) whose chunks went to
-// more than one workgroup: the pieces' states, in order, relative to their
-// largest maximum.  Wavefront w takes pieces w, w + 4, ...; a lane holds
-// D / 64 channels.
-template <int D, bool F16>
+// One wavefront (WIDE: four, a workgroup) per (sequence, new token, query
+// head) whose chunks went to more than one workgroup: the pieces' states,
+// relative to their largest maximum, added in order.  A lane holds D / 64
+// channels; with four wavefronts, w takes pieces w, w + 4, ...
+template <int D, bool F16, bool WIDE>
 __global__ __launch_bounds__(256) void kv4_join_kernel(AttendArgs a) {
-  constexpr int V = D / 64;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  constexpr int V = D / 64, STEP = WIDE ? 4 : 1;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int Hq = a.L.H * a.group;
-  const int hq = blockIdx.x % Hq;
-  const int i = blockIdx.x / Hq % a.Q, b = blockIdx.x / Hq / a.Q;
+  const int row = WIDE ? blockIdx.x : blockIdx.x * 4 + w;
+  if (row >= a.B * a.Q * Hq) return;
+  const int hq = row % Hq, i = row / Hq % a.Q, b = row / Hq / a.Q;
   const int h = hq / a.group, r = i * a.group + hq % a.group;
   const int HR = a.L.H * a.row_blocks;
-  int64_t before, all;
-  chunks_before(a, b, lane, before, all);
-  const int n = seq_chunks(seq_len(a, b));
-  const int64_t per = (all * HR + a.W - 1) / a.W;
-  const int64_t first = before * HR + (int64_t)(h * a.row_blocks + r / a.block_rows) * n;
-  const int64_t g0 = first / per, g1 = (first + n - 1) / per;
+  Line line;
+  int all = 0, n = 0, first = 0;
+  for (int base = 0; base < a.B; base += 64) {
+    all = line.look(a, base, all, lane);
+    if (b >= base && b < base + 64) {
+      n = seq_chunks(__builtin_amdgcn_readlane(line.len, b - base));
+      first = (__builtin_amdgcn_readlane(line.upto, b - base) - n - kKv4Start) * HR;
+    }
+  }
+  const int per = (all * HR + a.W - 1) / a.W;
+  // the line's place of the first chunk, and the workgroups with a chunk
+  first += (h * a.row_blocks + r / a.block_rows) * (n + kKv4Start);
+  const int g0 = (first + kKv4Start) / per, g1 = (first + kKv4Start + n - 1) / per;
   if (g0 == g1) return;
-  const int pieces = (int)(g1 - g0 + 1);
+  const int pieces = g1 - g0 + 1;
   const int rb = r % a.block_rows;
   const float *ml = a.part + 2 * (int64_t)a.W * a.block_rows * D;
-  auto slot = [&](int p) { return 2 * (g0 + p) + (p == 0 && first > g0 * per ? 1 : 0); };
+  auto place = [&](int p) {
+    return (int64_t)(2 * (g0 + p) + (p == 0 && first > g0 * per ? 1 : 0)) * a.block_rows + rb;
+  };
   float top = -__builtin_inff();
-  for (int p = lane; p < pieces; p += 64) top = fmaxf(top, ml[(slot(p) * a.block_rows + rb) * 2]);
+  for (int p = lane; p < pieces; p += 64) top = fmaxf(top, ml[place(p) * 2]);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
   const float ref = top == -__builtin_inff() ? 0.0f : top;
   float acc[V] = {}, l = 0.0f;
-  for (int p = w; p < pieces; p += 4) {
-    const int64_t at = slot(p) * a.block_rows + rb;
+#pragma unroll 4
+  for (int p = WIDE ? w : 0; p < pieces; p += STEP) {
+    const int64_t at = place(p);
     const float f = __builtin_amdgcn_exp2f(ml[at * 2] - ref);
     l = __builtin_fmaf(ml[at * 2 + 1], f, l);
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = __builtin_fmaf(a.part[at * D + lane * V + e], f, acc[e]);
   }
-  __shared__ float so[4][D], sl[4];
+  if constexpr (WIDE) {
+    __shared__ float so[3][D], sl[3];
+    if (w > 0) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) so[w][lane * V + e] = acc[e];
-  if (lane == 0) sl[w] = l;
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d < D) {
-    const float sum = (sl[0] + sl[1]) + (sl[2] + sl[3]);
-    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    const float y = ((so[0][d] + so[1][d]) + (so[2][d] + so[3][d])) * inv;
-    const int64_t at = (((int64_t)b * a.Q + i) * Hq + hq) * D + d;
-    a.out[at] = F16 ? __builtin_bit_cast(uint16_t, (_Float16)y) : __builtin_bit_cast(uint16_t, (__bf16)y);
+      for (int e = 0; e < V; ++e) so[w - 1][lane * V + e] = acc[e];
+      if (lane == 0) sl[w - 1] = l;
+    }
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      l += sl[k];
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += so[k][lane * V + e];
+    }
   }
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  const int64_t at = (((int64_t)b * a.Q + i) * Hq + hq) * D + lane * V;
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    a.out[at + e] = F16 ? __builtin_bit_cast(uint16_t, (_Float16)(acc[e] * inv))
+                        : __builtin_bit_cast(uint16_t, (__bf16)(acc[e] * inv));
 }
 
 // ------------------------------------------------------------------- host side
@@ -780,18 +858,30 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
   const int nt = a.rows > 16 ? 2 : 1;
   a.row_blocks = (a.rows + 16 * nt - 1) / (16 * nt);
   a.block_rows = a.rows < 16 * nt ? a.rows : 16 * nt;
-  a.scale = (float)((double)scale * 1.4426950408889634);
+  // Maxima are taken of the bare products, so the scale's sign goes to the
+  // queries, and a scale of zero becomes one that still hides masked scores.
+  a.scale = fmaxf((float)(fabs((double)scale) * 1.4426950408889634), 1e-37f);
+  a.flip = scale < 0.0f ? 0x80008000u : 0u;
   a.out = static_cast<uint16_t *>(out);
   a.part = static_cast<float *>(workspace);
   // no more workgroups than there can be chunks
-  const int64_t most = (((int64_t)table_width << L.page_shift) + kChunk - 1) / kChunk * B * L.H * a.row_blocks;
-  a.W = (int)(most < kKv4Groups ? most : kKv4Groups);
+  const int64_t chunks = (((int64_t)table_width << L.page_shift) + kKv4Chunk - 1) / kKv4Chunk;
+  const int64_t most = chunks * B * L.H * a.row_blocks;
+  if ((chunks + kKv4Start) * B * L.H * a.row_blocks + kKv4Groups > 0x7FFFFFFF)
+    return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_attention: B=%d Q=%d Hq=%d with a page table of %d columns is too much work",
+                B, Q, Hq, table_width);
+  const int resident = 256 * kv4_waves(L.D, nt);
+  a.W = (int)(most < resident ? most : resident);
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-  const dim3 join_grid((unsigned)((int64_t)B * Q * Hq));
-#define KV4_GO(DD, NN, FF)                                                                      \
-  do {                                                                                          \
-    hipLaunchKernelGGL((kv4_attend_kernel<DD, NN, FF>), dim3(a.W), dim3(256), 0, stream, a);    \
-    hipLaunchKernelGGL((kv4_join_kernel<DD, FF>), join_grid, dim3(256), 0, stream, a);          \
+  // pieces of a row, on average: from four on, a workgroup joins them
+  const bool wide_join = a.W >= 4ll * B * L.H * a.row_blocks;
+  const int64_t rows = (int64_t)B * Q * Hq;
+  const dim3 join_grid((unsigned)(wide_join ? rows : (rows + 3) / 4));
+#define KV4_GO(DD, NN, FF)                                                                                  \
+  do {                                                                                                      \
+    hipLaunchKernelGGL((kv4_attend_kernel<DD, NN, FF>), dim3(a.W), dim3(256), 0, stream, a);                \
+    if (wide_join) hipLaunchKernelGGL((kv4_join_kernel<DD, FF, true>), join_grid, dim3(256), 0, stream, a); \
+    else hipLaunchKernelGGL((kv4_join_kernel<DD, FF, false>), join_grid, dim3(256), 0, stream, a);          \
   } while (0)
 #define KV4_ROWS(DD, FF) do { if (nt == 1) KV4_GO(DD, 1, FF); else KV4_GO(DD, 2, FF); } while (0)
 #define KV4_TYPE(DD) do { if (dtype == SVDQ_FP16) KV4_ROWS(DD, true); else KV4_ROWS(DD, false); } while (0)

@@ -6,8 +6,17 @@
 
 namespace svdq {
 
-// Workgroups of an attention call at most: four for each of the 256 CUs.
-constexpr int kKv4Groups = 1024;
+// Wavefronts a SIMD (workgroups a CU) that the attention kernel is built for,
+// by head_dim and 16-row tiles: what its registers allow.  At D = 128 with one
+// tile, 524k tokens of 8 heads took 88 us with 2, 80 with 3 and 89 with 4 (128
+// registers, some of them spilled).
+constexpr int kv4_waves(int D, int NT) { return D == 64 ? (NT == 1 ? 4 : 2) : D == 128 ? (NT == 1 ? 3 : 2) : 1; }
+// Workgroups of an attention call at most (256 CUs), which sizes its workspace.
+constexpr int kKv4Groups = 256 * 4;
+// Tokens that a workgroup takes at a time, and the cost of beginning and ending
+// a (sequence, head), in such chunks.
+constexpr int kKv4Chunk = 128;
+constexpr int kKv4Start = 4;
 // Rows (new tokens times query heads of one key/value head) at most.
 constexpr int kKv4MaxRows = 1024;
 
