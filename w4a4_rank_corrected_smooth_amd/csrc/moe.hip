@@ -150,43 +150,105 @@ struct MoeArgs {
   const float *weights;
   uint16_t *h_hi, *h_lo;              // [T top_k][I] bf16, h = hi + lo
   float *part;                        // [T top_k][K]
+  MoePlan *plan;                      // above 64 pairs
   uint16_t *y;
 };
 
-// The workgroup's expert: the `slot`-th of those that the ids name (-1: there
-// are fewer), and its (token, choice) pairs in `pairs`.  The pairs' order does
-// not matter: a row of a matrix product does not depend on where it stands.
-struct Found { int expert, count; };
-__device__ __forceinline__ Found find_expert(const MoeArgs &a, int slot, uint16_t *pairs) {
-  __shared__ uint32_t seen[MOE_MAX_EXPERTS / 32];
-  __shared__ int count;
-  const int tid = threadIdx.x, lane = tid & 63, n = a.T * a.top_k;
-  if (tid < MOE_MAX_EXPERTS / 32) seen[tid] = 0u;
-  if (tid == 0) count = 0;
-  __syncthreads();
-  for (int i = tid; i < n; i += 256) {
-    const int e = a.ids[i];
-    if (e >= 0 && e < a.E) atomicOr(&seen[e >> 5], 1u << (e & 31));
+// The rows of one expert, for a wavefront: its (token, choice) pairs.  Their
+// order does not matter: a row of a matrix product does not depend on where
+// it stands.  Up to 64 pairs every wavefront finds them for itself, in
+// registers; above, moe_plan_kernel has sorted them.
+template <bool PLAN>
+struct Rows {
+  int expert = -1, count = 0;
+  int list = 0;                 // !PLAN: lane r holds the pair of row r
+  const uint16_t *sorted = nullptr;
+
+  // the `slot`-th expert that the ids name; false where there are fewer
+  __device__ __forceinline__ bool find(const MoeArgs &a, int slot, int lane) {
+    if constexpr (PLAN) {
+      if (slot >= a.plan->slots) return false;
+      expert = a.plan->expert[slot];
+      const int first = a.plan->first[slot];
+      count = a.plan->first[slot + 1] - first;
+      sorted = a.plan->pairs + first;
+    } else {
+      const int n = a.T * a.top_k;
+      const int id = lane < n ? a.ids[lane] : -1;
+      uint64_t left = __ballot(id >= 0 && id < a.E), same = 0;
+      do {
+        if (left == 0) return false;
+        expert = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        same = __ballot(id == expert);
+        left &= ~same;
+      } while (slot-- > 0);
+      count = __builtin_popcountll(same);
+      // lane i of the set goes to the lane of its rank; the others to the end
+      const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
+      const bool in = same >> lane & 1;
+      list = __builtin_amdgcn_ds_permute(4 * (in ? rank : 63 - (lane - rank)), lane);
+    }
+    return true;
   }
+  __device__ __forceinline__ int pair(int r) const {      // r in [0, count), any in each lane
+    if constexpr (PLAN) return sorted[r];
+    else return __shfl(list, r);
+  }
+};
+
+// Pairs sorted by expert.  One workgroup.
+__global__ __launch_bounds__(1024) void moe_plan_kernel(MoeArgs a) {
+  __shared__ int count[MOE_MAX_EXPERTS], first[MOE_MAX_EXPERTS], wsum[2][16];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n = a.T * a.top_k;
+  count[tid] = 0;
   __syncthreads();
-  uint32_t word = lane < MOE_MAX_EXPERTS / 32 ? seen[lane] : 0u;
-  int upto = __popc(word);
+  int id[kMoeMaxPairs / 1024], rank[kMoeMaxPairs / 1024];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up(upto, o);
-    if (lane >= o) upto += y;
+  for (int i = 0; i < kMoeMaxPairs / 1024; ++i) {
+    const int p = 1024 * i + tid;
+    id[i] = p < n ? a.ids[p] : -1;
+    if (id[i] >= a.E) id[i] = -1;
+    if (id[i] >= 0) rank[i] = atomicAdd(&count[id[i]], 1);
   }
-  const uint64_t past = __ballot(upto > slot);
-  if (past == 0) return Found{-1, 0};
-  const int at = __builtin_ctzll(past);
-  word = __shfl(word, at);
-  int skip = slot - (__shfl(upto, at) - __popc(word));
-  for (; skip > 0; --skip) word &= word - 1;
-  const int expert = 32 * at + __ffs(word) - 1;
-  for (int i = tid; i < n; i += 256)
-    if (a.ids[i] == expert) pairs[atomicAdd(&count, 1)] = (uint16_t)i;
   __syncthreads();
-  return Found{__builtin_amdgcn_readfirstlane(expert), __builtin_amdgcn_readfirstlane(count)};
+  // places of the experts that have pairs, and of their pairs
+  const int c = count[tid];
+  int pairs = c, slots = c > 0 ? 1 : 0;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int p = __shfl_up(pairs, o), q = __shfl_up(slots, o);
+    if (lane >= o) {
+      pairs += p;
+      slots += q;
+    }
+  }
+  if (lane == 63) {
+    wsum[0][w] = pairs;
+    wsum[1][w] = slots;
+  }
+  __syncthreads();
+  int all = 0, used = 0;
+  for (int i = 0; i < 16; ++i) {
+    if (i < w) {
+      pairs += wsum[0][i];
+      slots += wsum[1][i];
+    }
+    all += wsum[0][i];
+    used += wsum[1][i];
+  }
+  first[tid] = pairs - c;
+  if (c > 0) {
+    a.plan->expert[slots - 1] = tid;
+    a.plan->first[slots - 1] = pairs - c;
+  }
+  if (tid == 0) {
+    a.plan->slots = used;
+    a.plan->first[used] = all;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kMoeMaxPairs / 1024; ++i)
+    if (id[i] >= 0) a.plan->pairs[first[id[i]] + rank[i]] = (uint16_t)(1024 * i + tid);
 }
 
 // Eight codes of a blob word (even channels in the low half-words) as the
@@ -228,6 +290,9 @@ __device__ __forceinline__ v4f mma(uint4 a, v8bf b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_v8bf(a), b, c, 0, 0, 0);
 }
 
+template <int N>
+struct Int { static constexpr int value = N; };
+
 // acc += the group's 64 channels: s (sum x (128 + code) - (128 + zero) sum x)
 // for bf16 activations (sum x from one more product, with ones, shared by the
 // columns), s sum x (code - zero) for fp16.  a0, a1: the lane's row, channels
@@ -251,115 +316,251 @@ __device__ __forceinline__ void group_mma(uint4 a0, uint4 a1, v4f xsum, uint32_t
 }
 __device__ __forceinline__ v8bf ones() { return as_v8bf(make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u)); }
 
-// the pairs of groups (one 16-byte code load each) of wavefront w of four
-__device__ __forceinline__ void wave_pairs(int G, int w, int &p0, int &p1) {
-  const int P = (G + 1) / 2, each = (P + 3) / 4;
-  p0 = min(P, w * each);
+// Work of a wavefront: TP tiles of 16 output columns of one expert (gate_up:
+// TP gate tiles and the TP up tiles that belong to them) over one of KS equal
+// parts of the input channels; the four wavefronts of a workgroup are KS parts
+// of 4 / KS neighbouring sets of tiles.  Rows go 16 R at a time.  A step is a
+// pair of groups of 64 channels, one 16-byte code load for each tile; the next
+// step's loads are issued before a step's products, and the last step is
+// loaded once more at the end, so that every load is unconditional.
+template <int TILES, int R, int H>
+struct Step {
+  uint4 code[TILES];
+  uint2 sz[TILES];
+  uint4 x[R][H][4];                     // H pieces of the rows' 2 x 16 channels
+};
+
+struct Tiles {
+  const uint8_t *code;                  // the lane's 16 bytes of step 0 of tile 0
+  const uint32_t *sz;                   // the lane's column's scale words of tile 0
+};
+__device__ __forceinline__ Tiles tiles_of(const uint8_t *blob, const AwqLayout &L, int tile, int lane) {
+  return Tiles{blob + L.q + (int64_t)tile * awq_pairs(L.G) * kAwqBlockBytes + lane * 16,
+               reinterpret_cast<const uint32_t *>(blob + L.sz) +
+                   (int64_t)(tile * kAwqTile + (lane & 15)) * awq_g4(L.G)};
+}
+
+// this wavefront's steps
+__device__ __forceinline__ void wave_steps(int G, int part, int parts, int &p0, int &p1) {
+  const int P = (G + 1) / 2, each = (P + parts - 1) / parts;
+  p0 = min(P, part * each);
   p1 = min(P, p0 + each);
 }
 
-// One workgroup per 16 columns of h and expert: the four wavefronts take a
-// quarter of K each, for the gate and the up columns, and meet in LDS.
-template <bool F16, bool GELU>
-__global__ __launch_bounds__(256) void moe_gate_up_kernel(MoeArgs a) {
-  extern __shared__ uint16_t pairs[];
-  __shared__ v4f red[4][2][64];
-  const Found f = find_expert(a, blockIdx.y, pairs);
-  if (f.expert < 0) return;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = a.K / kGroup, G4 = (G + 3) & ~3, GP = (G + 1) / 2;
-  const AwqLayout L(2 * (int64_t)a.I, a.K);
-  const uint8_t *blob = a.gate_up + f.expert * a.gate_up_stride;
-  const int ct = blockIdx.x, ut = ct + a.I / kAwqTile;
-  const uint8_t *cg = blob + L.q + (int64_t)ct * GP * kAwqBlockBytes + lane * 16;
-  const uint8_t *cu = blob + L.q + (int64_t)ut * GP * kAwqBlockBytes + lane * 16;
-  const uint32_t *sg = reinterpret_cast<const uint32_t *>(blob + L.sz) + (int64_t)(ct * kAwqTile + (lane & 15)) * G4;
-  const uint32_t *su = reinterpret_cast<const uint32_t *>(blob + L.sz) + (int64_t)(ut * kAwqTile + (lane & 15)) * G4;
-  int p0, p1;
-  wave_pairs(G, w, p0, p1);
-  for (int r0 = 0; r0 < f.count; r0 += 16) {
-    const int pair = pairs[min(r0 + (lane & 15), f.count - 1)];
-    const uint16_t *xr = a.x + (int64_t)(pair / a.top_k) * a.K + 16 * (lane >> 4);
-    v4f accg = v4f{}, accu = v4f{};
-    for (int p = p0; p < p1; ++p) {
-      const uint4 wg = *reinterpret_cast<const uint4 *>(cg + (int64_t)p * kAwqBlockBytes);
-      const uint4 wu = *reinterpret_cast<const uint4 *>(cu + (int64_t)p * kAwqBlockBytes);
-      const uint2 zg = *reinterpret_cast<const uint2 *>(sg + 2 * p);
-      const uint2 zu = *reinterpret_cast<const uint2 *>(su + 2 * p);
+// Gate and up products of R x 16 rows; acc[0]: gate, acc[1]: up.
+template <bool F16, int TP, int R>
+__device__ __forceinline__ void gate_up_rows(const MoeArgs &a, const Tiles (&tl)[2][TP], const uint16_t *const (&xr)[R],
+                                             int G, int p0, int p1, v4f (&acc)[2][R][TP]) {
+  typedef Step<2 * TP, R, 1> S;
+  auto load = [&](int p, S &s) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (2 * p + i >= G) break;
-        const uint4 a0 = *reinterpret_cast<const uint4 *>(xr + (2 * p + i) * kGroup);
-        const uint4 a1 = *reinterpret_cast<const uint4 *>(xr + (2 * p + i) * kGroup + 8);
+    for (int i = 0; i < 2 * TP; ++i) {
+      const Tiles &t = tl[i / TP][i % TP];
+      s.code[i] = *reinterpret_cast<const uint4 *>(t.code + (int64_t)p * kAwqBlockBytes);
+      s.sz[i] = *reinterpret_cast<const uint2 *>(t.sz + 2 * p);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)     // an odd last group reads the one before it, and is not used
+        s.x[r][0][k] = *reinterpret_cast<const uint4 *>(xr[r] + min(2 * p + k / 2, G - 1) * kGroup + 8 * (k % 2));
+  };
+  auto work = [&](int p, const S &s) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (2 * p + i >= G) break;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint4 a0 = s.x[r][0][2 * i], a1 = s.x[r][0][2 * i + 1];
         v4f xsum = v4f{};
         if constexpr (!F16) xsum = mma(a1, ones(), mma(a0, ones(), v4f{}));
-        group_mma<F16>(a0, a1, xsum, i ? wg.z : wg.x, i ? wg.w : wg.y, i ? zg.y : zg.x, accg);
-        group_mma<F16>(a0, a1, xsum, i ? wu.z : wu.x, i ? wu.w : wu.y, i ? zu.y : zu.x, accu);
+#pragma unroll
+        for (int t = 0; t < 2 * TP; ++t)
+          group_mma<F16>(a0, a1, xsum, i ? s.code[t].z : s.code[t].x, i ? s.code[t].w : s.code[t].y,
+                         i ? s.sz[t].y : s.sz[t].x, acc[t / TP][r][t % TP]);
       }
     }
-    red[w][0][lane] = accg;
-    red[w][1][lane] = accu;
-    __syncthreads();
-    // one element a thread: row 4 (lane / 16) + w, column lane % 16
-    const int row = r0 + 4 * (lane >> 4) + w;
-    const float g = (red[0][0][lane][w] + red[1][0][lane][w]) + (red[2][0][lane][w] + red[3][0][lane][w]);
-    const float u = (red[0][1][lane][w] + red[1][1][lane][w]) + (red[2][1][lane][w] + red[3][1][lane][w]);
-    const float act = GELU ? gelu_tanh_f32(g) : g / (1.0f + __expf(-g));
-    const float h = act * u;
-    if (row < f.count) {
-      const int64_t at = (int64_t)pairs[row] * a.I + ct * kAwqTile + (lane & 15);
-      const __bf16 hi = (__bf16)h;
-      a.h_hi[at] = __builtin_bit_cast(uint16_t, hi);
-      a.h_lo[at] = __builtin_bit_cast(uint16_t, (__bf16)(__builtin_isfinite(h) ? h - (float)hi : 0.0f));
-    }
-    __syncthreads();
+  };
+  if (p0 >= p1) return;
+  S x, y;
+  load(p0, x);
+  for (int p = p0;; p += 2) {
+    load(min(p + 1, p1 - 1), y);
+    work(p, x);
+    if (p + 1 >= p1) break;
+    load(min(p + 2, p1 - 1), x);
+    work(p + 1, y);
+    if (p + 2 >= p1) break;
   }
 }
 
-// One workgroup per 16 columns of the output and expert.  h enters as its two
-// bf16 pieces (h to 2^-17, in float32's range).
-__global__ __launch_bounds__(256) void moe_down_kernel(MoeArgs a) {
-  extern __shared__ uint16_t pairs[];
-  __shared__ v4f red[4][64];
-  const Found f = find_expert(a, blockIdx.y, pairs);
-  if (f.expert < 0) return;
+template <bool F16, bool GELU, int TP, int KS, bool PLAN>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void moe_gate_up_kernel(MoeArgs a) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = a.I / kGroup, G4 = (G + 3) & ~3, GP = (G + 1) / 2;
-  const AwqLayout L(a.K, a.I);
-  const uint8_t *blob = a.down + f.expert * a.down_stride;
-  const int ct = blockIdx.x;
-  const uint8_t *c = blob + L.q + (int64_t)ct * GP * kAwqBlockBytes + lane * 16;
-  const uint32_t *sz = reinterpret_cast<const uint32_t *>(blob + L.sz) + (int64_t)(ct * kAwqTile + (lane & 15)) * G4;
+  Rows<PLAN> rows;
+  if (!rows.find(a, blockIdx.y, lane)) return;
+  const int G = a.K / kGroup, n = a.I / kAwqTile;
+  const AwqLayout L(2 * (int64_t)a.I, a.K);
+  const uint8_t *blob = a.gate_up + rows.expert * a.gate_up_stride;
+  const int tile0 = (blockIdx.x * (4 / KS) + w / KS) * TP;
+  Tiles tl[2][TP];
+#pragma unroll
+  for (int t = 0; t < TP; ++t) {        // tiles past the last are worked on as the last, and not stored
+    tl[0][t] = tiles_of(blob, L, min(tile0 + t, n - 1), lane);
+    tl[1][t] = tiles_of(blob, L, min(tile0 + t, n - 1) + n, lane);
+  }
   int p0, p1;
-  wave_pairs(G, w, p0, p1);
-  for (int r0 = 0; r0 < f.count; r0 += 16) {
-    const int64_t at = (int64_t)pairs[min(r0 + (lane & 15), f.count - 1)] * a.I + 16 * (lane >> 4);
-    v4f acc = v4f{};
-    for (int p = p0; p < p1; ++p) {
-      const uint4 wc = *reinterpret_cast<const uint4 *>(c + (int64_t)p * kAwqBlockBytes);
-      const uint2 z2 = *reinterpret_cast<const uint2 *>(sz + 2 * p);
+  wave_steps(G, w % KS, KS, p0, p1);
+  __shared__ v4f red[KS > 1 ? 4 : 1][KS > 1 ? 4 * TP : 1][64];
+
+  auto pass = [&](int r0, auto rt) {
+    constexpr int R = decltype(rt)::value;
+    const uint16_t *xr[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      xr[r] = a.x + (int64_t)(rows.pair(min(r0 + 16 * r + (lane & 15), rows.count - 1)) / a.top_k) * a.K + 16 * (lane >> 4);
+    v4f acc[2][R][TP] = {};
+    gate_up_rows<F16, TP, R>(a, tl, xr, G, p0, p1, acc);
+    if constexpr (KS > 1) {             // the parts meet, in order, in the first one's wavefront
+      if (w % KS != 0) {
+#pragma unroll
+        for (int i = 0; i < 2 * R * TP; ++i) red[w][i][lane] = acc[i / (R * TP)][i / TP % R][i % TP];
+      }
+      __syncthreads();
+      if (w % KS == 0) {
+#pragma unroll
+        for (int i = 0; i < 2 * R * TP; ++i)
+#pragma unroll
+          for (int k = 1; k < KS; ++k) {
+            const v4f y = red[w + k][i][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i / (R * TP)][i / TP % R][i % TP][e] += y[e];
+          }
+      }
+      __syncthreads();
+      if (w % KS != 0) return;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = r0 + 16 * r + 4 * (lane >> 4) + e;
+        const int64_t at = (int64_t)rows.pair(min(row, rows.count - 1)) * a.I + (lane & 15);
+#pragma unroll
+        for (int t = 0; t < TP; ++t) {
+          const float g = acc[0][r][t][e], u = acc[1][r][t][e];
+          const float h = (GELU ? gelu_tanh_f32(g) : g * __builtin_amdgcn_rcpf(1.0f + __expf(-g))) * u;
+          if (row < rows.count && tile0 + t < n) {
+            const __bf16 hi = (__bf16)h;
+            a.h_hi[at + (tile0 + t) * kAwqTile] = __builtin_bit_cast(uint16_t, hi);
+            a.h_lo[at + (tile0 + t) * kAwqTile] =
+                __builtin_bit_cast(uint16_t, (__bf16)(__builtin_isfinite(h) ? h - (float)hi : 0.0f));
+          }
+        }
+      }
+  };
+  for (int r0 = 0; r0 < rows.count;) {
+    if (rows.count - r0 > 16) {
+      pass(r0, Int<2>{});
+      r0 += 32;
+    } else {
+      pass(r0, Int<1>{});
+      r0 += 16;
+    }
+  }
+}
+
+// h enters the down product as its two bf16 pieces (h to 2^-17, in float32's
+// range).
+template <int TP, int KS, bool PLAN>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void moe_down_kernel(MoeArgs a) {
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Rows<PLAN> rows;
+  if (!rows.find(a, blockIdx.y, lane)) return;
+  const int G = a.I / kGroup, n = a.K / kAwqTile;
+  const AwqLayout L(a.K, a.I);
+  const uint8_t *blob = a.down + rows.expert * a.down_stride;
+  const int tile0 = (blockIdx.x * (4 / KS) + w / KS) * TP;
+  Tiles tl[TP];
+#pragma unroll
+  for (int t = 0; t < TP; ++t) tl[t] = tiles_of(blob, L, min(tile0 + t, n - 1), lane);
+  int p0, p1;
+  wave_steps(G, w % KS, KS, p0, p1);
+  __shared__ v4f red[KS > 1 ? 4 : 1][KS > 1 ? TP : 1][64];
+
+  for (int r0 = 0; r0 < rows.count; r0 += 16) {
+    const int64_t at = (int64_t)rows.pair(min(r0 + (lane & 15), rows.count - 1)) * a.I + 16 * (lane >> 4);
+    const uint16_t *hr[2] = {a.h_hi + at, a.h_lo + at};
+    v4f acc[TP] = {};
+    typedef Step<TP, 1, 2> S;
+    auto load = [&](int p, S &s) {
+#pragma unroll
+      for (int t = 0; t < TP; ++t) {
+        s.code[t] = *reinterpret_cast<const uint4 *>(tl[t].code + (int64_t)p * kAwqBlockBytes);
+        s.sz[t] = *reinterpret_cast<const uint2 *>(tl[t].sz + 2 * p);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          s.x[0][h][k] = *reinterpret_cast<const uint4 *>(hr[h] + min(2 * p + k / 2, G - 1) * kGroup + 8 * (k % 2));
+    };
+    auto work = [&](int p, const S &s) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (2 * p + i >= G) break;
-        const uint4 h0 = *reinterpret_cast<const uint4 *>(a.h_hi + at + (2 * p + i) * kGroup);
-        const uint4 h1 = *reinterpret_cast<const uint4 *>(a.h_hi + at + (2 * p + i) * kGroup + 8);
-        const uint4 l0 = *reinterpret_cast<const uint4 *>(a.h_lo + at + (2 * p + i) * kGroup);
-        const uint4 l1 = *reinterpret_cast<const uint4 *>(a.h_lo + at + (2 * p + i) * kGroup + 8);
-        const v8bf b0 = codes_128(i ? wc.z : wc.x), b1 = codes_128(i ? wc.w : wc.y);
+        const uint4 h0 = s.x[0][0][2 * i], h1 = s.x[0][0][2 * i + 1], l0 = s.x[0][1][2 * i], l1 = s.x[0][1][2 * i + 1];
         const v4f sum = mma(l1, ones(), mma(l0, ones(), mma(h1, ones(), mma(h0, ones(), v4f{}))));
-        const v4f prod = mma(l1, b1, mma(l0, b0, mma(h1, b1, mma(h0, b0, v4f{}))));
-        const uint32_t s = i ? z2.y : z2.x;
-        const float z = -(128.0f + (float)zero_of(s));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(__builtin_fmaf(z, sum[e], prod[e]), scale_of(s), acc[e]);
+        for (int t = 0; t < TP; ++t) {
+          const v8bf b0 = codes_128(i ? s.code[t].z : s.code[t].x), b1 = codes_128(i ? s.code[t].w : s.code[t].y);
+          const v4f prod = mma(l1, b1, mma(l0, b0, mma(h1, b1, mma(h0, b0, v4f{}))));
+          const uint32_t sz = i ? s.sz[t].y : s.sz[t].x;
+          const float z = -(128.0f + (float)zero_of(sz)), sc = scale_of(sz);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(__builtin_fmaf(z, sum[e], prod[e]), sc, acc[t][e]);
+        }
+      }
+    };
+    if (p0 < p1) {
+      S x, y;
+      load(p0, x);
+      for (int p = p0;; p += 2) {
+        load(min(p + 1, p1 - 1), y);
+        work(p, x);
+        if (p + 1 >= p1) break;
+        load(min(p + 2, p1 - 1), x);
+        work(p + 1, y);
+        if (p + 2 >= p1) break;
       }
     }
-    red[w][lane] = acc;
-    __syncthreads();
-    const int row = r0 + 4 * (lane >> 4) + w;
-    const float v = (red[0][lane][w] + red[1][lane][w]) + (red[2][lane][w] + red[3][lane][w]);
-    if (row < f.count) a.part[(int64_t)pairs[row] * a.K + ct * kAwqTile + (lane & 15)] = v;
-    __syncthreads();
+    if constexpr (KS > 1) {
+      if (w % KS != 0) {
+#pragma unroll
+        for (int t = 0; t < TP; ++t) red[w][t][lane] = acc[t];
+      }
+      __syncthreads();
+      if (w % KS == 0) {
+#pragma unroll
+        for (int t = 0; t < TP; ++t)
+#pragma unroll
+          for (int k = 1; k < KS; ++k) {
+            const v4f y = red[w + k][t][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[t][e] += y[e];
+          }
+      }
+      __syncthreads();
+      if (w % KS != 0) continue;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = r0 + 4 * (lane >> 4) + e;
+      const int64_t to = (int64_t)rows.pair(min(row, rows.count - 1)) * a.K + (lane & 15);
+#pragma unroll
+      for (int t = 0; t < TP; ++t)
+        if (row < rows.count && tile0 + t < n) a.part[to + (tile0 + t) * kAwqTile] = acc[t][e];
+    }
   }
 }
 
@@ -394,6 +595,19 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
 }
 
 }  // namespace
+
+#ifndef GTP0
+#define GTP0 1
+#define GKS0 4
+#define GTP1 1
+#define GKS1 1
+#define DTP0 1
+#define DKS0 2
+#define DTP1 4
+#define DKS1 1
+#define FEWG 2048
+#define FEWD 4096
+#endif
 
 extern "C" {
 
@@ -478,18 +692,33 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   a.h_lo = reinterpret_cast<uint16_t *>(ws + L.h_lo);
   a.part = reinterpret_cast<float *>(ws + L.part);
   a.y = static_cast<uint16_t *>(y);
+  a.plan = reinterpret_cast<MoePlan *>(ws + L.plan);
   const int pairs = T * top_k, slots = pairs < w->E ? pairs : w->E;
-  const size_t lds = ((size_t)pairs * 2 + 15) / 16 * 16;
+  const bool plan = pairs > 64;
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-  const dim3 g1((unsigned)(w->I / kAwqTile), (unsigned)slots), g2((unsigned)(w->K / kAwqTile), (unsigned)slots);
-#define MOE_GU(F, A) hipLaunchKernelGGL((moe_gate_up_kernel<F, A>), g1, dim3(256), lds, stream, a)
+  if (plan) hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
+  const int gt = w->I / kAwqTile, dt = w->K / kAwqTile;
+#define MOE_GU3(F, A, TP, KS, P)                                                                        \
+  hipLaunchKernelGGL((moe_gate_up_kernel<F, A, TP, KS, P>),                                             \
+                     dim3((gt + TP * (4 / KS) - 1) / (TP * (4 / KS)), (unsigned)slots), dim3(256), 0, stream, a)
+#define MOE_GU2(F, A, P) do { if (few) MOE_GU3(F, A, GTP0, GKS0, P); else MOE_GU3(F, A, GTP1, GKS1, P); } while (0)
+#define MOE_GU(F, A) do { if (plan) MOE_GU2(F, A, true); else MOE_GU2(F, A, false); } while (0)
+#define MOE_D3(TP, KS, P)                                                                               \
+  hipLaunchKernelGGL((moe_down_kernel<TP, KS, P>), dim3((dt + TP * (4 / KS) - 1) / (TP * (4 / KS)), (unsigned)slots), \
+                     dim3(256), 0, stream, a)
+#define MOE_D2(P) do { if (few_down) MOE_D3(DTP0, DKS0, P); else MOE_D3(DTP1, DKS1, P); } while (0)
+  const bool few = (int64_t)slots * gt < FEWG, few_down = (int64_t)slots * dt < FEWD;
   if (dtype == SVDQ_FP16) {
     if (act == SVDQ_MOE_GELU_TANH) MOE_GU(true, true); else MOE_GU(true, false);
   } else {
     if (act == SVDQ_MOE_GELU_TANH) MOE_GU(false, true); else MOE_GU(false, false);
   }
+  if (plan) MOE_D2(true); else MOE_D2(false);
+#undef MOE_D2
+#undef MOE_D3
 #undef MOE_GU
-  hipLaunchKernelGGL(moe_down_kernel, g2, dim3(256), lds, stream, a);
+#undef MOE_GU2
+#undef MOE_GU3
   const dim3 g3((unsigned)(((int64_t)T * (w->K / 4) + 255) / 256));
   if (dtype == SVDQ_FP16) hipLaunchKernelGGL((moe_sum_kernel<true>), g3, dim3(256), 0, stream, a);
   else hipLaunchKernelGGL((moe_sum_kernel<false>), g3, dim3(256), 0, stream, a);

@@ -25,15 +25,23 @@ constexpr bool moe_call_ok(int64_t T, int top_k) {
   return T >= 0 && top_k >= 1 && top_k <= kMoeMaxTopK && T * top_k <= kMoeMaxPairs;
 }
 
-// the gated products h as two bf16 pieces, then each pair's output row
+// (token, choice) pairs sorted by expert: the experts that have any, where
+// their pairs begin (and, after the last, end), and the pairs
+struct MoePlan {
+  int slots, expert[MOE_MAX_EXPERTS], first[MOE_MAX_EXPERTS + 1];
+  uint16_t pairs[kMoeMaxPairs];
+};
+
+// the gated products h as two bf16 pieces, each pair's output row, the plan
 struct MoeWork {
-  int64_t h_hi = 0, h_lo = 0, part = 0, total = 0;
+  int64_t h_hi = 0, h_lo = 0, part = 0, plan = 0, total = 0;
   constexpr MoeWork(int64_t T, int64_t top_k, int64_t K, int64_t I) {
     const int64_t n = T * top_k;
     int64_t o = 0;
     h_hi = o;  o = round_up(o + n * I * 2, kAlign);
     h_lo = o;  o = round_up(o + n * I * 2, kAlign);
     part = o;  o = round_up(o + n * K * 4, kAlign);
+    plan = o;  o = round_up(o + (n > 64 ? (int64_t)sizeof(MoePlan) : 0), kAlign);
     total = o;
   }
 };
