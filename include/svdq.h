@@ -495,9 +495,19 @@ svdq_status_t svdq_moe_route(const void *x, const void *w_router, const float *b
                              int K, int top_k, svdq_moe_score_t score, int normalize, int32_t *ids, float *weights,
                              void *workspace, size_t ws_bytes, void *hip_stream);
 
-/* Experts resident in device memory: E blobs of awq_pack_device_weights one
- * after another, each awq_device_weights_bytes long.  gate_up: [2 I, K] each
- * (the I gate rows, then the I up rows); down: [K, I] each. */
+/* Device blob of the AWQ weights of E experts' linears, each [N, K] (N and K
+ * multiples of 64; host memory, caller-allocated, `bytes` >=
+ * awq_moe_device_weights_bytes): q [E, N, K/2], scales and zeros [E, N, K/64]
+ * as awq_quantize_weights gives them for each expert.  Zero points and scales
+ * are checked as by awq_pack_device_weights.  Multi-threaded. */
+size_t awq_moe_device_weights_bytes(int E, int N, int K);
+svdq_status_t awq_moe_pack_device_weights(const uint8_t *q, const uint16_t *scales_fp16,
+                                          const uint16_t *zeros_fp16, int E, int N, int K,
+                                          void *host_blob, size_t bytes);
+
+/* Experts resident in device memory: blobs of awq_moe_pack_device_weights.
+ * gate_up: [2 I, K] each (the I gate rows, then the I up rows); down: [K, I]
+ * each. */
 typedef struct {
   const void *gate_up, *down;
   int32_t E, K, I;

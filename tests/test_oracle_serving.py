@@ -215,16 +215,42 @@ def test_wrappers_check_their_operands():
         S.awq_moe_forward(layer, x, ids, wt, activation="relu")
 
 
-def test_expert_blobs_are_the_linear_layers_blobs():
-    """Each expert's bytes are what awq_pack_device_weights gives for it, one after another."""
-    r = np.random.default_rng(1)
-    E, K, I = 3, 128, 192
-    parts = []
-    for N, D in ((2 * I, K), (K, I)):
-        qs = [awq.quantize((r.standard_normal((N, D)) / 8).astype(np.float16)) for _ in range(E)]
-        parts.append((np.stack([awq.pack(q) for q, _, _ in qs]), np.stack([s for _, s, _ in qs]), np.stack([z for *_, z in qs])))
-    layer = S.AwqMoe(*parts, device="cpu")
-    for got, (q, s, z) in ((layer.gate_up, parts[0]), (layer.down, parts[1])):
-        for e in range(E):
-            one = S.AwqLinear(q[e], s[e], z[e], device="cpu")
-            assert torch.equal(got[e], one.blob)
+@pytest.mark.parametrize("E,N,K", [(1, 64, 64), (3, 128, 192), (2, 192, 256)])
+def test_expert_blob_layout(E, N, K):
+    """A reader of the documented blocks finds every code, scale and zero point in its place."""
+    r = np.random.default_rng(E)
+    G, P = K // 64, (K // 64 + 1) // 2
+    codes = r.integers(0, 16, (E, N, K), dtype=np.uint8)
+    s = r.standard_normal((E, N, G)).astype(np.float16)
+    z = r.integers(0, 16, (E, N, G)).astype(np.float16)
+    blob = S._moe_blob((awq.pack(codes), s, z), N, K).reshape(E, N // 16, P, 1152)
+    for e in range(E):
+        for n in r.permutation(N)[:40]:
+            for g in range(G):
+                block = blob[e, n // 16, g // 2]
+                words = block[1024 + 8 * (n % 16) + 4 * (g % 2):][:4].view(np.float16)
+                assert words[0] == s[e, n, g] and words[1] == z[e, n, g]
+                for k in r.permutation(64)[:16]:
+                    lane = block[(n % 16 + 16 * (k // 16)) * 16 + 8 * (g % 2):][:8]
+                    word = int(lane[4 * (k % 16 // 8):][:4].view(np.uint32)[0])
+                    assert word >> (16 * (k % 2) + 4 * (k % 8 // 2)) & 15 == codes[e, n, 64 * g + k]
+    if G % 2:
+        last = blob[:, :, -1]
+        assert not last[..., 1024:].reshape(E, -1, 16, 8)[..., 4:].any()
+        assert not last[..., :1024].reshape(E, -1, 64, 16)[..., 8:].any()
+
+
+def test_expert_blob_refusals():
+    lib = S._lib
+    assert lib.awq_moe_device_weights_bytes(2, 128, 192) == 2 * 8 * 2 * 1152
+    for bad in ((0, 128, 128), (1025, 128, 128), (1, 100, 128), (1, 128, 96), (1, 0, 128), (1, 1 << 16, 1 << 16)):
+        assert lib.awq_moe_device_weights_bytes(*bad) == 0
+    q, s, z = np.zeros((1, 64, 32), np.uint8), np.ones((1, 64, 1), np.float16), np.zeros((1, 64, 1), np.float16)
+    blob = np.zeros(4 * 1152, np.uint8)
+
+    def pack(q=q, s=s, z=z, n=blob.size, K=64):
+        return lib.awq_moe_pack_device_weights(S._ptr(q), S._ptr(s), S._ptr(z), 1, 64, K, S._ptr(blob), n)
+    assert pack() == 0 and pack(q=None) == INV and pack(K=96) == SHAPE and pack(n=blob.size - 1) == WS
+    for bad in (0.5, 16.0, -1.0, np.nan):
+        assert pack(z=np.full_like(z, bad)) == INV
+    assert pack(s=np.full_like(s, np.inf)) == 6

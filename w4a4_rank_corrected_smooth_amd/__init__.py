@@ -54,8 +54,8 @@ EXPORTS = [
     "svdq_mx_linear_quantize", "svdq_mx_linear_gemm", "svdq_mx_quantize_activations",
     "svdq_merge_lora", "svdq_mx_merge_lora", "svdq_measure_stream", "svdq_measure_mfma",
     "svdq_kv4_cache_bytes", "svdq_kv4_append", "svdq_kv4_read", "svdq_kv4_attention_workspace_bytes",
-    "svdq_kv4_attention", "svdq_moe_route_workspace_bytes", "svdq_moe_route", "awq_moe_workspace_bytes",
-    "awq_moe_forward",
+    "svdq_kv4_attention", "svdq_moe_route_workspace_bytes", "svdq_moe_route",
+    "awq_moe_device_weights_bytes", "awq_moe_pack_device_weights", "awq_moe_workspace_bytes", "awq_moe_forward",
 ]
 
 
@@ -150,6 +150,8 @@ _sig("svdq_kv4_attention", _i, [_C, _vp, _i64, _i64, _i64, _i, _i, _i, _i, _vp, 
                                 _sz, _vp])
 _sig("svdq_moe_route_workspace_bytes", _sz, [_i, _i])
 _sig("svdq_moe_route", _i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp])
+_sig("awq_moe_device_weights_bytes", _sz, [_i, _i, _i])
+_sig("awq_moe_pack_device_weights", _i, [_vp, _vp, _vp, _i, _i, _i, _vp, _sz])
 _sig("awq_moe_workspace_bytes", _sz, [_i, _i, _i, _i])
 _sig("awq_moe_forward", _i, [ctypes.POINTER(MoeWeights), _vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp])
 
@@ -856,27 +858,21 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, bias: Optiona
     return ids, weights
 
 
-def _moe_blobs(qsz, N: int, K: int) -> np.ndarray:
-    """E AWQ weights (codes [E, N, K/2], scales and zeros [E, N, K/64]) packed one after another."""
-    from concurrent.futures import ThreadPoolExecutor
+def _moe_blob(qsz, N: int, K: int) -> np.ndarray:
+    """AWQ weights of E experts (codes [E, N, K/2], scales and zeros [E, N, K/64]) as one device blob."""
     q, s, z = (np.ascontiguousarray(t.cpu().numpy() if isinstance(t, torch.Tensor) else t) for t in qsz)
     E = q.shape[0]
     if q.shape != (E, N, K // 2) or q.dtype != np.uint8 or s.shape != (E, N, K // 64) or s.shape != z.shape \
             or s.dtype != np.float16 or z.dtype != np.float16:
         raise ValueError(f"expert weights must be codes uint8 [E, {N}, {K // 2}] with float16 scales and zeros "
                          f"[E, {N}, {K // 64}], got {q.shape} {q.dtype}, {s.shape} {s.dtype}, {z.shape} {z.dtype}")
-    n = _lib.awq_device_weights_bytes(N, K)
+    n = _lib.awq_moe_device_weights_bytes(E, N, K)
     if n == 0:
-        raise SvdqError(2, "awq_device_weights_bytes")
-    blobs = np.empty((E, n), np.uint8)
-
-    def pack(e):                         # the library call runs without the interpreter's lock
-        _check(_lib.awq_pack_device_weights(_ptr(q[e]), _ptr(s[e]), _ptr(z[e]), N, K, _ptr(blobs[e]), n),
-               "awq_pack_device_weights")
-
-    with ThreadPoolExecutor(min(len(os.sched_getaffinity(0)), 16)) as pool:
-        list(pool.map(pack, range(E)))
-    return blobs
+        raise SvdqError(2, "awq_moe_device_weights_bytes")
+    blob = np.empty(n, np.uint8)
+    _check(_lib.awq_moe_pack_device_weights(_ptr(q), _ptr(s), _ptr(z), E, N, K, _ptr(blob), n),
+           "awq_moe_pack_device_weights")
+    return blob
 
 
 class AwqMoe:
@@ -893,8 +889,8 @@ class AwqMoe:
             raise ValueError(f"gate_up {tuple(gate_up[0].shape)} and down {tuple(down[0].shape)} do not make an expert layer")
         if _lib.awq_moe_workspace_bytes(1, 1, self.K, self.I) == 0:
             raise SvdqError(2, "awq_moe_workspace_bytes")
-        self.gate_up = torch.from_numpy(_moe_blobs(gate_up, 2 * self.I, self.K)).to(device)
-        self.down = torch.from_numpy(_moe_blobs(down, self.K, self.I)).to(device)
+        self.gate_up = torch.from_numpy(_moe_blob(gate_up, 2 * self.I, self.K)).to(device)
+        self.down = torch.from_numpy(_moe_blob(down, self.K, self.I)).to(device)
         self.device = self.gate_up.device
         self._w = MoeWeights(self.gate_up.data_ptr(), self.down.data_ptr(), self.E, self.K, self.I)
 

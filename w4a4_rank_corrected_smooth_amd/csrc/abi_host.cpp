@@ -304,4 +304,24 @@ size_t awq_moe_workspace_bytes(int T, int top_k, int K, int I) {
   return (size_t)MoeWork(T > 0 ? T : 1, top_k, K, I).total;
 }
 
+static bool moe_linear_ok(int E, int N, int K, const char *who) {
+  if (E >= 1 && E <= MOE_MAX_EXPERTS && N >= kGroup && N % kGroup == 0 && K >= kGroup && K % kGroup == 0 &&
+      (int64_t)N * K <= (int64_t)1 << 31)
+    return true;
+  fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%s: E=%d N=%d K=%d (E in 1..%d, N and K multiples of 64)", who, E, N, K,
+       MOE_MAX_EXPERTS);
+  return false;
+}
+
+size_t awq_moe_device_weights_bytes(int E, int N, int K) {
+  return moe_linear_ok(E, N, K, "awq_moe_device_weights_bytes") ? (size_t)(E * MoeWeightLayout(N, K).total) : 0;
+}
+
+svdq_status_t awq_moe_pack_device_weights(const uint8_t *q, const uint16_t *s, const uint16_t *z, int E, int N, int K,
+                                          void *host_blob, size_t bytes) {
+  if (!q || !s || !z || !host_blob) return fail(SVDQ_ERR_INVALID_ARGUMENT, "awq_moe_pack_device_weights: NULL");
+  if (!moe_linear_ok(E, N, K, "awq_moe_pack_device_weights")) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  return awq_moe_pack(q, s, z, E, N, K, host_blob, bytes);
+}
+
 }  // extern "C"

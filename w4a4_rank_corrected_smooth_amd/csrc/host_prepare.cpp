@@ -14,6 +14,7 @@
 #include "host_linalg.h"
 #include "host_threads.h"
 #include "layout.h"
+#include "moe_layout.h"
 
 namespace svdq {
 
@@ -436,6 +437,48 @@ svdq_status_t awq_pack(const uint8_t *q, const uint16_t *s, const uint16_t *z, i
   for (int64_t n = 0; n < N; ++n)
     for (int64_t g = 0; g < L.G; ++g)
       sz[n * awq_g4(L.G) + g] = (uint32_t)s[n * L.G + g] | ((uint32_t)z[n * L.G + g] << 16);
+  return SVDQ_OK;
+}
+
+svdq_status_t awq_moe_pack(const uint8_t *q, const uint16_t *s, const uint16_t *z, int E, int N, int K,
+                           void *host_blob, size_t bytes) {
+  const MoeWeightLayout L(N, K);
+  if ((int64_t)(bytes / (size_t)E) < L.total)
+    return fail(SVDQ_ERR_WORKSPACE_TOO_SMALL, "blob needs %lld bytes, got %zu", (long long)E * (long long)L.total, bytes);
+  const int64_t G = L.G;
+  for (int64_t i = 0; i < (int64_t)E * N * G; ++i) {
+    const float zf = f16_to_f32(z[i]);
+    if (!(zf >= 0.0f && zf <= 15.0f && zf == std::floor(zf)))
+      return fail(SVDQ_ERR_INVALID_ARGUMENT, "awq_moe_pack_device_weights: zero point %g of expert %lld is not an integer in 0..15",
+                  (double)zf, (long long)(i / (N * G)));
+    if (!std::isfinite(f16_to_f32(s[i])))
+      return fail(SVDQ_ERR_NUMERICAL, "awq_moe_pack_device_weights: non-finite scale of expert %lld", (long long)(i / (N * G)));
+  }
+  uint8_t *b = static_cast<uint8_t *>(host_blob);
+  parallel_for((int64_t)E * (N / kAwqTile), 1, [&](int64_t begin, int64_t end) {
+    for (int64_t et = begin; et < end; ++et) {
+      const int64_t e = et / (N / kAwqTile), tile = et % (N / kAwqTile);
+      for (int64_t p = 0; p < L.P; ++p) {
+        uint8_t *block = b + e * L.total + L.block(tile, p);
+        std::memset(block, 0, kMoeBlockBytes);
+        for (int c = 0; c < kAwqTile; ++c) {
+          const int64_t n = e * N + tile * kAwqTile + c;
+          for (int64_t i = 0; i < 2 && 2 * p + i < G; ++i) {
+            const int64_t g = 2 * p + i;
+            const uint32_t sz = (uint32_t)s[n * G + g] | (uint32_t)z[n * G + g] << 16;
+            std::memcpy(block + kAwqBlockBytes + 8 * c + 4 * i, &sz, 4);
+            for (int w = 0; w < 8; ++w) {          // eight channels each: quarter w / 2 of the group
+              const uint8_t *in = q + n * (K / 2) + g * (kGroup / 2) + 4 * w;
+              uint32_t word = 0;
+              for (int j = 0; j < 4; ++j)
+                word |= (uint32_t)(in[j] & 15u) << (4 * j) | (uint32_t)(in[j] >> 4) << (16 + 4 * j);
+              std::memcpy(block + (c + 16 * (w / 2)) * 16 + 8 * i + 4 * (w % 2), &word, 4);
+            }
+          }
+        }
+      }
+    }
+  });
   return SVDQ_OK;
 }
 

@@ -37,4 +37,7 @@ svdq_status_t awq_quantize(const uint16_t *W_fp16, int N, int K, uint8_t *q, uin
 svdq_status_t awq_pack(const uint8_t *q, const uint16_t *s, const uint16_t *z, int N, int K,
                        void *host_blob, size_t bytes);
 
+svdq_status_t awq_moe_pack(const uint8_t *q, const uint16_t *s, const uint16_t *z, int E, int N, int K,
+                           void *host_blob, size_t bytes);
+
 }  // namespace svdq

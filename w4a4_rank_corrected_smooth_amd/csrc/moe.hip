@@ -14,6 +14,30 @@
 #include "moe_layout.h"
 
 using namespace svdq;
+#ifndef GKS0
+#define GKS0 4
+#endif
+#ifndef DT0
+#define DT0 2
+#endif
+#ifndef DK0
+#define DK0 2
+#endif
+#ifndef DT1
+#define DT1 4
+#endif
+#ifndef FEWG
+#define FEWG 1024
+#endif
+#ifndef FEWD
+#define FEWD 4096
+#endif
+#ifndef GUW
+#define GUW 3
+#endif
+#ifndef DNW
+#define DNW 3
+#endif
 
 namespace {
 
@@ -148,7 +172,7 @@ struct MoeArgs {
   int T, top_k;
   const int *ids;
   const float *weights;
-  uint16_t *h_hi, *h_lo;              // [T top_k][I] bf16, h = hi + lo
+  uint16_t *h;                        // [T top_k][I / 64][2][64] bf16: h = first piece + second
   float *part;                        // [T top_k][K]
   MoePlan *plan;                      // above 64 pairs
   uint16_t *y;
@@ -168,9 +192,9 @@ struct Rows {
   __device__ __forceinline__ bool find(const MoeArgs &a, int slot, int lane) {
     if constexpr (PLAN) {
       if (slot >= a.plan->slots) return false;
-      expert = a.plan->expert[slot];
-      const int first = a.plan->first[slot];
-      count = a.plan->first[slot + 1] - first;
+      expert = __builtin_amdgcn_readfirstlane(a.plan->expert[slot]);
+      const int first = __builtin_amdgcn_readfirstlane(a.plan->first[slot]);
+      count = __builtin_amdgcn_readfirstlane(a.plan->first[slot + 1]) - first;
       sorted = a.plan->pairs + first;
     } else {
       const int n = a.T * a.top_k;
@@ -189,6 +213,10 @@ struct Rows {
       list = __builtin_amdgcn_ds_permute(4 * (in ? rank : 63 - (lane - rank)), lane);
     }
     return true;
+  }
+  __device__ __forceinline__ int one(int r) const {       // the same r in all lanes
+    if constexpr (PLAN) return __builtin_amdgcn_readfirstlane(sorted[r]);
+    else return __builtin_amdgcn_readlane(list, r);
   }
   __device__ __forceinline__ int pair(int r) const {      // r in [0, count), any in each lane
     if constexpr (PLAN) return sorted[r];
@@ -290,9 +318,6 @@ __device__ __forceinline__ v4f mma(uint4 a, v8bf b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_v8bf(a), b, c, 0, 0, 0);
 }
 
-template <int N>
-struct Int { static constexpr int value = N; };
-
 // acc += the group's 64 channels: s (sum x (128 + code) - (128 + zero) sum x)
 // for bf16 activations (sum x from one more product, with ones, shared by the
 // columns), s sum x (code - zero) for fp16.  a0, a1: the lane's row, channels
@@ -316,251 +341,250 @@ __device__ __forceinline__ void group_mma(uint4 a0, uint4 a1, v4f xsum, uint32_t
 }
 __device__ __forceinline__ v8bf ones() { return as_v8bf(make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u)); }
 
-// Work of a wavefront: TP tiles of 16 output columns of one expert (gate_up:
-// TP gate tiles and the TP up tiles that belong to them) over one of KS equal
-// parts of the input channels; the four wavefronts of a workgroup are KS parts
-// of 4 / KS neighbouring sets of tiles.  Rows go 16 R at a time.  A step is a
-// pair of groups of 64 channels, one 16-byte code load for each tile; the next
-// step's loads are issued before a step's products, and the last step is
-// loaded once more at the end, so that every load is unconditional.
-template <int TILES, int R, int H>
-struct Step {
-  uint4 code[TILES];
-  uint2 sz[TILES];
-  uint4 x[R][H][4];                     // H pieces of the rows' 2 x 16 channels
-};
+// One expert's product for 16 R rows at a time, the form both products share.
+//
+// Work of a wavefront: TILES tiles of 16 output columns over one of KS equal
+// parts of the input channels; a workgroup's four wavefronts are KS parts of
+// 4 / KS neighbouring sets of tiles.  A step is a pair of groups of 64
+// channels.
+// Weights: each wavefront streams its tiles from memory into a ring of RING
+// steps of registers; a step's place is filled anew as soon as it is used up.
+// Rows: in PIECES 16-bit pieces (x itself, or h's two), through LDS, CHUNK
+// steps of every part at a time, shared by the wavefronts; a chunk is fetched
+// to registers while the one before is worked on and then written to the
+// other buffer.  (Loads are waited for in the order in which they are
+// issued, so rows loaded straight into operands would hold up the weights
+// asked for after them.)
+// A row's chunk is 64 pieces of 16 bytes, 16 for each (part, step, piece);
+// piece p of row r is at place p ^ (r % 16) of its 16, so that the operand
+// reads, one row a lane, fall on different banks.
+// Every load is unconditional: past the end a wavefront reads its last step
+// again, and rows past the last repeat it.
+template <int TILES, int PIECES, int KS, int R>
+struct Product {
+  static constexpr int CHUNK = 4 / (KS * PIECES), RING = CHUNK < 4 && TILES <= 2 ? 4 : CHUNK;
+  static_assert(CHUNK >= 1 && RING % CHUNK == 0, "whole chunks in a ring");
+  static constexpr int LDS_BYTES = 2 * 16 * R * 1024;
 
-struct Tiles {
-  const uint8_t *code;                  // the lane's 16 bytes of step 0 of tile 0
-  const uint32_t *sz;                   // the lane's column's scale words of tile 0
-};
-__device__ __forceinline__ Tiles tiles_of(const uint8_t *blob, const AwqLayout &L, int tile, int lane) {
-  return Tiles{blob + L.q + (int64_t)tile * awq_pairs(L.G) * kAwqBlockBytes + lane * 16,
-               reinterpret_cast<const uint32_t *>(blob + L.sz) +
-                   (int64_t)(tile * kAwqTile + (lane & 15)) * awq_g4(L.G)};
-}
+  // (addresses are kept as a base that the wavefront shares, in scalar
+  // registers, and a lane's own 32-bit offset)
+  const uint8_t *w[TILES];            // the tiles' step 0
+  const uint16_t *src;                // rows of ld elements; with two pieces, 64 of one and 64 of the other in turn
+  int64_t ld;
+  int G, P, each, p0, p1;             // groups, steps, steps of a part, this wavefront's steps
 
-// this wavefront's steps
-__device__ __forceinline__ void wave_steps(int G, int part, int parts, int &p0, int &p1) {
-  const int P = (G + 1) / 2, each = (P + parts - 1) / parts;
-  p0 = min(P, part * each);
-  p1 = min(P, p0 + each);
-}
+  uint4 code[RING][TILES];
+  uint2 sz[RING][TILES];
+  uint4 stage[4 * R];
 
-// Gate and up products of R x 16 rows; acc[0]: gate, acc[1]: up.
-template <bool F16, int TP, int R>
-__device__ __forceinline__ void gate_up_rows(const MoeArgs &a, const Tiles (&tl)[2][TP], const uint16_t *const (&xr)[R],
-                                             int G, int p0, int p1, v4f (&acc)[2][R][TP]) {
-  typedef Step<2 * TP, R, 1> S;
-  auto load = [&](int p, S &s) {
+  __device__ __forceinline__ void init(const uint8_t *blob, const MoeWeightLayout &L, const int (&tile)[TILES],
+                                       int wave) {
 #pragma unroll
-    for (int i = 0; i < 2 * TP; ++i) {
-      const Tiles &t = tl[i / TP][i % TP];
-      s.code[i] = *reinterpret_cast<const uint4 *>(t.code + (int64_t)p * kAwqBlockBytes);
-      s.sz[i] = *reinterpret_cast<const uint2 *>(t.sz + 2 * p);
+    for (int t = 0; t < TILES; ++t) w[t] = blob + L.block(tile[t], 0);
+    G = (int)L.G;
+    P = (int)L.P;
+    each = (P + KS - 1) / KS;
+    p0 = min(P, wave % KS * each);
+    p1 = min(P, p0 + each);
+  }
+  __device__ __forceinline__ void load_step(int i, int p, int lane) {
+    p = max(min(min(p, p1 - 1), P - 1), 0);
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      const uint8_t *block = w[t] + (int64_t)p * kMoeBlockBytes;
+      const v4u c = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(block + (uint32_t)lane * 16));
+      code[i][t] = make_uint4(c.x, c.y, c.z, c.w);
+      sz[i][t] = *reinterpret_cast<const uint2 *>(block + (kAwqBlockBytes + (uint32_t)(lane & 15) * 8));
     }
+  }
+  // chunk c of the rows into registers: thread (wave, lane) takes 16-byte
+  // piece `lane` of rows wave, wave + 4, ...; row[j]: those rows' places in src
+  __device__ __forceinline__ void fetch(int c, const int (&row)[4 * R], int lane) {
+    const int s = lane / 16, piece = s % PIECES, step = s / PIECES % CHUNK, part = s / PIECES / CHUNK;
+    int p = min(min(part * each + c * CHUNK + step, part * each + each - 1), P - 1);
+    const int group = min(2 * p + lane % 16 / 8, G - 1);      // an odd last step has one group
+    const uint32_t at = (uint32_t)((group * PIECES + piece) * kGroup + lane % 8 * 8) * 2;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int j = 0; j < 4 * R; ++j)
+      stage[j] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(src + row[j] * ld) + at);
+  }
+  __device__ __forceinline__ void put(uint8_t *lds, int wave, int lane) const {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)     // an odd last group reads the one before it, and is not used
-        s.x[r][0][k] = *reinterpret_cast<const uint4 *>(xr[r] + min(2 * p + k / 2, G - 1) * kGroup + 8 * (k % 2));
-  };
-  auto work = [&](int p, const S &s) {
+    for (int j = 0; j < 4 * R; ++j) {
+      const int r = wave + 4 * j;
+      *reinterpret_cast<uint4 *>(lds + r * 1024 + (lane / 16) * 256 + ((lane ^ r) % 16) * 16) = stage[j];
+    }
+  }
+  __device__ __forceinline__ uint4 operand(const uint8_t *lds, int r, int s, int k, int lane) const {
+    const int row = 16 * r + lane % 16, piece = 8 * (k / 2) + 2 * (lane / 16) + k % 2;
+    return *reinterpret_cast<const uint4 *>(lds + row * 1024 + s * 256 + ((piece ^ row) % 16) * 16);
+  }
+  // all steps; `group(i, ring place, operands of piece 0 and 1, r)` adds a group
+  template <typename Group>
+  __device__ __forceinline__ void run(uint8_t *lds, const int (&row)[4 * R], int wave, int lane, Group group) {
+    const int chunks = (each + CHUNK - 1) / CHUNK;
+    fetch(0, row, lane);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (2 * p + i >= G) break;
+    for (int i = 0; i < RING; ++i) load_step(i, p0 + i, lane);
+    put(lds, wave, lane);
+    __syncthreads();
+    uint8_t *cur = lds, *other = lds + 16 * R * 1024;
+    for (int c = 0; c < chunks; c += RING / CHUNK) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const uint4 a0 = s.x[r][0][2 * i], a1 = s.x[r][0][2 * i + 1];
-        v4f xsum = v4f{};
-        if constexpr (!F16) xsum = mma(a1, ones(), mma(a0, ones(), v4f{}));
+      for (int i = 0; i < RING; ++i) {
+        if (i % CHUNK == 0) {
+          if (i > 0 && c + i / CHUNK >= chunks) break;
+          fetch(c + i / CHUNK + 1, row, lane);
+        }
+        const int p = p0 + c * CHUNK + i;
+        if (p < p1) {
 #pragma unroll
-        for (int t = 0; t < 2 * TP; ++t)
-          group_mma<F16>(a0, a1, xsum, i ? s.code[t].z : s.code[t].x, i ? s.code[t].w : s.code[t].y,
-                         i ? s.sz[t].y : s.sz[t].x, acc[t / TP][r][t % TP]);
+          for (int g = 0; g < 2; ++g) {
+            if (2 * p + g >= G) break;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              uint4 a[PIECES][2];
+#pragma unroll
+              for (int h = 0; h < PIECES; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  a[h][k] = operand(cur, r, (wave % KS * CHUNK + i % CHUNK) * PIECES + h, 2 * g + k, lane);
+              group(g, i, a, r);
+            }
+          }
+        }
+        load_step(i, p + RING, lane);
+        if (i % CHUNK == CHUNK - 1) {
+          put(other, wave, lane);
+          __syncthreads();
+          uint8_t *x = cur;
+          cur = other;
+          other = x;
+        }
       }
     }
-  };
-  if (p0 >= p1) return;
-  S x, y;
-  load(p0, x);
-  for (int p = p0;; p += 2) {
-    load(min(p + 1, p1 - 1), y);
-    work(p, x);
-    if (p + 1 >= p1) break;
-    load(min(p + 2, p1 - 1), x);
-    work(p + 1, y);
-    if (p + 2 >= p1) break;
+  }
+};
+
+// The KS parts' sums meet, in order, in the first part's wavefront.
+template <int N, int KS>
+__device__ __forceinline__ void meet(v4f (&acc)[N], uint8_t *lds, int w, int lane) {
+  if constexpr (KS > 1) {
+    v4f (*red)[N][64] = reinterpret_cast<v4f (*)[N][64]>(lds);
+    if (w % KS != 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[w][i][lane] = acc[i];
+    }
+    __syncthreads();
+    if (w % KS == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 1; k < KS; ++k) {
+          const v4f y = red[w + k][i][lane];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] += y[e];
+        }
+    }
+    __syncthreads();
   }
 }
 
-template <bool F16, bool GELU, int TP, int KS, bool PLAN>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void moe_gate_up_kernel(MoeArgs a) {
+// h = act(gate) * up of 16 columns a wavefront (tiles: the gate's and the up's).
+template <bool F16, bool GELU, int KS, int R, bool PLAN>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(GUW))) void moe_gate_up_kernel(MoeArgs a) {
+  typedef Product<2, 1, KS, R> Pr;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Pr::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Rows<PLAN> rows;
   if (!rows.find(a, blockIdx.y, lane)) return;
-  const int G = a.K / kGroup, n = a.I / kAwqTile;
-  const AwqLayout L(2 * (int64_t)a.I, a.K);
-  const uint8_t *blob = a.gate_up + rows.expert * a.gate_up_stride;
-  const int tile0 = (blockIdx.x * (4 / KS) + w / KS) * TP;
-  Tiles tl[2][TP];
+  const int n = a.I / kAwqTile, tile = blockIdx.x * (4 / KS) + w / KS;
+  Pr pr;
+  const int tiles[2] = {min(tile, n - 1), min(tile, n - 1) + n};
+  pr.init(a.gate_up + rows.expert * a.gate_up_stride, MoeWeightLayout(2 * (int64_t)a.I, a.K), tiles, w);
+  pr.src = a.x;
+  pr.ld = a.K;
+  for (int r0 = 0; r0 < rows.count; r0 += 16 * R) {
+    int row[4 * R];
 #pragma unroll
-  for (int t = 0; t < TP; ++t) {        // tiles past the last are worked on as the last, and not stored
-    tl[0][t] = tiles_of(blob, L, min(tile0 + t, n - 1), lane);
-    tl[1][t] = tiles_of(blob, L, min(tile0 + t, n - 1) + n, lane);
-  }
-  int p0, p1;
-  wave_steps(G, w % KS, KS, p0, p1);
-  __shared__ v4f red[KS > 1 ? 4 : 1][KS > 1 ? 4 * TP : 1][64];
-
-  auto pass = [&](int r0, auto rt) {
-    constexpr int R = decltype(rt)::value;
-    const uint16_t *xr[R];
+    for (int j = 0; j < 4 * R; ++j) row[j] = rows.one(min(r0 + w + 4 * j, rows.count - 1)) / a.top_k;
+    v4f acc[2 * R] = {};
+    pr.run(lds, row, w, lane, [&](int g, int i, const uint4 (&x)[1][2], int r) {
+      v4f xsum = v4f{};
+      if constexpr (!F16) xsum = mma(x[0][1], ones(), mma(x[0][0], ones(), v4f{}));
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      xr[r] = a.x + (int64_t)(rows.pair(min(r0 + 16 * r + (lane & 15), rows.count - 1)) / a.top_k) * a.K + 16 * (lane >> 4);
-    v4f acc[2][R][TP] = {};
-    gate_up_rows<F16, TP, R>(a, tl, xr, G, p0, p1, acc);
-    if constexpr (KS > 1) {             // the parts meet, in order, in the first one's wavefront
-      if (w % KS != 0) {
-#pragma unroll
-        for (int i = 0; i < 2 * R * TP; ++i) red[w][i][lane] = acc[i / (R * TP)][i / TP % R][i % TP];
-      }
-      __syncthreads();
-      if (w % KS == 0) {
-#pragma unroll
-        for (int i = 0; i < 2 * R * TP; ++i)
-#pragma unroll
-          for (int k = 1; k < KS; ++k) {
-            const v4f y = red[w + k][i][lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i / (R * TP)][i / TP % R][i % TP][e] += y[e];
-          }
-      }
-      __syncthreads();
-      if (w % KS != 0) return;
-    }
+      for (int t = 0; t < 2; ++t)
+        group_mma<F16>(x[0][0], x[0][1], xsum, g ? pr.code[i][t].z : pr.code[i][t].x,
+                       g ? pr.code[i][t].w : pr.code[i][t].y, g ? pr.sz[i][t].y : pr.sz[i][t].x, acc[2 * r + t]);
+    });
+    meet<2 * R, KS>(acc, lds, w, lane);
+    if (w % KS != 0) continue;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int row = r0 + 16 * r + 4 * (lane >> 4) + e;
-        const int64_t at = (int64_t)rows.pair(min(row, rows.count - 1)) * a.I + (lane & 15);
-#pragma unroll
-        for (int t = 0; t < TP; ++t) {
-          const float g = acc[0][r][t][e], u = acc[1][r][t][e];
-          const float h = (GELU ? gelu_tanh_f32(g) : g * __builtin_amdgcn_rcpf(1.0f + __expf(-g))) * u;
-          if (row < rows.count && tile0 + t < n) {
-            const __bf16 hi = (__bf16)h;
-            a.h_hi[at + (tile0 + t) * kAwqTile] = __builtin_bit_cast(uint16_t, hi);
-            a.h_lo[at + (tile0 + t) * kAwqTile] =
-                __builtin_bit_cast(uint16_t, (__bf16)(__builtin_isfinite(h) ? h - (float)hi : 0.0f));
-          }
+        const int at_row = r0 + 16 * r + 4 * (lane >> 4) + e;
+        const int64_t at = (int64_t)rows.pair(min(at_row, rows.count - 1)) * (2 * a.I) + tile / 4 * 128 +
+                           tile % 4 * kAwqTile + (lane & 15);
+        const float g = acc[2 * r][e], u = acc[2 * r + 1][e];
+        const float h = (GELU ? gelu_tanh_f32(g) : g * __builtin_amdgcn_rcpf(1.0f + __expf(-g))) * u;
+        if (at_row < rows.count && tile < n) {
+          const __bf16 hi = (__bf16)h;
+          a.h[at] = __builtin_bit_cast(uint16_t, hi);
+          a.h[at + kGroup] = __builtin_bit_cast(uint16_t, (__bf16)(__builtin_isfinite(h) ? h - (float)hi : 0.0f));
         }
       }
-  };
-  for (int r0 = 0; r0 < rows.count;) {
-    if (rows.count - r0 > 16) {
-      pass(r0, Int<2>{});
-      r0 += 32;
-    } else {
-      pass(r0, Int<1>{});
-      r0 += 16;
-    }
   }
 }
 
-// h enters the down product as its two bf16 pieces (h to 2^-17, in float32's
-// range).
-template <int TP, int KS, bool PLAN>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void moe_down_kernel(MoeArgs a) {
+// TILES tiles of 16 columns of h Down^T a wavefront; h enters as its two bf16
+// pieces (h to 2^-17, in float32's range).
+template <int TILES, int KS, int R, bool PLAN>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DNW))) void moe_down_kernel(MoeArgs a) {
+  typedef Product<TILES, 2, KS, R> Pr;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Pr::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Rows<PLAN> rows;
   if (!rows.find(a, blockIdx.y, lane)) return;
-  const int G = a.I / kGroup, n = a.K / kAwqTile;
-  const AwqLayout L(a.K, a.I);
-  const uint8_t *blob = a.down + rows.expert * a.down_stride;
-  const int tile0 = (blockIdx.x * (4 / KS) + w / KS) * TP;
-  Tiles tl[TP];
+  const int n = a.K / kAwqTile, tile0 = (blockIdx.x * (4 / KS) + w / KS) * TILES;
+  Pr pr;
+  int tiles[TILES];
 #pragma unroll
-  for (int t = 0; t < TP; ++t) tl[t] = tiles_of(blob, L, min(tile0 + t, n - 1), lane);
-  int p0, p1;
-  wave_steps(G, w % KS, KS, p0, p1);
-  __shared__ v4f red[KS > 1 ? 4 : 1][KS > 1 ? TP : 1][64];
-
-  for (int r0 = 0; r0 < rows.count; r0 += 16) {
-    const int64_t at = (int64_t)rows.pair(min(r0 + (lane & 15), rows.count - 1)) * a.I + 16 * (lane >> 4);
-    const uint16_t *hr[2] = {a.h_hi + at, a.h_lo + at};
-    v4f acc[TP] = {};
-    typedef Step<TP, 1, 2> S;
-    auto load = [&](int p, S &s) {
+  for (int t = 0; t < TILES; ++t) tiles[t] = min(tile0 + t, n - 1);
+  pr.init(a.down + rows.expert * a.down_stride, MoeWeightLayout(a.K, a.I), tiles, w);
+  pr.src = a.h;
+  pr.ld = 2 * a.I;
+  for (int r0 = 0; r0 < rows.count; r0 += 16 * R) {
+    int row[4 * R];
 #pragma unroll
-      for (int t = 0; t < TP; ++t) {
-        s.code[t] = *reinterpret_cast<const uint4 *>(tl[t].code + (int64_t)p * kAwqBlockBytes);
-        s.sz[t] = *reinterpret_cast<const uint2 *>(tl[t].sz + 2 * p);
+    for (int j = 0; j < 4 * R; ++j) row[j] = rows.one(min(r0 + w + 4 * j, rows.count - 1));
+    v4f acc[TILES * R] = {};
+    pr.run(lds, row, w, lane, [&](int g, int i, const uint4 (&h)[2][2], int r) {
+      const v4f sum = mma(h[1][1], ones(), mma(h[1][0], ones(), mma(h[0][1], ones(), mma(h[0][0], ones(), v4f{}))));
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        const v8bf b0 = codes_128(g ? pr.code[i][t].z : pr.code[i][t].x);
+        const v8bf b1 = codes_128(g ? pr.code[i][t].w : pr.code[i][t].y);
+        const v4f prod = mma(h[1][1], b1, mma(h[1][0], b0, mma(h[0][1], b1, mma(h[0][0], b0, v4f{}))));
+        const uint32_t sz = g ? pr.sz[i][t].y : pr.sz[i][t].x;
+        const float z = -(128.0f + (float)zero_of(sz)), sc = scale_of(sz);
+        v4f &o = acc[TILES * r + t];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(__builtin_fmaf(z, sum[e], prod[e]), sc, o[e]);
       }
+    });
+    meet<TILES * R, KS>(acc, lds, w, lane);
+    if (w % KS != 0) continue;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          s.x[0][h][k] = *reinterpret_cast<const uint4 *>(hr[h] + min(2 * p + k / 2, G - 1) * kGroup + 8 * (k % 2));
-    };
-    auto work = [&](int p, const S &s) {
+      for (int e = 0; e < 4; ++e) {
+        const int at_row = r0 + 16 * r + 4 * (lane >> 4) + e;
+        const int64_t to = (int64_t)rows.pair(min(at_row, rows.count - 1)) * a.K + (lane & 15);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (2 * p + i >= G) break;
-        const uint4 h0 = s.x[0][0][2 * i], h1 = s.x[0][0][2 * i + 1], l0 = s.x[0][1][2 * i], l1 = s.x[0][1][2 * i + 1];
-        const v4f sum = mma(l1, ones(), mma(l0, ones(), mma(h1, ones(), mma(h0, ones(), v4f{}))));
-#pragma unroll
-        for (int t = 0; t < TP; ++t) {
-          const v8bf b0 = codes_128(i ? s.code[t].z : s.code[t].x), b1 = codes_128(i ? s.code[t].w : s.code[t].y);
-          const v4f prod = mma(l1, b1, mma(l0, b0, mma(h1, b1, mma(h0, b0, v4f{}))));
-          const uint32_t sz = i ? s.sz[t].y : s.sz[t].x;
-          const float z = -(128.0f + (float)zero_of(sz)), sc = scale_of(sz);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(__builtin_fmaf(z, sum[e], prod[e]), sc, acc[t][e]);
-        }
+        for (int t = 0; t < TILES; ++t)
+          if (at_row < rows.count && tile0 + t < n) a.part[to + (tile0 + t) * kAwqTile] = acc[TILES * r + t][e];
       }
-    };
-    if (p0 < p1) {
-      S x, y;
-      load(p0, x);
-      for (int p = p0;; p += 2) {
-        load(min(p + 1, p1 - 1), y);
-        work(p, x);
-        if (p + 1 >= p1) break;
-        load(min(p + 2, p1 - 1), x);
-        work(p + 1, y);
-        if (p + 2 >= p1) break;
-      }
-    }
-    if constexpr (KS > 1) {
-      if (w % KS != 0) {
-#pragma unroll
-        for (int t = 0; t < TP; ++t) red[w][t][lane] = acc[t];
-      }
-      __syncthreads();
-      if (w % KS == 0) {
-#pragma unroll
-        for (int t = 0; t < TP; ++t)
-#pragma unroll
-          for (int k = 1; k < KS; ++k) {
-            const v4f y = red[w + k][t][lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[t][e] += y[e];
-          }
-      }
-      __syncthreads();
-      if (w % KS != 0) continue;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = r0 + 4 * (lane >> 4) + e;
-      const int64_t to = (int64_t)rows.pair(min(row, rows.count - 1)) * a.K + (lane & 15);
-#pragma unroll
-      for (int t = 0; t < TP; ++t)
-        if (row < rows.count && tile0 + t < n) a.part[to + (tile0 + t) * kAwqTile] = acc[t][e];
-    }
   }
 }
 
@@ -595,19 +619,6 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
 }
 
 }  // namespace
-
-#ifndef GTP0
-#define GTP0 1
-#define GKS0 4
-#define GTP1 1
-#define GKS1 1
-#define DTP0 1
-#define DKS0 2
-#define DTP1 4
-#define DKS1 1
-#define FEWG 2048
-#define FEWD 4096
-#endif
 
 extern "C" {
 
@@ -678,8 +689,8 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   MoeArgs a{};
   a.gate_up = static_cast<const uint8_t *>(w->gate_up);
   a.down = static_cast<const uint8_t *>(w->down);
-  a.gate_up_stride = AwqLayout(2 * (int64_t)w->I, w->K).total;
-  a.down_stride = AwqLayout(w->K, w->I).total;
+  a.gate_up_stride = MoeWeightLayout(2 * (int64_t)w->I, w->K).total;
+  a.down_stride = MoeWeightLayout(w->K, w->I).total;
   a.E = w->E;
   a.K = w->K;
   a.I = w->I;
@@ -688,37 +699,36 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   a.top_k = top_k;
   a.ids = ids;
   a.weights = weights;
-  a.h_hi = reinterpret_cast<uint16_t *>(ws + L.h_hi);
-  a.h_lo = reinterpret_cast<uint16_t *>(ws + L.h_lo);
+  a.h = reinterpret_cast<uint16_t *>(ws + L.h);
   a.part = reinterpret_cast<float *>(ws + L.part);
   a.y = static_cast<uint16_t *>(y);
   a.plan = reinterpret_cast<MoePlan *>(ws + L.plan);
   const int pairs = T * top_k, slots = pairs < w->E ? pairs : w->E;
-  const bool plan = pairs > 64;
+  const bool plan = pairs > 64 || pairs > 12 * slots;
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   if (plan) hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
   const int gt = w->I / kAwqTile, dt = w->K / kAwqTile;
-#define MOE_GU3(F, A, TP, KS, P)                                                                        \
-  hipLaunchKernelGGL((moe_gate_up_kernel<F, A, TP, KS, P>),                                             \
-                     dim3((gt + TP * (4 / KS) - 1) / (TP * (4 / KS)), (unsigned)slots), dim3(256), 0, stream, a)
-#define MOE_GU2(F, A, P) do { if (few) MOE_GU3(F, A, GTP0, GKS0, P); else MOE_GU3(F, A, GTP1, GKS1, P); } while (0)
-#define MOE_GU(F, A) do { if (plan) MOE_GU2(F, A, true); else MOE_GU2(F, A, false); } while (0)
-#define MOE_D3(TP, KS, P)                                                                               \
-  hipLaunchKernelGGL((moe_down_kernel<TP, KS, P>), dim3((dt + TP * (4 / KS) - 1) / (TP * (4 / KS)), (unsigned)slots), \
+  const bool few = (int64_t)slots * gt < FEWG, few_down = (int64_t)slots * dt < FEWD, many = pairs > 12 * slots;
+#define MOE_GU(F, A, KS, R, P)                                                                                         \
+  hipLaunchKernelGGL((moe_gate_up_kernel<F, A, KS, R, P>), dim3((gt + 4 / KS - 1) / (4 / KS), (unsigned)slots),        \
                      dim3(256), 0, stream, a)
-#define MOE_D2(P) do { if (few_down) MOE_D3(DTP0, DKS0, P); else MOE_D3(DTP1, DKS1, P); } while (0)
-  const bool few = (int64_t)slots * gt < FEWG, few_down = (int64_t)slots * dt < FEWD;
+#define MOE_GU_R(F, A, KS) do { if (many) MOE_GU(F, A, KS, 2, true); else if (plan) MOE_GU(F, A, KS, 1, true); else MOE_GU(F, A, KS, 1, false); } while (0)
+#define MOE_GU_K(F, A) do { if (few) MOE_GU_R(F, A, GKS0); else MOE_GU_R(F, A, 1); } while (0)
+#define MOE_DN(TT, KS, R, P)                                                                                           \
+  hipLaunchKernelGGL((moe_down_kernel<TT, KS, R, P>), dim3((dt + TT * (4 / KS) - 1) / (TT * (4 / KS)), (unsigned)slots), \
+                     dim3(256), 0, stream, a)
+#define MOE_DN_R(TT, KS) do { if (many) MOE_DN(TT, KS, 2, true); else if (plan) MOE_DN(TT, KS, 1, true); else MOE_DN(TT, KS, 1, false); } while (0)
   if (dtype == SVDQ_FP16) {
-    if (act == SVDQ_MOE_GELU_TANH) MOE_GU(true, true); else MOE_GU(true, false);
+    if (act == SVDQ_MOE_GELU_TANH) MOE_GU_K(true, true); else MOE_GU_K(true, false);
   } else {
-    if (act == SVDQ_MOE_GELU_TANH) MOE_GU(false, true); else MOE_GU(false, false);
+    if (act == SVDQ_MOE_GELU_TANH) MOE_GU_K(false, true); else MOE_GU_K(false, false);
   }
-  if (plan) MOE_D2(true); else MOE_D2(false);
-#undef MOE_D2
-#undef MOE_D3
+  if (few_down) MOE_DN_R(DT0, DK0); else MOE_DN_R(DT1, 1);
+#undef MOE_DN_R
+#undef MOE_DN
+#undef MOE_GU_K
+#undef MOE_GU_R
 #undef MOE_GU
-#undef MOE_GU2
-#undef MOE_GU3
   const dim3 g3((unsigned)(((int64_t)T * (w->K / 4) + 255) / 256));
   if (dtype == SVDQ_FP16) hipLaunchKernelGGL((moe_sum_kernel<true>), g3, dim3(256), 0, stream, a);
   else hipLaunchKernelGGL((moe_sum_kernel<false>), g3, dim3(256), 0, stream, a);
