@@ -412,7 +412,8 @@ size_t svdq_kv4_cache_bytes(int num_pages, int page_size, int kv_heads, int head
  * for svdq_mx_linear_forward's activations; a block that holds an infinity or
  * a NaN gets scale byte 255, for which all its values read as NaN.  A slot outside
  * the cache is skipped (-1 marks padding rows).  The slots of one call must
- * differ; one named twice is left with parts of both rows.  One kernel. */
+ * differ; one named twice is left with parts of both rows.  T kv_heads
+ * head_dim <= 2^35.  One kernel. */
 svdq_status_t svdq_kv4_append(const svdq_kv4_cache_t *cache, const void *k, int64_t k_row, int64_t k_head,
                               const void *v, int64_t v_row, int64_t v_head, svdq_dtype_t dtype, int T,
                               const int32_t *slots, void *hip_stream);

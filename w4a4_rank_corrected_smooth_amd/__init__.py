@@ -714,24 +714,27 @@ def _need(t, name: str, device, dtypes, ndim: int) -> None:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _need_dense(t, name: str, device, dtypes, shape) -> None:
-    _need(t, name, device, dtypes, len(shape))
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got {tuple(t.shape)}")
+def _need_dense(t, name: str, device, dtype, shape) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-def _stride(t: torch.Tensor, i: int) -> int:
-    """The stride of dimension i, 0 where it has one element (torch leaves any value there)."""
-    return t.stride(i) if t.shape[i] > 1 else 0
+def _need_workspace(t, device) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
 
 
 def _call(device, f, *args) -> None:
     """A device entry point on `device`'s current stream."""
-    if torch.cuda.current_device() == device.index:
-        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    i = device.index
+    if i is None or i == torch.cuda.current_device():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     else:
         with torch.cuda.device(device):
-            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+            status = f(*args, torch._C._cuda_getCurrentRawStream(i))
     if status != OK:
         raise SvdqError(status, f.__name__)
 
@@ -750,23 +753,30 @@ class Kv4Cache:
         self.data = torch.zeros(n, dtype=torch.uint8, device=device)
         self.device = self.data.device
         self._c = Kv4CacheStruct(self.data.data_ptr(), num_pages, page_size, kv_heads, head_dim)
+        self._ref = ctypes.byref(self._c)
 
 
 def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
     """Encodes key and value rows [T, kv_heads, head_dim] (bf16 or fp16; any row and
     head strides that are multiples of 8) into the cache's slots [T] (int32, all different; slots
     outside the cache, such as -1, are skipped)."""
+    dev = cache.device
     for t, name in ((k, "k"), (v, "v")):
-        _need(t, name, cache.device, _DT16, 3)
-        if t.shape[1] != cache.kv_heads or t.shape[2] != cache.head_dim or t.stride(2) != 1:
+        _need(t, name, dev, _DT16, 3)
+        if t.shape[1:] != (cache.kv_heads, cache.head_dim) or t.stride(2) != 1:
             raise ValueError(f"{name} must be [T, {cache.kv_heads}, {cache.head_dim}] with adjacent channels, "
                              f"got {tuple(t.shape)} with strides {t.stride()}")
     T = k.shape[0]
     if v.shape[0] != T or v.dtype != k.dtype:
         raise ValueError("k and v must have the same rows and dtype")
-    _need_dense(slots, "slots", cache.device, (torch.int32,), (T,))
-    _call(cache.device, _lib.svdq_kv4_append, ctypes.byref(cache._c), k.data_ptr(), _stride(k, 0), _stride(k, 1),
-          v.data_ptr(), _stride(v, 0), _stride(v, 1), _DT16[k.dtype], T, slots.data_ptr())
+    _need_dense(slots, "slots", dev, torch.int32, (T,))
+    (k0, k1, _), (v0, v1, _) = k.stride(), v.stride()
+    if T == 1:                           # torch leaves any stride where there is one element
+        k0 = v0 = 0
+    if cache.kv_heads == 1:
+        k1 = v1 = 0
+    _call(dev, _lib.svdq_kv4_append, cache._ref, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, _DT16[k.dtype], T,
+          slots.data_ptr())
 
 
 def kv4_read(cache: Kv4Cache, slots: torch.Tensor, dtype=torch.bfloat16):
@@ -777,8 +787,9 @@ def kv4_read(cache: Kv4Cache, slots: torch.Tensor, dtype=torch.bfloat16):
     if not slots.is_contiguous():
         raise ValueError("slots must be contiguous")
     T = slots.shape[0]
-    k, v = (torch.empty((T, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device) for _ in "kv")
-    _call(cache.device, _lib.svdq_kv4_read, ctypes.byref(cache._c), slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
+    k = torch.empty((T, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
+    v = torch.empty((T, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
+    _call(cache.device, _lib.svdq_kv4_read, cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
           FP32 if dtype == torch.float32 else BF16)
     return k, v
 
@@ -806,18 +817,20 @@ def kv4_attention(cache: Kv4Cache, q: torch.Tensor, page_table: torch.Tensor, se
     _need(page_table, "page_table", dev, (torch.int32,), 2)
     if page_table.shape[0] != B or not page_table.is_contiguous():
         raise ValueError(f"page_table must be contiguous with {B} rows, got {tuple(page_table.shape)}")
-    _need_dense(seq_lens, "seq_lens", dev, (torch.int32,), (B,))
+    _need_dense(seq_lens, "seq_lens", dev, torch.int32, (B,))
     if out is None:
         out = torch.empty((B, Q, Hq, D), dtype=q.dtype, device=dev)
     else:
-        _need_dense(out, "out", dev, (q.dtype,), (B, Q, Hq, D))
+        _need_dense(out, "out", dev, q.dtype, (B, Q, Hq, D))
     if workspace is None:
         workspace = kv4_attention_workspace(cache, q)
     else:
-        _need_dense(workspace, "workspace", dev, (torch.uint8,), workspace.shape)
-    _call(dev, _lib.svdq_kv4_attention, ctypes.byref(cache._c), q.data_ptr(), _stride(q, 0), _stride(q, 1),
-          _stride(q, 2), _DT16[q.dtype], B, Q, Hq, page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
-          D ** -0.5 if scale is None else float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel())
+        _need_workspace(workspace, dev)
+    q0, q1, q2, _ = q.stride()           # torch leaves any stride where there is one element
+    _call(dev, _lib.svdq_kv4_attention, cache._ref, q.data_ptr(), q0 if B > 1 else 0, q1 if Q > 1 else 0,
+          q2 if Hq > 1 else 0, _DT16[q.dtype], B, Q, Hq, page_table.data_ptr(), page_table.shape[1],
+          seq_lens.data_ptr(), D ** -0.5 if scale is None else float(scale), out.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
     return out
 
 
@@ -840,14 +853,14 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, bias: Optiona
     if score not in MOE_SCORES:
         raise ValueError(f"score must be one of {tuple(MOE_SCORES)}, got {score!r}")
     if bias is not None:
-        _need_dense(bias, "bias", dev, (torch.float32,), (E,))
+        _need_dense(bias, "bias", dev, torch.float32, (E,))
     if workspace is None:
         n = _lib.svdq_moe_route_workspace_bytes(T, E)
         if n == 0:
             raise SvdqError(2, "svdq_moe_route_workspace_bytes")
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     else:
-        _need_dense(workspace, "workspace", dev, (torch.uint8,), workspace.shape)
+        _need_workspace(workspace, dev)
     if not 1 <= top_k <= E:
         raise ValueError(f"top_k={top_k} outside [1, {E}]")
     ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
@@ -893,6 +906,7 @@ class AwqMoe:
         self.down = torch.from_numpy(_moe_blob(down, self.K, self.I)).to(device)
         self.device = self.gate_up.device
         self._w = MoeWeights(self.gate_up.data_ptr(), self.down.data_ptr(), self.E, self.K, self.I)
+        self._ref = ctypes.byref(self._w)
 
     def workspace_bytes(self, T: int, top_k: int) -> int:
         n = _lib.awq_moe_workspace_bytes(T, top_k, self.K, self.I)
@@ -919,18 +933,18 @@ def awq_moe_forward(layer: AwqMoe, x: torch.Tensor, ids: torch.Tensor, weights: 
     top_k = ids.shape[1]
     if ids.shape[0] != T or not ids.is_contiguous():
         raise ValueError(f"ids must be contiguous with {T} rows, got {tuple(ids.shape)}")
-    _need_dense(weights, "weights", dev, (torch.float32,), (T, top_k))
+    _need_dense(weights, "weights", dev, torch.float32, (T, top_k))
     if activation not in MOE_ACTIVATIONS:
         raise ValueError(f"activation must be one of {tuple(MOE_ACTIVATIONS)}, got {activation!r}")
     if out is None:
         out = torch.empty((T, layer.K), dtype=x.dtype, device=dev)
     else:
-        _need_dense(out, "out", dev, (x.dtype,), (T, layer.K))
+        _need_dense(out, "out", dev, x.dtype, (T, layer.K))
     if workspace is None:
         workspace = layer.new_workspace(T, top_k)
     else:
-        _need_dense(workspace, "workspace", dev, (torch.uint8,), workspace.shape)
-    _call(dev, _lib.awq_moe_forward, ctypes.byref(layer._w), x.data_ptr(), _DT16[x.dtype], T, ids.data_ptr(),
+        _need_workspace(workspace, dev)
+    _call(dev, _lib.awq_moe_forward, layer._ref, x.data_ptr(), _DT16[x.dtype], T, ids.data_ptr(),
           weights.data_ptr(), top_k, MOE_ACTIVATIONS[activation], out.data_ptr(), workspace.data_ptr(),
           workspace.numel())
     return out

@@ -41,7 +41,7 @@ __device__ __forceinline__ float wide(uint32_t h) {
 }
 
 // ---------------------------------------------------------------- append, read
-// One thread per (row, keys or values, head, block of 32 channels).  With
+// One thread per (row, keys or values, head, block of 32 channels): with
 // a = max |v| and E its biased exponent field, e = E - 129 clamped at -127
 // (E = 0: -127); v 2^-e is exact and below 8, and the packed conversion
 // rounds it to the nearest E2M1 value, ties to the even code, 6 the largest.
@@ -68,87 +68,160 @@ __device__ __forceinline__ uint32_t encode_block(const float (&v)[32], uint32_t 
   return E == 255 ? 255u : (uint32_t)(e + 127);
 }
 
+// A thread's place: row, keys or values, head and block of 32 channels, four
+// neighbouring rows in neighbouring lanes and 16 rows of a head next to each
+// other, so that a wavefront of consecutive slots covers whole units.
+struct Item {
+  int t, h, b, is_v, i;
+  __device__ __forceinline__ explicit Item(uint32_t idx, const Kv4Layout &L) {
+    const int shift = L.D == 64 ? 1 : L.D == 128 ? 2 : 3;        // blocks of a row: 2, 4 or 8
+    i = idx & 3;
+    b = idx >> 2 & ((1 << shift) - 1);
+    const uint32_t r = idx >> (2 + shift), u = r >> 3, tile = u / (uint32_t)L.H;
+    is_v = r >> 2 & 1;
+    h = u - tile * L.H;
+    t = tile * 16 + 4 * (r & 3) + i;
+  }
+};
+// Whether the four lanes of a row quad hold tokens 4 c .. 4 c + 3 of a unit:
+// then a word of value codes, four tokens' bytes, is read or written whole.
+__device__ __forceinline__ bool whole_quad(int64_t slot, bool in, int i) {
+  const int first = __builtin_amdgcn_update_dpp(0, (int)slot, 0x00, 0xF, 0xF, true);    // quad_perm 0,0,0,0
+  const uint64_t ok = __ballot(in && (first & 3) == 0 && (int)slot == first + i);
+  return (ok >> (threadIdx.x & 60) & 15) == 15;
+}
+// four words of bytes, transposed: byte k of word j becomes byte j of word k
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+  const uint32_t c = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+  w[0] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+  w[1] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+  w[2] = __builtin_amdgcn_perm(d, c, 0x05040100u);
+  w[3] = __builtin_amdgcn_perm(d, c, 0x07060302u);
+}
+
 template <bool F16>
 __global__ __launch_bounds__(256) void kv4_append_kernel(uint8_t *__restrict__ data, Kv4Layout L,
                                                          const uint16_t *__restrict__ k, int64_t k_row,
                                                          int64_t k_head, const uint16_t *__restrict__ v,
                                                          int64_t v_row, int64_t v_head,
                                                          const int *__restrict__ slots, int T) {
+  __shared__ uint32_t swap[256][4];
   const int blocks = L.D / 32;
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int b = (int)(idx % blocks), h = (int)(idx / blocks % L.H);
-  const int64_t rest = idx / blocks / L.H;
-  const int t = (int)(rest >> 1), is_v = (int)(rest & 1);
-  if (t >= T) return;
-  const int64_t slot = slots[t];
-  if (slot < 0 || slot >= (int64_t)L.pages << L.page_shift) return;
-  const uint16_t *src = is_v ? v + t * v_row + h * v_head : k + t * k_row + h * k_head;
-  float x[32];
+  const Item it(blockIdx.x * 256 + threadIdx.x, L);
+  const int64_t slot = it.t < T ? slots[it.t] : -1;
+  const bool in = slot >= 0 && slot < (int64_t)L.pages << L.page_shift;
+  uint32_t w[4] = {0u, 0u, 0u, 0u}, scale = 0;
+  uint8_t *unit = data;
+  if (in) {
+    const uint16_t *src = it.is_v ? v + it.t * v_row + it.h * v_head : k + it.t * k_row + it.h * k_head;
+    float x[32];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(src + 32 * b + 8 * j);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int j = 0; j < 4; ++j) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(src + 32 * it.b + 8 * j);
+      const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      x[8 * j + 2 * c] = wide<F16>(w[c] & 0xFFFFu);
-      x[8 * j + 2 * c + 1] = wide<F16>(w[c] >> 16);
+      for (int c = 0; c < 4; ++c) {
+        x[8 * j + 2 * c] = wide<F16>(uw[c] & 0xFFFFu);
+        x[8 * j + 2 * c + 1] = wide<F16>(uw[c] >> 16);
+      }
     }
+    scale = encode_block(x, w);
+    unit += L.unit(slot >> L.page_shift, it.h, (int)(slot & (L.page_size() - 1)) >> 4);
   }
-  uint32_t w[4];
-  const uint32_t scale = encode_block(x, w);
-  uint8_t *unit = data + L.unit(slot >> L.page_shift, h, (int)(slot & (L.page_size() - 1)) >> 4);
   const int token = (int)(slot & 15);
-  if (!is_v) {
+  const bool quad = whole_quad(slot, in, it.i);
+  // value bytes r = 4 q .. 4 q + 3 of this token: channels r low, 16 + r high
+  uint32_t bytes[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t lo = w[q / 2] >> (16 * (q % 2)) & 0xFFFFu, hi = w[2 + q / 2] >> (16 * (q % 2)) & 0xFFFFu;
+    lo = (lo | lo << 8) & 0x00FF00FFu;
+    hi = (hi | hi << 8) & 0x00FF00FFu;
+    bytes[q] = ((lo | lo << 4) & 0x0F0F0F0Fu) | ((hi | hi << 4) & 0x0F0F0F0Fu) << 4;
+  }
+  *reinterpret_cast<uint4 *>(swap[threadIdx.x]) = make_uint4(bytes[0], bytes[1], bytes[2], bytes[3]);
+  __syncthreads();
+  if (!in) return;
+  if (!it.is_v) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      reinterpret_cast<uint32_t *>(unit)[(16 * c + token) * blocks + b] = w[c];
-    unit[L.k_scales() + token * blocks + b] = (uint8_t)scale;
+      reinterpret_cast<uint32_t *>(unit)[(16 * c + token) * blocks + it.b] = w[c];
+    unit[L.k_scales() + token * blocks + it.b] = (uint8_t)scale;
   } else {
-    uint8_t *vals = unit + L.v_codes();
+    if (quad) {                          // this lane writes words r = 4 i .. 4 i + 3
+      uint32_t m[4];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const uint32_t low = w[r / 8] >> (4 * (r % 8)) & 15u, high = w[2 + r / 8] >> (4 * (r % 8)) & 15u;
-      vals[((token / 4 * 16 + r) * blocks + b) * 4 + token % 4] = (uint8_t)(low | high << 4);
+      for (int n = 0; n < 4; ++n) m[n] = swap[(threadIdx.x & ~3) + n][it.i];
+      transpose4(m);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        reinterpret_cast<uint32_t *>(unit + L.v_codes())[(token / 4 * 16 + 4 * it.i + n) * blocks + it.b] = m[n];
+    } else {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        unit[L.v_codes() + ((token / 4 * 16 + r) * blocks + it.b) * 4 + token % 4] = (uint8_t)(bytes[r / 4] >> (8 * (r % 4)));
     }
-    unit[L.v_scales() + token * blocks + b] = (uint8_t)scale;
+    unit[L.v_scales() + token * blocks + it.b] = (uint8_t)scale;
   }
 }
 
-// One thread per (row, keys or values, head, block of 32 channels): the
-// values of a slot, as bf16 (exact: two significant bits) or float32; slots
-// outside the cache read as zeros.
+// The values of a slot, as bf16 (exact: two significant bits) or float32;
+// slots outside the cache read as zeros.
 template <bool F32>
 __global__ __launch_bounds__(256) void kv4_read_kernel(const uint8_t *__restrict__ data, Kv4Layout L,
                                                        const int *__restrict__ slots, int T,
                                                        void *__restrict__ k, void *__restrict__ v) {
+  __shared__ uint32_t swap[256][4];
+  __shared__ uint4 out[256][5];
   const int blocks = L.D / 32;
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int b = (int)(idx % blocks), h = (int)(idx / blocks % L.H);
-  const int64_t rest = idx / blocks / L.H;
-  const int t = (int)(rest >> 1), is_v = (int)(rest & 1);
-  if (t >= T) return;
-  const int64_t slot = slots[t];
+  const Item it(blockIdx.x * 256 + threadIdx.x, L);
+  const int64_t slot = it.t < T ? slots[it.t] : -1;
+  const bool in = slot >= 0 && slot < (int64_t)L.pages << L.page_shift;
+  const int token = (int)(slot & 15);
+  const bool quad = whole_quad(slot, in, it.i);
   uint32_t w[4] = {0u, 0u, 0u, 0u}, scale = 0;
-  if (slot >= 0 && slot < (int64_t)L.pages << L.page_shift) {
-    const uint8_t *unit = data + L.unit(slot >> L.page_shift, h, (int)(slot & (L.page_size() - 1)) >> 4);
-    const int token = (int)(slot & 15);
-    if (!is_v) {
+  if (in) {
+    const uint8_t *unit = data + L.unit(slot >> L.page_shift, it.h, (int)(slot & (L.page_size() - 1)) >> 4);
+    if (!it.is_v) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) w[c] = reinterpret_cast<const uint32_t *>(unit)[(16 * c + token) * blocks + b];
-      scale = unit[L.k_scales() + token * blocks + b];
+      for (int c = 0; c < 4; ++c) w[c] = reinterpret_cast<const uint32_t *>(unit)[(16 * c + token) * blocks + it.b];
+      scale = unit[L.k_scales() + token * blocks + it.b];
     } else {
-      const uint8_t *vals = unit + L.v_codes();
+      if (quad) {                        // words r = 4 i .. 4 i + 3, a byte of each token
+        uint32_t m[4];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const uint32_t byte = vals[((token / 4 * 16 + r) * blocks + b) * 4 + token % 4];
-        w[r / 8] |= (byte & 15u) << (4 * (r % 8));
-        w[2 + r / 8] |= (byte >> 4) << (4 * (r % 8));
+        for (int n = 0; n < 4; ++n)
+          m[n] = reinterpret_cast<const uint32_t *>(unit + L.v_codes())[(token / 4 * 16 + 4 * it.i + n) * blocks + it.b];
+        transpose4(m);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) swap[(threadIdx.x & ~3) + n][it.i] = m[n];
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            m |= (uint32_t)unit[L.v_codes() + ((token / 4 * 16 + 4 * q + n) * blocks + it.b) * 4 + token % 4] << (8 * n);
+          swap[threadIdx.x][q] = m;
+        }
       }
-      scale = unit[L.v_scales() + token * blocks + b];
+      scale = unit[L.v_scales() + token * blocks + it.b];
+    }
+  }
+  __syncthreads();
+  if (in && it.is_v) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {        // bytes r = 4 q .. 4 q + 3 back to nibbles of channels r and 16 + r
+      const uint32_t m = swap[threadIdx.x][q];
+      uint32_t lo = m & 0x0F0F0F0Fu, hi = m >> 4 & 0x0F0F0F0Fu;
+      lo = (lo | lo >> 4) & 0x00FF00FFu;
+      hi = (hi | hi >> 4) & 0x00FF00FFu;
+      w[q / 2] |= ((lo | lo >> 8) & 0xFFFFu) << (16 * (q % 2));
+      w[2 + q / 2] |= ((hi | hi >> 8) & 0xFFFFu) << (16 * (q % 2));
     }
   }
   const float s = __uint_as_float(scale << 23);
-  const int64_t at = ((int64_t)t * L.H + h) * L.D + 32 * b;
   uint32_t pairs[16];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -157,17 +230,28 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(const uint8_t *__restrict
     pairs[4 * j + 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 2));
     pairs[4 * j + 3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 3));
   }
-  if constexpr (F32) {
-    float4 *out = reinterpret_cast<float4 *>(static_cast<float *>(is_v ? v : k) + at);
+  // through LDS, so that neighbouring lanes store neighbouring 16-byte pieces
+  // of a row (a block is four; 8190 rows of 8 heads of 128 took 15 us without)
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      out[j] = make_float4(bf16_lo(pairs[2 * j]), bf16_hi(pairs[2 * j]), bf16_lo(pairs[2 * j + 1]),
-                           bf16_hi(pairs[2 * j + 1]));
-  } else {
-    uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(is_v ? v : k) + at);
+  for (int j = 0; j < 4; ++j)
+    out[threadIdx.x][j] = make_uint4(pairs[4 * j], pairs[4 * j + 1], pairs[4 * j + 2], pairs[4 * j + 3]);
+  __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      out[j] = make_uint4(pairs[4 * j], pairs[4 * j + 1], pairs[4 * j + 2], pairs[4 * j + 3]);
+  for (int j = 0; j < 4; ++j) {
+    const int piece = threadIdx.x + 256 * j, off = piece & (4 * blocks - 1);
+    const int seg = piece >> (L.D == 64 ? 3 : L.D == 128 ? 4 : 5);
+    const int item = ((seg >> 2) * blocks + (off >> 2)) * 4 + (seg & 3);
+    const Item to(blockIdx.x * 256 + item, L);
+    if (to.t >= T) continue;
+    const uint4 u = out[item][off % 4];
+    const int64_t at = ((int64_t)to.t * L.H + to.h) * L.D + 8 * off;
+    if constexpr (F32) {
+      float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(to.is_v ? v : k) + at);
+      f[0] = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+      f[1] = make_float4(bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w));
+    } else {
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(to.is_v ? v : k) + at) = u;
+    }
   }
 }
 
@@ -772,8 +856,8 @@ svdq_status_t svdq_kv4_append(const svdq_kv4_cache_t *cache, const void *k, int6
   const int64_t strides[4] = {k_row, k_head, v_row, v_head};
   if (!aligned16(k) || !aligned16(v) || ((uintptr_t)slots & 3u) || !strides_ok(strides, 4))
     return fail(SVDQ_ERR_INVALID_ARGUMENT, "svdq_kv4_append: misaligned pointer, or a stride that is not a multiple of 8");
-  const int64_t threads = (int64_t)T * L.H * 2 * (L.D / 32);
-  if (threads > (int64_t)1 << 38) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_append: T=%d", T);
+  const int64_t threads = ((int64_t)T + 15) / 16 * 16 * L.H * 2 * (L.D / 32);
+  if (threads > (int64_t)1 << 31) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_append: T=%d", T);
   st = svdq_device_check();
   if (st != SVDQ_OK) return st;
   const dim3 grid((unsigned)((threads + 255) / 256));
@@ -801,8 +885,8 @@ svdq_status_t svdq_kv4_read(const svdq_kv4_cache_t *cache, const int32_t *slots,
   if (!k || !v || !slots) return fail(SVDQ_ERR_INVALID_ARGUMENT, "svdq_kv4_read: NULL pointer");
   if (!aligned16(k) || !aligned16(v) || ((uintptr_t)slots & 3u))
     return fail(SVDQ_ERR_INVALID_ARGUMENT, "svdq_kv4_read: misaligned pointer");
-  const int64_t threads = (int64_t)T * L.H * 2 * (L.D / 32);
-  if (threads > (int64_t)1 << 38) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_read: T=%d", T);
+  const int64_t threads = ((int64_t)T + 15) / 16 * 16 * L.H * 2 * (L.D / 32);
+  if (threads > (int64_t)1 << 31) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_read: T=%d", T);
   st = svdq_device_check();
   if (st != SVDQ_OK) return st;
   const dim3 grid((unsigned)((threads + 255) / 256));

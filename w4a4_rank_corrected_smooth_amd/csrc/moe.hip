@@ -17,6 +17,18 @@ using namespace svdq;
 #ifndef GKS0
 #define GKS0 4
 #endif
+#ifndef GFKS
+#define GFKS 4
+#endif
+#ifndef FEWI
+#define FEWI 128
+#endif
+#ifndef DFW
+#define DFW 8
+#endif
+#ifndef FEWP
+#define FEWP 16
+#endif
 #ifndef DT0
 #define DT0 2
 #endif
@@ -58,6 +70,10 @@ __device__ __forceinline__ float wide(uint32_t h) {
 // sum cannot move a logit across its neighbour's and the choice does not
 // depend on how the work is split.  One wavefront per expert and kTokens tokens.
 constexpr int kTokens = 4;
+// Logits of a call above which the matrix form takes over: at K = 4096 the two
+// took 15.5 and 20.4 us for 64 x 256 logits (router in all), 23.5 and 21.5 for
+// 128 x 256, 37.4 and 22.1 for 250 x 256.
+constexpr int kTileLogits = 24576;
 
 template <bool F16>
 __global__ __launch_bounds__(256) void moe_logits_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ wr,
@@ -66,17 +82,29 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const uint16_t *__restr
   const int t0 = blockIdx.y * kTokens;
   if (e >= E) return;
   double acc[kTokens] = {};
-  for (int k = lane * 8; k < K; k += 512) {
-    const uint4 wv = *reinterpret_cast<const uint4 *>(wr + (int64_t)e * K + k);
-    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+  // two turns of 512 channels at a time, all their loads in flight
+  for (int k0 = lane * 8; k0 < K + lane * 8; k0 += 1024) {
+    uint4 wv[2], xv[2][kTokens];
 #pragma unroll
-    for (int t = 0; t < kTokens; ++t) {
-      const uint4 xv = *reinterpret_cast<const uint4 *>(x + (int64_t)min(t0 + t, T - 1) * K + k);
-      const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+    for (int i = 0; i < 2; ++i) {
+      const int k = min(k0 + 512 * i, K - 8);
+      wv[i] = *reinterpret_cast<const uint4 *>(wr + (int64_t)e * K + k);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[t] += (double)(wide<F16>(ww[i] & 0xFFFFu) * wide<F16>(xw[i] & 0xFFFFu));
-        acc[t] += (double)(wide<F16>(ww[i] >> 16) * wide<F16>(xw[i] >> 16));
+      for (int t = 0; t < kTokens; ++t)
+        xv[i][t] = *reinterpret_cast<const uint4 *>(x + (int64_t)min(t0 + t, T - 1) * K + k);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (k0 + 512 * i >= K) break;
+      const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+#pragma unroll
+      for (int t = 0; t < kTokens; ++t) {
+        const uint32_t xw[4] = {xv[i][t].x, xv[i][t].y, xv[i][t].z, xv[i][t].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[t] += (double)(wide<F16>(ww[j] & 0xFFFFu) * wide<F16>(xw[j] & 0xFFFFu));
+          acc[t] += (double)(wide<F16>(ww[j] >> 16) * wide<F16>(xw[j] >> 16));
+        }
       }
     }
   }
@@ -88,78 +116,192 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const uint16_t *__restr
   }
 }
 
+// The same for more tokens: 16 x 16 logits a workgroup on the float64 matrix
+// instruction, its eight wavefronts an eighth of K each (in turns of 32
+// channels), met in LDS in order.  A lane holds row (token, expert) l % 16 and
+// channels 8 (l / 16) + [0, 8) of a turn, one for each of eight products; the
+// channels' order does not matter as long as both operands agree.  Both
+// operands are used by 16 rows of the other, where the form above converts
+// every product.
+typedef double v4d __attribute__((ext_vector_type(4)));
+
+template <bool F16>
+__global__ __launch_bounds__(512) void moe_logits_tile_kernel(const uint16_t *__restrict__ x,
+                                                              const uint16_t *__restrict__ wr, int T, int E, int K,
+                                                              double *__restrict__ logits) {
+  __shared__ v4d red[8][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = 8 * (lane >> 4);
+  const int t0 = blockIdx.y * 16, e0 = blockIdx.x * 16;
+  const uint16_t *xr = x + (int64_t)min(t0 + (lane & 15), T - 1) * K;
+  const uint16_t *er = wr + (int64_t)min(e0 + (lane & 15), E - 1) * K;
+  v4d acc = v4d{};
+  const int turns = (K + 31) / 32;
+  auto load = [&](int i, uint4 &a, uint4 &b) {
+    const int k = min(32 * i + c, K - 8);
+    a = *reinterpret_cast<const uint4 *>(xr + k);
+    b = *reinterpret_cast<const uint4 *>(er + k);
+  };
+  constexpr int AHEAD = 4;
+  uint4 a[AHEAD], b[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) load(min(w + 8 * i, turns - 1), a[i], b[i]);
+  for (int i0 = w; i0 < turns; i0 += 8 * AHEAD) {
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) {
+      const int i = i0 + 8 * n;
+      if (i >= turns) break;
+      const bool in = 32 * i + c < K;                     // the last turn may end inside
+      const uint32_t aw[4] = {a[n].x, a[n].y, a[n].z, a[n].w}, bw[4] = {b[n].x, b[n].y, b[n].z, b[n].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const double a0 = in ? (double)wide<F16>(aw[j] & 0xFFFFu) : 0.0, a1 = in ? (double)wide<F16>(aw[j] >> 16) : 0.0;
+        const double b0 = in ? (double)wide<F16>(bw[j] & 0xFFFFu) : 0.0, b1 = in ? (double)wide<F16>(bw[j] >> 16) : 0.0;
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a0, b0, acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a1, b1, acc, 0, 0, 0);
+      }
+      load(min(i + 8 * AHEAD, turns - 1), a[n], b[n]);
+    }
+  }
+  red[w][lane] = acc;
+  __syncthreads();
+  // wavefronts 0..3 take one element of each lane: token 4 e + lane / 16, expert lane % 16
+  if (w >= 4) return;
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s += red[k][lane][w];
+  const int t = t0 + 4 * w + (lane >> 4), e = e0 + (lane & 15);
+  if (t < T && e < E) logits[(int64_t)t * E + e] = s;
+}
+
+// Reductions over the wavefront within the vector unit: lanes of a row of 16,
+// then the rows' last lanes into the next; the result stands in lane 63.
+template <typename Op>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t x, uint32_t none, Op op) {
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, 0x111, 0xF, 0xF, false));   // row_shr:1
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, 0x112, 0xF, 0xF, false));
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, 0x114, 0xF, 0xF, false));
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, 0x118, 0xF, 0xF, false));
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, 0x142, 0xA, 0xF, false));   // row_bcast:15
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, 0x143, 0xC, 0xF, false));   // row_bcast:31
+  return __builtin_amdgcn_readlane(x, 63);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  return wave_reduce(x, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+__device__ __forceinline__ uint32_t wave_min(uint32_t x) {
+  return wave_reduce(x, ~0u, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_dpp(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+  return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_f64(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double x) {
+  x = add_dpp<0x111, 0xF>(x);
+  x = add_dpp<0x112, 0xF>(x);
+  x = add_dpp<0x114, 0xF>(x);
+  x = add_dpp<0x118, 0xF>(x);
+  x = add_dpp<0x142, 0xA>(x);
+  x = add_dpp<0x143, 0xC>(x);
+  return lane_f64(x, 63);
+}
+// A number's place in the order of numbers, as an unsigned integer; NaN is the
+// smallest, and the two zeros are equal.
+__device__ __forceinline__ uint64_t order_of(double x) {
+  if (x != x) return 0;
+  const int64_t u = __builtin_bit_cast(int64_t, x + 0.0);
+  return (uint64_t)(u < 0 ? ~u : u | (int64_t)1 << 63);
+}
+
 // One wavefront per token.  The order is by key, the lower index first where
 // keys are equal; the key is the score plus the expert's bias, or the logit
 // itself where there is no bias (the score grows with it).  A NaN key is
-// taken as the smallest.  P: keys of a lane, E <= 64 P.
-
+// taken as the smallest.  A choice is the largest upper half of a key, and
+// only where several lanes have it, the largest lower half, then the lowest
+// index.  P: keys of a lane, E <= 64 P.
 template <int P>
 __global__ __launch_bounds__(64) void moe_choose_kernel(const double *__restrict__ logits, const float *__restrict__ bias,
                                                         int E, int top_k, int sigmoid, int normalize,
                                                         int *__restrict__ ids, float *__restrict__ weights) {
   const int lane = threadIdx.x;
   const int64_t t = blockIdx.x;
-  __shared__ double score[MOE_MAX_EXPERTS];
-  double key[P];
-  double top = -__builtin_inf();
+  double logit[P], score[P], top = -__builtin_inf();
+  uint64_t key[P];
 #pragma unroll
-  for (int i = 0; i < P; ++i)
-    if (64 * i < E) {
-      const int e = 64 * i + lane;
-      key[i] = e < E ? logits[t * E + e] : -__builtin_inf();
-      top = fmax(top, key[i]);
-    }
-  for (int o = 32; o > 0; o >>= 1) top = fmax(top, __shfl_xor(top, o));
+  for (int i = 0; i < P; ++i) {
+    const int e = 64 * i + lane;
+    logit[i] = e < E ? logits[t * E + e] : -__builtin_inf();
+    top = fmax(top, logit[i]);
+  }
+  if (!sigmoid) {
+    const uint64_t u = order_of(top);
+    const uint32_t hi = wave_max((uint32_t)(u >> 32));
+    const uint32_t lo = wave_max((uint32_t)(u >> 32) == hi ? (uint32_t)u : 0u);
+    // back from the order: the largest logit
+    const uint64_t m = (uint64_t)hi << 32 | lo;
+    top = __builtin_bit_cast(double, m >> 63 ? m & ~(1ull << 63) : ~m);
+  }
   double sum = 0.0;
 #pragma unroll
-  for (int i = 0; i < P; ++i)
-    if (64 * i < E) {
-      const int e = 64 * i + lane;
-      if (e < E) {
-        const double s = sigmoid ? 1.0 / (1.0 + exp(-key[i])) : exp(key[i] - top);
-        score[e] = s;
-        sum += s;
-      }
-    }
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-  __syncthreads();
-  if (bias)
-  #pragma unroll
-  for (int i = 0; i < P; ++i)
-      if (64 * i + lane < E) key[i] = (sigmoid ? score[64 * i + lane] : score[64 * i + lane] / sum) + (double)bias[64 * i + lane];
+  for (int i = 0; i < P; ++i) {
+    const bool real = 64 * i + lane < E;
+    score[i] = !real ? 0.0 : sigmoid ? 1.0 / (1.0 + exp(-logit[i])) : exp(logit[i] - top);
+    sum += score[i];
+  }
+  const bool whole = !sigmoid && (bias || !normalize);      // the softmax's own denominator is needed
+  sum = whole ? wave_sum(sum) : 1.0;
 #pragma unroll
-  for (int i = 0; i < P; ++i)
-    if (64 * i < E && key[i] != key[i]) key[i] = -__builtin_inf();
+  for (int i = 0; i < P; ++i) {
+    const int e = 64 * i + lane;
+    key[i] = e < E ? order_of(bias ? score[i] / sum + (double)bias[e] : logit[i]) : 0;
+  }
   // lane j keeps the j-th choice
   int mine = 0;
+  double mine_score = 0.0;
   uint32_t taken = 0;
   for (int j = 0; j < top_k; ++j) {
-    double best = -__builtin_inf();
-    int at = MOE_MAX_EXPERTS;
-  #pragma unroll
-  for (int i = 0; i < P; ++i)
-      if (64 * i + lane < E && !(taken >> i & 1u) && (at == MOE_MAX_EXPERTS || key[i] > best)) {
+    uint64_t best = 0;
+    uint32_t at = ~0u;                                      // an expert of this lane, if any is left
+    double sc = 0.0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const uint32_t e = 64 * i + lane;
+      if ((int)e < E && !(taken >> i & 1u) && (at == ~0u || key[i] > best)) {
         best = key[i];
-        at = 64 * i + lane;
-      }
-    for (int o = 32; o > 0; o >>= 1) {
-      const double b = __shfl_xor(best, o);
-      const int a = __shfl_xor(at, o);
-      if (a != MOE_MAX_EXPERTS && (at == MOE_MAX_EXPERTS || b > best || (b == best && a < at))) {
-        best = b;
-        at = a;
+        at = e;
+        sc = score[i];
       }
     }
-    if ((at & 63) == lane) taken |= 1u << (at >> 6);
-    if (lane == j) mine = at;
+    const uint32_t hi = wave_max((uint32_t)(best >> 32));
+    uint64_t in = __ballot(at != ~0u && (uint32_t)(best >> 32) == hi);
+    if (in & (in - 1)) {
+      const uint32_t lo = wave_max(in >> lane & 1 ? (uint32_t)best : 0u);
+      in &= __ballot((uint32_t)best == lo);
+      if (in & (in - 1)) {
+        const uint32_t e = wave_min(in >> lane & 1 ? at : ~0u);
+        in = __ballot(at == e);
+      }
+    }
+    const int who = __builtin_ctzll(in);
+    const int e = __builtin_amdgcn_readlane((int)at, who);
+    const double s = lane_f64(sc, who);
+    if (lane == who) taken |= 1u << (e >> 6);
+    if (lane == j) {
+      mine = e;
+      mine_score = s;
+    }
   }
-  const double s = lane < top_k ? score[mine] : 0.0;
-  double chosen = s;
-  for (int o = 32; o > 0; o >>= 1) chosen += __shfl_xor(chosen, o);
-  const double div = normalize ? chosen : sigmoid ? 1.0 : sum;
+  const double div = normalize ? wave_sum(mine_score) : sum;
   if (lane < top_k) {
     ids[t * top_k + lane] = mine;
-    weights[t * top_k + lane] = (float)(s / div);
+    weights[t * top_k + lane] = (float)(mine_score / div);
   }
 }
 
@@ -588,6 +730,194 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DNW))) void
   }
 }
 
+// ------------------------------------------------- a handful of pairs
+// Up to kMoeFewPairs (token, choice) pairs, a step of one or two sequences, the
+// layer is two kernels and all latency: each wavefront holds all its loads in
+// flight, rows come straight into operands (there are few, so they share
+// lines), and the down product's workgroups own their columns of y, so the
+// sum over the choices needs no kernel of its own.
+template <int TILES>
+struct FewWeights {
+  uint4 code[TILES];
+  uint2 sz[TILES];
+  __device__ __forceinline__ void load(const uint8_t *const (&w)[TILES], int p, int lane) {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      const uint8_t *block = w[t] + (int64_t)p * kMoeBlockBytes;
+      code[t] = *reinterpret_cast<const uint4 *>(block + (uint32_t)lane * 16);
+      sz[t] = *reinterpret_cast<const uint2 *>(block + (kAwqBlockBytes + (uint32_t)(lane & 15) * 8));
+    }
+  }
+};
+template <int PIECES>
+struct FewRows {
+  uint4 x[PIECES][4];
+  __device__ __forceinline__ void load(const uint16_t *row, int p, int G, int lane) {
+#pragma unroll
+    for (int h = 0; h < PIECES; ++h)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[h][k] = *reinterpret_cast<const uint4 *>(row + (min(2 * p + k / 2, G - 1) * PIECES + h) * kGroup +
+                                                   16 * (lane >> 4) + 8 * (k % 2));
+  }
+};
+
+template <bool F16, bool GELU, int KS>
+__global__ __launch_bounds__(KS * 64) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_few_kernel(MoeArgs a) {
+  __shared__ v4f red[KS][2][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Rows<false> rows;
+  if (!rows.find(a, blockIdx.y, lane)) return;
+  const int n = a.I / kAwqTile, tile = blockIdx.x;
+  const MoeWeightLayout L(2 * (int64_t)a.I, a.K);
+  const uint8_t *blob = a.gate_up + rows.expert * a.gate_up_stride;
+  const uint8_t *const tiles[2] = {blob + L.block(tile, 0), blob + L.block(tile + n, 0)};
+  const uint16_t *x = a.x + (int64_t)(rows.pair(min(lane & 15, rows.count - 1)) / a.top_k) * a.K;
+  const int G = (int)L.G, P = (int)L.P, each = (P + KS - 1) / KS;
+  const int p0 = min(P, w * each), p1 = min(P, p0 + each);
+  v4f acc[2] = {};
+  constexpr int AHEAD = 4;
+  FewWeights<2> s[AHEAD];
+  FewRows<1> r[AHEAD];
+  for (int p = p0; p < p1; p += AHEAD) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) s[i].load(tiles, min(p + i, p1 - 1), lane);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) r[i].load(x, min(p + i, p1 - 1), G, lane);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (p + i >= p1) break;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (2 * (p + i) + g >= G) break;
+        const uint4 a0 = r[i].x[0][2 * g], a1 = r[i].x[0][2 * g + 1];
+        v4f xsum = v4f{};
+        if constexpr (!F16) xsum = mma(a1, ones(), mma(a0, ones(), v4f{}));
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          group_mma<F16>(a0, a1, xsum, g ? s[i].code[t].z : s[i].code[t].x, g ? s[i].code[t].w : s[i].code[t].y,
+                         g ? s[i].sz[t].y : s[i].sz[t].x, acc[t]);
+      }
+    }
+  }
+  red[w][0][lane] = acc[0];
+  red[w][1][lane] = acc[1];
+  __syncthreads();
+  // one element a thread of the first four wavefronts: row 4 (lane / 16) + w
+  if (w >= 4) return;
+  float g = 0.0f, u = 0.0f;
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    g += red[k][0][lane][w];
+    u += red[k][1][lane][w];
+  }
+  const float h = (GELU ? gelu_tanh_f32(g) : g * __builtin_amdgcn_rcpf(1.0f + __expf(-g))) * u;
+  const int row = 4 * (lane >> 4) + w;
+  const int64_t at = (int64_t)rows.pair(min(row, rows.count - 1)) * (2 * a.I) + tile / 4 * 128 + tile % 4 * kAwqTile + (lane & 15);
+  if (row < rows.count) {
+    const __bf16 hi = (__bf16)h;
+    a.h[at] = __builtin_bit_cast(uint16_t, hi);
+    a.h[at + kGroup] = __builtin_bit_cast(uint16_t, (__bf16)(__builtin_isfinite(h) ? h - (float)hi : 0.0f));
+  }
+}
+
+// y's 16 columns of one workgroup.  The (expert, step) items of all experts
+// form one line, of which each wavefront takes an equal piece.  Row t of the
+// tile is token t's; a token that did not choose the expert gets another's
+// row, and its product is not taken.  A token that names an expert twice
+// counts it with both weights.
+template <bool F16, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void moe_down_few_kernel(MoeArgs a) {
+  __shared__ v4f red[WAVES][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = a.T * a.top_k;
+  const int id = lane < n ? a.ids[lane] : -1;
+  const float wt = lane < n ? a.weights[lane] : 0.0f;
+  const MoeWeightLayout L(a.K, a.I);
+  const int G = (int)L.G, P = (int)L.P;
+  uint64_t left = __ballot(id >= 0 && id < a.E);
+  // the experts: lane i is the first of its expert's pairs if no lower one has the same id
+  bool first = false;
+  {
+    uint64_t rest = left;
+    while (rest) {
+      const int f = __builtin_ctzll(rest);
+      rest &= ~__ballot(id == __builtin_amdgcn_readlane(id, f));
+      if (lane == f) first = true;
+    }
+  }
+  uint64_t firsts = __ballot(first);
+  const int items = __builtin_popcountll(firsts) * P, each = (items + WAVES - 1) / WAVES;
+  int at = min(items, w * each);
+  const int end = min(items, at + each);
+  v4f y = v4f{};
+  for (int slot = 0; at < end; ++slot, firsts &= firsts - 1) {
+    if (at >= (slot + 1) * P) continue;
+    const int expert = __builtin_amdgcn_readlane(id, __builtin_ctzll(firsts));
+    const uint64_t same = __ballot(id == expert);
+    // the pairs of token lane % 16, and its weight
+    const int t0 = (lane & 15) * a.top_k;
+    const uint64_t mine = t0 < 64 ? same >> t0 & ((2ull << (a.top_k - 1)) - 1) : 0;
+    const int pair = mine ? t0 + __builtin_ctzll(mine) : __builtin_ctzll(same);
+    float weight = 0.0f;
+    for (uint64_t any = __ballot(mine != 0), m = mine; any; any = __ballot(m != 0)) {
+      const float x = __shfl(wt, m ? t0 + __builtin_ctzll(m) : 0);
+      if (m) weight += x;
+      m &= m - 1;
+    }
+    const uint8_t *const tile[1] = {a.down + expert * a.down_stride + L.block(blockIdx.x, 0)};
+    const uint16_t *h = a.h + (int64_t)pair * (2 * a.I);
+    const int p1 = min(P, end - slot * P);
+    v4f acc = v4f{};
+    // weights four steps ahead, rows (from the cache) two
+    constexpr int AHEAD = 4;
+    FewWeights<1> s[AHEAD];
+    FewRows<2> r[2];
+    for (int p = at - slot * P; p < p1; p += AHEAD) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) s[i].load(tile, min(p + i, p1 - 1), lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) r[i].load(h, min(p + i, p1 - 1), G, lane);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (p + i >= p1) break;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (2 * (p + i) + g >= G) break;
+          const uint4 h0 = r[i % 2].x[0][2 * g], h1 = r[i % 2].x[0][2 * g + 1];
+          const uint4 l0 = r[i % 2].x[1][2 * g], l1 = r[i % 2].x[1][2 * g + 1];
+          const v8bf b0 = codes_128(g ? s[i].code[0].z : s[i].code[0].x), b1 = codes_128(g ? s[i].code[0].w : s[i].code[0].y);
+          const v4f sum = mma(l1, ones(), mma(l0, ones(), mma(h1, ones(), mma(h0, ones(), v4f{}))));
+          const v4f prod = mma(l1, b1, mma(l0, b0, mma(h1, b1, mma(h0, b0, v4f{}))));
+          const uint32_t sz = g ? s[i].sz[0].y : s[i].sz[0].x;
+          const float z = -(128.0f + (float)zero_of(sz)), sc = scale_of(sz);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(__builtin_fmaf(z, sum[e], prod[e]), sc, acc[e]);
+        }
+        if (i + 2 < AHEAD) r[i % 2].load(h, min(p + i + 2, p1 - 1), G, lane);
+      }
+    }
+    const uint64_t chose = __ballot(mine != 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = 4 * (lane >> 4) + e;
+      const float x = __shfl(weight, t);
+      if (chose >> t & 1) y[e] = __builtin_fmaf(x, acc[e], y[e]);
+    }
+    at = slot * P + p1;
+  }
+  red[w][lane] = y;
+  __syncthreads();
+  if (w >= 4) return;
+  const int t = 4 * (lane >> 4) + w;
+  float v = 0.0f;
+#pragma unroll
+  for (int k = 0; k < WAVES; ++k) v += red[k][lane][w];
+  if (t < a.T)
+    a.y[(int64_t)t * a.K + blockIdx.x * kAwqTile + (lane & 15)] =
+        F16 ? __builtin_bit_cast(uint16_t, (_Float16)v) : __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
 // y[t] = sum over the token's choices of weight times part, in order; choices
 // without an expert here are left out.  One thread per 4 columns.
 template <bool F16>
@@ -645,11 +975,19 @@ svdq_status_t svdq_moe_route(const void *x, const void *w_router, const float *b
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   double *logits = static_cast<double *>(workspace);
   const uint16_t *xp = static_cast<const uint16_t *>(x), *wp = static_cast<const uint16_t *>(w_router);
-  const dim3 grid((unsigned)((E + 3) / 4), (unsigned)((T + kTokens - 1) / kTokens));
-  if (dtype == SVDQ_FP16)
-    hipLaunchKernelGGL((moe_logits_kernel<true>), grid, dim3(256), 0, stream, xp, wp, T, E, K, logits);
-  else
-    hipLaunchKernelGGL((moe_logits_kernel<false>), grid, dim3(256), 0, stream, xp, wp, T, E, K, logits);
+  if ((int64_t)T * E > kTileLogits) {
+    const dim3 grid((unsigned)((E + 15) / 16), (unsigned)((T + 15) / 16));
+    if (dtype == SVDQ_FP16)
+      hipLaunchKernelGGL((moe_logits_tile_kernel<true>), grid, dim3(512), 0, stream, xp, wp, T, E, K, logits);
+    else
+      hipLaunchKernelGGL((moe_logits_tile_kernel<false>), grid, dim3(512), 0, stream, xp, wp, T, E, K, logits);
+  } else {
+    const dim3 grid((unsigned)((E + 3) / 4), (unsigned)((T + kTokens - 1) / kTokens));
+    if (dtype == SVDQ_FP16)
+      hipLaunchKernelGGL((moe_logits_kernel<true>), grid, dim3(256), 0, stream, xp, wp, T, E, K, logits);
+    else
+      hipLaunchKernelGGL((moe_logits_kernel<false>), grid, dim3(256), 0, stream, xp, wp, T, E, K, logits);
+  }
   const int sigmoid = score == SVDQ_MOE_SIGMOID ? 1 : 0;
 #define MOE_CHOOSE(P) hipLaunchKernelGGL((moe_choose_kernel<P>), dim3((unsigned)T), dim3(64), 0, stream, logits, bias, E, \
                                          top_k, sigmoid, normalize, ids, weights)
@@ -704,6 +1042,20 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   a.y = static_cast<uint16_t *>(y);
   a.plan = reinterpret_cast<MoePlan *>(ws + L.plan);
   const int pairs = T * top_k, slots = pairs < w->E ? pairs : w->E;
+  if (pairs <= kMoeFewPairs && slots * ((w->I + 127) / 128) <= FEWI) {
+    const dim3 few_grid((unsigned)(w->I / kAwqTile), (unsigned)slots);
+#define MOE_FEW(F, A) hipLaunchKernelGGL((moe_gate_up_few_kernel<F, A, GFKS>), few_grid, dim3(GFKS * 64), 0, stream_, a)
+    const hipStream_t stream_ = static_cast<hipStream_t>(hip_stream);
+    if (dtype == SVDQ_FP16) {
+      if (act == SVDQ_MOE_GELU_TANH) MOE_FEW(true, true); else MOE_FEW(true, false);
+      hipLaunchKernelGGL((moe_down_few_kernel<true, DFW>), dim3(w->K / kAwqTile), dim3(DFW * 64), 0, stream_, a);
+    } else {
+      if (act == SVDQ_MOE_GELU_TANH) MOE_FEW(false, true); else MOE_FEW(false, false);
+      hipLaunchKernelGGL((moe_down_few_kernel<false, DFW>), dim3(w->K / kAwqTile), dim3(DFW * 64), 0, stream_, a);
+    }
+#undef MOE_FEW
+    return launch_status("expert layer launch");
+  }
   const bool plan = pairs > 64 || pairs > 12 * slots;
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   if (plan) hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
