@@ -291,7 +291,7 @@ struct AttendArgs {
   const int *table;
   int width;                    // entries of a page-table row
   const int *lens;
-  int B, Q, group, rows, row_blocks, block_rows;   // block_rows = min(rows, 16 NT)
+  int B, Q, group, rows, row_blocks, block_rows;   // block_rows = min(rows, ROWS)
   float scale;                  // |softmax scale| log2(e), positive
   uint32_t flip;                // sign bits of the queries to turn, for a negative scale
   uint16_t *out;
@@ -424,6 +424,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v2bf{(__bf16)a, (__bf16)b});
 }
 
+// the lane 8 columns on, of the same quarter
+__device__ __forceinline__ float other_half(float x) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), 0x128, 0xF, 0xF, true));
+}
 // the largest x of the four lanes of a column (l % 16)
 __device__ __forceinline__ float column_max(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -437,13 +441,21 @@ __device__ __forceinline__ float column_max(float x) {
 // Registers: at least two wavefronts a SIMD keeps the matrix accumulators in
 // ordinary registers (with all 512 allowed, the compiler moves them to and from
 // the accumulation registers around every tile).
-template <int D, int NT, bool F16>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D, NT)))) void kv4_attend_kernel(AttendArgs a) {
+// ROWS: rows of a block at most, 8, 16 or 32.  Eight rows leave half of a
+// tile's columns free: columns 8..15 then take the second pieces of the same
+// rows (of fp16 queries, and of the weights), which halves the products of
+// those; a lane's two column halves are added where they meet (rotating a row
+// of 16 lanes by 8).
+template <int D, int ROWS, bool F16>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D, ROWS)))) void kv4_attend_kernel(AttendArgs a) {
   constexpr int NB = D / 32;                       // blocks of 32 channels
+  constexpr int NT = ROWS == 32 ? 2 : 1;           // 16-column tiles
+  constexpr bool HALF = ROWS == 8;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c4 = lane >> 4;
-  __shared__ float sm[4][NT * 16], sl[4][NT * 16];
-  __shared__ v4f so[2][NT * 2 * NB][64];
+  const bool second = HALF && col >= 8;            // a lane of the second pieces
+  __shared__ float sm[4][ROWS], sl[4][ROWS];
+  __shared__ __attribute__((aligned(16))) float so[4][ROWS][D + 4];    // + 4: columns on different banks
 
   const int HR = a.L.H * a.row_blocks;
   Line line;
@@ -466,6 +478,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
     }
   }
 
+  // the lane's rows of the first block of rows
+  int row_i[NT], row_j[NT];
+  bool row_in[NT];
+#pragma unroll
+  for (int x = 0; x < NT; ++x) {
+    const int r = HALF ? col & 7 : 16 * x + col;
+    row_in[x] = r < a.rows;
+    row_i[x] = row_in[x] ? r / a.group : 0;
+    row_j[x] = row_in[x] ? r % a.group : 0;
+  }
+
   int u = u0;
   while (u < u1) {
     if (b - line.base >= 64) line.look(a, line.base + 64, 0, lane);
@@ -477,16 +500,21 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
     const int next = start + (hr + 1) * span;
     const int next_b = hr + 1 == HR ? b + 1 : b, next_start = hr + 1 == HR ? next : start;
     if (ch1 <= 0) break;                                  // the line ends before the first chunk
-    const int h = hr / a.row_blocks, r0 = hr % a.row_blocks * (16 * NT);
+    const int h = hr / a.row_blocks, r0 = hr % a.row_blocks * ROWS;
     // queries: row r = i * group + j is new token i, head h * group + j
     // (asked for before the pages, which are waited for)
     uint4 qv[NT][NB];
     int limit[NT];                                 // tokens that the lane's row sees
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-      const int r = r0 + 16 * x + col;
-      const bool real = r < a.rows;
-      const int i = real ? r / a.group : 0, j = real ? r % a.group : 0;
+      int i = row_i[x], j = row_j[x];
+      bool real = row_in[x];
+      if (a.row_blocks > 1) {
+        const int r = r0 + (HALF ? col & 7 : 16 * x + col);
+        real = r < a.rows;
+        i = real ? r / a.group : 0;
+        j = real ? r % a.group : 0;
+      }
       limit[x] = min(len, len - a.Q + i + 1);
       const uint16_t *src = a.q + b * a.q_b + i * a.q_i + (int64_t)(h * a.group + j) * a.q_h + 8 * c4;
 #pragma unroll
@@ -495,24 +523,29 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
     }
     Pages pages{a.table + (int64_t)b * a.width, a.width, a.L.pages, 0, 0};
     pages.load(ch0 * kKv4Chunk >> a.L.page_shift, lane);
-    v8bf qh[NT][NB], ql[NT][F16 ? NB : 1];
+    v8bf qh[NT][NB], ql[NT][F16 && !HALF ? NB : 1];
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int s = 0; s < NB; ++s) {
         const uint4 v = make_uint4(qv[x][s].x ^ a.flip, qv[x][s].y ^ a.flip, qv[x][s].z ^ a.flip, qv[x][s].w ^ a.flip);
         if constexpr (F16) {
+          // the upper 16 bits of the value as float32, and the rest (a value that is
+          // not finite leaves a row that is not, either way)
           const uint32_t in[4] = {v.x, v.y, v.z, v.w};
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float f0 = wide<true>(in[e] & 0xFFFFu), f1 = wide<true>(in[e] >> 16);
-            hi[e] = pack_bf16(f0, f1);
-            const float g0 = f0 - bf16_lo(hi[e]), g1 = f1 - bf16_hi(hi[e]);
-            lo[e] = pack_bf16(__builtin_isfinite(f0) ? g0 : 0.0f, __builtin_isfinite(f1) ? g1 : 0.0f);
+            const uint32_t f0 = __float_as_uint(wide<true>(in[e] & 0xFFFFu)), f1 = __float_as_uint(wide<true>(in[e] >> 16));
+            hi[e] = __builtin_amdgcn_perm(f1, f0, 0x07060302u);
+            lo[e] = pack_bf16(__uint_as_float(f0) - bf16_hi(f0), __uint_as_float(f1) - bf16_hi(f1));
           }
-          qh[x][s] = as_v8bf(make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          ql[x][s] = as_v8bf(make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          if constexpr (HALF) {
+            qh[x][s] = as_v8bf(second ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          } else {
+            qh[x][s] = as_v8bf(make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            ql[x][s] = as_v8bf(make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          }
         } else {
           qh[x][s] = as_v8bf(v);
         }
@@ -562,11 +595,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
 #pragma unroll
           for (int x = 0; x < NT; ++x) {
             s[x][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, qh[x][k], s[x][g], 0, 0, 0);
-            if constexpr (F16) s[x][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, ql[x][k], s[x][g], 0, 0, 0);
+            if constexpr (F16 && !HALF) s[x][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, ql[x][k], s[x][g], 0, 0, 0);
           }
         }
       }
       load_keys<D>(next, nlane, keys);
+      if constexpr (F16 && HALF) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[0][g][i] += other_half(s[0][g][i]);
+      }
       if (t + 32 > whole || !place.ok[0] || !place.ok[1]) {
         // rows' own limits, and units without a page
 #pragma unroll
@@ -625,8 +664,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
             hi[2 * g + i] = pk;
             lo[2 * g + i] = pack_bf16(p0 - bf16_lo(pk), p1 - bf16_hi(pk));
           }
-        ph[x] = as_v8bf(make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        pl[x] = as_v8bf(make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        if constexpr (HALF) {
+          ph[x] = as_v8bf(second ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        } else {
+          ph[x] = as_v8bf(make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          pl[x] = as_v8bf(make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
       }
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
@@ -649,96 +692,82 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
         for (int x = 0; x < NT; ++x) {
           o[x][2 * k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, ph[x], o[x][2 * k], 0, 0, 0);
           o[x][2 * k + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, ph[x], o[x][2 * k + 1], 0, 0, 0);
-          o[x][2 * k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pl[x], o[x][2 * k], 0, 0, 0);
-          o[x][2 * k + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pl[x], o[x][2 * k + 1], 0, 0, 0);
+          if constexpr (!HALF) {
+            o[x][2 * k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pl[x], o[x][2 * k], 0, 0, 0);
+            o[x][2 * k + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pl[x], o[x][2 * k + 1], 0, 0, 0);
+          }
         }
       }
       load_values<D>(next, nlane, vals);
       place = next;
     }
 
-    // the four wavefronts' states meet: everything relative to the largest
-    // maximum, then wavefronts 2 and 3 into 0 and 1, and 1 into 0
+    // The four wavefronts' states meet: all of them into LDS, then every
+    // thread takes some channels of one row, relative to the row's largest
+    // maximum, and writes them.
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
       l[x] += __shfl_xor(l[x], 16);
       l[x] += __shfl_xor(l[x], 32);
-      m[x] = m[x] * a.scale;
-      if (c4 == 0) {
-        sm[w][16 * x + col] = m[x];
+      const bool mine = !second;
+      if (mine && c4 == 0) {
+        sm[w][16 * x + col] = m[x] * a.scale;
         sl[w][16 * x + col] = l[x];
+      }
+#pragma unroll
+      for (int k = 0; k < 2 * NB; ++k) {
+        if constexpr (HALF) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[x][k][e] += other_half(o[x][k][e]);
+        }
+        if (mine) *reinterpret_cast<v4f *>(&so[w][16 * x + col][16 * k + 4 * c4]) = o[x][k];
       }
     }
     __syncthreads();
-    float mall[NT], lall[NT];
+    {
+      constexpr int THREADS = 256 / ROWS, EACH = D / THREADS, U = EACH < 4 ? EACH : 4;
+      const int c = threadIdx.x / THREADS, first = threadIdx.x % THREADS * U;
+      const int r = r0 + c;
+      float f[4], top = fmaxf(fmaxf(sm[0][c], sm[1][c]), fmaxf(sm[2][c], sm[3][c])), sum = 0.0f;
+      const float ref = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-      const int i = 16 * x + col;
-      mall[x] = fmaxf(fmaxf(sm[0][i], sm[1][i]), fmaxf(sm[2][i], sm[3][i]));
-      const float ref = mall[x] == -__builtin_inff() ? 0.0f : mall[x];
-      lall[x] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) lall[x] += sl[k][i] * __builtin_amdgcn_exp2f(sm[k][i] - ref);
-      const float f = __builtin_amdgcn_exp2f(m[x] - ref);
-#pragma unroll
-      for (int k = 0; k < 2 * NB; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[x][k][e] *= f;
-    }
-    if (w >= 2) {
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int k = 0; k < 2 * NB; ++k) so[w - 2][x * 2 * NB + k][lane] = o[x][k];
-    }
-    __syncthreads();
-    if (w < 2) {
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int k = 0; k < 2 * NB; ++k) {
-          const v4f y = so[w][x * 2 * NB + k][lane];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[x][k][e] += y[e];
-          if (w == 1) so[1][x * 2 * NB + k][lane] = o[x][k];
-        }
-    }
-    __syncthreads();
-    if (w == 0) {
+      for (int k = 0; k < 4; ++k) {
+        f[k] = __builtin_amdgcn_exp2f(sm[k][c] - ref);
+        sum = __builtin_fmaf(sl[k][c], f[k], sum);
+      }
       const bool done = ch0 == 0 && ch1 == n;
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (u > u0 ? 1 : 0);
+      const float inv = !done ? 1.0f : sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      const int i = r / a.group, j = r % a.group;
+      uint16_t *out = a.out + (((int64_t)b * a.Q + i) * (a.L.H * a.group) + h * a.group + j) * D;
+      const int64_t slot = (2 * (int64_t)blockIdx.x + (u > u0 ? 1 : 0)) * a.block_rows + c;
+      if (r < a.rows) {
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        const int r = r0 + 16 * x + col;
-        const int i = r / a.group, j = r % a.group;
-        const float inv = lall[x] > 0.0f || lall[x] != lall[x] ? 1.0f / lall[x] : 0.0f;
+        for (int d0 = 0; d0 < D; d0 += THREADS * U) {
+          const int d = d0 + first;
+          float y[U];
 #pragma unroll
-        for (int k = 0; k < 2 * NB; ++k) {
-          const v4f y = so[1][x * 2 * NB + k][lane];
+          for (int e = 0; e < U; ++e) {
+            y[e] = so[0][c][d + e] * f[0];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[x][k][e] += y[e];
-          const int d = 16 * k + 4 * c4;
-          if (r < a.rows) {
+            for (int k = 1; k < 4; ++k) y[e] = __builtin_fmaf(so[k][c][d + e], f[k], y[e]);
+            y[e] *= inv;
+          }
+#pragma unroll
+          for (int e = 0; e < U; e += 2) {
             if (done) {
-              uint2 out;
-              if constexpr (F16) {
-                out.x = __builtin_bit_cast(uint32_t, v2h{(_Float16)(o[x][k][0] * inv), (_Float16)(o[x][k][1] * inv)});
-                out.y = __builtin_bit_cast(uint32_t, v2h{(_Float16)(o[x][k][2] * inv), (_Float16)(o[x][k][3] * inv)});
-              } else {
-                out.x = pack_bf16(o[x][k][0] * inv, o[x][k][1] * inv);
-                out.y = pack_bf16(o[x][k][2] * inv, o[x][k][3] * inv);
-              }
-              *reinterpret_cast<uint2 *>(
-                  a.out + (((int64_t)b * a.Q + i) * (a.L.H * a.group) + h * a.group + j) * D + d) = out;
+              if constexpr (F16)
+                *reinterpret_cast<v2h *>(out + d + e) = v2h{(_Float16)y[e], (_Float16)y[e + 1]};
+              else
+                *reinterpret_cast<uint32_t *>(out + d + e) = pack_bf16(y[e], y[e + 1]);
             } else {
-              *reinterpret_cast<v4f *>(a.part + (slot * a.block_rows + 16 * x + col) * D + d) = o[x][k];
+              *reinterpret_cast<float2 *>(a.part + slot * D + d + e) = make_float2(y[e], y[e + 1]);
             }
           }
         }
-        if (!done && r < a.rows && c4 == 0) {
-          float *ml = a.part + 2 * (int64_t)a.W * a.block_rows * D + (slot * a.block_rows + 16 * x + col) * 2;
-          ml[0] = mall[x];
-          ml[1] = lall[x];
+        if (!done && first == 0) {
+          float *ml = a.part + 2 * (int64_t)a.W * a.block_rows * D + slot * 2;
+          ml[0] = top;
+          ml[1] = sum;
         }
       }
     }
@@ -939,9 +968,9 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
   a.Q = Q;
   a.group = Hq / L.H;
   a.rows = a.group * Q;
-  const int nt = a.rows > 16 ? 2 : 1;
-  a.row_blocks = (a.rows + 16 * nt - 1) / (16 * nt);
-  a.block_rows = a.rows < 16 * nt ? a.rows : 16 * nt;
+  const int block = a.rows > 16 ? 32 : a.rows > 8 ? 16 : 8;
+  a.row_blocks = (a.rows + block - 1) / block;
+  a.block_rows = a.rows < block ? a.rows : block;
   // Maxima are taken of the bare products, so the scale's sign goes to the
   // queries, and a scale of zero becomes one that still hides masked scores.
   a.scale = fmaxf((float)(fabs((double)scale) * 1.4426950408889634), 1e-37f);
@@ -954,7 +983,7 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
   if ((chunks + kKv4Start) * B * L.H * a.row_blocks + kKv4Groups > 0x7FFFFFFF)
     return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_attention: B=%d Q=%d Hq=%d with a page table of %d columns is too much work",
                 B, Q, Hq, table_width);
-  const int resident = 256 * kv4_waves(L.D, nt);
+  const int resident = 256 * kv4_waves(L.D, block);
   a.W = (int)(most < resident ? most : resident);
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   // pieces of a row, on average: from four on, a workgroup joins them
@@ -967,7 +996,12 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
     if (wide_join) hipLaunchKernelGGL((kv4_join_kernel<DD, FF, true>), join_grid, dim3(256), 0, stream, a); \
     else hipLaunchKernelGGL((kv4_join_kernel<DD, FF, false>), join_grid, dim3(256), 0, stream, a);          \
   } while (0)
-#define KV4_ROWS(DD, FF) do { if (nt == 1) KV4_GO(DD, 1, FF); else KV4_GO(DD, 2, FF); } while (0)
+#define KV4_ROWS(DD, FF)                       \
+  do {                                         \
+    if (block == 8) KV4_GO(DD, 8, FF);         \
+    else if (block == 16) KV4_GO(DD, 16, FF);  \
+    else KV4_GO(DD, 32, FF);                   \
+  } while (0)
 #define KV4_TYPE(DD) do { if (dtype == SVDQ_FP16) KV4_ROWS(DD, true); else KV4_ROWS(DD, false); } while (0)
   if (L.D == 64) KV4_TYPE(64);
   else if (L.D == 128) KV4_TYPE(128);
