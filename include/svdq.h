@@ -506,6 +506,14 @@ svdq_status_t awq_moe_pack_device_weights(const uint8_t *q, const uint16_t *scal
                                           const uint16_t *zeros_fp16, int E, int N, int K,
                                           void *host_blob, size_t bytes);
 
+/* The same from device memory to device memory (q and blob 16-byte aligned),
+ * asynchronous on `hip_stream`.  Zero points and scales are the caller's to
+ * check: with others than integers 0..15 and finite values the experts'
+ * products are wrong (and nothing else is). */
+svdq_status_t awq_moe_pack_on_device(const uint8_t *q, const uint16_t *scales_fp16,
+                                     const uint16_t *zeros_fp16, int E, int N, int K,
+                                     void *blob, size_t bytes, void *hip_stream);
+
 /* Experts resident in device memory: blobs of awq_moe_pack_device_weights.
  * gate_up: [2 I, K] each (the I gate rows, then the I up rows); down: [K, I]
  * each. */
@@ -520,6 +528,8 @@ typedef struct {
  * outside [0, E) adds nothing (experts held elsewhere, padding rows); one
  * that a token names twice counts twice.  The gated product is kept to 16
  * significant bits in float32's range, sums are float32, and y is rounded once.
+ * A row of x that is not finite gives a row of y that is not, and touches no
+ * other; which tokens share a call changes the order of float32 sums only.
  * E <= 1024, K and I multiples of 64 with 2 I K <= 2^31, T top_k <= 4096.
  * Each expert that some token names is read once per 16 of its rows.  The
  * workspace needs no clearing and keeps nothing from one call for the next. */

@@ -185,6 +185,9 @@ CASES = [
     ([40] * 150, 1, 2, 1, 64, 16, "bf16"),              # more sequences than lanes
     ([1, 2000] * 70, 1, 4, 4, 64, 64, "fp16"),
     ([20000], 1, 8, 1, 128, 256, "bf16"),               # one sequence over many workgroups
+    ([333, 9], 1, 9, 1, 64, 16, "bf16"), ([333, 9], 1, 16, 1, 128, 16, "fp16"), ([50], 4, 4, 1, 128, 16, "bf16"),
+    ([200, 31], 1, 12, 1, 64, 32, "fp16"), ([130], 3, 4, 1, 256, 16, "fp16"), ([90, 300], 8, 3, 1, 256, 64, "fp16"),
+    ([200], 6, 16, 4, 64, 16, "bf16"), ([100], 1, 8, 8, 256, 16, "fp16"), ([64, 70], 33, 2, 1, 64, 16, "bf16"),
 ]
 
 
@@ -283,6 +286,64 @@ def test_attention_slots_past_32_bit_offsets(S):
     got = S.kv4_attention(cache, q, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
     bb = type("B", (), dict(k=[O.values(f64(k))], v=[O.values(f64(v))], lens=[n]))
     check(got, q, bb, D ** -0.5)
+
+
+def test_attention_over_shared_pages(S):
+    """Sequences of one prompt: every row of the table names the same pages, far more of them than a register holds."""
+    r = np.random.default_rng(12)
+    n, H, D, page, B = 4000, 8, 64, 16, 64
+    cache = S.Kv4Cache(n // page, page, H, D)
+    k, v = rows(r, (n, H, D), "bf16"), rows(r, (n, H, D), "bf16")
+    order = r.permutation(n // page).astype(np.int32)
+    t = np.arange(n)
+    S.kv4_append(cache, k, v, torch.from_numpy((order[t // page] * page + t % page).astype(np.int32)).cuda())
+    lens = [int(x) for x in r.integers(3000, n + 1, B)]
+    table = torch.from_numpy(np.tile(order, (B, 1))).cuda()
+    q = torch.from_numpy(r.standard_normal((B, 1, H, D))).to(torch.bfloat16).cuda()
+    announce("kv4 attention over shared pages")
+    got = S.kv4_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    bb = type("B", (), dict(k=[O.values(f64(k))] * B, v=[O.values(f64(v))] * B, lens=lens))
+    check(got, q, bb, D ** -0.5)
+
+
+def test_attention_of_queries_that_are_not_finite(S):
+    for dtype in DT:
+        b = Batch(S, 55, [70, 33], 1, 128, 16, dtype)
+        q = b.queries(1, 5)
+        want = f64(S.kv4_attention(b.cache, q, b.table, b.seq_lens))
+        q[0, 0, 1, 9], q[1, 0, 4, 2] = float("inf"), float("nan")
+        announce(f"kv4 attention of queries that are not finite, {dtype}")
+        got = f64(S.kv4_attention(b.cache, q, b.table, b.seq_lens))
+        assert np.isnan(got[0, 0, 1]).all() and np.isnan(got[1, 0, 4]).all()
+        got[0, 0, 1], got[1, 0, 4] = want[0, 0, 1], want[1, 0, 4]
+        assert np.array_equal(got, want)
+
+
+def test_two_graphs_share_a_workspace(S):
+    bs = [Batch(S, 56 + i, [900, 5], 2, 128, 32, "bf16") for i in range(2)]
+    qs = [b.queries(1, 8) for b in bs]
+    ws = S.kv4_attention_workspace(bs[0].cache, qs[0])
+    outs, graphs = [torch.empty_like(q) for q in qs], []
+    announce("kv4 attention: two graphs on one workspace")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for b, q, o in zip(bs, qs, outs):
+            S.kv4_attention(b.cache, q, b.table, b.seq_lens, out=o, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    for b, q, o in zip(bs, qs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            S.kv4_attention(b.cache, q, b.table, b.seq_lens, out=o, workspace=ws)
+        graphs.append(g)
+    for i in range(4):
+        for b, q in zip(bs, qs):
+            q.copy_(b.queries(1, 8))
+        for g in graphs:
+            g.replay()
+        want = [S.kv4_attention(b.cache, q, b.table, b.seq_lens) for b, q in zip(bs, qs)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want)), f"replay {i}"
 
 
 def test_append_and_attention_in_a_graph(S):

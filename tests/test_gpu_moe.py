@@ -121,6 +121,67 @@ def test_expert_layer(S, case, act, dtype):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("E,N,K", [(1, 64, 64), (5, 192, 320), (33, 128, 1024)])
+def test_packing_on_the_device(S, E, N, K):
+    """The bytes of the host's packing, from any strides."""
+    announce(f"expert packing E={E} N={N} K={K}")
+    r = np.random.default_rng(E)
+    q = r.integers(0, 256, (E, N, K // 2), dtype=np.uint8)
+    s = r.standard_normal((E, N, K // 64)).astype(np.float16)
+    z = r.integers(0, 16, (E, N, K // 64)).astype(np.float16)
+    want = S._moe_blob((q, s, z), N, K, "cpu")
+    dev = [torch.from_numpy(t).cuda() for t in (q, s, z)]
+    assert torch.equal(S._moe_blob(dev, N, K, "cuda").cpu(), want)
+    turned = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in dev]
+    assert torch.equal(S._moe_blob(turned, N, K, "cuda").cpu(), want)
+    for i, bad in ((2, 16.0), (2, 2.5), (2, -1.0), (2, float("nan")), (1, float("inf"))):
+        broken = [t.clone() for t in dev]
+        broken[i][0, 5, 0] = bad
+        with pytest.raises(ValueError):
+            S._moe_blob(broken, N, K, "cuda")
+
+
+# every way in which a call is split: pairs an expert, pairs in all, tiles of columns, steps of weights
+SPLITS = [
+    # T, E, K, I, k
+    (16, 20, 64, 128, 1), (8, 16, 64, 1152, 2),       # 16 pairs: few steps, and too many for the small form
+    (10, 8, 320, 192, 2), (20, 16, 64, 704, 2),       # up to 5 pairs an expert, at most 64: few tiles, many tiles
+    (40, 64, 192, 64, 3), (40, 64, 64, 256, 2),       # the same above 64 pairs
+    (64, 16, 128, 704, 2), (32, 4, 448, 64, 1),       # 8 pairs an expert: above 64 pairs, and not
+    (128, 16, 64, 704, 2), (100, 4, 192, 320, 1),     # 16 and 25 pairs an expert
+    (32, 64, 2048, 64, 1), (48, 32, 2048, 64, 4), (128, 32, 2048, 64, 4),   # down products of many tiles
+    (128, 4, 64, 64, 4), (300, 2, 64, 64, 2), (1, 32, 128, 64, 32),   # as many choices as experts
+]
+
+
+@pytest.mark.parametrize("case", range(len(SPLITS)))
+def test_expert_layer_splits(S, case):
+    T, E, K, I, k = SPLITS[case]
+    dtype, act = ("bf16", "fp16")[case % 2], ("silu", "gelu")[case // 2 % 2]
+    announce(f"experts split {case}: T={T} E={E} K={K} I={I} k={k} {act} {dtype}")
+    r = np.random.default_rng(100 + case)
+    parts = experts(r, E, K, I)
+    layer = device_layer(S, parts)
+    x = torch.from_numpy(r.standard_normal((T, K))).to(DT[dtype]).cuda()
+    ids = torch.from_numpy(np.stack([r.permutation(E)[:k] for _ in range(T)]).astype(np.int32)).cuda()
+    ids[::7, -1] = -1
+    wt = torch.from_numpy(r.random((T, k)) + 0.05).float().cuda()
+    check(S.awq_moe_forward(layer, x, ids, wt, activation=act), x, parts, ids, wt, act)
+
+
+def test_expert_layer_all_tokens_to_one_expert(S):
+    r = np.random.default_rng(29)
+    E, K, I, T = 6, 128, 192, 90
+    parts = experts(r, E, K, I)
+    layer = device_layer(S, parts)
+    x = torch.from_numpy(r.standard_normal((T, K))).half().cuda()
+    ids = torch.full((T, 1), 4, dtype=torch.int32, device="cuda")
+    ids[50] = 1
+    wt = torch.ones(T, 1, device="cuda")
+    announce("experts: 89 tokens to one expert")
+    check(S.awq_moe_forward(layer, x, ids, wt), x, parts, ids, wt, "silu")
+
+
 def test_expert_layer_ids_outside_and_twice(S):
     r = np.random.default_rng(30)
     E, K, I, T, k = 4, 128, 64, 9, 3
@@ -143,7 +204,7 @@ def test_expert_layer_ids_outside_and_twice(S):
 
 
 def test_expert_layer_rows_do_not_touch_each_other(S):
-    """A token of NaN or infinities spoils its own row only, and a token's row is the same in any company."""
+    """A token of NaN or infinities spoils its own row only, and a token alone gives its row up to the order of sums."""
     r = np.random.default_rng(31)
     E, K, I, T, k = 3, 192, 128, 21, 2
     parts = experts(r, E, K, I)
@@ -158,9 +219,10 @@ def test_expert_layer_rows_do_not_touch_each_other(S):
         y[4, 7], y[11] = float("nan"), float("inf")
         got = S.awq_moe_forward(layer, y, ids, wt)
         rest = [t for t in range(T) if t not in (4, 11)]
-        assert torch.isnan(got[4]).all() and torch.equal(got[rest], want[rest])
+        assert not torch.isfinite(got[[4, 11]]).any() and torch.equal(got[rest], want[rest])
         for t in (0, 20):
-            assert torch.equal(S.awq_moe_forward(layer, x[t:t + 1], ids[t:t + 1].contiguous(), wt[t:t + 1].contiguous())[0], want[t])
+            one = slice(t, t + 1)
+            check(S.awq_moe_forward(layer, x[one], ids[one], wt[one]), x[one], parts, ids[one], wt[one], "silu")
 
 
 def test_expert_layer_large_gated_products(S):

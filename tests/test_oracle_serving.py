@@ -185,6 +185,11 @@ def test_wrappers_check_their_operands():
         S.kv4_attention(cache, q, table, lens, out=torch.zeros(2, 1, 4, 64))
     with pytest.raises(S.SvdqError):
         S.kv4_attention(cache, torch.zeros(2, 1, 3, 64, dtype=bf), table, lens)      # 3 heads over 2
+    # operands that fit, in CPU memory
+    for call in (lambda: S.kv4_append(cache, k, k, slots), lambda: S.kv4_read(cache, slots),
+                 lambda: S.kv4_attention(cache, q, table, lens)):
+        with pytest.raises(ValueError, match="not on cpu"):
+            call()
     with pytest.raises(S.SvdqError):
         S.Kv4Cache(4, 20, 2, 64, device="cpu")
     x, w = torch.zeros(3, 64, dtype=bf), torch.zeros(8, 64, dtype=bf)
@@ -213,6 +218,9 @@ def test_wrappers_check_their_operands():
             S.awq_moe_forward(layer, *bad)
     with pytest.raises(ValueError):
         S.awq_moe_forward(layer, x, ids, wt, activation="relu")
+    for call in (lambda: S.awq_moe_forward(layer, x, ids, wt), lambda: S.moe_route(x, torch.zeros(8, 128, dtype=bf), 2)):
+        with pytest.raises(ValueError, match="not on cpu"):
+            call()
 
 
 @pytest.mark.parametrize("E,N,K", [(1, 64, 64), (3, 128, 192), (2, 192, 256)])
@@ -223,7 +231,7 @@ def test_expert_blob_layout(E, N, K):
     codes = r.integers(0, 16, (E, N, K), dtype=np.uint8)
     s = r.standard_normal((E, N, G)).astype(np.float16)
     z = r.integers(0, 16, (E, N, G)).astype(np.float16)
-    blob = S._moe_blob((awq.pack(codes), s, z), N, K).reshape(E, N // 16, P, 1152)
+    blob = S._moe_blob((awq.pack(codes), s, z), N, K, "cpu").numpy().reshape(E, N // 16, P, 1152)
     for e in range(E):
         for n in r.permutation(N)[:40]:
             for g in range(G):
@@ -254,3 +262,9 @@ def test_expert_blob_refusals():
     for bad in (0.5, 16.0, -1.0, np.nan):
         assert pack(z=np.full_like(z, bad)) == INV
     assert pack(s=np.full_like(s, np.inf)) == 6
+
+    def on_device(q=FAKE, s=FAKE, z=FAKE, E=1, K=64, blob=FAKE, n=blob.size):
+        return lib.awq_moe_pack_on_device(q, s, z, E, 64, K, blob, n, None)
+    assert on_device(q=0) == INV and on_device(s=0) == INV and on_device(blob=0) == INV and on_device(q=FAKE + 8) == INV
+    assert on_device(z=FAKE + 1) == INV and on_device(blob=FAKE + 4) == INV and on_device(K=96) == SHAPE
+    assert on_device(E=0) == SHAPE and on_device(n=blob.size - 1) == WS

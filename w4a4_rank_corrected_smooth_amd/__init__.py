@@ -55,7 +55,7 @@ EXPORTS = [
     "svdq_merge_lora", "svdq_mx_merge_lora", "svdq_measure_stream", "svdq_measure_mfma",
     "svdq_kv4_cache_bytes", "svdq_kv4_append", "svdq_kv4_read", "svdq_kv4_attention_workspace_bytes",
     "svdq_kv4_attention", "svdq_moe_route_workspace_bytes", "svdq_moe_route",
-    "awq_moe_device_weights_bytes", "awq_moe_pack_device_weights", "awq_moe_workspace_bytes", "awq_moe_forward",
+    "awq_moe_device_weights_bytes", "awq_moe_pack_device_weights", "awq_moe_pack_on_device", "awq_moe_workspace_bytes", "awq_moe_forward",
 ]
 
 
@@ -152,6 +152,7 @@ _sig("svdq_moe_route_workspace_bytes", _sz, [_i, _i])
 _sig("svdq_moe_route", _i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp])
 _sig("awq_moe_device_weights_bytes", _sz, [_i, _i, _i])
 _sig("awq_moe_pack_device_weights", _i, [_vp, _vp, _vp, _i, _i, _i, _vp, _sz])
+_sig("awq_moe_pack_on_device", _i, [_vp, _vp, _vp, _i, _i, _i, _vp, _sz, _vp])
 _sig("awq_moe_workspace_bytes", _sz, [_i, _i, _i, _i])
 _sig("awq_moe_forward", _i, [ctypes.POINTER(MoeWeights), _vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp])
 
@@ -700,6 +701,7 @@ def awq_forward(layer: AwqLinear, x: torch.Tensor, bias: Optional[torch.Tensor] 
 
 
 # ------------------------------------------------- 4-bit key/value cache
+# Inference only, as the linears: no gradients flow through these calls.
 _DT16 = {torch.bfloat16: BF16, torch.float16: FP16}
 
 
@@ -730,8 +732,10 @@ def _need_workspace(t, device) -> None:
 def _call(device, f, *args) -> None:
     """A device entry point on `device`'s current stream."""
     i = device.index
-    if i is None or i == torch.cuda.current_device():
-        status = f(*args, torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    if i is None:                        # a CPU tensor's memory must not reach a kernel
+        raise ValueError(f"{f.__name__} runs on a GPU, not on {device}")
+    if i == torch.cuda.current_device():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(device):
             status = f(*args, torch._C._cuda_getCurrentRawStream(i))
@@ -871,21 +875,35 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, bias: Optiona
     return ids, weights
 
 
-def _moe_blob(qsz, N: int, K: int) -> np.ndarray:
-    """AWQ weights of E experts (codes [E, N, K/2], scales and zeros [E, N, K/64]) as one device blob."""
-    q, s, z = (np.ascontiguousarray(t.cpu().numpy() if isinstance(t, torch.Tensor) else t) for t in qsz)
-    E = q.shape[0]
-    if q.shape != (E, N, K // 2) or q.dtype != np.uint8 or s.shape != (E, N, K // 64) or s.shape != z.shape \
-            or s.dtype != np.float16 or z.dtype != np.float16:
-        raise ValueError(f"expert weights must be codes uint8 [E, {N}, {K // 2}] with float16 scales and zeros "
-                         f"[E, {N}, {K // 64}], got {q.shape} {q.dtype}, {s.shape} {s.dtype}, {z.shape} {z.dtype}")
+def _moe_blob(qsz, N: int, K: int, device) -> torch.Tensor:
+    """AWQ weights of E experts (codes [E, N, K/2], scales and zeros [E, N, K/64]) as one blob
+    on `device`: packed there if the three are there already, on the host otherwise."""
+    device = torch.device(device)
+    E, shapes = qsz[0].shape[0], [tuple(t.shape) for t in qsz]
+    if shapes != [(E, N, K // 2), (E, N, K // 64), (E, N, K // 64)]:
+        raise ValueError(f"expert weights must be codes [E, {N}, {K // 2}] with scales and zeros [E, {N}, {K // 64}], got {shapes}")
+    q, s, z = qsz
     n = _lib.awq_moe_device_weights_bytes(E, N, K)
     if n == 0:
         raise SvdqError(2, "awq_moe_device_weights_bytes")
+    if all(isinstance(t, torch.Tensor) and t.is_cuda for t in qsz) and device.type == "cuda":
+        if q.dtype != torch.uint8 or s.dtype != torch.float16 or z.dtype != torch.float16:
+            raise ValueError(f"codes must be uint8 with float16 scales and zeros, got {q.dtype}, {s.dtype}, {z.dtype}")
+        if q.device != s.device or q.device != z.device:
+            raise ValueError(f"codes, scales and zeros are on {q.device}, {s.device} and {z.device}")
+        if not bool(((z >= 0) & (z <= 15) & (z == z.floor())).all()) or not bool(torch.isfinite(s).all()):
+            raise ValueError("zero points must be integers in 0..15 and scales finite")
+        blob = torch.empty(n, dtype=torch.uint8, device=q.device)
+        q, s, z = q.contiguous(), s.contiguous(), z.contiguous()
+        _call(q.device, _lib.awq_moe_pack_on_device, q.data_ptr(), s.data_ptr(), z.data_ptr(), E, N, K, blob.data_ptr(), n)
+        return blob.to(device)
+    q, s, z = (np.ascontiguousarray(t.cpu().numpy() if isinstance(t, torch.Tensor) else t) for t in qsz)
+    if q.dtype != np.uint8 or s.dtype != np.float16 or z.dtype != np.float16:
+        raise ValueError(f"codes must be uint8 with float16 scales and zeros, got {q.dtype}, {s.dtype}, {z.dtype}")
     blob = np.empty(n, np.uint8)
     _check(_lib.awq_moe_pack_device_weights(_ptr(q), _ptr(s), _ptr(z), E, N, K, _ptr(blob), n),
            "awq_moe_pack_device_weights")
-    return blob
+    return torch.from_numpy(blob).to(device)
 
 
 class AwqMoe:
@@ -902,8 +920,8 @@ class AwqMoe:
             raise ValueError(f"gate_up {tuple(gate_up[0].shape)} and down {tuple(down[0].shape)} do not make an expert layer")
         if _lib.awq_moe_workspace_bytes(1, 1, self.K, self.I) == 0:
             raise SvdqError(2, "awq_moe_workspace_bytes")
-        self.gate_up = torch.from_numpy(_moe_blob(gate_up, 2 * self.I, self.K)).to(device)
-        self.down = torch.from_numpy(_moe_blob(down, self.K, self.I)).to(device)
+        self.gate_up = _moe_blob(gate_up, 2 * self.I, self.K, device)
+        self.down = _moe_blob(down, self.K, self.I, device)
         self.device = self.gate_up.device
         self._w = MoeWeights(self.gate_up.data_ptr(), self.down.data_ptr(), self.E, self.K, self.I)
         self._ref = ctypes.byref(self._w)

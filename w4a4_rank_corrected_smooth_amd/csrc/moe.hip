@@ -1,6 +1,7 @@
 // The expert layer of a mixture of experts for a few tokens, with AWQ W4A16
 // experts, and the router that picks them.
 //
+//  moe_pack_kernel     weights to the experts' blobs, on the device
 //  moe_logits_kernel   x w^T in float64
 //  moe_choose_kernel   scores, the best top_k of each token, their weights
 //  moe_gate_up_kernel  h = act(x Gate^T) * (x Up^T) of every (token, expert)
@@ -14,42 +15,6 @@
 #include "moe_layout.h"
 
 using namespace svdq;
-#ifndef GKS0
-#define GKS0 4
-#endif
-#ifndef GFKS
-#define GFKS 4
-#endif
-#ifndef FEWI
-#define FEWI 128
-#endif
-#ifndef DFW
-#define DFW 8
-#endif
-#ifndef FEWP
-#define FEWP 16
-#endif
-#ifndef DT0
-#define DT0 2
-#endif
-#ifndef DK0
-#define DK0 2
-#endif
-#ifndef DT1
-#define DT1 4
-#endif
-#ifndef FEWG
-#define FEWG 1024
-#endif
-#ifndef FEWD
-#define FEWD 4096
-#endif
-#ifndef GUW
-#define GUW 3
-#endif
-#ifndef DNW
-#define DNW 3
-#endif
 
 namespace {
 
@@ -62,6 +27,41 @@ template <bool F16>
 __device__ __forceinline__ float wide(uint32_t h) {
   if constexpr (F16) return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
   else return __uint_as_float(h << 16);
+}
+
+// ------------------------------------------------------------------------ pack
+// One wavefront per block of 1152 bytes.  Four canonical bytes (channel 2 j in
+// the low nibble of byte j, 2 j + 1 in the high one) become a blob word (channel
+// 2 j at nibble j of the low half-word, 2 j + 1 of the high one).
+__device__ __forceinline__ uint32_t blob_word(uint32_t u) {
+  uint32_t a = u & 0x0F0F0F0Fu, b = u >> 4 & 0x0F0F0F0Fu;
+  a = (a | a >> 4) & 0x00FF00FFu;
+  b = (b | b >> 4) & 0x00FF00FFu;
+  return ((a | a >> 8) & 0xFFFFu) | (b | b >> 8) << 16;
+}
+__global__ __launch_bounds__(256) void moe_pack_kernel(const uint8_t *__restrict__ q, const uint16_t *__restrict__ s,
+                                                       const uint16_t *__restrict__ z, int64_t blocks, int K, int G,
+                                                       int P, uint8_t *__restrict__ blob) {
+  const int lane = threadIdx.x & 63;
+  const int64_t block = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);     // (expert, tile, step)
+  if (block >= blocks) return;
+  const int64_t tile = block / P, n = tile * kAwqTile + lane % 16;
+  const int p = (int)(block % P);
+  uint8_t *out = blob + block * kMoeBlockBytes;
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (2 * p + i < G) {
+      const uint2 u = *reinterpret_cast<const uint2 *>(q + n * (K / 2) + (2 * p + i) * (kGroup / 2) + 8 * (lane / 16));
+      w[2 * i] = blob_word(u.x);
+      w[2 * i + 1] = blob_word(u.y);
+    }
+  *reinterpret_cast<uint4 *>(out + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (lane < 32) {
+    const int64_t at = (tile * kAwqTile + lane / 2) * G + 2 * p + lane % 2;
+    const bool in = 2 * p + lane % 2 < G;
+    reinterpret_cast<uint32_t *>(out + kAwqBlockBytes)[lane] = in ? (uint32_t)s[at] | (uint32_t)z[at] << 16 : 0u;
+  }
 }
 
 // ---------------------------------------------------------------------- router
@@ -306,6 +306,19 @@ __global__ __launch_bounds__(64) void moe_choose_kernel(const double *__restrict
 }
 
 // --------------------------------------------------------------------- experts
+// With s and z the scale and zero point of an output channel and group of 64
+// input channels, q the codes: an expert's product is sum_g s sum_k x (q - z).
+// bf16 rows take the codes as the bf16 values 128 + q (one and-or a pair, exact)
+// and sum_k x from one more product, with ones:
+//   sum_k x (q - z) = sum_k x (128 + q) - (128 + z) sum_k x,
+// in float32 (the terms are about 30 times the result's, so 2^-19 of it); fp16
+// rows take q - z exactly (1024 + q minus 1024 + z).  The gated product
+// h = act(gate) up goes on as two bf16 pieces, which hold it to 2^-17 in
+// float32's range (an fp16 h would overflow where y does not).
+// What bounds it: the experts' bytes, each read once.  128 tokens with 8 of 128
+// experts of 2048 x 768 (341 MB) take 86 us: gate and up 47 (227 MB, 4.8 TB/s; the
+// weights' stream alone 41, the products alone 28), down 33 (113 MB; 24 and 20),
+// the plan and the sum 3 and 4.
 struct MoeArgs {
   const uint8_t *gate_up, *down;      // E blobs each, one after another
   int64_t gate_up_stride, down_stride;
@@ -483,30 +496,39 @@ __device__ __forceinline__ void group_mma(uint4 a0, uint4 a1, v4f xsum, uint32_t
 }
 __device__ __forceinline__ v8bf ones() { return as_v8bf(make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u)); }
 
-// One expert's product for 16 R rows at a time, the form both products share.
+// One expert's product for a block of rows, the form both products share.
 //
 // Work of a wavefront: TILES tiles of 16 output columns over one of KS equal
-// parts of the input channels; a workgroup's four wavefronts are KS parts of
-// 4 / KS neighbouring sets of tiles.  A step is a pair of groups of 64
-// channels.
+// parts of the input channels; a workgroup's kWaves wavefronts are KS parts
+// of kWaves / KS neighbouring sets of tiles.  A step is a pair of groups of
+// 64 channels.
 // Weights: each wavefront streams its tiles from memory into a ring of RING
 // steps of registers; a step's place is filled anew as soon as it is used up.
-// Rows: in PIECES 16-bit pieces (x itself, or h's two), through LDS, CHUNK
-// steps of every part at a time, shared by the wavefronts; a chunk is fetched
-// to registers while the one before is worked on and then written to the
-// other buffer.  (Loads are waited for in the order in which they are
-// issued, so rows loaded straight into operands would hold up the weights
-// asked for after them.)
-// A row's chunk is 64 pieces of 16 bytes, 16 for each (part, step, piece);
-// piece p of row r is at place p ^ (r % 16) of its 16, so that the operand
-// reads, one row a lane, fall on different banks.
+// Rows: through LDS, CHUNK steps of every part at a time, shared by the
+// wavefronts; a chunk is fetched to registers while the one before is worked
+// on and then written to the other buffer.  (Loads are waited for in the
+// order in which they are issued, so rows loaded straight into operands would
+// hold up the weights asked for after them.)
+// Rows come in one 16-bit piece (x) or in two (h): FORM 1: one piece, 16 R rows;
+// 2: two pieces, 16 R rows, a product of each; 3: two pieces, 8 R rows, the second
+// pieces in the tile's upper eight rows, so that one product takes both (and
+// the two halves of the sums are added at the end).
+// A row's chunk is kWaves x 16 pieces of 16 bytes, 16 for each (part, step,
+// piece); 16-byte piece p of tile row r is at place p ^ (r % 16) of its 16, so
+// that the operand reads, one row a lane, fall on different banks.
 // Every load is unconditional: past the end a wavefront reads its last step
 // again, and rows past the last repeat it.
-template <int TILES, int PIECES, int KS, int R>
+constexpr int kWaves = 4;       // (8: 99 us against 92 for 128 tokens, 52.6 against 57 for 40)
+
+template <int TILES, int FORM, int KS, int R>
 struct Product {
-  static constexpr int CHUNK = 4 / (KS * PIECES), RING = CHUNK < 4 && TILES <= 2 ? 4 : CHUNK;
-  static_assert(CHUNK >= 1 && RING % CHUNK == 0, "whole chunks in a ring");
-  static constexpr int LDS_BYTES = 2 * 16 * R * 1024;
+  static constexpr int PIECES = FORM == 2 ? 2 : 1;       // products of a tile row
+  static constexpr int ROWS = (FORM == 3 ? 8 : 16) * R;  // rows of a block
+  static constexpr int CHUNK = kWaves / (KS * PIECES), RING = TILES <= 2 ? 4 : 2;
+  static constexpr int UNROLL = CHUNK > RING ? CHUNK : RING;
+  static_assert(CHUNK >= 1 && UNROLL % CHUNK == 0 && UNROLL % RING == 0, "whole chunks and rings");
+  static constexpr int ROW_BYTES = kWaves * 256, BUFFER = 16 * R * ROW_BYTES, LDS_BYTES = 2 * BUFFER;
+  static constexpr int WPR = kWaves / 4;              // wavefronts that fetch a row
 
   // (addresses are kept as a base that the wavefront shares, in scalar
   // registers, and a lane's own 32-bit offset)
@@ -529,6 +551,12 @@ struct Product {
     p0 = min(P, wave % KS * each);
     p1 = min(P, p0 + each);
   }
+  // tile row of the j-th 16-byte piece that the wavefront fetches, and its row of the block
+  static __device__ __forceinline__ int tile_row(int wave, int j) { return wave / WPR + 4 * j; }
+  static __device__ __forceinline__ int block_row(int wave, int j) {
+    const int r = tile_row(wave, j);
+    return FORM == 3 ? r / 16 * 8 + r % 8 : r;
+  }
   __device__ __forceinline__ void load_step(int i, int p, int lane) {
     p = max(min(min(p, p1 - 1), P - 1), 0);
 #pragma unroll
@@ -539,44 +567,45 @@ struct Product {
       sz[i][t] = *reinterpret_cast<const uint2 *>(block + (kAwqBlockBytes + (uint32_t)(lane & 15) * 8));
     }
   }
-  // chunk c of the rows into registers: thread (wave, lane) takes 16-byte
-  // piece `lane` of rows wave, wave + 4, ...; row[j]: those rows' places in src
-  __device__ __forceinline__ void fetch(int c, const int (&row)[4 * R], int lane) {
-    const int s = lane / 16, piece = s % PIECES, step = s / PIECES % CHUNK, part = s / PIECES / CHUNK;
-    int p = min(min(part * each + c * CHUNK + step, part * each + each - 1), P - 1);
+  // chunk c of the rows into registers; row[j]: the place in src of block row block_row(wave, j)
+  __device__ __forceinline__ void fetch(int c, const int (&row)[4 * R], int wave, int lane) {
+    const int s = wave % WPR * 4 + lane / 16, step = s / PIECES % CHUNK, part = s / PIECES / CHUNK;
+    const int p = min(min(part * each + c * CHUNK + step, part * each + each - 1), P - 1);
     const int group = min(2 * p + lane % 16 / 8, G - 1);      // an odd last step has one group
-    const uint32_t at = (uint32_t)((group * PIECES + piece) * kGroup + lane % 8 * 8) * 2;
 #pragma unroll
-    for (int j = 0; j < 4 * R; ++j)
+    for (int j = 0; j < 4 * R; ++j) {
+      const int piece = FORM == 2 ? s % 2 : FORM == 3 ? j / 2 % 2 : 0;
+      const uint32_t at = (uint32_t)((group * (FORM == 1 ? 1 : 2) + piece) * kGroup + lane % 8 * 8) * 2;
       stage[j] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(src + row[j] * ld) + at);
+    }
   }
   __device__ __forceinline__ void put(uint8_t *lds, int wave, int lane) const {
 #pragma unroll
     for (int j = 0; j < 4 * R; ++j) {
-      const int r = wave + 4 * j;
-      *reinterpret_cast<uint4 *>(lds + r * 1024 + (lane / 16) * 256 + ((lane ^ r) % 16) * 16) = stage[j];
+      const int r = tile_row(wave, j);
+      *reinterpret_cast<uint4 *>(lds + r * ROW_BYTES + (wave % WPR * 4 + lane / 16) * 256 + ((lane ^ r) % 16) * 16) = stage[j];
     }
   }
   __device__ __forceinline__ uint4 operand(const uint8_t *lds, int r, int s, int k, int lane) const {
     const int row = 16 * r + lane % 16, piece = 8 * (k / 2) + 2 * (lane / 16) + k % 2;
-    return *reinterpret_cast<const uint4 *>(lds + row * 1024 + s * 256 + ((piece ^ row) % 16) * 16);
+    return *reinterpret_cast<const uint4 *>(lds + row * ROW_BYTES + s * 256 + ((piece ^ row) % 16) * 16);
   }
-  // all steps; `group(i, ring place, operands of piece 0 and 1, r)` adds a group
+  // all steps; `group(g, ring place, operands of each piece, r)` adds a group
   template <typename Group>
   __device__ __forceinline__ void run(uint8_t *lds, const int (&row)[4 * R], int wave, int lane, Group group) {
     const int chunks = (each + CHUNK - 1) / CHUNK;
-    fetch(0, row, lane);
+    fetch(0, row, wave, lane);
 #pragma unroll
     for (int i = 0; i < RING; ++i) load_step(i, p0 + i, lane);
     put(lds, wave, lane);
     __syncthreads();
-    uint8_t *cur = lds, *other = lds + 16 * R * 1024;
-    for (int c = 0; c < chunks; c += RING / CHUNK) {
+    uint8_t *cur = lds, *other = lds + BUFFER;
+    for (int c = 0; c < chunks; c += UNROLL / CHUNK) {
 #pragma unroll
-      for (int i = 0; i < RING; ++i) {
+      for (int i = 0; i < UNROLL; ++i) {
         if (i % CHUNK == 0) {
           if (i > 0 && c + i / CHUNK >= chunks) break;
-          fetch(c + i / CHUNK + 1, row, lane);
+          fetch(c + i / CHUNK + 1, row, wave, lane);
         }
         const int p = p0 + c * CHUNK + i;
         if (p < p1) {
@@ -591,11 +620,11 @@ struct Product {
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
                   a[h][k] = operand(cur, r, (wave % KS * CHUNK + i % CHUNK) * PIECES + h, 2 * g + k, lane);
-              group(g, i, a, r);
+              group(g, i % RING, a, r);
             }
           }
         }
-        load_step(i, p + RING, lane);
+        load_step(i % RING, p + RING, lane);
         if (i % CHUNK == CHUNK - 1) {
           put(other, wave, lane);
           __syncthreads();
@@ -634,13 +663,13 @@ __device__ __forceinline__ void meet(v4f (&acc)[N], uint8_t *lds, int w, int lan
 
 // h = act(gate) * up of 16 columns a wavefront (tiles: the gate's and the up's).
 template <bool F16, bool GELU, int KS, int R, bool PLAN>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(GUW))) void moe_gate_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_kernel(MoeArgs a) {
   typedef Product<2, 1, KS, R> Pr;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Pr::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Rows<PLAN> rows;
   if (!rows.find(a, blockIdx.y, lane)) return;
-  const int n = a.I / kAwqTile, tile = blockIdx.x * (4 / KS) + w / KS;
+  const int n = a.I / kAwqTile, tile = blockIdx.x * (kWaves / KS) + w / KS;
   Pr pr;
   const int tiles[2] = {min(tile, n - 1), min(tile, n - 1) + n};
   pr.init(a.gate_up + rows.expert * a.gate_up_stride, MoeWeightLayout(2 * (int64_t)a.I, a.K), tiles, w);
@@ -649,7 +678,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(GUW))) void
   for (int r0 = 0; r0 < rows.count; r0 += 16 * R) {
     int row[4 * R];
 #pragma unroll
-    for (int j = 0; j < 4 * R; ++j) row[j] = rows.one(min(r0 + w + 4 * j, rows.count - 1)) / a.top_k;
+    for (int j = 0; j < 4 * R; ++j) row[j] = rows.one(min(r0 + Pr::block_row(w, j), rows.count - 1)) / a.top_k;
     v4f acc[2 * R] = {};
     pr.run(lds, row, w, lane, [&](int g, int i, const uint4 (&x)[1][2], int r) {
       v4f xsum = v4f{};
@@ -681,14 +710,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(GUW))) void
 
 // TILES tiles of 16 columns of h Down^T a wavefront; h enters as its two bf16
 // pieces (h to 2^-17, in float32's range).
-template <int TILES, int KS, int R, bool PLAN>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DNW))) void moe_down_kernel(MoeArgs a) {
-  typedef Product<TILES, 2, KS, R> Pr;
+template <int TILES, int FORM, int KS, int R, bool PLAN>
+__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2))) void moe_down_kernel(MoeArgs a) {
+  typedef Product<TILES, FORM, KS, R> Pr;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Pr::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Rows<PLAN> rows;
   if (!rows.find(a, blockIdx.y, lane)) return;
-  const int n = a.K / kAwqTile, tile0 = (blockIdx.x * (4 / KS) + w / KS) * TILES;
+  const int n = a.K / kAwqTile, tile0 = (blockIdx.x * (kWaves / KS) + w / KS) * TILES;
   Pr pr;
   int tiles[TILES];
 #pragma unroll
@@ -696,18 +725,22 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DNW))) void
   pr.init(a.down + rows.expert * a.down_stride, MoeWeightLayout(a.K, a.I), tiles, w);
   pr.src = a.h;
   pr.ld = 2 * a.I;
-  for (int r0 = 0; r0 < rows.count; r0 += 16 * R) {
+  for (int r0 = 0; r0 < rows.count; r0 += Pr::ROWS) {
     int row[4 * R];
 #pragma unroll
-    for (int j = 0; j < 4 * R; ++j) row[j] = rows.one(min(r0 + w + 4 * j, rows.count - 1));
+    for (int j = 0; j < 4 * R; ++j) row[j] = rows.one(min(r0 + Pr::block_row(w, j), rows.count - 1));
     v4f acc[TILES * R] = {};
-    pr.run(lds, row, w, lane, [&](int g, int i, const uint4 (&h)[2][2], int r) {
-      const v4f sum = mma(h[1][1], ones(), mma(h[1][0], ones(), mma(h[0][1], ones(), mma(h[0][0], ones(), v4f{}))));
+    pr.run(lds, row, w, lane, [&](int g, int i, const uint4 (&h)[Pr::PIECES][2], int r) {
+      v4f sum = v4f{};
+#pragma unroll
+      for (int k = 0; k < 2 * Pr::PIECES; ++k) sum = mma(h[k / 2][k % 2], ones(), sum);
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         const v8bf b0 = codes_128(g ? pr.code[i][t].z : pr.code[i][t].x);
         const v8bf b1 = codes_128(g ? pr.code[i][t].w : pr.code[i][t].y);
-        const v4f prod = mma(h[1][1], b1, mma(h[1][0], b0, mma(h[0][1], b1, mma(h[0][0], b0, v4f{}))));
+        v4f prod = v4f{};
+#pragma unroll
+        for (int k = 0; k < 2 * Pr::PIECES; ++k) prod = mma(h[k / 2][k % 2], k % 2 ? b1 : b0, prod);
         const uint32_t sz = g ? pr.sz[i][t].y : pr.sz[i][t].x;
         const float z = -(128.0f + (float)zero_of(sz)), sc = scale_of(sz);
         v4f &o = acc[TILES * r + t];
@@ -717,11 +750,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DNW))) void
     });
     meet<TILES * R, KS>(acc, lds, w, lane);
     if (w % KS != 0) continue;
+    if constexpr (FORM == 3) {            // the second pieces' sums stand 32 lanes on
+#pragma unroll
+      for (int i = 0; i < TILES * R; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] += __shfl_xor(acc[i][e], 32);
+      if (lane >= 32) continue;
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int at_row = r0 + 16 * r + 4 * (lane >> 4) + e;
+        const int at_row = r0 + (FORM == 3 ? 8 : 16) * r + 4 * (lane >> 4) + e;
         const int64_t to = (int64_t)rows.pair(min(at_row, rows.count - 1)) * a.K + (lane & 15);
 #pragma unroll
         for (int t = 0; t < TILES; ++t)
@@ -731,11 +771,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DNW))) void
 }
 
 // ------------------------------------------------- a handful of pairs
-// Up to kMoeFewPairs (token, choice) pairs, a step of one or two sequences, the
+// A step of one or two sequences: up to kMoeFewPairs (token, choice) pairs, and at
+// most kFewSteps steps of weights for a column tile of the down product.  The
 // layer is two kernels and all latency: each wavefront holds all its loads in
 // flight, rows come straight into operands (there are few, so they share
 // lines), and the down product's workgroups own their columns of y, so the
-// sum over the choices needs no kernel of its own.
+// sum over the choices needs no kernel of its own.  One token with 8 of 64
+// experts of 2048 x 768: 15.4 us against 22 in the form above (21 MB of weights,
+// 3.4 us at the rate of a long read; the two kernels' launches and the chain
+// ids, rows and weights, product, meeting make up the rest); 8 tokens with 2 of 8
+// experts of 4096 x 3584 (224 steps): 67 us against 57.
+constexpr int kFewSteps = 128;
+constexpr int kFewGateParts = 4, kFewDownWaves = 8;     // wavefronts a workgroup (8 and 16: 19.9 and 16.6 us)
 template <int TILES>
 struct FewWeights {
   uint4 code[TILES];
@@ -827,7 +874,7 @@ __global__ __launch_bounds__(KS * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
 // row, and its product is not taken.  A token that names an expert twice
 // counts it with both weights.
 template <bool F16, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void moe_down_few_kernel(MoeArgs a) {
+__global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(WAVES / 4))) void moe_down_few_kernel(MoeArgs a) {
   __shared__ v4f red[WAVES][64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = a.T * a.top_k;
@@ -869,23 +916,23 @@ __global__ __launch_bounds__(WAVES * 64) void moe_down_few_kernel(MoeArgs a) {
     const uint16_t *h = a.h + (int64_t)pair * (2 * a.I);
     const int p1 = min(P, end - slot * P);
     v4f acc = v4f{};
-    // weights four steps ahead, rows (from the cache) two
-    constexpr int AHEAD = 4;
+    // weights eight steps ahead, rows (from the cache) two
+    constexpr int AHEAD = 8, RA = 2;
     FewWeights<1> s[AHEAD];
-    FewRows<2> r[2];
+    FewRows<2> r[RA];
     for (int p = at - slot * P; p < p1; p += AHEAD) {
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) s[i].load(tile, min(p + i, p1 - 1), lane);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) r[i].load(h, min(p + i, p1 - 1), G, lane);
+      for (int i = 0; i < RA; ++i) r[i].load(h, min(p + i, p1 - 1), G, lane);
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         if (p + i >= p1) break;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           if (2 * (p + i) + g >= G) break;
-          const uint4 h0 = r[i % 2].x[0][2 * g], h1 = r[i % 2].x[0][2 * g + 1];
-          const uint4 l0 = r[i % 2].x[1][2 * g], l1 = r[i % 2].x[1][2 * g + 1];
+          const uint4 h0 = r[i % RA].x[0][2 * g], h1 = r[i % RA].x[0][2 * g + 1];
+          const uint4 l0 = r[i % RA].x[1][2 * g], l1 = r[i % RA].x[1][2 * g + 1];
           const v8bf b0 = codes_128(g ? s[i].code[0].z : s[i].code[0].x), b1 = codes_128(g ? s[i].code[0].w : s[i].code[0].y);
           const v4f sum = mma(l1, ones(), mma(l0, ones(), mma(h1, ones(), mma(h0, ones(), v4f{}))));
           const v4f prod = mma(l1, b1, mma(l0, b0, mma(h1, b1, mma(h0, b0, v4f{}))));
@@ -894,7 +941,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_down_few_kernel(MoeArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(__builtin_fmaf(z, sum[e], prod[e]), sc, acc[e]);
         }
-        if (i + 2 < AHEAD) r[i % 2].load(h, min(p + i + 2, p1 - 1), G, lane);
+        if (i + RA < AHEAD) r[i % RA].load(h, min(p + i + RA, p1 - 1), G, lane);
       }
     }
     const uint64_t chose = __ballot(mine != 0);
@@ -919,23 +966,29 @@ __global__ __launch_bounds__(WAVES * 64) void moe_down_few_kernel(MoeArgs a) {
 }
 
 // y[t] = sum over the token's choices of weight times part, in order; choices
-// without an expert here are left out.  One thread per 4 columns.
+// without an expert here are left out.  One thread per 4 columns of a token.
 template <bool F16>
 __global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int quads = a.K / 4;
-  const int64_t t = idx / quads;
-  const int c = (int)(idx % quads) * 4;
-  if (t >= a.T) return;
+  const int t = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (c >= a.K) return;
+  const int *ids = a.ids + (int64_t)t * a.top_k;
+  const float *weights = a.weights + (int64_t)t * a.top_k;
+  const float *part = a.part + (int64_t)t * a.top_k * a.K + c;
   v4f y = v4f{};
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t p = t * a.top_k + j;
-    const int e = a.ids[p];
-    if (e < 0 || e >= a.E) continue;
-    const float w = a.weights[p];
-    const v4f v = *reinterpret_cast<const v4f *>(a.part + p * a.K + c);
+  for (int j0 = 0; j0 < a.top_k; j0 += 4) {      // four rows' loads in flight
+    v4f v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(w, v[i], y[i]);
+    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const v4f *>(part + (int64_t)min(j0 + k, a.top_k - 1) * a.K);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (j0 + k >= a.top_k) break;
+      const int e = ids[j0 + k];
+      const float w = weights[j0 + k];
+      if (e >= 0 && e < a.E) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(w, v[k][i], y[i]);
+      }
+    }
   }
   uint2 out;
   if constexpr (F16) {
@@ -945,12 +998,30 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
     out.x = pack_bf16(y[0], y[1]);
     out.y = pack_bf16(y[2], y[3]);
   }
-  *reinterpret_cast<uint2 *>(a.y + t * a.K + c) = out;
+  *reinterpret_cast<uint2 *>(a.y + (int64_t)t * a.K + c) = out;
 }
 
 }  // namespace
 
 extern "C" {
+
+svdq_status_t awq_moe_pack_on_device(const uint8_t *q, const uint16_t *s, const uint16_t *z, int E, int N, int K,
+                                     void *blob, size_t bytes, void *hip_stream) {
+  if (!q || !s || !z || !blob) return fail(SVDQ_ERR_INVALID_ARGUMENT, "awq_moe_pack_on_device: NULL");
+  if (!aligned16(q) || !aligned16(blob) || (((uintptr_t)s | (uintptr_t)z) & 1u))
+    return fail(SVDQ_ERR_INVALID_ARGUMENT, "awq_moe_pack_on_device: misaligned pointer");
+  const size_t need = awq_moe_device_weights_bytes(E, N, K);
+  if (need == 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (bytes < need)
+    return fail(SVDQ_ERR_WORKSPACE_TOO_SMALL, "awq_moe_pack_on_device: blob needs %zu bytes, got %zu", need, bytes);
+  const svdq_status_t st = svdq_device_check();
+  if (st != SVDQ_OK) return st;
+  const MoeWeightLayout L(N, K);
+  const int64_t blocks = (int64_t)E * (N / kAwqTile) * L.P;
+  hipLaunchKernelGGL(moe_pack_kernel, dim3((unsigned)((blocks + 3) / 4)), dim3(256), 0, static_cast<hipStream_t>(hip_stream),
+                     q, s, z, blocks, K, (int)L.G, (int)L.P, static_cast<uint8_t *>(blob));
+  return launch_status("expert weight packing launch");
+}
 
 svdq_status_t svdq_moe_route(const void *x, const void *w_router, const float *bias, svdq_dtype_t dtype, int T, int E,
                              int K, int top_k, svdq_moe_score_t score, int normalize, int32_t *ids, float *weights,
@@ -1041,47 +1112,75 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   a.part = reinterpret_cast<float *>(ws + L.part);
   a.y = static_cast<uint16_t *>(y);
   a.plan = reinterpret_cast<MoePlan *>(ws + L.plan);
-  const int pairs = T * top_k, slots = pairs < w->E ? pairs : w->E;
-  if (pairs <= kMoeFewPairs && slots * ((w->I + 127) / 128) <= FEWI) {
-    const dim3 few_grid((unsigned)(w->I / kAwqTile), (unsigned)slots);
-#define MOE_FEW(F, A) hipLaunchKernelGGL((moe_gate_up_few_kernel<F, A, GFKS>), few_grid, dim3(GFKS * 64), 0, stream_, a)
-    const hipStream_t stream_ = static_cast<hipStream_t>(hip_stream);
+  const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  const int pairs = T * top_k, slots = pairs < w->E ? pairs : w->E;       // experts in use at most
+  const int gt = w->I / kAwqTile, dt = w->K / kAwqTile;
+  const bool gelu = act == SVDQ_MOE_GELU_TANH;
+  if (pairs <= kMoeFewPairs && slots * ((w->I + 127) / 128) <= kFewSteps) {
+#define MOE_FEW(F, A)                                                                                            \
+  hipLaunchKernelGGL((moe_gate_up_few_kernel<F, A, kFewGateParts>), dim3((unsigned)gt, (unsigned)slots),         \
+                     dim3(kFewGateParts * 64), 0, stream, a)
+#define MOE_FEW_DOWN(F)                                                                                          \
+  hipLaunchKernelGGL((moe_down_few_kernel<F, kFewDownWaves>), dim3((unsigned)dt), dim3(kFewDownWaves * 64), 0, stream, a)
     if (dtype == SVDQ_FP16) {
-      if (act == SVDQ_MOE_GELU_TANH) MOE_FEW(true, true); else MOE_FEW(true, false);
-      hipLaunchKernelGGL((moe_down_few_kernel<true, DFW>), dim3(w->K / kAwqTile), dim3(DFW * 64), 0, stream_, a);
+      if (gelu) MOE_FEW(true, true); else MOE_FEW(true, false);
+      MOE_FEW_DOWN(true);
     } else {
-      if (act == SVDQ_MOE_GELU_TANH) MOE_FEW(false, true); else MOE_FEW(false, false);
-      hipLaunchKernelGGL((moe_down_few_kernel<false, DFW>), dim3(w->K / kAwqTile), dim3(DFW * 64), 0, stream_, a);
+      if (gelu) MOE_FEW(false, true); else MOE_FEW(false, false);
+      MOE_FEW_DOWN(false);
     }
+#undef MOE_FEW_DOWN
 #undef MOE_FEW
     return launch_status("expert layer launch");
   }
-  const bool plan = pairs > 64 || pairs > 12 * slots;
-  const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  // Blocks of 32 rows from 12 pairs an expert on: an expert of more than 16 rows
+  // then reads its weights once, not twice.
+  const bool many = pairs > 12 * slots;
+  // Up to 5 pairs an expert, both pieces of h in one tile: 12 tokens with 6 of 64
+  // experts took 57.3 us against 62.6, 8 with 2 of 8 45 against 51; at 8 pairs an
+  // expert, where four experts in ten have more than 8 rows, 108 against 92.
+  const bool packed = pairs <= 5 * slots;
+  // Few tiles: K in parts for the wavefronts of a workgroup.  With 256 and 512
+  // tiles of gate and up 16.2 and 26.5 us in four parts, 20.2 and 31.5 in one;
+  // with 768, 28.4 and 27.5.  Down: 1024 and 2048 tiles 14.6 and 28.4 us as two
+  // parts of two tiles, 17.0 and 29.2 as four tiles; with 16384, 107 and 92.
+  const bool few = (int64_t)slots * gt < 640, few_down = (int64_t)slots * dt < 4096;
+  const bool plan = pairs > 64 || many;
   if (plan) hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
-  const int gt = w->I / kAwqTile, dt = w->K / kAwqTile;
-  const bool few = (int64_t)slots * gt < FEWG, few_down = (int64_t)slots * dt < FEWD, many = pairs > 12 * slots;
-#define MOE_GU(F, A, KS, R, P)                                                                                         \
-  hipLaunchKernelGGL((moe_gate_up_kernel<F, A, KS, R, P>), dim3((gt + 4 / KS - 1) / (4 / KS), (unsigned)slots),        \
-                     dim3(256), 0, stream, a)
-#define MOE_GU_R(F, A, KS) do { if (many) MOE_GU(F, A, KS, 2, true); else if (plan) MOE_GU(F, A, KS, 1, true); else MOE_GU(F, A, KS, 1, false); } while (0)
-#define MOE_GU_K(F, A) do { if (few) MOE_GU_R(F, A, GKS0); else MOE_GU_R(F, A, 1); } while (0)
-#define MOE_DN(TT, KS, R, P)                                                                                           \
-  hipLaunchKernelGGL((moe_down_kernel<TT, KS, R, P>), dim3((dt + TT * (4 / KS) - 1) / (TT * (4 / KS)), (unsigned)slots), \
-                     dim3(256), 0, stream, a)
-#define MOE_DN_R(TT, KS) do { if (many) MOE_DN(TT, KS, 2, true); else if (plan) MOE_DN(TT, KS, 1, true); else MOE_DN(TT, KS, 1, false); } while (0)
+#define MOE_GU(F, A, KS, R, P)                                                                                   \
+  hipLaunchKernelGGL((moe_gate_up_kernel<F, A, KS, R, P>),                                                       \
+                     dim3((gt + kWaves / KS - 1) / (kWaves / KS), (unsigned)slots), dim3(kWaves * 64), 0, stream, a)
+#define MOE_GU_R(F, A, KS)                          \
+  do {                                              \
+    if (many) MOE_GU(F, A, KS, 2, true);            \
+    else if (plan) MOE_GU(F, A, KS, 1, true);       \
+    else MOE_GU(F, A, KS, 1, false);                \
+  } while (0)
+#define MOE_GU_K(F, A) do { if (few) MOE_GU_R(F, A, 4); else MOE_GU_R(F, A, 1); } while (0)
+#define MOE_DN(TT, FM, KS, R, P)                                                                                 \
+  hipLaunchKernelGGL((moe_down_kernel<TT, FM, KS, R, P>),                                                        \
+                     dim3((dt + TT * (kWaves / KS) - 1) / (TT * (kWaves / KS)), (unsigned)slots),                \
+                     dim3(kWaves * 64), 0, stream, a)
+#define MOE_DN_R(TT, KS)                            \
+  do {                                              \
+    if (many) MOE_DN(TT, 2, KS, 2, true);           \
+    else if (packed && plan) MOE_DN(TT, 3, KS, 1, true);  \
+    else if (packed) MOE_DN(TT, 3, KS, 1, false);   \
+    else if (plan) MOE_DN(TT, 2, KS, 1, true);      \
+    else MOE_DN(TT, 2, KS, 1, false);               \
+  } while (0)
   if (dtype == SVDQ_FP16) {
-    if (act == SVDQ_MOE_GELU_TANH) MOE_GU_K(true, true); else MOE_GU_K(true, false);
+    if (gelu) MOE_GU_K(true, true); else MOE_GU_K(true, false);
   } else {
-    if (act == SVDQ_MOE_GELU_TANH) MOE_GU_K(false, true); else MOE_GU_K(false, false);
+    if (gelu) MOE_GU_K(false, true); else MOE_GU_K(false, false);
   }
-  if (few_down) MOE_DN_R(DT0, DK0); else MOE_DN_R(DT1, 1);
+  if (few_down) MOE_DN_R(2, 2); else MOE_DN_R(4, 1);
 #undef MOE_DN_R
 #undef MOE_DN
 #undef MOE_GU_K
 #undef MOE_GU_R
 #undef MOE_GU
-  const dim3 g3((unsigned)(((int64_t)T * (w->K / 4) + 255) / 256));
+  const dim3 g3((unsigned)((w->K / 4 + 255) / 256), (unsigned)T);
   if (dtype == SVDQ_FP16) hipLaunchKernelGGL((moe_sum_kernel<true>), g3, dim3(256), 0, stream, a);
   else hipLaunchKernelGGL((moe_sum_kernel<false>), g3, dim3(256), 0, stream, a);
   return launch_status("expert layer launch");

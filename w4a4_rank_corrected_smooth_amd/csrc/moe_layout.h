@@ -8,15 +8,12 @@
 
 #define MOE_MAX_EXPERTS 1024
 
-#ifndef FEWP
-#define FEWP 16
-#endif
 namespace svdq {
 
 constexpr int kMoeMaxTopK = 32;
 constexpr int kMoeMaxPairs = 4096;     // tokens times choices of one call
 
-constexpr int kMoeFewPairs = FEWP;
+constexpr int kMoeFewPairs = 16;       // the form for a handful of pairs
 constexpr bool moe_route_ok(int64_t T, int E, int K, int top_k) {
   return T >= 0 && E >= 1 && E <= MOE_MAX_EXPERTS && K >= 8 && K % 8 == 0 && K <= (1 << 20) && top_k >= 1 &&
          top_k <= E && top_k <= kMoeMaxTopK && T <= 65535;
