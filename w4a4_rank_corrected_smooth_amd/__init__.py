@@ -760,24 +760,29 @@ class Kv4Cache:
         self._ref = ctypes.byref(self._c)
 
 
+def _rows_ok(t, dev, H: int, D: int) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype in _DT16 and t.dim() == 3 and t.size(1) == H and t.size(2) == D
+            and t.stride(2) == 1 and t.device == dev)
+
+
 def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
     """Encodes key and value rows [T, kv_heads, head_dim] (bf16 or fp16; any row and
     head strides that are multiples of 8) into the cache's slots [T] (int32, all different; slots
     outside the cache, such as -1, are skipped)."""
-    dev = cache.device
+    dev, H, D = cache.device, cache.kv_heads, cache.head_dim
     for t, name in ((k, "k"), (v, "v")):
-        _need(t, name, dev, _DT16, 3)
-        if t.shape[1:] != (cache.kv_heads, cache.head_dim) or t.stride(2) != 1:
-            raise ValueError(f"{name} must be [T, {cache.kv_heads}, {cache.head_dim}] with adjacent channels, "
+        if not _rows_ok(t, dev, H, D):
+            _need(t, name, dev, _DT16, 3)
+            raise ValueError(f"{name} must be [T, {H}, {D}] with adjacent channels, "
                              f"got {tuple(t.shape)} with strides {t.stride()}")
-    T = k.shape[0]
-    if v.shape[0] != T or v.dtype != k.dtype:
+    T = k.size(0)
+    if v.size(0) != T or v.dtype != k.dtype:
         raise ValueError("k and v must have the same rows and dtype")
     _need_dense(slots, "slots", dev, torch.int32, (T,))
     (k0, k1, _), (v0, v1, _) = k.stride(), v.stride()
     if T == 1:                           # torch leaves any stride where there is one element
         k0 = v0 = 0
-    if cache.kv_heads == 1:
+    if H == 1:
         k1 = v1 = 0
     _call(dev, _lib.svdq_kv4_append, cache._ref, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, _DT16[k.dtype], T,
           slots.data_ptr())
@@ -785,15 +790,16 @@ def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
 
 def kv4_read(cache: Kv4Cache, slots: torch.Tensor, dtype=torch.bfloat16):
     """The values in the cache's slots [T] as (k, v) [T, kv_heads, head_dim], bf16 or float32 (both exact)."""
-    if dtype not in (torch.bfloat16, torch.float32):
+    dev = cache.device
+    if dtype != torch.bfloat16 and dtype != torch.float32:
         raise ValueError(f"dtype must be bfloat16 or float32, got {dtype}")
-    _need(slots, "slots", cache.device, (torch.int32,), 1)
+    _need(slots, "slots", dev, (torch.int32,), 1)
     if not slots.is_contiguous():
         raise ValueError("slots must be contiguous")
-    T = slots.shape[0]
-    k = torch.empty((T, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
-    v = torch.empty((T, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
-    _call(cache.device, _lib.svdq_kv4_read, cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
+    T = slots.size(0)
+    k = torch.empty((T, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
+    _call(dev, _lib.svdq_kv4_read, cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
           FP32 if dtype == torch.float32 else BF16)
     return k, v
 
@@ -823,7 +829,7 @@ def kv4_attention(cache: Kv4Cache, q: torch.Tensor, page_table: torch.Tensor, se
         raise ValueError(f"page_table must be contiguous with {B} rows, got {tuple(page_table.shape)}")
     _need_dense(seq_lens, "seq_lens", dev, torch.int32, (B,))
     if out is None:
-        out = torch.empty((B, Q, Hq, D), dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _need_dense(out, "out", dev, q.dtype, (B, Q, Hq, D))
     if workspace is None:
@@ -945,7 +951,7 @@ def awq_moe_forward(layer: AwqMoe, x: torch.Tensor, ids: torch.Tensor, weights: 
     dev = layer.device
     _need(x, "x", dev, _DT16, 2)
     T = x.shape[0]
-    if x.shape[1] != layer.K or not x.is_contiguous():
+    if x.size(1) != layer.K or not x.is_contiguous():
         raise ValueError(f"x must be contiguous [T, {layer.K}], got {tuple(x.shape)}")
     _need(ids, "ids", dev, (torch.int32,), 2)
     top_k = ids.shape[1]
@@ -955,7 +961,7 @@ def awq_moe_forward(layer: AwqMoe, x: torch.Tensor, ids: torch.Tensor, weights: 
     if activation not in MOE_ACTIVATIONS:
         raise ValueError(f"activation must be one of {tuple(MOE_ACTIVATIONS)}, got {activation!r}")
     if out is None:
-        out = torch.empty((T, layer.K), dtype=x.dtype, device=dev)
+        out = torch.empty_like(x)
     else:
         _need_dense(out, "out", dev, x.dtype, (T, layer.K))
     if workspace is None:

@@ -150,12 +150,12 @@ __global__ __launch_bounds__(512) void moe_logits_tile_kernel(const uint16_t *__
     for (int n = 0; n < AHEAD; ++n) {
       const int i = i0 + 8 * n;
       if (i >= turns) break;
-      const bool in = 32 * i + c < K;                     // the last turn may end inside
+      if (32 * i + 32 > K && 32 * i + c >= K) a[n] = b[n] = make_uint4(0, 0, 0, 0);     // the last turn may end inside
       const uint32_t aw[4] = {a[n].x, a[n].y, a[n].z, a[n].w}, bw[4] = {b[n].x, b[n].y, b[n].z, b[n].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const double a0 = in ? (double)wide<F16>(aw[j] & 0xFFFFu) : 0.0, a1 = in ? (double)wide<F16>(aw[j] >> 16) : 0.0;
-        const double b0 = in ? (double)wide<F16>(bw[j] & 0xFFFFu) : 0.0, b1 = in ? (double)wide<F16>(bw[j] >> 16) : 0.0;
+        const double a0 = (double)wide<F16>(aw[j] & 0xFFFFu), a1 = (double)wide<F16>(aw[j] >> 16);
+        const double b0 = (double)wide<F16>(bw[j] & 0xFFFFu), b1 = (double)wide<F16>(bw[j] >> 16);
         acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a0, b0, acc, 0, 0, 0);
         acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a1, b1, acc, 0, 0, 0);
       }
