@@ -4,6 +4,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 
 #include "common.h"
 #include "host_prepare.h"
@@ -321,7 +322,11 @@ svdq_status_t awq_moe_pack_device_weights(const uint8_t *q, const uint16_t *s, c
                                           void *host_blob, size_t bytes) {
   if (!q || !s || !z || !host_blob) return fail(SVDQ_ERR_INVALID_ARGUMENT, "awq_moe_pack_device_weights: NULL");
   if (!moe_linear_ok(E, N, K, "awq_moe_pack_device_weights")) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  return awq_moe_pack(q, s, z, E, N, K, host_blob, bytes);
+  try {
+    return awq_moe_pack(q, s, z, E, N, K, host_blob, bytes);
+  } catch (const std::exception &e) {       // the thread pool could not start
+    return fail(SVDQ_ERR_INVALID_ARGUMENT, "awq_moe_pack_device_weights: %s", e.what());
+  }
 }
 
 }  // extern "C"
