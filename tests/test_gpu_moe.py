@@ -150,6 +150,9 @@ SPLITS = [
     (64, 16, 128, 704, 2), (32, 4, 448, 64, 1),       # 8 pairs an expert: above 64 pairs, and not
     (128, 16, 64, 704, 2), (100, 4, 192, 320, 1),     # 16 and 25 pairs an expert
     (32, 64, 2048, 64, 1), (48, 32, 2048, 64, 4), (128, 32, 2048, 64, 4),   # down products of many tiles
+    # many steps of weights: eight wavefronts a workgroup, at up to 5, 8 and 16 pairs an expert (odd groups too)
+    (12, 8, 3136, 1344, 2), (32, 8, 3200, 1344, 2), (36, 8, 3136, 1344, 2), (64, 8, 3200, 1408, 2),
+    (20, 2, 64, 3136, 1), (33, 3, 64, 3200, 3), (20, 4, 64, 3200, 2),
     (128, 4, 64, 64, 4), (300, 2, 64, 64, 2), (1, 32, 128, 64, 32),   # as many choices as experts
 ]
 

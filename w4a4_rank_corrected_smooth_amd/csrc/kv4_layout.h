@@ -8,18 +8,19 @@ namespace svdq {
 
 // Wavefronts a SIMD (workgroups a CU) that the attention kernel is built for,
 // by head_dim and rows: what its registers allow.  At D = 128 with up to 8 rows
-// 524k tokens of 8 heads took 74.1, 73.5 and 74.8 us with 2, 3 and 4, 48 ragged
-// sequences 28.4, 27.6 and 28.6; at D = 256 with 8 rows 16 x 16000 tokens of 8
-// heads took 105 us with 1 and 101 with 2; with 32 rows 16 x 4000 took 57 and 71.
+// 524k tokens of 8 heads take 74.0, 73.8 and 85.8 us with 2, 3 and 4 (128 registers,
+// some of them spilled), 48 ragged sequences 27.1, 26.0 and 31.8; at D = 64, 3 and 4
+// are alike; at D = 256 with 8 rows 16 x 16000 tokens of 8 heads take 106 us with 1
+// and 101 with 2, with 32 rows 16 x 4000 tokens 57 and 71.
 constexpr int kv4_waves(int D, int rows) {
   return D == 64 ? (rows <= 16 ? 4 : 2) : D == 128 ? (rows <= 16 ? 3 : 2) : rows <= 16 ? 2 : 1;
 }
 // Workgroups of an attention call at most (256 CUs), which sizes its workspace.
 constexpr int kKv4Groups = 256 * 4;
 // Tokens that a workgroup takes at a time, and the cost of beginning and ending
-// a (sequence, head), in such chunks (1, 2, 3, 4, 6: 48 ragged sequences took
-// 31.5, 26.4, 26.9, 26.9 and 33 us, 16 sequences of 5 new tokens 16.2, 15.0,
-// 15.5, 15.4 and 16.9).
+// a (sequence, head), in such chunks (with 1, 2, 3 and 4, 48 ragged sequences
+// take 28.2, 26.0, 26.5 and 26.5 us, 16 sequences of 5 new tokens 15.6, 14.9,
+// 15.5 and 15.4).
 constexpr int kKv4Chunk = 128;
 constexpr int kKv4Start = 2;
 // Rows (new tokens times query heads of one key/value head) at most.

@@ -499,8 +499,8 @@ __device__ __forceinline__ v8bf ones() { return as_v8bf(make_uint4(0x3F803F80u, 
 // One expert's product for a block of rows, the form both products share.
 //
 // Work of a wavefront: TILES tiles of 16 output columns over one of KS equal
-// parts of the input channels; a workgroup's kWaves wavefronts are KS parts
-// of kWaves / KS neighbouring sets of tiles.  A step is a pair of groups of
+// parts of the input channels; a workgroup's WAVES wavefronts are KS parts
+// of WAVES / KS neighbouring sets of tiles.  A step is a pair of groups of
 // 64 channels.
 // Weights: each wavefront streams its tiles from memory into a ring of RING
 // steps of registers; a step's place is filled anew as soon as it is used up.
@@ -513,22 +513,20 @@ __device__ __forceinline__ v8bf ones() { return as_v8bf(make_uint4(0x3F803F80u, 
 // 2: two pieces, 16 R rows, a product of each; 3: two pieces, 8 R rows, the second
 // pieces in the tile's upper eight rows, so that one product takes both (and
 // the two halves of the sums are added at the end).
-// A row's chunk is kWaves x 16 pieces of 16 bytes, 16 for each (part, step,
+// A row's chunk is WAVES x 16 pieces of 16 bytes, 16 for each (part, step,
 // piece); 16-byte piece p of tile row r is at place p ^ (r % 16) of its 16, so
 // that the operand reads, one row a lane, fall on different banks.
 // Every load is unconditional: past the end a wavefront reads its last step
 // again, and rows past the last repeat it.
-constexpr int kWaves = 4;       // (8: 99 us against 92 for 128 tokens, 52.6 against 57 for 40)
-
-template <int TILES, int FORM, int KS, int R>
+template <int TILES, int FORM, int KS, int R, int WAVES>
 struct Product {
   static constexpr int PIECES = FORM == 2 ? 2 : 1;       // products of a tile row
   static constexpr int ROWS = (FORM == 3 ? 8 : 16) * R;  // rows of a block
-  static constexpr int CHUNK = kWaves / (KS * PIECES), RING = TILES <= 2 ? 4 : 2;
+  static constexpr int CHUNK = WAVES / (KS * PIECES), RING = TILES <= 2 ? 4 : 2;
   static constexpr int UNROLL = CHUNK > RING ? CHUNK : RING;
   static_assert(CHUNK >= 1 && UNROLL % CHUNK == 0 && UNROLL % RING == 0, "whole chunks and rings");
-  static constexpr int ROW_BYTES = kWaves * 256, BUFFER = 16 * R * ROW_BYTES, LDS_BYTES = 2 * BUFFER;
-  static constexpr int WPR = kWaves / 4;              // wavefronts that fetch a row
+  static constexpr int ROW_BYTES = WAVES * 256, BUFFER = 16 * R * ROW_BYTES, LDS_BYTES = 2 * BUFFER;
+  static constexpr int WPR = WAVES / 4;              // wavefronts that fetch a row
 
   // (addresses are kept as a base that the wavefront shares, in scalar
   // registers, and a lane's own 32-bit offset)
@@ -662,14 +660,14 @@ __device__ __forceinline__ void meet(v4f (&acc)[N], uint8_t *lds, int w, int lan
 }
 
 // h = act(gate) * up of 16 columns a wavefront (tiles: the gate's and the up's).
-template <bool F16, bool GELU, int KS, int R, bool PLAN>
-__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_kernel(MoeArgs a) {
-  typedef Product<2, 1, KS, R> Pr;
+template <bool F16, bool GELU, int KS, int R, bool PLAN, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_kernel(MoeArgs a) {
+  typedef Product<2, 1, KS, R, WAVES> Pr;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Pr::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Rows<PLAN> rows;
   if (!rows.find(a, blockIdx.y, lane)) return;
-  const int n = a.I / kAwqTile, tile = blockIdx.x * (kWaves / KS) + w / KS;
+  const int n = a.I / kAwqTile, tile = blockIdx.x * (WAVES / KS) + w / KS;
   Pr pr;
   const int tiles[2] = {min(tile, n - 1), min(tile, n - 1) + n};
   pr.init(a.gate_up + rows.expert * a.gate_up_stride, MoeWeightLayout(2 * (int64_t)a.I, a.K), tiles, w);
@@ -710,14 +708,14 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2))
 
 // TILES tiles of 16 columns of h Down^T a wavefront; h enters as its two bf16
 // pieces (h to 2^-17, in float32's range).
-template <int TILES, int FORM, int KS, int R, bool PLAN>
-__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2))) void moe_down_kernel(MoeArgs a) {
-  typedef Product<TILES, FORM, KS, R> Pr;
+template <int TILES, int FORM, int KS, int R, bool PLAN, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2))) void moe_down_kernel(MoeArgs a) {
+  typedef Product<TILES, FORM, KS, R, WAVES> Pr;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Pr::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Rows<PLAN> rows;
   if (!rows.find(a, blockIdx.y, lane)) return;
-  const int n = a.K / kAwqTile, tile0 = (blockIdx.x * (kWaves / KS) + w / KS) * TILES;
+  const int n = a.K / kAwqTile, tile0 = (blockIdx.x * (WAVES / KS) + w / KS) * TILES;
   Pr pr;
   int tiles[TILES];
 #pragma unroll
@@ -1147,34 +1145,47 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   const bool few = (int64_t)slots * gt < 640, few_down = (int64_t)slots * dt < 4096;
   const bool plan = pairs > 64 || many;
   if (plan) hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
-#define MOE_GU(F, A, KS, R, P)                                                                                   \
-  hipLaunchKernelGGL((moe_gate_up_kernel<F, A, KS, R, P>),                                                       \
-                     dim3((gt + kWaves / KS - 1) / (kWaves / KS), (unsigned)slots), dim3(kWaves * 64), 0, stream, a)
-#define MOE_GU_R(F, A, KS)                          \
+  // Wavefronts a workgroup: eight share a row's chunk, twice as long, where a
+  // product has many steps and few tiles; with more tiles, or few steps, smaller
+  // workgroups fill the machine more evenly.  Layer of 8 experts of 4096 x 3584
+  // (1792 tiles of gate and up): 52.7 us with eight, 55.4 with four; of 32 experts
+  // of 4096 x 1536 (3072 tiles) 72.9 and 62.3; gate and up of 16 steps 51.7 and 47.3.
+  const bool large_gate = w->K >= 24 * 2 * kGroup && (int64_t)slots * gt < 2560;
+  const bool large_down = w->I >= 24 * 2 * kGroup && few_down;
+#define MOE_GU(F, A, KS, R, P, W)                                                                                \
+  hipLaunchKernelGGL((moe_gate_up_kernel<F, A, KS, R, P, W>), dim3((gt + W / KS - 1) / (W / KS), (unsigned)slots), \
+                     dim3(W * 64), 0, stream, a)
+#define MOE_GU_R(F, A, KS, W)                       \
   do {                                              \
-    if (many) MOE_GU(F, A, KS, 2, true);            \
-    else if (plan) MOE_GU(F, A, KS, 1, true);       \
-    else MOE_GU(F, A, KS, 1, false);                \
+    if (many) MOE_GU(F, A, KS, 2, true, W);         \
+    else if (plan) MOE_GU(F, A, KS, 1, true, W);    \
+    else MOE_GU(F, A, KS, 1, false, W);             \
   } while (0)
-#define MOE_GU_K(F, A) do { if (few) MOE_GU_R(F, A, 4); else MOE_GU_R(F, A, 1); } while (0)
-#define MOE_DN(TT, FM, KS, R, P)                                                                                 \
-  hipLaunchKernelGGL((moe_down_kernel<TT, FM, KS, R, P>),                                                        \
-                     dim3((dt + TT * (kWaves / KS) - 1) / (TT * (kWaves / KS)), (unsigned)slots),                \
-                     dim3(kWaves * 64), 0, stream, a)
-#define MOE_DN_R(TT, KS)                            \
+#define MOE_GU_K(F, A)                              \
   do {                                              \
-    if (many) MOE_DN(TT, 2, KS, 2, true);           \
-    else if (packed && plan) MOE_DN(TT, 3, KS, 1, true);  \
-    else if (packed) MOE_DN(TT, 3, KS, 1, false);   \
-    else if (plan) MOE_DN(TT, 2, KS, 1, true);      \
-    else MOE_DN(TT, 2, KS, 1, false);               \
+    if (few) MOE_GU_R(F, A, 4, 4);                  \
+    else if (large_gate) MOE_GU_R(F, A, 1, 8);       \
+    else MOE_GU_R(F, A, 1, 4);                      \
+  } while (0)
+#define MOE_DN(TT, FM, KS, R, P, W)                                                                              \
+  hipLaunchKernelGGL((moe_down_kernel<TT, FM, KS, R, P, W>),                                                     \
+                     dim3((dt + TT * (W / KS) - 1) / (TT * (W / KS)), (unsigned)slots), dim3(W * 64), 0, stream, a)
+#define MOE_DN_R(TT, KS, W)                                  \
+  do {                                                       \
+    if (many) MOE_DN(TT, 2, KS, 2, true, W);                 \
+    else if (packed && plan) MOE_DN(TT, 3, KS, 1, true, W);  \
+    else if (packed) MOE_DN(TT, 3, KS, 1, false, W);         \
+    else if (plan) MOE_DN(TT, 2, KS, 1, true, W);            \
+    else MOE_DN(TT, 2, KS, 1, false, W);                     \
   } while (0)
   if (dtype == SVDQ_FP16) {
     if (gelu) MOE_GU_K(true, true); else MOE_GU_K(true, false);
   } else {
     if (gelu) MOE_GU_K(false, true); else MOE_GU_K(false, false);
   }
-  if (few_down) MOE_DN_R(2, 2); else MOE_DN_R(4, 1);
+  if (large_down) MOE_DN_R(2, 2, 8);
+  else if (few_down) MOE_DN_R(2, 2, 4);
+  else MOE_DN_R(4, 1, 4);
 #undef MOE_DN_R
 #undef MOE_DN
 #undef MOE_GU_K
