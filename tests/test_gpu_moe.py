@@ -145,6 +145,7 @@ def test_packing_on_the_device(S, E, N, K):
 SPLITS = [
     # T, E, K, I, k
     (16, 20, 64, 128, 1), (8, 16, 64, 1152, 2),       # 16 pairs: few steps, and too many for the small form
+    (8, 6, 64, 1152, 2), (16, 8, 4160, 192, 1), (16, 9, 64, 64, 1),         # ... taken, in two turns, and too many experts
     (10, 8, 320, 192, 2), (20, 16, 64, 704, 2),       # up to 5 pairs an expert, at most 64: few tiles, many tiles
     (40, 64, 192, 64, 3), (40, 64, 64, 256, 2),       # the same above 64 pairs
     (64, 16, 128, 704, 2), (32, 4, 448, 64, 1),       # 8 pairs an expert: above 64 pairs, and not
@@ -170,6 +171,27 @@ def test_expert_layer_splits(S, case):
     ids[::7, -1] = -1
     wt = torch.from_numpy(r.random((T, k)) + 0.05).float().cuda()
     check(S.awq_moe_forward(layer, x, ids, wt, activation=act), x, parts, ids, wt, act)
+
+
+@pytest.mark.parametrize("I", [1344, 1408])
+def test_expert_layer_of_many_steps_and_tiles(S, I):
+    """20 experts of over 24 steps and 1536 tiles.  They are two experts' matrices in
+    turn and the tokens six rows in turn, so that six rows' oracle checks all."""
+    r = np.random.default_rng(I)
+    E, K, k = 20, 3136 if I == 1344 else 3200, 2
+    parts = [tuple(np.ascontiguousarray(a[np.arange(E) % 2]) for a in p) for p in experts(r, 2, K, I)]
+    layer = device_layer(S, parts)
+    six = torch.from_numpy(r.standard_normal((6, K))).cuda()
+    kinds, six_wt = r.integers(0, 2, (6, k)), torch.from_numpy(r.random((6, k)) + 0.05).float().cuda()
+    for T, dtype, act in ((24, "bf16", "gelu"), (24, "fp16", "silu"), (70, "fp16", "gelu"), (70, "bf16", "silu"),
+                          (130, "bf16", "silu"), (131, "fp16", "silu")):
+        announce(f"{E} experts of {K} x {I}: T={T} {act} {dtype}")
+        turn = np.arange(T) % 6
+        x, wt = six.to(DT[dtype])[turn], six_wt[turn]
+        ids = torch.from_numpy((kinds[turn] + 2 * r.integers(0, E // 2, (T, k))).astype(np.int32)).cuda()
+        got = S.awq_moe_forward(layer, x, ids, wt, activation=act)
+        check(got[:6], x[:6], parts, ids[:6], wt[:6], act)
+        assert torch.equal(got, got[:6][turn])
 
 
 def test_expert_layer_all_tokens_to_one_expert(S):

@@ -769,17 +769,22 @@ __global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2)))
 }
 
 // ------------------------------------------------- a handful of pairs
-// A step of one or two sequences: up to kMoeFewPairs (token, choice) pairs, and at
-// most kFewSteps steps of weights for a column tile of the down product.  The
-// layer is two kernels and all latency: each wavefront holds all its loads in
-// flight, rows come straight into operands (there are few, so they share
-// lines), and the down product's workgroups own their columns of y, so the
-// sum over the choices needs no kernel of its own.  One token with 8 of 64
-// experts of 2048 x 768: 15.4 us against 22 in the form above (21 MB of weights,
-// 3.4 us at the rate of a long read; the two kernels' launches and the chain
-// ids, rows and weights, product, meeting make up the rest); 8 tokens with 2 of 8
-// experts of 4096 x 3584 (224 steps): 67 us against 57.
-constexpr int kFewSteps = 128;
+// A step of one or two sequences: up to kMoeFewPairs (token, choice) pairs of up
+// to kFewExperts experts.  The layer is two kernels and all latency: each
+// wavefront holds all its loads in flight, rows come straight into operands
+// (there are few, so they share lines), and the down product's workgroups own
+// their columns of y, so the sum over the choices needs no kernel of its own.
+// One token with 8 of 64 experts of 2048 x 768: 15.4 us against 17.0 in the form
+// above (21 MB of weights, 3.4 us at the rate of a long read; the two kernels'
+// launches and the chain ids, rows and weights, product, meeting make up the rest).
+// A workgroup's weights of down are (experts) x I / 128 steps, and every 256
+// column tiles are a turn of the machine's CUs; at most kFewSteps steps in all
+// turns: 64 steps (2 experts of 4096 x 4096) 21.4 against 29.5, 128 (8 of 2048 x
+// 2048) 25.9 and 23.6, 224 (8 of 4096 x 3584) 64 and 44; two turns of 64 (4 of
+// 7168 x 2048) 38.6 and 33.7.  With more experts the other form's workgroups
+// are enough: 12 tokens with one of 32 experts of 2048 x 512 17.2 and 16.1, 8 with
+// one of 64 of 2048 x 768 15.3 and 16.3.
+constexpr int kFewSteps = 64, kFewExperts = 8;
 constexpr int kFewGateParts = 4, kFewDownWaves = 8;     // wavefronts a workgroup (8 and 16: 19.9 and 16.6 us)
 template <int TILES>
 struct FewWeights {
@@ -1114,7 +1119,8 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   const int pairs = T * top_k, slots = pairs < w->E ? pairs : w->E;       // experts in use at most
   const int gt = w->I / kAwqTile, dt = w->K / kAwqTile;
   const bool gelu = act == SVDQ_MOE_GELU_TANH;
-  if (pairs <= kMoeFewPairs && slots * ((w->I + 127) / 128) <= kFewSteps) {
+  const int64_t few_steps = (int64_t)slots * ((w->I + 127) / 128) * ((dt + 255) / 256);
+  if (pairs <= kMoeFewPairs && slots <= kFewExperts && few_steps <= kFewSteps) {
 #define MOE_FEW(F, A)                                                                                            \
   hipLaunchKernelGGL((moe_gate_up_few_kernel<F, A, kFewGateParts>), dim3((unsigned)gt, (unsigned)slots),         \
                      dim3(kFewGateParts * 64), 0, stream, a)
@@ -1140,17 +1146,23 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   const bool packed = pairs <= 5 * slots;
   // Few tiles: K in parts for the wavefronts of a workgroup.  With 256 and 512
   // tiles of gate and up 16.2 and 26.5 us in four parts, 20.2 and 31.5 in one;
-  // with 768, 28.4 and 27.5.  Down: 1024 and 2048 tiles 14.6 and 28.4 us as two
-  // parts of two tiles, 17.0 and 29.2 as four tiles; with 16384, 107 and 92.
-  const bool few = (int64_t)slots * gt < 640, few_down = (int64_t)slots * dt < 4096;
+  // layers with 768 tiles 29.6 us in two parts (24.3 and 26.1 with 1024), 36.8 in
+  // one (24.7, 26.9), 29.7 in four (28.8, 30.9); with 1280 tiles of 32 steps 51.9
+  // in two, 55.1 in one, 57.6 in four; with 1792, 59.1, 55.5 and 67.3.
+  // Down: 1024 and 2048 tiles 14.6 and 28.4 us as two parts of two tiles, 17.0
+  // and 29.2 as four tiles; with 16384, 107 and 92.
+  const int64_t gate_tiles = (int64_t)slots * gt;
+  const int gate_parts = gate_tiles < 640 ? 4 : gate_tiles < 1536 ? 2 : 1;
+  const bool few_down = (int64_t)slots * dt < 4096;
   const bool plan = pairs > 64 || many;
   if (plan) hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
   // Wavefronts a workgroup: eight share a row's chunk, twice as long, where a
   // product has many steps and few tiles; with more tiles, or few steps, smaller
   // workgroups fill the machine more evenly.  Layer of 8 experts of 4096 x 3584
   // (1792 tiles of gate and up): 52.7 us with eight, 55.4 with four; of 32 experts
-  // of 4096 x 1536 (3072 tiles) 72.9 and 62.3; gate and up of 16 steps 51.7 and 47.3.
-  const bool large_gate = w->K >= 24 * 2 * kGroup && (int64_t)slots * gt < 2560;
+  // of 4096 x 1536 72.9 and 62.3; gate and up of 16 steps 51.7 and 47.3; down of 20
+  // steps 50.9 and 46.0.
+  const bool large_gate = w->K >= 24 * 2 * kGroup && gate_tiles < 2560;
   const bool large_down = w->I >= 24 * 2 * kGroup && few_down;
 #define MOE_GU(F, A, KS, R, P, W)                                                                                \
   hipLaunchKernelGGL((moe_gate_up_kernel<F, A, KS, R, P, W>), dim3((gt + W / KS - 1) / (W / KS), (unsigned)slots), \
@@ -1163,8 +1175,9 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   } while (0)
 #define MOE_GU_K(F, A)                              \
   do {                                              \
-    if (few) MOE_GU_R(F, A, 4, 4);                  \
-    else if (large_gate) MOE_GU_R(F, A, 1, 8);       \
+    if (gate_parts == 4) MOE_GU_R(F, A, 4, 4);      \
+    else if (gate_parts == 2) MOE_GU_R(F, A, 2, 4); \
+    else if (large_gate) MOE_GU_R(F, A, 1, 8);      \
     else MOE_GU_R(F, A, 1, 4);                      \
   } while (0)
 #define MOE_DN(TT, FM, KS, R, P, W)                                                                              \
