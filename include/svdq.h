@@ -434,11 +434,13 @@ svdq_status_t svdq_kv4_read(const svdq_kv4_cache_t *cache, const int32_t *slots,
  * head_dim] of the same type, dense.  page_table [B, table_width] and
  * seq_lens [B] are int32 device arrays; a length past the table's end counts
  * up to it and a negative one as 0, and a page outside the cache hides its
- * tokens.  B <= 65536, Hq a multiple of kv_heads, Q g <= 1024, B Q Hq <= 2^24.
+ * tokens.  B <= 65536, Hq a multiple of kv_heads, Q g <= 1024, B Q Hq <= 2^24,
+ * |scale| < 2^127.
  * Scores, softmax statistics and sums are float32; the weights p enter the
  * product with 16 significant bits.  The result does not depend on the
  * order in which workgroups run.  Two kernels; the workspace needs no
- * clearing and keeps nothing from one call for the next. */
+ * clearing and keeps nothing from one call for the next (calls that run at the
+ * same time need one each). */
 size_t svdq_kv4_attention_workspace_bytes(int B, int Q, int Hq, int kv_heads, int head_dim);
 svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, int64_t q_batch, int64_t q_token,
                                  int64_t q_head, svdq_dtype_t dtype, int B, int Q, int Hq,
@@ -490,7 +492,8 @@ typedef enum { SVDQ_MOE_SILU = 0, SVDQ_MOE_GELU_TANH = 1 } svdq_moe_act_t;
  * x [T, K] and w_router [E, K] are bf16 or fp16 (device, 16-byte aligned), bias
  * [E] float32 or NULL.  Logits and scores are float64, so the choice does not
  * hang on the order of a sum.  E <= 1024, K a multiple of 8 up to 2^20,
- * top_k <= min(E, 32), T <= 65535.  Two kernels. */
+ * top_k <= min(E, 32), T <= 65535.  Two kernels, with the logits in the
+ * workspace (calls that run at the same time need one each). */
 size_t svdq_moe_route_workspace_bytes(int T, int E);
 svdq_status_t svdq_moe_route(const void *x, const void *w_router, const float *bias, svdq_dtype_t dtype, int T, int E,
                              int K, int top_k, svdq_moe_score_t score, int normalize, int32_t *ids, float *weights,
@@ -531,8 +534,9 @@ typedef struct {
  * A row of x that is not finite gives a row of y that is not, and touches no
  * other; which tokens share a call changes the order of float32 sums only.
  * E <= 1024, K and I multiples of 64 with 2 I K <= 2^31, T top_k <= 4096.
- * Each expert that some token names is read once per 16 of its rows.  The
- * workspace needs no clearing and keeps nothing from one call for the next. */
+ * Each expert that some token names is read once per 16 or 32 of its rows.  The
+ * workspace needs no clearing and keeps nothing from one call for the next
+ * (calls that run at the same time need one each). */
 size_t awq_moe_workspace_bytes(int T, int top_k, int K, int I);
 svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dtype_t dtype, int T, const int32_t *ids,
                               const float *weights, int top_k, svdq_moe_act_t act, void *y, void *workspace,

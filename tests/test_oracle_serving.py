@@ -121,6 +121,7 @@ def test_cache_argument_errors():
     assert attend(ws=0) == INV and attend(q=FAKE + 2) == INV and attend(out=FAKE + 8) == INV and attend(table=FAKE + 2) == INV
     assert attend(qs=(1024, 1024, 100)) == INV and attend(dt=S.FP32) == INV
     assert attend(scale=float("nan")) == INV and attend(scale=float("inf")) == INV
+    assert attend(scale=2.0 ** 127) == INV and attend(scale=-(2.0 ** 127)) == INV
     assert attend(width=0) == SHAPE and attend(Hq=7) == SHAPE and attend(Q=0) == SHAPE and attend(B=-1) == SHAPE
     assert attend(n=need - 1) == WS and attend(B=0) == 0
 

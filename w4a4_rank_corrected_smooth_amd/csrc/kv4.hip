@@ -279,7 +279,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(const uint8_t *__restrict
 // into chunks of 128 (32 for each wavefront at a time); all chunks of the
 // call form one line, of which each workgroup takes an equal piece, so short
 // and long sequences share the machine evenly.  Beginning and ending a
-// (sequence, head) takes about as long as kStart chunks, which stand on the
+// (sequence, head) takes about as long as kKv4Start chunks, which stand on the
 // line before its first one.  A workgroup that holds all chunks of a
 // (sequence, head) writes the output, otherwise its running state, which
 // kv4_join_kernel joins in order.
@@ -298,7 +298,6 @@ struct AttendArgs {
   float *part;                  // [2 W][block_rows][D], then [2 W][block_rows][2]
   int W;
 };
-
 
 __device__ __forceinline__ int seq_len(const AttendArgs &a, int b) {
   return min(max(a.lens[b], 0), (int)min((int64_t)a.width << a.L.page_shift, (int64_t)1 << 30));
@@ -948,7 +947,8 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
       ((uintptr_t)seq_lens & 3u) || !strides_ok(strides, 3))
     return fail(SVDQ_ERR_INVALID_ARGUMENT,
                 "svdq_kv4_attention: misaligned pointer, or a stride that is not a multiple of 8");
-  if (!__builtin_isfinite(scale)) return fail(SVDQ_ERR_INVALID_ARGUMENT, "svdq_kv4_attention: scale is not finite");
+  if (!(fabsf(scale) < 0x1p127f))        // times log2(e) it is a float32 number
+    return fail(SVDQ_ERR_INVALID_ARGUMENT, "svdq_kv4_attention: scale is not a number below 2^127");
   const size_t need = svdq_kv4_attention_workspace_bytes(B, Q, Hq, L.H, L.D);
   if (ws_bytes < need)
     return fail(SVDQ_ERR_WORKSPACE_TOO_SMALL, "svdq_kv4_attention: workspace needs %zu bytes, got %zu", need, ws_bytes);
