@@ -173,25 +173,41 @@ def test_expert_layer_splits(S, case):
     check(S.awq_moe_forward(layer, x, ids, wt, activation=act), x, parts, ids, wt, act)
 
 
-@pytest.mark.parametrize("I", [1344, 1408])
-def test_expert_layer_of_many_steps_and_tiles(S, I):
-    """20 experts of over 24 steps and 1536 tiles.  They are two experts' matrices in
-    turn and the tokens six rows in turn, so that six rows' oracle checks all."""
-    r = np.random.default_rng(I)
-    E, K, k = 20, 3136 if I == 1344 else 3200, 2
-    parts = [tuple(np.ascontiguousarray(a[np.arange(E) % 2]) for a in p) for p in experts(r, 2, K, I)]
-    layer = device_layer(S, parts)
-    six = torch.from_numpy(r.standard_normal((6, K))).cuda()
-    kinds, six_wt = r.integers(0, 2, (6, k)), torch.from_numpy(r.random((6, k)) + 0.05).float().cuda()
-    for T, dtype, act in ((24, "bf16", "gelu"), (24, "fp16", "silu"), (70, "fp16", "gelu"), (70, "bf16", "silu"),
-                          (130, "bf16", "silu"), (131, "fp16", "silu")):
-        announce(f"{E} experts of {K} x {I}: T={T} {act} {dtype}")
-        turn = np.arange(T) % 6
-        x, wt = six.to(DT[dtype])[turn], six_wt[turn]
-        ids = torch.from_numpy((kinds[turn] + 2 * r.integers(0, E // 2, (T, k))).astype(np.int32)).cuda()
-        got = S.awq_moe_forward(layer, x, ids, wt, activation=act)
-        check(got[:6], x[:6], parts, ids[:6], wt[:6], act)
-        assert torch.equal(got, got[:6][turn])
+# larger calls: the experts are two experts' matrices in turn and the tokens six rows in
+# turn, so that six rows' oracle checks all
+LARGE = [
+    # T, E, K, I, k: over 24 steps and 1536 tiles of gate and up, at 2, 7 and 13 pairs an expert
+    (24, 20, 3136, 1344, 2), (24, 20, 3200, 1408, 2), (70, 20, 3136, 1344, 2), (70, 20, 3200, 1408, 2),
+    (130, 20, 3136, 1344, 2), (131, 20, 3200, 1408, 2),
+    # over 1024 pairs: 16 and more an expert, 8, and 5
+    (300, 4, 64, 64, 4), (260, 64, 64, 192, 4), (260, 64, 3136, 384, 4), (260, 64, 64, 384, 4), (300, 4, 64, 3136, 4),
+    (260, 64, 1024, 64, 4), (130, 128, 64, 64, 8), (130, 128, 64, 128, 8), (130, 128, 3136, 192, 8),
+    (130, 128, 64, 192, 8), (130, 128, 64, 3136, 8), (130, 128, 512, 64, 8), (150, 256, 64, 64, 8),
+    (150, 256, 64, 3136, 8), (150, 256, 256, 64, 8),
+    (100, 20, 64, 1344, 3), (12, 4, 64, 3136, 1), (40, 16, 64, 3136, 2),    # at most 1024 pairs
+    # as many as a call takes, and 1024 of a kind
+    (128, 1024, 64, 64, 32), (4096, 3, 64, 64, 1), (1024, 1, 64, 64, 1), (32, 1024, 64, 64, 32),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LARGE)))
+def test_expert_layer_of_many_pairs_or_weights(S, case):
+    T, E, K, I, k = LARGE[case]
+    dtype, act = ("bf16", "fp16")[case % 2], ("silu", "gelu")[case // 2 % 2]
+    announce(f"experts large {case}: T={T} E={E} K={K} I={I} k={k} {act} {dtype}")
+    r = np.random.default_rng(200 + case)
+    two = min(E, 2)
+    parts = experts(r, two, K, I)
+    turns = torch.arange(E, device="cuda") % two
+    layer = S.AwqMoe(*(tuple(torch.from_numpy(t).cuda()[turns] for t in (awq.pack(q), s, z)) for q, s, z in parts))
+    turn = np.arange(T) % 6
+    x = torch.from_numpy(r.standard_normal((6, K))).to(DT[dtype]).cuda()[turn]
+    kinds = r.integers(0, two, (6, k))[turn]
+    ids = torch.from_numpy((kinds + two * r.integers(0, E // two, (T, k))).astype(np.int32)).cuda()
+    wt = torch.from_numpy(r.random((6, k)) + 0.05).float().cuda()[turn]
+    got = S.awq_moe_forward(layer, x, ids, wt, activation=act)
+    check(got[:6], x[:6], parts, ids[:6] % two, wt[:6], act)
+    assert torch.equal(got, got[:6][turn])
 
 
 def test_expert_layer_all_tokens_to_one_expert(S):

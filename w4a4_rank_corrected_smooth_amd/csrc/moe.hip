@@ -4,6 +4,7 @@
 //  moe_pack_kernel     weights to the experts' blobs, on the device
 //  moe_logits_kernel   x w^T in float64
 //  moe_choose_kernel   scores, the best top_k of each token, their weights
+//  moe_plan_kernel     the pairs of many, sorted by expert
 //  moe_gate_up_kernel  h = act(x Gate^T) * (x Up^T) of every (token, expert)
 //  moe_down_kernel     h Down^T of every (token, expert)
 //  moe_sum_kernel      the weighted sum over a token's experts
@@ -212,6 +213,16 @@ __device__ __forceinline__ double wave_sum(double x) {
   x = add_dpp<0x143, 0xC>(x);
   return lane_f64(x, 63);
 }
+// sum of x over lanes 0..lane
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+  return x;
+}
 // A number's place in the order of numbers, as an unsigned integer; NaN is the
 // smallest, and the two zeros are equal.
 __device__ __forceinline__ uint64_t order_of(double x) {
@@ -316,9 +327,9 @@ __global__ __launch_bounds__(64) void moe_choose_kernel(const double *__restrict
 // h = act(gate) up goes on as two bf16 pieces, which hold it to 2^-17 in
 // float32's range (an fp16 h would overflow where y does not).
 // What bounds it: the experts' bytes, each read once.  128 tokens with 8 of 128
-// experts of 2048 x 768 (341 MB) take 86 us: gate and up 47 (227 MB, 4.8 TB/s; the
+// experts of 2048 x 768 (341 MB) take 84 us: gate and up 47 (227 MB, 4.8 TB/s; the
 // weights' stream alone 41, the products alone 28), down 33 (113 MB; 24 and 20),
-// the plan and the sum 3 and 4.
+// the sum 4.
 struct MoeArgs {
   const uint8_t *gate_up, *down;      // E blobs each, one after another
   int64_t gate_up_stride, down_stride;
@@ -329,55 +340,125 @@ struct MoeArgs {
   const float *weights;
   uint16_t *h;                        // [T top_k][I / 64][2][64] bf16: h = first piece + second
   float *part;                        // [T top_k][K]
-  MoePlan *plan;                      // above 64 pairs
+  MoePlan *plan;                      // above kLocalPairs pairs
   uint16_t *y;
 };
 
-// The rows of one expert, for a wavefront: its (token, choice) pairs.  Their
-// order does not matter: a row of a matrix product does not depend on where
-// it stands.  Up to 64 pairs every wavefront finds them for itself, in
-// registers; above, moe_plan_kernel has sorted them.
-template <bool PLAN>
-struct Rows {
+// The rows of one expert are its (token, choice) pairs.  Their order does not
+// matter: a row of a matrix product does not depend on where it stands.
+
+// Up to 64 pairs, for a wavefront by itself, in registers.
+struct WaveRows {
   int expert = -1, count = 0;
-  int list = 0;                 // !PLAN: lane r holds the pair of row r
-  const uint16_t *sorted = nullptr;
+  int list = 0;                 // lane r holds the pair of row r
 
   // the `slot`-th expert that the ids name; false where there are fewer
   __device__ __forceinline__ bool find(const MoeArgs &a, int slot, int lane) {
-    if constexpr (PLAN) {
-      if (slot >= a.plan->slots) return false;
-      expert = __builtin_amdgcn_readfirstlane(a.plan->expert[slot]);
-      const int first = __builtin_amdgcn_readfirstlane(a.plan->first[slot]);
-      count = __builtin_amdgcn_readfirstlane(a.plan->first[slot + 1]) - first;
-      sorted = a.plan->pairs + first;
-    } else {
-      const int n = a.T * a.top_k;
-      const int id = lane < n ? a.ids[lane] : -1;
-      uint64_t left = __ballot(id >= 0 && id < a.E), same = 0;
-      do {
-        if (left == 0) return false;
-        expert = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        same = __ballot(id == expert);
-        left &= ~same;
-      } while (slot-- > 0);
-      count = __builtin_popcountll(same);
-      // lane i of the set goes to the lane of its rank; the others to the end
-      const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
-      const bool in = same >> lane & 1;
-      list = __builtin_amdgcn_ds_permute(4 * (in ? rank : 63 - (lane - rank)), lane);
-    }
+    const int n = a.T * a.top_k;
+    const int id = lane < n ? a.ids[lane] : -1;
+    uint64_t left = __ballot(id >= 0 && id < a.E), same = 0;
+    do {
+      if (left == 0) return false;
+      expert = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+      same = __ballot(id == expert);
+      left &= ~same;
+    } while (slot-- > 0);
+    count = __builtin_popcountll(same);
+    // lane i of the set goes to the lane of its rank; the others to the end
+    const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
+    const bool in = same >> lane & 1;
+    list = __builtin_amdgcn_ds_permute(4 * (in ? rank : 63 - (lane - rank)), lane);
     return true;
   }
-  __device__ __forceinline__ int one(int r) const {       // the same r in all lanes
-    if constexpr (PLAN) return __builtin_amdgcn_readfirstlane(sorted[r]);
-    else return __builtin_amdgcn_readlane(list, r);
-  }
-  __device__ __forceinline__ int pair(int r) const {      // r in [0, count), any in each lane
-    if constexpr (PLAN) return sorted[r];
-    else return __shfl(list, r);
-  }
+  __device__ __forceinline__ int pair(int r) const { return __shfl(list, r); }     // r in [0, count)
 };
+
+// Up to kLocalPairs pairs, for a workgroup by itself, in LDS: which experts the
+// ids name is a set of bits, of which the `slot`-th is this one's.  (A kernel
+// that sorts them once costs 3.5 us more: 56.0 against 52.5 for 72 pairs, 85.9
+// against 84.0 for 1024.)  Up to 64, each wavefront finds them as above and
+// writes the list itself, the same as the others do: no barrier, 1 us less.
+constexpr int kLocalPairs = 1024;
+template <int WAVES>
+struct LocalRows {
+  static constexpr int LDS_BYTES = 2 * kLocalPairs + MOE_MAX_EXPERTS / 8 + 16;
+  int expert = -1, count = 0;
+  const uint16_t *sorted = nullptr;
+
+  __device__ __forceinline__ bool find(const MoeArgs &a, int slot, uint8_t *lds, int lane) {
+    uint16_t *list = reinterpret_cast<uint16_t *>(lds);
+    uint32_t *named = reinterpret_cast<uint32_t *>(lds + 2 * kLocalPairs);
+    int *used = reinterpret_cast<int *>(named + MOE_MAX_EXPERTS / 32);
+    constexpr int EACH = kLocalPairs / (WAVES * 64), WORDS = MOE_MAX_EXPERTS / 32;
+    const int tid = threadIdx.x, n = a.T * a.top_k;
+    sorted = list;
+    if (n <= 64) {
+      WaveRows own;
+      if (!own.find(a, slot, lane)) return false;
+      expert = own.expert;
+      count = own.count;
+      if (lane < count) list[lane] = (uint16_t)own.list;
+      return true;
+    }
+    int id[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int p = WAVES * 64 * i + tid;
+      id[i] = p < n ? a.ids[p] : -1;
+    }
+    if (tid <= WORDS) (tid < WORDS ? (int *)named + tid : used)[0] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+      if (id[i] >= 0 && id[i] < a.E) atomicOr(&named[id[i] / 32], 1u << (id[i] % 32));
+    __syncthreads();
+    uint32_t word = lane < WORDS ? named[lane] : 0u;
+    const int own = __builtin_popcount(word);
+    const int upto = wave_scan(own);
+    const uint64_t past = __ballot(upto > slot);
+    if (past == 0) return false;
+    const int at = __builtin_ctzll(past);
+    uint32_t bits = __builtin_amdgcn_readlane((int)word, at);
+    for (int i = slot - (__builtin_amdgcn_readlane(upto, at) - __builtin_popcount(bits)); i > 0; --i) bits &= bits - 1;
+    expert = 32 * at + __builtin_ctz(bits);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const uint64_t in = __ballot(id[i] == expert);
+      if (in) {
+        int first = 0;
+        if (lane == 0) first = atomicAdd(used, __builtin_popcountll(in));
+        first = __builtin_amdgcn_readfirstlane(first);
+        if (in >> lane & 1) list[first + __builtin_popcountll(in & ((1ull << lane) - 1))] = (uint16_t)(WAVES * 64 * i + tid);
+      }
+    }
+    __syncthreads();
+    count = __builtin_amdgcn_readfirstlane(*used);
+    return true;
+  }
+  __device__ __forceinline__ int one(int r) const { return __builtin_amdgcn_readfirstlane(sorted[r]); }   // the same r in all lanes
+  __device__ __forceinline__ int pair(int r) const { return sorted[r]; }
+};
+
+// More: moe_plan_kernel has sorted them (a thread of the form above holds 4
+// ids; the kernel is 4 us of the 140 and more that such calls take).
+struct PlanRows {
+  static constexpr int LDS_BYTES = 16;
+  int expert = -1, count = 0;
+  const uint16_t *sorted = nullptr;
+
+  __device__ __forceinline__ bool find(const MoeArgs &a, int slot, uint8_t *, int) {
+    if (slot >= a.plan->slots) return false;
+    expert = __builtin_amdgcn_readfirstlane(a.plan->expert[slot]);
+    const int first = __builtin_amdgcn_readfirstlane(a.plan->first[slot]);
+    count = __builtin_amdgcn_readfirstlane(a.plan->first[slot + 1]) - first;
+    sorted = a.plan->pairs + first;
+    return true;
+  }
+  __device__ __forceinline__ int one(int r) const { return __builtin_amdgcn_readfirstlane(sorted[r]); }
+  __device__ __forceinline__ int pair(int r) const { return sorted[r]; }
+};
+template <bool PLAN, int WAVES> struct RowsOf { typedef LocalRows<WAVES> type; };
+template <int WAVES> struct RowsOf<true, WAVES> { typedef PlanRows type; };
 
 // Pairs sorted by expert.  One workgroup.
 __global__ __launch_bounds__(1024) void moe_plan_kernel(MoeArgs a) {
@@ -665,8 +746,10 @@ __global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2)))
   typedef Product<2, 1, KS, R, WAVES> Pr;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Pr::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  Rows<PLAN> rows;
-  if (!rows.find(a, blockIdx.y, lane)) return;
+  typedef typename RowsOf<PLAN, WAVES>::type Rows;
+  __shared__ __attribute__((aligned(16))) uint8_t plan[Rows::LDS_BYTES];
+  Rows rows;
+  if (!rows.find(a, blockIdx.y, plan, lane)) return;
   const int n = a.I / kAwqTile, tile = blockIdx.x * (WAVES / KS) + w / KS;
   Pr pr;
   const int tiles[2] = {min(tile, n - 1), min(tile, n - 1) + n};
@@ -713,8 +796,10 @@ __global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2)))
   typedef Product<TILES, FORM, KS, R, WAVES> Pr;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Pr::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  Rows<PLAN> rows;
-  if (!rows.find(a, blockIdx.y, lane)) return;
+  typedef typename RowsOf<PLAN, WAVES>::type Rows;
+  __shared__ __attribute__((aligned(16))) uint8_t plan[Rows::LDS_BYTES];
+  Rows rows;
+  if (!rows.find(a, blockIdx.y, plan, lane)) return;
   const int n = a.K / kAwqTile, tile0 = (blockIdx.x * (WAVES / KS) + w / KS) * TILES;
   Pr pr;
   int tiles[TILES];
@@ -816,7 +901,7 @@ template <bool F16, bool GELU, int KS>
 __global__ __launch_bounds__(KS * 64) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_few_kernel(MoeArgs a) {
   __shared__ v4f red[KS][2][64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  Rows<false> rows;
+  WaveRows rows;
   if (!rows.find(a, blockIdx.y, lane)) return;
   const int n = a.I / kAwqTile, tile = blockIdx.x;
   const MoeWeightLayout L(2 * (int64_t)a.I, a.K);
@@ -1154,7 +1239,7 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   const int64_t gate_tiles = (int64_t)slots * gt;
   const int gate_parts = gate_tiles < 640 ? 4 : gate_tiles < 1536 ? 2 : 1;
   const bool few_down = (int64_t)slots * dt < 4096;
-  const bool plan = pairs > 64 || many;
+  const bool plan = pairs > kLocalPairs;
   if (plan) hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
   // Wavefronts a workgroup: eight share a row's chunk, twice as long, where a
   // product has many steps and few tiles; with more tiles, or few steps, smaller
@@ -1169,7 +1254,8 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
                      dim3(W * 64), 0, stream, a)
 #define MOE_GU_R(F, A, KS, W)                       \
   do {                                              \
-    if (many) MOE_GU(F, A, KS, 2, true, W);         \
+    if (many && plan) MOE_GU(F, A, KS, 2, true, W); \
+    else if (many) MOE_GU(F, A, KS, 2, false, W);   \
     else if (plan) MOE_GU(F, A, KS, 1, true, W);    \
     else MOE_GU(F, A, KS, 1, false, W);             \
   } while (0)
@@ -1185,7 +1271,8 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
                      dim3((dt + TT * (W / KS) - 1) / (TT * (W / KS)), (unsigned)slots), dim3(W * 64), 0, stream, a)
 #define MOE_DN_R(TT, KS, W)                                  \
   do {                                                       \
-    if (many) MOE_DN(TT, 2, KS, 2, true, W);                 \
+    if (many && plan) MOE_DN(TT, 2, KS, 2, true, W);         \
+    else if (many) MOE_DN(TT, 2, KS, 2, false, W);           \
     else if (packed && plan) MOE_DN(TT, 3, KS, 1, true, W);  \
     else if (packed) MOE_DN(TT, 3, KS, 1, false, W);         \
     else if (plan) MOE_DN(TT, 2, KS, 1, true, W);            \
