@@ -492,8 +492,8 @@ typedef enum { SVDQ_MOE_SILU = 0, SVDQ_MOE_GELU_TANH = 1 } svdq_moe_act_t;
  * x [T, K] and w_router [E, K] are bf16 or fp16 (device, 16-byte aligned), bias
  * [E] float32 or NULL.  Logits and scores are float64, so the choice does not
  * hang on the order of a sum.  E <= 1024, K a multiple of 8 up to 2^20,
- * top_k <= min(E, 32), T <= 65535.  Two kernels, with the logits in the
- * workspace (calls that run at the same time need one each). */
+ * top_k <= min(E, 32), T <= 65535.  One kernel or two, with the logits
+ * in the workspace (calls that run at the same time need one each). */
 size_t svdq_moe_route_workspace_bytes(int T, int E);
 svdq_status_t svdq_moe_route(const void *x, const void *w_router, const float *bias, svdq_dtype_t dtype, int T, int E,
                              int K, int top_k, svdq_moe_score_t score, int normalize, int32_t *ids, float *weights,

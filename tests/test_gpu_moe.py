@@ -41,6 +41,23 @@ def test_route(S, T, E, K, k, score, bias, normalize, dtype):
     assert (np.abs(f64(wt) - rwt) <= (2.0 ** -24 + 2.0 ** -40) * rwt + 2.0 ** -149).all()
 
 
+@pytest.mark.parametrize("T,E,K,k", [
+    (256, 64, 2048, 6), (256, 128, 1024, 8), (3, 129, 1000, 2), (7, 256, 512, 8),              # one kernel
+    (257, 64, 64, 4), (257, 90, 72, 8), (3, 200, 1024, 32), (1, 256, 520, 5), (2, 300, 64, 8), (1, 600, 72, 1),
+    (400, 64, 72, 4), (200, 128, 1032, 8), (100, 256, 520, 8), (60, 512, 136, 3), (30, 1000, 264, 16)])      # tiles
+def test_route_forms(S, T, E, K, k):
+    """Every way in which the logits are formed, with every number of experts a lane holds."""
+    announce(f"route T={T} E={E} K={K} k={k}")
+    r = np.random.default_rng(T + E)
+    dtype = ("bf16", "fp16")[K // 8 % 2]
+    x = torch.from_numpy(r.standard_normal((T, K))).to(DT[dtype]).cuda()
+    w = torch.from_numpy(r.standard_normal((E, K)) / np.sqrt(K)).to(DT[dtype]).cuda()
+    ids, wt = S.moe_route(x, w, k)
+    rid, rwt = O.route(f64(x), f64(w), k)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    assert (np.abs(f64(wt) - rwt) <= (2.0 ** -24 + 2.0 ** -40) * rwt + 2.0 ** -149).all()
+
+
 def test_route_ties_go_to_the_lower_index(S):
     w = torch.ones(200, 64, dtype=torch.bfloat16, device="cuda")
     w[[70, 150]] *= 2

@@ -238,17 +238,15 @@ __device__ __forceinline__ uint64_t order_of(double x) {
 // only where several lanes have it, the largest lower half, then the lowest
 // index.  P: keys of a lane, E <= 64 P.
 template <int P>
-__global__ __launch_bounds__(64) void moe_choose_kernel(const double *__restrict__ logits, const float *__restrict__ bias,
-                                                        int E, int top_k, int sigmoid, int normalize,
-                                                        int *__restrict__ ids, float *__restrict__ weights) {
-  const int lane = threadIdx.x;
-  const int64_t t = blockIdx.x;
+__device__ __forceinline__ void choose(const double *logits, const float *__restrict__ bias, int E, int top_k, int sigmoid,
+                                       int normalize, int64_t t, int lane, int *__restrict__ ids,
+                                       float *__restrict__ weights) {
   double logit[P], score[P], top = -__builtin_inf();
   uint64_t key[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int e = 64 * i + lane;
-    logit[i] = e < E ? logits[t * E + e] : -__builtin_inf();
+    logit[i] = e < E ? logits[e] : -__builtin_inf();
     top = fmax(top, logit[i]);
   }
   if (!sigmoid) {
@@ -314,6 +312,66 @@ __global__ __launch_bounds__(64) void moe_choose_kernel(const double *__restrict
     ids[t * top_k + lane] = mine;
     weights[t * top_k + lane] = (float)(mine_score / div);
   }
+}
+template <int P>
+__global__ __launch_bounds__(64) void moe_choose_kernel(const double *__restrict__ logits, const float *__restrict__ bias,
+                                                        int E, int top_k, int sigmoid, int normalize,
+                                                        int *__restrict__ ids, float *__restrict__ weights) {
+  const int64_t t = blockIdx.x;
+  choose<P>(logits + t * E, bias, E, top_k, sigmoid, normalize, t, threadIdx.x, ids, weights);
+}
+
+// Both in one kernel, a workgroup per token, where each can read the router's
+// whole matrix: its sixteen wavefronts take four experts each at a time, and the
+// first one chooses.  A launch less is 2.5 us less of a call from the host (1
+// token, 64 experts of 2048: 14.0 against 11.6), and the kernels' own time is
+// alike, 6.7 and 7.2 us, with 250 tokens 10.3 and 8.3; but with 600 tokens, more
+// than there are CUs, 12.1 and 15.6, and with 128 experts 7.3 and 12.1.
+constexpr int kSmallRouter = 1 << 17;           // elements of the matrix
+template <bool F16, int P>
+__global__ __launch_bounds__(1024) void moe_route_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ wr,
+                                                         const float *__restrict__ bias, int E, int K, int top_k,
+                                                         int sigmoid, int normalize, int *__restrict__ ids,
+                                                         float *__restrict__ weights) {
+  __shared__ double logits[64 * P];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = blockIdx.x;
+  const uint16_t *xr = x + t * K;
+  for (int e0 = w; e0 < E; e0 += 64) {
+    double acc[4] = {};
+    for (int k0 = lane * 8; k0 < K + lane * 8; k0 += 1024) {
+      uint4 wv[2][4], xv[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = min(k0 + 512 * i, K - 8);
+        xv[i] = *reinterpret_cast<const uint4 *>(xr + k);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          wv[i][n] = *reinterpret_cast<const uint4 *>(wr + (int64_t)min(e0 + 16 * n, E - 1) * K + k);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (k0 + 512 * i >= K) break;
+        const uint32_t xw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t ww[4] = {wv[i][n].x, wv[i][n].y, wv[i][n].z, wv[i][n].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[n] += (double)(wide<F16>(ww[j] & 0xFFFFu) * wide<F16>(xw[j] & 0xFFFFu));
+            acc[n] += (double)(wide<F16>(ww[j] >> 16) * wide<F16>(xw[j] >> 16));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const double sum = wave_sum(acc[n]);
+      if (lane == 0 && e0 + 16 * n < E) logits[e0 + 16 * n] = sum;
+    }
+  }
+  __syncthreads();
+  if (w == 0) choose<P>(logits, bias, E, top_k, sigmoid, normalize, t, lane, ids, weights);
 }
 
 // --------------------------------------------------------------------- experts
@@ -439,8 +497,8 @@ struct LocalRows {
   __device__ __forceinline__ int pair(int r) const { return sorted[r]; }
 };
 
-// More: moe_plan_kernel has sorted them (a thread of the form above holds 4
-// ids; the kernel is 4 us of the 140 and more that such calls take).
+// More: moe_plan_kernel has sorted them, in 4 us, where every thread of the form
+// above would look at up to 16 ids.
 struct PlanRows {
   static constexpr int LDS_BYTES = 16;
   int expert = -1, count = 0;
@@ -1134,6 +1192,18 @@ svdq_status_t svdq_moe_route(const void *x, const void *w_router, const float *b
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   double *logits = static_cast<double *>(workspace);
   const uint16_t *xp = static_cast<const uint16_t *>(x), *wp = static_cast<const uint16_t *>(w_router);
+  const int sigmoid = score == SVDQ_MOE_SIGMOID ? 1 : 0;
+  if (E <= 256 && (int64_t)E * K <= kSmallRouter && T <= 256) {
+#define MOE_ROUTE(F, P) hipLaunchKernelGGL((moe_route_kernel<F, P>), dim3((unsigned)T), dim3(1024), 0, stream, xp, wp, bias, E, \
+                                           K, top_k, sigmoid, normalize, ids, weights)
+    if (dtype == SVDQ_FP16) {
+      if (E <= 64) MOE_ROUTE(true, 1); else if (E <= 128) MOE_ROUTE(true, 2); else MOE_ROUTE(true, 4);
+    } else {
+      if (E <= 64) MOE_ROUTE(false, 1); else if (E <= 128) MOE_ROUTE(false, 2); else MOE_ROUTE(false, 4);
+    }
+#undef MOE_ROUTE
+    return launch_status("router launch");
+  }
   if ((int64_t)T * E > kTileLogits) {
     const dim3 grid((unsigned)((E + 15) / 16), (unsigned)((T + 15) / 16));
     if (dtype == SVDQ_FP16)
@@ -1147,7 +1217,6 @@ svdq_status_t svdq_moe_route(const void *x, const void *w_router, const float *b
     else
       hipLaunchKernelGGL((moe_logits_kernel<false>), grid, dim3(256), 0, stream, xp, wp, T, E, K, logits);
   }
-  const int sigmoid = score == SVDQ_MOE_SIGMOID ? 1 : 0;
 #define MOE_CHOOSE(P) hipLaunchKernelGGL((moe_choose_kernel<P>), dim3((unsigned)T), dim3(64), 0, stream, logits, bias, E, \
                                          top_k, sigmoid, normalize, ids, weights)
   if (E <= 64) MOE_CHOOSE(1);
