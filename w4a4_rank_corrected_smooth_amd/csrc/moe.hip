@@ -4,6 +4,7 @@
 //  moe_pack_kernel     weights to the experts' blobs, on the device
 //  moe_logits_kernel   x w^T in float64
 //  moe_choose_kernel   scores, the best top_k of each token, their weights
+//  moe_route_kernel    both, where the matrix is small
 //  moe_plan_kernel     the pairs of many, sorted by expert
 //  moe_gate_up_kernel  h = act(x Gate^T) * (x Up^T) of every (token, expert)
 //  moe_down_kernel     h Down^T of every (token, expert)
