@@ -261,6 +261,27 @@ def test_expert_layer_ids_outside_and_twice(S):
     assert not S.awq_moe_forward(layer, x, ids, wt).any()
 
 
+@pytest.mark.parametrize("T", [5, 30, 70, 600])
+def test_expert_layer_of_padding_rows(S, T):
+    """Batches of which no token, or only the last, has an expert here."""
+    r = np.random.default_rng(31)
+    E, K, I, k = 9, 128, 64, 2
+    parts = experts(r, E, K, I)
+    layer = device_layer(S, parts)
+    x = torch.from_numpy(r.standard_normal((T, K))).bfloat16().cuda()
+    x[:-1] = float("nan")
+    ids = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    ids[::2, 1] = E
+    wt = torch.ones(T, k, device="cuda")
+    out = torch.full_like(x, float("nan"))
+    announce(f"experts: {T} rows of padding")
+    assert not S.awq_moe_forward(layer, x, ids, wt, out=out).any()
+    ids[-1, 0] = 8
+    got = S.awq_moe_forward(layer, x, ids, wt, out=torch.full_like(x, float("nan")))
+    assert not got[:-1].any()
+    check(got[-1:], x[-1:], parts, ids[-1:], wt[-1:], "silu")
+
+
 def test_expert_layer_rows_do_not_touch_each_other(S):
     """A token of NaN or infinities spoils its own row only, and a token alone gives its row up to the order of sums."""
     r = np.random.default_rng(31)
