@@ -408,3 +408,44 @@ def test_attention_on_two_streams(S):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+def put(S, b, seq, token, k, v):
+    """Token `token` of sequence `seq` of a batch anew: k, v [H, D] float64, NaN blocks and all."""
+    page = b.cache.page_size
+    slot = b.table[seq, token // page] * page + token % page
+    rows16 = [torch.from_numpy(x[None]).to(DT[b.dtype]).cuda() for x in (k, v)]
+    S.kv4_append(b.cache, *rows16, slot.reshape(1).to(torch.int32))
+    b.k[seq][token], b.v[seq][token] = (O.values(f64(x))[0] for x in rows16)
+
+
+def check_nan(got, q, b, scale):
+    """Not a number where the oracle's sum has one, and the bound of `check` everywhere else."""
+    with np.errstate(invalid="ignore"):
+        nan = np.isnan(O.attend(f64(q), b.k, b.v, b.lens, scale)[0])
+    assert nan.any() and not nan.all()
+    assert np.array_equal(np.isnan(f64(got)), nan)
+    clean = type("B", (), dict(k=[np.nan_to_num(x) for x in b.k], v=[np.nan_to_num(x) for x in b.v], lens=b.lens))
+    fill = torch.from_numpy(O.attend(f64(q), clean.k, clean.v, b.lens, scale)[0]).to(got)
+    check(torch.where(torch.from_numpy(nan).cuda(), fill, got), q, clean, scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Q,group", [(2, 3), (3, 2), (3, 5), (5, 3), (5, 4), (3, 16), (40, 1)])
+def test_new_tokens_do_not_see_what_is_not_finite_after_them(S, Q, group, D, dtype):
+    """An infinity or a NaN in a new token's value or key reaches that token and those after it, and none before:
+    the last one's, a middle one's and the first one's, on both sides of a unit's, a page's and a chunk's end."""
+    H, lens = 2, [130, 35, 259, 3, 70]
+    announce(f"kv4 attention, not finite among {Q} new tokens, {Q * group} rows, D={D} {dtype}")
+    b = Batch(S, 60 + Q + group, lens, H, D, 16, dtype)
+    r = b.r
+    for seq, back, head, channel, bad, key in ((0, 1, 0, 3, np.nan, False), (0, 2, 1, D - 1, np.inf, False),
+                                               (1, 1, 1, 40, -np.inf, False), (2, 2, 0, 0, np.nan, True),
+                                               (2, Q, 1, 33, np.inf, False), (3, 1, 0, D - 2, np.nan, False)):
+        n = lens[seq]
+        k, v = r.standard_normal((2, H, D))
+        (k if key else v)[head, channel] = bad
+        put(S, b, seq, max(n - back, 0), k, v)
+    q = b.queries(Q, H * group)
+    check_nan(S.kv4_attention(b.cache, q, b.table, b.seq_lens), q, b, D ** -0.5)

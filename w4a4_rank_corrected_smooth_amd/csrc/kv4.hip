@@ -415,6 +415,8 @@ __device__ __forceinline__ void load_values(const Place &p, int lane, Values<D> 
 __device__ __forceinline__ float scale_of(uint32_t w, int i) {
   return __uint_as_float(i == 0 ? w << 23 : i == 1 ? w << 15 : i == 2 ? w << 7 : w >> 1);
 }
+// 0x80 in the bytes of `w` that are 255 (without those bits they are the scale 1)
+__device__ __forceinline__ uint32_t bytes_255(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u; }
 template <int I>
 __device__ __forceinline__ uint32_t two_values(uint32_t w, float s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, I));
@@ -445,7 +447,10 @@ __device__ __forceinline__ float column_max(float x) {
 // rows (of fp16 queries, and of the weights), which halves the products of
 // those; a lane's two column halves are added where they meet (rotating a row
 // of 16 lanes by 8).
-template <int D, int ROWS, bool F16>
+// MANY: several new tokens, so that rows see different tokens.  (One new token, without
+// what that takes: 48 ragged sequences 26.1 us against 26.6 with it, 16 x 4000 tokens of
+// 8 heads of 256 with 32 rows 62.7 and 64.5.)
+template <int D, int ROWS, bool F16, bool MANY>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D, ROWS)))) void kv4_attend_kernel(AttendArgs a) {
   constexpr int NB = D / 32;                       // blocks of 32 channels
   constexpr int NT = ROWS == 32 ? 2 : 1;           // 16-column tiles
@@ -572,6 +577,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
     Keys<D> keys;
     Values<D> vals;
     Place place;
+    uint64_t not_finite = 0;
     if (tw < t1) {
       place = locate<D>(a, pages, h, tw, lane);
       load_keys<D>(place, lane, keys);
@@ -629,6 +635,21 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
 #pragma unroll
             for (int k = 0; k < NB; ++k)
               if (!(keep >> (8 * i) & 1u)) vals.s[g][(i * NB + k) / 4] &= ~(0xFFu << (8 * ((i * NB + k) % 4)));
+        }
+        // Where rows see different tokens, a block of values that is not finite (scale
+        // byte 255) must not meet the zero weights of the rows that do not see its
+        // token: it gets another scale, and the rows that do become NaN after the last tile.
+        if constexpr (MANY) {
+          uint32_t any = 0;
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              const uint32_t bytes = bytes_255(vals.s[g][i]);
+              vals.s[g][i] &= ~bytes;
+              any |= bytes;
+            }
+          not_finite |= __ballot(any != 0);
         }
       }
       // running maximum (of the bare products) and weights
@@ -699,6 +720,36 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
       }
       load_values<D>(next, nlane, vals);
       place = next;
+    }
+
+    if (MANY && __builtin_expect(not_finite != 0, 0)) {
+      // the rows that see a block of values that is not finite (the scales are read again,
+      // so that nothing is kept for this in the loop's registers)
+      for (int t = tw; t < t1; t += kKv4Chunk) {
+        if (t + 32 <= whole) continue;
+        pages.load(t >> a.L.page_shift, lane);
+        const Place p = locate<D>(a, pages, h, t, lane);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (!p.ok[g]) continue;
+          uint32_t sc[NB];
+          load_words(sc, p.unit[g] + 16 * D + D / 2 + c4 * (D / 8));
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+              bool sees = false;                   // one of the lane's four tokens
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                sees |= (bytes_255(sc[(i * NB + k) / 4]) >> (8 * ((i * NB + k) % 4)) & 0x80u) != 0 &&
+                        t + 16 * g + 4 * c4 + i < limit[x];
+              uint64_t rows = __ballot(sees);      // of a column's four lanes
+              rows |= rows >> 32;
+              rows |= rows >> 16;
+              if (rows >> col & 1) o[x][2 * k] = o[x][2 * k + 1] = v4f{} + __builtin_nanf("");
+            }
+        }
+      }
     }
 
     // The four wavefronts' states meet: all of them into LDS, then every
@@ -992,7 +1043,8 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
   const dim3 join_grid((unsigned)(wide_join ? rows : (rows + 3) / 4));
 #define KV4_GO(DD, NN, FF)                                                                                  \
   do {                                                                                                      \
-    hipLaunchKernelGGL((kv4_attend_kernel<DD, NN, FF>), dim3(a.W), dim3(256), 0, stream, a);                \
+    if (Q > 1) hipLaunchKernelGGL((kv4_attend_kernel<DD, NN, FF, true>), dim3(a.W), dim3(256), 0, stream, a); \
+    else hipLaunchKernelGGL((kv4_attend_kernel<DD, NN, FF, false>), dim3(a.W), dim3(256), 0, stream, a);    \
     if (wide_join) hipLaunchKernelGGL((kv4_join_kernel<DD, FF, true>), join_grid, dim3(256), 0, stream, a); \
     else hipLaunchKernelGGL((kv4_join_kernel<DD, FF, false>), join_grid, dim3(256), 0, stream, a);          \
   } while (0)
