@@ -449,3 +449,30 @@ def test_new_tokens_do_not_see_what_is_not_finite_after_them(S, Q, group, D, dty
         put(S, b, seq, max(n - back, 0), k, v)
     q = b.queries(Q, H * group)
     check_nan(S.kv4_attention(b.cache, q, b.table, b.seq_lens), q, b, D ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("Q,group,D", [(1, 4, 128), (1, 12, 64), (3, 8, 128), (1, 20, 256)])
+def test_a_row_of_infinite_scores_is_not_a_row_without_tokens(S, Q, group, D, dtype):
+    """Scores that are all minus infinity leave 0 / 0, whether one workgroup or many take the row; a row
+    that sees no token is zero whatever its query holds."""
+    lens = [40, 0, 5000, 1, 64]
+    b = Batch(S, 80, lens, 1, D, 16, dtype)
+    for x in b.k:
+        x[:] = 1.0
+    n = b.pages * 16
+    ones = torch.ones(n, 1, D, dtype=DT[dtype], device="cuda")
+    S.kv4_append(b.cache, ones, ones, torch.arange(n, dtype=torch.int32, device="cuda"))
+    b.table[4] = -1                                  # a sequence of which no page is here
+    announce(f"kv4 attention of infinite scores, {Q * group} rows, D={D} {dtype}")
+    q = b.queries(Q, group)
+    want = S.kv4_attention(b.cache, q, b.table, b.seq_lens)
+    q[:, :, 1] = 0
+    q[:, :, 1, 7] = -float("inf")
+    got = S.kv4_attention(b.cache, q, b.table, b.seq_lens)
+    for seq, m in enumerate(lens):
+        for i in range(Q):
+            sees = m - Q + i + 1 > 0 and seq != 4
+            assert torch.isnan(got[seq, i, 1]).all() if sees else not got[seq, i, 1].any(), (seq, i)
+    got[:, :, 1] = want[:, :, 1]
+    assert torch.equal(got, want)

@@ -439,6 +439,12 @@ __device__ __forceinline__ float column_max(float x) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+constexpr float kLargest = 3.402823466e38f;        // of the float32 numbers
+// 1 / the sum of a row's weights; zero for a row that has no maximum, since it saw no token
+__device__ __forceinline__ float inverse_of(float sum, float top) {
+  return sum > 0.0f || sum != sum ? 1.0f / sum : top == -__builtin_inff() ? 0.0f : __builtin_nanf("");
+}
+
 // Registers: at least two wavefronts a SIMD keeps the matrix accumulators in
 // ordinary registers (with all 512 allowed, the compiler moves them to and from
 // the accumulation registers around every tile).
@@ -752,6 +758,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
       }
     }
 
+    // A row whose scores are all minus infinity is 0 / 0, and one that sees no token is
+    // zero.  Both have no maximum yet; the first gets the lowest number for one.
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+      if (__ballot(m[x] == -__builtin_inff()))
+        for (int t = tw; t < t1; t += kKv4Chunk) {
+          pages.load(t >> a.L.page_shift, lane);
+          const Place p = locate<D>(a, pages, h, t, lane);
+          if (m[x] == -__builtin_inff() && ((p.ok[0] && t < limit[x]) || (p.ok[1] && t + 16 < limit[x]))) m[x] = -kLargest;
+        }
+
     // The four wavefronts' states meet: all of them into LDS, then every
     // thread takes some channels of one row, relative to the row's largest
     // maximum, and writes them.
@@ -761,7 +778,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
       l[x] += __shfl_xor(l[x], 32);
       const bool mine = !second;
       if (mine && c4 == 0) {
-        sm[w][16 * x + col] = m[x] * a.scale;
+        sm[w][16 * x + col] = m[x] == -kLargest ? m[x] : m[x] * a.scale;
         sl[w][16 * x + col] = l[x];
       }
 #pragma unroll
@@ -786,7 +803,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
         sum = __builtin_fmaf(sl[k][c], f[k], sum);
       }
       const bool done = ch0 == 0 && ch1 == n;
-      const float inv = !done ? 1.0f : sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      const float inv = done ? inverse_of(sum, top) : 1.0f;
       const int i = r / a.group, j = r % a.group;
       uint16_t *out = a.out + (((int64_t)b * a.Q + i) * (a.L.H * a.group) + h * a.group + j) * D;
       const int64_t slot = (2 * (int64_t)blockIdx.x + (u > u0 ? 1 : 0)) * a.block_rows + c;
@@ -892,7 +909,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(AttendArgs a) {
       for (int e = 0; e < V; ++e) acc[e] += so[k][lane * V + e];
     }
   }
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  const float inv = inverse_of(l, top);
   const int64_t at = (((int64_t)b * a.Q + i) * Hq + hq) * D + lane * V;
 #pragma unroll
   for (int e = 0; e < V; ++e)
