@@ -354,3 +354,19 @@ def test_route_and_experts_in_a_graph(S):
         torch.cuda.synchronize()
         for o, v in zip(outs, want):
             assert torch.equal(o, v), f"replay {i}"
+
+
+@pytest.mark.parametrize("power", [(70, 70), (-70, -70), (120, 5), (-120, -5), (0, 100)])
+@pytest.mark.parametrize("T,E,K,k", [(3, 64, 512, 3), (256, 100, 136, 4), (3, 300, 512, 3), (100, 256, 520, 2)])
+def test_route_over_the_range_of_bf16(S, T, E, K, k, power):
+    """Products past float32's largest number and below its normal range, in every form in which the logits are formed."""
+    announce(f"route T={T} E={E} K={K} k={k}, rows times 2^{power[0]} and matrix times 2^{power[1]}")
+    r = np.random.default_rng(T + E + K)
+    x = torch.from_numpy(r.standard_normal((T, K)) * 2.0 ** power[0]).bfloat16().cuda()
+    w = torch.from_numpy(r.standard_normal((E, K)) / np.sqrt(K) * 2.0 ** power[1]).bfloat16().cuda()
+    for score in ("softmax", "sigmoid"):
+        ids, wt = S.moe_route(x, w, k, score=score)
+        with np.errstate(over="ignore"):
+            rid, rwt = O.route(f64(x), f64(w), k, None, score)
+        assert np.array_equal(ids.cpu().numpy(), rid)
+        assert (np.abs(f64(wt) - rwt) <= (2.0 ** -24 + 2.0 ** -40) * rwt + 2.0 ** -149).all()

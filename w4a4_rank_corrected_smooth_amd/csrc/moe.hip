@@ -67,10 +67,11 @@ __global__ __launch_bounds__(256) void moe_pack_kernel(const uint8_t *__restrict
 }
 
 // ---------------------------------------------------------------------- router
-// Logits in float64: a product of two 16-bit values is exact in float32, and
-// their sum in float64 is exact to 2^-53 of its terms, so the order of the
-// sum cannot move a logit across its neighbour's and the choice does not
-// depend on how the work is split.  One wavefront per expert and kTokens tokens.
+// Logits in float64: a product of two 16-bit values is exact there (of bf16
+// ones not in float32, whose range it can leave), and their sum is good to 2^-53
+// of its terms, so the order of the sum cannot move a logit across its
+// neighbour's and the choice does not depend on how the work is split.  One
+// wavefront per expert and kTokens tokens.
 constexpr int kTokens = 4;
 // Logits of a call above which the matrix form takes over: at K = 4096 the two
 // took 15.5 and 20.4 us for 64 x 256 logits (router in all), 23.5 and 21.5 for
@@ -104,8 +105,8 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const uint16_t *__restr
         const uint32_t xw[4] = {xv[i][t].x, xv[i][t].y, xv[i][t].z, xv[i][t].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          acc[t] += (double)(wide<F16>(ww[j] & 0xFFFFu) * wide<F16>(xw[j] & 0xFFFFu));
-          acc[t] += (double)(wide<F16>(ww[j] >> 16) * wide<F16>(xw[j] >> 16));
+          acc[t] = __builtin_fma((double)wide<F16>(ww[j] & 0xFFFFu), (double)wide<F16>(xw[j] & 0xFFFFu), acc[t]);
+          acc[t] = __builtin_fma((double)wide<F16>(ww[j] >> 16), (double)wide<F16>(xw[j] >> 16), acc[t]);
         }
       }
     }
@@ -359,8 +360,8 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(const uint16_t *__restr
           const uint32_t ww[4] = {wv[i][n].x, wv[i][n].y, wv[i][n].z, wv[i][n].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            acc[n] += (double)(wide<F16>(ww[j] & 0xFFFFu) * wide<F16>(xw[j] & 0xFFFFu));
-            acc[n] += (double)(wide<F16>(ww[j] >> 16) * wide<F16>(xw[j] >> 16));
+            acc[n] = __builtin_fma((double)wide<F16>(ww[j] & 0xFFFFu), (double)wide<F16>(xw[j] & 0xFFFFu), acc[n]);
+            acc[n] = __builtin_fma((double)wide<F16>(ww[j] >> 16), (double)wide<F16>(xw[j] >> 16), acc[n]);
           }
         }
       }
