@@ -486,8 +486,10 @@ typedef enum { SVDQ_MOE_SILU = 0, SVDQ_MOE_GELU_TANH = 1 } svdq_moe_act_t;
 
 /* The experts of each token: logits x w_router^T [T, E], scores their softmax
  * over the E experts or their sigmoid, and the top_k experts of the largest
- * score (+ bias), the lower index first where two are equal (a NaN counts as
- * the smallest).  ids [T, top_k] int32 in that order; weights [T, top_k]
+ * score + bias, or without a bias of the largest logit, which the score grows
+ * with: sigmoids of 38 and 40 are both 1 in float64, and a bias, zeros too,
+ * makes them equal.  The lower index goes first where two are equal (a NaN
+ * counts as the smallest).  ids [T, top_k] int32 in that order; weights [T, top_k]
  * float32 their scores without the bias, divided by their sum if `normalize`.
  * x [T, K] and w_router [E, K] are bf16 or fp16 (device, 16-byte aligned), bias
  * [E] float32 or NULL.  Logits and scores are float64, so the choice does not

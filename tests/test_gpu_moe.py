@@ -370,3 +370,17 @@ def test_route_over_the_range_of_bf16(S, T, E, K, k, power):
             rid, rwt = O.route(f64(x), f64(w), k, None, score)
         assert np.array_equal(ids.cpu().numpy(), rid)
         assert (np.abs(f64(wt) - rwt) <= (2.0 ** -24 + 2.0 ** -40) * rwt + 2.0 ** -149).all()
+
+
+def test_route_of_saturated_scores(S):
+    """A sigmoid of 38 and one of 40 are both 1 in float64: without a bias the order is the logits', with one
+    (zeros too) it is the scores' and the lower index goes first.  The weights are the scores' either way."""
+    w = torch.zeros(70, 64, dtype=torch.bfloat16, device="cuda")
+    w[5, 0], w[66, 0], w[7, 1] = 38, 40, 1
+    x = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1
+    announce("route of saturated scores")
+    ids, wt = S.moe_route(x, w, 3, score="sigmoid", normalize=False)
+    assert ids.tolist() == [[66, 5, 0]] * 2 and wt.tolist() == [[1, 1, 0.5]] * 2
+    ids, wt = S.moe_route(x, w, 3, bias=torch.zeros(70, device="cuda"), score="sigmoid", normalize=False)
+    assert ids.tolist() == [[5, 66, 0]] * 2 and wt.tolist() == [[1, 1, 0.5]] * 2

@@ -849,7 +849,9 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, bias: Optiona
               score: str = "softmax", normalize: bool = True, workspace: Optional[torch.Tensor] = None):
     """The top_k experts of each row of x [T, K] by the softmax or sigmoid of
     x w_router^T (w_router [E, K]), plus bias [E] for the choice: (ids int32,
-    weights float32), both [T, top_k], best first, ties to the lower index."""
+    weights float32), both [T, top_k], best first, ties to the lower index.
+    Without a bias the choice is by the logits themselves, which tells scores
+    apart that are equal in float64 (sigmoids near 1)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     dev = x.device
