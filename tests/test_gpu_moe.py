@@ -384,3 +384,67 @@ def test_route_of_saturated_scores(S):
     assert ids.tolist() == [[66, 5, 0]] * 2 and wt.tolist() == [[1, 1, 0.5]] * 2
     ids, wt = S.moe_route(x, w, 3, bias=torch.zeros(70, device="cuda"), score="sigmoid", normalize=False)
     assert ids.tolist() == [[5, 66, 0]] * 2 and wt.tolist() == [[1, 1, 0.5]] * 2
+
+
+def wide_range_experts(r, E):
+    """Experts of 128 x 64 whose gates take channel 0 alone out of the first group, and whose ups take nothing of it."""
+    (q, s, z), (qd, sd, zd) = experts(r, E, 128, 64)
+    z[..., 0] = 8
+    q[:, :64, 0] = r.integers(9, 16, (E, 64))
+    q[:, 64:, 0] = 8
+    return (q, s, z), (qd, sd, zd)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T,E", [(1, 1), (3, 2), (20, 8), (40, 3), (90, 2)])
+def test_expert_layer_over_float32s_range(S, T, E, act):
+    """Rows up to 2^125 and gated products near 2^118, past which 128 + 15 times 64 of them is no float32 number any
+    more, where neither the gate's and the up's results nor the output are."""
+    announce(f"experts over float32's range, T={T} E={E} {act}")
+    r = np.random.default_rng(T)
+    parts = wide_range_experts(r, E)
+    parts[0][1][..., 0] = 2.0 ** -11
+    parts[1][1][:] = (r.choice([-1.0, 1.0], parts[1][1].shape) * 2.0 ** -20).astype(np.float16)
+    layer = device_layer(S, parts)
+    x = r.standard_normal((T, 128))
+    x[:, :64] = 0
+    x[:, 0] = 2.0 ** 125
+    x = torch.from_numpy(x).bfloat16().cuda()
+    ids = torch.from_numpy(r.integers(0, E, (T, 1)).astype(np.int32)).cuda()
+    wt = torch.ones(T, 1, device="cuda")
+    got = S.awq_moe_forward(layer, x, ids, wt, activation=act)
+    with np.errstate(over="ignore"):
+        check(got, x, parts, ids, wt, act)
+
+
+@pytest.mark.parametrize("T", [1, 20])
+def test_expert_layer_of_the_largest_gated_products(S, T):
+    """h = 1023 x 2^118 is a float32 number, and the bf16 number next to it is not."""
+    r = np.random.default_rng(5)
+    (q, s, z), (qd, sd, zd) = wide_range_experts(r, 4)
+    s[:], z[:], q[:] = 1.0, 8, 8
+    q[:, :64, 0], q[:, :64, 1], q[:, 64:, 64] = 9, 7, 9          # gate: x0 - x1, up: x64
+    sd[:] = 2.0 ** -24
+    layer = device_layer(S, ((q, s, z), (qd, sd, zd)))
+    x = torch.zeros(T, 128)
+    x[:, 0], x[:, 1], x[:, 64] = 2.0 ** 70, 2.0 ** 60, 2.0 ** 58
+    x = x.bfloat16().cuda()
+    ids, wt = (torch.arange(T, dtype=torch.int32, device="cuda") % 4)[:, None], torch.ones(T, 1, device="cuda")
+    announce(f"experts of the largest gated products, T={T}")
+    with np.errstate(over="ignore"):
+        check(S.awq_moe_forward(layer, x, ids, wt), x, ((q, s, z), (qd, sd, zd)), ids, wt, "silu")
+
+
+@pytest.mark.parametrize("T,E", [(1, 1), (20, 8), (90, 2)])
+def test_expert_layer_of_small_rows(S, T, E):
+    """Gated products near 2^-118, whose second pieces are near the end of float32's range."""
+    announce(f"experts of small rows, T={T} E={E}")
+    r = np.random.default_rng(T + 7)
+    parts = experts(r, E, 128, 64)
+    for p in parts:
+        p[1][:] = (0.5 + r.random(p[1].shape)).astype(np.float16)
+    layer = device_layer(S, parts)
+    x = torch.from_numpy(r.standard_normal((T, 128)) * 2.0 ** -64).bfloat16().cuda()
+    ids = torch.from_numpy(r.integers(0, E, (T, 1)).astype(np.int32)).cuda()
+    wt = torch.ones(T, 1, device="cuda")
+    check(S.awq_moe_forward(layer, x, ids, wt), x, parts, ids, wt, "silu")

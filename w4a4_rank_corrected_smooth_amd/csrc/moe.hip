@@ -379,11 +379,13 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(const uint16_t *__restr
 // --------------------------------------------------------------------- experts
 // With s and z the scale and zero point of an output channel and group of 64
 // input channels, q the codes: an expert's product is sum_g s sum_k x (q - z).
-// bf16 rows take the codes as the bf16 values 128 + q (one and-or a pair, exact)
-// and sum_k x from one more product, with ones:
-//   sum_k x (q - z) = sum_k x (128 + q) - (128 + z) sum_k x,
-// in float32 (the terms are about 30 times the result's, so 2^-19 of it); fp16
-// rows take q - z exactly (1024 + q minus 1024 + z).  The gated product
+// bf16 rows take the codes as the bf16 values c (128 + q) (one and-or a pair,
+// exact) and c sum_k x from one more product, with c in the place of the code:
+//   c sum_k x (q - z) = sum_k x c (128 + q) - (128 + z) sum_k x c,
+// in float32 (the terms are about 30 times the result's, so 2^-19 of it, and less
+// of a row with a common offset).  c = 2^-14: 64 terms of up to 143 c |x| each
+// stay in float32's range for any x, and 1 / c is taken off at the end, exactly.
+// fp16 rows take q - z exactly (1024 + q minus 1024 + z).  The gated product
 // h = act(gate) up goes on as two bf16 pieces, which hold it to 2^-17 in
 // float32's range (an fp16 h would overflow where y does not).
 // What bounds it: the experts' bytes, each read once.  128 tokens with 8 of 128
@@ -576,8 +578,8 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(MoeArgs a) {
 }
 
 // Eight codes of a blob word (even channels in the low half-words) as the
-// bf16 values 128 + code: 0x4300 is 128 and a code fills the last mantissa
-// bits, so one shift and one and-or make a pair.  (An instruction takes one
+// bf16 values 2^-14 (128 + code): 0x3C00 is 2^-14 128 and a code fills the last
+// mantissa bits, so one shift and one and-or make a pair.  (An instruction takes one
 // constant from scalar registers, so the other is put into a vector register;
 // the and-or itself is left to the compiler, which then knows what the matrix
 // instructions have to wait for.)
@@ -586,9 +588,10 @@ __device__ __forceinline__ uint32_t in_vector(uint32_t c) {
   asm("v_mov_b32 %0, %1" : "=v"(v) : "s"(c));
   return v;
 }
+constexpr float kCodeUnit = 0x1p-14f;
 __device__ __forceinline__ v8bf codes_128(uint32_t word) {
   uint32_t o[4];
-  const uint32_t magic = in_vector(0x43004300u);
+  const uint32_t magic = in_vector(0x3C003C00u);
 #pragma unroll
   for (int j = 0; j < 4; ++j) o[j] = (word >> (4 * j) & 0x000F000Fu) | magic;
   return as_v8bf(make_uint4(o[0], o[1], o[2], o[3]));
@@ -614,9 +617,9 @@ __device__ __forceinline__ v4f mma(uint4 a, v8bf b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_v8bf(a), b, c, 0, 0, 0);
 }
 
-// acc += the group's 64 channels: s (sum x (128 + code) - (128 + zero) sum x)
-// for bf16 activations (sum x from one more product, with ones, shared by the
-// columns), s sum x (code - zero) for fp16.  a0, a1: the lane's row, channels
+// acc += the group's 64 channels: s c (sum x (128 + code) - (128 + zero) sum x)
+// for bf16 activations (c sum x from one more product, shared by the columns; c is
+// kCodeUnit), s sum x (code - zero) for fp16.  a0, a1: the lane's row, channels
 // 16 (lane / 16) + [0, 16) of the group.
 template <bool F16>
 __device__ __forceinline__ void group_mma(uint4 a0, uint4 a1, v4f xsum, uint32_t w0, uint32_t w1, uint32_t sz, v4f &acc) {
@@ -635,7 +638,18 @@ __device__ __forceinline__ void group_mma(uint4 a0, uint4 a1, v4f xsum, uint32_t
     for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(__builtin_fmaf(z, xsum[e], p[e]), s, acc[e]);
   }
 }
-__device__ __forceinline__ v8bf ones() { return as_v8bf(make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u)); }
+__device__ __forceinline__ v8bf units() { return as_v8bf(make_uint4(0x38803880u, 0x38803880u, 0x38803880u, 0x38803880u)); }   // kCodeUnit
+// 1 / c of the sums of group_mma
+template <bool F16>
+__device__ __forceinline__ float whole(float sum) { return F16 ? sum : sum * (1.0f / kCodeUnit); }
+// The two bf16 pieces of a gated product.  The largest numbers, for which the
+// first piece would round to infinity, get the largest one that does not.
+__device__ __forceinline__ void split_h(float h, uint16_t &first, uint16_t &second) {
+  __bf16 hi = (__bf16)h;
+  if (__builtin_isfinite(h) && !__builtin_isfinite((float)hi)) hi = __builtin_bit_cast(__bf16, (uint16_t)(h > 0.0f ? 0x7F7F : 0xFF7F));
+  first = __builtin_bit_cast(uint16_t, hi);
+  second = __builtin_bit_cast(uint16_t, (__bf16)(__builtin_isfinite(h) ? h - (float)hi : 0.0f));
+}
 
 // One expert's product for a block of rows, the form both products share.
 //
@@ -823,7 +837,7 @@ __global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2)))
     v4f acc[2 * R] = {};
     pr.run(lds, row, w, lane, [&](int g, int i, const uint4 (&x)[1][2], int r) {
       v4f xsum = v4f{};
-      if constexpr (!F16) xsum = mma(x[0][1], ones(), mma(x[0][0], ones(), v4f{}));
+      if constexpr (!F16) xsum = mma(x[0][1], units(), mma(x[0][0], units(), v4f{}));
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         group_mma<F16>(x[0][0], x[0][1], xsum, g ? pr.code[i][t].z : pr.code[i][t].x,
@@ -838,13 +852,9 @@ __global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2)))
         const int at_row = r0 + 16 * r + 4 * (lane >> 4) + e;
         const int64_t at = (int64_t)rows.pair(min(at_row, rows.count - 1)) * (2 * a.I) + tile / 4 * 128 +
                            tile % 4 * kAwqTile + (lane & 15);
-        const float g = acc[2 * r][e], u = acc[2 * r + 1][e];
+        const float g = whole<F16>(acc[2 * r][e]), u = whole<F16>(acc[2 * r + 1][e]);
         const float h = (GELU ? gelu_tanh_f32(g) : g * __builtin_amdgcn_rcpf(1.0f + __expf(-g))) * u;
-        if (at_row < rows.count && tile < n) {
-          const __bf16 hi = (__bf16)h;
-          a.h[at] = __builtin_bit_cast(uint16_t, hi);
-          a.h[at + kGroup] = __builtin_bit_cast(uint16_t, (__bf16)(__builtin_isfinite(h) ? h - (float)hi : 0.0f));
-        }
+        if (at_row < rows.count && tile < n) split_h(h, a.h[at], a.h[at + kGroup]);
       }
   }
 }
@@ -876,7 +886,7 @@ __global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2)))
     pr.run(lds, row, w, lane, [&](int g, int i, const uint4 (&h)[Pr::PIECES][2], int r) {
       v4f sum = v4f{};
 #pragma unroll
-      for (int k = 0; k < 2 * Pr::PIECES; ++k) sum = mma(h[k / 2][k % 2], ones(), sum);
+      for (int k = 0; k < 2 * Pr::PIECES; ++k) sum = mma(h[k / 2][k % 2], units(), sum);
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         const v8bf b0 = codes_128(g ? pr.code[i][t].z : pr.code[i][t].x);
@@ -908,7 +918,7 @@ __global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2)))
         const int64_t to = (int64_t)rows.pair(min(at_row, rows.count - 1)) * a.K + (lane & 15);
 #pragma unroll
         for (int t = 0; t < TILES; ++t)
-          if (at_row < rows.count && tile0 + t < n) a.part[to + (tile0 + t) * kAwqTile] = acc[TILES * r + t][e];
+          if (at_row < rows.count && tile0 + t < n) a.part[to + (tile0 + t) * kAwqTile] = whole<false>(acc[TILES * r + t][e]);
       }
   }
 }
@@ -987,7 +997,7 @@ __global__ __launch_bounds__(KS * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
         if (2 * (p + i) + g >= G) break;
         const uint4 a0 = r[i].x[0][2 * g], a1 = r[i].x[0][2 * g + 1];
         v4f xsum = v4f{};
-        if constexpr (!F16) xsum = mma(a1, ones(), mma(a0, ones(), v4f{}));
+        if constexpr (!F16) xsum = mma(a1, units(), mma(a0, units(), v4f{}));
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           group_mma<F16>(a0, a1, xsum, g ? s[i].code[t].z : s[i].code[t].x, g ? s[i].code[t].w : s[i].code[t].y,
@@ -1006,14 +1016,12 @@ __global__ __launch_bounds__(KS * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
     g += red[k][0][lane][w];
     u += red[k][1][lane][w];
   }
+  g = whole<F16>(g);
+  u = whole<F16>(u);
   const float h = (GELU ? gelu_tanh_f32(g) : g * __builtin_amdgcn_rcpf(1.0f + __expf(-g))) * u;
   const int row = 4 * (lane >> 4) + w;
   const int64_t at = (int64_t)rows.pair(min(row, rows.count - 1)) * (2 * a.I) + tile / 4 * 128 + tile % 4 * kAwqTile + (lane & 15);
-  if (row < rows.count) {
-    const __bf16 hi = (__bf16)h;
-    a.h[at] = __builtin_bit_cast(uint16_t, hi);
-    a.h[at + kGroup] = __builtin_bit_cast(uint16_t, (__bf16)(__builtin_isfinite(h) ? h - (float)hi : 0.0f));
-  }
+  if (row < rows.count) split_h(h, a.h[at], a.h[at + kGroup]);
 }
 
 // y's 16 columns of one workgroup.  The (expert, step) items of all experts
@@ -1082,7 +1090,7 @@ __global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(WAVE
           const uint4 h0 = r[i % RA].x[0][2 * g], h1 = r[i % RA].x[0][2 * g + 1];
           const uint4 l0 = r[i % RA].x[1][2 * g], l1 = r[i % RA].x[1][2 * g + 1];
           const v8bf b0 = codes_128(g ? s[i].code[0].z : s[i].code[0].x), b1 = codes_128(g ? s[i].code[0].w : s[i].code[0].y);
-          const v4f sum = mma(l1, ones(), mma(l0, ones(), mma(h1, ones(), mma(h0, ones(), v4f{}))));
+          const v4f sum = mma(l1, units(), mma(l0, units(), mma(h1, units(), mma(h0, units(), v4f{}))));
           const v4f prod = mma(l1, b1, mma(l0, b0, mma(h1, b1, mma(h0, b0, v4f{}))));
           const uint32_t sz = g ? s[i].sz[0].y : s[i].sz[0].x;
           const float z = -(128.0f + (float)zero_of(sz)), sc = scale_of(sz);
@@ -1097,7 +1105,7 @@ __global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(WAVE
     for (int e = 0; e < 4; ++e) {
       const int t = 4 * (lane >> 4) + e;
       const float x = __shfl(weight, t);
-      if (chose >> t & 1) y[e] = __builtin_fmaf(x, acc[e], y[e]);
+      if (chose >> t & 1) y[e] = __builtin_fmaf(x, whole<false>(acc[e]), y[e]);
     }
     at = slot * P + p1;
   }
