@@ -533,11 +533,16 @@ typedef struct {
  * outside [0, E) adds nothing (experts held elsewhere, padding rows); one
  * that a token names twice counts twice.  The gated product is kept to 16
  * significant bits in float32's range, sums are float32, and y is rounded once.
+ * A sum over 64 channels of a bf16 row or of gated products is the difference of
+ * sum x (128 + q) and (128 + z) sum x, so its rounding is 2^-24 of terms of up to
+ * 143 |x|: about 2^-19 of a result, more where the x have a common offset.
  * A row of x that is not finite gives a row of y that is not, and touches no
  * other; which tokens share a call changes the order of float32 sums only.
  * E <= 1024, K and I multiples of 64 with 2 I K <= 2^31, T top_k <= 4096.
- * Each expert that some token names is read once per 16 or 32 of its rows.  The
- * workspace needs no clearing and keeps nothing from one call for the next
+ * Each expert that some token names is read once per 16 or 32 of its rows, its
+ * down weights once per 8 where the call has up to five pairs an expert: that
+ * goes by the average, so tokens that crowd on one expert have it read more
+ * often.  The workspace needs no clearing and keeps nothing from one call for the next
  * (calls that run at the same time need one each). */
 size_t awq_moe_workspace_bytes(int T, int top_k, int K, int I);
 svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dtype_t dtype, int T, const int32_t *ids,

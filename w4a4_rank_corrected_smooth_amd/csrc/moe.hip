@@ -1306,7 +1306,9 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   const bool many = pairs > 12 * slots;
   // Up to 5 pairs an expert, both pieces of h in one tile: 12 tokens with 6 of 64
   // experts took 57.3 us against 62.6, 8 with 2 of 8 45 against 51; at 8 pairs an
-  // expert, where four experts in ten have more than 8 rows, 108 against 92.
+  // expert, where four experts in ten have more than 8 rows, 108 against 92.  (The
+  // rule knows the average only: an expert's down weights are read once per 8
+  // of its rows however many those are.)
   const bool packed = pairs <= 5 * slots;
   // Few tiles: K in parts for the wavefronts of a workgroup.  With 256 and 512
   // tiles of gate and up 16.2 and 26.5 us in four parts, 20.2 and 31.5 in one;
