@@ -1054,9 +1054,13 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
   const int resident = 256 * kv4_waves(L.D, block);
   a.W = (int)(most < resident ? most : resident);
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-  // pieces of a row, on average: from four on, a workgroup joins them
-  const bool wide_join = a.W >= 4ll * B * L.H * a.row_blocks;
+  // A workgroup joins each row where there are few rows of many pieces, at most 64 rows
+  // for each piece of one, and a wavefront where there are more.  With a workgroup and
+  // with a wavefront (rows, pieces on average): 128 and 24 74.5 and 75.7 us; 512 and 24
+  // 17.1 and 18.9; 384 and 8 41.4 and 41.7; 1024 and 16 45.1 and 45.6; 1024 and 12 23.3
+  // and 23.0; 768 and 4 42.9 and 42.5; 1536 and 6 23.6 and 22.6; 2560 and 4 29.7 and 26.7.
   const int64_t rows = (int64_t)B * Q * Hq;
+  const bool wide_join = rows * B * L.H * a.row_blocks <= 64ll * a.W;
   const dim3 join_grid((unsigned)(wide_join ? rows : (rows + 3) / 4));
 #define KV4_GO(DD, NN, FF)                                                                                  \
   do {                                                                                                      \
