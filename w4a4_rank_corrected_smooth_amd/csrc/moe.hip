@@ -1315,11 +1315,14 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   // layers with 768 tiles 29.6 us in two parts (24.3 and 26.1 with 1024), 36.8 in
   // one (24.7, 26.9), 29.7 in four (28.8, 30.9); with 1280 tiles of 32 steps 51.9
   // in two, 55.1 in one, 57.6 in four; with 1792, 59.1, 55.5 and 67.3.
-  // Down: 1024 and 2048 tiles 14.6 and 28.4 us as two parts of two tiles, 17.0
-  // and 29.2 as four tiles; with 16384, 107 and 92.
+  // Down, as two parts of two tiles and as four tiles: layers of 2048 tiles 20.8 and
+  // 23.0 us (11 steps 27.3 and 30.6), 2560 23.0 and 23.9 (30.8, 31.7), 2816 23.3 and 24.5,
+  // 12 x 256 24.8 and 25.4 (32.9, 33.1), 3328 29.5 and 28.0 (37.0, 36.6), 4096 32.4 and 29.5,
+  // 8192 51.0 and 45.8.
   const int64_t gate_tiles = (int64_t)slots * gt;
   const int gate_parts = gate_tiles < 640 ? 4 : gate_tiles < 1536 ? 2 : 1;
-  const bool few_down = (int64_t)slots * dt < 4096;
+  const int64_t down_tiles = (int64_t)slots * dt;
+  const bool few_down = down_tiles <= 12 * 256;
   const bool plan = pairs > kLocalPairs;
   if (plan) hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
   // Wavefronts a workgroup: eight share a row's chunk, twice as long, where a
@@ -1327,9 +1330,11 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
   // workgroups fill the machine more evenly.  Layer of 8 experts of 4096 x 3584
   // (1792 tiles of gate and up): 52.7 us with eight, 55.4 with four; of 32 experts
   // of 4096 x 1536 72.9 and 62.3; gate and up of 16 steps 51.7 and 47.3; down of 20
-  // steps 50.9 and 46.0.
+  // steps 50.9 and 46.0.  Layers whose down has 28 or 32 steps, with eight (two parts) and
+  // with four wavefronts as four tiles: 3328 tiles 72.8 and 74.6, 84.7 and 89.7; 4096
+  // tiles 89.5 and 88.7.
   const bool large_gate = w->K >= 24 * 2 * kGroup && gate_tiles < 2560;
-  const bool large_down = w->I >= 24 * 2 * kGroup && few_down;
+  const bool large_down = w->I >= 24 * 2 * kGroup && down_tiles < 4096;
 #define MOE_GU(F, A, KS, R, P, W)                                                                                \
   hipLaunchKernelGGL((moe_gate_up_kernel<F, A, KS, R, P, W>), dim3((gt + W / KS - 1) / (W / KS), (unsigned)slots), \
                      dim3(W * 64), 0, stream, a)
