@@ -324,12 +324,17 @@ __global__ __launch_bounds__(64) void moe_choose_kernel(const double *__restrict
 }
 
 // Both in one kernel, a workgroup per token, where each can read the router's
-// whole matrix: its sixteen wavefronts take four experts each at a time, and the
-// first one chooses.  A launch less is 2.5 us less of a call from the host (1
-// token, 64 experts of 2048: 14.0 against 11.6), and the kernels' own time is
-// alike, 6.7 and 7.2 us, with 250 tokens 10.3 and 8.3; but with 600 tokens, more
-// than there are CUs, 12.1 and 15.6, and with 128 experts 7.3 and 12.1.
-constexpr int kSmallRouter = 1 << 17;           // elements of the matrix
+// whole matrix: its sixteen wavefronts take four experts each at a time, 1024
+// channels a turn, and the first one chooses.  A launch less is 2.2 us less of a call
+// from the host (14.0 against 11.8), and a turn is 2 us in a graph, where the two
+// kernels need not wait for the host: up to two turns it costs at most what it saves.
+// In one kernel and in two, 1 and 250 tokens: 64 experts of 512 (one turn) 4.7 and 5.6, 5.3
+// and 7.7 us; 64 of 1536 (two) 6.6 and 6.3, 7.6 and 9.6; 64 of 2048 7.4 and 6.5, 8.8 and
+// 10.5; 128 of 1024 8.5 and 6.3, 9.7 and 9.6; but 64 of 2560 (three) 8.5 and 7.2, 9.7 and
+// 12.0; 192 of 1024 12.2 and 7.4, 13.6 and 10.5; 32 of 4096 (four) 11.2 and 8.1, 12.6 and
+// 12.2.  With 600 tokens, more than there are CUs, 64 of 2048 take 15.6 and 12.1.
+constexpr int kSmallTurns = 2;
+constexpr int64_t route_turns(int E, int K) { return (int64_t)((E + 63) / 64) * ((K + 1023) / 1024); }
 template <bool F16, int P>
 __global__ __launch_bounds__(1024) void moe_route_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ wr,
                                                          const float *__restrict__ bias, int E, int K, int top_k,
@@ -1203,13 +1208,13 @@ svdq_status_t svdq_moe_route(const void *x, const void *w_router, const float *b
   double *logits = static_cast<double *>(workspace);
   const uint16_t *xp = static_cast<const uint16_t *>(x), *wp = static_cast<const uint16_t *>(w_router);
   const int sigmoid = score == SVDQ_MOE_SIGMOID ? 1 : 0;
-  if (E <= 256 && (int64_t)E * K <= kSmallRouter && T <= 256) {
+  if (route_turns(E, K) <= kSmallTurns && T <= 256) {
 #define MOE_ROUTE(F, P) hipLaunchKernelGGL((moe_route_kernel<F, P>), dim3((unsigned)T), dim3(1024), 0, stream, xp, wp, bias, E, \
                                            K, top_k, sigmoid, normalize, ids, weights)
     if (dtype == SVDQ_FP16) {
-      if (E <= 64) MOE_ROUTE(true, 1); else if (E <= 128) MOE_ROUTE(true, 2); else MOE_ROUTE(true, 4);
+      if (E <= 64) MOE_ROUTE(true, 1); else MOE_ROUTE(true, 2);
     } else {
-      if (E <= 64) MOE_ROUTE(false, 1); else if (E <= 128) MOE_ROUTE(false, 2); else MOE_ROUTE(false, 4);
+      if (E <= 64) MOE_ROUTE(false, 1); else MOE_ROUTE(false, 2);
     }
 #undef MOE_ROUTE
     return launch_status("router launch");
