@@ -944,6 +944,8 @@ __global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2)))
 // 7168 x 2048) 38.6 and 33.7.  With more experts the other form's workgroups
 // are enough: 12 tokens with one of 32 experts of 2048 x 512 17.2 and 16.1, 8 with
 // one of 64 of 2048 x 768 15.3 and 16.3.
+// kMoeFewPairs is the rows of its tile; with 16 pairs of 8 experts of 2048 x 768
+// 16.1 and 16.8 us, of 4 experts 13.2 and 15.0.
 constexpr int kFewSteps = 64, kFewExperts = 8;
 constexpr int kFewGateParts = 4, kFewDownWaves = 8;     // wavefronts a workgroup (8 and 16: 19.9 and 16.6 us)
 template <int TILES>
@@ -1307,13 +1309,16 @@ svdq_status_t awq_moe_forward(const awq_moe_weights_t *w, const void *x, svdq_dt
     return launch_status("expert layer launch");
   }
   // Blocks of 32 rows from 12 pairs an expert on: an expert of more than 16 rows
-  // then reads its weights once, not twice.
+  // then reads its weights once, not twice.  16 experts of 2048 x 704, blocks of 16
+  // and of 32: 10 pairs an expert 23.9 and 29.7 us, 12 30.9 and 30.0, 14 31.6 and 30.3, 16
+  // 36.2 and 30.6; 8 of 4096 x 3584: 10 49.9 and 65.0, 12 61.4 and 66.2, 16 84.0 and 67.5.
   const bool many = pairs > 12 * slots;
   // Up to 5 pairs an expert, both pieces of h in one tile: 12 tokens with 6 of 64
   // experts took 57.3 us against 62.6, 8 with 2 of 8 45 against 51; at 8 pairs an
   // expert, where four experts in ten have more than 8 rows, 108 against 92.  (The
   // rule knows the average only: an expert's down weights are read once per 8
-  // of its rows however many those are.)
+  // of its rows however many those are.  128 tokens that all choose the same one of
+  // 128 experts of 2048 x 768 take 186 us, 132 in the other form.)
   const bool packed = pairs <= 5 * slots;
   // Few tiles: K in parts for the wavefronts of a workgroup.  With 256 and 512
   // tiles of gate and up 16.2 and 26.5 us in four parts, 20.2 and 31.5 in one;
