@@ -435,7 +435,8 @@ svdq_status_t svdq_kv4_read(const svdq_kv4_cache_t *cache, const int32_t *slots,
  * seq_lens [B] are int32 device arrays; a length past the table's end counts
  * up to it and a negative one as 0, and a page outside the cache hides its
  * tokens.  B <= 65536, Hq a multiple of kv_heads, Q g <= 1024, B Q Hq <= 2^24,
- * |scale| < 2^127.
+ * |scale| < 2^127, table_width page_size <= 2^30, and
+ * (table_width page_size / 128 + 3) B kv_heads ceil(Q g / 32) <= 2^31 - 1025.
  * Scores, softmax statistics and sums are float32; the weights p enter the
  * product with 16 significant bits.  The result does not depend on the
  * order in which workgroups run.  Two kernels; the workspace needs no

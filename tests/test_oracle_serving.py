@@ -269,3 +269,15 @@ def test_expert_blob_refusals():
     assert on_device(q=0) == INV and on_device(s=0) == INV and on_device(blob=0) == INV and on_device(q=FAKE + 8) == INV
     assert on_device(z=FAKE + 1) == INV and on_device(blob=FAKE + 4) == INV and on_device(K=96) == SHAPE
     assert on_device(E=0) == SHAPE and on_device(n=blob.size - 1) == WS
+
+
+def test_attention_refuses_tables_past_its_token_numbers():
+    """A length past 2^30 tokens would be cut off there, and a line of work past 2^31 would wrap.  (The calls have no
+    workspace, so one that is taken ends there.)"""
+    def attend(B, width, page=64, Q=1, Hq=8):
+        return S._lib.svdq_kv4_attention(ctypes.byref(_cache(page=page)), FAKE, 1024, 1024, 128, S.BF16, B, Q, Hq, FAKE,
+                                         width, FAKE, 0.1, FAKE, FAKE, 0, None)
+    assert attend(1, (1 << 24) + 1) == SHAPE and attend(1, (1 << 22) + 1, page=256) == SHAPE and attend(1, 2 ** 31 - 1) == SHAPE
+    assert attend(65536, 1 << 16) == SHAPE and attend(1000, 1 << 17, Q=256) == SHAPE
+    assert attend(1, 1 << 24) == WS and attend(1, 1 << 22, page=256) == WS and attend(65536, 1 << 10) == WS
+    assert attend(1000, 1 << 15, Q=256) == WS

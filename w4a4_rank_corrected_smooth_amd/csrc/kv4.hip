@@ -300,7 +300,7 @@ struct AttendArgs {
 };
 
 __device__ __forceinline__ int seq_len(const AttendArgs &a, int b) {
-  return min(max(a.lens[b], 0), (int)min((int64_t)a.width << a.L.page_shift, (int64_t)1 << 30));
+  return min(max(a.lens[b], 0), a.width << a.L.page_shift);
 }
 __device__ __forceinline__ int seq_chunks(int len) { return max(1, (len + kKv4Chunk - 1) / kKv4Chunk); }
 
@@ -1004,9 +1004,15 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
   if (st != SVDQ_OK) return st;
   if (dtype != SVDQ_BF16 && dtype != SVDQ_FP16)
     return fail(SVDQ_ERR_INVALID_ARGUMENT, "svdq_kv4_attention: dtype must be SVDQ_BF16 or SVDQ_FP16");
-  if (!kv4_query_ok(B, Q, Hq, L.H) || table_width < 1)
+  if (!kv4_query_ok(B, Q, Hq, L.H) || table_width < 1 || (int64_t)table_width << L.page_shift > kKv4MaxTokens)
     return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_attention: B=%d Q=%d Hq=%d over %d heads, page table of %d columns",
                 B, Q, Hq, L.H, table_width);
+  const int rows = Q * (Hq / L.H), block = rows > 16 ? 32 : rows > 8 ? 16 : 8, row_blocks = (rows + block - 1) / block;
+  // the chunks of the longest sequences that the table can name, on the kernels' 32-bit line
+  const int64_t chunks = (((int64_t)table_width << L.page_shift) + kKv4Chunk - 1) / kKv4Chunk;
+  if ((chunks + kKv4Start) * B * L.H * row_blocks + kKv4Groups > 0x7FFFFFFF)
+    return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_attention: B=%d Q=%d Hq=%d with a page table of %d columns is too much work",
+                B, Q, Hq, table_width);
   if (B == 0) return SVDQ_OK;
   if (!q || !page_table || !seq_lens || !out || !workspace)
     return fail(SVDQ_ERR_INVALID_ARGUMENT, "svdq_kv4_attention: NULL pointer");
@@ -1035,10 +1041,9 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
   a.B = B;
   a.Q = Q;
   a.group = Hq / L.H;
-  a.rows = a.group * Q;
-  const int block = a.rows > 16 ? 32 : a.rows > 8 ? 16 : 8;
-  a.row_blocks = (a.rows + block - 1) / block;
-  a.block_rows = a.rows < block ? a.rows : block;
+  a.rows = rows;
+  a.row_blocks = row_blocks;
+  a.block_rows = rows < block ? rows : block;
   // Maxima are taken of the bare products, so the scale's sign goes to the
   // queries, and a scale of zero becomes one that still hides masked scores.
   a.scale = fmaxf((float)(fabs((double)scale) * 1.4426950408889634), 1e-37f);
@@ -1046,11 +1051,7 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
   a.out = static_cast<uint16_t *>(out);
   a.part = static_cast<float *>(workspace);
   // no more workgroups than there can be chunks
-  const int64_t chunks = (((int64_t)table_width << L.page_shift) + kKv4Chunk - 1) / kKv4Chunk;
-  const int64_t most = chunks * B * L.H * a.row_blocks;
-  if ((chunks + kKv4Start) * B * L.H * a.row_blocks + kKv4Groups > 0x7FFFFFFF)
-    return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_kv4_attention: B=%d Q=%d Hq=%d with a page table of %d columns is too much work",
-                B, Q, Hq, table_width);
+  const int64_t most = chunks * B * L.H * row_blocks;
   const int resident = 256 * kv4_waves(L.D, block);
   a.W = (int)(most < resident ? most : resident);
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
@@ -1059,9 +1060,9 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
   // with a wavefront (rows, pieces on average): 128 and 24 74.5 and 75.7 us; 512 and 24
   // 17.1 and 18.9; 384 and 8 41.4 and 41.7; 1024 and 16 45.1 and 45.6; 1024 and 12 23.3
   // and 23.0; 768 and 4 42.9 and 42.5; 1536 and 6 23.6 and 22.6; 2560 and 4 29.7 and 26.7.
-  const int64_t rows = (int64_t)B * Q * Hq;
-  const bool wide_join = rows * B * L.H * a.row_blocks <= 64ll * a.W;
-  const dim3 join_grid((unsigned)(wide_join ? rows : (rows + 3) / 4));
+  const int64_t all_rows = (int64_t)B * Q * Hq;
+  const bool wide_join = all_rows * B * L.H * row_blocks <= 64ll * a.W;
+  const dim3 join_grid((unsigned)(wide_join ? all_rows : (all_rows + 3) / 4));
 #define KV4_GO(DD, NN, FF)                                                                                  \
   do {                                                                                                      \
     if (Q > 1) hipLaunchKernelGGL((kv4_attend_kernel<DD, NN, FF, true>), dim3(a.W), dim3(256), 0, stream, a); \

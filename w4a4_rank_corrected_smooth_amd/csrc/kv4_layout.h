@@ -23,6 +23,9 @@ constexpr int kKv4Groups = 256 * 4;
 // 15.5 and 15.4).
 constexpr int kKv4Chunk = 128;
 constexpr int kKv4Start = 2;
+// Tokens that a row of a page table names at most: token numbers, and those up to two
+// chunks on, are 32-bit integers.
+constexpr int64_t kKv4MaxTokens = (int64_t)1 << 30;
 // Rows (new tokens times query heads of one key/value head) at most.
 constexpr int kKv4MaxRows = 1024;
 
