@@ -281,3 +281,25 @@ def test_attention_refuses_tables_past_its_token_numbers():
     assert attend(65536, 1 << 16) == SHAPE and attend(1000, 1 << 17, Q=256) == SHAPE
     assert attend(1, 1 << 24) == WS and attend(1, 1 << 22, page=256) == WS and attend(65536, 1 << 10) == WS
     assert attend(1000, 1 << 15, Q=256) == WS
+
+
+def test_wrappers_refuse_sizes_past_32_bits():
+    """2^32 + n would reach the library as n."""
+    more = 1 << 32
+    for bad in ((more + 4, 16, 2, 64), (4, more + 16, 2, 64), (4, 16, more + 2, 64), (4, 16, 2, more + 64), (4 - more, 16, 2, 64)):
+        with pytest.raises(ValueError, match="32-bit"):
+            S.Kv4Cache(*bad, device="meta")
+    cache = S.Kv4Cache(4, 16, 2, 64, device="meta")
+    rows = torch.empty(more + 1, 2, 64, dtype=torch.bfloat16, device="meta")
+    slots = torch.empty(more + 1, dtype=torch.int32, device="meta")
+    for call in (lambda: S.kv4_append(cache, rows, rows, slots), lambda: S.kv4_read(cache, slots),
+                 lambda: S.kv4_attention_workspace(cache, torch.empty(more + 1, 1, 2, 64, device="meta")),
+                 lambda: S.kv4_attention(cache, rows[:1, None], slots[None], slots[:1]),
+                 lambda: S.moe_route(rows[:, 0, :8].contiguous(), rows[:4, 0, :8].contiguous(), 2)):
+        with pytest.raises(ValueError, match="32-bit"):
+            call()
+    part = [np.zeros((1, 128, 64), np.uint8), np.ones((1, 128, 2), np.float16), np.zeros((1, 128, 2), np.float16)]
+    layer = S.AwqMoe(part, [np.zeros((1, 128, 32), np.uint8), *(a[..., :1] for a in part[1:])], device="cpu")
+    for sizes in ((more + 3, 2), (3, more + 2)):
+        with pytest.raises(ValueError, match="32-bit"):
+            layer.new_workspace(*sizes)

@@ -724,6 +724,12 @@ def _need_dense(t, name: str, device, dtype, shape) -> None:
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
+def _need_int(n: int, name: str) -> None:
+    """A size that the library takes as an int: of a larger one ctypes would pass the lowest 32 bits."""
+    if not -0x80000000 <= n <= 0x7FFFFFFF:
+        raise ValueError(f"{name}={n} is no 32-bit integer")
+
+
 def _need_workspace(t, device) -> None:
     if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
@@ -749,6 +755,8 @@ class Kv4Cache:
     bookkeeping."""
 
     def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
+        for n, name in ((num_pages, "num_pages"), (page_size, "page_size"), (kv_heads, "kv_heads"), (head_dim, "head_dim")):
+            _need_int(n, name)
         n = _lib.svdq_kv4_cache_bytes(num_pages, page_size, kv_heads, head_dim)
         if n == 0:
             raise SvdqError(2, "svdq_kv4_cache_bytes")
@@ -776,6 +784,7 @@ def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
             raise ValueError(f"{name} must be [T, {H}, {D}] with adjacent channels, "
                              f"got {tuple(t.shape)} with strides {t.stride()}")
     T = k.size(0)
+    _need_int(T, "rows")
     if v.size(0) != T or v.dtype != k.dtype:
         raise ValueError("k and v must have the same rows and dtype")
     _need_dense(slots, "slots", dev, torch.int32, (T,))
@@ -797,6 +806,7 @@ def kv4_read(cache: Kv4Cache, slots: torch.Tensor, dtype=torch.bfloat16):
     if not slots.is_contiguous():
         raise ValueError("slots must be contiguous")
     T = slots.size(0)
+    _need_int(T, "slots")
     k = torch.empty((T, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev)
     v = torch.empty_like(k)
     _call(dev, _lib.svdq_kv4_read, cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
@@ -806,6 +816,8 @@ def kv4_read(cache: Kv4Cache, slots: torch.Tensor, dtype=torch.bfloat16):
 
 def kv4_attention_workspace(cache: Kv4Cache, q: torch.Tensor) -> torch.Tensor:
     """A workspace for kv4_attention calls with queries shaped like q [B, Q, Hq, head_dim]."""
+    for n in q.shape:
+        _need_int(n, "a size of q")
     n = _lib.svdq_kv4_attention_workspace_bytes(q.shape[0], q.shape[1], q.shape[2], cache.kv_heads, cache.head_dim)
     if n == 0:
         raise SvdqError(2, "svdq_kv4_attention_workspace_bytes")
@@ -825,6 +837,7 @@ def kv4_attention(cache: Kv4Cache, q: torch.Tensor, page_table: torch.Tensor, se
     if D != cache.head_dim or q.stride(3) != 1:
         raise ValueError(f"q must have {cache.head_dim} adjacent channels, got {tuple(q.shape)} with strides {q.stride()}")
     _need(page_table, "page_table", dev, (torch.int32,), 2)
+    _need_int(page_table.shape[1], "page_table columns")
     if page_table.shape[0] != B or not page_table.is_contiguous():
         raise ValueError(f"page_table must be contiguous with {B} rows, got {tuple(page_table.shape)}")
     _need_dense(seq_lens, "seq_lens", dev, torch.int32, (B,))
@@ -862,6 +875,7 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, bias: Optiona
     if not x.is_contiguous() or not w_router.is_contiguous() or w_router.shape[1] != K:
         raise ValueError(f"x and w_router must be contiguous [T, K] and [E, K], got {tuple(x.shape)} and "
                          f"{tuple(w_router.shape)}")
+    _need_int(max(T, E, K), "a size of x or w_router")
     if score not in MOE_SCORES:
         raise ValueError(f"score must be one of {tuple(MOE_SCORES)}, got {score!r}")
     if bias is not None:
@@ -935,6 +949,8 @@ class AwqMoe:
         self._ref = ctypes.byref(self._w)
 
     def workspace_bytes(self, T: int, top_k: int) -> int:
+        _need_int(T, "T")
+        _need_int(top_k, "top_k")
         n = _lib.awq_moe_workspace_bytes(T, top_k, self.K, self.I)
         if n == 0:
             raise SvdqError(2, "awq_moe_workspace_bytes")
