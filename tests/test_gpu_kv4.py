@@ -476,3 +476,37 @@ def test_a_row_of_infinite_scores_is_not_a_row_without_tokens(S, Q, group, D, dt
             assert torch.isnan(got[seq, i, 1]).all() if sees else not got[seq, i, 1].any(), (seq, i)
     got[:, :, 1] = want[:, :, 1]
     assert torch.equal(got, want)
+
+
+def test_attention_of_thousands_of_sequences(S):
+    """A batch of many short sequences, every fifth slot of it empty."""
+    r = np.random.default_rng(90)
+    lens = [0 if b % 5 == 3 else int(x) for b, x in enumerate(r.integers(1, 40, 3000))]
+    b = Batch(S, 91, lens, 1, 64, 16, "bf16")
+    q = b.queries(1, 2)
+    announce("kv4 attention of 3000 sequences")
+    got = S.kv4_attention(b.cache, q, b.table, b.seq_lens)
+    check(got, q, b, 0.125)
+    assert not got[3::5].any()
+
+
+@pytest.mark.parametrize("Q,group,H,D,lens,dtype", [
+    (128, 8, 1, 64, [300, 130, 100], "bf16"), (256, 4, 1, 128, [256], "fp16"), (64, 8, 2, 128, [65, 400], "bf16"),
+    (1024, 1, 1, 64, [1500, 700], "fp16"), (33, 31, 1, 64, [90], "bf16"), (130, 4, 1, 256, [140, 20], "fp16")])
+def test_attention_of_a_prompts_chunk(S, Q, group, H, D, lens, dtype):
+    """Up to 1024 rows of a key/value head, sequences shorter than the chunk among them."""
+    announce(f"kv4 attention of {Q} new tokens of {H * group} heads, D={D} {dtype}")
+    b = Batch(S, 92, lens, H, D, 16, dtype)
+    q = b.queries(Q, H * group)
+    check(S.kv4_attention(b.cache, q, b.table, b.seq_lens), q, b, D ** -0.5)
+
+
+def test_attention_of_expanded_queries(S):
+    """One token's query for every sequence, and one head's for all, by strides of zero."""
+    b = Batch(S, 93, [200, 31, 64], 2, 64, 32, "fp16")
+    q = b.queries(1, 8)
+    announce("kv4 attention of expanded queries")
+    for e in (q[:1].expand(3, 1, 8, 64), q[:, :, :1].expand(3, 1, 8, 64)):
+        got = S.kv4_attention(b.cache, e, b.table, b.seq_lens)
+        check(got, e, b, 0.125)
+        assert torch.equal(got, S.kv4_attention(b.cache, e.contiguous(), b.table, b.seq_lens))

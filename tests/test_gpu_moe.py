@@ -448,3 +448,49 @@ def test_expert_layer_of_small_rows(S, T, E):
     ids = torch.from_numpy(r.integers(0, E, (T, 1)).astype(np.int32)).cuda()
     wt = torch.ones(T, 1, device="cuda")
     check(S.awq_moe_forward(layer, x, ids, wt), x, parts, ids, wt, "silu")
+
+
+@pytest.mark.parametrize("T,k", [(5, 3), (16, 1), (1, 16), (2, 8)])
+def test_expert_layer_of_few_pairs_outside_and_twice(S, T, k):
+    """Experts named twice, three times and not at all by a call of up to 16 pairs."""
+    r = np.random.default_rng(34)
+    E, K, I = 4, 128, 64
+    parts = experts(r, E, K, I)
+    layer = device_layer(S, parts)
+    for dtype in DT.values():
+        x = torch.from_numpy(r.standard_normal((T, K))).to(dtype).cuda()
+        ids = torch.from_numpy(r.integers(-1, E + 1, (T, k)).astype(np.int32)).cuda()
+        ids[0] = 2
+        if T > 2:
+            ids[1], ids[2, 0] = -1, 2 ** 31 - 1
+        wt = torch.from_numpy(r.standard_normal((T, k))).float().cuda()
+        wt[(ids < 0) | (ids >= E)] = float("nan")
+        announce(f"experts: {T} tokens of {k} choices, outside and twice, {dtype}")
+        got = S.awq_moe_forward(layer, x, ids, wt)
+        check(got, x, parts, ids, wt, "silu")
+        if T > 2:
+            assert not got[1].any()
+
+
+def test_route_and_experts_on_two_streams(S):
+    r = np.random.default_rng(35)
+    E, K, I, T, k = 6, 128, 64, 40, 2
+    layer = device_layer(S, experts(r, E, K, I))
+    w = torch.from_numpy(r.standard_normal((E, K))).bfloat16().cuda()
+    xs = [torch.from_numpy(r.standard_normal((T, K))).bfloat16().cuda() for _ in range(2)]
+
+    def step(x):
+        ids, wt = S.moe_route(x, w, k)
+        return S.awq_moe_forward(layer, x, ids, wt)
+
+    want = [step(x) for x in xs]
+    torch.cuda.synchronize()
+    announce("router and experts on two streams")
+    streams, outs = [torch.cuda.Stream() for _ in xs], [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(step(xs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
