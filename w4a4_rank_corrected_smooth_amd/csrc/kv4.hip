@@ -445,9 +445,12 @@ __device__ __forceinline__ float inverse_of(float sum, float top) {
   return sum > 0.0f || sum != sum ? 1.0f / sum : top == -__builtin_inff() ? 0.0f : __builtin_nanf("");
 }
 
-// Registers: at least two wavefronts a SIMD keeps the matrix accumulators in
-// ordinary registers (with all 512 allowed, the compiler moves them to and from
-// the accumulation registers around every tile).
+// Registers: two or more wavefronts a SIMD keep the matrix accumulators in
+// ordinary registers; with all 512 of one, the compiler moves them to and from
+// the accumulation registers around every tile.  Heads of 256 with 32 rows run that
+// way all the same (128 accumulators and up to 128 words of queries a lane; two
+// wavefronts would spill them).  There, and in two fp16 forms of 16 rows, a few registers
+// that the loop over tiles does not use go to scratch memory, up to 60 bytes a lane.
 // ROWS: rows of a block at most, 8, 16 or 32.  Eight rows leave half of a
 // tile's columns free: columns 8..15 then take the second pieces of the same
 // rows (of fp16 queries, and of the weights), which halves the products of
@@ -762,7 +765,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
     // zero.  Both have no maximum yet; the first gets the lowest number for one.
 #pragma unroll
     for (int x = 0; x < NT; ++x)
-      if (__ballot(m[x] == -__builtin_inff()))
+      if (__builtin_expect(__ballot(m[x] == -__builtin_inff()) != 0, 0))
         for (int t = tw; t < t1; t += kKv4Chunk) {
           pages.load(t >> a.L.page_shift, lane);
           const Place p = locate<D>(a, pages, h, t, lane);
