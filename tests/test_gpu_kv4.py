@@ -510,3 +510,47 @@ def test_attention_of_expanded_queries(S):
         got = S.kv4_attention(b.cache, e, b.table, b.seq_lens)
         check(got, e, b, 0.125)
         assert torch.equal(got, S.kv4_attention(b.cache, e.contiguous(), b.table, b.seq_lens))
+
+
+def test_attention_at_the_largest_sizes(S):
+    """65536 sequences, most of them empty or one token long, and 1024 key/value heads."""
+    r = np.random.default_rng(94)
+    B, pages, D = 65536, 40, 64
+    cache = S.Kv4Cache(pages, 16, 1, D)
+    k, v = rows(r, (pages * 16, 1, D), "bf16"), rows(r, (pages * 16, 1, D), "bf16")
+    S.kv4_append(cache, k, v, torch.arange(pages * 16, dtype=torch.int32, device="cuda"))
+    lens = r.integers(0, 3, B)
+    lens[[0, 777, B - 1]] = 16
+    table = r.integers(0, pages, (B, 1)).astype(np.int32)
+    q = torch.from_numpy(r.standard_normal((B, 1, 1, D))).to(torch.bfloat16).cuda()
+    announce("kv4 attention of 65536 sequences")
+    got = S.kv4_attention(cache, q, torch.from_numpy(table).cuda(), torch.from_numpy(lens.astype(np.int32)).cuda())
+    kv, vv = O.values(f64(k)), O.values(f64(v))
+    bb = type("B", (), dict(k=[kv[16 * t[0]:16 * t[0] + n] for t, n in zip(table, lens)],
+                            v=[vv[16 * t[0]:16 * t[0] + n] for t, n in zip(table, lens)], lens=lens))
+    check(got, q, bb, 0.125)
+    announce("kv4 attention of 1024 heads")
+    b = Batch(S, 95, [20, 0, 33], 1024, D, 16, "fp16")
+    q = b.queries(1, 1024)
+    check(S.kv4_attention(b.cache, q, b.table, b.seq_lens), q, b, 0.125)
+
+
+@pytest.mark.parametrize("Q,group", [(1, 4), (1, 16), (3, 7)])
+def test_attention_of_the_smallest_keys_and_values(S, Q, group):
+    """Blocks of the smallest scales, whose numbers are bf16's subnormal ones, under large queries."""
+    r = np.random.default_rng(96)
+    lens, D = [100, 7], 64
+    b = Batch(S, 97, lens, 1, D, 16, "bf16")
+    n = b.pages * 16
+    k = torch.from_numpy(r.standard_normal((n, 1, D)) * 2.0 ** -127).to(torch.bfloat16).cuda()
+    v = torch.from_numpy(r.standard_normal((n, 1, D)) * 2.0 ** -100).to(torch.bfloat16).cuda()
+    S.kv4_append(b.cache, k, v, torch.arange(n, dtype=torch.int32, device="cuda"))
+    kv, vv = O.values(f64(k)), O.values(f64(v))
+    t = b.table.cpu().numpy()
+    for s, m in enumerate(lens):
+        at = t[s, np.arange(m) // 16] * 16 + np.arange(m) % 16
+        b.k[s], b.v[s] = kv[at], vv[at]
+    assert (np.abs(kv[kv != 0]) < 2.0 ** -126).any()
+    q = b.queries(Q, group, 2.0 ** 112)
+    announce(f"kv4 attention of the smallest keys, {Q * group} rows")
+    check(S.kv4_attention(b.cache, q, b.table, b.seq_lens, scale=2.0 ** 12), q, b, 2.0 ** 12)

@@ -494,3 +494,44 @@ def test_route_and_experts_on_two_streams(S):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,E,K,k", [(65535, 3, 8, 2), (2, 4, 1 << 20, 2), (1, 1024, 8, 32), (24576, 1, 8, 1), (300, 1024, 8, 1)])
+def test_route_at_the_largest_sizes(S, T, E, K, k, dtype):
+    announce(f"route T={T} E={E} K={K} k={k} {dtype}")
+    r = np.random.default_rng(K)
+    x = torch.from_numpy(r.standard_normal((T, K))).to(DT[dtype]).cuda()
+    w = torch.from_numpy(r.standard_normal((E, K)) / np.sqrt(K)).to(DT[dtype]).cuda()
+    ids, wt = S.moe_route(x, w, k)
+    rid, rwt = O.route(f64(x), f64(w), k)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    assert (np.abs(f64(wt) - rwt) <= (2.0 ** -24 + 2.0 ** -40) * rwt + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("T,E,K,I,k", [(1, 2, 32768, 64, 2), (20, 2, 32768, 64, 1), (1, 2, 64, 16384, 2), (40, 3, 64, 16384, 2)])
+def test_expert_layer_of_long_rows(S, T, E, K, I, k):
+    announce(f"experts of long rows T={T} E={E} K={K} I={I} k={k}")
+    r = np.random.default_rng(K + I)
+    parts = experts(r, E, K, I)
+    layer = device_layer(S, parts)
+    for dtype in DT.values():
+        x = torch.from_numpy(r.standard_normal((T, K))).to(dtype).cuda()
+        ids = torch.from_numpy(np.stack([r.permutation(E)[:k] for _ in range(T)]).astype(np.int32)).cuda()
+        wt = torch.from_numpy(r.random((T, k)) + 0.05).float().cuda()
+        check(S.awq_moe_forward(layer, x, ids, wt), x, parts, ids, wt, "silu")
+
+
+@pytest.mark.parametrize("T", [1, 20, 90])
+def test_expert_layer_of_subnormal_rows(S, T):
+    """fp16 rows below 2^-14 under large scales."""
+    announce(f"experts of subnormal fp16 rows, T={T}")
+    r = np.random.default_rng(T + 9)
+    parts = experts(r, 3, 128, 64)
+    for p in parts:
+        p[1][:] = (p[1].astype(np.float64) * 2.0 ** 12).astype(np.float16)
+    layer = device_layer(S, parts)
+    x = torch.from_numpy(r.standard_normal((T, 128)) * 2.0 ** -18).half().cuda()
+    ids = torch.from_numpy(r.integers(0, 3, (T, 1)).astype(np.int32)).cuda()
+    wt = torch.ones(T, 1, device="cuda")
+    check(S.awq_moe_forward(layer, x, ids, wt), x, parts, ids, wt, "silu")
