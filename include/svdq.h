@@ -448,6 +448,48 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
                                  const int32_t *page_table, int table_width, const int32_t *seq_lens, float scale,
                                  void *out, void *workspace, size_t ws_bytes, void *hip_stream);
 
+/* ====================================================== rotary positions
+ * Rotation of query and key rows by positions with one to eight axes (a
+ * text's, a picture's height and width, a video's time too).  Pair j of a row of
+ * head_dim channels turns by the angle positions[t, axis[j]] * freq[j] radians:
+ *   (a, b) -> (a cos - b sin, a sin + b cos)
+ * where (a, b) are channels 2 j and 2 j + 1 (`interleaved`) or j and pairs + j.
+ * Channels from 2 pairs on stay as they are. */
+#define SVDQ_ROTARY_MAX_PAIRS 128
+#define SVDQ_ROTARY_MAX_AXES 8
+typedef struct {
+  int32_t head_dim, pairs, axes, interleaved;
+  double freq[SVDQ_ROTARY_MAX_PAIRS];   /* radians for a step of one */
+  uint8_t axis[SVDQ_ROTARY_MAX_PAIRS];  /* 0..axes - 1 */
+} svdq_rotary_t;
+
+/* Fills a plan (host): axis a owns widths[a] / 2 consecutive pairs, with freq =
+ * theta^(-2 i / widths[a]) for the i-th of them (`per_axis`) or theta^(-2 j /
+ * sum(widths)) for pair j of the whole row.  widths even and positive, their
+ * sum at most head_dim; head_dim a multiple of 8 up to 256; theta positive and finite.
+ * A caller with other frequencies or another order of the axes fills the
+ * struct itself. */
+svdq_status_t svdq_rotary_plan(int head_dim, const int32_t *widths, int axes, double theta, int interleaved,
+                               int per_axis, svdq_rotary_t *plan);
+
+/* Turns T rows of q_heads query heads and k_heads key heads (bf16 or fp16,
+ * device): row t's head h of q starts at q + t q_row + h q_head elements, its
+ * channels next to each other, and goes to q_out + t q_out_row + h q_out_head; k
+ * likewise.  q_out may be q with the same strides (in place), and k_out k; other
+ * overlaps of what is read and written are the caller's to avoid.  Either may be
+ * absent (no heads; its pointers are not looked at).  positions [T, axes] is int32, or
+ * float32 if `float_positions` (device, dense); a negative position turns
+ * backwards, which is also the rotation's transpose.  Pointers are 16-byte aligned (positions 4) and
+ * strides multiples of 8 elements, not negative.  Angles are
+ * float64, reduced to a turn exactly; sines, cosines and the products float32, and
+ * the result is rounded once.  T (q_heads + k_heads) head_dim <= 2^34 and
+ * q_heads + k_heads <= 65536.  One kernel. */
+svdq_status_t svdq_rotary_apply(const svdq_rotary_t *plan, const void *q, int64_t q_row, int64_t q_head, int q_heads,
+                                void *q_out, int64_t q_out_row, int64_t q_out_head, const void *k, int64_t k_row,
+                                int64_t k_head, int k_heads, void *k_out, int64_t k_out_row, int64_t k_out_head,
+                                svdq_dtype_t dtype, const void *positions, int float_positions, int T,
+                                void *hip_stream);
+
 /* ============================================================== AWQ W4A16
  * "Bringing Nunchaku 4-bit diffusion inference to Diffusers" (Russian
  * edition, technical-details section; Korean edition, "Diffusers 내

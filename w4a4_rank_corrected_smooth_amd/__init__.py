@@ -56,6 +56,7 @@ EXPORTS = [
     "svdq_kv4_cache_bytes", "svdq_kv4_append", "svdq_kv4_read", "svdq_kv4_attention_workspace_bytes",
     "svdq_kv4_attention", "svdq_moe_route_workspace_bytes", "svdq_moe_route",
     "awq_moe_device_weights_bytes", "awq_moe_pack_device_weights", "awq_moe_pack_on_device", "awq_moe_workspace_bytes", "awq_moe_forward",
+    "svdq_rotary_plan", "svdq_rotary_apply",
 ]
 
 
@@ -79,6 +80,11 @@ class DeviceWeights(ctypes.Structure):
 class Kv4CacheStruct(ctypes.Structure):
     _fields_ = [("data", _vp), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class RotaryStruct(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("pairs", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("freq", ctypes.c_double * 128), ("axis", ctypes.c_uint8 * 128)]
 
 
 class MoeWeights(ctypes.Structure):
@@ -148,6 +154,9 @@ _sig("svdq_kv4_read", _i, [_C, _vp, _i, _vp, _vp, _i, _vp])
 _sig("svdq_kv4_attention_workspace_bytes", _sz, [_i, _i, _i, _i, _i])
 _sig("svdq_kv4_attention", _i, [_C, _vp, _i64, _i64, _i64, _i, _i, _i, _i, _vp, _i, _vp, ctypes.c_float, _vp, _vp,
                                 _sz, _vp])
+_sig("svdq_rotary_plan", _i, [_i, _vp, _i, ctypes.c_double, _i, _i, ctypes.POINTER(RotaryStruct)])
+_sig("svdq_rotary_apply", _i, [ctypes.POINTER(RotaryStruct), *[_vp, ctypes.c_int64, ctypes.c_int64, _i, _vp, ctypes.c_int64, ctypes.c_int64] * 2,
+                               _i, _vp, _i, _i, _vp])
 _sig("svdq_moe_route_workspace_bytes", _sz, [_i, _i])
 _sig("svdq_moe_route", _i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp])
 _sig("awq_moe_device_weights_bytes", _sz, [_i, _i, _i])
@@ -855,6 +864,93 @@ def kv4_attention(cache: Kv4Cache, q: torch.Tensor, page_table: torch.Tensor, se
           seq_lens.data_ptr(), D ** -0.5 if scale is None else float(scale), out.data_ptr(), workspace.data_ptr(),
           workspace.numel())
     return out
+
+
+# -------------------------------------------------------- rotary positions
+class RotaryPlan:
+    """How rows of head_dim channels turn with positions of several axes: axis a
+    owns widths[a] / 2 consecutive pairs, turning by theta^(-2 i / widths[a]) radians a step
+    for the i-th of them (per_axis), or by one ladder theta^(-2 j / sum(widths)) over
+    all pairs.  A pair is two neighbouring channels (interleaved) or channels j and
+    j + sum(widths) / 2; channels past sum(widths) stay."""
+
+    def __init__(self, head_dim: int, widths, theta: float = 10000.0, interleaved: bool = True, per_axis: bool = True):
+        widths = [int(w) for w in widths]
+        for n in (head_dim, len(widths), *widths):
+            _need_int(n, "a size of the plan")
+        self._c = RotaryStruct()
+        self._ref = ctypes.byref(self._c)
+        w = (ctypes.c_int32 * max(1, len(widths)))(*widths)
+        _check(_lib.svdq_rotary_plan(head_dim, ctypes.addressof(w), len(widths), float(theta), int(bool(interleaved)),
+                                     int(bool(per_axis)), self._ref), "svdq_rotary_plan")
+        self.head_dim, self.axes, self.pairs = head_dim, len(widths), self._c.pairs
+
+    @classmethod
+    def from_tables(cls, head_dim: int, freq, axis, interleaved: bool = True) -> "RotaryPlan":
+        """A plan with each pair's own frequency (radians a step) and axis: scaled
+        ladders, axes that take turns."""
+        freq, axis = [float(f) for f in freq], [int(x) for x in axis]
+        _need_int(head_dim, "head_dim")
+        if head_dim < 8 or head_dim % 8 or not 1 <= len(freq) <= min(128, head_dim // 2) or len(axis) != len(freq):
+            raise ValueError(f"{len(freq)} frequencies and {len(axis)} axes do not fit head_dim={head_dim}")
+        if min(axis) < 0 or max(axis) > 7 or not all(np.isfinite(freq)):
+            raise ValueError("axes must be in 0..7 and frequencies finite")
+        self = cls.__new__(cls)
+        self.head_dim, self.axes, self.pairs = head_dim, max(axis) + 1, len(freq)
+        self._c = RotaryStruct(head_dim, len(freq), max(axis) + 1, int(bool(interleaved)))
+        self._c.freq[:len(freq)], self._c.axis[:len(axis)] = freq, axis
+        self._ref = ctypes.byref(self._c)
+        return self
+
+
+_NO_ROWS = (None, 0, 0, 0, None, 0, 0)
+
+
+def _rotary_rows(x, name: str, dev, T: int, D: int, dtype, out):
+    """One of the two operands of svdq_rotary_apply, with its output."""
+    for t, n in ((x, name), (out, name + "_out")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+        if t.dtype != dtype or t.dim() != 3 or t.size(0) != T or t.size(2) != D or t.device != dev or (t.numel() and t.stride(2) != 1):
+            raise ValueError(f"{n} must be [{T}, heads, {D}] {dtype} with adjacent channels on {dev}, "
+                             f"got {tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
+    H = x.size(1)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=dtype, device=dev)
+    elif out.size(1) != H:
+        raise ValueError(f"{name}_out has {out.size(1)} heads, {name} {H}")
+    # torch leaves any stride where there is one element
+    strides = [0 if n == 1 else t.stride(i) for t in (x, out) for i, n in ((0, T), (1, H))]
+    return out, (x.data_ptr(), strides[0], strides[1], H, out.data_ptr(), strides[2], strides[3])
+
+
+def rotary_apply(plan: RotaryPlan, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Query rows q [T, Hq, head_dim] and key rows k [T, Hk, head_dim] (bf16 or fp16;
+    any row and head strides that are multiples of 8; k may be None) turned by
+    positions [T, axes] (int32 or float32): (q_out, k_out), new dense tensors unless
+    given.  q_out=q, k_out=k turns in place.  Negative positions turn backwards."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    dev = q.device
+    _need(q, "q", dev, _DT16, 3)
+    T, D = q.size(0), plan.head_dim
+    _need_int(max(q.shape), "a size of q")
+    _need(positions, "positions", dev, (torch.int32, torch.float32), 2)
+    if positions.size(0) != T or positions.size(1) != plan.axes or not positions.is_contiguous():
+        raise ValueError(f"positions must be contiguous [{T}, {plan.axes}], got {tuple(positions.shape)}")
+    q_out, q_args = _rotary_rows(q, "q", dev, T, D, q.dtype, q_out)
+    k_args = _NO_ROWS
+    if k is not None:
+        k_out, k_args = _rotary_rows(k, "k", dev, T, D, q.dtype, k_out)
+        _need_int(k.size(1), "k's heads")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _call(dev, _lib.svdq_rotary_apply, plan._ref, *q_args, *k_args, _DT16[q.dtype], positions.data_ptr(),
+          int(positions.dtype == torch.float32), T)
+    return q_out, k_out
 
 
 # ------------------------------------------------------- mixture of experts

@@ -289,6 +289,36 @@ size_t svdq_kv4_attention_workspace_bytes(int B, int Q, int Hq, int kv_heads, in
   return (size_t)kv4_workspace_bytes(Q, Hq, kv_heads, head_dim);
 }
 
+svdq_status_t svdq_rotary_plan(int head_dim, const int32_t *widths, int axes, double theta, int interleaved,
+                               int per_axis, svdq_rotary_t *plan) {
+  const char *who = "svdq_rotary_plan";
+  if (!widths || !plan) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: NULL pointer", who);
+  if (head_dim < 8 || head_dim % 8 != 0 || head_dim > 2 * SVDQ_ROTARY_MAX_PAIRS || axes < 1 || axes > SVDQ_ROTARY_MAX_AXES)
+    return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%s: head_dim=%d with %d axes", who, head_dim, axes);
+  if (!(theta > 0.0) || !std::isfinite(theta)) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: theta=%g", who, theta);
+  int64_t turned = 0;
+  for (int a = 0; a < axes; ++a) {
+    if (widths[a] < 2 || widths[a] % 2 != 0)
+      return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%s: axis %d of %d channels", who, a, widths[a]);
+    turned += widths[a];
+  }
+  if (turned > head_dim)
+    return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%s: axes of %lld channels in %d", who, (long long)turned, head_dim);
+  *plan = svdq_rotary_t{};
+  plan->head_dim = head_dim;
+  plan->axes = axes;
+  plan->interleaved = interleaved != 0;
+  int j = 0;
+  for (int a = 0; a < axes; ++a)
+    for (int i = 0; i < widths[a] / 2; ++i, ++j) {
+      plan->axis[j] = (uint8_t)a;
+      plan->freq[j] = std::pow(theta, per_axis ? -2.0 * i / widths[a] : -2.0 * j / (double)turned);
+      if (!std::isfinite(plan->freq[j])) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: theta=%g", who, theta);
+    }
+  plan->pairs = j;
+  return SVDQ_OK;
+}
+
 size_t svdq_moe_route_workspace_bytes(int T, int E) {
   if (!moe_route_ok(T, E, 8, 1)) {
     fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_moe_route_workspace_bytes: T=%d E=%d", T, E);
