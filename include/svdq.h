@@ -490,6 +490,36 @@ svdq_status_t svdq_rotary_apply(const svdq_rotary_t *plan, const void *q, int64_
                                 svdq_dtype_t dtype, const void *positions, int float_positions, int T,
                                 void *hip_stream);
 
+/* ======================================================== cross attention
+ * Attention of queries over an encoder's states of another length (a prompt's,
+ * a picture's, a recording's), all in 16 bits:
+ *   out[b, i, h] = sum_t p_t v[b, t, h / g] / sum_t p_t,
+ *   p_t = exp(scale q[b, i, h] . k[b, t, h / g] - max),  t visible in batch row b
+ * with g = Hq / Hkv query heads to a key/value head.  t is visible if t <
+ * key_lens[b] (int32 [B], or NULL for Lk; values past Lk count as Lk, negative ones as 0)
+ * and mask[b, t] is not zero (uint8 [B, Lk] dense, or NULL).  Rows of k and v that are not
+ * visible are not looked at, whatever they hold; a batch row that sees none gives
+ * zeros.  q[b, i, h] starts at q + b q_batch + i q_token + h q_head elements, its D
+ * channels next to each other; k and v likewise; out [B, Lq, Hq, D] dense.
+ * q, k, v and out are bf16 or fp16, all the same.  Pointers are 16-byte aligned and
+ * strides multiples of 8 elements, not negative.  D a multiple of 8 up to 256, Hq a
+ * multiple of Hkv, B <= 65536, Lk <= 2^30, B Lq Hq <= 2^28,
+ * B Hkv <= 2^20, strides of k_token and v_token below 2^24, |scale| < 2^127.
+ * Scores, softmax statistics and sums are float32; the weights p enter the
+ * product in the inputs' type (p is 1 at the largest score to within a factor of
+ * 2^8, so float16's lower end is 2^-31 below it), and out is rounded once.
+ * The result does not depend on the order in which workgroups run.  One kernel, another
+ * that lists the visible states where there is a mask, and one that joins the
+ * pieces where few queries meet many states.  The workspace (`masked`: for
+ * calls with a mask) needs no clearing and keeps nothing
+ * from one call for the next (calls that run at the same time need one each). */
+size_t svdq_cross_attention_workspace_bytes(int B, int Lq, int Lk, int Hq, int Hkv, int D, int masked);
+svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_token, int64_t q_head, const void *k,
+                                   int64_t k_batch, int64_t k_token, int64_t k_head, const void *v, int64_t v_batch,
+                                   int64_t v_token, int64_t v_head, svdq_dtype_t dtype, int B, int Lq, int Lk, int Hq,
+                                   int Hkv, int D, const int32_t *key_lens, const uint8_t *mask, float scale,
+                                   void *out, void *workspace, size_t ws_bytes, void *hip_stream);
+
 /* ============================================================== AWQ W4A16
  * "Bringing Nunchaku 4-bit diffusion inference to Diffusers" (Russian
  * edition, technical-details section; Korean edition, "Diffusers 내

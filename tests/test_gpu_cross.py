@@ -1,0 +1,246 @@
+"""Cross attention on the GPU against the float64 oracle.
+
+Tolerance.  With u half a step of the 16-bit type (eps / 2) and, per element,
+mean = sum p |v| / sum p:
+  - a score's float32 sum over D channels and its product with scale log2(e) are off
+    by at most (D + 4) 2^-23 size (size: the row's largest |scale| sum |q k|; a step of the matrix
+    instruction counted as 2^-23), the exponent's argument by 2^-23 of itself (below 2 size) and the exponential by 2^-22:
+    a relative error E of each weight, at most 2 E mean in the result;
+  - the weights are rounded to the type: u mean (float16's below 2^-14 of 2^7 by an
+    absolute 2^-25 of at least 2^7: n 2^-32 of the largest value);
+  - the two sums over n states: 2 n 2^-23 mean at most;
+  - the result is rounded: u |out|.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cross as O
+from tests.conftest import announce
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def S():
+    import w4a4_rank_corrected_smooth_amd as lib
+    lib.device_check()
+    return lib
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rows(r, shape, dtype, scale=1.0):
+    x = r.standard_normal(shape) * scale
+    x[..., ::29] *= 3.0
+    return torch.from_numpy(x).to(DT[dtype]).cuda()
+
+
+def near(got, q, k, v, visible=None, scale=None):
+    q, k, v = f64(q), f64(k), f64(v)
+    B, Lk, D = k.shape[0], k.shape[1], q.shape[3]
+    visible = np.ones((B, Lk), bool) if visible is None else visible
+    want, mean, size = O.attend(q, k, v, visible, D ** -0.5 if scale is None else scale)
+    u = torch.finfo(got.dtype).eps / 2
+    E = (D + 6) * 2.0 ** -23 * size + 2.0 ** -22
+    tol = u * np.abs(want) + (u + 2 * E + 2 * Lk * 2.0 ** -23) * mean * (1 + 2.0 ** -6)
+    if got.dtype == torch.float16:
+        vis = np.where(visible[:, :, None, None], np.abs(v), 0)
+        tol = tol + 2.0 ** -25 + Lk * 2.0 ** -32 * (vis.max() if vis.size else 0)
+    got = f64(got)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    off = np.abs(got - want)
+    fine = np.isfinite(want)
+    assert (off[fine] <= tol[fine]).all(), (off[fine].max(), (off[fine] / np.maximum(tol[fine], 1e-30)).max())
+
+
+CASES = [  # B, Lq, Lk, Hq, Hkv, D
+    (1, 1, 1, 1, 1, 64),
+    (2, 1, 1500, 4, 4, 64),
+    (3, 1, 257, 8, 2, 128),
+    (1, 32, 31, 1, 1, 96),
+    (1, 33, 33, 2, 1, 8),
+    (2, 5, 700, 6, 3, 72),
+    (1, 128, 64, 2, 2, 128),
+    (2, 129, 65, 3, 3, 128),
+    (1, 300, 1000, 2, 1, 64),
+    (1, 77, 513, 2, 2, 80),
+    (2, 64, 2050, 8, 2, 128),
+    (1, 200, 96, 2, 2, 160),
+    (1, 3, 95, 2, 2, 160),
+    (1, 140, 130, 2, 1, 256),
+    (2, 1, 999, 2, 1, 256),
+    (1, 40, 100, 2, 2, 200),
+    (1, 1000, 300, 8, 8, 72),
+    (1, 31, 4097, 1, 1, 104),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("B,Lq,Lk,Hq,Hkv,D", CASES)
+@pytest.mark.parametrize("hide", ["none", "lens", "mask", "both"])
+def test_cross_attention_against_the_oracle(S, B, Lq, Lk, Hq, Hkv, D, hide, dtype):
+    announce(f"cross B={B} Lq={Lq} Lk={Lk} Hq={Hq} Hkv={Hkv} D={D} {hide} {dtype}")
+    r = np.random.default_rng(Lq * 1000 + Lk + D)
+    q, kv = rows(r, (B, Lq, Hq, D), dtype), rows(r, (B, Lk, 2 * Hkv, D), dtype)
+    k, v = kv[:, :, :Hkv], kv[:, :, Hkv:]
+    visible = np.ones((B, Lk), bool)
+    lens = mask = None
+    if hide in ("lens", "both"):
+        n = r.integers(1, Lk + 1, B)
+        if B > 1:
+            n[1] = 0
+        lens = torch.from_numpy(n.astype(np.int32)).cuda()
+        visible &= np.arange(Lk) < n[:, None]
+    if hide in ("mask", "both"):
+        m = r.random((B, Lk)) < 0.6
+        mask = torch.from_numpy(m).cuda()
+        visible &= m
+    # what is not visible may be anything
+    hidden = torch.from_numpy(~visible).cuda()
+    k[hidden], v[hidden] = float("nan"), float("inf")
+    got = S.cross_attention(q, k, v, key_lens=lens, mask=mask)
+    assert got.shape == q.shape and got.dtype == q.dtype and got.is_contiguous()
+    k, v = k.masked_fill(hidden[..., None, None], 0), v.masked_fill(hidden[..., None, None], 0)
+    near(got, q, k, v, visible)
+    assert not got[torch.from_numpy(~visible.any(1)).cuda()].any()
+
+
+@pytest.mark.parametrize("Lq", [1, 200])
+def test_cross_attention_strides_and_scales(S, Lq):
+    """Heads before tokens, shared batches (stride 0), negative, zero and large scales."""
+    r = np.random.default_rng(3)
+    B, Lk, H, D = 2, 300, 4, 64
+    q = rows(r, (B, H, Lq, D), "bf16").transpose(1, 2)
+    k = rows(r, (1, H, Lk, D), "bf16").transpose(1, 2).expand(B, -1, -1, -1)
+    v = rows(r, (Lk, B, H, D), "bf16").transpose(0, 1)
+    for scale in (None, -0.3, 0.0, 20.0):
+        announce(f"cross of strided rows, scale {scale}, Lq={Lq}")
+        near(S.cross_attention(q, k, v, scale=scale), q, k, v, scale=scale)
+
+
+@pytest.mark.parametrize("Lq", [3, 150])
+def test_cross_attention_edge_values(S, Lq):
+    """Infinities and NaN in queries stay in their row; in visible states they reach the rows that see them."""
+    r = np.random.default_rng(4)
+    q, k, v = rows(r, (2, Lq, 2, 64), "bf16"), rows(r, (2, 70, 2, 64), "bf16"), rows(r, (2, 70, 2, 64), "bf16")
+    want = S.cross_attention(q, k, v)
+    bad = q.clone()
+    bad[0, 1, 0, 5], bad[1, 2, 1, 63] = float("nan"), float("inf")
+    announce(f"cross with a NaN and an infinity in queries, Lq={Lq}")
+    got = S.cross_attention(bad, k, v)
+    hit = torch.zeros(2, Lq, 2, dtype=torch.bool, device="cuda")
+    hit[0, 1, 0] = hit[1, 2, 1] = True
+    assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], want[~hit])
+    bv = v.clone()
+    bv[0, 69, 1, 7] = float("nan")
+    got = S.cross_attention(q, k, bv)
+    assert torch.isnan(got[0, :, 1, 7]).all()
+    got[0, :, 1, 7] = want[0, :, 1, 7]
+    assert torch.equal(got, want)
+    # scores of -inf only: 0 / 0; one finite score among them: its value
+    k2, q2 = torch.zeros_like(k), torch.ones_like(q)
+    k2[..., 0] = -float("inf")
+    k2[1, 40] = 0
+    announce(f"cross with scores of -inf, Lq={Lq}")
+    got = S.cross_attention(q2, k2, v)
+    assert torch.isnan(got[0]).all() and torch.equal(got[1], v[1, 40].expand(Lq, -1, -1))
+
+
+@pytest.mark.parametrize("Lq", [1, 130])
+def test_cross_attention_rising_scores(S, Lq):
+    """Scores that climb from tile to tile, in steps below and above the slack of the running maximum, and a late giant."""
+    r = np.random.default_rng(5)
+    Lk, D = 900, 64
+    for step in (0.02, 0.3, 3.0):
+        q = torch.ones(1, Lq, 1, D, dtype=torch.float16, device="cuda")
+        t = np.arange(Lk) * step / D
+        t[-3] += 200.0 / D
+        k = torch.from_numpy(np.broadcast_to(t[:, None], (Lk, D)).copy()).half().cuda()[None, :, None]
+        v = rows(r, (1, Lk, 1, D), "fp16")
+        announce(f"cross with scores rising by {step}, Lq={Lq}")
+        near(S.cross_attention(q, k, v, scale=1.0), q, k, v, scale=1.0)
+
+
+def test_cross_attention_many_small_weights(S):
+    """One state of weight 1 and 16000 of weight e^-17: in float16 as such they would all vanish."""
+    Lk, D = 16001, 64
+    k = torch.zeros(1, Lk, 1, D, dtype=torch.float16, device="cuda")
+    k[0, 77, 0, 0] = 17.0
+    q = torch.zeros(1, 40, 1, D, dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0
+    v = torch.full((1, Lk, 1, D), 1000.0, dtype=torch.float16, device="cuda")
+    v[0, 77] = 0.0
+    announce("cross with many small weights")
+    near(S.cross_attention(q, k, v, scale=1.0), q, k, v, scale=1.0)
+
+
+def test_cross_attention_empty_calls(S):
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    announce("cross of empty calls")
+    assert S.cross_attention(torch.empty(0, 4, 2, 64, **bf), torch.empty(0, 4, 2, 64, **bf), torch.empty(0, 4, 2, 64, **bf)).numel() == 0
+    assert S.cross_attention(torch.empty(2, 0, 2, 64, **bf), torch.empty(2, 4, 2, 64, **bf), torch.empty(2, 4, 2, 64, **bf)).numel() == 0
+    for Lq in (2, 200):
+        q = torch.ones(2, Lq, 2, 64, **bf)
+        none = torch.empty(2, 0, 2, 64, **bf)
+        assert not S.cross_attention(q, none, none).any()
+        assert not S.cross_attention(q, none, none, mask=torch.empty(2, 0, dtype=torch.bool, device="cuda")).any()
+        k = torch.ones(2, 50, 2, 64, **bf)
+        out = torch.full_like(q, 3.0)
+        assert not S.cross_attention(q, k, k, mask=torch.zeros(2, 50, dtype=torch.bool, device="cuda"), out=out).any()
+        assert not S.cross_attention(q, k, k, key_lens=torch.tensor([-5, 0], dtype=torch.int32, device="cuda")).any()
+        assert torch.equal(S.cross_attention(q, k, k, key_lens=torch.tensor([51, 1 << 30], dtype=torch.int32, device="cuda")), q)
+
+
+def test_cross_attention_large(S):
+    """Row tiles, heads and states beyond one round of workgroups, against float32 products on the GPU."""
+    B, Lq, Lk, H, D = 1, 5000, 3000, 6, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn(B, n, H, D, device="cuda", generator=g).bfloat16() for n in (Lq, Lk, Lk))
+    announce("cross of 5000 queries over 3000 states")
+    got = S.cross_attention(q, k, v)
+    for h in range(H):
+        p = torch.softmax(q[0, :, h].double() @ k[0, :, h].double().t() / D ** 0.5, -1)
+        want, mean = p @ v[0, :, h].double(), p @ v[0, :, h].double().abs()
+        # scores below 30: an error of 140 2^-23 30 in a weight, and the sums' 3000 2^-23, beside 2^-8
+        assert ((got[0, :, h].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -9) * mean).all()
+
+
+def test_cross_attention_streams_graphs_and_two_at_once(S):
+    """Two captured calls with workspaces of their own, replayed against eager results over changing inputs."""
+    r = np.random.default_rng(6)
+    shapes = [(2, 1, 900, 8, 4, 64), (1, 150, 400, 2, 2, 128)]
+    sets = []
+    for B, Lq, Lk, Hq, Hkv, D in shapes:
+        q = [rows(r, (B, Lq, Hq, D), "fp16") for _ in range(3)]
+        k, v = rows(r, (B, Lk, Hkv, D), "fp16"), rows(r, (B, Lk, Hkv, D), "fp16")
+        mask = [torch.from_numpy(r.random((B, Lk)) < x).cuda() for x in (0.9, 0.5, 0.0)]
+        sets.append((q, k, v, mask, [S.cross_attention(a, k, v, mask=m) for a, m in zip(q, mask)]))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    announce("cross on two streams")
+    got = []
+    for s, (q, k, v, mask, want) in zip(streams, sets):
+        with torch.cuda.stream(s):
+            got.append([S.cross_attention(a, k, v, mask=m) for a, m in zip(q, mask)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g, s in zip(got, sets) for a, b in zip(g, s[4]))
+    graphs = []
+    announce("cross in two graphs")
+    for q, k, v, mask, want in sets:
+        bufs = (q[0].clone(), mask[0].clone(), torch.empty_like(q[0]), S.cross_attention_workspace(q[0], k))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            S.cross_attention(bufs[0], k, v, mask=bufs[1], out=bufs[2], workspace=bufs[3])
+        graphs.append((g, bufs))
+    for i in (1, 2, 0, 1):
+        for (g, bufs), (q, k, v, mask, want) in zip(graphs, sets):
+            bufs[0].copy_(q[i])
+            bufs[1].copy_(mask[i])
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(bufs[2], s[4][i]) for (g, bufs), s in zip(graphs, sets))

@@ -103,3 +103,78 @@ def test_rotary_wrapper_checks():
     big = torch.empty((1 << 32) + 1, 1, 64, dtype=torch.bfloat16, device="meta")
     with pytest.raises(ValueError, match="32-bit"):
         S.rotary_apply(plan, big, None, torch.empty((1 << 32) + 1, 2, dtype=torch.int32, device="meta"))
+
+
+# --------------------------------------------------------- cross attention
+def test_cross_oracle_is_a_softmax():
+    from oracle import cross
+    r = np.random.default_rng(2)
+    q, k, v = r.standard_normal((2, 3, 4, 8)), r.standard_normal((2, 5, 2, 8)), r.standard_normal((2, 5, 2, 8))
+    seen = np.array([[1, 0, 1, 1, 0], [0, 0, 0, 0, 0]], bool)
+    out, mean, size = cross.attend(q, k, v, seen, 0.5)
+    for i in range(3):
+        for h in range(4):
+            e = [math.exp(0.5 * (q[0, i, h] * k[0, t, h // 2]).sum()) for t in (0, 2, 3)]
+            want = sum(x * v[0, t, h // 2] for x, t in zip(e, (0, 2, 3))) / sum(e)
+            assert np.allclose(out[0, i, h], want) and (mean[0, i, h] >= abs(want) - 1e-12).all()
+            assert size[0, i, h, 0] == pytest.approx(max(0.5 * np.abs(q[0, i, h] * k[0, t, h // 2]).sum() for t in (0, 2, 3)))
+    assert not out[1].any()
+
+
+def test_cross_workspace_and_shapes():
+    f = S._lib.svdq_cross_attention_workspace_bytes
+    assert f(1, 4096, 512, 16, 16, 128, 0) >= 1 and f(2, 4096, 300, 16, 16, 72, 1) >= 4 * 2 * 300
+    assert f(8, 1, 1500, 20, 20, 64, 0) > 0 and f(0, 0, 0, 1, 1, 8, 0) >= 1
+    for bad in ((-1, 1, 1, 1, 1, 64), (65537, 1, 1, 1, 1, 64), (1, -1, 1, 1, 1, 64), (1, 1, -1, 1, 1, 64), (1, 1, (1 << 30) + 1, 1, 1, 64),
+                (1, 1, 1, 0, 1, 64), (1, 1, 1, 1, 0, 64), (1, 1, 1, 3, 2, 64), (1, 1, 1, 1, 1, 0), (1, 1, 1, 1, 1, 60),
+                (1, 1, 1, 1, 1, 264), (2, 1 << 27, 1, 2, 1, 64), (65536, 1, 1, 17, 17, 64), (1, 2 ** 31 - 1, 1, 2 ** 31 - 1, 1, 64)):
+        assert f(*bad, 0) == 0, bad
+
+
+def test_cross_argument_errors():
+    need = S._lib.svdq_cross_attention_workspace_bytes(2, 4, 50, 4, 2, 64, 1)
+    row = dict(q=(FAKE, 1024, 256, 64), k=(FAKE, 8192, 128, 64), v=(FAKE, 8192, 128, 64))
+
+    def go(dt=S.BF16, B=2, Lq=4, Lk=50, Hq=4, Hkv=2, D=64, lens=None, mask=FAKE, scale=0.1, out=FAKE, ws=FAKE, n=need, **kw):
+        r = {**row, **kw}
+        return S._lib.svdq_cross_attention(*r["q"], *r["k"], *r["v"], dt, B, Lq, Lk, Hq, Hkv, D, lens, mask, scale, out, ws, n, None)
+    for name in "qkv":
+        p, b, t, h = row[name]
+        assert go(**{name: (0, b, t, h)}) == INV and go(**{name: (p + 8, b, t, h)}) == INV
+        for bad in ((p, b + 4, t, h), (p, b, -t, h), (p, b, t, 4)):
+            assert go(**{name: bad}) == INV
+    assert go(k=(FAKE, 0, 1 << 24, 64)) == SHAPE and go(v=(FAKE, 0, 1 << 24, 64)) == SHAPE
+    assert go(dt=S.FP32) == INV and go(out=0) == INV and go(out=FAKE + 2) == INV and go(ws=0) == INV and go(ws=FAKE + 8) == INV
+    assert go(lens=FAKE + 2) == INV and go(n=need - 1) == WS and go(D=68) == SHAPE and go(Hq=3) == SHAPE and go(B=-1) == SHAPE
+    for scale in (math.inf, -math.inf, math.nan, 2.0 ** 127):
+        assert go(scale=scale) == INV
+    assert go(B=0, q=(0, 0, 0, 0)) == 0 and go(Lq=0, out=0) == 0
+    if not torch.cuda.is_available():
+        assert go() == NODEV and go(Lk=0, k=(0, 0, 0, 0), v=(0, 0, 0, 0)) == NODEV
+
+
+def test_cross_wrapper_checks():
+    bf = torch.bfloat16
+    q, k = torch.zeros(2, 3, 4, 64, dtype=bf), torch.zeros(2, 7, 2, 64, dtype=bf)
+    lens, mask = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 7, dtype=torch.bool)
+    good = dict(q=q, k=k, v=k)
+    for bad in (dict(q=q.float()), dict(k=k.half()), dict(v=k.half()), dict(k=k[:1]), dict(v=k[:, :6]), dict(k=k[..., :32]),
+                dict(q=q[0]), dict(key_lens=lens.long()), dict(key_lens=lens[:1]), dict(mask=mask.byte()), dict(mask=mask[:, :6]),
+                dict(mask=mask.t().contiguous().t()), dict(out=q.half()), dict(out=q[:, :2]), dict(workspace=torch.zeros(9)),
+                dict(q=q.transpose(2, 3).contiguous().transpose(2, 3)), dict(v=k.transpose(2, 3).contiguous().transpose(2, 3))):
+        with pytest.raises(ValueError):
+            S.cross_attention(**{**good, **bad})
+    for bad in (dict(q=1), dict(k=None), dict(v=[1]), dict(mask=[1]), dict(key_lens=[1, 2])):
+        with pytest.raises(TypeError):
+            S.cross_attention(**{**good, **bad})
+    with pytest.raises(S.SvdqError):
+        S.cross_attention(q[:, :, :3], k, k)               # 3 heads over 2
+    with pytest.raises(ValueError, match="not on cpu"):
+        S.cross_attention(q, k, k)
+    big = torch.empty(1, (1 << 32) + 1, 1, 64, dtype=bf, device="meta")
+    with pytest.raises(ValueError, match="32-bit"):
+        S.cross_attention(big, big[:, :1], big[:, :1])
+    with pytest.raises(ValueError, match="32-bit"):
+        S.cross_attention(big[:, :1], big, big)
+    with pytest.raises(ValueError, match="32-bit"):
+        S.cross_attention_workspace(big[:, :1], big)

@@ -56,7 +56,7 @@ EXPORTS = [
     "svdq_kv4_cache_bytes", "svdq_kv4_append", "svdq_kv4_read", "svdq_kv4_attention_workspace_bytes",
     "svdq_kv4_attention", "svdq_moe_route_workspace_bytes", "svdq_moe_route",
     "awq_moe_device_weights_bytes", "awq_moe_pack_device_weights", "awq_moe_pack_on_device", "awq_moe_workspace_bytes", "awq_moe_forward",
-    "svdq_rotary_plan", "svdq_rotary_apply",
+    "svdq_rotary_plan", "svdq_rotary_apply", "svdq_cross_attention_workspace_bytes", "svdq_cross_attention",
 ]
 
 
@@ -157,6 +157,9 @@ _sig("svdq_kv4_attention", _i, [_C, _vp, _i64, _i64, _i64, _i, _i, _i, _i, _vp, 
 _sig("svdq_rotary_plan", _i, [_i, _vp, _i, ctypes.c_double, _i, _i, ctypes.POINTER(RotaryStruct)])
 _sig("svdq_rotary_apply", _i, [ctypes.POINTER(RotaryStruct), *[_vp, ctypes.c_int64, ctypes.c_int64, _i, _vp, ctypes.c_int64, ctypes.c_int64] * 2,
                                _i, _vp, _i, _i, _vp])
+_sig("svdq_cross_attention_workspace_bytes", _sz, [_i] * 7)
+_sig("svdq_cross_attention", _i, [*[_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64] * 3, *[_i] * 7, _vp, _vp, ctypes.c_float, _vp,
+                                  _vp, _sz, _vp])
 _sig("svdq_moe_route_workspace_bytes", _sz, [_i, _i])
 _sig("svdq_moe_route", _i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp])
 _sig("awq_moe_device_weights_bytes", _sz, [_i, _i, _i])
@@ -951,6 +954,65 @@ def rotary_apply(plan: RotaryPlan, q: torch.Tensor, k: Optional[torch.Tensor], p
     _call(dev, _lib.svdq_rotary_apply, plan._ref, *q_args, *k_args, _DT16[q.dtype], positions.data_ptr(),
           int(positions.dtype == torch.float32), T)
     return q_out, k_out
+
+
+# --------------------------------------------------------- cross attention
+def cross_attention_workspace(q: torch.Tensor, k: torch.Tensor, masked: bool = True) -> torch.Tensor:
+    """A workspace for cross_attention calls with queries shaped like q [B, Lq, Hq, D] over
+    states like k [B, Lk, Hkv, D]; masked=False for calls without a mask, which need less."""
+    for n in (*q.shape, *k.shape):
+        _need_int(n, "a size of q or k")
+    n = _lib.svdq_cross_attention_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3],
+                                                  int(bool(masked)))
+    if n == 0:
+        raise SvdqError(2, "svdq_cross_attention_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_lens: Optional[torch.Tensor] = None,
+                    mask: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of queries q [B, Lq, Hq, D] over states k, v [B, Lk, Hkv, D] of another
+    length (bf16 or fp16; any strides that are multiples of 8, channels adjacent; Hq a multiple
+    of Hkv).  Batch row b sees the states before key_lens[b] (int32 [B]) whose mask[b, t]
+    (bool [B, Lk]) is true; what the others hold is not looked at, and a row that sees none gives
+    zeros.  Returns [B, Lq, Hq, D].  scale: 1 / sqrt(D) if not given."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    dev = q.device
+    _need(q, "q", dev, _DT16, 4)
+    B, Lq, Hq, D = q.shape
+    _need(k, "k", dev, (q.dtype,), 4)
+    Lk, Hkv = k.size(1), k.size(2)
+    if k.size(0) != B or k.size(3) != D:
+        raise ValueError(f"k {tuple(k.shape)} does not go with q {tuple(q.shape)}")
+    _need(v, "v", dev, (q.dtype,), 4)
+    if v.shape != k.shape:
+        raise ValueError(f"v must be shaped like k, {tuple(k.shape)}, got {tuple(v.shape)}")
+    _need_int(max(*q.shape, Lk, Hkv), "a size of q or k")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.numel() and t.stride(3) != 1:
+            raise ValueError(f"{name} must have adjacent channels, got strides {t.stride()}")
+    if key_lens is not None:
+        _need_dense(key_lens, "key_lens", dev, torch.int32, (B,))
+    if mask is not None:
+        _need_dense(mask, "mask", dev, torch.bool, (B, Lk))
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _need_dense(out, "out", dev, q.dtype, (B, Lq, Hq, D))
+    if workspace is None:
+        workspace = cross_attention_workspace(q, k, mask is not None)
+    else:
+        _need_workspace(workspace, dev)
+    rows = []
+    for t in (q, k, v):                  # torch leaves any stride where there is one element
+        s = t.stride()
+        rows += [t.data_ptr(), *(0 if n == 1 else x for n, x in zip(t.shape[:3], s))]
+    _call(dev, _lib.svdq_cross_attention, *rows, _DT16[q.dtype], B, Lq, Lk, Hq, Hkv, D,
+          None if key_lens is None else key_lens.data_ptr(), None if mask is None else mask.data_ptr(),
+          D ** -0.5 if scale is None else float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
 
 
 # ------------------------------------------------------- mixture of experts

@@ -7,6 +7,7 @@
 #include <exception>
 
 #include "common.h"
+#include "cross_layout.h"
 #include "host_prepare.h"
 #include "kv4_layout.h"
 #include "layout.h"
@@ -317,6 +318,16 @@ svdq_status_t svdq_rotary_plan(int head_dim, const int32_t *widths, int axes, do
     }
   plan->pairs = j;
   return SVDQ_OK;
+}
+
+size_t svdq_cross_attention_workspace_bytes(int B, int Lq, int Lk, int Hq, int Hkv, int D, int masked) {
+  if (!cross_shape_ok(B, Lq, Lk, Hq, Hkv, D)) {
+    fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_cross_attention_workspace_bytes: B=%d Lq=%d Lk=%d, %d heads over %d of %d channels",
+         B, Lq, Lk, Hq, Hkv, D);
+    return 0;
+  }
+  const size_t n = (size_t)cross_plan(B, Lq, Lk, Hq, Hkv, D, masked != 0).total;
+  return n > 0 ? n : 1;        // 0 is for errors
 }
 
 size_t svdq_moe_route_workspace_bytes(int T, int E) {

@@ -1,0 +1,53 @@
+// Limits, forms and workspace of the cross attention, shared by the host's size
+// query and the device kernels.
+#pragma once
+
+#include <stdint.h>
+
+namespace svdq {
+
+constexpr bool cross_shape_ok(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D) {
+  return B >= 0 && B <= 65536 && Lq >= 0 && Lk >= 0 && Lk <= (1 << 30) && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && D >= 8 &&
+         D <= 256 && D % 8 == 0 && B * Hkv <= (1 << 20) && Lq * Hq <= (1 << 28) && B * (Lq * Hq) <= (1 << 28);
+}
+
+// How a call is cut up.  Rows: the Lq queries of the g heads that share a key/value head.
+struct CrossPlan {
+  int64_t rows = 0;       // of a (batch row, key/value head)
+  int blocks = 0;         // blocks of 32 channels that the kernel is built for
+  bool own = false;       // each wavefront has states of its own (few rows), not rows of its own
+  int tile_rows = 0;      // rows of a workgroup
+  int tile_keys = 0;      // states that a workgroup (own: a wavefront) takes at a time
+  int64_t tiles = 0;      // row tiles of a (batch row, key/value head)
+  int parts = 1;          // pieces that the states are cut into, over workgroups
+  int pieces = 1;         // pieces that the join sees: 4 to a workgroup if `own`
+  int64_t index_off = 0, count_off = 0, ml_off = 0, o_off = 0, total = 0;
+};
+
+constexpr int64_t cross_up(int64_t x) { return (x + 255) / 256 * 256; }
+
+inline CrossPlan cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D, bool masked) {
+  CrossPlan p;
+  p.rows = Lq * (Hq / Hkv);
+  p.blocks = D <= 64 ? 2 : D <= 96 ? 3 : D <= 128 ? 4 : D <= 160 ? 5 : 8;
+  p.own = p.rows <= 32 && p.blocks <= 4;    // wider states: four pairs of tiles are more than the LDS
+  p.tile_rows = p.own ? 32 : 128;
+  p.tile_keys = p.own || p.blocks > 4 ? 32 : 64;
+  p.tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+  const int64_t work = B * Hkv * p.tiles;
+  const int64_t key_tiles = (Lk + p.tile_keys - 1) / p.tile_keys;
+  if (work > 0 && work < 512) {
+    const int64_t want = (512 + work - 1) / work, most = p.own ? (key_tiles + 7) / 8 : key_tiles / 4;
+    p.parts = (int)(want < most ? want : most);
+    if (p.parts < 1) p.parts = 1;
+  }
+  p.pieces = p.own ? 4 * p.parts : p.parts;
+  const int64_t heads = B * Hkv;
+  p.count_off = masked ? cross_up(4 * B * Lk) : 0;
+  p.ml_off = p.count_off + (masked ? cross_up(4 * B) : 0);
+  p.o_off = p.ml_off + (p.pieces > 1 ? cross_up(8 * p.pieces * heads * p.rows) : 0);
+  p.total = p.o_off + (p.pieces > 1 ? cross_up(4 * p.pieces * heads * p.rows * D) : 0);
+  return p;
+}
+
+}  // namespace svdq

@@ -41,27 +41,6 @@ __device__ __forceinline__ uint4 scale_row_operand(float s) {
   return make_uint4(h1 | (h1 << 16), h1 | (h2 << 16), h2 | (h2 << 16), h3 | (h3 << 16));
 }
 
-// Global -> LDS copy of 16 bytes per lane by the load unit
-// (global_load_lds_dwordx4): lane i writes LDS address lds_base + 16 i.
-// lds_base must be uniform across the wavefront.  Written as inline asm so
-// that the copy's completion is tracked by the caller's own vmcnt waits
-// (the compiler would otherwise wait for every copy before any LDS read).
-// The asm has no register outputs; M0 is set and used inside the block.
-__device__ __forceinline__ void lds_dma16(const void *gsrc, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-               :: "v"(gsrc), "s"(lds_base) : "memory");
-}
-// The same copy with a wave-uniform base address in scalar registers and a
-// 32-bit per-lane byte offset.
-__device__ __forceinline__ void lds_dma16_s(const void *sbase, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :: "v"(voff), "s"(sbase), "s"(lds_base) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void vmcnt_wait() {
-  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
-}
-__device__ __forceinline__ void vmcnt_wait0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 // vmcnt(0) through the builtin (expcnt and lgkmcnt left at their maxima), so
 // the compiler's own wait bookkeeping knows every load has landed
 __device__ __forceinline__ void vmcnt_wait0_known() { __builtin_amdgcn_s_waitcnt(0x0F70); }

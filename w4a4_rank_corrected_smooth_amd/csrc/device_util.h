@@ -1,5 +1,6 @@
 // Helpers shared by the device translation units: vector types, bf16
-// conversion, the GELU, and the host-side argument and launch checks.
+// conversion, copies into LDS, the GELU, and the host-side argument and launch
+// checks.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,6 +28,28 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
 }
 
 __device__ __forceinline__ v8bf as_v8bf(uint4 u) { return __builtin_bit_cast(v8bf, u); }
+
+// Global -> LDS copy of 16 bytes per lane by the load unit
+// (global_load_lds_dwordx4): lane i writes LDS address lds_base + 16 i.
+// lds_base must be uniform across the wavefront.  Written as inline asm so
+// that the copy's completion is tracked by the caller's own vmcnt waits
+// (the compiler would otherwise wait for every copy before any LDS read).
+// The asm has no register outputs; M0 is set and used inside the block.
+__device__ __forceinline__ void lds_dma16(const void *gsrc, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :: "v"(gsrc), "s"(lds_base) : "memory");
+}
+// The same copy with a wave-uniform base address in scalar registers and a
+// 32-bit per-lane byte offset.
+__device__ __forceinline__ void lds_dma16_s(const void *sbase, uint32_t voff, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds_base) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void vmcnt_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
+__device__ __forceinline__ void vmcnt_wait0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // tanh-form GELU, 0.5 y (1 + tanh u) with u = sqrt(2/pi) (y + 0.044715 y^3),
 // evaluated as y / (1 + exp(-2u)) (the same function) so that large negative
