@@ -2,7 +2,9 @@
  * svdq.h -- C ABI of libsvdq, an MI355X (gfx950) implementation of the
  * SVDQuant W4A4 linear layer with its 16-bit low-rank branch, and of the
  * AWQ-style W4A16 linear used for modulation layers; with a 4-bit key/value
- * cache and its attention, and an expert layer of W4A16 linears.
+ * cache and its attention, and an expert layer of W4A16 linears; and with what
+ * stands around the linears of an attention block: a linear in 8-bit floating
+ * point, rotary positions and cross attention.
  *
  * Method.  "Bringing Nunchaku 4-bit diffusion inference to Diffusers"
  * (Vietnamese edition, section "Bối cảnh: SVDQuant và Nunchaku"; Korean
@@ -447,6 +449,57 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
                                  int64_t q_head, svdq_dtype_t dtype, int B, int Q, int Hq,
                                  const int32_t *page_table, int table_width, const int32_t *seq_lens, float scale,
                                  void *out, void *workspace, size_t ws_bytes, void *hip_stream);
+
+/* ================================================ linear in 8-bit floating point
+ * Y = Q8(X) W^T + b on e4m3 codes (OCP FP8 E4M3FN) with a scale for each block of 128,
+ * as 8-bit checkpoints hold it: between the 4-bit linears above and the W4A16 one, for
+ * projections that 4 bits hurt.  A weight is its code times the float32 scale of its 128 x 128
+ * block; 128 consecutive channels of a row of X share the smallest power of
+ * two s with max |x| <= 448 s (at least 2^-127), and x / s, which is exact, is
+ * rounded to e4m3 once, ties to even.  So
+ *   Y[m, n] = sum_b sw[n / 128, b] sx[m, b] sum_{k in block b} a[m, k] w[n, k]  (+ bias[n]).
+ * Blocks are summed in float32.  Inside a block the matrix instruction adds
+ * groups of eight neighbouring channels' products with each cut off below 2^-13 of the group's largest
+ * (measured: 2^-16 of a result's size, far below a 16-bit result's step, which is
+ * why there is no float32 result), and sums below 2^-126, float32's normal range, count
+ * as zero.  A block of X that holds an infinity or a NaN makes its row of Y
+ * NaN and touches no other. */
+
+/* Host: codes [N, K] and scales [ceil(N/128), ceil(K/128)] of W [N, K] float32:
+ * scale = max |w| / 448 of the block rounded to float32 (1 for a block of zeros and where that
+ * rounds to zero), code = the nearest e4m3 value to fl32(w / scale), at most 448, ties to even.  K a multiple of
+ * 8; a W that is not finite gives SVDQ_ERR_NUMERICAL.  Multi-threaded. */
+svdq_status_t svdq_fp8_quantize_weights(const float *W, int N, int K, uint8_t *codes, float *scales);
+
+/* The device blob of a weight, from device memory to device memory (codes and
+ * blob 16-byte aligned): asynchronous on `hip_stream`.  K a multiple of 8 up to 2^20,
+ * N up to 2^20, N K <= 2^33. */
+size_t svdq_fp8_device_weights_bytes(int N, int K);
+svdq_status_t svdq_fp8_pack_on_device(const uint8_t *codes, const float *scales, int N, int K, void *blob, size_t bytes,
+                                      void *hip_stream);
+
+typedef struct {
+  const void *blob;   /* device, from svdq_fp8_pack_on_device */
+  const float *bias;  /* device [N], or NULL */
+  int32_t N, K;
+} svdq_fp8_weights_t;
+
+/* out [M, N] (bf16 or fp16, dense) for x [M, K] of bf16 or fp16, row m at x +
+ * m x_row elements (16-byte aligned, x_row a multiple of 8, not negative).
+ * epilogue: SVDQ_EPILOGUE_NONE or SVDQ_EPILOGUE_GELU_TANH, in float32 before
+ * the result is rounded once.  M <= 2^22, M N and M K <= 2^34.  One kernel for few rows, or two or three:
+ * the quantiser, the product, and the sum of its parts where K is cut up.  The result does not depend on the
+ * order in which workgroups run.  The workspace needs no clearing and keeps nothing from one
+ * call for the next (calls that run at the same time need one each). */
+size_t svdq_fp8_workspace_bytes(int M, int N, int K);
+svdq_status_t svdq_fp8_linear_forward(const svdq_fp8_weights_t *w, const void *x, int64_t x_row, svdq_dtype_t x_dtype,
+                                      int M, void *out, svdq_dtype_t out_dtype, svdq_epilogue_t epilogue,
+                                      void *workspace, size_t ws_bytes, void *hip_stream);
+
+/* The quantiser alone: codes [M, K] (e4m3, dense) and scales [M, ceil(K/128)] as E8M0
+ * bytes (2^(byte - 127)).  A block that is not finite gets codes 0x7F (NaN) and the byte 127. */
+svdq_status_t svdq_fp8_quantize_activations(const void *x, int64_t x_row, svdq_dtype_t dtype, int M, int K,
+                                            uint8_t *codes, uint8_t *scales, void *hip_stream);
 
 /* ====================================================== rotary positions
  * Rotation of query and key rows by positions with one to eight axes (a

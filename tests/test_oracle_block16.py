@@ -178,3 +178,120 @@ def test_cross_wrapper_checks():
         S.cross_attention(big[:, :1], big, big)
     with pytest.raises(ValueError, match="32-bit"):
         S.cross_attention_workspace(big[:, :1], big)
+
+
+# ------------------------------------------------- linear in 8-bit floating point
+def test_fp8_oracle_grid():
+    """Decoding agrees with torch's e4m3, and rounding with its conversion, ties and subnormals among them."""
+    from oracle import fp8
+    codes = np.arange(256, dtype=np.uint8)
+    table = torch.from_numpy(codes).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(fp8.decode(codes), table, equal_nan=True)
+    grid = np.sort(table[np.isfinite(table)])
+    v = np.concatenate([grid, (grid[1:] + grid[:-1]) / 2, np.random.default_rng(3).standard_normal(2000) * 30])
+    v = v[np.abs(v) <= 448].astype(np.float32)
+    assert np.array_equal(fp8.e4m3(v), torch.from_numpy(v).to(torch.float8_e4m3fn).double().numpy())
+    x = np.array([[448.0, 1.0] + [0.0] * 126 + [450.0, -0.001], [0.0] * 130])
+    val, e = fp8.quantize_rows(x)
+    assert e.tolist() == [[0, 1], [-127, -127]] and val[0, 0] == 448 and val[0, 128] == 224 and val[0, 129] == 0.0
+
+
+@pytest.mark.parametrize("N,K", [(1, 8), (128, 128), (130, 264), (300, 1000)])
+def test_fp8_weight_quantiser(N, K):
+    from oracle import fp8
+    r = np.random.default_rng(N + K)
+    W = (r.standard_normal((N, K)) * np.exp2(r.integers(-20, 20, (N, K)))).astype(np.float32)
+    W[:, ::5] = 0
+    codes, scales = S.fp8_quantize_weights(W)
+    assert codes.dtype == np.uint8 and codes.shape == (N, K) and scales.shape == (-(-N // 128), fp8.blocks(K))
+    for nb in range(scales.shape[0]):
+        for kb in range(scales.shape[1]):
+            at = np.s_[128 * nb:128 * nb + 128, 128 * kb:128 * kb + 128]
+            s = np.abs(W[at]).max() / np.float32(448)
+            assert scales[nb, kb] == (s if s > 0 else 1)
+            assert np.array_equal(fp8.decode(codes[at]), fp8.e4m3(np.clip(W[at] / scales[nb, kb], -448, 448)))
+    again, s2 = S.fp8_quantize_weights(torch.from_numpy(W))
+    assert np.array_equal(again, codes) and np.array_equal(s2, scales)
+
+
+def test_fp8_weight_quantiser_edges():
+    W = np.zeros((2, 256), np.float32)
+    W[0, 0], W[1, 130], W[0, 131] = 1e-44, 3.4e38, -1.0            # a scale that rounds to zero; the largest numbers
+    codes, scales = S.fp8_quantize_weights(W)
+    assert scales[0, 0] == 1 and not codes[:, :128].any() and codes[1, 130] == 0x7E and codes[0, 131] == 0x80
+    for bad in (np.inf, np.nan):
+        W[1, 5] = bad
+        with pytest.raises(S.SvdqError):
+            S.fp8_quantize_weights(W)
+    for shape in ((2, 12), (0, 8), (2, 0)):
+        with pytest.raises(S.SvdqError):
+            S.fp8_quantize_weights(np.zeros(shape, np.float32))
+    with pytest.raises(ValueError):
+        S.fp8_quantize_weights(np.zeros(8, np.float32))
+    assert S._lib.svdq_fp8_quantize_weights(None, 1, 8, FAKE, FAKE) == INV
+
+
+def test_fp8_argument_errors():
+    lib = S._lib
+    assert lib.svdq_fp8_device_weights_bytes(33, 136) == 2 * 2 * 4112
+    for bad in ((0, 8), (1, 0), (1, 12), (-1, 8), ((1 << 20) + 1, 8), (1, (1 << 20) + 8), (1 << 20, 1 << 14)):
+        assert lib.svdq_fp8_device_weights_bytes(*bad) == 0
+    assert lib.svdq_fp8_workspace_bytes(0, 1, 8) >= 1 and lib.svdq_fp8_workspace_bytes(100, 64, 256) >= 100 * 256
+    for bad in ((-1, 1, 8), (1, 1, 12), ((1 << 22) + 1, 1, 8), (1 << 20, 1 << 15, 8), (1 << 20, 8, 1 << 15)):
+        assert lib.svdq_fp8_workspace_bytes(*bad) == 0
+
+    def pack(codes=FAKE, scales=FAKE, N=33, K=136, blob=FAKE, n=4 * 4112):
+        return lib.svdq_fp8_pack_on_device(codes, scales, N, K, blob, n, None)
+    assert pack(codes=0) == INV and pack(scales=0) == INV and pack(blob=0) == INV and pack(codes=FAKE + 8) == INV
+    assert pack(blob=FAKE + 4) == INV and pack(scales=FAKE + 2) == INV and pack(K=132) == SHAPE and pack(N=0) == SHAPE
+    assert pack(n=4 * 4112 - 1) == WS
+    w = S.Fp8Weights(FAKE, None, 64, 256)
+    need = lib.svdq_fp8_workspace_bytes(100, 64, 256)
+
+    def go(w=w, x=FAKE, row=256, dt=S.BF16, M=100, out=FAKE, odt=S.BF16, epi=0, ws=FAKE, n=need):
+        return lib.svdq_fp8_linear_forward(ctypes.byref(w) if w else None, x, row, dt, M, out, odt, epi, ws, n, None)
+    assert go(w=None) == INV and go(w=S.Fp8Weights(None, None, 64, 256)) == INV and go(w=S.Fp8Weights(FAKE + 8, None, 64, 256)) == INV
+    assert go(w=S.Fp8Weights(FAKE, FAKE + 2, 64, 256)) == INV and go(w=S.Fp8Weights(FAKE, None, 64, 100)) == SHAPE
+    assert go(x=0) == INV and go(x=FAKE + 8) == INV and go(row=257) == INV and go(row=-8) == INV and go(dt=S.FP32) == INV
+    assert go(out=0) == INV and go(out=FAKE + 2) == INV and go(odt=S.FP32) == INV and go(epi=2) == INV and go(ws=0) == INV
+    assert go(ws=FAKE + 4) == INV and go(n=need - 1) == WS and go(M=-1) == SHAPE and go(M=(1 << 22) + 1) == SHAPE
+    assert go(M=0, x=0, out=0) == 0
+
+    def quantise(x=FAKE, row=256, dt=S.BF16, M=3, K=256, codes=FAKE, scales=FAKE):
+        return lib.svdq_fp8_quantize_activations(x, row, dt, M, K, codes, scales, None)
+    assert quantise(x=0) == INV and quantise(codes=0) == INV and quantise(scales=0) == INV and quantise(codes=FAKE + 8) == INV
+    assert quantise(row=4) == INV and quantise(dt=S.FP32) == INV and quantise(K=12) == SHAPE and quantise(M=-1) == SHAPE
+    assert quantise(M=0, x=0) == 0
+    if not torch.cuda.is_available():
+        assert go() == NODEV and pack() == NODEV and quantise() == NODEV
+
+
+def test_fp8_wrapper_checks():
+    codes, scales = torch.zeros(200, 136, dtype=torch.uint8), torch.ones(2, 2)
+    for bad in (dict(codes=codes.int()), dict(codes=codes[0]), dict(scales=scales[:1]), dict(scales=scales.double()),
+                dict(scales=scales * math.inf), dict(bias=torch.zeros(199)), dict(codes=codes[:, :132])):
+        with pytest.raises((ValueError, S.SvdqError)):
+            S.Fp8Linear(**{**dict(codes=codes, scales=scales, device="cpu"), **bad})
+    with pytest.raises(TypeError):
+        S.Fp8Linear([1], scales, device="cpu")
+    with pytest.raises(ValueError, match="not on cpu"):
+        S.Fp8Linear(codes, scales, device="cpu")
+    layer = S.Fp8Linear.__new__(S.Fp8Linear)
+    layer.N, layer.K, layer.device = 200, 136, torch.device("cpu")
+    layer._ref = ctypes.byref(S.Fp8Weights(FAKE, None, 200, 136))
+    x = torch.zeros(5, 136, dtype=torch.bfloat16)
+    for bad in (dict(x=x.float()), dict(x=x[:, :128]), dict(x=x[0]), dict(x=x.t().contiguous().t()), dict(out=x), dict(out_dtype=torch.float32),
+                dict(out=torch.zeros(5, 200)), dict(out=torch.zeros(5, 200).bfloat16(), out_dtype=torch.float16),
+                dict(workspace=torch.zeros(5))):
+        with pytest.raises(ValueError):
+            S.fp8_linear_forward(**{**dict(layer=layer, x=x), **bad})
+    with pytest.raises(TypeError):
+        S.fp8_linear_forward(layer, [1])
+    with pytest.raises(ValueError, match="not on cpu"):
+        S.fp8_linear_forward(layer, x)
+    with pytest.raises(ValueError, match="not on cpu"):
+        S.fp8_quantize_activations(x)
+    with pytest.raises(TypeError):
+        S.fp8_quantize_activations([1])
+    with pytest.raises(ValueError, match="32-bit"):
+        layer.new_workspace((1 << 32) + 1)

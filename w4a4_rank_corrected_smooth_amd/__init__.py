@@ -1,6 +1,7 @@
 """Python binding of libsvdq: the SVDQuant W4A4 + low-rank linear layer, the
-AWQ W4A16 linear, the MXFP4 key/value cache with its attention, and the W4A16
-expert layer with its router, on MI355X (gfx950).
+AWQ W4A16 linear, the MXFP4 key/value cache with its attention, the W4A16
+expert layer with its router, the 8-bit floating point linear, rotary positions
+and cross attention, on MI355X (gfx950).
 
 This module only marshals arguments into the C ABI declared in
 ``include/svdq.h``: every step of the method runs in the library (host
@@ -57,6 +58,8 @@ EXPORTS = [
     "svdq_kv4_attention", "svdq_moe_route_workspace_bytes", "svdq_moe_route",
     "awq_moe_device_weights_bytes", "awq_moe_pack_device_weights", "awq_moe_pack_on_device", "awq_moe_workspace_bytes", "awq_moe_forward",
     "svdq_rotary_plan", "svdq_rotary_apply", "svdq_cross_attention_workspace_bytes", "svdq_cross_attention",
+    "svdq_fp8_quantize_weights", "svdq_fp8_device_weights_bytes", "svdq_fp8_pack_on_device", "svdq_fp8_workspace_bytes",
+    "svdq_fp8_linear_forward", "svdq_fp8_quantize_activations",
 ]
 
 
@@ -80,6 +83,10 @@ class DeviceWeights(ctypes.Structure):
 class Kv4CacheStruct(ctypes.Structure):
     _fields_ = [("data", _vp), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class Fp8Weights(ctypes.Structure):
+    _fields_ = [("blob", _vp), ("bias", _vp), ("N", ctypes.c_int32), ("K", ctypes.c_int32)]
 
 
 class RotaryStruct(ctypes.Structure):
@@ -154,6 +161,12 @@ _sig("svdq_kv4_read", _i, [_C, _vp, _i, _vp, _vp, _i, _vp])
 _sig("svdq_kv4_attention_workspace_bytes", _sz, [_i, _i, _i, _i, _i])
 _sig("svdq_kv4_attention", _i, [_C, _vp, _i64, _i64, _i64, _i, _i, _i, _i, _vp, _i, _vp, ctypes.c_float, _vp, _vp,
                                 _sz, _vp])
+_sig("svdq_fp8_quantize_weights", _i, [_vp, _i, _i, _vp, _vp])
+_sig("svdq_fp8_device_weights_bytes", _sz, [_i, _i])
+_sig("svdq_fp8_pack_on_device", _i, [_vp, _vp, _i, _i, _vp, _sz, _vp])
+_sig("svdq_fp8_workspace_bytes", _sz, [_i, _i, _i])
+_sig("svdq_fp8_linear_forward", _i, [ctypes.POINTER(Fp8Weights), _vp, ctypes.c_int64, _i, _i, _vp, _i, _i, _vp, _sz, _vp])
+_sig("svdq_fp8_quantize_activations", _i, [_vp, ctypes.c_int64, _i, _i, _i, _vp, _vp, _vp])
 _sig("svdq_rotary_plan", _i, [_i, _vp, _i, ctypes.c_double, _i, _i, ctypes.POINTER(RotaryStruct)])
 _sig("svdq_rotary_apply", _i, [ctypes.POINTER(RotaryStruct), *[_vp, ctypes.c_int64, ctypes.c_int64, _i, _vp, ctypes.c_int64, ctypes.c_int64] * 2,
                                _i, _vp, _i, _i, _vp])
@@ -867,6 +880,117 @@ def kv4_attention(cache: Kv4Cache, q: torch.Tensor, page_table: torch.Tensor, se
           seq_lens.data_ptr(), D ** -0.5 if scale is None else float(scale), out.data_ptr(), workspace.data_ptr(),
           workspace.numel())
     return out
+
+
+# ------------------------------------------------ linear in 8-bit floating point
+def fp8_quantize_weights(W):
+    """W [N, K] (K a multiple of 8) as (codes uint8 [N, K] of e4m3 bit patterns, scales
+    float32 [ceil(N/128), ceil(K/128)]), arrays: a weight is its code's value times its
+    128 x 128 block's scale."""
+    W = W.detach().float().cpu().numpy() if isinstance(W, torch.Tensor) else W
+    W = np.ascontiguousarray(W, dtype=np.float32)
+    if W.ndim != 2:
+        raise ValueError(f"W must be [N, K], got {W.shape}")
+    N, K = W.shape
+    _need_int(max(N, K), "a size of W")
+    q = np.empty((N, K), np.uint8)
+    s = np.empty((-(-N // 128), -(-K // 128)), np.float32)
+    _check(_lib.svdq_fp8_quantize_weights(_ptr(W), N, K, _ptr(q), _ptr(s)), "svdq_fp8_quantize_weights")
+    return q, s
+
+
+class Fp8Linear:
+    """A linear of e4m3 weights with a float32 scale for each 128 x 128 of them, resident
+    on one device: codes [N, K] (uint8 bit patterns or float8_e4m3fn), scales float32
+    [ceil(N/128), ceil(K/128)], as fp8_quantize_weights or a checkpoint has them, and
+    a bias [N] or None; arrays or tensors."""
+
+    def __init__(self, codes, scales, bias=None, device=None):
+        codes, scales = (torch.from_numpy(np.ascontiguousarray(t)) if isinstance(t, np.ndarray) else t for t in (codes, scales))
+        for t, name in ((codes, "codes"), (scales, "scales")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be an array or a torch.Tensor")
+        if codes.dtype not in (torch.uint8, torch.float8_e4m3fn) or codes.dim() != 2:
+            raise ValueError(f"codes must be uint8 or float8_e4m3fn [N, K], got {codes.dtype} {tuple(codes.shape)}")
+        N, K = codes.shape
+        _need_int(max(N, K), "a size of codes")
+        if scales.dtype != torch.float32 or tuple(scales.shape) != (-(-N // 128), -(-K // 128)):
+            raise ValueError(f"scales must be float32 [{-(-N // 128)}, {-(-K // 128)}], got {scales.dtype} {tuple(scales.shape)}")
+        if not bool(torch.isfinite(scales).all()):
+            raise ValueError("scales must be finite")
+        n = _lib.svdq_fp8_device_weights_bytes(N, K)
+        if n == 0:
+            raise SvdqError(2, "svdq_fp8_device_weights_bytes")
+        dev = torch.device(device if device is not None else codes.device if codes.is_cuda else "cuda")
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.N, self.K, self.device = N, K, dev
+        self.bias = None
+        if bias is not None:
+            self.bias = torch.as_tensor(bias).detach().to(dev, torch.float32).contiguous()
+            if self.bias.shape != (N,):
+                raise ValueError(f"bias must be [{N}], got {tuple(self.bias.shape)}")
+        codes, scales = codes.view(torch.uint8).to(dev).contiguous(), scales.to(dev).contiguous()
+        self.blob = torch.empty(n, dtype=torch.uint8, device=dev)
+        _call(dev, _lib.svdq_fp8_pack_on_device, codes.data_ptr(), scales.data_ptr(), N, K, self.blob.data_ptr(), n)
+        self._w = Fp8Weights(self.blob.data_ptr(), None if self.bias is None else self.bias.data_ptr(), N, K)
+        self._ref = ctypes.byref(self._w)
+
+    def workspace_bytes(self, M: int) -> int:
+        _need_int(M, "M")
+        n = _lib.svdq_fp8_workspace_bytes(M, self.N, self.K)
+        if n == 0:
+            raise SvdqError(2, "svdq_fp8_workspace_bytes")
+        return n
+
+    def new_workspace(self, M: int) -> torch.Tensor:
+        return torch.empty(self.workspace_bytes(M), dtype=torch.uint8, device=self.device)
+
+
+def _fp8_rows(x, dev, K) -> int:
+    """The row stride of x [M, K]."""
+    _need(x, "x", dev, _DT16, 2)
+    if (K is not None and x.size(1) != K) or (x.numel() and x.size(1) > 1 and x.stride(1) != 1):
+        raise ValueError(f"x must be [M, {K or 'K'}] with adjacent channels, got {tuple(x.shape)} with strides {x.stride()}")
+    _need_int(max(x.shape), "a size of x")
+    return x.stride(0) if x.size(0) > 1 else 0
+
+
+def fp8_linear_forward(layer: Fp8Linear, x: torch.Tensor, gelu: bool = False, out_dtype: Optional[torch.dtype] = None,
+                       out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [M, K] (bf16 or fp16, any row stride that is a multiple of 8) through the layer, with
+    its bias and, if `gelu`, the tanh GELU: [M, N] of x's type, or out_dtype (bf16 or fp16).
+    The rows are quantised to e4m3 with a power of two for each 128 channels."""
+    dev = layer.device
+    row = _fp8_rows(x, dev, layer.K)
+    M = x.size(0)
+    if out is None:
+        out = torch.empty((M, layer.N), dtype=out_dtype or x.dtype, device=dev)
+    else:
+        _need_dense(out, "out", dev, out_dtype or out.dtype, (M, layer.N))
+    if out.dtype not in _DT16:
+        raise ValueError(f"out must be bfloat16 or float16, not {out.dtype}")
+    if workspace is None:
+        workspace = layer.new_workspace(M)
+    else:
+        _need_workspace(workspace, dev)
+    _call(dev, _lib.svdq_fp8_linear_forward, layer._ref, x.data_ptr(), row, _DT16[x.dtype], M, out.data_ptr(),
+          _DT16[out.dtype], EPILOGUE_GELU_TANH if gelu else EPILOGUE_NONE, workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def fp8_quantize_activations(x: torch.Tensor):
+    """The linear's quantiser alone: x [M, K] (bf16 or fp16) as (codes float8_e4m3fn [M, K],
+    scales uint8 [M, ceil(K/128)], E8M0: 2^(byte - 127))."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
+    row = _fp8_rows(x, dev, None)
+    M, K = x.shape
+    codes = torch.empty((M, K), dtype=torch.uint8, device=dev)
+    scales = torch.empty((M, -(-K // 128)), dtype=torch.uint8, device=dev)
+    _call(dev, _lib.svdq_fp8_quantize_activations, x.data_ptr(), row, _DT16[x.dtype], M, K, codes.data_ptr(), scales.data_ptr())
+    return codes.view(torch.float8_e4m3fn), scales
 
 
 # -------------------------------------------------------- rotary positions

@@ -27,7 +27,7 @@ HOST_UNITS = {
     "host_threads.cpp": [],
     "host_linalg.cpp": ["-ffp-contract=fast"],
 }
-DEVICE_UNITS = ["device.hip", "kv4.hip", "moe.hip", "rotary.hip", "cross.hip"]
+DEVICE_UNITS = ["device.hip", "kv4.hip", "moe.hip", "fp8.hip", "rotary.hip", "cross.hip"]
 DEVICE_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
                 "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
                 "-Wno-unused-result", f"-I{INCLUDE}", f"-I{CSRC}"]

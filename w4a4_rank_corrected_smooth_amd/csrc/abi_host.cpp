@@ -8,6 +8,7 @@
 
 #include "common.h"
 #include "cross_layout.h"
+#include "fp8_layout.h"
 #include "host_prepare.h"
 #include "kv4_layout.h"
 #include "layout.h"
@@ -288,6 +289,34 @@ size_t svdq_kv4_attention_workspace_bytes(int B, int Q, int Hq, int kv_heads, in
     return 0;
   }
   return (size_t)kv4_workspace_bytes(Q, Hq, kv_heads, head_dim);
+}
+
+size_t svdq_fp8_device_weights_bytes(int N, int K) {
+  if (!fp8_weights_ok(N, K)) {
+    fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_fp8_device_weights_bytes: N=%d K=%d", N, K);
+    return 0;
+  }
+  return (size_t)fp8_w_bytes(N, K);
+}
+
+size_t svdq_fp8_workspace_bytes(int M, int N, int K) {
+  if (!fp8_weights_ok(N, K) || !fp8_call_ok(M, N) || !fp8_call_ok(M, K)) {
+    fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "svdq_fp8_workspace_bytes: M=%d N=%d K=%d", M, N, K);
+    return 0;
+  }
+  const size_t n = M > 0 ? (size_t)fp8_plan(M, N, K).total : 0;
+  return n > 0 ? n : 1;        // 0 is for errors
+}
+
+svdq_status_t svdq_fp8_quantize_weights(const float *W, int N, int K, uint8_t *codes, float *scales) {
+  const char *who = "svdq_fp8_quantize_weights";
+  if (!W || !codes || !scales) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: NULL pointer", who);
+  if (!fp8_weights_ok(N, K)) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%s: N=%d K=%d", who, N, K);
+  try {
+    return fp8_quantize(W, N, K, codes, scales);
+  } catch (const std::exception &e) {       // the thread pool could not start
+    return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: %s", who, e.what());
+  }
 }
 
 svdq_status_t svdq_rotary_plan(int head_dim, const int32_t *widths, int axes, double theta, int interleaved,

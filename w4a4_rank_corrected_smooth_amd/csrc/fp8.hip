@@ -1,0 +1,514 @@
+// Linear in 8-bit floating point with a scale for each block of 128.
+//
+//  fp8_pack_kernel       canonical codes and scales -> operand blocks
+//  fp8_quantize_kernel   16-bit rows -> operand blocks, or canonical codes
+//  fp8_tile_kernel       the product, a tile of rows by channels to a workgroup
+//  fp8_rows_kernel       the product for few rows: one stream of the weights
+//
+// A block of 128 channels is two 32x32x64 block-scaled matrix instructions
+// (e4m3, operands in fp8_layout.h's order), with the rows' power-of-two scales as the
+// instruction's own E8M0 scales.  The weights' float32 scale, the same for a whole tile, is
+// m 2^e: 2^e is the instruction's other scale, so that no sum leaves float32's range before the
+// result does, and m in [1, 2) is applied by one FMA an element and block on the way into the sums:
+//   P = sum_{k in block} (sx a) (2^e w),   acc = fma(P, m, acc).
+// W is the A operand and X the B operand, so a lane's 16 results are of one row m
+// = lane % 32, channels n = 8 j + 4 (lane / 32) + [0, 4) of the tile.
+#include <hip/hip_runtime.h>
+
+#include "common.h"
+#include "device_util.h"
+#include "fp8_layout.h"
+
+using namespace svdq;
+
+namespace {
+
+struct Fp8Args {
+  const uint8_t *w, *x;          // blocks
+  const float *bias;
+  uint16_t *out;
+  float *part;                   // pieces [part][M][N], or NULL
+  int M, N, blocks_k;
+  int m_blocks, n_blocks;        // of 32
+  int tiles_m, tiles_n, parts;
+  int gelu;
+  // FP8_ROWS with its own quantiser
+  const uint16_t *rows;
+  int64_t rows_stride;
+  int K;
+};
+
+template <bool F16>
+__device__ __forceinline__ float widen(uint32_t h) {
+  if constexpr (F16) return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+  else return __uint_as_float(h << 16);
+}
+
+// ---------------------------------------------------------------- quantiser
+// Sixteen channels of a row (zeros past the end) to codes; the eight lanes of a block of 128
+// are neighbours.  With a = max |x| = 1.f 2^(E - 127), 448 = 1.75 2^8: the smallest e
+// with a <= 448 2^e is E - 135, or one more where f > 0.75, and at least -127.
+// x 2^-e is exact (16-bit values, at most 2^-133, times at most 2^127) and at most 448.
+template <bool F16>
+__device__ __forceinline__ uint32_t quantize16(const uint16_t *src, int k, int K, v4u &codes) {
+  uint32_t in[8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const v4u u = k + 8 * i < K ? *reinterpret_cast<const v4u *>(src + k + 8 * i) : v4u{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) in[4 * i + j] = u[j];
+  }
+  float x[16];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    x[i] = widen<F16>(in[i / 2] >> (16 * (i & 1)) & 0xFFFFu);
+    top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  }
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, s));
+  if (top >= 0x7F800000u) {
+    codes = v4u{0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
+    return 127u;
+  }
+  const int scale = max((int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u), 0);
+  const float inv = __uint_as_float((uint32_t)(254 - scale) << 23);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    int d = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * j] * inv, x[4 * j + 1] * inv, 0, false);
+    d = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * j + 2] * inv, x[4 * j + 3] * inv, d, true);
+    codes[j] = (uint32_t)d;
+  }
+  return (uint32_t)scale;
+}
+
+// A workgroup: 32 rows by one block.  CANON: codes [M, K] and scales [M, blocks] instead of operand blocks.
+template <bool F16, bool CANON>
+__global__ __launch_bounds__(256) void fp8_quantize_kernel(const uint16_t *__restrict__ x, int64_t x_row, int M, int K,
+                                                           int blocks_k, uint8_t *__restrict__ out,
+                                                           uint8_t *__restrict__ scales) {
+  const int mb = blockIdx.x / blocks_k, kb = blockIdx.x - mb * blocks_k;
+  const int u = threadIdx.x & 7, r = threadIdx.x >> 3, m = 32 * mb + r;
+  if (m >= M) return;
+  v4u codes;
+  const int k = 128 * kb + 16 * u;
+  const uint32_t s = quantize16<F16>(x + (int64_t)m * x_row, k, K, codes);
+  if constexpr (CANON) {
+    uint8_t *to = out + (int64_t)m * K + k;
+    if (k < K) *reinterpret_cast<uint2 *>(to) = make_uint2(codes[0], codes[1]);
+    if (k + 8 < K) *reinterpret_cast<uint2 *>(to + 8) = make_uint2(codes[2], codes[3]);
+    if (u == 0) scales[(int64_t)m * blocks_k + kb] = (uint8_t)s;
+  } else {
+    uint8_t *to = out + (int64_t)blockIdx.x * kFp8XBlock;
+    *reinterpret_cast<v4u *>(to + (u >> 1) * 1024 + (u & 1) * 512 + 16 * r) = codes;
+    if (u == 0) to[kFp8Block + r] = (uint8_t)s;
+  }
+}
+
+__global__ __launch_bounds__(256) void fp8_pack_kernel(const uint8_t *__restrict__ codes, const float *__restrict__ scales,
+                                                       int N, int K, int blocks_k, uint8_t *__restrict__ blob) {
+  const int nb = blockIdx.x / blocks_k, kb = blockIdx.x - nb * blocks_k;
+  const int u = threadIdx.x & 7, r = threadIdx.x >> 3, n = 32 * nb + r, k = 128 * kb + 16 * u;
+  const uint8_t *src = codes + (int64_t)n * K + k;
+  uint2 lo = make_uint2(0, 0), hi = lo;
+  if (n < N && k < K) lo = *reinterpret_cast<const uint2 *>(src);
+  if (n < N && k + 8 < K) hi = *reinterpret_cast<const uint2 *>(src + 8);
+  uint8_t *to = blob + (int64_t)blockIdx.x * kFp8WBlock;
+  *reinterpret_cast<uint4 *>(to + (u >> 1) * 1024 + (u & 1) * 512 + 16 * r) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  if (threadIdx.x == 0) {
+    const float sw = scales[(int64_t)(nb / 4) * blocks_k + kb];
+    const uint32_t e = max(__float_as_uint(sw) >> 23 & 255u, 1u);
+    // 2^(e - 127) with e from 1 (a subnormal scale's m is below 1) to 254
+    const float m = ldexpf(sw, 127 - (int)e);
+    *reinterpret_cast<uint4 *>(to + kFp8Block) = make_uint4(__float_as_uint(m), e, 0, 0);
+  }
+}
+
+// ------------------------------------------------------------------ product
+__device__ __forceinline__ v16f mma(const v4u (&w)[4], int we, const v4u (&x)[4], int sx) {
+  v16f p;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) p[i] = 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const v8i a = {(int)w[2 * h][0], (int)w[2 * h][1], (int)w[2 * h][2], (int)w[2 * h][3],
+                   (int)w[2 * h + 1][0], (int)w[2 * h + 1][1], (int)w[2 * h + 1][2], (int)w[2 * h + 1][3]};
+    const v8i b = {(int)x[2 * h][0], (int)x[2 * h][1], (int)x[2 * h][2], (int)x[2 * h][3],
+                   (int)x[2 * h + 1][0], (int)x[2 * h + 1][1], (int)x[2 * h + 1][2], (int)x[2 * h + 1][3]};
+    p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, p, 0, 0, 0, we, 0, sx);
+  }
+  return p;
+}
+
+// OUT: svdq_dtype_t of the result
+template <int OUT>
+__device__ __forceinline__ uint16_t narrow(float y) {
+  if constexpr (OUT == SVDQ_FP16) return __builtin_bit_cast(uint16_t, (_Float16)y);
+  else return __builtin_bit_cast(uint16_t, (__bf16)y);
+}
+template <int OUT>
+__device__ __forceinline__ uint32_t pair_of(float a, float b) {
+  if constexpr (OUT == SVDQ_FP16) {
+    const v2h h = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, h);
+  } else {
+    typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+    const v2b h = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, h);
+  }
+}
+
+// Four results of row m, channels n .. n + 3 (those below N).
+template <int OUT>
+__device__ __forceinline__ void store4(const Fp8Args &a, int64_t m, int n, v4f y) {
+  if (a.bias) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] += a.bias[min(n + e, a.N - 1)];
+  }
+  if (a.gelu) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = gelu_tanh_f32(y[e]);
+  }
+  const int64_t at = m * a.N + n;
+  if (n + 4 <= a.N && (a.N & 3) == 0) {
+    *reinterpret_cast<uint2 *>(a.out + at) = make_uint2(pair_of<OUT>(y[0], y[1]), pair_of<OUT>(y[2], y[3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.N) a.out[at + e] = narrow<OUT>(y[e]);
+  }
+}
+
+// A wavefront's tile is TM blocks of rows by TN blocks of channels, a workgroup's
+// WM by WN of those; ST stages of one block of K in LDS.
+template <int TM, int TN, int WM, int WN, int ST, int OUT>
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args a) {
+  constexpr int XB = TM * WM, WB = TN * WN, WAVES = WM * WN, COPIES = (XB + WB) / WAVES;
+  static_assert((XB + WB) % WAVES == 0, "blocks dealt out evenly");
+  constexpr int W_AT = XB * kFp8XBlock, STAGE = W_AT + WB * kFp8WBlock;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * STAGE];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w % WM, wn = w / WM;
+  // Workgroups are dealt out to the eight XCDs in turn: each XCD gets a contiguous
+  // run of tiles, eight rows of tiles high, so that its L2 holds few rows and channels.
+  const int tiles = a.tiles_m * a.tiles_n * a.parts, per = (tiles + 7) / 8;
+  const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || id >= tiles) return;
+  const int part = id / (a.tiles_m * a.tiles_n), tile = id - part * (a.tiles_m * a.tiles_n);
+  const int band = tile / (8 * a.tiles_n), high = min(8, a.tiles_m - 8 * band), in = tile - band * 8 * a.tiles_n;
+  const int tm = 8 * band + in % high, tn = in / high;
+  const int kb0 = (int)((int64_t)a.blocks_k * part / a.parts), kb1 = (int)((int64_t)a.blocks_k * (part + 1) / a.parts);
+
+  const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds);
+  // the blocks that this wavefront copies
+  const uint8_t *from[COPIES];
+  uint32_t to[COPIES];
+#pragma unroll
+  for (int c = 0; c < COPIES; ++c) {
+    const int i = w + WAVES * c;
+    if (i < XB) {
+      from[c] = a.x + ((int64_t)min(tm * XB + i, a.m_blocks - 1) * a.blocks_k + kb0) * kFp8XBlock;
+      to[c] = lds_at + i * kFp8XBlock;
+    } else {
+      from[c] = a.w + ((int64_t)min(tn * WB + i - XB, a.n_blocks - 1) * a.blocks_k + kb0) * kFp8WBlock;
+      to[c] = lds_at + W_AT + (i - XB) * kFp8WBlock;
+    }
+  }
+  auto fetch = [&](int stage) {          // the next block of K
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) {
+      const bool is_x = w + WAVES * c < XB;
+      const uint32_t at = to[c] + stage * STAGE;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) lds_dma16_s(from[c] + 1024 * j, 16 * lane, at + 1024 * j);
+      if (lane < (is_x ? 2 : 1)) lds_dma16_s(from[c] + kFp8Block, 16 * lane, at + kFp8Block);
+      from[c] += is_x ? kFp8XBlock : kFp8WBlock;
+    }
+  };
+
+  v16f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+#pragma unroll
+  for (int s = 0; s < ST - 1; ++s)
+    if (kb0 + s < kb1) fetch(s);
+  int stage = 0;
+  for (int kb = kb0; kb < kb1; ++kb) {
+    // stage `kb` has landed when only the copies of the stages after it are outstanding
+    if (ST > 2 && kb + ST - 1 <= kb1) vmcnt_wait<(ST - 2) * 5 * COPIES>();
+    else vmcnt_wait0();
+    __syncthreads();
+    if (kb + ST - 1 < kb1) fetch(stage == 0 ? ST - 1 : stage - 1);
+    const uint8_t *st = lds + stage * STAGE;
+    v4u wf[TN][4];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        wf[j][q] = *reinterpret_cast<const v4u *>(st + W_AT + (wn * TN + j) * kFp8WBlock + 1024 * q + 16 * lane);
+    uint2 sw[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) sw[j] = *reinterpret_cast<const uint2 *>(st + W_AT + (wn * TN + j) * kFp8WBlock + kFp8Block);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const uint8_t *xb = st + (wm * TM + i) * kFp8XBlock;
+      v4u xf[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) xf[q] = *reinterpret_cast<const v4u *>(xb + 1024 * q + 16 * lane);
+      const int sx = xb[kFp8Block + (lane & 31)];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const v16f p = mma(wf[j], (int)sw[j].y, xf, sx);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(p[e], __uint_as_float(sw[j].x), acc[i][j][e]);
+      }
+    }
+    stage = stage + 1 == ST ? 0 : stage + 1;
+  }
+
+  const int h = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t m = 32ll * ((int64_t)tm * XB + wm * TM + i) + (lane & 31);
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = 32 * (tn * WB + wn * TN + j) + 8 * q + 4 * h;
+        const v4f y = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if (n < a.N) store4<OUT>(a, m, n, y);
+      }
+  }
+}
+
+// Few rows.  A workgroup has 32 output channels; its eight wavefronts deal out
+// the blocks of K among themselves and add up in LDS.  Weights go from memory
+// straight into operands, AHEAD blocks of a wavefront in flight.  OWN: the
+// workgroup quantises the rows itself, into LDS (one block of 32 rows, up to 32768 channels in all).
+constexpr int kFp8RowsWaves = 8, kFp8Ahead = 4;
+template <int XB, bool OWN, bool F16, int OUT>
+__global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_rows_kernel(const Fp8Args a) {
+  constexpr int RED = kFp8RowsWaves * XB * 16 * 65 * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RED];
+  __shared__ __attribute__((aligned(16))) uint8_t xl[OWN ? 32768 : 16];
+  __shared__ uint8_t xs[OWN ? 256 : 1];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 31;
+  const int nb = blockIdx.x;
+  const uint8_t *wp = a.w + (int64_t)nb * a.blocks_k * kFp8WBlock;
+
+  v4u wf[kFp8Ahead][4];
+  uint2 sw[kFp8Ahead];
+  auto load = [&](int slot, int kb) {
+    const uint8_t *b = wp + (int64_t)min(kb, a.blocks_k - 1) * kFp8WBlock;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) wf[slot][q] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(b + 1024 * q + 16 * lane));
+    sw[slot] = *reinterpret_cast<const uint2 *>(b + kFp8Block);
+  };
+#pragma unroll
+  for (int i = 0; i < kFp8Ahead; ++i) load(i, w + kFp8RowsWaves * i);
+
+  if constexpr (OWN) {
+    // (row, block) pairs, eight lanes to each
+    for (int i = threadIdx.x >> 3; i < a.M * a.blocks_k; i += 8 * kFp8RowsWaves) {
+      const int kb = i / a.M, m = i - kb * a.M, u = threadIdx.x & 7;
+      v4u codes;
+      const uint32_t s = quantize16<F16>(a.rows + m * a.rows_stride, 128 * kb + 16 * u, a.K, codes);
+      *reinterpret_cast<v4u *>(xl + ((kb * 8 + u) * a.M + m) * 16) = codes;
+      if (u == 0) xs[i] = (uint8_t)s;
+    }
+    __syncthreads();
+  }
+
+  v16f acc[XB];
+#pragma unroll
+  for (int x = 0; x < XB; ++x)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[x][e] = 0.0f;
+  for (int base = w; base < a.blocks_k; base += kFp8RowsWaves * kFp8Ahead) {
+#pragma unroll
+    for (int i = 0; i < kFp8Ahead; ++i) {
+      const int kb = base + kFp8RowsWaves * i;
+      if (kb >= a.blocks_k) break;
+#pragma unroll
+      for (int x = 0; x < XB; ++x) {
+        v4u xf[4];
+        int sx;
+        if constexpr (OWN) {
+          const bool in = r < a.M;
+          const int rr = in ? r : 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            xf[q] = *reinterpret_cast<const v4u *>(xl + ((kb * 8 + 2 * q + (lane >> 5)) * a.M + rr) * 16);
+            if (!in) xf[q] = v4u{0u, 0u, 0u, 0u};
+          }
+          sx = xs[kb * a.M + rr];
+        } else {
+          const uint8_t *b = a.x + ((int64_t)min(x, a.m_blocks - 1) * a.blocks_k + kb) * kFp8XBlock;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) xf[q] = *reinterpret_cast<const v4u *>(b + 1024 * q + 16 * lane);
+          sx = b[kFp8Block + r];
+        }
+        const v16f p = mma(wf[i], (int)sw[i].y, xf, sx);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[x][e] = __builtin_fmaf(p[e], __uint_as_float(sw[i].x), acc[x][e]);
+      }
+      if (kb + kFp8RowsWaves * kFp8Ahead < a.blocks_k) load(i, kb + kFp8RowsWaves * kFp8Ahead);
+    }
+  }
+  float *red = reinterpret_cast<float *>(lds);      // [wavefront][block][register][65]
+#pragma unroll
+  for (int x = 0; x < XB; ++x)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) red[((w * XB + x) * 16 + e) * 65 + lane] = acc[x][e];
+  __syncthreads();
+  const int rows = min(a.M, 32 * XB);
+  for (int i = threadIdx.x; i < 32 * rows; i += 64 * kFp8RowsWaves) {
+    const int c = i & 31, m = i >> 5, n = 32 * nb + c;
+    if (n >= a.N) continue;
+    const int e = (c >> 3) * 4 + (c & 3), l = (c >> 2 & 1) * 32 + (m & 31), x = m >> 5;
+    float y = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kFp8RowsWaves; ++v) y += red[((v * XB + x) * 16 + e) * 65 + l];
+    if (a.bias) y += a.bias[n];
+    if (a.gelu) y = gelu_tanh_f32(y);
+    a.out[(int64_t)m * a.N + n] = narrow<OUT>(y);
+  }
+}
+
+template <int OUT>
+void launch_product(const Fp8Plan &p, Fp8Args &a, bool f16, hipStream_t stream) {
+  if (p.form == FP8_ROWS) {
+    const dim3 grid((unsigned)a.n_blocks), block(64 * kFp8RowsWaves);
+    if (p.inline_x && f16) hipLaunchKernelGGL((fp8_rows_kernel<1, true, true, OUT>), grid, block, 0, stream, a);
+    else if (p.inline_x) hipLaunchKernelGGL((fp8_rows_kernel<1, true, false, OUT>), grid, block, 0, stream, a);
+    else if (p.x_blocks == 1) hipLaunchKernelGGL((fp8_rows_kernel<1, false, false, OUT>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((fp8_rows_kernel<2, false, false, OUT>), grid, block, 0, stream, a);
+    return;
+  }
+  const int side = p.form == FP8_256 ? 256 : p.form == FP8_128 ? 128 : 64;
+  a.tiles_m = (a.M + side - 1) / side;
+  a.tiles_n = (a.N + side - 1) / side;
+  const dim3 grid((unsigned)((a.tiles_m * a.tiles_n * a.parts + 7) / 8 * 8));
+  if (p.form == FP8_256) hipLaunchKernelGGL((fp8_tile_kernel<4, 2, 2, 4, 2, OUT>), grid, dim3(512), 0, stream, a);
+  else if (p.form == FP8_128) hipLaunchKernelGGL((fp8_tile_kernel<2, 2, 2, 2, 2, OUT>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((fp8_tile_kernel<1, 1, 2, 2, 4, OUT>), grid, dim3(256), 0, stream, a);
+}
+
+svdq_status_t rows_ok(const char *who, const void *x, int64_t x_row, svdq_dtype_t dtype) {
+  if (dtype != SVDQ_BF16 && dtype != SVDQ_FP16)
+    return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: x must be SVDQ_BF16 or SVDQ_FP16", who);
+  if (!aligned16(x) || x_row < 0 || x_row % 8 != 0)
+    return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: misaligned x, or a row stride that is not a multiple of 8", who);
+  return SVDQ_OK;
+}
+
+void launch_quantize(const void *x, int64_t x_row, svdq_dtype_t dtype, int M, int K, void *out, uint8_t *scales,
+                     hipStream_t stream) {
+  const int blocks_k = (K + 127) / 128;
+  const dim3 grid((unsigned)((int64_t)((M + 31) / 32) * blocks_k));
+  const uint16_t *xp = static_cast<const uint16_t *>(x);
+  uint8_t *to = static_cast<uint8_t *>(out);
+#define FP8_QUANTIZE(FF, CC) \
+  hipLaunchKernelGGL((fp8_quantize_kernel<FF, CC>), grid, dim3(256), 0, stream, xp, x_row, M, K, blocks_k, to, scales)
+  if (dtype == SVDQ_FP16) {
+    if (scales) FP8_QUANTIZE(true, true);
+    else FP8_QUANTIZE(true, false);
+  } else {
+    if (scales) FP8_QUANTIZE(false, true);
+    else FP8_QUANTIZE(false, false);
+  }
+#undef FP8_QUANTIZE
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status_t svdq_fp8_pack_on_device(const uint8_t *codes, const float *scales, int N, int K, void *blob, size_t bytes,
+                                      void *hip_stream) {
+  const char *who = "svdq_fp8_pack_on_device";
+  if (!fp8_weights_ok(N, K)) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%s: N=%d K=%d", who, N, K);
+  if (!codes || !scales || !blob) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: NULL pointer", who);
+  if (!aligned16(codes) || !aligned16(blob) || ((uintptr_t)scales & 3u))
+    return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", who);
+  if (bytes < (size_t)fp8_w_bytes(N, K))
+    return fail(SVDQ_ERR_WORKSPACE_TOO_SMALL, "%s: blob needs %lld bytes, got %zu", who, (long long)fp8_w_bytes(N, K), bytes);
+  svdq_status_t st = svdq_device_check();
+  if (st != SVDQ_OK) return st;
+  const int blocks_k = (K + 127) / 128;
+  hipLaunchKernelGGL(fp8_pack_kernel, dim3((unsigned)((int64_t)((N + 31) / 32) * blocks_k)), dim3(256), 0,
+                     static_cast<hipStream_t>(hip_stream), codes, scales, N, K, blocks_k, static_cast<uint8_t *>(blob));
+  return launch_status("fp8 pack launch");
+}
+
+svdq_status_t svdq_fp8_quantize_activations(const void *x, int64_t x_row, svdq_dtype_t dtype, int M, int K,
+                                            uint8_t *codes, uint8_t *scales, void *hip_stream) {
+  const char *who = "svdq_fp8_quantize_activations";
+  if (!fp8_weights_ok(1, K) || !fp8_call_ok(M, K)) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%s: M=%d K=%d", who, M, K);
+  if (M == 0) return SVDQ_OK;
+  if (!x || !codes || !scales) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: NULL pointer", who);
+  svdq_status_t st = rows_ok(who, x, x_row, dtype);
+  if (st != SVDQ_OK) return st;
+  if (!aligned16(codes)) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: misaligned codes", who);
+  st = svdq_device_check();
+  if (st != SVDQ_OK) return st;
+  launch_quantize(x, x_row, dtype, M, K, codes, scales, static_cast<hipStream_t>(hip_stream));
+  return launch_status("fp8 quantize launch");
+}
+
+svdq_status_t svdq_fp8_linear_forward(const svdq_fp8_weights_t *w, const void *x, int64_t x_row, svdq_dtype_t x_dtype,
+                                      int M, void *out, svdq_dtype_t out_dtype, svdq_epilogue_t epilogue,
+                                      void *workspace, size_t ws_bytes, void *hip_stream) {
+  const char *who = "svdq_fp8_linear_forward";
+  if (!w || !w->blob) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: NULL weights", who);
+  if (!aligned16(w->blob) || ((uintptr_t)w->bias & 3u)) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: misaligned weights", who);
+  if (!fp8_weights_ok(w->N, w->K) || !fp8_call_ok(M, w->N) || !fp8_call_ok(M, w->K))
+    return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%s: M=%d N=%d K=%d", who, M, w->N, w->K);
+  if (epilogue != SVDQ_EPILOGUE_NONE && epilogue != SVDQ_EPILOGUE_GELU_TANH)
+    return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: epilogue %d", who, (int)epilogue);
+  if (out_dtype != SVDQ_BF16 && out_dtype != SVDQ_FP16)
+    return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: out must be SVDQ_BF16 or SVDQ_FP16", who);
+  svdq_status_t st = rows_ok(who, x, x_row, x_dtype);
+  if (st != SVDQ_OK) return st;
+  if (M == 0) return SVDQ_OK;
+  const Fp8Plan p = fp8_plan(M, w->N, w->K);
+  if (!x || !out || (!workspace && p.total > 0)) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: NULL pointer", who);
+  if (!aligned16(out) || !aligned16(workspace)) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", who);
+  if (ws_bytes < (size_t)p.total)
+    return fail(SVDQ_ERR_WORKSPACE_TOO_SMALL, "%s: workspace needs %lld bytes, got %zu", who, (long long)p.total, ws_bytes);
+  st = svdq_device_check();
+  if (st != SVDQ_OK) return st;
+  const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  Fp8Args a{};
+  a.w = static_cast<const uint8_t *>(w->blob);
+  a.x = static_cast<const uint8_t *>(workspace);
+  a.bias = w->bias;
+  a.out = static_cast<uint16_t *>(out);
+  a.M = M;
+  a.N = w->N;
+  a.K = w->K;
+  a.blocks_k = (w->K + 127) / 128;
+  a.m_blocks = (M + 31) / 32;
+  a.n_blocks = (w->N + 31) / 32;
+  a.parts = p.parts;
+  a.gelu = epilogue == SVDQ_EPILOGUE_GELU_TANH;
+  a.rows = static_cast<const uint16_t *>(x);
+  a.rows_stride = x_row;
+  if (!p.inline_x) {
+    launch_quantize(x, x_row, x_dtype, M, w->K, workspace, nullptr, stream);
+    st = launch_status("fp8 quantize launch");
+    if (st != SVDQ_OK) return st;
+  }
+  const bool f16 = x_dtype == SVDQ_FP16;
+  if (out_dtype == SVDQ_FP16) launch_product<SVDQ_FP16>(p, a, f16, stream);
+  else launch_product<SVDQ_BF16>(p, a, f16, stream);
+  return launch_status("fp8 product launch");
+}
+
+}  // extern "C"

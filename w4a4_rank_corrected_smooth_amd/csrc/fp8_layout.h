@@ -1,0 +1,60 @@
+// Layout, limits and workspace of the 8-bit floating point linear, shared by the
+// host's size queries and the device kernels.
+#pragma once
+
+#include <stdint.h>
+
+namespace svdq {
+
+// Codes are kept in blocks of 32 rows (of X, or of W: output channels) by 128
+// channels, 4096 bytes in the order of the matrix operand: channel c of row r is byte c
+// % 16 of unit q = c / 16, and unit q of row r stands at
+//   (q / 2) 1024 + (q % 2) 512 + 16 r,
+// so that lane l = 32 (q % 2) + r of a wavefront reads its two 32-byte operands of
+// a 32x32x64 instruction as four contiguous kilobytes.  Rows and channels past the
+// end are zeros in W; X's channels too, and its rows are never looked at.  Behind the
+// codes stand the block's scales: 32 bytes E8M0, one a row (X), or the scale of the
+// 128 x 128 block as m 2^(e - 127), m float32 and e an int32, in 8 of 16 bytes (W).
+constexpr int kFp8Block = 4096;
+constexpr int kFp8XBlock = kFp8Block + 32;
+constexpr int kFp8WBlock = kFp8Block + 16;
+
+constexpr bool fp8_weights_ok(int64_t N, int64_t K) {
+  return N >= 1 && N <= (1 << 20) && K >= 8 && K <= (1 << 20) && K % 8 == 0 && N * K <= (int64_t)1 << 33;
+}
+constexpr bool fp8_call_ok(int64_t M, int64_t N) { return M >= 0 && M <= (1 << 22) && M * N <= (int64_t)1 << 34; }
+
+constexpr int64_t fp8_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+constexpr int64_t fp8_w_bytes(int64_t N, int64_t K) { return fp8_up(N, 32) / 32 * (fp8_up(K, 128) / 128) * kFp8WBlock; }
+constexpr int64_t fp8_x_bytes(int64_t M, int64_t K) {
+  return fp8_up(fp8_up(M, 32) / 32 * (fp8_up(K, 128) / 128) * kFp8XBlock, 256);
+}
+
+// Which kernel multiplies, and how its work is cut.
+enum Fp8Form { FP8_ROWS = 0, FP8_64 = 1, FP8_128 = 2, FP8_256 = 3 };
+struct Fp8Plan {
+  Fp8Form form = FP8_ROWS;
+  bool inline_x = false;       // FP8_ROWS: each workgroup quantises the rows for itself
+  int x_blocks = 1;            // FP8_ROWS: blocks of 32 rows
+  int parts = 1;               // pieces of K
+  int64_t part_off = 0, total = 0;
+};
+
+inline Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
+  Fp8Plan p;
+  const int64_t kb = (K + 127) / 128;
+  if (M <= 32) {
+    p.inline_x = M * kb * 128 <= 32768;
+  } else if (M <= 64) {
+    p.x_blocks = 2;
+  } else {
+    const int64_t t128 = (M + 127) / 128 * ((N + 127) / 128), t256 = (M + 255) / 256 * ((N + 255) / 256);
+    p.form = t256 >= 512 ? FP8_256 : t128 >= 192 ? FP8_128 : FP8_64;
+  }
+  (void)kb;
+  p.part_off = p.inline_x ? 0 : fp8_x_bytes(M, K);
+  p.total = p.part_off + (p.parts > 1 ? fp8_up(4 * (int64_t)p.parts * M * N, 256) : 0);
+  return p;
+}
+
+}  // namespace svdq

@@ -6,6 +6,7 @@
 #include "host_prepare.h"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <vector>
@@ -479,6 +480,42 @@ svdq_status_t awq_moe_pack(const uint8_t *q, const uint16_t *s, const uint16_t *
       }
     }
   });
+  return SVDQ_OK;
+}
+
+// The e4m3 code of |v| <= 448, ties to even: in steps of 2^-9 below 2^-6, with
+// three bits behind the first above.
+static uint8_t f32_to_e4m3(float v) {
+  const uint32_t u = f32_bits(v), a = u & 0x7FFFFFFFu, sign = u >> 24 & 0x80u;
+  if (f32_from_bits(a) < 0x1p-6f) return (uint8_t)(sign | (uint32_t)std::nearbyint(f32_from_bits(a) * 512.0f));
+  return (uint8_t)(sign | (((a + 0x7FFFFu + (a >> 20 & 1u)) >> 20) - (120u << 3)));
+}
+
+svdq_status_t fp8_quantize(const float *W, int N, int K, uint8_t *codes, float *scales) {
+  const int64_t KB = ((int64_t)K + 127) / 128;
+  std::atomic<bool> finite{true};
+  parallel_for(((int64_t)N + 127) / 128, 1, [&](int64_t begin, int64_t end) {
+    for (int64_t nb = begin; nb < end; ++nb)
+      for (int64_t kb = 0; kb < KB; ++kb) {
+        const int64_t n1 = std::min<int64_t>(N, 128 * nb + 128), k1 = std::min<int64_t>(K, 128 * kb + 128);
+        float top = 0.0f;
+        bool ok = true;
+        for (int64_t n = 128 * nb; n < n1; ++n)
+          for (int64_t k = 128 * kb; k < k1; ++k) {
+            const float a = std::fabs(W[n * K + k]);
+            ok = ok && std::isfinite(a);
+            top = std::max(top, a);
+          }
+        if (!ok) finite = false;
+        float scale = top / 448.0f;
+        if (!(scale > 0.0f)) scale = 1.0f;
+        scales[nb * KB + kb] = scale;
+        for (int64_t n = 128 * nb; ok && n < n1; ++n)
+          for (int64_t k = 128 * kb; k < k1; ++k)
+            codes[n * K + k] = f32_to_e4m3(std::max(-448.0f, std::min(448.0f, W[n * K + k] / scale)));
+      }
+  });
+  if (!finite) return fail(SVDQ_ERR_NUMERICAL, "svdq_fp8_quantize_weights: W is not finite");
   return SVDQ_OK;
 }
 

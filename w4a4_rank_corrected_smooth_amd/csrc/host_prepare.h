@@ -40,4 +40,6 @@ svdq_status_t awq_pack(const uint8_t *q, const uint16_t *s, const uint16_t *z, i
 svdq_status_t awq_moe_pack(const uint8_t *q, const uint16_t *s, const uint16_t *z, int E, int N, int K,
                            void *host_blob, size_t bytes);
 
+svdq_status_t fp8_quantize(const float *W, int N, int K, uint8_t *codes, float *scales);
+
 }  // namespace svdq
