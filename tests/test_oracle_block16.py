@@ -233,18 +233,18 @@ def test_fp8_weight_quantiser_edges():
 
 def test_fp8_argument_errors():
     lib = S._lib
-    assert lib.svdq_fp8_device_weights_bytes(33, 136) == 2 * 2 * 4112
+    assert lib.svdq_fp8_device_weights_bytes(33, 136) == 2 * 2 * 4104
     for bad in ((0, 8), (1, 0), (1, 12), (-1, 8), ((1 << 20) + 1, 8), (1, (1 << 20) + 8), (1 << 20, 1 << 14)):
         assert lib.svdq_fp8_device_weights_bytes(*bad) == 0
     assert lib.svdq_fp8_workspace_bytes(0, 1, 8) >= 1 and lib.svdq_fp8_workspace_bytes(100, 64, 256) >= 100 * 256
     for bad in ((-1, 1, 8), (1, 1, 12), ((1 << 22) + 1, 1, 8), (1 << 20, 1 << 15, 8), (1 << 20, 8, 1 << 15)):
         assert lib.svdq_fp8_workspace_bytes(*bad) == 0
 
-    def pack(codes=FAKE, scales=FAKE, N=33, K=136, blob=FAKE, n=4 * 4112):
+    def pack(codes=FAKE, scales=FAKE, N=33, K=136, blob=FAKE, n=4 * 4104):
         return lib.svdq_fp8_pack_on_device(codes, scales, N, K, blob, n, None)
     assert pack(codes=0) == INV and pack(scales=0) == INV and pack(blob=0) == INV and pack(codes=FAKE + 8) == INV
     assert pack(blob=FAKE + 4) == INV and pack(scales=FAKE + 2) == INV and pack(K=132) == SHAPE and pack(N=0) == SHAPE
-    assert pack(n=4 * 4112 - 1) == WS
+    assert pack(n=4 * 4104 - 1) == WS
     w = S.Fp8Weights(FAKE, None, 64, 256)
     need = lib.svdq_fp8_workspace_bytes(100, 64, 256)
 

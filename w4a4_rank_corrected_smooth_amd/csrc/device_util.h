@@ -45,6 +45,11 @@ __device__ __forceinline__ void lds_dma16_s(const void *sbase, uint32_t voff, ui
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(voff), "s"(sbase), "s"(lds_base) : "memory");
 }
+// and of 4 bytes per lane: lane i writes LDS address lds_base + 4 i
+__device__ __forceinline__ void lds_dma4_s(const void *sbase, uint32_t voff, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds_base) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void vmcnt_wait() {
   asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");

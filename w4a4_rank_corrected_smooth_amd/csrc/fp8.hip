@@ -25,6 +25,7 @@ namespace {
 
 struct Fp8Args {
   const uint8_t *w, *x;          // blocks
+  const uint8_t *ws, *xs;        // their scales
   const float *bias;
   uint16_t *out;
   float *part;                   // pieces [part][M][N], or NULL
@@ -99,9 +100,8 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(const uint16_t *__res
     if (k + 8 < K) *reinterpret_cast<uint2 *>(to + 8) = make_uint2(codes[2], codes[3]);
     if (u == 0) scales[(int64_t)m * blocks_k + kb] = (uint8_t)s;
   } else {
-    uint8_t *to = out + (int64_t)blockIdx.x * kFp8XBlock;
-    *reinterpret_cast<v4u *>(to + (u >> 1) * 1024 + (u & 1) * 512 + 16 * r) = codes;
-    if (u == 0) to[kFp8Block + r] = (uint8_t)s;
+    *reinterpret_cast<v4u *>(out + (int64_t)blockIdx.x * kFp8Block + (u >> 1) * 1024 + (u & 1) * 512 + 16 * r) = codes;
+    if (u == 0) scales[(int64_t)blockIdx.x * kFp8XScales + r] = (uint8_t)s;
   }
 }
 
@@ -113,31 +113,32 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const uint8_t *__restrict
   uint2 lo = make_uint2(0, 0), hi = lo;
   if (n < N && k < K) lo = *reinterpret_cast<const uint2 *>(src);
   if (n < N && k + 8 < K) hi = *reinterpret_cast<const uint2 *>(src + 8);
-  uint8_t *to = blob + (int64_t)blockIdx.x * kFp8WBlock;
-  *reinterpret_cast<uint4 *>(to + (u >> 1) * 1024 + (u & 1) * 512 + 16 * r) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  *reinterpret_cast<uint4 *>(blob + (int64_t)blockIdx.x * kFp8Block + (u >> 1) * 1024 + (u & 1) * 512 + 16 * r) = make_uint4(lo.x, lo.y, hi.x, hi.y);
   if (threadIdx.x == 0) {
     const float sw = scales[(int64_t)(nb / 4) * blocks_k + kb];
     const uint32_t e = max(__float_as_uint(sw) >> 23 & 255u, 1u);
     // 2^(e - 127) with e from 1 (a subnormal scale's m is below 1) to 254
     const float m = ldexpf(sw, 127 - (int)e);
-    *reinterpret_cast<uint4 *>(to + kFp8Block) = make_uint4(__float_as_uint(m), e, 0, 0);
+    *reinterpret_cast<uint2 *>(blob + (int64_t)gridDim.x * kFp8Block + (int64_t)blockIdx.x * kFp8WScales) =
+        make_uint2(__float_as_uint(m), e);
   }
 }
 
 // ------------------------------------------------------------------ product
-__device__ __forceinline__ v16f mma(const v4u (&w)[4], int we, const v4u (&x)[4], int sx) {
+// One half (64 channels) of a tile's product with a block of K.
+__device__ __forceinline__ v16f mma_half(const v4u &w0, const v4u &w1, int we, const v4u &x0, const v4u &x1, int sx, v16f p) {
+  const v8i a = {(int)w0[0], (int)w0[1], (int)w0[2], (int)w0[3], (int)w1[0], (int)w1[1], (int)w1[2], (int)w1[3]};
+  const v8i b = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, p, 0, 0, 0, we, 0, sx);
+}
+__device__ __forceinline__ v16f zero16() {
   v16f p;
 #pragma unroll
   for (int i = 0; i < 16; ++i) p[i] = 0.0f;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const v8i a = {(int)w[2 * h][0], (int)w[2 * h][1], (int)w[2 * h][2], (int)w[2 * h][3],
-                   (int)w[2 * h + 1][0], (int)w[2 * h + 1][1], (int)w[2 * h + 1][2], (int)w[2 * h + 1][3]};
-    const v8i b = {(int)x[2 * h][0], (int)x[2 * h][1], (int)x[2 * h][2], (int)x[2 * h][3],
-                   (int)x[2 * h + 1][0], (int)x[2 * h + 1][1], (int)x[2 * h + 1][2], (int)x[2 * h + 1][3]};
-    p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, p, 0, 0, 0, we, 0, sx);
-  }
   return p;
+}
+__device__ __forceinline__ v16f mma(const v4u (&w)[4], int we, const v4u (&x)[4], int sx) {
+  return mma_half(w[2], w[3], we, x[2], x[3], sx, mma_half(w[0], w[1], we, x[0], x[1], sx, zero16()));
 }
 
 // OUT: svdq_dtype_t of the result
@@ -158,71 +159,72 @@ __device__ __forceinline__ uint32_t pair_of(float a, float b) {
   }
 }
 
-// Four results of row m, channels n .. n + 3 (those below N).
-template <int OUT>
-__device__ __forceinline__ void store4(const Fp8Args &a, int64_t m, int n, v4f y) {
-  if (a.bias) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] += a.bias[min(n + e, a.N - 1)];
-  }
+// The epilogue of four results of one row, channels n .. n + 3.
+__device__ __forceinline__ v4f finish(const Fp8Args &a, v4f bias, v4f y) {
+  y += bias;
   if (a.gelu) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = gelu_tanh_f32(y[e]);
   }
-  const int64_t at = m * a.N + n;
-  if (n + 4 <= a.N && (a.N & 3) == 0) {
-    *reinterpret_cast<uint2 *>(a.out + at) = make_uint2(pair_of<OUT>(y[0], y[1]), pair_of<OUT>(y[2], y[3]));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (n + e < a.N) a.out[at + e] = narrow<OUT>(y[e]);
-  }
+  return y;
 }
 
 // A wavefront's tile is TM blocks of rows by TN blocks of channels, a workgroup's
 // WM by WN of those; ST stages of one block of K in LDS.
+//
+// The matrix core and the vector ALU work side by side only where the code lets them: the two
+// instructions of a tile are followed by the 16 FMAs of the tile before, eight to each
+// (alone, such an instruction takes 27 ns, with eight FMAs 31, and FMAs that wait for their own
+// tile's result cost their full 15 ns for eight).  Operands of the next block of K are read from LDS during the last row of
+// tiles, so that the barrier before it, which frees the stage just read for the
+// next copy, costs no read of its own.
 template <int TM, int TN, int WM, int WN, int ST, int OUT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args a) {
   constexpr int XB = TM * WM, WB = TN * WN, WAVES = WM * WN, COPIES = (XB + WB) / WAVES;
   static_assert((XB + WB) % WAVES == 0, "blocks dealt out evenly");
-  constexpr int W_AT = XB * kFp8XBlock, STAGE = W_AT + WB * kFp8WBlock;
+  // a stage: the blocks of X and W, then their scales, 256 bytes to each (what a copy writes)
+  constexpr int W_AT = XB * kFp8Block, XS_AT = W_AT + WB * kFp8Block, WS_AT = XS_AT + XB * 256;
+  constexpr int STAGE = WS_AT + WB * 256;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * STAGE];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w % WM, wn = w / WM;
   // Workgroups are dealt out to the eight XCDs in turn: each XCD gets a contiguous
   // run of tiles, eight rows of tiles high, so that its L2 holds few rows and channels.
-  const int tiles = a.tiles_m * a.tiles_n * a.parts, per = (tiles + 7) / 8;
+  const int tiles = a.tiles_m * a.tiles_n, per = (tiles + 7) / 8;
   const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= per || id >= tiles) return;
-  const int part = id / (a.tiles_m * a.tiles_n), tile = id - part * (a.tiles_m * a.tiles_n);
-  const int band = tile / (8 * a.tiles_n), high = min(8, a.tiles_m - 8 * band), in = tile - band * 8 * a.tiles_n;
+  const int band = id / (8 * a.tiles_n), high = min(8, a.tiles_m - 8 * band), in = id - band * 8 * a.tiles_n;
   const int tm = 8 * band + in % high, tn = in / high;
-  const int kb0 = (int)((int64_t)a.blocks_k * part / a.parts), kb1 = (int)((int64_t)a.blocks_k * (part + 1) / a.parts);
 
   const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds);
   // the blocks that this wavefront copies
-  const uint8_t *from[COPIES];
-  uint32_t to[COPIES];
+  const uint8_t *from[COPIES], *scale[COPIES];
+  uint32_t scale_lane[COPIES];
+  int scale_step[COPIES];
 #pragma unroll
   for (int c = 0; c < COPIES; ++c) {
     const int i = w + WAVES * c;
-    if (i < XB) {
-      from[c] = a.x + ((int64_t)min(tm * XB + i, a.m_blocks - 1) * a.blocks_k + kb0) * kFp8XBlock;
-      to[c] = lds_at + i * kFp8XBlock;
-    } else {
-      from[c] = a.w + ((int64_t)min(tn * WB + i - XB, a.n_blocks - 1) * a.blocks_k + kb0) * kFp8WBlock;
-      to[c] = lds_at + W_AT + (i - XB) * kFp8WBlock;
-    }
+    const bool is_x = i < XB;
+    const int64_t at = (int64_t)(is_x ? min(tm * XB + i, a.m_blocks - 1) : min(tn * WB + i - XB, a.n_blocks - 1)) * a.blocks_k;
+    from[c] = (is_x ? a.x : a.w) + at * kFp8Block;
+    scale_step[c] = is_x ? kFp8XScales : kFp8WScales;
+    scale[c] = (is_x ? a.xs : a.ws) + at * scale_step[c];
+    scale_lane[c] = min(4 * lane, scale_step[c] - 4);
   }
-  auto fetch = [&](int stage) {          // the next block of K
+  // The next block of K, five copies for each of its blocks; behind the last one
+  // it is copied again, so that the loop has no branch for the compiler to move its work across.
+  int fetched = 0;
+  auto fetch = [&](int stage) {
+    const int more = ++fetched < a.blocks_k ? 1 : 0;
 #pragma unroll
     for (int c = 0; c < COPIES; ++c) {
-      const bool is_x = w + WAVES * c < XB;
-      const uint32_t at = to[c] + stage * STAGE;
+      const int i = w + WAVES * c;
+      const uint32_t at = lds_at + stage * STAGE;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) lds_dma16_s(from[c] + 1024 * j, 16 * lane, at + 1024 * j);
-      if (lane < (is_x ? 2 : 1)) lds_dma16_s(from[c] + kFp8Block, 16 * lane, at + kFp8Block);
-      from[c] += is_x ? kFp8XBlock : kFp8WBlock;
+      for (int j = 0; j < 4; ++j) lds_dma16_s(from[c] + 1024 * j, 16 * lane, at + i * kFp8Block + 1024 * j);
+      lds_dma4_s(scale[c], scale_lane[c], at + XS_AT + i * 256);
+      from[c] += more * kFp8Block;
+      scale[c] += more * scale_step[c];
     }
   };
 
@@ -234,56 +236,124 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
+  v4u wf[TN][4], xf[4];
+  uint2 sw[TN];
+  int sx;
+  auto read_w = [&](const uint8_t *st, int j, int half) {
 #pragma unroll
-  for (int s = 0; s < ST - 1; ++s)
-    if (kb0 + s < kb1) fetch(s);
+    for (int q = 2 * half; q < 2 * half + 2; ++q)
+      wf[j][q] = *reinterpret_cast<const v4u *>(st + W_AT + (wn * TN + j) * kFp8Block + 1024 * q + 16 * lane);
+    if (half == 1) sw[j] = *reinterpret_cast<const uint2 *>(st + WS_AT + (wn * TN + j) * 256);
+  };
+  auto read_x = [&](const uint8_t *st, int i, int half) {
+#pragma unroll
+    for (int q = 2 * half; q < 2 * half + 2; ++q)
+      xf[q] = *reinterpret_cast<const v4u *>(st + (wm * TM + i) * kFp8Block + 1024 * q + 16 * lane);
+    if (half == 1) sx = st[XS_AT + (wm * TM + i) * 256 + (lane & 31)];
+  };
+
+#pragma unroll
+  for (int s = 0; s < ST; ++s) fetch(s);
+  vmcnt_wait<(ST - 1) * 5 * COPIES>();
+  __syncthreads();
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) read_w(lds, j, half);
+    read_x(lds, 0, half);
+  }
+  // the product before, not yet added, and its m: its tile is the last one
+  v16f p[2] = {zero16(), zero16()};
+  float m = 0.0f;
   int stage = 0;
-  for (int kb = kb0; kb < kb1; ++kb) {
-    // stage `kb` has landed when only the copies of the stages after it are outstanding
-    if (ST > 2 && kb + ST - 1 <= kb1) vmcnt_wait<(ST - 2) * 5 * COPIES>();
-    else vmcnt_wait0();
-    __syncthreads();
-    if (kb + ST - 1 < kb1) fetch(stage == 0 ? ST - 1 : stage - 1);
+  for (int kb = 0; kb < a.blocks_k; ++kb) {
     const uint8_t *st = lds + stage * STAGE;
-    v4u wf[TN][4];
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        wf[j][q] = *reinterpret_cast<const v4u *>(st + W_AT + (wn * TN + j) * kFp8WBlock + 1024 * q + 16 * lane);
-    uint2 sw[TN];
-#pragma unroll
-    for (int j = 0; j < TN; ++j) sw[j] = *reinterpret_cast<const uint2 *>(st + W_AT + (wn * TN + j) * kFp8WBlock + kFp8Block);
+    const int next = stage + 1 == ST ? 0 : stage + 1;
+    const uint8_t *ahead = lds + next * STAGE;        // behind the last block: bytes that are read and not used
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const uint8_t *xb = st + (wm * TM + i) * kFp8XBlock;
-      v4u xf[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) xf[q] = *reinterpret_cast<const v4u *>(xb + 1024 * q + 16 * lane);
-      const int sx = xb[kFp8Block + (lane & 31)];
+      const bool last = i + 1 == TM;
+      if (last) {
+        // All reads of this stage are done, and the next one has landed when only the
+        // copies of those after it are outstanding.
+        vmcnt_wait<(ST - 2) * 5 * COPIES>();
+        __syncthreads();
+        fetch(stage);
+      }
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        const v16f p = mma(wf[j], (int)sw[j].y, xf, sx);
+        const int s = i * TN + j;
+        const float m_now = __uint_as_float(sw[j].x);
+        const int we = (int)sw[j].y, scale_x = sx;
+        v16f &sum = s == 0 ? acc[TM - 1][TN - 1] : acc[(s - 1) / TN][(s - 1) % TN];
+        const v16f &before = p[~s & 1];
+        v16f now = zero16();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(p[e], __uint_as_float(sw[j].x), acc[i][j][e]);
+        for (int half = 0; half < 2; ++half) {
+          now = mma_half(wf[j][2 * half], wf[j][2 * half + 1], we, xf[2 * half], xf[2 * half + 1], scale_x, now);
+          // operands that this was the last to use make room for their successors
+          if (last) read_w(ahead, j, half);
+          if (j + 1 == TN) read_x(last ? ahead : st, last ? 0 : i + 1, half);
+#pragma unroll
+          for (int e = 8 * half; e < 8 * half + 8; ++e) sum[e] = __builtin_fmaf(before[e], m, sum[e]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        p[s & 1] = now;
+        m = m_now;
       }
     }
-    stage = stage + 1 == ST ? 0 : stage + 1;
+    if constexpr (TM * TN & 1) p[1] = p[0];
+    stage = next;
   }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[TM - 1][TN - 1][e] = __builtin_fmaf(p[1][e], m, acc[TM - 1][TN - 1][e]);
 
-  const int h = lane >> 5;
+  // Results go through LDS, 32 rows at a time, so that a row's channels leave in whole
+  // lines: 8 bytes a lane to 32 rows took a quarter of the kernel's time.
+  constexpr int PITCH = 64 * TN + 16;                  // bytes of a row in LDS
+  static_assert(WAVES * 32 * PITCH <= ST * STAGE, "LDS");
+  vmcnt_wait0();
+  __syncthreads();
+  const int h = lane >> 5, n0 = 32 * (tn * WB + wn * TN);
+  uint8_t *mine = lds + w * 32 * PITCH;
+  const bool whole = (a.N & 7) == 0;
+  v4f bias[TN][4];
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bias[j][q][e] = a.bias ? a.bias[min(n0 + 32 * j + 8 * q + 4 * h + e, a.N - 1)] : 0.0f;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int64_t m = 32ll * ((int64_t)tm * XB + wm * TM + i) + (lane & 31);
-    if (m >= a.M) continue;
+    const int64_t m0 = 32ll * ((int64_t)tm * XB + wm * TM + i);
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int n = 32 * (tn * WB + wn * TN + j) + 8 * q + 4 * h;
-        const v4f y = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        if (n < a.N) store4<OUT>(a, m, n, y);
+        const v4f y = finish(a, bias[j][q], v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
+        *reinterpret_cast<uint2 *>(mine + (lane & 31) * PITCH + 64 * j + 16 * q + 8 * h) =
+            make_uint2(pair_of<OUT>(y[0], y[1]), pair_of<OUT>(y[2], y[3]));
       }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    constexpr int LANES = 4 * TN, ROWS = 64 / LANES;   // lanes of 16 bytes to a row
+#pragma unroll
+    for (int r = lane / LANES; r < 32; r += ROWS) {
+      const uint4 y = *reinterpret_cast<const uint4 *>(mine + r * PITCH + (lane % LANES) * 16);
+      const int n = n0 + (lane % LANES) * 8;
+      if (m0 + r < a.M && n < a.N) {
+        uint16_t *dst = a.out + (m0 + r) * a.N + n;
+        if (whole) {
+          *reinterpret_cast<uint4 *>(dst) = y;
+        } else {
+          const uint32_t words[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < a.N) dst[e] = (uint16_t)(words[e / 2] >> (16 * (e & 1)));
+        }
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
@@ -300,15 +370,16 @@ __global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_rows_kernel(const Fp8A
   __shared__ uint8_t xs[OWN ? 256 : 1];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 31;
   const int nb = blockIdx.x;
-  const uint8_t *wp = a.w + (int64_t)nb * a.blocks_k * kFp8WBlock;
+  const uint8_t *wp = a.w + (int64_t)nb * a.blocks_k * kFp8Block, *wsp = a.ws + (int64_t)nb * a.blocks_k * kFp8WScales;
 
   v4u wf[kFp8Ahead][4];
   uint2 sw[kFp8Ahead];
   auto load = [&](int slot, int kb) {
-    const uint8_t *b = wp + (int64_t)min(kb, a.blocks_k - 1) * kFp8WBlock;
+    kb = min(kb, a.blocks_k - 1);
+    const uint8_t *b = wp + (int64_t)kb * kFp8Block;
 #pragma unroll
     for (int q = 0; q < 4; ++q) wf[slot][q] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(b + 1024 * q + 16 * lane));
-    sw[slot] = *reinterpret_cast<const uint2 *>(b + kFp8Block);
+    sw[slot] = *reinterpret_cast<const uint2 *>(wsp + (int64_t)kb * kFp8WScales);
   };
 #pragma unroll
   for (int i = 0; i < kFp8Ahead; ++i) load(i, w + kFp8RowsWaves * i);
@@ -349,10 +420,11 @@ __global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_rows_kernel(const Fp8A
           }
           sx = xs[kb * a.M + rr];
         } else {
-          const uint8_t *b = a.x + ((int64_t)min(x, a.m_blocks - 1) * a.blocks_k + kb) * kFp8XBlock;
+          const int64_t at = (int64_t)min(x, a.m_blocks - 1) * a.blocks_k + kb;
+          const uint8_t *b = a.x + at * kFp8Block;
 #pragma unroll
           for (int q = 0; q < 4; ++q) xf[q] = *reinterpret_cast<const v4u *>(b + 1024 * q + 16 * lane);
-          sx = b[kFp8Block + r];
+          sx = a.xs[at * kFp8XScales + r];
         }
         const v16f p = mma(wf[i], (int)sw[i].y, xf, sx);
 #pragma unroll
@@ -409,7 +481,7 @@ svdq_status_t rows_ok(const char *who, const void *x, int64_t x_row, svdq_dtype_
 }
 
 void launch_quantize(const void *x, int64_t x_row, svdq_dtype_t dtype, int M, int K, void *out, uint8_t *scales,
-                     hipStream_t stream) {
+                     bool canon, hipStream_t stream) {
   const int blocks_k = (K + 127) / 128;
   const dim3 grid((unsigned)((int64_t)((M + 31) / 32) * blocks_k));
   const uint16_t *xp = static_cast<const uint16_t *>(x);
@@ -417,10 +489,10 @@ void launch_quantize(const void *x, int64_t x_row, svdq_dtype_t dtype, int M, in
 #define FP8_QUANTIZE(FF, CC) \
   hipLaunchKernelGGL((fp8_quantize_kernel<FF, CC>), grid, dim3(256), 0, stream, xp, x_row, M, K, blocks_k, to, scales)
   if (dtype == SVDQ_FP16) {
-    if (scales) FP8_QUANTIZE(true, true);
+    if (canon) FP8_QUANTIZE(true, true);
     else FP8_QUANTIZE(true, false);
   } else {
-    if (scales) FP8_QUANTIZE(false, true);
+    if (canon) FP8_QUANTIZE(false, true);
     else FP8_QUANTIZE(false, false);
   }
 #undef FP8_QUANTIZE
@@ -458,7 +530,7 @@ svdq_status_t svdq_fp8_quantize_activations(const void *x, int64_t x_row, svdq_d
   if (!aligned16(codes)) return fail(SVDQ_ERR_INVALID_ARGUMENT, "%s: misaligned codes", who);
   st = svdq_device_check();
   if (st != SVDQ_OK) return st;
-  launch_quantize(x, x_row, dtype, M, K, codes, scales, static_cast<hipStream_t>(hip_stream));
+  launch_quantize(x, x_row, dtype, M, K, codes, scales, true, static_cast<hipStream_t>(hip_stream));
   return launch_status("fp8 quantize launch");
 }
 
@@ -488,6 +560,8 @@ svdq_status_t svdq_fp8_linear_forward(const svdq_fp8_weights_t *w, const void *x
   Fp8Args a{};
   a.w = static_cast<const uint8_t *>(w->blob);
   a.x = static_cast<const uint8_t *>(workspace);
+  a.ws = a.w + fp8_blocks(w->N, w->K) * kFp8Block;
+  a.xs = a.x + fp8_blocks(M, w->K) * kFp8Block;
   a.bias = w->bias;
   a.out = static_cast<uint16_t *>(out);
   a.M = M;
@@ -501,7 +575,7 @@ svdq_status_t svdq_fp8_linear_forward(const svdq_fp8_weights_t *w, const void *x
   a.rows = static_cast<const uint16_t *>(x);
   a.rows_stride = x_row;
   if (!p.inline_x) {
-    launch_quantize(x, x_row, x_dtype, M, w->K, workspace, nullptr, stream);
+    launch_quantize(x, x_row, x_dtype, M, w->K, workspace, const_cast<uint8_t *>(a.xs), false, stream);
     st = launch_status("fp8 quantize launch");
     if (st != SVDQ_OK) return st;
   }

@@ -11,13 +11,13 @@ namespace svdq {
 // % 16 of unit q = c / 16, and unit q of row r stands at
 //   (q / 2) 1024 + (q % 2) 512 + 16 r,
 // so that lane l = 32 (q % 2) + r of a wavefront reads its two 32-byte operands of
-// a 32x32x64 instruction as four contiguous kilobytes.  Rows and channels past the
-// end are zeros in W; X's channels too, and its rows are never looked at.  Behind the
-// codes stand the block's scales: 32 bytes E8M0, one a row (X), or the scale of the
-// 128 x 128 block as m 2^(e - 127), m float32 and e an int32, in 8 of 16 bytes (W).
+// a 32x32x64 instruction as four contiguous kilobytes.  The blocks of 32 rows follow each
+// other along K.  Rows and channels past the end are zeros in W; X's channels too, and its rows
+// are never looked at.  Behind all codes stand the scales, in the blocks' order: X's as 32
+// bytes E8M0 a block, one a row; W's as m 2^(e - 127) of the 128 x 128 block, m
+// float32 and e an int32.
 constexpr int kFp8Block = 4096;
-constexpr int kFp8XBlock = kFp8Block + 32;
-constexpr int kFp8WBlock = kFp8Block + 16;
+constexpr int kFp8XScales = 32, kFp8WScales = 8;    // bytes a block
 
 constexpr bool fp8_weights_ok(int64_t N, int64_t K) {
   return N >= 1 && N <= (1 << 20) && K >= 8 && K <= (1 << 20) && K % 8 == 0 && N * K <= (int64_t)1 << 33;
@@ -25,10 +25,9 @@ constexpr bool fp8_weights_ok(int64_t N, int64_t K) {
 constexpr bool fp8_call_ok(int64_t M, int64_t N) { return M >= 0 && M <= (1 << 22) && M * N <= (int64_t)1 << 34; }
 
 constexpr int64_t fp8_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-constexpr int64_t fp8_w_bytes(int64_t N, int64_t K) { return fp8_up(N, 32) / 32 * (fp8_up(K, 128) / 128) * kFp8WBlock; }
-constexpr int64_t fp8_x_bytes(int64_t M, int64_t K) {
-  return fp8_up(fp8_up(M, 32) / 32 * (fp8_up(K, 128) / 128) * kFp8XBlock, 256);
-}
+constexpr int64_t fp8_blocks(int64_t rows, int64_t K) { return fp8_up(rows, 32) / 32 * (fp8_up(K, 128) / 128); }
+constexpr int64_t fp8_w_bytes(int64_t N, int64_t K) { return fp8_blocks(N, K) * (kFp8Block + kFp8WScales); }
+constexpr int64_t fp8_x_bytes(int64_t M, int64_t K) { return fp8_up(fp8_blocks(M, K) * (kFp8Block + kFp8XScales), 256); }
 
 // Which kernel multiplies, and how its work is cut.
 enum Fp8Form { FP8_ROWS = 0, FP8_64 = 1, FP8_128 = 2, FP8_256 = 3 };
