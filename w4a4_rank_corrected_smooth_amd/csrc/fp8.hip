@@ -211,21 +211,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args
     scale[c] = (is_x ? a.xs : a.ws) + at * scale_step[c];
     scale_lane[c] = min(4 * lane, scale_step[c] - 4);
   }
-  // The next block of K, five copies for each of its blocks; behind the last one
+  // The next block of K, five copies for each of its blocks, one at a time; behind the last one
   // it is copied again, so that the loop has no branch for the compiler to move its work across.
+  constexpr int FETCHES = 5 * COPIES;
   int fetched = 0;
-  auto fetch = [&](int stage) {
-    const int more = ++fetched < a.blocks_k ? 1 : 0;
-#pragma unroll
-    for (int c = 0; c < COPIES; ++c) {
-      const int i = w + WAVES * c;
-      const uint32_t at = lds_at + stage * STAGE;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) lds_dma16_s(from[c] + 1024 * j, 16 * lane, at + i * kFp8Block + 1024 * j);
+  auto fetch1 = [&](int stage, int f) {
+    const int c = f / 5, j = f % 5, i = w + WAVES * c;
+    const uint32_t at = lds_at + stage * STAGE;
+    if (j < 4) {
+      lds_dma16_s(from[c] + 1024 * j, 16 * lane, at + i * kFp8Block + 1024 * j);
+    } else {
       lds_dma4_s(scale[c], scale_lane[c], at + XS_AT + i * 256);
+      if (c + 1 == COPIES) ++fetched;
+      const int more = c + 1 == COPIES ? fetched < a.blocks_k : fetched + 1 < a.blocks_k;
       from[c] += more * kFp8Block;
       scale[c] += more * scale_step[c];
     }
+  };
+  auto fetch = [&](int stage) {
+#pragma unroll
+    for (int f = 0; f < FETCHES; ++f) fetch1(stage, f);
   };
 
   v16f acc[TM][TN];
@@ -246,15 +251,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args
     if (half == 1) sw[j] = *reinterpret_cast<const uint2 *>(st + WS_AT + (wn * TN + j) * 256);
   };
   auto read_x = [&](const uint8_t *st, int i, int half) {
+    if (half == 0) sx = st[XS_AT + (wm * TM + i) * 256 + (lane & 31)];
 #pragma unroll
     for (int q = 2 * half; q < 2 * half + 2; ++q)
       xf[q] = *reinterpret_cast<const v4u *>(st + (wm * TM + i) * kFp8Block + 1024 * q + 16 * lane);
-    if (half == 1) sx = st[XS_AT + (wm * TM + i) * 256 + (lane & 31)];
   };
 
 #pragma unroll
   for (int s = 0; s < ST; ++s) fetch(s);
-  vmcnt_wait<(ST - 1) * 5 * COPIES>();
+  vmcnt_wait<(ST - 1) * FETCHES>();
   __syncthreads();
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -276,9 +281,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args
       if (last) {
         // All reads of this stage are done, and the next one has landed when only the
         // copies of those after it are outstanding.
-        vmcnt_wait<(ST - 2) * 5 * COPIES>();
+        vmcnt_wait<(ST - 2) * FETCHES>();
         __syncthreads();
-        fetch(stage);
       }
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
@@ -290,9 +294,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args
         v16f now = zero16();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          __builtin_amdgcn_s_setprio(1);
           now = mma_half(wf[j][2 * half], wf[j][2 * half + 1], we, xf[2 * half], xf[2 * half + 1], scale_x, now);
+          __builtin_amdgcn_s_setprio(0);
           // operands that this was the last to use make room for their successors
-          if (last) read_w(ahead, j, half);
+          if (last) {
+            read_w(ahead, j, half);
+#pragma unroll
+            for (int f = (2 * j + half) * FETCHES / (2 * TN); f < (2 * j + half + 1) * FETCHES / (2 * TN); ++f) fetch1(stage, f);
+          }
           if (j + 1 == TN) read_x(last ? ahead : st, last ? 0 : i + 1, half);
 #pragma unroll
           for (int e = 8 * half; e < 8 * half + 8; ++e) sum[e] = __builtin_fmaf(before[e], m, sum[e]);
