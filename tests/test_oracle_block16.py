@@ -123,7 +123,7 @@ def test_cross_oracle_is_a_softmax():
 
 def test_cross_workspace_and_shapes():
     f = S._lib.svdq_cross_attention_workspace_bytes
-    assert f(1, 4096, 512, 16, 16, 128, 0) >= 1 and f(2, 4096, 300, 16, 16, 72, 1) >= 4 * 2 * 300
+    assert f(1, 4096, 512, 16, 16, 128, 0) >= 1 and f(2, 4096, 4100, 16, 16, 72, 1) >= 4 * 2 * 4100
     assert f(8, 1, 1500, 20, 20, 64, 0) > 0 and f(0, 0, 0, 1, 1, 8, 0) >= 1
     for bad in ((-1, 1, 1, 1, 1, 64), (65537, 1, 1, 1, 1, 64), (1, -1, 1, 1, 1, 64), (1, 1, -1, 1, 1, 64), (1, 1, (1 << 30) + 1, 1, 1, 64),
                 (1, 1, 1, 0, 1, 64), (1, 1, 1, 1, 0, 64), (1, 1, 1, 3, 2, 64), (1, 1, 1, 1, 1, 0), (1, 1, 1, 1, 1, 60),
@@ -132,10 +132,10 @@ def test_cross_workspace_and_shapes():
 
 
 def test_cross_argument_errors():
-    need = S._lib.svdq_cross_attention_workspace_bytes(2, 4, 50, 4, 2, 64, 1)
+    need = S._lib.svdq_cross_attention_workspace_bytes(2, 4, 5000, 4, 2, 64, 1)
     row = dict(q=(FAKE, 1024, 256, 64), k=(FAKE, 8192, 128, 64), v=(FAKE, 8192, 128, 64))
 
-    def go(dt=S.BF16, B=2, Lq=4, Lk=50, Hq=4, Hkv=2, D=64, lens=None, mask=FAKE, scale=0.1, out=FAKE, ws=FAKE, n=need, **kw):
+    def go(dt=S.BF16, B=2, Lq=4, Lk=5000, Hq=4, Hkv=2, D=64, lens=None, mask=FAKE, scale=0.1, out=FAKE, ws=FAKE, n=need, **kw):
         r = {**row, **kw}
         return S._lib.svdq_cross_attention(*r["q"], *r["k"], *r["v"], dt, B, Lq, Lk, Hq, Hkv, D, lens, mask, scale, out, ws, n, None)
     for name in "qkv":

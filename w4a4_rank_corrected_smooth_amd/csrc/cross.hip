@@ -1,7 +1,8 @@
 // Cross attention: queries over an encoder's states of another length.
 //
 //  cross_list_kernel     the visible states of each batch row, where there is a mask
-//  cross_attend_kernel   attention of a tile of rows over a piece of the states
+//  cross_many_kernel     attention of a tile of rows over a piece of the states
+//  cross_few_kernel      the same for a handful of rows
 //  cross_join_kernel     joins the pieces of a row
 //
 // One pass over the states with a running maximum m and sum l (float32, in units
@@ -45,12 +46,13 @@ constexpr float kShift16 = 7.0f;
 struct CrossArgs {
   const uint16_t *q, *k, *v;
   int64_t q_b, q_i, q_h, k_b, k_t, k_h, v_b, v_t, v_h;
-  const int *lens;                       // visible states of a batch row (or NULL: all)
-  const int *index;                      // [B, Lk] their numbers, where there is a mask
+  const int *lens;                       // states of a batch row (or NULL: all)
+  const uint8_t *mask;                   // which of them are visible: the workgroup lists them itself; or
+  const int *index, *count;              // [B, Lk] the visible ones' numbers, and how many
   uint16_t *out;
   float *ml, *o;                         // pieces: [piece][B Hkv][row] (m, l), and [..][D]
   int B, Lq, Lk, Hq, Hkv, group, D, rows, tiles, parts;
-  int64_t work, per_xcd;
+  int run, work;                         // pieces of work; how many go to one XCD together
   float c;
   uint32_t flip;
 };
@@ -82,146 +84,182 @@ __device__ __forceinline__ float half_sum(float x) {
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
-// The tiles' place in LDS, for blocks of 32 channels DB: rows of SLOTS chunks of 16 bytes.
-template <int DB, int KEYS>
-struct Tile {
+// Rows of K and V in LDS, for DB blocks of 32 channels: rows of SLOTS chunks of 16 bytes.
+template <int DB>
+struct Rows {
   static constexpr int SLOTS = DB <= 2 ? 8 : DB <= 4 ? 16 : 32;
-  static constexpr int ROW = SLOTS * 16, HALF = KEYS * ROW, BYTES = 2 * HALF;   // K, then V
-  static constexpr int COPY_ROWS = 64 / SLOTS;                                  // rows of one copy
+  static constexpr int ROW = SLOTS * 16, COPY_ROWS = 64 / SLOTS;   // bytes of a row, rows of one copy
   // A chunk's slot is the chunk xor this.  K: 8 or 16 neighbouring rows are read
   // at the same chunk.  V: 4 neighbouring rows at 4 neighbouring chunks.
   static __device__ __forceinline__ int k_swap(int row) { return SLOTS == 8 ? row >> 1 & 7 : SLOTS == 16 ? row & 15 : row & 7; }
   static __device__ __forceinline__ int v_swap(int row) { return SLOTS == 8 ? (row >> 1 & 1) << 2 : (row & 3) << 2; }
 };
 
-// DB: blocks of 32 channels.  KEYS: states of a tile.  OWN: the four wavefronts
-// share 32 rows and take tiles of their own, in LDS of their own, without barriers;
-// otherwise each has 32 rows and all read the same tiles.
-template <int DB, int KEYS, bool OWN, bool F16, bool LIST>
-__global__ __launch_bounds__(256, OWN && DB > 2 ? 1 : 2) void cross_attend_kernel(const CrossArgs a) {
-  typedef Tile<DB, KEYS> L;
-  constexpr int KB = KEYS / 32, STEPS = 2 * DB;
-  constexpr int COPIES = KEYS / L::COPY_ROWS / (OWN ? 1 : 4);     // copies of K (and of V) that a wavefront makes for a tile
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[(OWN ? 4 : 1) * 2 * L::BYTES];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Neighbouring pieces of work, which read the same states, go to one XCD (workgroups
-  // are dealt out to the eight in turn).
-  const int64_t id = (int64_t)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
-  if (id >= a.work) return;
-  const int tile_row = (int)(id % a.tiles), part = (int)(id / a.tiles % a.parts);
-  const int64_t bh = id / a.tiles / a.parts;
-  const int b = (int)(bh / a.Hkv), hk = (int)(bh - (int64_t)b * a.Hkv);
-  int n = a.lens ? min(max(a.lens[b], 0), a.Lk) : a.Lk;
-  const int all = (n + KEYS - 1) / KEYS;                           // tiles
-  int t0 = (int)((int64_t)all * part / a.parts), t1 = (int)((int64_t)all * (part + 1) / a.parts);
-  if constexpr (OWN) t0 += w;
-  constexpr int STRIDE = OWN ? 4 : 1;
+// Numbers the visible ones of n states in order, by WAVES wavefronts, and returns how many: a
+// thread counts a run of neighbouring states and writes it behind the runs before.
+template <int WAVES>
+__device__ __forceinline__ int list_visible(const uint8_t *seen, int n, int *out) {
+  __shared__ int sums[WAVES];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int run = (n + 64 * WAVES - 1) / (64 * WAVES);
+  const int from = (int)min((int64_t)threadIdx.x * run, (int64_t)n), to = min(from + run, n);
+  int mine = 0;
+  for (int t = from; t < to; ++t) mine += seen[t] != 0;
+  int upto = mine;                                   // of this lane and those before it
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) {
+    const int y = __shfl_up(upto, x);
+    if (lane >= x) upto += y;
+  }
+  if (lane == 63) sums[w] = upto;
+  __syncthreads();
+  int at = upto - mine, all = 0;
+  for (int i = 0; i < WAVES; ++i) {
+    at += i < w ? sums[i] : 0;
+    all += sums[i];
+  }
+  if (mine)
+    for (int t = from; t < to; ++t)
+      if (seen[t] != 0) out[at++] = t;
+  return all;
+}
 
-  // this lane's row and the queries' operand
-  const int m = lane & 31, h = lane >> 5;
-  const int row = tile_row * (OWN ? 32 : 128) + (OWN ? 0 : 32 * w) + m;
-  const int rr = min(row, a.rows - 1), qi = rr / a.group, hq = hk * a.group + rr - qi * a.group;
-  v4u q[STEPS];
-  {
-    const uint16_t *src = a.q + (int64_t)b * a.q_b + qi * a.q_i + hq * a.q_h;
+// A workgroup's piece of the work, the same in all its lanes, and its batch row's states.
+struct Piece {
+  int tile_row, part, bh, b, hk, n, t0, t1;
+  const int *index;                      // where there is a mask
+  bool any;
+  // Workgroups are dealt out to the eight XCDs in turn: runs of neighbouring row tiles,
+  // which read the same states, go to one XCD.
+  __device__ __forceinline__ explicit Piece(const CrossArgs &a) {
+    const uint32_t x = blockIdx.x & 7, i = blockIdx.x >> 3, run = (uint32_t)a.run;
+    const uint32_t id = (i / run * 8 + x) * run + i % run;
+    any = id < (uint32_t)a.work;
+    const uint32_t piece = id / (uint32_t)a.tiles;
+    tile_row = (int)(id - piece * (uint32_t)a.tiles);
+    bh = (int)(piece / (uint32_t)a.parts);
+    part = (int)piece - bh * a.parts;
+    b = (int)((uint32_t)bh / (uint32_t)a.Hkv);
+    hk = bh - b * a.Hkv;
+  }
+  // The states, listed in `list` if they are not listed yet, and this piece's tiles of `keys` of them.
+  template <bool LIST>
+  __device__ __forceinline__ void cut(const CrossArgs &a, int keys, int *list) {
+    n = a.lens ? min(max(a.lens[b], 0), a.Lk) : a.Lk;
+    if constexpr (LIST) {
+      if (a.mask) {
+        n = list_visible<4>(a.mask + (int64_t)b * a.Lk, n, list);
+        __syncthreads();
+        index = list;
+      } else {
+        n = a.count[b];
+        index = a.index + (int64_t)b * a.Lk;
+      }
+    }
+    const uint32_t all = (uint32_t)(n + keys - 1) / (uint32_t)keys;
+    t0 = a.parts == 1 ? 0 : (int)((uint64_t)all * part / (uint32_t)a.parts);
+    t1 = a.parts == 1 ? (int)all : (int)((uint64_t)all * (part + 1) / (uint32_t)a.parts);
+  }
+};
+
+// Where a lane's row is, and its operand of the first product.
+struct Row {
+  int row, qi, hq;
+  __device__ __forceinline__ Row(const CrossArgs &a, const Piece &p, int row_) : row(row_) {
+    const int rr = min(row, a.rows - 1);
+    qi = rr / a.group;
+    hq = p.hk * a.group + rr - qi * a.group;
+  }
+  template <int STEPS>
+  __device__ __forceinline__ void load(const CrossArgs &a, const Piece &p, int h, v4u (&q)[STEPS]) const {
+    const uint16_t *src = a.q + (int64_t)p.b * a.q_b + qi * a.q_i + hq * a.q_h;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       const int at = 16 * s + 8 * h;
       q[s] = at < a.D ? *reinterpret_cast<const v4u *>(src + at) : v4u{0u, 0u, 0u, 0u};
-      q[s] ^= a.flip;
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) q[s] ^= a.flip;
+  }
+};
+
+// Copies a tile's rows into LDS, K's and V's, COPIES copies of each by one of WAVES wavefronts.
+template <int DB, int KEYS, int WAVES, bool LIST>
+struct Copier {
+  typedef Rows<DB> L;
+  static constexpr int COPIES = KEYS / L::COPY_ROWS / WAVES;
+  const uint8_t *k, *v;
+  const int *index;
+  int64_t k_t, v_t;                      // bytes from a state to the next
+  int n, chunks, lane, w;
+  int key[COPIES];                       // the listed states of the next tile's rows, this lane's
+  __device__ __forceinline__ Copier(const CrossArgs &a, const Piece &p, int lane_, int w_)
+      : k(reinterpret_cast<const uint8_t *>(a.k + (int64_t)p.b * a.k_b + p.hk * a.k_h)),
+        v(reinterpret_cast<const uint8_t *>(a.v + (int64_t)p.b * a.v_b + p.hk * a.v_h)), index(p.index), k_t(2 * a.k_t),
+        v_t(2 * a.v_t), n(p.n), chunks(a.D / 8), lane(lane_), w(w_) {}
+  __device__ __forceinline__ int base_of(int j) const { return (WAVES * j + w) * L::COPY_ROWS; }
+  // Reads tile t's part of the list, a tile ahead of its use.
+  __device__ __forceinline__ void look_up(int t) {
+    if constexpr (LIST) {
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j) key[j] = index[min(t * KEYS + base_of(j) + lane / L::SLOTS, n - 1)];
     }
   }
-
-  uint8_t *mine = lds + (OWN ? w * 2 * L::BYTES : 0);
-  const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)mine);
-  // chunks past D are never copied: zeros from the start
-  if (a.D < 32 * DB) {
-    for (int i = threadIdx.x * 16; i < (int)sizeof(lds); i += 256 * 16) *reinterpret_cast<uint4 *>(lds + i) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-  }
-
-  const uint8_t *kb = reinterpret_cast<const uint8_t *>(a.k + (int64_t)b * a.k_b + hk * a.k_h);
-  const uint8_t *vb = reinterpret_cast<const uint8_t *>(a.v + (int64_t)b * a.v_b + hk * a.v_h);
-  const int *index = LIST ? a.index + (int64_t)b * a.Lk : nullptr;
-  const int chunks = a.D / 8, slot = lane & (L::SLOTS - 1);
-  // Copies tile t's rows into buffer `buf`.
-  auto fetch = [&](int t, int buf) {
-    const bool whole = !LIST && (t + 1) * KEYS <= n;
+  // Rows behind the last state repeat it.
+  __device__ __forceinline__ void both(int t, uint32_t k_to, uint32_t v_to) const {
+    const int slot = lane & (L::SLOTS - 1);
+    if (!LIST && (t + 1) * KEYS <= n && chunks == 4 * DB) {
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j) {
+        const int base = base_of(j), r = base + lane / L::SLOTS, kc = slot ^ L::k_swap(r), vc = slot ^ L::v_swap(r);
+        const int64_t first = (int64_t)t * KEYS + base;
+        if (L::SLOTS == 4 * DB || kc < 4 * DB)
+          lds_dma16_s(k + first * k_t, (uint32_t)(lane / L::SLOTS) * (uint32_t)k_t + 16 * kc, k_to + base * L::ROW);
+        if (L::SLOTS == 4 * DB || vc < 4 * DB)
+          lds_dma16_s(v + first * v_t, (uint32_t)(lane / L::SLOTS) * (uint32_t)v_t + 16 * vc, v_to + base * L::ROW);
+      }
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < COPIES; ++j) {
-      const int base = (OWN ? j : 4 * j + w) * L::COPY_ROWS, r = base + lane / L::SLOTS;
-      const int kc = slot ^ L::k_swap(r), vc = slot ^ L::v_swap(r);
-      const uint32_t to = lds_at + buf * L::BYTES + base * L::ROW;
-      if (whole) {
-        const int64_t first = (int64_t)t * KEYS + base;
-        if (kc < chunks) lds_dma16_s(kb + 2 * first * a.k_t, (uint32_t)(lane / L::SLOTS) * (uint32_t)(2 * a.k_t) + 16 * kc, to);
-        if (vc < chunks) lds_dma16_s(vb + 2 * first * a.v_t, (uint32_t)(lane / L::SLOTS) * (uint32_t)(2 * a.v_t) + 16 * vc, to + L::HALF);
-      } else {
-        int key = min(t * KEYS + r, n - 1);
-        if constexpr (LIST) key = index[key];
-        if (kc < chunks) lds_dma16(kb + 2 * (int64_t)key * a.k_t + 16 * kc, to);
-        if (vc < chunks) lds_dma16(vb + 2 * (int64_t)key * a.v_t + 16 * vc, to + L::HALF);
-      }
+      const int base = base_of(j), r = base + lane / L::SLOTS, kc = slot ^ L::k_swap(r), vc = slot ^ L::v_swap(r);
+      const int64_t at = LIST ? key[j] : min(t * KEYS + r, n - 1);
+      if (kc < chunks) lds_dma16(k + at * k_t + 16 * kc, k_to + base * L::ROW);
+      if (vc < chunks) lds_dma16(v + at * v_t + 16 * vc, v_to + base * L::ROW);
     }
-  };
+  }
+};
 
+__device__ __forceinline__ uint32_t lds_offset(const void *p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)p);
+}
+__device__ __forceinline__ v16f zero16() {
+  v16f z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  return z;
+}
+// Two transposing reads: the operand of 16 states by 32 channels.
+template <int DB>
+__device__ __forceinline__ v4u read_v(const uint8_t *at) {
+  typedef __attribute__((address_space(3))) v4i16 *Read;
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Read)(uint8_t *)at);
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Read)(uint8_t *)(at + 8 * Rows<DB>::ROW));
+  const uint2 x = __builtin_bit_cast(uint2, lo), y = __builtin_bit_cast(uint2, hi);
+  return v4u{x.x, x.y, y.x, y.y};
+}
+
+// A row's running state, and its results: pieces for the join, or the output.
+template <int DB, bool F16>
+struct Sums {
   v16f o[DB];
+  float top = kLowest, sum = 0.0f;       // `sum`: of this lane's half; the halves' are added at the end
+  __device__ __forceinline__ Sums() {
 #pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
-  float top = kLowest, sum = 0.0f;       // of this lane's half: the halves' sums are added at the end
-
-  const int k_lane = m * L::ROW, k_x = h ^ L::k_swap(m);
-  // the transposing read: row 4 h + (lane % 16) / 4 of a block of 16 states, channels 16 (lane / 16 % 2) + 4 (lane % 4)
-  const int v_row = 4 * h + (lane >> 2 & 3), v_z = L::v_swap(v_row) >> 2;
-  const int v_lane = L::HALF + v_row * L::ROW + (2 * (lane >> 4 & 1) + (lane >> 1 & 1)) * 16 + (lane & 1) * 8;
-
-  if (t0 < t1) fetch(t0, 0);
-  int buf = 0;
-  for (int t = t0; t < t1; t += STRIDE, buf ^= 1) {
-    vmcnt_wait0();
-    if constexpr (!OWN) __syncthreads();
-    const bool last = (t + 1) * KEYS > n;
-    uint8_t *st = mine + buf * L::BYTES;
-    if (last) {                            // V rows behind the last state: zero, whatever the last one holds
-      const int from = n - t * KEYS;
-      for (int i = from * L::ROW + (OWN ? lane : (int)threadIdx.x) * 16; i < L::HALF; i += (OWN ? 64 : 256) * 16)
-        *reinterpret_cast<uint4 *>(st + L::HALF + i) = make_uint4(0, 0, 0, 0);
-      if constexpr (OWN) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      else __syncthreads();
-    }
-    if (t + STRIDE < t1) {
-      if constexpr (OWN) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the other buffer has been read
-      fetch(t + STRIDE, buf ^ 1);
-    }
-
-    v16f s[KB];
-#pragma unroll
-    for (int k = 0; k < KB; ++k)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[k][i] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        const v4u x = *reinterpret_cast<const v4u *>(st + 32 * k * L::ROW + k_lane + ((k_x ^ (2 * i)) << 4));
-        s[k] = mma<F16>(x, q[i], s[k]);
-      }
-    if (last) {
-      const int left = n - t * KEYS - 4 * h;
-#pragma unroll
-      for (int k = 0; k < KB; ++k)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (32 * k + 8 * (i / 4) + i % 4 >= left) s[k][i] = -__builtin_inff();
-    }
-    float best = s[0][0];
-#pragma unroll
-    for (int k = 0; k < KB; ++k)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) best = fmaxf(best, s[k][i]);
-    best = half_max(best) * a.c;
+    for (int d = 0; d < DB; ++d) o[d] = zero16();
+  }
+  // makes room for scores whose largest is `best` (times c)
+  __device__ __forceinline__ void raise(float best) {
     if (__any(best > top + kSlack)) {
       const float to = best > top + kSlack ? best : top;
       const float r = __builtin_amdgcn_exp2f(top - to);
@@ -232,93 +270,287 @@ __global__ __launch_bounds__(256, OWN && DB > 2 ? 1 : 2) void cross_attend_kerne
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= r;
     }
-    const float off = (F16 ? kShift16 : 0.0f) - top;
-#pragma unroll
-    for (int k = 0; k < KB; ++k) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][i], a.c, off));
-        sum += s[k][i];
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        v4u p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = pack2<F16>(s[k][8 * u + 2 * i], s[k][8 * u + 2 * i + 1]);
-#pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          typedef __attribute__((address_space(3))) v4i16 *Read;
-          const uint8_t *at = st + (32 * k + 16 * u) * L::ROW + v_lane + ((d ^ v_z) << 6);
-          const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Read)(uint8_t *)at);
-          const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Read)(uint8_t *)(at + 8 * L::ROW));
-          const uint2 x = __builtin_bit_cast(uint2, lo), y = __builtin_bit_cast(uint2, hi);
-          o[d] = mma<F16>(v4u{x.x, x.y, y.x, y.y}, p, o[d]);
-        }
-      }
-    }
   }
-
-  sum = half_sum(sum);
-  if (row >= a.rows) return;
-  if (a.ml) {
-    const int64_t piece = OWN ? 4 * part + w : part;
-    const int64_t at = (piece * a.B * a.Hkv + bh) * a.rows + row;
+  // a piece for the join
+  __device__ __forceinline__ void leave(const CrossArgs &a, const Piece &p, const Row &r, int h, int piece, bool some) {
+    sum = half_sum(sum);
+    if (r.row >= a.rows) return;
+    const int64_t at = ((int64_t)piece * a.B * a.Hkv + p.bh) * a.rows + r.row;
     if (h == 0) {
       a.ml[2 * at] = top;
-      a.ml[2 * at + 1] = t0 < t1 ? sum : -1.0f;      // -1: a piece without states
+      a.ml[2 * at + 1] = some ? sum : -1.0f;           // -1: a piece without states
     }
-    if (t0 < t1) {
+    if (!some) return;
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int ch = 32 * d + 8 * j + 4 * h;
-          if (ch < a.D)
-            *reinterpret_cast<v4f *>(a.o + at * a.D + ch) = v4f{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
-        }
-    }
-    return;
+      for (int j = 0; j < 4; ++j) {
+        const int ch = 32 * d + 8 * j + 4 * h;
+        if (ch < a.D)
+          *reinterpret_cast<v4f *>(a.o + at * a.D + ch) = v4f{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+      }
   }
-  const float inv = n > 0 ? 1.0f / sum : 0.0f;
-  uint16_t *dst = a.out + (((int64_t)b * a.Lq + qi) * a.Hq + hq) * a.D;
+  // The output of 32 rows from row0 on, through a wavefront's 2048 DB bytes of LDS, so that
+  // rows leave 16 bytes a lane.
+  __device__ __forceinline__ void finish(const CrossArgs &a, const Piece &p, int row0, int lane, uint8_t *mine) {
+    sum = half_sum(sum);
+    const float inv = p.n > 0 ? 1.0f / sum : 0.0f;
+    const int m = lane & 31, h = lane >> 5;
 #pragma unroll
-  for (int d = 0; d < DB; ++d)
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int ch = 32 * d + 8 * j + 4 * h;
-      if (ch < a.D)
-        *reinterpret_cast<uint2 *>(dst + ch) = make_uint2(pack2<F16>(o[d][4 * j] * inv, o[d][4 * j + 1] * inv),
-                                                          pack2<F16>(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv));
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint2 *>(mine + m * 64 * DB + ((4 * d + j) ^ (m & 3)) * 16 + 8 * h) =
+            make_uint2(pack2<F16>(o[d][4 * j] * inv, o[d][4 * j + 1] * inv), pack2<F16>(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv));
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) {
+      const int at = 64 * i + lane, m2 = at / (4 * DB), c = at % (4 * DB), row = row0 + m2;
+      if (row < a.rows && 8 * c < a.D) {
+        const int qi = row / a.group, hq = p.hk * a.group + row - qi * a.group;
+        *reinterpret_cast<uint4 *>(a.out + (((int64_t)p.b * a.Lq + qi) * a.Hq + hq) * a.D + 8 * c) =
+            *reinterpret_cast<const uint4 *>(mine + m2 * 64 * DB + (c ^ (m2 & 3)) * 16);
+      }
     }
+  }
+};
+
+// sets the scores of block rows from `left` on to -inf (h: the lane's half)
+__device__ __forceinline__ void hide(v16f &s, int left, int h) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (8 * (i / 4) + 4 * h + i % 4 >= left) s[i] = -__builtin_inff();
+}
+__device__ __forceinline__ float largest(const v16f &s) {
+  float best = s[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) best = fmaxf(best, s[i]);
+  return best;
+}
+
+// The exponentials of a block's scores, and packed as the operand of the second product (pw[u]: half u
+// of the block).  (Adding up with the two-element dot product, half the instructions, was slower.)
+template <bool F16>
+__device__ __forceinline__ void weigh(const v16f &s, float c, float off, float &sum, v4u (&pw)[2]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * e], c, off));
+    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * e + 1], c, off));
+    sum += x;
+    sum += y;
+    pw[e / 4][e % 4] = pack2<F16>(x, y);
+  }
+}
+
+// Many rows: each of the four wavefronts has 32, and all read the same tiles of
+// KEYS states, two in LDS.  While a 16-bit matrix instruction runs, the SIMD's vector ALU stands nearly
+// still (an instruction and 16 FMAs, from two wavefronts: 31 ns, 14 and 16 alone), so the kernel's time is the sum of
+// both: 16 instructions of 14 ns for 32 x 32 scores of 128 channels, and about 100 ns of maxima, exponentials and
+// conversions.  Ordering the two by hand, the next block's scores between this one's exponentials, was
+// slower than the compiler's order (564 against 539 us at 4096 x 16384, 16 heads).
+template <int DB, int KEYS, bool F16, bool LIST>
+__global__ __launch_bounds__(256, 2) void cross_many_kernel(const CrossArgs a) {
+  typedef Rows<DB> L;
+  constexpr int KB = KEYS / 32, STEPS = 2 * DB, HALF = KEYS * L::ROW;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * HALF];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ int list[LIST ? kCrossOwnList : 1];
+  Piece p(a);
+  if (!p.any) return;
+  p.template cut<LIST>(a, KEYS, list);
+  const int m = lane & 31, h = lane >> 5;
+  const uint32_t lds_at = lds_offset(lds);
+  // chunks past D are never copied: zeros from the start
+  if (a.D < 32 * DB) {
+    for (int i = threadIdx.x * 16; i < (int)sizeof(lds); i += 256 * 16) *reinterpret_cast<uint4 *>(lds + i) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
+  Copier<DB, KEYS, 4, LIST> copy(a, p, lane, w);
+  auto fetch = [&](int t, int buf) { copy.both(t, lds_at + 2 * buf * HALF, lds_at + (2 * buf + 1) * HALF); };
+  const int row0 = p.tile_row * 128 + 32 * w;
+  const Row r(a, p, row0 + m);
+  v4u q[STEPS];
+  if (p.t0 < p.t1) {
+    copy.look_up(p.t0);
+    fetch(p.t0, 0);
+    copy.look_up(p.t0 + 1);
+  }
+  r.load(a, p, h, q);
+
+  Sums<DB, F16> acc;
+  const int k_lane = m * L::ROW, k_x = h ^ L::k_swap(m);
+  // the transposing read: row 4 h + (lane % 16) / 4 of a block of 16 states, channels 16 (lane / 16 % 2) + 4 (lane % 4)
+  const int v_row = 4 * h + (lane >> 2 & 3), v_z = L::v_swap(v_row) >> 2;
+  const int v_lane = HALF + v_row * L::ROW + (2 * (lane >> 4 & 1) + (lane >> 1 & 1)) * 16 + (lane & 1) * 8;
+
+  int buf = 0;
+  for (int t = p.t0; t < p.t1; ++t, buf ^= 1) {
+    vmcnt_wait0_known();
+    __syncthreads();
+    const bool last = (t + 1) * KEYS > p.n;
+    uint8_t *st = lds + 2 * buf * HALF;
+    if (last) {                            // V rows behind the last state: zero, whatever the last one holds
+      for (int i = (p.n - t * KEYS) * L::ROW + (int)threadIdx.x * 16; i < HALF; i += 256 * 16)
+        *reinterpret_cast<uint4 *>(st + HALF + i) = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+    }
+    if (t + 1 < p.t1) {
+      fetch(t + 1, buf ^ 1);
+      copy.look_up(t + 2);
+    }
+    v16f s[KB];
+#pragma unroll
+    for (int k = 0; k < KB; ++k) s[k] = zero16();
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+        s[k] = mma<F16>(*reinterpret_cast<const v4u *>(st + 32 * k * L::ROW + k_lane + ((k_x ^ (2 * i)) << 4)), q[i], s[k]);
+    if (last) {
+#pragma unroll
+      for (int k = 0; k < KB; ++k) hide(s[k], p.n - t * KEYS - 32 * k, h);
+    }
+    float best = largest(s[0]);
+#pragma unroll
+    for (int k = 1; k < KB; ++k) best = fmaxf(best, largest(s[k]));
+    acc.raise(half_max(best) * a.c);
+    const float off = (F16 ? kShift16 : 0.0f) - acc.top;
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      v4u pw[2];
+      weigh<F16>(s[k], a.c, off, acc.sum, pw);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+          acc.o[d] = mma<F16>(read_v<DB>(st + (32 * k + 16 * u) * L::ROW + v_lane + ((d ^ v_z) << 6)), pw[u], acc.o[d]);
+    }
+  }
+  if (a.ml) {
+    acc.leave(a, p, r, h, p.part, p.t0 < p.t1);
+  } else {
+    __syncthreads();
+    acc.finish(a, p, row0, lane, lds + w * 2048 * DB);
+  }
+}
+
+// Few rows (up to 32 of a key/value head): the four wavefronts take tiles of 32 states of
+// their own, in LDS of their own, without barriers.  Bound by memory.
+template <int DB, bool F16, bool LIST>
+__global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const CrossArgs a) {
+  typedef Rows<DB> L;
+  constexpr int KEYS = 32, STEPS = 2 * DB, HALF = KEYS * L::ROW;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * 4 * HALF];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ int list[LIST ? kCrossOwnList : 1];
+  Piece p(a);
+  if (!p.any) return;
+  p.template cut<LIST>(a, KEYS, list);
+  const int m = lane & 31, h = lane >> 5;
+  uint8_t *mine = lds + w * 4 * HALF;
+  const uint32_t lds_at = lds_offset(mine);
+  if (a.D < 32 * DB) {
+    for (int i = lane * 16; i < 4 * HALF; i += 64 * 16) *reinterpret_cast<uint4 *>(mine + i) = make_uint4(0, 0, 0, 0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+  Copier<DB, KEYS, 1, LIST> copy(a, p, lane, 0);
+  auto fetch = [&](int t, int buf) { copy.both(t, lds_at + 2 * buf * HALF, lds_at + (2 * buf + 1) * HALF); };
+  const int t0 = p.t0 + w;
+  const Row r(a, p, m);
+  v4u q[STEPS];
+  if (t0 < p.t1) {
+    copy.look_up(t0);
+    fetch(t0, 0);
+    copy.look_up(t0 + 4);
+  }
+  r.load(a, p, h, q);
+
+  Sums<DB, F16> acc;
+  const int k_lane = m * L::ROW, k_x = h ^ L::k_swap(m);
+  const int v_row = 4 * h + (lane >> 2 & 3), v_z = L::v_swap(v_row) >> 2;
+  const int v_lane = HALF + v_row * L::ROW + (2 * (lane >> 4 & 1) + (lane >> 1 & 1)) * 16 + (lane & 1) * 8;
+  int buf = 0;
+  for (int t = t0; t < p.t1; t += 4, buf ^= 1) {
+    vmcnt_wait0_known();
+    asm volatile("" ::: "memory");
+    const bool last = (t + 1) * KEYS > p.n;
+    uint8_t *st = mine + 2 * buf * HALF;
+    if (last) {
+      for (int i = (p.n - t * KEYS) * L::ROW + lane * 16; i < HALF; i += 64 * 16)
+        *reinterpret_cast<uint4 *>(st + HALF + i) = make_uint4(0, 0, 0, 0);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");       // the other buffer has been read
+    if (t + 4 < p.t1) {
+      fetch(t + 4, buf ^ 1);
+      copy.look_up(t + 8);
+    }
+    v16f s = zero16();
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) s = mma<F16>(*reinterpret_cast<const v4u *>(st + k_lane + ((k_x ^ (2 * i)) << 4)), q[i], s);
+    if (last) hide(s, p.n - t * KEYS, h);
+    acc.raise(half_max(largest(s)) * a.c);
+    v4u pw[2];
+    weigh<F16>(s, a.c, (F16 ? kShift16 : 0.0f) - acc.top, acc.sum, pw);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) acc.o[d] = mma<F16>(read_v<DB>(st + 16 * u * L::ROW + v_lane + ((d ^ v_z) << 6)), pw[u], acc.o[d]);
+  }
+  acc.leave(a, p, r, h, 4 * p.part + w, t0 < p.t1);
 }
 
 // A wavefront joins a row's pieces: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
-template <bool F16>
+// LANES lanes hold a row's channels, four each; 64 / LANES pieces are read at a time, and four of
+// those in flight.
+template <int LANES, bool F16>
 __global__ __launch_bounds__(256) void cross_join_kernel(const CrossArgs a, int pieces) {
   const int lane = threadIdx.x & 63;
-  const int64_t heads = (int64_t)a.B * a.Hkv, all = heads * a.rows, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t all = (int64_t)a.B * a.Hkv * a.rows, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (at >= all) return;
-  float top = kLowest;
-  for (int i = lane; i < pieces; i += 64)
-    if (a.ml[2 * (i * all + at) + 1] != -1.0f) top = fmaxf(top, a.ml[2 * (i * all + at)]);
-#pragma unroll
-  for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-  const int ch = 4 * lane;
-  float sum = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int GROUPS = 64 / LANES;
+  const int g = lane / LANES, ch = 4 * (lane % LANES);
+  const float2 *ml = reinterpret_cast<const float2 *>(a.ml);
+  float top = kLowest, sum = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   bool some = false;
-  for (int i = 0; i < pieces; ++i) {
-    const float l = a.ml[2 * (i * all + at) + 1];
-    if (l == -1.0f) continue;
-    some = true;
-    const float f = __builtin_amdgcn_exp2f(a.ml[2 * (i * all + at)] - top);
-    sum = __builtin_fmaf(f, l, sum);
-    if (ch < a.D) {
-      const v4f x = *reinterpret_cast<const v4f *>(a.o + (i * all + at) * a.D + ch);
+  // 64 pieces at a time, their maxima and sums a lane each
+  for (int p0 = 0; p0 < pieces; p0 += 64) {
+    const float2 x = p0 + lane < pieces ? ml[(p0 + lane) * all + at] : make_float2(kLowest, -1.0f);
+    const bool in = x.y != -1.0f;
+    float to = in ? fmaxf(top, x.x) : top;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(f, x[e], o[e]);
+    for (int i = 32; i > 0; i >>= 1) to = fmaxf(to, __shfl_xor(to, i));
+    const float r = __builtin_amdgcn_exp2f(top - to), f = in ? __builtin_amdgcn_exp2f(x.x - to) : 0.0f;
+    some = some || __any(in);
+    top = to;
+    float add = in ? f * x.y : 0.0f;
+#pragma unroll
+    for (int i = 32; i > 0; i >>= 1) add += __shfl_xor(add, i);
+    sum = __builtin_fmaf(sum, r, add);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] *= r;
+    const uint64_t have = __ballot(in);
+    const int n = min(64, pieces - p0);
+    for (int i = 0; i < n; i += 4 * GROUPS) {
+      v4f y[4];
+      float fy[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = i + u * GROUPS + g;              // up to 63 + 3 GROUPS: the factor of a lane past 63 is not used
+        const bool ok = j < n && (have >> (j & 63) & 1) != 0 && ch < a.D;
+        fy[u] = __shfl(f, j & 63);
+        y[u] = ok ? *reinterpret_cast<const v4f *>(a.o + ((p0 + j) * all + at) * a.D + ch) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(fy[u], y[u][e], o[e]);
     }
   }
-  if (ch >= a.D) return;
+#pragma unroll
+  for (int i = LANES; i < 64; i <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], i);
+  if (g != 0 || ch >= a.D) return;
   const float inv = some ? 1.0f / sum : 0.0f;
   const int64_t bh = at / a.rows;
   const int row = (int)(at - bh * a.rows), qi = row / a.group, b = (int)(bh / a.Hkv);
@@ -327,31 +559,12 @@ __global__ __launch_bounds__(256) void cross_join_kernel(const CrossArgs a, int 
       make_uint2(pack2<F16>(o[0] * inv, o[1] * inv), pack2<F16>(o[2] * inv, o[3] * inv));
 }
 
-// The numbers of each batch row's visible states in order, and how many.  A
-// thread counts a run of neighbouring states and writes it behind the runs before.
+// The lists of all batch rows, where they are too long for a workgroup to make its own.
 __global__ __launch_bounds__(1024) void cross_list_kernel(const uint8_t *__restrict__ mask, const int *__restrict__ lens,
                                                           int Lk, int *__restrict__ index, int *__restrict__ count) {
-  __shared__ int sums[16];
-  const int b = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int n = lens ? min(max(lens[b], 0), Lk) : Lk;
-  const uint8_t *seen = mask + (int64_t)b * Lk;
-  int *out = index + (int64_t)b * Lk;
-  const int run = (n + 1023) / 1024;
-  const int from = min((int64_t)threadIdx.x * run, (int64_t)n), to = min(from + run, n);
-  int mine = 0;
-  for (int t = from; t < to; ++t) mine += seen[t] != 0;
-  int upto = mine;                                   // of this lane and those before it
-  for (int x = 1; x < 64; x <<= 1) {
-    const int y = __shfl_up(upto, x);
-    if (lane >= x) upto += y;
-  }
-  if (lane == 63) sums[w] = upto;
-  __syncthreads();
-  int at = upto - mine;
-  for (int i = 0; i < w; ++i) at += sums[i];
-  for (int t = from; t < to; ++t)
-    if (seen[t] != 0) out[at++] = t;
-  if (threadIdx.x == 1023) count[b] = at;
+  const int b = blockIdx.x, n = lens ? min(max(lens[b], 0), Lk) : Lk;
+  const int all = list_visible<16>(mask + (int64_t)b * Lk, n, index + (int64_t)b * Lk);
+  if (threadIdx.x == 0) count[b] = all;
 }
 
 }  // namespace
@@ -400,49 +613,64 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
   }
   a.lens = key_lens;
   const bool list = mask && Lk > 0;
-  if (list) {
+  if (list && Lk <= kCrossOwnList) {
+    a.mask = mask;
+  } else if (list) {
     int *index = reinterpret_cast<int *>(ws), *count = reinterpret_cast<int *>(ws + p.count_off);
     hipLaunchKernelGGL(cross_list_kernel, dim3(B), dim3(1024), 0, stream, mask, key_lens, Lk, index, count);
     st = launch_status("cross attention list launch");
     if (st != SVDQ_OK) return st;
     a.index = index;
-    a.lens = count;
+    a.count = count;
   }
   // Maxima are taken of the bare products, so the scale's sign goes to the queries, and
   // a scale of zero becomes one that still hides the rows behind the last state.
   a.c = fmaxf((float)(fabs((double)scale) * 1.4426950408889634), 1e-37f);
   a.flip = scale < 0.0f ? 0x80008000u : 0u;
-  a.work = (int64_t)B * Hkv * p.tiles * p.parts;
-  a.per_xcd = (a.work + 7) / 8;
-  const dim3 grid((unsigned)(8 * a.per_xcd));
-#define CROSS_GO(DB, KEYS, OWN, FF, LL) \
-  hipLaunchKernelGGL((cross_attend_kernel<DB, KEYS, OWN, FF, LL>), grid, dim3(256), 0, stream, a)
-#define CROSS_TYPE(DB, KEYS, OWN)                             \
-  do {                                                        \
-    if (dtype == SVDQ_FP16) {                                 \
-      if (list) CROSS_GO(DB, KEYS, OWN, true, true);          \
-      else CROSS_GO(DB, KEYS, OWN, true, false);              \
-    } else {                                                  \
-      if (list) CROSS_GO(DB, KEYS, OWN, false, true);         \
-      else CROSS_GO(DB, KEYS, OWN, false, false);             \
-    }                                                         \
+  a.work = (int)(B * Hkv * p.tiles * p.parts);        // at most 2^28 / 128 + 2^20
+  a.run = (int)(p.tiles < 32 ? p.tiles : 32);
+  const dim3 grid((unsigned)((a.work + 8 * a.run - 1) / (8 * a.run) * (8 * a.run)));
+#define CROSS_MANY(DB, KEYS)                                                              \
+  do {                                                                                    \
+    if (dtype == SVDQ_FP16) {                                                             \
+      if (list) hipLaunchKernelGGL((cross_many_kernel<DB, KEYS, true, true>), grid, dim3(256), 0, stream, a);   \
+      else hipLaunchKernelGGL((cross_many_kernel<DB, KEYS, true, false>), grid, dim3(256), 0, stream, a);       \
+    } else {                                                                              \
+      if (list) hipLaunchKernelGGL((cross_many_kernel<DB, KEYS, false, true>), grid, dim3(256), 0, stream, a);  \
+      else hipLaunchKernelGGL((cross_many_kernel<DB, KEYS, false, false>), grid, dim3(256), 0, stream, a);      \
+    }                                                                                     \
   } while (0)
-#define CROSS_FORM(DB, KEYS) do { if (p.own) CROSS_TYPE(DB, 32, true); else CROSS_TYPE(DB, KEYS, false); } while (0)
+#define CROSS_FEW(DB)                                                                     \
+  do {                                                                                    \
+    if (dtype == SVDQ_FP16) {                                                             \
+      if (list) hipLaunchKernelGGL((cross_few_kernel<DB, true, true>), grid, dim3(256), 0, stream, a);   \
+      else hipLaunchKernelGGL((cross_few_kernel<DB, true, false>), grid, dim3(256), 0, stream, a);       \
+    } else {                                                                              \
+      if (list) hipLaunchKernelGGL((cross_few_kernel<DB, false, true>), grid, dim3(256), 0, stream, a);  \
+      else hipLaunchKernelGGL((cross_few_kernel<DB, false, false>), grid, dim3(256), 0, stream, a);      \
+    }                                                                                     \
+  } while (0)
   switch (p.blocks) {
-    case 2: CROSS_FORM(2, 64); break;
-    case 3: CROSS_FORM(3, 64); break;
-    case 4: CROSS_FORM(4, 64); break;
-    case 5: CROSS_TYPE(5, 32, false); break;
-    default: CROSS_TYPE(8, 32, false); break;
+    case 2: if (p.own) CROSS_FEW(2); else CROSS_MANY(2, 64); break;
+    case 3: if (p.own) CROSS_FEW(3); else CROSS_MANY(3, 64); break;
+    case 4: if (p.own) CROSS_FEW(4); else CROSS_MANY(4, 64); break;
+    case 5: CROSS_MANY(5, 32); break;
+    default: CROSS_MANY(8, 32); break;
   }
-#undef CROSS_FORM
-#undef CROSS_TYPE
-#undef CROSS_GO
+#undef CROSS_FEW
+#undef CROSS_MANY
   st = launch_status("cross attention launch");
   if (st != SVDQ_OK || p.pieces == 1) return st;
   const dim3 joins((unsigned)(((int64_t)B * Hkv * p.rows + 3) / 4));
-  if (dtype == SVDQ_FP16) hipLaunchKernelGGL(cross_join_kernel<true>, joins, dim3(256), 0, stream, a, p.pieces);
-  else hipLaunchKernelGGL(cross_join_kernel<false>, joins, dim3(256), 0, stream, a, p.pieces);
+#define CROSS_JOIN(LANES)                                                                                            \
+  do {                                                                                                               \
+    if (dtype == SVDQ_FP16) hipLaunchKernelGGL((cross_join_kernel<LANES, true>), joins, dim3(256), 0, stream, a, p.pieces); \
+    else hipLaunchKernelGGL((cross_join_kernel<LANES, false>), joins, dim3(256), 0, stream, a, p.pieces);            \
+  } while (0)
+  if (D <= 64) CROSS_JOIN(16);
+  else if (D <= 128) CROSS_JOIN(32);
+  else CROSS_JOIN(64);
+#undef CROSS_JOIN
   return launch_status("cross attention join launch");
 }
 

@@ -11,6 +11,10 @@ constexpr bool cross_shape_ok(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int
          D <= 256 && D % 8 == 0 && B * Hkv <= (1 << 20) && Lq * Hq <= (1 << 28) && B * (Lq * Hq) <= (1 << 28);
 }
 
+// States of a batch row that a workgroup lists for itself, in LDS, where there is a
+// mask; longer rows are listed by a kernel of their own.
+constexpr int kCrossOwnList = 2048;
+
 // How a call is cut up.  Rows: the Lq queries of the g heads that share a key/value head.
 struct CrossPlan {
   int64_t rows = 0;       // of a (batch row, key/value head)
@@ -43,8 +47,9 @@ inline CrossPlan cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64
   }
   p.pieces = p.own ? 4 * p.parts : p.parts;
   const int64_t heads = B * Hkv;
-  p.count_off = masked ? cross_up(4 * B * Lk) : 0;
-  p.ml_off = p.count_off + (masked ? cross_up(4 * B) : 0);
+  const bool lists = masked && Lk > kCrossOwnList;
+  p.count_off = lists ? cross_up(4 * B * Lk) : 0;
+  p.ml_off = p.count_off + (lists ? cross_up(4 * B) : 0);
   p.o_off = p.ml_off + (p.pieces > 1 ? cross_up(8 * p.pieces * heads * p.rows) : 0);
   p.total = p.o_off + (p.pieces > 1 ? cross_up(4 * p.pieces * heads * p.rows * D) : 0);
   return p;

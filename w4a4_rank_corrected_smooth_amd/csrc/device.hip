@@ -41,9 +41,6 @@ __device__ __forceinline__ uint4 scale_row_operand(float s) {
   return make_uint4(h1 | (h1 << 16), h1 | (h2 << 16), h2 | (h2 << 16), h3 | (h3 << 16));
 }
 
-// vmcnt(0) through the builtin (expcnt and lgkmcnt left at their maxima), so
-// the compiler's own wait bookkeeping knows every load has landed
-__device__ __forceinline__ void vmcnt_wait0_known() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 // wait until at most n vector-memory operations are outstanding, n a runtime
 // value (clamped to the counter's 6-bit maximum, which only waits longer)
 template <int N>
