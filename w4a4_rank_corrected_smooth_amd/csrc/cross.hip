@@ -95,32 +95,40 @@ struct Rows {
   static __device__ __forceinline__ int v_swap(int row) { return SLOTS == 8 ? (row >> 1 & 1) << 2 : (row & 3) << 2; }
 };
 
-// Numbers the visible ones of n states in order, by WAVES wavefronts, and returns how many: a
-// thread counts a run of neighbouring states and writes it behind the runs before.
+// Numbers the visible ones of n states in order, by WAVES wavefronts, and returns how many.  Eight states
+// a thread at a time, 64 WAVES apart: one trip to memory, and a ballot for each.
 template <int WAVES>
 __device__ __forceinline__ int list_visible(const uint8_t *seen, int n, int *out) {
-  __shared__ int sums[WAVES];
+  __shared__ int sums[8][WAVES];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int run = (n + 64 * WAVES - 1) / (64 * WAVES);
-  const int from = (int)min((int64_t)threadIdx.x * run, (int64_t)n), to = min(from + run, n);
-  int mine = 0;
-  for (int t = from; t < to; ++t) mine += seen[t] != 0;
-  int upto = mine;                                   // of this lane and those before it
+  int all = 0;
+  for (int64_t from = 0; from < n; from += 8 * 64 * WAVES) {
+    uint8_t flag[8];
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) {
-    const int y = __shfl_up(upto, x);
-    if (lane >= x) upto += y;
+    for (int i = 0; i < 8; ++i) {
+      const int64_t t = from + 64 * WAVES * i + threadIdx.x;
+      flag[i] = t < n ? seen[t] : 0;
+    }
+    uint64_t votes[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      votes[i] = __ballot(flag[i] != 0);
+      if (lane == 0) sums[i][w] = __popcll(votes[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      int at = all + __popcll(votes[i] & ((1ull << lane) - 1));
+#pragma unroll
+      for (int v = 0; v < WAVES; ++v) {
+        const int x = sums[i][v];
+        at += v < w ? x : 0;
+        all += x;
+      }
+      if (flag[i] != 0) out[at] = (int)(from + 64 * WAVES * i + threadIdx.x);
+    }
+    __syncthreads();
   }
-  if (lane == 63) sums[w] = upto;
-  __syncthreads();
-  int at = upto - mine, all = 0;
-  for (int i = 0; i < WAVES; ++i) {
-    at += i < w ? sums[i] : 0;
-    all += sums[i];
-  }
-  if (mine)
-    for (int t = from; t < to; ++t)
-      if (seen[t] != 0) out[at++] = t;
   return all;
 }
 
@@ -149,7 +157,6 @@ struct Piece {
     if constexpr (LIST) {
       if (a.mask) {
         n = list_visible<4>(a.mask + (int64_t)b * a.Lk, n, list);
-        __syncthreads();
         index = list;
       } else {
         n = a.count[b];
@@ -188,50 +195,92 @@ template <int DB, int KEYS, int WAVES, bool LIST>
 struct Copier {
   typedef Rows<DB> L;
   static constexpr int COPIES = KEYS / L::COPY_ROWS / WAVES;
+  // With four wavefronts a lane copies the same chunk each time: their rows are a multiple of the swap's period apart.
+  static constexpr bool SAME = WAVES == 4;
   const uint8_t *k, *v;
   const int *index;
-  int64_t k_t, v_t;                      // bytes from a state to the next
+  uint32_t k_t, v_t;                     // bytes from a state to the next, below 2^25
   int n, chunks, lane, w;
-  int key[COPIES];                       // the listed states of the next tile's rows, this lane's
+  uint32_t key[LIST ? COPIES : 1];       // the listed states of the next tile's rows, this lane's
   __device__ __forceinline__ Copier(const CrossArgs &a, const Piece &p, int lane_, int w_)
       : k(reinterpret_cast<const uint8_t *>(a.k + (int64_t)p.b * a.k_b + p.hk * a.k_h)),
-        v(reinterpret_cast<const uint8_t *>(a.v + (int64_t)p.b * a.v_b + p.hk * a.v_h)), index(p.index), k_t(2 * a.k_t),
-        v_t(2 * a.v_t), n(p.n), chunks(a.D / 8), lane(lane_), w(w_) {}
+        v(reinterpret_cast<const uint8_t *>(a.v + (int64_t)p.b * a.v_b + p.hk * a.v_h)), index(p.index), k_t((uint32_t)(2 * a.k_t)),
+        v_t((uint32_t)(2 * a.v_t)), n(p.n), chunks(a.D / 8), lane(lane_), w(w_) {}
   __device__ __forceinline__ int base_of(int j) const { return (WAVES * j + w) * L::COPY_ROWS; }
+  __device__ __forceinline__ int k_chunk(int j) const {
+    return (lane & (L::SLOTS - 1)) ^ L::k_swap(base_of(SAME ? 0 : j) + lane / L::SLOTS);
+  }
+  __device__ __forceinline__ int v_chunk(int j) const {
+    return (lane & (L::SLOTS - 1)) ^ L::v_swap(base_of(SAME ? 0 : j) + lane / L::SLOTS);
+  }
   // Reads tile t's part of the list, a tile ahead of its use.
   __device__ __forceinline__ void look_up(int t) {
     if constexpr (LIST) {
 #pragma unroll
-      for (int j = 0; j < COPIES; ++j) key[j] = index[min(t * KEYS + base_of(j) + lane / L::SLOTS, n - 1)];
+      for (int j = 0; j < COPIES; ++j) key[j] = (uint32_t)index[min(t * KEYS + base_of(j) + lane / L::SLOTS, n - 1)];
     }
   }
-  // Rows behind the last state repeat it.
-  __device__ __forceinline__ void both(int t, uint32_t k_to, uint32_t v_to) const {
-    const int slot = lane & (L::SLOTS - 1);
-    if (!LIST && (t + 1) * KEYS <= n && chunks == 4 * DB) {
+  // The rows of K (or of V): `chunk` of each, that of copy j.
+  template <typename Chunk>
+  __device__ __forceinline__ void half(int t, const uint8_t *rows, uint32_t step, const Chunk &chunk, uint32_t to) const {
+    if (!LIST && (t + 1) * KEYS <= n) {
+      auto copy = [&](int j) __attribute__((always_inline)) {
+        // scalar registers, also where the compiler has lost sight of it
+        const uint64_t first = reinterpret_cast<uint64_t>(rows) + (uint64_t)(uint32_t)(t * KEYS + base_of(j)) * step;
+        const uint64_t at = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(first >> 32)) << 32 |
+                            (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)first);
+        lds_dma16_s(reinterpret_cast<const void *>(at), (uint32_t)(lane / L::SLOTS) * step + 16 * chunk(j),
+                    __builtin_amdgcn_readfirstlane(to + base_of(j) * L::ROW));
+      };
+      if (L::SLOTS == 4 * DB && chunks == 4 * DB) {
 #pragma unroll
-      for (int j = 0; j < COPIES; ++j) {
-        const int base = base_of(j), r = base + lane / L::SLOTS, kc = slot ^ L::k_swap(r), vc = slot ^ L::v_swap(r);
-        const int64_t first = (int64_t)t * KEYS + base;
-        if (L::SLOTS == 4 * DB || kc < 4 * DB)
-          lds_dma16_s(k + first * k_t, (uint32_t)(lane / L::SLOTS) * (uint32_t)k_t + 16 * kc, k_to + base * L::ROW);
-        if (L::SLOTS == 4 * DB || vc < 4 * DB)
-          lds_dma16_s(v + first * v_t, (uint32_t)(lane / L::SLOTS) * (uint32_t)v_t + 16 * vc, v_to + base * L::ROW);
+        for (int j = 0; j < COPIES; ++j) copy(j);
+      } else if constexpr (SAME) {
+        if (chunk(0) < chunks) {
+#pragma unroll
+          for (int j = 0; j < COPIES; ++j) copy(j);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < COPIES; ++j)
+          if (chunk(j) < chunks) copy(j);
       }
       return;
     }
+    auto copy = [&](int j) __attribute__((always_inline)) {   // rows behind the last state repeat it
+      const uint32_t at = LIST ? key[LIST ? j : 0] : (uint32_t)min(t * KEYS + base_of(j) + lane / L::SLOTS, n - 1);
+      lds_dma16(rows + 16 * chunk(j) + (uint64_t)at * step, __builtin_amdgcn_readfirstlane(to + base_of(j) * L::ROW));
+    };
+    if constexpr (SAME) {
+      if (chunk(0) < chunks) {
 #pragma unroll
-    for (int j = 0; j < COPIES; ++j) {
-      const int base = base_of(j), r = base + lane / L::SLOTS, kc = slot ^ L::k_swap(r), vc = slot ^ L::v_swap(r);
-      const int64_t at = LIST ? key[j] : min(t * KEYS + r, n - 1);
-      if (kc < chunks) lds_dma16(k + at * k_t + 16 * kc, k_to + base * L::ROW);
-      if (vc < chunks) lds_dma16(v + at * v_t + 16 * vc, v_to + base * L::ROW);
+        for (int j = 0; j < COPIES; ++j) copy(j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j)
+        if (chunk(j) < chunks) copy(j);
     }
+  }
+  __device__ __forceinline__ void both(int t, uint32_t k_to, uint32_t v_to) const {
+    half(t, k, k_t, [&](int j) __attribute__((always_inline)) { return k_chunk(j); }, k_to);
+    half(t, v, v_t, [&](int j) __attribute__((always_inline)) { return v_chunk(j); }, v_to);
   }
 };
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)p);
+}
+// K's chunks from D to 32 DB channels, which no copy writes, in two tiles of K and V: zeros from the start.  (Queries are zero
+// there, but what LDS holds may be NaN.  V's only reach results that are not stored.)
+template <int DB, int KEYS>
+__device__ __forceinline__ void clear_pads(const CrossArgs &a, uint8_t *tiles, int thread, int threads) {
+  typedef Rows<DB> L;
+  const int chunks = a.D / 8, pads = 4 * DB - chunks;
+  for (int i = thread; i < 2 * KEYS * pads; i += threads) {
+    const int r = i / pads, key = r % KEYS, slot = (chunks + i - r * pads) ^ L::k_swap(key);
+    *reinterpret_cast<uint4 *>(tiles + (r / KEYS) * 2 * KEYS * L::ROW + key * L::ROW + slot * 16) = make_uint4(0, 0, 0, 0);
+  }
 }
 __device__ __forceinline__ v16f zero16() {
   v16f z;
@@ -303,11 +352,18 @@ struct Sums {
         *reinterpret_cast<uint2 *>(mine + m * 64 * DB + ((4 * d + j) ^ (m & 3)) * 16 + 8 * h) =
             make_uint2(pack2<F16>(o[d][4 * j] * inv, o[d][4 * j + 1] * inv), pack2<F16>(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv));
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    constexpr int SLOTS = Rows<DB>::SLOTS;
+    const int c = lane & (SLOTS - 1);
+    if (8 * c >= a.D) return;
 #pragma unroll
-    for (int i = 0; i < 2 * DB; ++i) {
-      const int at = 64 * i + lane, m2 = at / (4 * DB), c = at % (4 * DB), row = row0 + m2;
-      if (row < a.rows && 8 * c < a.D) {
-        const int qi = row / a.group, hq = p.hk * a.group + row - qi * a.group;
+    for (int i = 0; i < 32 * SLOTS / 64; ++i) {
+      const int m2 = 64 / SLOTS * i + lane / SLOTS, row = row0 + m2;
+      if (row < a.rows) {
+        int qi = row, hq = p.hk;
+        if (a.group > 1) {
+          qi = row / a.group;
+          hq = p.hk * a.group + row - qi * a.group;
+        }
         *reinterpret_cast<uint4 *>(a.out + (((int64_t)p.b * a.Lq + qi) * a.Hq + hq) * a.D + 8 * c) =
             *reinterpret_cast<const uint4 *>(mine + m2 * 64 * DB + (c ^ (m2 & 3)) * 16);
       }
@@ -360,13 +416,9 @@ __global__ __launch_bounds__(256, 2) void cross_many_kernel(const CrossArgs a) {
   p.template cut<LIST>(a, KEYS, list);
   const int m = lane & 31, h = lane >> 5;
   const uint32_t lds_at = lds_offset(lds);
-  // chunks past D are never copied: zeros from the start
-  if (a.D < 32 * DB) {
-    for (int i = threadIdx.x * 16; i < (int)sizeof(lds); i += 256 * 16) *reinterpret_cast<uint4 *>(lds + i) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-  }
+  clear_pads<DB, KEYS>(a, lds, threadIdx.x, 256);
   Copier<DB, KEYS, 4, LIST> copy(a, p, lane, w);
-  auto fetch = [&](int t, int buf) { copy.both(t, lds_at + 2 * buf * HALF, lds_at + (2 * buf + 1) * HALF); };
+  auto fetch = [&](int t, int buf) __attribute__((always_inline)) { copy.both(t, lds_at + 2 * buf * HALF, lds_at + (2 * buf + 1) * HALF); };
   const int row0 = p.tile_row * 128 + 32 * w;
   const Row r(a, p, row0 + m);
   v4u q[STEPS];
@@ -449,12 +501,9 @@ __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const Cr
   const int m = lane & 31, h = lane >> 5;
   uint8_t *mine = lds + w * 4 * HALF;
   const uint32_t lds_at = lds_offset(mine);
-  if (a.D < 32 * DB) {
-    for (int i = lane * 16; i < 4 * HALF; i += 64 * 16) *reinterpret_cast<uint4 *>(mine + i) = make_uint4(0, 0, 0, 0);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  }
+  clear_pads<DB, KEYS>(a, mine, lane, 64);
   Copier<DB, KEYS, 1, LIST> copy(a, p, lane, 0);
-  auto fetch = [&](int t, int buf) { copy.both(t, lds_at + 2 * buf * HALF, lds_at + (2 * buf + 1) * HALF); };
+  auto fetch = [&](int t, int buf) __attribute__((always_inline)) { copy.both(t, lds_at + 2 * buf * HALF, lds_at + (2 * buf + 1) * HALF); };
   const int t0 = p.t0 + w;
   const Row r(a, p, m);
   v4u q[STEPS];
