@@ -195,6 +195,51 @@ def test_cross_attention_empty_calls(S):
         assert torch.equal(S.cross_attention(q, k, k, key_lens=torch.tensor([51, 1 << 30], dtype=torch.int32, device="cuda")), q)
 
 
+def gpu_reference(q, k, v, visible, scale):
+    """The same reference as near()'s, in float64 on the GPU, for many rows: out, mean and size."""
+    B, Lq, Hq, D = q.shape
+    g = Hq // k.shape[2]
+    q, k, v = q.double(), k.double(), v.double()
+    out, mean, size = torch.zeros_like(q), torch.zeros_like(q), torch.zeros(B, Lq, Hq, 1, dtype=torch.float64, device="cuda")
+    for b in range(B):
+        at = torch.nonzero(visible[b])[:, 0]
+        for h in range(Hq if len(at) else 0):
+            kk, vv = k[b, at, h // g], v[b, at, h // g]
+            p = torch.softmax(scale * (q[b, :, h] @ kk.t()), -1)
+            out[b, :, h], mean[b, :, h] = p @ vv, p @ vv.abs()
+            size[b, :, h] = abs(scale) * (q[b, :, h].abs() @ kk.abs().t()).amax(-1, keepdim=True)
+    return out, mean, size
+
+
+@pytest.mark.parametrize("hide", ["none", "lens", "mask"])
+@pytest.mark.parametrize("B,Lq,Lk,Hq,Hkv,D", [
+    (1, 4100, 77, 16, 16, 64), (2, 2049, 576, 32, 16, 40), (1, 2200, 577, 32, 32, 64), (3, 5000, 1, 6, 6, 72), (2, 2048, 300, 32, 16, 72),
+    (1, 5500, 384, 12, 12, 96), (1, 2050, 385, 32, 32, 96), (2, 4097, 256, 8, 8, 128), (1, 3000, 64, 24, 24, 104),
+    (1, 2100, 257, 32, 32, 128), (300, 40, 9, 4, 4, 32)])
+def test_cross_attention_many_rows_few_states(S, B, Lq, Lk, Hq, Hkv, D, hide):
+    """The form that keeps a head's states in LDS, at its largest lengths and one past them."""
+    announce(f"cross of many rows B={B} Lq={Lq} Lk={Lk} Hq={Hq} Hkv={Hkv} D={D} {hide}")
+    dtype = torch.float16 if (Lq + Lk) % 2 else torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(Lq + Lk)
+    q = torch.randn(B, Lq, Hq, D, device="cuda", generator=g).to(dtype)
+    kv = torch.randn(B, Lk, 2 * Hkv, D, device="cuda", generator=g).to(dtype)
+    k, v = kv[:, :, :Hkv], kv[:, :, Hkv:]
+    visible = torch.ones(B, Lk, dtype=torch.bool, device="cuda")
+    lens = mask = None
+    if hide == "lens":
+        lens = torch.randint(0, Lk + 1, (B,), device="cuda", generator=g).int()
+        lens[0] = Lk
+        visible = torch.arange(Lk, device="cuda") < lens[:, None]
+    if hide == "mask":
+        mask = visible = torch.rand(B, Lk, device="cuda", generator=g) < 0.7
+    k[~visible], v[~visible] = float("nan"), float("inf")
+    got = S.cross_attention(q, k, v, key_lens=lens, mask=mask)
+    want, mean, size = gpu_reference(q, k, v, visible, D ** -0.5)
+    u = torch.finfo(dtype).eps / 2
+    tol = u * want.abs() + (u + 2 * ((D + 6) * 2.0 ** -23 * size + 2.0 ** -22) + 2 * Lk * 2.0 ** -23) * mean * (1 + 2.0 ** -6) + 2.0 ** -25
+    assert ((got.double() - want).abs() <= tol).all()
+
+
 def test_cross_attention_large(S):
     """Row tiles, heads and states beyond one round of workgroups, against float32 products on the GPU."""
     B, Lq, Lk, H, D = 1, 5000, 3000, 6, 128

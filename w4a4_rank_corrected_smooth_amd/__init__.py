@@ -1033,24 +1033,29 @@ class RotaryPlan:
 _NO_ROWS = (None, 0, 0, 0, None, 0, 0)
 
 
+def _rotary_operand(t, name: str, dev, T: int, D: int, dtype):
+    """Raises unless t is rows that svdq_rotary_apply takes; its heads and strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or strides[2] != 1 or t.dtype != dtype or t.device != dev:
+        if len(shape) != 3 or shape[0] != T or shape[2] != D or t.dtype != dtype or t.device != dev or t.numel():
+            raise ValueError(f"{name} must be [{T}, heads, {D}] {dtype} with adjacent channels on {dev}, "
+                             f"got {tuple(shape)} {t.dtype} with strides {strides} on {t.device}")
+    # torch leaves any stride where there is one element
+    return shape[1], 0 if T == 1 else strides[0], 0 if shape[1] == 1 else strides[1]
+
+
 def _rotary_rows(x, name: str, dev, T: int, D: int, dtype, out):
     """One of the two operands of svdq_rotary_apply, with its output."""
-    for t, n in ((x, name), (out, name + "_out")):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{n} must be a torch.Tensor")
-        if t.dtype != dtype or t.dim() != 3 or t.size(0) != T or t.size(2) != D or t.device != dev or (t.numel() and t.stride(2) != 1):
-            raise ValueError(f"{n} must be [{T}, heads, {D}] {dtype} with adjacent channels on {dev}, "
-                             f"got {tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
-    H = x.size(1)
+    H, row, head = _rotary_operand(x, name, dev, T, D, dtype)
     if out is None:
         out = torch.empty((T, H, D), dtype=dtype, device=dev)
-    elif out.size(1) != H:
-        raise ValueError(f"{name}_out has {out.size(1)} heads, {name} {H}")
-    # torch leaves any stride where there is one element
-    strides = [0 if n == 1 else t.stride(i) for t in (x, out) for i, n in ((0, T), (1, H))]
-    return out, (x.data_ptr(), strides[0], strides[1], H, out.data_ptr(), strides[2], strides[3])
+        return out, (x.data_ptr(), row, head, H, out.data_ptr(), H * D, D)
+    out_heads, out_row, out_head = _rotary_operand(out, name + "_out", dev, T, D, dtype)
+    if out_heads != H:
+        raise ValueError(f"{name}_out has {out_heads} heads, {name} {H}")
+    return out, (x.data_ptr(), row, head, H, out.data_ptr(), out_row, out_head)
 
 
 def rotary_apply(plan: RotaryPlan, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
@@ -1061,22 +1066,24 @@ def rotary_apply(plan: RotaryPlan, q: torch.Tensor, k: Optional[torch.Tensor], p
     given.  q_out=q, k_out=k turns in place.  Negative positions turn backwards."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    dev = q.device
-    _need(q, "q", dev, _DT16, 3)
+    dev, dtype = q.device, q.dtype
+    if dtype not in _DT16 or q.dim() != 3:
+        _need(q, "q", dev, _DT16, 3)
     T, D = q.size(0), plan.head_dim
     _need_int(max(q.shape), "a size of q")
-    _need(positions, "positions", dev, (torch.int32, torch.float32), 2)
-    if positions.size(0) != T or positions.size(1) != plan.axes or not positions.is_contiguous():
-        raise ValueError(f"positions must be contiguous [{T}, {plan.axes}], got {tuple(positions.shape)}")
-    q_out, q_args = _rotary_rows(q, "q", dev, T, D, q.dtype, q_out)
+    floats = isinstance(positions, torch.Tensor) and positions.dtype == torch.float32
+    if not floats:
+        _need(positions, "positions", dev, (torch.int32,), 2)
+    if positions.shape != (T, plan.axes) or positions.device != dev or not positions.is_contiguous():
+        raise ValueError(f"positions must be contiguous [{T}, {plan.axes}] on {dev}, got {tuple(positions.shape)} on {positions.device}")
+    q_out, q_args = _rotary_rows(q, "q", dev, T, D, dtype, q_out)
     k_args = _NO_ROWS
     if k is not None:
-        k_out, k_args = _rotary_rows(k, "k", dev, T, D, q.dtype, k_out)
-        _need_int(k.size(1), "k's heads")
+        k_out, k_args = _rotary_rows(k, "k", dev, T, D, dtype, k_out)
+        _need_int(k_args[3], "k's heads")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _call(dev, _lib.svdq_rotary_apply, plan._ref, *q_args, *k_args, _DT16[q.dtype], positions.data_ptr(),
-          int(positions.dtype == torch.float32), T)
+    _call(dev, _lib.svdq_rotary_apply, plan._ref, *q_args, *k_args, _DT16[dtype], positions.data_ptr(), int(floats), T)
     return q_out, k_out
 
 

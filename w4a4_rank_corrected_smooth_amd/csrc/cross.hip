@@ -2,6 +2,7 @@
 //
 //  cross_list_kernel     the visible states of each batch row, where there is a mask
 //  cross_many_kernel     attention of a tile of rows over a piece of the states
+//  cross_near_kernel     the same over few states, all of them in LDS
 //  cross_few_kernel      the same for a handful of rows
 //  cross_join_kernel     joins the pieces of a row
 //
@@ -84,15 +85,29 @@ __device__ __forceinline__ float half_sum(float x) {
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
-// Rows of K and V in LDS, for DB blocks of 32 channels: rows of SLOTS chunks of 16 bytes.
+// Rows of K and V in LDS, for DB blocks of 32 channels: SLOTS chunks of 16 bytes, permuted
+// so that no read meets a bank twice (64 banks of 4 bytes).  K is read 16 rows at the same chunk,
+// V 4 neighbouring rows at 4 neighbouring chunks.  Where the slots are a power of two, a chunk's slot is the chunk
+// xor a number that goes with the row; 12 slots are turned by a quarter of the row in K (the
+// rows' starts, 48 words apart, take four places in the banks), and stay in V.
 template <int DB>
 struct Rows {
-  static constexpr int SLOTS = DB <= 2 ? 8 : DB <= 4 ? 16 : 32;
-  static constexpr int ROW = SLOTS * 16, COPY_ROWS = 64 / SLOTS;   // bytes of a row, rows of one copy
-  // A chunk's slot is the chunk xor this.  K: 8 or 16 neighbouring rows are read
-  // at the same chunk.  V: 4 neighbouring rows at 4 neighbouring chunks.
-  static __device__ __forceinline__ int k_swap(int row) { return SLOTS == 8 ? row >> 1 & 7 : SLOTS == 16 ? row & 15 : row & 7; }
-  static __device__ __forceinline__ int v_swap(int row) { return SLOTS == 8 ? (row >> 1 & 1) << 2 : (row & 3) << 2; }
+  static constexpr int SLOTS = DB <= 2 ? 8 : DB == 3 ? 12 : DB == 4 ? 16 : 32, ROW = SLOTS * 16;
+  static constexpr bool XOR = SLOTS != 12;
+  static __device__ __forceinline__ int k_swap(int row) {
+    return SLOTS == 8 ? row >> 1 & 7 : SLOTS == 12 ? row >> 2 & 3 : SLOTS == 16 ? row & 15 : row & 7;
+  }
+  static __device__ __forceinline__ int v_swap(int row) { return SLOTS == 8 ? (row >> 1 & 1) << 2 : SLOTS == 12 ? 0 : (row & 3) << 2; }
+  static __device__ __forceinline__ int k_slot(int row, int chunk) {
+    const int s = chunk + k_swap(row);
+    return XOR ? chunk ^ k_swap(row) : s >= 12 ? s - 12 : s;
+  }
+  static __device__ __forceinline__ int k_chunk(int row, int slot) {
+    const int c = slot - k_swap(row);
+    return XOR ? slot ^ k_swap(row) : c < 0 ? c + 12 : c;
+  }
+  static __device__ __forceinline__ int v_slot(int row, int chunk) { return chunk ^ v_swap(row); }
+  static __device__ __forceinline__ int v_chunk(int row, int slot) { return slot ^ v_swap(row); }
 };
 
 // Numbers the visible ones of n states in order, by WAVES wavefronts, and returns how many.  Eight states
@@ -151,12 +166,12 @@ struct Piece {
     hk = bh - b * a.Hkv;
   }
   // The states, listed in `list` if they are not listed yet, and this piece's tiles of `keys` of them.
-  template <bool LIST>
+  template <bool LIST, int WAVES>
   __device__ __forceinline__ void cut(const CrossArgs &a, int keys, int *list) {
     n = a.lens ? min(max(a.lens[b], 0), a.Lk) : a.Lk;
     if constexpr (LIST) {
       if (a.mask) {
-        n = list_visible<4>(a.mask + (int64_t)b * a.Lk, n, list);
+        n = list_visible<WAVES>(a.mask + (int64_t)b * a.Lk, n, list);
         index = list;
       } else {
         n = a.count[b];
@@ -185,18 +200,22 @@ struct Row {
       const int at = 16 * s + 8 * h;
       q[s] = at < a.D ? *reinterpret_cast<const v4u *>(src + at) : v4u{0u, 0u, 0u, 0u};
     }
+  }
+  // the scale's sign
+  template <int STEPS>
+  static __device__ __forceinline__ void flip(const CrossArgs &a, v4u (&q)[STEPS]) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) q[s] ^= a.flip;
   }
 };
 
-// Copies a tile's rows into LDS, K's and V's, COPIES copies of each by one of WAVES wavefronts.
+// Copies a tile's rows into LDS, K's and V's, 64 chunks at a time, by WAVES wavefronts.
 template <int DB, int KEYS, int WAVES, bool LIST>
 struct Copier {
   typedef Rows<DB> L;
-  static constexpr int COPIES = KEYS / L::COPY_ROWS / WAVES;
-  // With four wavefronts a lane copies the same chunk each time: their rows are a multiple of the swap's period apart.
-  static constexpr bool SAME = WAVES == 4;
+  static constexpr int ALL = KEYS * L::SLOTS / 64, COPIES = (ALL + WAVES - 1) / WAVES;
+  // A lane copies the same chunk each time where the wavefronts' rows together are a multiple of the swaps' period.
+  static constexpr bool SAME = L::XOR && WAVES >= 4;
   const uint8_t *k, *v;
   const int *index;
   uint32_t k_t, v_t;                     // bytes from a state to the next, below 2^25
@@ -206,52 +225,38 @@ struct Copier {
       : k(reinterpret_cast<const uint8_t *>(a.k + (int64_t)p.b * a.k_b + p.hk * a.k_h)),
         v(reinterpret_cast<const uint8_t *>(a.v + (int64_t)p.b * a.v_b + p.hk * a.v_h)), index(p.index), k_t((uint32_t)(2 * a.k_t)),
         v_t((uint32_t)(2 * a.v_t)), n(p.n), chunks(a.D / 8), lane(lane_), w(w_) {}
-  __device__ __forceinline__ int base_of(int j) const { return (WAVES * j + w) * L::COPY_ROWS; }
-  __device__ __forceinline__ int k_chunk(int j) const {
-    return (lane & (L::SLOTS - 1)) ^ L::k_swap(base_of(SAME ? 0 : j) + lane / L::SLOTS);
-  }
-  __device__ __forceinline__ int v_chunk(int j) const {
-    return (lane & (L::SLOTS - 1)) ^ L::v_swap(base_of(SAME ? 0 : j) + lane / L::SLOTS);
-  }
+  __device__ __forceinline__ bool mine(int j) const { return ALL % WAVES == 0 || WAVES * j + w < ALL; }
+  __device__ __forceinline__ int row(int j) const { return (64 * (WAVES * j + w) + lane) / L::SLOTS; }
+  __device__ __forceinline__ int slot(int j) const { return (64 * (WAVES * j + w) + lane) % L::SLOTS; }
   // Reads tile t's part of the list, a tile ahead of its use.
   __device__ __forceinline__ void look_up(int t) {
     if constexpr (LIST) {
 #pragma unroll
-      for (int j = 0; j < COPIES; ++j) key[j] = (uint32_t)index[min(t * KEYS + base_of(j) + lane / L::SLOTS, n - 1)];
+      for (int j = 0; j < COPIES; ++j) key[j] = (uint32_t)index[min(t * KEYS + row(j), n - 1)];
     }
   }
   // The rows of K (or of V): `chunk` of each, that of copy j.
   template <typename Chunk>
   __device__ __forceinline__ void half(int t, const uint8_t *rows, uint32_t step, const Chunk &chunk, uint32_t to) const {
-    if (!LIST && (t + 1) * KEYS <= n) {
-      auto copy = [&](int j) __attribute__((always_inline)) {
-        // scalar registers, also where the compiler has lost sight of it
-        const uint64_t first = reinterpret_cast<uint64_t>(rows) + (uint64_t)(uint32_t)(t * KEYS + base_of(j)) * step;
-        const uint64_t at = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(first >> 32)) << 32 |
-                            (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)first);
-        lds_dma16_s(reinterpret_cast<const void *>(at), (uint32_t)(lane / L::SLOTS) * step + 16 * chunk(j),
-                    __builtin_amdgcn_readfirstlane(to + base_of(j) * L::ROW));
-      };
-      if (L::SLOTS == 4 * DB && chunks == 4 * DB) {
-#pragma unroll
-        for (int j = 0; j < COPIES; ++j) copy(j);
-      } else if constexpr (SAME) {
-        if (chunk(0) < chunks) {
-#pragma unroll
-          for (int j = 0; j < COPIES; ++j) copy(j);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < COPIES; ++j)
-          if (chunk(j) < chunks) copy(j);
+    const bool whole = !LIST && (t + 1) * KEYS <= n;
+    auto copy = [&](int j) __attribute__((always_inline)) {
+      const uint32_t at = __builtin_amdgcn_readfirstlane(to + 1024 * (WAVES * j + w));
+      if (whole) {
+        // a scalar base (also where the compiler has lost sight of that) and the lane's 32-bit offset
+        const int skip = L::XOR ? (WAVES * j + w) * (64 / L::SLOTS) : 0;
+        const uint64_t first = reinterpret_cast<uint64_t>(rows) + (uint64_t)(uint32_t)(t * KEYS + skip) * step;
+        const uint64_t base = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(first >> 32)) << 32 |
+                              (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)first);
+        lds_dma16_s(reinterpret_cast<const void *>(base), (uint32_t)(row(j) - skip) * step + 16 * chunk(j), at);
+      } else {                           // rows behind the last state repeat it
+        const uint32_t key_at = LIST ? key[LIST ? j : 0] : (uint32_t)min(t * KEYS + row(j), n - 1);
+        lds_dma16(rows + 16 * chunk(j) + (uint64_t)key_at * step, at);
       }
-      return;
-    }
-    auto copy = [&](int j) __attribute__((always_inline)) {   // rows behind the last state repeat it
-      const uint32_t at = LIST ? key[LIST ? j : 0] : (uint32_t)min(t * KEYS + base_of(j) + lane / L::SLOTS, n - 1);
-      lds_dma16(rows + 16 * chunk(j) + (uint64_t)at * step, __builtin_amdgcn_readfirstlane(to + base_of(j) * L::ROW));
     };
-    if constexpr (SAME) {
+    if (SAME && (whole && L::SLOTS == 4 * DB && chunks == 4 * DB)) {
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j) copy(j);
+    } else if constexpr (SAME) {
       if (chunk(0) < chunks) {
 #pragma unroll
         for (int j = 0; j < COPIES; ++j) copy(j);
@@ -259,28 +264,33 @@ struct Copier {
     } else {
 #pragma unroll
       for (int j = 0; j < COPIES; ++j)
-        if (chunk(j) < chunks) copy(j);
+        if (mine(j) && chunk(j) < chunks) copy(j);
     }
   }
   __device__ __forceinline__ void both(int t, uint32_t k_to, uint32_t v_to) const {
-    half(t, k, k_t, [&](int j) __attribute__((always_inline)) { return k_chunk(j); }, k_to);
-    half(t, v, v_t, [&](int j) __attribute__((always_inline)) { return v_chunk(j); }, v_to);
+    half(t, k, k_t, [&](int j) __attribute__((always_inline)) { return L::k_chunk(row(SAME ? 0 : j), slot(SAME ? 0 : j)); }, k_to);
+    half(t, v, v_t, [&](int j) __attribute__((always_inline)) { return L::v_chunk(row(SAME ? 0 : j), slot(SAME ? 0 : j)); }, v_to);
   }
 };
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)p);
 }
-// K's chunks from D to 32 DB channels, which no copy writes, in two tiles of K and V: zeros from the start.  (Queries are zero
+// K's chunks from D to 32 DB channels, which no copy writes: zeros from the start.  (Queries are zero
 // there, but what LDS holds may be NaN.  V's only reach results that are not stored.)
-template <int DB, int KEYS>
-__device__ __forceinline__ void clear_pads(const CrossArgs &a, uint8_t *tiles, int thread, int threads) {
-  typedef Rows<DB> L;
+template <int DB>
+__device__ __forceinline__ void clear_pads(const CrossArgs &a, uint8_t *rows, int count, int thread, int threads) {
   const int chunks = a.D / 8, pads = 4 * DB - chunks;
-  for (int i = thread; i < 2 * KEYS * pads; i += threads) {
-    const int r = i / pads, key = r % KEYS, slot = (chunks + i - r * pads) ^ L::k_swap(key);
-    *reinterpret_cast<uint4 *>(tiles + (r / KEYS) * 2 * KEYS * L::ROW + key * L::ROW + slot * 16) = make_uint4(0, 0, 0, 0);
+  for (int i = thread; i < count * pads; i += threads) {
+    const int r = i / pads;
+    *reinterpret_cast<uint4 *>(rows + r * Rows<DB>::ROW + Rows<DB>::k_slot(r, chunks + i - r * pads) * 16) = make_uint4(0, 0, 0, 0);
   }
+}
+// V's rows from `from` to `to`, behind the last state: zero, whatever that one holds.
+template <int DB>
+__device__ __forceinline__ void clear_rows(uint8_t *rows, int from, int to, int thread, int threads) {
+  for (int i = from * Rows<DB>::ROW + thread * 16; i < to * Rows<DB>::ROW; i += threads * 16)
+    *reinterpret_cast<uint4 *>(rows + i) = make_uint4(0, 0, 0, 0);
 }
 __device__ __forceinline__ v16f zero16() {
   v16f z;
@@ -288,15 +298,36 @@ __device__ __forceinline__ v16f zero16() {
   for (int i = 0; i < 16; ++i) z[i] = 0.0f;
   return z;
 }
-// Two transposing reads: the operand of 16 states by 32 channels.
+// A lane's part of the operands: K rows m = lane % 32 (chunk 2 i + lane / 32 of step i), and through the
+// transposing read V's rows 4 (lane / 32) + lane % 16 / 4 of a block of 16 states, channels 16 (lane / 16 % 2) + 4 (lane % 4).
 template <int DB>
-__device__ __forceinline__ v4u read_v(const uint8_t *at) {
-  typedef __attribute__((address_space(3))) v4i16 *Read;
-  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Read)(uint8_t *)at);
-  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Read)(uint8_t *)(at + 8 * Rows<DB>::ROW));
-  const uint2 x = __builtin_bit_cast(uint2, lo), y = __builtin_bit_cast(uint2, hi);
-  return v4u{x.x, x.y, y.x, y.y};
-}
+struct Reader {
+  typedef Rows<DB> L;
+  int k_at[L::XOR ? 1 : 2 * DB], k_x, v_at, v_z;
+  __device__ __forceinline__ explicit Reader(int lane) {
+    const int m = lane & 31, h = lane >> 5, v_row = 4 * h + (lane >> 2 & 3);
+    k_x = h ^ L::k_swap(m);
+    if constexpr (L::XOR) {
+      k_at[0] = m * L::ROW;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * DB; ++i) k_at[i] = m * L::ROW + L::k_slot(m, 2 * i + h) * 16;
+    }
+    v_z = L::v_swap(v_row) >> 2;
+    v_at = v_row * L::ROW + (2 * (lane >> 4 & 1) + (lane >> 1 & 1)) * 16 + (lane & 1) * 8;
+  }
+  __device__ __forceinline__ v4u k(const uint8_t *block, int i) const {
+    return *reinterpret_cast<const v4u *>(block + (L::XOR ? k_at[0] + ((k_x ^ (2 * i)) << 4) : k_at[L::XOR ? 0 : i]));
+  }
+  __device__ __forceinline__ v4u v(const uint8_t *block, int d) const {
+    typedef __attribute__((address_space(3))) v4i16 *Read;
+    const uint8_t *at = block + v_at + ((d ^ v_z) << 6);
+    const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Read)(uint8_t *)at);
+    const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Read)(uint8_t *)(at + 8 * L::ROW));
+    const uint2 x = __builtin_bit_cast(uint2, lo), y = __builtin_bit_cast(uint2, hi);
+    return v4u{x.x, x.y, y.x, y.y};
+  }
+};
 
 // A row's running state, and its results: pieces for the join, or the output.
 template <int DB, bool F16>
@@ -339,6 +370,28 @@ struct Sums {
           *reinterpret_cast<v4f *>(a.o + at * a.D + ch) = v4f{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
       }
   }
+  // The output of a lane's row.  The halves exchange pieces of four channels for eight each.
+  __device__ __forceinline__ void store(const CrossArgs &a, const Piece &p, const Row &r, int h) {
+    sum = half_sum(sum);
+    const float inv = p.n > 0 ? 1.0f / sum : 0.0f;
+    uint16_t *dst = a.out + (((int64_t)p.b * a.Lq + r.qi) * a.Hq + r.hq) * a.D;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        uint32_t w[2][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const auto x = __builtin_amdgcn_permlane32_swap(
+              pack2<F16>(o[d][4 * j + 2 * e] * inv, o[d][4 * j + 2 * e + 1] * inv),
+              pack2<F16>(o[d][4 * j + 4 + 2 * e] * inv, o[d][4 * j + 5 + 2 * e] * inv), false, false);
+          w[0][e] = x[0];
+          w[1][e] = x[1];
+        }
+        const int ch = 32 * d + 8 * j + 8 * h;
+        if (r.row < a.rows && ch < a.D) *reinterpret_cast<uint4 *>(dst + ch) = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
+      }
+  }
   // The output of 32 rows from row0 on, through a wavefront's 2048 DB bytes of LDS, so that
   // rows leave 16 bytes a lane.
   __device__ __forceinline__ void finish(const CrossArgs &a, const Piece &p, int row0, int lane, uint8_t *mine) {
@@ -352,7 +405,7 @@ struct Sums {
         *reinterpret_cast<uint2 *>(mine + m * 64 * DB + ((4 * d + j) ^ (m & 3)) * 16 + 8 * h) =
             make_uint2(pack2<F16>(o[d][4 * j] * inv, o[d][4 * j + 1] * inv), pack2<F16>(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv));
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    constexpr int SLOTS = Rows<DB>::SLOTS;
+    constexpr int SLOTS = Rows<DB>::XOR ? Rows<DB>::SLOTS : 16;       // lanes to a row
     const int c = lane & (SLOTS - 1);
     if (8 * c >= a.D) return;
 #pragma unroll
@@ -398,6 +451,37 @@ __device__ __forceinline__ void weigh(const v16f &s, float c, float off, float &
   }
 }
 
+// KB blocks of 32 states, of which `left` are there: scores, weights and sums.
+template <int DB, int KB, bool F16>
+__device__ __forceinline__ void attend(Sums<DB, F16> &acc, const v4u (&q)[2 * DB], const Reader<DB> &read, const uint8_t *k,
+                                       const uint8_t *v, int left, int h, float c) {
+  v16f s[KB];
+#pragma unroll
+  for (int b = 0; b < KB; ++b) s[b] = zero16();
+#pragma unroll
+  for (int i = 0; i < 2 * DB; ++i)
+#pragma unroll
+    for (int b = 0; b < KB; ++b) s[b] = mma<F16>(read.k(k + 32 * b * Rows<DB>::ROW, i), q[i], s[b]);
+  if (left < 32 * KB) {
+#pragma unroll
+    for (int b = 0; b < KB; ++b) hide(s[b], left - 32 * b, h);
+  }
+  float best = largest(s[0]);
+#pragma unroll
+  for (int b = 1; b < KB; ++b) best = fmaxf(best, largest(s[b]));
+  acc.raise(half_max(best) * c);
+  const float off = (F16 ? kShift16 : 0.0f) - acc.top;
+#pragma unroll
+  for (int b = 0; b < KB; ++b) {
+    v4u pw[2];
+    weigh<F16>(s[b], c, off, acc.sum, pw);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) acc.o[d] = mma<F16>(read.v(v + (32 * b + 16 * u) * Rows<DB>::ROW, d), pw[u], acc.o[d]);
+  }
+}
+
 // Many rows: each of the four wavefronts has 32, and all read the same tiles of
 // KEYS states, two in LDS.  While a 16-bit matrix instruction runs, the SIMD's vector ALU stands nearly
 // still (an instruction and 16 FMAs, from two wavefronts: 31 ns, 14 and 16 alone), so the kernel's time is the sum of
@@ -413,10 +497,11 @@ __global__ __launch_bounds__(256, 2) void cross_many_kernel(const CrossArgs a) {
   __shared__ int list[LIST ? kCrossOwnList : 1];
   Piece p(a);
   if (!p.any) return;
-  p.template cut<LIST>(a, KEYS, list);
+  p.template cut<LIST, 4>(a, KEYS, list);
   const int m = lane & 31, h = lane >> 5;
   const uint32_t lds_at = lds_offset(lds);
-  clear_pads<DB, KEYS>(a, lds, threadIdx.x, 256);
+  clear_pads<DB>(a, lds, KEYS, threadIdx.x, 256);
+  clear_pads<DB>(a, lds + 2 * HALF, KEYS, threadIdx.x, 256);
   Copier<DB, KEYS, 4, LIST> copy(a, p, lane, w);
   auto fetch = [&](int t, int buf) __attribute__((always_inline)) { copy.both(t, lds_at + 2 * buf * HALF, lds_at + (2 * buf + 1) * HALF); };
   const int row0 = p.tile_row * 128 + 32 * w;
@@ -428,61 +513,83 @@ __global__ __launch_bounds__(256, 2) void cross_many_kernel(const CrossArgs a) {
     copy.look_up(p.t0 + 1);
   }
   r.load(a, p, h, q);
+  Row::flip(a, q);
 
   Sums<DB, F16> acc;
-  const int k_lane = m * L::ROW, k_x = h ^ L::k_swap(m);
-  // the transposing read: row 4 h + (lane % 16) / 4 of a block of 16 states, channels 16 (lane / 16 % 2) + 4 (lane % 4)
-  const int v_row = 4 * h + (lane >> 2 & 3), v_z = L::v_swap(v_row) >> 2;
-  const int v_lane = HALF + v_row * L::ROW + (2 * (lane >> 4 & 1) + (lane >> 1 & 1)) * 16 + (lane & 1) * 8;
-
+  const Reader<DB> read(lane);
   int buf = 0;
   for (int t = p.t0; t < p.t1; ++t, buf ^= 1) {
     vmcnt_wait0_known();
     __syncthreads();
     const bool last = (t + 1) * KEYS > p.n;
     uint8_t *st = lds + 2 * buf * HALF;
-    if (last) {                            // V rows behind the last state: zero, whatever the last one holds
-      for (int i = (p.n - t * KEYS) * L::ROW + (int)threadIdx.x * 16; i < HALF; i += 256 * 16)
-        *reinterpret_cast<uint4 *>(st + HALF + i) = make_uint4(0, 0, 0, 0);
+    if (last) {
+      clear_rows<DB>(st + HALF, p.n - t * KEYS, KEYS, threadIdx.x, 256);
       __syncthreads();
     }
     if (t + 1 < p.t1) {
       fetch(t + 1, buf ^ 1);
       copy.look_up(t + 2);
     }
-    v16f s[KB];
-#pragma unroll
-    for (int k = 0; k < KB; ++k) s[k] = zero16();
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-      for (int k = 0; k < KB; ++k)
-        s[k] = mma<F16>(*reinterpret_cast<const v4u *>(st + 32 * k * L::ROW + k_lane + ((k_x ^ (2 * i)) << 4)), q[i], s[k]);
-    if (last) {
-#pragma unroll
-      for (int k = 0; k < KB; ++k) hide(s[k], p.n - t * KEYS - 32 * k, h);
-    }
-    float best = largest(s[0]);
-#pragma unroll
-    for (int k = 1; k < KB; ++k) best = fmaxf(best, largest(s[k]));
-    acc.raise(half_max(best) * a.c);
-    const float off = (F16 ? kShift16 : 0.0f) - acc.top;
-#pragma unroll
-    for (int k = 0; k < KB; ++k) {
-      v4u pw[2];
-      weigh<F16>(s[k], a.c, off, acc.sum, pw);
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-          acc.o[d] = mma<F16>(read_v<DB>(st + (32 * k + 16 * u) * L::ROW + v_lane + ((d ^ v_z) << 6)), pw[u], acc.o[d]);
-    }
+    attend<DB, KB, F16>(acc, q, read, st, st + HALF, last ? p.n - t * KEYS : 32 * KB, h, a.c);
   }
   if (a.ml) {
     acc.leave(a, p, r, h, p.part, p.t0 < p.t1);
   } else {
     __syncthreads();
     acc.finish(a, p, row0, lane, lds + w * 2048 * DB);
+  }
+}
+
+// Many rows over few states: a workgroup keeps all of a key/value head's states in LDS (up to CAP), and its
+// eight wavefronts go through rows by 32, each by itself, without barriers.
+template <int DB, int CAP, bool F16, bool LIST>
+__global__ __launch_bounds__(512, 2) void cross_near_kernel(const CrossArgs a) {
+  typedef Rows<DB> L;
+  constexpr int KEYS = 64;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * CAP * L::ROW];
+  __shared__ int list[LIST ? CAP : 1];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = lane & 31, h = lane >> 5;
+  Piece p(a);
+  if (!p.any) return;
+  p.template cut<LIST, 8>(a, KEYS, list);
+  uint8_t *kl = lds, *vl = lds + CAP * L::ROW;
+  const uint32_t k_at = lds_offset(kl), v_at = lds_offset(vl);
+  Copier<DB, KEYS, 8, LIST> copy(a, p, lane, w);
+  for (int t = 0; t < p.t1; ++t) {
+    if constexpr (LIST) {
+#pragma unroll
+      for (int j = 0; j < copy.COPIES; ++j) copy.key[j] = (uint32_t)list[min(t * KEYS + copy.row(j), p.n - 1)];
+    }
+    copy.both(t, k_at + t * KEYS * L::ROW, v_at + t * KEYS * L::ROW);
+  }
+  clear_pads<DB>(a, kl, p.t1 * KEYS, threadIdx.x, 512);
+  // this workgroup's blocks of 32 rows
+  const int blocks = (a.rows + 31) / 32;
+  const int b0 = (int)((int64_t)blocks * p.tile_row / a.tiles), b1 = (int)((int64_t)blocks * (p.tile_row + 1) / a.tiles);
+  Row r(a, p, 32 * (b0 + w) + m);
+  v4u q[2 * DB];
+  r.load(a, p, h, q);
+  Row::flip(a, q);
+  const Reader<DB> read(lane);
+  vmcnt_wait0_known();
+  __syncthreads();
+  if (p.n < p.t1 * KEYS) {
+    clear_rows<DB>(vl, p.n, p.t1 * KEYS, threadIdx.x, 512);
+    __syncthreads();
+  }
+  for (int i = b0 + w; i < b1; i += 8) {
+    // the next rows' queries, asked for before this block's states are gone through
+    const Row next(a, p, 32 * (i + 8) + m);
+    v4u ahead[2 * DB];
+    next.load(a, p, h, ahead);
+    Sums<DB, F16> acc;
+    for (int t = 0; t < p.t1; ++t)
+      attend<DB, 2, F16>(acc, q, read, kl + t * KEYS * L::ROW, vl + t * KEYS * L::ROW, p.n - t * KEYS, h, a.c);
+    acc.store(a, p, r, h);
+    r = next;
+#pragma unroll
+    for (int j = 0; j < 2 * DB; ++j) q[j] = ahead[j] ^ a.flip;
   }
 }
 
@@ -497,11 +604,12 @@ __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const Cr
   __shared__ int list[LIST ? kCrossOwnList : 1];
   Piece p(a);
   if (!p.any) return;
-  p.template cut<LIST>(a, KEYS, list);
+  p.template cut<LIST, 4>(a, KEYS, list);
   const int m = lane & 31, h = lane >> 5;
   uint8_t *mine = lds + w * 4 * HALF;
   const uint32_t lds_at = lds_offset(mine);
-  clear_pads<DB, KEYS>(a, mine, lane, 64);
+  clear_pads<DB>(a, mine, KEYS, lane, 64);
+  clear_pads<DB>(a, mine + 2 * HALF, KEYS, lane, 64);
   Copier<DB, KEYS, 1, LIST> copy(a, p, lane, 0);
   auto fetch = [&](int t, int buf) __attribute__((always_inline)) { copy.both(t, lds_at + 2 * buf * HALF, lds_at + (2 * buf + 1) * HALF); };
   const int t0 = p.t0 + w;
@@ -513,37 +621,23 @@ __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const Cr
     copy.look_up(t0 + 4);
   }
   r.load(a, p, h, q);
+  Row::flip(a, q);
 
   Sums<DB, F16> acc;
-  const int k_lane = m * L::ROW, k_x = h ^ L::k_swap(m);
-  const int v_row = 4 * h + (lane >> 2 & 3), v_z = L::v_swap(v_row) >> 2;
-  const int v_lane = HALF + v_row * L::ROW + (2 * (lane >> 4 & 1) + (lane >> 1 & 1)) * 16 + (lane & 1) * 8;
+  const Reader<DB> read(lane);
   int buf = 0;
   for (int t = t0; t < p.t1; t += 4, buf ^= 1) {
     vmcnt_wait0_known();
     asm volatile("" ::: "memory");
     const bool last = (t + 1) * KEYS > p.n;
     uint8_t *st = mine + 2 * buf * HALF;
-    if (last) {
-      for (int i = (p.n - t * KEYS) * L::ROW + lane * 16; i < HALF; i += 64 * 16)
-        *reinterpret_cast<uint4 *>(st + HALF + i) = make_uint4(0, 0, 0, 0);
-    }
+    if (last) clear_rows<DB>(st + HALF, p.n - t * KEYS, KEYS, lane, 64);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");       // the other buffer has been read
     if (t + 4 < p.t1) {
       fetch(t + 4, buf ^ 1);
       copy.look_up(t + 8);
     }
-    v16f s = zero16();
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) s = mma<F16>(*reinterpret_cast<const v4u *>(st + k_lane + ((k_x ^ (2 * i)) << 4)), q[i], s);
-    if (last) hide(s, p.n - t * KEYS, h);
-    acc.raise(half_max(largest(s)) * a.c);
-    v4u pw[2];
-    weigh<F16>(s, a.c, (F16 ? kShift16 : 0.0f) - acc.top, acc.sum, pw);
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int d = 0; d < DB; ++d) acc.o[d] = mma<F16>(read_v<DB>(st + 16 * u * L::ROW + v_lane + ((d ^ v_z) << 6)), pw[u], acc.o[d]);
+    attend<DB, 1, F16>(acc, q, read, st, st + HALF, last ? p.n - t * KEYS : KEYS, h, a.c);
   }
   acc.leave(a, p, r, h, 4 * p.part + w, t0 < p.t1);
 }
@@ -677,7 +771,11 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
   a.c = fmaxf((float)(fabs((double)scale) * 1.4426950408889634), 1e-37f);
   a.flip = scale < 0.0f ? 0x80008000u : 0u;
   a.work = (int)(B * Hkv * p.tiles * p.parts);        // at most 2^28 / 128 + 2^20
-  a.run = (int)(p.tiles < 32 ? p.tiles : 32);
+  // Row tiles of a head that go to one XCD together: up to 32, as far as no XCD gets a sixteenth more
+  // than its share; the workgroups of the form with the states in LDS, one to a CU, singly (252 of
+  // them in runs of 11, 33 to some XCDs' 32 CUs: 115 us, singly 74).
+  a.run = (int)(p.near ? 1 : p.tiles < 32 ? p.tiles : 32);
+  while (a.run > 1 && 16 * ((a.work + 8 * a.run - 1) / (8 * a.run) * 8ll * a.run) > 17ll * a.work) a.run = (a.run + 1) / 2;
   const dim3 grid((unsigned)((a.work + 8 * a.run - 1) / (8 * a.run) * (8 * a.run)));
 #define CROSS_MANY(DB, KEYS)                                                              \
   do {                                                                                    \
@@ -687,6 +785,17 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
     } else {                                                                              \
       if (list) hipLaunchKernelGGL((cross_many_kernel<DB, KEYS, false, true>), grid, dim3(256), 0, stream, a);  \
       else hipLaunchKernelGGL((cross_many_kernel<DB, KEYS, false, false>), grid, dim3(256), 0, stream, a);      \
+    }                                                                                     \
+  } while (0)
+#define CROSS_NEAR(DB)                                                                    \
+  do {                                                                                    \
+    constexpr int CAP = cross_near_states(DB);                                            \
+    if (dtype == SVDQ_FP16) {                                                             \
+      if (list) hipLaunchKernelGGL((cross_near_kernel<DB, CAP, true, true>), grid, dim3(512), 0, stream, a);   \
+      else hipLaunchKernelGGL((cross_near_kernel<DB, CAP, true, false>), grid, dim3(512), 0, stream, a);       \
+    } else {                                                                              \
+      if (list) hipLaunchKernelGGL((cross_near_kernel<DB, CAP, false, true>), grid, dim3(512), 0, stream, a);  \
+      else hipLaunchKernelGGL((cross_near_kernel<DB, CAP, false, false>), grid, dim3(512), 0, stream, a);      \
     }                                                                                     \
   } while (0)
 #define CROSS_FEW(DB)                                                                     \
@@ -700,13 +809,14 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
     }                                                                                     \
   } while (0)
   switch (p.blocks) {
-    case 2: if (p.own) CROSS_FEW(2); else CROSS_MANY(2, 64); break;
-    case 3: if (p.own) CROSS_FEW(3); else CROSS_MANY(3, 64); break;
-    case 4: if (p.own) CROSS_FEW(4); else CROSS_MANY(4, 64); break;
+    case 2: if (p.own) CROSS_FEW(2); else if (p.near) CROSS_NEAR(2); else CROSS_MANY(2, 64); break;
+    case 3: if (p.own) CROSS_FEW(3); else if (p.near) CROSS_NEAR(3); else CROSS_MANY(3, 64); break;
+    case 4: if (p.own) CROSS_FEW(4); else if (p.near) CROSS_NEAR(4); else CROSS_MANY(4, 64); break;
     case 5: CROSS_MANY(5, 32); break;
     default: CROSS_MANY(8, 32); break;
   }
 #undef CROSS_FEW
+#undef CROSS_NEAR
 #undef CROSS_MANY
   st = launch_status("cross attention launch");
   if (st != SVDQ_OK || p.pieces == 1) return st;

@@ -15,14 +15,18 @@ constexpr bool cross_shape_ok(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int
 // mask; longer rows are listed by a kernel of their own.
 constexpr int kCrossOwnList = 2048;
 
+// States that the form that keeps them all in LDS is built for, by blocks of 32 channels: what fits there, 64 at a
+// time, beside their list.
+constexpr int cross_near_states(int blocks) { return blocks == 2 ? 576 : blocks == 3 ? 384 : blocks == 4 ? 256 : 0; }
+
 // How a call is cut up.  Rows: the Lq queries of the g heads that share a key/value head.
 struct CrossPlan {
   int64_t rows = 0;       // of a (batch row, key/value head)
   int blocks = 0;         // blocks of 32 channels that the kernel is built for
+  bool near = false;      // all states in LDS, many rows
   bool own = false;       // each wavefront has states of its own (few rows), not rows of its own
-  int tile_rows = 0;      // rows of a workgroup
   int tile_keys = 0;      // states that a workgroup (own: a wavefront) takes at a time
-  int64_t tiles = 0;      // row tiles of a (batch row, key/value head)
+  int64_t tiles = 0;      // workgroups that share the rows of a (batch row, key/value head)
   int parts = 1;          // pieces that the states are cut into, over workgroups
   int pieces = 1;         // pieces that the join sees: 4 to a workgroup if `own`
   int64_t index_off = 0, count_off = 0, ml_off = 0, o_off = 0, total = 0;
@@ -35,18 +39,24 @@ inline CrossPlan cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64
   p.rows = Lq * (Hq / Hkv);
   p.blocks = D <= 64 ? 2 : D <= 96 ? 3 : D <= 128 ? 4 : D <= 160 ? 5 : 8;
   p.own = p.rows <= 32 && p.blocks <= 4;    // wider states: four pairs of tiles are more than the LDS
-  p.tile_rows = p.own ? 32 : 128;
   p.tile_keys = p.own || p.blocks > 4 ? 32 : 64;
-  p.tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
-  const int64_t work = B * Hkv * p.tiles;
+  const int64_t heads = B * Hkv, blocks32 = (p.rows + 31) / 32;
+  p.near = !p.own && Lk <= cross_near_states(p.blocks) && heads * blocks32 >= 8 * 256;
+  if (p.near) {
+    // a workgroup to a CU, eight blocks of 32 rows to each at least
+    p.tiles = heads < 256 ? 256 / heads : 1;
+    if (p.tiles > (blocks32 + 7) / 8) p.tiles = (blocks32 + 7) / 8;
+  } else {
+    p.tiles = p.own ? 1 : (p.rows + 127) / 128;
+  }
+  const int64_t work = heads * p.tiles;
   const int64_t key_tiles = (Lk + p.tile_keys - 1) / p.tile_keys;
-  if (work > 0 && work < 512) {
+  if (!p.near && work > 0 && work < 512) {
     const int64_t want = (512 + work - 1) / work, most = p.own ? (key_tiles + 7) / 8 : key_tiles / 4;
     p.parts = (int)(want < most ? want : most);
     if (p.parts < 1) p.parts = 1;
   }
   p.pieces = p.own ? 4 * p.parts : p.parts;
-  const int64_t heads = B * Hkv;
   const bool lists = masked && Lk > kCrossOwnList;
   p.count_off = lists ? cross_up(4 * B * Lk) : 0;
   p.ml_off = p.count_off + (lists ? cross_up(4 * B) : 0);
