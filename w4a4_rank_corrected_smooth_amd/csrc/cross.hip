@@ -594,12 +594,13 @@ __global__ __launch_bounds__(512, 2) void cross_near_kernel(const CrossArgs a) {
 }
 
 // Few rows (up to 32 of a key/value head): the four wavefronts take tiles of 32 states of
-// their own, in LDS of their own, without barriers.  Bound by memory.
+// their own, in LDS of their own, without barriers, two tiles in flight, and add up at the end.  Bound by memory.
 template <int DB, bool F16, bool LIST>
 __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const CrossArgs a) {
   typedef Rows<DB> L;
-  constexpr int KEYS = 32, STEPS = 2 * DB, HALF = KEYS * L::ROW;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * 4 * HALF];
+  constexpr int KEYS = 32, STEPS = 2 * DB, HALF = KEYS * L::ROW, PITCH = 32 * DB + 4;     // floats of a row of sums
+  constexpr int TILES = 4 * 4 * HALF, SUMS = 4 * 32 * (PITCH + 2) * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[TILES > SUMS ? TILES : SUMS];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   __shared__ int list[LIST ? kCrossOwnList : 1];
   Piece p(a);
@@ -615,31 +616,90 @@ __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const Cr
   const int t0 = p.t0 + w;
   const Row r(a, p, m);
   v4u q[STEPS];
+  r.load(a, p, h, q);
   if (t0 < p.t1) {
     copy.look_up(t0);
     fetch(t0, 0);
-    copy.look_up(t0 + 4);
   }
-  r.load(a, p, h, q);
+  if (t0 + 4 < p.t1) {
+    copy.look_up(t0 + 4);
+    fetch(t0 + 4, 1);
+    copy.look_up(t0 + 8);
+  }
   Row::flip(a, q);
 
   Sums<DB, F16> acc;
   const Reader<DB> read(lane);
   int buf = 0;
   for (int t = t0; t < p.t1; t += 4, buf ^= 1) {
-    vmcnt_wait0_known();
-    asm volatile("" ::: "memory");
+    // this tile has landed when only the next one's copies are outstanding (a list's reads are among those)
+    if (!LIST && t + 4 < p.t1) vmcnt_wait<2 * Copier<DB, KEYS, 1, LIST>::COPIES>();
+    else vmcnt_wait0();
     const bool last = (t + 1) * KEYS > p.n;
     uint8_t *st = mine + 2 * buf * HALF;
     if (last) clear_rows<DB>(st + HALF, p.n - t * KEYS, KEYS, lane, 64);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");       // the other buffer has been read
-    if (t + 4 < p.t1) {
-      fetch(t + 4, buf ^ 1);
-      copy.look_up(t + 8);
-    }
     attend<DB, 1, F16>(acc, q, read, st, st + HALF, last ? p.n - t * KEYS : KEYS, h, a.c);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");       // the tile has been read
+    if (t + 8 < p.t1) {
+      fetch(t + 8, buf);
+      copy.look_up(t + 12);
+    }
   }
-  acc.leave(a, p, r, h, 4 * p.part + w, t0 < p.t1);
+  // The wavefronts' sums, [wavefront][row][channel], with their maxima and sums behind.
+  acc.sum = half_sum(acc.sum);
+  __syncthreads();
+  float *so = reinterpret_cast<float *>(lds), *sm = so + 4 * 32 * PITCH, *sl = sm + 4 * 32;
+  if (m < a.rows) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<v4f *>(so + (32 * w + m) * PITCH + 32 * d + 8 * j + 4 * h) =
+            v4f{acc.o[d][4 * j], acc.o[d][4 * j + 1], acc.o[d][4 * j + 2], acc.o[d][4 * j + 3]};
+    sm[32 * w + m] = acc.top;
+    sl[32 * w + m] = t0 < p.t1 ? acc.sum : -1.0f;            // -1: no states
+  }
+  __syncthreads();
+  const int row = threadIdx.x >> 3, part = threadIdx.x & 7;   // eight threads to a row
+  if (row >= a.rows) return;
+  float top = kLowest, sum = 0.0f, f[4];
+  bool some = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool in = sl[32 * i + row] != -1.0f;
+    some = some || in;
+    if (in) top = fmaxf(top, sm[32 * i + row]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool in = sl[32 * i + row] != -1.0f;
+    f[i] = in ? __builtin_amdgcn_exp2f(sm[32 * i + row] - top) : 0.0f;
+    sum = in ? __builtin_fmaf(f[i], sl[32 * i + row], sum) : sum;
+  }
+  const Row at_row(a, p, row);
+  const int64_t at = ((int64_t)p.part * a.B * a.Hkv + p.bh) * a.rows + row;
+  uint16_t *dst = a.out + (((int64_t)p.b * a.Lq + at_row.qi) * a.Hq + at_row.hq) * a.D;
+  const float inv = some ? 1.0f / sum : 0.0f;
+  if (a.ml && part == 0) {
+    a.ml[2 * at] = top;
+    a.ml[2 * at + 1] = some ? sum : -1.0f;
+  }
+#pragma unroll
+  for (int c = 4 * part; c < 32 * DB; c += 32) {
+    if (c >= a.D) break;
+    v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const v4f x = *reinterpret_cast<const v4f *>(so + (32 * i + row) * PITCH + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(f[i], x[e], y[e]);
+    }
+    if (a.ml) {
+      *reinterpret_cast<v4f *>(a.o + at * a.D + c) = y;
+    } else {
+      *reinterpret_cast<uint2 *>(dst + c) = make_uint2(pack2<F16>(y[0] * inv, y[1] * inv), pack2<F16>(y[2] * inv, y[3] * inv));
+    }
+  }
 }
 
 // A wavefront joins a row's pieces: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
@@ -750,7 +810,7 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
   a.out = static_cast<uint16_t *>(out);
   a.B = B; a.Lq = Lq; a.Lk = Lk; a.Hq = Hq; a.Hkv = Hkv; a.group = Hq / Hkv; a.D = D;
   a.rows = (int)p.rows; a.tiles = (int)p.tiles; a.parts = p.parts;
-  if (p.pieces > 1) {
+  if (p.parts > 1) {
     a.ml = reinterpret_cast<float *>(ws + p.ml_off);
     a.o = reinterpret_cast<float *>(ws + p.o_off);
   }
@@ -819,12 +879,12 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
 #undef CROSS_NEAR
 #undef CROSS_MANY
   st = launch_status("cross attention launch");
-  if (st != SVDQ_OK || p.pieces == 1) return st;
+  if (st != SVDQ_OK || p.parts == 1) return st;
   const dim3 joins((unsigned)(((int64_t)B * Hkv * p.rows + 3) / 4));
 #define CROSS_JOIN(LANES)                                                                                            \
   do {                                                                                                               \
-    if (dtype == SVDQ_FP16) hipLaunchKernelGGL((cross_join_kernel<LANES, true>), joins, dim3(256), 0, stream, a, p.pieces); \
-    else hipLaunchKernelGGL((cross_join_kernel<LANES, false>), joins, dim3(256), 0, stream, a, p.pieces);            \
+    if (dtype == SVDQ_FP16) hipLaunchKernelGGL((cross_join_kernel<LANES, true>), joins, dim3(256), 0, stream, a, p.parts); \
+    else hipLaunchKernelGGL((cross_join_kernel<LANES, false>), joins, dim3(256), 0, stream, a, p.parts);            \
   } while (0)
   if (D <= 64) CROSS_JOIN(16);
   else if (D <= 128) CROSS_JOIN(32);

@@ -28,7 +28,6 @@ struct CrossPlan {
   int tile_keys = 0;      // states that a workgroup (own: a wavefront) takes at a time
   int64_t tiles = 0;      // workgroups that share the rows of a (batch row, key/value head)
   int parts = 1;          // pieces that the states are cut into, over workgroups
-  int pieces = 1;         // pieces that the join sees: 4 to a workgroup if `own`
   int64_t index_off = 0, count_off = 0, ml_off = 0, o_off = 0, total = 0;
 };
 
@@ -51,17 +50,19 @@ inline CrossPlan cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64
   }
   const int64_t work = heads * p.tiles;
   const int64_t key_tiles = (Lk + p.tile_keys - 1) / p.tile_keys;
-  if (!p.near && work > 0 && work < 512) {
-    const int64_t want = (512 + work - 1) / work, most = p.own ? (key_tiles + 7) / 8 : key_tiles / 4;
+  // The states in parts where there is less work than places for workgroups (one to a CU where
+  // the form for few rows needs most of the LDS, two elsewhere): as many as fit in one round.
+  const int64_t places = p.own && p.blocks > 2 ? 256 : 512;
+  if (!p.near && work > 0 && work < places) {
+    const int64_t want = places / work, most = p.own ? (key_tiles + 3) / 4 : key_tiles / 4;
     p.parts = (int)(want < most ? want : most);
     if (p.parts < 1) p.parts = 1;
   }
-  p.pieces = p.own ? 4 * p.parts : p.parts;
   const bool lists = masked && Lk > kCrossOwnList;
   p.count_off = lists ? cross_up(4 * B * Lk) : 0;
   p.ml_off = p.count_off + (lists ? cross_up(4 * B) : 0);
-  p.o_off = p.ml_off + (p.pieces > 1 ? cross_up(8 * p.pieces * heads * p.rows) : 0);
-  p.total = p.o_off + (p.pieces > 1 ? cross_up(4 * p.pieces * heads * p.rows * D) : 0);
+  p.o_off = p.ml_off + (p.parts > 1 ? cross_up(8 * p.parts * heads * p.rows) : 0);
+  p.total = p.o_off + (p.parts > 1 ? cross_up(4 * p.parts * heads * p.rows * D) : 0);
   return p;
 }
 
