@@ -211,6 +211,32 @@ def gpu_reference(q, k, v, visible, scale):
     return out, mean, size
 
 
+@pytest.mark.parametrize("B,Lq,Lk,Hq,Hkv,D", [(6, 64, 3001, 4, 1, 128), (7, 3, 5000, 2, 2, 64), (64, 1, 900, 2, 1, 96), (65, 1, 900, 2, 1, 64),
+                                              (2, 200, 2500, 1, 1, 256), (20, 2, 1100, 3, 3, 128)])
+@pytest.mark.parametrize("kind", ["spread", "one", "none", "equal"])
+def test_cross_attention_ragged_lengths(S, B, Lq, Lk, Hq, Hkv, D, kind):
+    """Parts shared out by length: very different lengths, all states in one batch row, none anywhere, all alike."""
+    announce(f"cross of ragged lengths B={B} Lq={Lq} Lk={Lk} Hq={Hq} Hkv={Hkv} D={D} {kind}")
+    r = np.random.default_rng(B * Lk)
+    lens = {"spread": np.exp(r.uniform(0, np.log(Lk), B)).astype(int), "one": np.zeros(B, int), "none": np.zeros(B, int),
+            "equal": np.full(B, Lk)}[kind]
+    if kind == "spread":
+        lens[0], lens[-1] = Lk, 0
+    if kind == "one":
+        lens[B // 2] = Lk
+    g = torch.Generator(device="cuda").manual_seed(B)
+    q = torch.randn(B, Lq, Hq, D, device="cuda", generator=g).half()
+    k, v = (torch.randn(B, Lk, Hkv, D, device="cuda", generator=g).half() for _ in range(2))
+    n = torch.from_numpy(lens.astype(np.int32)).cuda()
+    visible = torch.arange(Lk, device="cuda") < n[:, None]
+    k[~visible], v[~visible] = float("nan"), float("inf")
+    got = S.cross_attention(q, k, v, key_lens=n)
+    want, mean, size = gpu_reference(q, k, v, visible, D ** -0.5)
+    u = 2.0 ** -11
+    tol = u * want.abs() + (u + 2 * ((D + 6) * 2.0 ** -23 * size + 2.0 ** -22) + 2 * Lk * 2.0 ** -23) * mean * (1 + 2.0 ** -6) + 2.0 ** -25
+    assert ((got.double() - want).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("hide", ["none", "lens", "mask"])
 @pytest.mark.parametrize("B,Lq,Lk,Hq,Hkv,D", [
     (1, 4100, 77, 16, 16, 64), (2, 2049, 576, 32, 16, 40), (1, 2200, 577, 32, 32, 64), (3, 5000, 1, 6, 6, 72), (2, 2048, 300, 32, 16, 72),

@@ -51,9 +51,10 @@ struct CrossArgs {
   const uint8_t *mask;                   // which of them are visible: the workgroup lists them itself; or
   const int *index, *count;              // [B, Lk] the visible ones' numbers, and how many
   uint16_t *out;
-  float *ml, *o;                         // pieces: [piece][B Hkv][row] (m, l), and [..][D]
+  float *ml, *o;                         // pieces: [place][row] (m, l), and [..][D]
   int B, Lq, Lk, Hq, Hkv, group, D, rows, tiles, parts;
   int run, work;                         // pieces of work; how many go to one XCD together
+  int line, least;                       // parts of all batch rows together, shared out by their lengths (0: `parts` each); tiles of one
   float c;
   uint32_t flip;
 };
@@ -147,27 +148,71 @@ __device__ __forceinline__ int list_visible(const uint8_t *seen, int n, int *out
   return all;
 }
 
+// The parts of a line that each of up to 64 batch rows gets, by its tiles of `keys` states: its share, rounded
+// down, and one at least, together no more than line + B.  A lane holds a batch row's.
+struct Shares {
+  int n, tiles, parts, before;           // states, tiles, parts, parts of the batch rows before
+  __device__ __forceinline__ Shares(const CrossArgs &a, int keys) {
+    const int lane = threadIdx.x & 63;
+    n = lane < a.B ? min(max(a.lens[lane], 0), a.Lk) : 0;
+    tiles = (n + keys - 1) / keys;
+    int64_t all = tiles;
+#pragma unroll
+    for (int i = 32; i > 0; i >>= 1) all += __shfl_xor((long long)all, i);
+    parts = tiles > 0 ? max(1, min((int)((int64_t)tiles * a.line / all), tiles / a.least)) : 0;
+    before = parts;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) {
+      const int x = __shfl_up(before, i);
+      if (lane >= i) before += x;
+    }
+    before -= parts;
+  }
+};
+
 // A workgroup's piece of the work, the same in all its lanes, and its batch row's states.
 struct Piece {
-  int tile_row, part, bh, b, hk, n, t0, t1;
+  int tile_row, part, b, hk, n, t0, t1;
+  int place;                             // of its sums for the join
   const int *index;                      // where there is a mask
   bool any;
   // Workgroups are dealt out to the eight XCDs in turn: runs of neighbouring row tiles,
   // which read the same states, go to one XCD.
-  __device__ __forceinline__ explicit Piece(const CrossArgs &a) {
+  __device__ __forceinline__ Piece(const CrossArgs &a, int keys) {
     const uint32_t x = blockIdx.x & 7, i = blockIdx.x >> 3, run = (uint32_t)a.run;
     const uint32_t id = (i / run * 8 + x) * run + i % run;
     any = id < (uint32_t)a.work;
+    if (!any) return;
     const uint32_t piece = id / (uint32_t)a.tiles;
     tile_row = (int)(id - piece * (uint32_t)a.tiles);
-    bh = (int)(piece / (uint32_t)a.parts);
+    if (a.line) {
+      const uint32_t at = piece / (uint32_t)a.Hkv;
+      hk = (int)(piece - at * (uint32_t)a.Hkv);
+      place = (int)piece;
+      const Shares s(a, keys);
+      const uint64_t mine = __ballot(s.before <= (int)at && (int)at < s.before + s.parts);
+      any = mine != 0;
+      if (!any) return;
+      b = __builtin_amdgcn_readfirstlane(__ffsll((long long)mine) - 1);
+      n = __builtin_amdgcn_readlane(s.n, b);
+      part = (int)at - __builtin_amdgcn_readlane(s.before, b);
+      span(__builtin_amdgcn_readlane(s.tiles, b), __builtin_amdgcn_readlane(s.parts, b));
+      return;
+    }
+    const int bh = (int)(piece / (uint32_t)a.parts);
     part = (int)piece - bh * a.parts;
     b = (int)((uint32_t)bh / (uint32_t)a.Hkv);
     hk = bh - b * a.Hkv;
+    place = part * a.B * a.Hkv + bh;
+  }
+  __device__ __forceinline__ void span(int all, int parts) {
+    t0 = parts == 1 ? 0 : (int)((uint64_t)(uint32_t)all * (uint32_t)part / (uint32_t)parts);
+    t1 = parts == 1 ? all : (int)((uint64_t)(uint32_t)all * (uint32_t)(part + 1) / (uint32_t)parts);
   }
   // The states, listed in `list` if they are not listed yet, and this piece's tiles of `keys` of them.
   template <bool LIST, int WAVES>
   __device__ __forceinline__ void cut(const CrossArgs &a, int keys, int *list) {
+    if (a.line) return;                  // by its share already
     n = a.lens ? min(max(a.lens[b], 0), a.Lk) : a.Lk;
     if constexpr (LIST) {
       if (a.mask) {
@@ -178,9 +223,7 @@ struct Piece {
         index = a.index + (int64_t)b * a.Lk;
       }
     }
-    const uint32_t all = (uint32_t)(n + keys - 1) / (uint32_t)keys;
-    t0 = a.parts == 1 ? 0 : (int)((uint64_t)all * part / (uint32_t)a.parts);
-    t1 = a.parts == 1 ? (int)all : (int)((uint64_t)all * (part + 1) / (uint32_t)a.parts);
+    span((int)((uint32_t)(n + keys - 1) / (uint32_t)keys), a.parts);
   }
 };
 
@@ -352,10 +395,10 @@ struct Sums {
     }
   }
   // a piece for the join
-  __device__ __forceinline__ void leave(const CrossArgs &a, const Piece &p, const Row &r, int h, int piece, bool some) {
+  __device__ __forceinline__ void leave(const CrossArgs &a, const Piece &p, const Row &r, int h, bool some) {
     sum = half_sum(sum);
     if (r.row >= a.rows) return;
-    const int64_t at = ((int64_t)piece * a.B * a.Hkv + p.bh) * a.rows + r.row;
+    const int64_t at = (int64_t)p.place * a.rows + r.row;
     if (h == 0) {
       a.ml[2 * at] = top;
       a.ml[2 * at + 1] = some ? sum : -1.0f;           // -1: a piece without states
@@ -495,7 +538,7 @@ __global__ __launch_bounds__(256, 2) void cross_many_kernel(const CrossArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * HALF];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   __shared__ int list[LIST ? kCrossOwnList : 1];
-  Piece p(a);
+  Piece p(a, KEYS);
   if (!p.any) return;
   p.template cut<LIST, 4>(a, KEYS, list);
   const int m = lane & 31, h = lane >> 5;
@@ -534,7 +577,7 @@ __global__ __launch_bounds__(256, 2) void cross_many_kernel(const CrossArgs a) {
     attend<DB, KB, F16>(acc, q, read, st, st + HALF, last ? p.n - t * KEYS : 32 * KB, h, a.c);
   }
   if (a.ml) {
-    acc.leave(a, p, r, h, p.part, p.t0 < p.t1);
+    acc.leave(a, p, r, h, p.t0 < p.t1);
   } else {
     __syncthreads();
     acc.finish(a, p, row0, lane, lds + w * 2048 * DB);
@@ -550,7 +593,7 @@ __global__ __launch_bounds__(512, 2) void cross_near_kernel(const CrossArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * CAP * L::ROW];
   __shared__ int list[LIST ? CAP : 1];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = lane & 31, h = lane >> 5;
-  Piece p(a);
+  Piece p(a, KEYS);
   if (!p.any) return;
   p.template cut<LIST, 8>(a, KEYS, list);
   uint8_t *kl = lds, *vl = lds + CAP * L::ROW;
@@ -603,7 +646,7 @@ __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const Cr
   __shared__ __attribute__((aligned(1024))) uint8_t lds[TILES > SUMS ? TILES : SUMS];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   __shared__ int list[LIST ? kCrossOwnList : 1];
-  Piece p(a);
+  Piece p(a, KEYS);
   if (!p.any) return;
   p.template cut<LIST, 4>(a, KEYS, list);
   const int m = lane & 31, h = lane >> 5;
@@ -677,7 +720,7 @@ __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const Cr
     sum = in ? __builtin_fmaf(f[i], sl[32 * i + row], sum) : sum;
   }
   const Row at_row(a, p, row);
-  const int64_t at = ((int64_t)p.part * a.B * a.Hkv + p.bh) * a.rows + row;
+  const int64_t at = (int64_t)p.place * a.rows + row;
   uint16_t *dst = a.out + (((int64_t)p.b * a.Lq + at_row.qi) * a.Hq + at_row.hq) * a.D;
   const float inv = some ? 1.0f / sum : 0.0f;
   if (a.ml && part == 0) {
@@ -706,10 +749,20 @@ __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const Cr
 // LANES lanes hold a row's channels, four each; 64 / LANES pieces are read at a time, and four of
 // those in flight.
 template <int LANES, bool F16>
-__global__ __launch_bounds__(256) void cross_join_kernel(const CrossArgs a, int pieces) {
+__global__ __launch_bounds__(256) void cross_join_kernel(const CrossArgs a, int keys) {
   const int lane = threadIdx.x & 63;
-  const int64_t all = (int64_t)a.B * a.Hkv * a.rows, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= all) return;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (id >= (int64_t)a.B * a.Hkv * a.rows) return;
+  // the row, and where its first piece is; the others follow `all` rows apart
+  const int bh = (int)(id / a.rows), row = (int)(id - (int64_t)bh * a.rows), b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  int pieces = a.parts;
+  int64_t at = id, all = (int64_t)a.B * a.Hkv * a.rows;
+  if (a.line) {
+    const Shares s(a, keys);
+    pieces = __shfl(s.parts, b);
+    at = ((int64_t)__shfl(s.before, b) * a.Hkv + hk) * a.rows + row;
+    all = (int64_t)a.Hkv * a.rows;
+  }
   constexpr int GROUPS = 64 / LANES;
   const int g = lane / LANES, ch = 4 * (lane % LANES);
   const float2 *ml = reinterpret_cast<const float2 *>(a.ml);
@@ -755,9 +808,7 @@ __global__ __launch_bounds__(256) void cross_join_kernel(const CrossArgs a, int 
     for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], i);
   if (g != 0 || ch >= a.D) return;
   const float inv = some ? 1.0f / sum : 0.0f;
-  const int64_t bh = at / a.rows;
-  const int row = (int)(at - bh * a.rows), qi = row / a.group, b = (int)(bh / a.Hkv);
-  const int hq = (int)(bh - (int64_t)b * a.Hkv) * a.group + row - qi * a.group;
+  const int qi = row / a.group, hq = hk * a.group + row - qi * a.group;
   *reinterpret_cast<uint2 *>(a.out + (((int64_t)b * a.Lq + qi) * a.Hq + hq) * a.D + ch) =
       make_uint2(pack2<F16>(o[0] * inv, o[1] * inv), pack2<F16>(o[2] * inv, o[3] * inv));
 }
@@ -810,7 +861,10 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
   a.out = static_cast<uint16_t *>(out);
   a.B = B; a.Lq = Lq; a.Lk = Lk; a.Hq = Hq; a.Hkv = Hkv; a.group = Hq / Hkv; a.D = D;
   a.rows = (int)p.rows; a.tiles = (int)p.tiles; a.parts = p.parts;
-  if (p.parts > 1) {
+  // lengths that differ: the parts are shared out on the device, by length
+  a.line = key_lens && !mask ? p.line : 0;
+  a.least = p.least;
+  if (p.parts > 1 || a.line) {
     a.ml = reinterpret_cast<float *>(ws + p.ml_off);
     a.o = reinterpret_cast<float *>(ws + p.o_off);
   }
@@ -830,7 +884,7 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
   // a scale of zero becomes one that still hides the rows behind the last state.
   a.c = fmaxf((float)(fabs((double)scale) * 1.4426950408889634), 1e-37f);
   a.flip = scale < 0.0f ? 0x80008000u : 0u;
-  a.work = (int)(B * Hkv * p.tiles * p.parts);        // at most 2^28 / 128 + 2^20
+  a.work = (int)(Hkv * p.tiles * (a.line ? a.line + B : B * (int64_t)p.parts));      // at most 2^28 / 128 + 2^20
   // Row tiles of a head that go to one XCD together: up to 32, as far as no XCD gets a sixteenth more
   // than its share; the workgroups of the form with the states in LDS, one to a CU, singly (252 of
   // them in runs of 11, 33 to some XCDs' 32 CUs: 115 us, singly 74).
@@ -879,12 +933,12 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
 #undef CROSS_NEAR
 #undef CROSS_MANY
   st = launch_status("cross attention launch");
-  if (st != SVDQ_OK || p.parts == 1) return st;
+  if (st != SVDQ_OK || !a.ml) return st;
   const dim3 joins((unsigned)(((int64_t)B * Hkv * p.rows + 3) / 4));
 #define CROSS_JOIN(LANES)                                                                                            \
   do {                                                                                                               \
-    if (dtype == SVDQ_FP16) hipLaunchKernelGGL((cross_join_kernel<LANES, true>), joins, dim3(256), 0, stream, a, p.parts); \
-    else hipLaunchKernelGGL((cross_join_kernel<LANES, false>), joins, dim3(256), 0, stream, a, p.parts);            \
+    if (dtype == SVDQ_FP16) hipLaunchKernelGGL((cross_join_kernel<LANES, true>), joins, dim3(256), 0, stream, a, p.tile_keys); \
+    else hipLaunchKernelGGL((cross_join_kernel<LANES, false>), joins, dim3(256), 0, stream, a, p.tile_keys);            \
   } while (0)
   if (D <= 64) CROSS_JOIN(16);
   else if (D <= 128) CROSS_JOIN(32);

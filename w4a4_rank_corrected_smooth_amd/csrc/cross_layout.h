@@ -25,9 +25,11 @@ struct CrossPlan {
   int blocks = 0;         // blocks of 32 channels that the kernel is built for
   bool near = false;      // all states in LDS, many rows
   bool own = false;       // each wavefront has states of its own (few rows), not rows of its own
+  int least = 1;          // tiles of a part, for that the parts' sums are not most of the work
   int tile_keys = 0;      // states that a workgroup (own: a wavefront) takes at a time
   int64_t tiles = 0;      // workgroups that share the rows of a (batch row, key/value head)
-  int parts = 1;          // pieces that the states are cut into, over workgroups
+  int parts = 1;          // pieces that the states are cut into, over workgroups; or, where the lengths differ,
+  int line = 0;           // pieces of all batch rows, shared out by their lengths (0: `parts` each)
   int64_t index_off = 0, count_off = 0, ml_off = 0, o_off = 0, total = 0;
 };
 
@@ -39,6 +41,7 @@ inline CrossPlan cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64
   p.blocks = D <= 64 ? 2 : D <= 96 ? 3 : D <= 128 ? 4 : D <= 160 ? 5 : 8;
   p.own = p.rows <= 32 && p.blocks <= 4;    // wider states: four pairs of tiles are more than the LDS
   p.tile_keys = p.own || p.blocks > 4 ? 32 : 64;
+  p.least = p.own ? 4 : 6;
   const int64_t heads = B * Hkv, blocks32 = (p.rows + 31) / 32;
   p.near = !p.own && Lk <= cross_near_states(p.blocks) && heads * blocks32 >= 8 * 256;
   if (p.near) {
@@ -51,18 +54,24 @@ inline CrossPlan cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64
   const int64_t work = heads * p.tiles;
   const int64_t key_tiles = (Lk + p.tile_keys - 1) / p.tile_keys;
   // The states in parts where there is less work than places for workgroups (one to a CU where
-  // the form for few rows needs most of the LDS, two elsewhere): as many as fit in one round.
+  // the form for few rows needs most of the LDS, two elsewhere): as many as fit in one round, of `least` tiles
+  // (many rows: 256 over 1500 states, 16 heads of 64, with 4, 6, 8 and 12 take 14.7, 15.3, 17.1 and 19.4 us, 512 over 4096, 8
+  // heads of 64, 22.9, 21.4, 19.2 and 21.8; 256 rows over 15804 states of 6 batch rows 33.4, 32.5, 32.3 and 41.8).
   const int64_t places = p.own && p.blocks > 2 ? 256 : 512;
   if (!p.near && work > 0 && work < places) {
-    const int64_t want = places / work, most = p.own ? (key_tiles + 3) / 4 : key_tiles / 4;
+    const int64_t want = places / work, most = key_tiles / p.least;
     p.parts = (int)(want < most ? want : most);
     if (p.parts < 1) p.parts = 1;
+    // up to 64 batch rows, with two pieces each on average
+    const int64_t line = places / (Hkv * p.tiles);
+    if (B > 1 && B <= 64 && most > 1 && line >= 2 * B) p.line = (int)(line < B * most ? line : B * most);
   }
   const bool lists = masked && Lk > kCrossOwnList;
   p.count_off = lists ? cross_up(4 * B * Lk) : 0;
+  const int64_t even = p.parts > 1 ? p.parts * heads : 0, shared = p.line ? (p.line + B) * Hkv : 0, pieces = even > shared ? even : shared;
   p.ml_off = p.count_off + (lists ? cross_up(4 * B) : 0);
-  p.o_off = p.ml_off + (p.parts > 1 ? cross_up(8 * p.parts * heads * p.rows) : 0);
-  p.total = p.o_off + (p.parts > 1 ? cross_up(4 * p.parts * heads * p.rows * D) : 0);
+  p.o_off = p.ml_off + (pieces > 0 ? cross_up(8 * pieces * p.rows) : 0);
+  p.total = p.o_off + (pieces > 0 ? cross_up(4 * pieces * p.rows * D) : 0);
   return p;
 }
 
