@@ -59,7 +59,7 @@ def near(got, want, size, K, gelu=False):
 
 
 CASES = [  # M, N, K
-    (1, 1, 8), (1, 64, 128), (1, 300, 1000), (2, 1152, 4608), (5, 33, 136), (8, 96, 4096), (9, 40, 4096), (31, 65, 2056),
+    (1, 1, 8), (1, 64, 128), (1, 4100, 520), (11, 4200, 264), (1, 300, 1000), (2, 1152, 4608), (5, 33, 136), (8, 96, 3000), (7, 96, 4096), (9, 40, 4096), (16, 50, 1536), (16, 50, 1544), (17, 70, 1024), (31, 65, 2056), (80, 70, 1000), (96, 40, 520),
     (32, 64, 1024), (33, 64, 256), (64, 200, 520), (65, 130, 384), (77, 2121, 1160), (100, 31, 8), (128, 128, 128),
     (129, 257, 264), (200, 1000, 640), (513, 384, 2048),
 ]

@@ -3,7 +3,8 @@
 //  fp8_pack_kernel       canonical codes and scales -> operand blocks
 //  fp8_quantize_kernel   16-bit rows -> operand blocks, or canonical codes
 //  fp8_tile_kernel       the product, a tile of rows by channels to a workgroup
-//  fp8_rows_kernel       the product for few rows: one stream of the weights
+//  fp8_rows_kernel       the product for up to 96 rows: one stream of the weights
+//  fp8_few_kernel        the same for up to 16 rows
 //
 // A block of 128 channels is two 32x32x64 block-scaled matrix instructions
 // (e4m3, operands in fp8_layout.h's order), with the rows' power-of-two scales as the
@@ -367,17 +368,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args
   }
 }
 
+// All rows, quantised into LDS by a workgroup of kFp8RowsWaves wavefronts: unit u of block kb of row m at ((8 kb + u)
+// M + m) 16, its scale at kb M + m.  (Row, block) pairs, eight lanes to each.
+constexpr int kFp8RowsWaves = 8, kFp8Ahead = 4;
+template <bool F16>
+__device__ __forceinline__ void quantize_rows(const Fp8Args &a, uint8_t *xl, uint8_t *xs) {
+  for (int i = threadIdx.x >> 3; i < a.M * a.blocks_k; i += 8 * kFp8RowsWaves) {
+    const int kb = i / a.M, m = i - kb * a.M, u = threadIdx.x & 7;
+    v4u codes;
+    const uint32_t s = quantize16<F16>(a.rows + m * a.rows_stride, 128 * kb + 16 * u, a.K, codes);
+    *reinterpret_cast<v4u *>(xl + ((kb * 8 + u) * a.M + m) * 16) = codes;
+    if (u == 0) xs[i] = (uint8_t)s;
+  }
+}
+
 // Few rows.  A workgroup has 32 output channels; its eight wavefronts deal out
 // the blocks of K among themselves and add up in LDS.  Weights go from memory
 // straight into operands, AHEAD blocks of a wavefront in flight.  OWN: the
-// workgroup quantises the rows itself, into LDS (one block of 32 rows, up to 32768 channels in all).
-constexpr int kFp8RowsWaves = 8, kFp8Ahead = 4;
+// workgroup quantises the rows itself, into LDS (one block of 32 rows, up to 24576 values in all).
 template <int XB, bool OWN, bool F16, int OUT>
 __global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_rows_kernel(const Fp8Args a) {
   constexpr int RED = kFp8RowsWaves * XB * 16 * 65 * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[RED];
-  __shared__ __attribute__((aligned(16))) uint8_t xl[OWN ? 32768 : 16];
-  __shared__ uint8_t xs[OWN ? 256 : 1];
+  __shared__ __attribute__((aligned(16))) uint8_t xl[OWN ? 24576 : 16];
+  __shared__ uint8_t xs[OWN ? 192 : 1];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 31;
   const int nb = blockIdx.x;
   const uint8_t *wp = a.w + (int64_t)nb * a.blocks_k * kFp8Block, *wsp = a.ws + (int64_t)nb * a.blocks_k * kFp8WScales;
@@ -395,14 +409,7 @@ __global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_rows_kernel(const Fp8A
   for (int i = 0; i < kFp8Ahead; ++i) load(i, w + kFp8RowsWaves * i);
 
   if constexpr (OWN) {
-    // (row, block) pairs, eight lanes to each
-    for (int i = threadIdx.x >> 3; i < a.M * a.blocks_k; i += 8 * kFp8RowsWaves) {
-      const int kb = i / a.M, m = i - kb * a.M, u = threadIdx.x & 7;
-      v4u codes;
-      const uint32_t s = quantize16<F16>(a.rows + m * a.rows_stride, 128 * kb + 16 * u, a.K, codes);
-      *reinterpret_cast<v4u *>(xl + ((kb * 8 + u) * a.M + m) * 16) = codes;
-      if (u == 0) xs[i] = (uint8_t)s;
-    }
+    quantize_rows<F16>(a, xl, xs);
     __syncthreads();
   }
 
@@ -463,14 +470,97 @@ __global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_rows_kernel(const Fp8A
   }
 }
 
+// Up to 16 rows.  As above, with 16 output channels to a workgroup, so that few channels make more
+// workgroups, and more of a wavefront's part of K in flight.  The instruction takes a whole block of 128: lane l holds units 2
+// (l / 16) and 2 (l / 16) + 1 of channel (of row) l % 16, and its results are of row l % 16, channels 4 (l / 16) + [0, 4).
+constexpr int kFp8FewAhead = 8;
+template <bool OWN, bool F16, int OUT>
+__global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_few_kernel(const Fp8Args a) {
+  __shared__ float red[kFp8RowsWaves][4][65];
+  __shared__ __attribute__((aligned(16))) uint8_t xl[OWN ? 24576 : 16];
+  __shared__ uint8_t xs[OWN ? 192 : 1];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int64_t first = (int64_t)(blockIdx.x >> 1) * a.blocks_k;
+  const uint8_t *wp = a.w + first * kFp8Block + (blockIdx.x & 1) * 256 + g * 1024 + 16 * r, *wsp = a.ws + first * kFp8WScales;
+
+  v4u wf[kFp8FewAhead][2];
+  uint2 sw[kFp8FewAhead];
+  auto load = [&](int slot, int kb) {
+    kb = min(kb, a.blocks_k - 1);
+    const uint8_t *b = wp + (int64_t)kb * kFp8Block;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) wf[slot][q] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(b + 512 * q));
+    sw[slot] = *reinterpret_cast<const uint2 *>(wsp + (int64_t)kb * kFp8WScales);
+  };
+#pragma unroll
+  for (int i = 0; i < kFp8FewAhead; ++i) load(i, w + kFp8RowsWaves * i);
+  if constexpr (OWN) {
+    quantize_rows<F16>(a, xl, xs);
+    __syncthreads();
+  }
+
+  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  const bool in = r < a.M;
+  const int rr = in ? r : 0;
+  for (int base = w; base < a.blocks_k; base += kFp8RowsWaves * kFp8FewAhead) {
+#pragma unroll
+    for (int i = 0; i < kFp8FewAhead; ++i) {
+      const int kb = base + kFp8RowsWaves * i;
+      if (kb >= a.blocks_k) break;
+      v4u xf[2];
+      int sx;
+      if constexpr (OWN) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          xf[q] = *reinterpret_cast<const v4u *>(xl + ((kb * 8 + 2 * g + q) * a.M + rr) * 16);
+          if (!in) xf[q] = v4u{0u, 0u, 0u, 0u};
+        }
+        sx = xs[kb * a.M + rr];
+      } else {
+        const uint8_t *b = a.x + (int64_t)kb * kFp8Block + g * 1024 + 16 * r;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) xf[q] = *reinterpret_cast<const v4u *>(b + 512 * q);
+        sx = a.xs[(int64_t)kb * kFp8XScales + r];
+      }
+      const v8i wa = {(int)wf[i][0][0], (int)wf[i][0][1], (int)wf[i][0][2], (int)wf[i][0][3],
+                      (int)wf[i][1][0], (int)wf[i][1][1], (int)wf[i][1][2], (int)wf[i][1][3]};
+      const v8i xb = {(int)xf[0][0], (int)xf[0][1], (int)xf[0][2], (int)xf[0][3],
+                      (int)xf[1][0], (int)xf[1][1], (int)xf[1][2], (int)xf[1][3]};
+      const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, xb, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, (int)sw[i].y, 0, sx);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(p[e], __uint_as_float(sw[i].x), acc[e]);
+      if (kb + kFp8RowsWaves * kFp8FewAhead < a.blocks_k) load(i, kb + kFp8RowsWaves * kFp8FewAhead);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) red[w][e][lane] = acc[e];
+  __syncthreads();
+  const int c = threadIdx.x & 15, m = threadIdx.x >> 4, n = 16 * blockIdx.x + c;
+  if (m >= a.M || n >= a.N) return;
+  float y = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kFp8RowsWaves; ++v) y += red[v][c & 3][16 * (c >> 2) + m];
+  if (a.bias) y += a.bias[n];
+  if (a.gelu) y = gelu_tanh_f32(y);
+  a.out[(int64_t)m * a.N + n] = narrow<OUT>(y);
+}
+
 template <int OUT>
 void launch_product(const Fp8Plan &p, Fp8Args &a, bool f16, hipStream_t stream) {
+  if (p.form == FP8_FEW) {
+    const dim3 grid((unsigned)(2 * a.n_blocks)), block(64 * kFp8RowsWaves);
+    if (p.inline_x && f16) hipLaunchKernelGGL((fp8_few_kernel<true, true, OUT>), grid, block, 0, stream, a);
+    else if (p.inline_x) hipLaunchKernelGGL((fp8_few_kernel<true, false, OUT>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((fp8_few_kernel<false, false, OUT>), grid, block, 0, stream, a);
+    return;
+  }
   if (p.form == FP8_ROWS) {
     const dim3 grid((unsigned)a.n_blocks), block(64 * kFp8RowsWaves);
     if (p.inline_x && f16) hipLaunchKernelGGL((fp8_rows_kernel<1, true, true, OUT>), grid, block, 0, stream, a);
     else if (p.inline_x) hipLaunchKernelGGL((fp8_rows_kernel<1, true, false, OUT>), grid, block, 0, stream, a);
     else if (p.x_blocks == 1) hipLaunchKernelGGL((fp8_rows_kernel<1, false, false, OUT>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((fp8_rows_kernel<2, false, false, OUT>), grid, block, 0, stream, a);
+    else if (p.x_blocks == 2) hipLaunchKernelGGL((fp8_rows_kernel<2, false, false, OUT>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((fp8_rows_kernel<3, false, false, OUT>), grid, block, 0, stream, a);
     return;
   }
   const int side = p.form == FP8_256 ? 256 : p.form == FP8_128 ? 128 : 64;

@@ -30,10 +30,10 @@ constexpr int64_t fp8_w_bytes(int64_t N, int64_t K) { return fp8_blocks(N, K) * 
 constexpr int64_t fp8_x_bytes(int64_t M, int64_t K) { return fp8_up(fp8_blocks(M, K) * (kFp8Block + kFp8XScales), 256); }
 
 // Which kernel multiplies, and how its work is cut.
-enum Fp8Form { FP8_ROWS = 0, FP8_64 = 1, FP8_128 = 2, FP8_256 = 3 };
+enum Fp8Form { FP8_ROWS = 0, FP8_FEW = 4, FP8_64 = 1, FP8_128 = 2, FP8_256 = 3 };
 struct Fp8Plan {
   Fp8Form form = FP8_ROWS;
-  bool inline_x = false;       // FP8_ROWS: each workgroup quantises the rows for itself
+  bool inline_x = false;       // FP8_FEW, FP8_ROWS: each workgroup quantises the rows for itself
   int x_blocks = 1;            // FP8_ROWS: blocks of 32 rows
   int parts = 1;               // pieces of K
   int64_t part_off = 0, total = 0;
@@ -43,14 +43,20 @@ inline Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
   Fp8Plan p;
   const int64_t kb = (K + 127) / 128;
   if (M <= 32) {
-    p.inline_x = M * kb * 128 <= 32768;
-  } else if (M <= 64) {
-    p.x_blocks = 2;
+    // up to 24576 values each workgroup quantises the rows itself (rows of 4096, both ways: 1: 7.1 and 9.5 us, 4: 9.4
+    // and 10.0, 6: 9.8 and 10.1, 8: 10.6 and 10.3)
+    p.inline_x = M * kb * 128 <= 24576;
+    // 16 channels to a workgroup where that makes no more than one round of them (one row of 4096 x 14336: 15.3 us, by 32
+    // channels 17.5; of 1152 x 4608: 6.0 and 6.6; of 6144 x 4096: 9.1 and 7.1)
+    if (M <= 16 && N <= 4096) p.form = FP8_FEW;
+  } else if (M <= 64 || (M <= 96 && N <= 8192)) {
+    // a round of workgroups of 32 channels (96 x 6144 x 4096 14.6 us, in 64 x 64 tiles 16.2; at 128 rows 16.4 and 16.0, at
+    // 128 x 16384 x 4096 30 and 25)
+    p.x_blocks = (int)((M + 31) / 32);
   } else {
     const int64_t t128 = (M + 127) / 128 * ((N + 127) / 128), t256 = (M + 255) / 256 * ((N + 255) / 256);
     p.form = t256 >= 512 ? FP8_256 : t128 >= 192 ? FP8_128 : FP8_64;
   }
-  (void)kb;
   p.part_off = p.inline_x ? 0 : fp8_x_bytes(M, K);
   p.total = p.part_off + (p.parts > 1 ? fp8_up(4 * (int64_t)p.parts * M * N, 256) : 0);
   return p;
