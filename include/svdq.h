@@ -487,8 +487,8 @@ typedef struct {
 /* out [M, N] (bf16 or fp16, dense) for x [M, K] of bf16 or fp16, row m at x +
  * m x_row elements (16-byte aligned, x_row a multiple of 8, not negative).
  * epilogue: SVDQ_EPILOGUE_NONE or SVDQ_EPILOGUE_GELU_TANH, in float32 before
- * the result is rounded once.  M <= 2^22, M N and M K <= 2^34.  One kernel for few rows, or two or three:
- * the quantiser, the product, and the sum of its parts where K is cut up.  The result does not depend on the
+ * the result is rounded once.  M <= 2^22, M N and M K <= 2^34.  One kernel for few rows, or two:
+ * the quantiser and the product.  The result does not depend on the
  * order in which workgroups run.  The workspace needs no clearing and keeps nothing from one
  * call for the next (calls that run at the same time need one each). */
 size_t svdq_fp8_workspace_bytes(int M, int N, int K);

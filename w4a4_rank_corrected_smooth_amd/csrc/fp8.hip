@@ -29,10 +29,9 @@ struct Fp8Args {
   const uint8_t *ws, *xs;        // their scales
   const float *bias;
   uint16_t *out;
-  float *part;                   // pieces [part][M][N], or NULL
   int M, N, blocks_k;
   int m_blocks, n_blocks;        // of 32
-  int tiles_m, tiles_n, parts;
+  int tiles_m, tiles_n;
   int gelu;
   // FP8_ROWS with its own quantiser
   const uint16_t *rows;
@@ -566,8 +565,9 @@ void launch_product(const Fp8Plan &p, Fp8Args &a, bool f16, hipStream_t stream) 
   const int side = p.form == FP8_256 ? 256 : p.form == FP8_128 ? 128 : 64;
   a.tiles_m = (a.M + side - 1) / side;
   a.tiles_n = (a.N + side - 1) / side;
-  const dim3 grid((unsigned)((a.tiles_m * a.tiles_n * a.parts + 7) / 8 * 8));
+  const dim3 grid((unsigned)((a.tiles_m * a.tiles_n + 7) / 8 * 8));
   if (p.form == FP8_256) hipLaunchKernelGGL((fp8_tile_kernel<4, 2, 2, 4, 2, OUT>), grid, dim3(512), 0, stream, a);
+  else if (p.form == FP8_128 && p.deep) hipLaunchKernelGGL((fp8_tile_kernel<2, 1, 2, 4, 4, OUT>), grid, dim3(512), 0, stream, a);
   else if (p.form == FP8_128) hipLaunchKernelGGL((fp8_tile_kernel<2, 2, 2, 2, 2, OUT>), grid, dim3(256), 0, stream, a);
   else hipLaunchKernelGGL((fp8_tile_kernel<1, 1, 2, 2, 4, OUT>), grid, dim3(256), 0, stream, a);
 }
@@ -670,7 +670,6 @@ svdq_status_t svdq_fp8_linear_forward(const svdq_fp8_weights_t *w, const void *x
   a.blocks_k = (w->K + 127) / 128;
   a.m_blocks = (M + 31) / 32;
   a.n_blocks = (w->N + 31) / 32;
-  a.parts = p.parts;
   a.gelu = epilogue == SVDQ_EPILOGUE_GELU_TANH;
   a.rows = static_cast<const uint16_t *>(x);
   a.rows_stride = x_row;
