@@ -230,6 +230,23 @@ def test_fp8_linear_large(S):
         assert ((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + (7 * 2.0 ** -13 + (K / 8 + K / 128 + 2) * 2.0 ** -23) * size).all()
 
 
+@pytest.mark.parametrize("M,N", [(2100, 1000), (2900, 1500), (4500, 2700), (1500, 300)])
+@pytest.mark.parametrize("K", [8, 128, 136, 384, 504, 640])
+def test_fp8_linear_every_tile_form_short_k(S, M, N, K):
+    """Tiles of 128 x 128 with four stages and with two, of 256 x 256 and of 64 x 64, over fewer blocks of K than
+    stages and a few more: small integers, as above, so that the result is the exact one rounded once."""
+    announce(f"fp8 linear of small integers M={M} N={N} K={K}")
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    xi, wi = (torch.randint(-3, 4, (n, K), device="cuda", generator=g).double() for n in (M, N))
+    scales = torch.randint(1, 5, (-(-N // 128), -(-K // 128)), device="cuda", generator=g).float() / 8
+    bias = torch.randint(-20, 21, (N,), device="cuda", generator=g).float() / 8
+    layer = S.Fp8Linear(wi.float().to(torch.float8_e4m3fn), scales, bias)
+    w = wi * scales.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    want = xi @ w.t() + bias.double()
+    for dtype in (torch.float16, torch.bfloat16):
+        assert torch.equal(S.fp8_linear_forward(layer, xi.to(dtype)), want.to(dtype))
+
+
 @pytest.mark.parametrize("M", [8, 60, 400])
 def test_fp8_linear_error_on_average(S, M):
     r = np.random.default_rng(12)
