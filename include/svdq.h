@@ -488,7 +488,7 @@ typedef struct {
  * m x_row elements (16-byte aligned, x_row a multiple of 8, not negative).
  * epilogue: SVDQ_EPILOGUE_NONE or SVDQ_EPILOGUE_GELU_TANH, in float32 before
  * the result is rounded once.  M <= 2^22, M N and M K <= 2^34.  One kernel for few rows, or two:
- * the quantiser and the product.  The result does not depend on the
+ * the quantiser and the product.  out does not overlap x.  The result does not depend on the
  * order in which workgroups run.  The workspace needs no clearing and keeps nothing from one
  * call for the next (calls that run at the same time need one each). */
 size_t svdq_fp8_workspace_bytes(int M, int N, int K);
@@ -562,9 +562,9 @@ svdq_status_t svdq_rotary_apply(const svdq_rotary_t *plan, const void *q, int64_
  * product in the inputs' type (p is 1 at the largest score to within a factor of
  * 2^8, so float16's lower end is 2^-31 below it), and out is rounded once.
  * The result does not depend on the order in which workgroups run.  One kernel, another
- * that lists the visible states where there is a mask, and one that joins the
- * pieces where few queries meet many states.  The workspace (`masked`: for
- * calls with a mask) needs no clearing and keeps nothing
+ * that lists the visible states where there is a mask over more than 2048, and one that joins the
+ * pieces where few queries meet many states.  out may be q where q is dense; it overlaps nothing
+ * else.  The workspace (`masked`: for calls with a mask) needs no clearing and keeps nothing
  * from one call for the next (calls that run at the same time need one each). */
 size_t svdq_cross_attention_workspace_bytes(int B, int Lq, int Lk, int Hq, int Hkv, int D, int masked);
 svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_token, int64_t q_head, const void *k,

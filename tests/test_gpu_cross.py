@@ -280,6 +280,20 @@ def test_cross_attention_large(S):
         assert ((got[0, :, h].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -9) * mean).all()
 
 
+@pytest.mark.parametrize("B,Lq,Lk,Hq,Hkv,D", [
+    (2, 3, 40, 4, 2, 64), (2, 3, 1500, 4, 2, 128), (1, 200, 70, 4, 1, 96), (1, 200, 3000, 2, 2, 128), (1, 150, 500, 4, 2, 160),
+    (1, 4100, 300, 16, 16, 72)])
+@pytest.mark.parametrize("mask", [False, True])
+def test_cross_attention_over_its_queries(S, B, Lq, Lk, Hq, Hkv, D, mask):
+    """The output in the queries' place, in every form."""
+    g = torch.Generator(device="cuda").manual_seed(Lk)
+    q, k, v = (torch.randn(B, *s, D, device="cuda", generator=g).bfloat16() for s in ((Lq, Hq), (Lk, Hkv), (Lk, Hkv)))
+    m = torch.rand(B, Lk, device="cuda", generator=g) < 0.5 if mask else None
+    want = S.cross_attention(q, k, v, mask=m)
+    announce(f"cross in place B={B} Lq={Lq} Lk={Lk} Hq={Hq} Hkv={Hkv} D={D}")
+    assert torch.equal(S.cross_attention(q, k, v, mask=m, out=q), want) and torch.equal(q, want)
+
+
 def test_cross_attention_streams_graphs_and_two_at_once(S):
     """Two captured calls with workspaces of their own, replayed against eager results over changing inputs."""
     r = np.random.default_rng(6)

@@ -266,6 +266,18 @@ def test_fp8_linear_error_on_average(S, M):
     assert np.sqrt((off ** 2).mean()) <= 1.1 * np.sqrt((cut ** 2 + rounding ** 2).mean())
 
 
+def test_fp8_linear_of_a_slice_of_rows(S):
+    """Codes that start in the middle of a larger matrix, at an address that is no multiple of 16."""
+    r = np.random.default_rng(9)
+    codes, _ = weight(r, 200, 136)
+    scales = np.ones((1, 2), np.float32)
+    whole = torch.from_numpy(codes).cuda()
+    x = rows(r, 5, 136, "bf16")
+    announce("fp8 linear of a slice of rows")
+    got = S.fp8_linear_forward(S.Fp8Linear(whole[3:103], torch.from_numpy(scales).cuda()), x)
+    assert torch.equal(got, S.fp8_linear_forward(S.Fp8Linear(codes[3:103], scales), x))
+
+
 def test_fp8_linear_streams_and_graphs(S):
     """Two layers on two streams at once, and captured with workspaces of their own."""
     r = np.random.default_rng(6)

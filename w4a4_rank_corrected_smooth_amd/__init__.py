@@ -931,6 +931,8 @@ class Fp8Linear:
             if self.bias.shape != (N,):
                 raise ValueError(f"bias must be [{N}], got {tuple(self.bias.shape)}")
         codes, scales = codes.view(torch.uint8).to(dev).contiguous(), scales.to(dev).contiguous()
+        if codes.data_ptr() % 16:            # rows of a larger matrix
+            codes = codes.clone()
         self.blob = torch.empty(n, dtype=torch.uint8, device=dev)
         _call(dev, _lib.svdq_fp8_pack_on_device, codes.data_ptr(), scales.data_ptr(), N, K, self.blob.data_ptr(), n)
         self._w = Fp8Weights(self.blob.data_ptr(), None if self.bias is None else self.bias.data_ptr(), N, K)
@@ -1107,7 +1109,7 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_lens:
     length (bf16 or fp16; any strides that are multiples of 8, channels adjacent; Hq a multiple
     of Hkv).  Batch row b sees the states before key_lens[b] (int32 [B]) whose mask[b, t]
     (bool [B, Lk]) is true; what the others hold is not looked at, and a row that sees none gives
-    zeros.  Returns [B, Lq, Hq, D].  scale: 1 / sqrt(D) if not given."""
+    zeros.  Returns [B, Lq, Hq, D], in `out` if given, which may be a dense q.  scale: 1 / sqrt(D) if not given."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     dev = q.device
