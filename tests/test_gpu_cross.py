@@ -280,6 +280,31 @@ def test_cross_attention_large(S):
         assert ((got[0, :, h].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -9) * mean).all()
 
 
+@pytest.mark.parametrize("hide", ["none", "lens", "mask"])
+@pytest.mark.parametrize("B,Lq,Lk,Hq,Hkv,D", [
+    (8, 1, 1500, 20, 20, 64), (16, 1, 448, 16, 16, 64), (43, 2, 2048, 6, 3, 40), (130, 7, 250, 4, 1, 64), (17, 32, 33, 8, 8, 8),
+    (64, 4, 256, 12, 3, 56), (16, 3, 2049, 16, 16, 64), (150, 1, 1, 1, 1, 64)])
+def test_cross_attention_few_rows_of_many_heads(S, B, Lq, Lk, Hq, Hkv, D, hide):
+    """The form with a workgroup of eight wavefronts to a head, at its limits: 129 to 256 heads, 2048 states."""
+    announce(f"cross of many heads B={B} Lq={Lq} Lk={Lk} Hq={Hq} Hkv={Hkv} D={D} {hide}")
+    dtype = torch.float16 if (B + Lk) % 2 else torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(B + Lk)
+    q = torch.randn(B, Lq, Hq, D, device="cuda", generator=g).to(dtype)
+    kv = torch.randn(B, Lk, 2 * Hkv, D, device="cuda", generator=g).to(dtype)
+    k, v = kv[:, :, :Hkv], kv[:, :, Hkv:]
+    visible = torch.ones(B, Lk, dtype=torch.bool, device="cuda")
+    lens = mask = None
+    if hide == "lens":
+        lens = torch.randint(0, Lk + 1, (B,), device="cuda", generator=g).int()
+        lens[1] = 0
+        visible = torch.arange(Lk, device="cuda") < lens[:, None]
+    if hide == "mask":
+        mask = visible = torch.rand(B, Lk, device="cuda", generator=g) < 0.7
+        mask[1] = False
+    k[~visible], v[~visible] = float("nan"), float("inf")
+    near(S.cross_attention(q, k, v, key_lens=lens, mask=mask), q, k, v, visible.cpu().numpy())
+
+
 @pytest.mark.parametrize("B,Lq,Lk,Hq,Hkv,D", [
     (2, 3, 40, 4, 2, 64), (2, 3, 1500, 4, 2, 128), (1, 200, 70, 4, 1, 96), (1, 200, 3000, 2, 2, 128), (1, 150, 500, 4, 2, 160),
     (1, 4100, 300, 16, 16, 72)])

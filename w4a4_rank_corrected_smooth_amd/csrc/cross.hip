@@ -636,19 +636,19 @@ __global__ __launch_bounds__(512, 2) void cross_near_kernel(const CrossArgs a) {
   }
 }
 
-// Few rows (up to 32 of a key/value head): the four wavefronts take tiles of 32 states of
+// Few rows (up to 32 of a key/value head): the wavefronts (four or eight) take tiles of 32 states of
 // their own, in LDS of their own, without barriers, two tiles in flight, and add up at the end.  Bound by memory.
-template <int DB, bool F16, bool LIST>
-__global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const CrossArgs a) {
+template <int DB, int W, bool F16, bool LIST>
+__global__ __launch_bounds__(64 * W, DB > 2 ? 1 : 2) void cross_few_kernel(const CrossArgs a) {
   typedef Rows<DB> L;
   constexpr int KEYS = 32, STEPS = 2 * DB, HALF = KEYS * L::ROW, PITCH = 32 * DB + 4;     // floats of a row of sums
-  constexpr int TILES = 4 * 4 * HALF, SUMS = 4 * 32 * (PITCH + 2) * 4;
+  constexpr int TILES = W * 4 * HALF, SUMS = W * 32 * (PITCH + 2) * 4, SHARE = 2 * W;     // threads to a row
   __shared__ __attribute__((aligned(1024))) uint8_t lds[TILES > SUMS ? TILES : SUMS];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   __shared__ int list[LIST ? kCrossOwnList : 1];
   Piece p(a, KEYS);
   if (!p.any) return;
-  p.template cut<LIST, 4>(a, KEYS, list);
+  p.template cut<LIST, W>(a, KEYS, list);
   const int m = lane & 31, h = lane >> 5;
   uint8_t *mine = lds + w * 4 * HALF;
   const uint32_t lds_at = lds_offset(mine);
@@ -664,34 +664,34 @@ __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const Cr
     copy.look_up(t0);
     fetch(t0, 0);
   }
-  if (t0 + 4 < p.t1) {
-    copy.look_up(t0 + 4);
-    fetch(t0 + 4, 1);
-    copy.look_up(t0 + 8);
+  if (t0 + W < p.t1) {
+    copy.look_up(t0 + W);
+    fetch(t0 + W, 1);
+    copy.look_up(t0 + 2 * W);
   }
   Row::flip(a, q);
 
   Sums<DB, F16> acc;
   const Reader<DB> read(lane);
   int buf = 0;
-  for (int t = t0; t < p.t1; t += 4, buf ^= 1) {
+  for (int t = t0; t < p.t1; t += W, buf ^= 1) {
     // this tile has landed when only the next one's copies are outstanding (a list's reads are among those)
-    if (!LIST && t + 4 < p.t1) vmcnt_wait<2 * Copier<DB, KEYS, 1, LIST>::COPIES>();
+    if (!LIST && t + W < p.t1) vmcnt_wait<2 * Copier<DB, KEYS, 1, LIST>::COPIES>();
     else vmcnt_wait0();
     const bool last = (t + 1) * KEYS > p.n;
     uint8_t *st = mine + 2 * buf * HALF;
     if (last) clear_rows<DB>(st + HALF, p.n - t * KEYS, KEYS, lane, 64);
     attend<DB, 1, F16>(acc, q, read, st, st + HALF, last ? p.n - t * KEYS : KEYS, h, a.c);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");       // the tile has been read
-    if (t + 8 < p.t1) {
-      fetch(t + 8, buf);
-      copy.look_up(t + 12);
+    if (t + 2 * W < p.t1) {
+      fetch(t + 2 * W, buf);
+      copy.look_up(t + 3 * W);
     }
   }
   // The wavefronts' sums, [wavefront][row][channel], with their maxima and sums behind.
   acc.sum = half_sum(acc.sum);
   __syncthreads();
-  float *so = reinterpret_cast<float *>(lds), *sm = so + 4 * 32 * PITCH, *sl = sm + 4 * 32;
+  float *so = reinterpret_cast<float *>(lds), *sm = so + W * 32 * PITCH, *sl = sm + W * 32;
   if (m < a.rows) {
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -703,18 +703,18 @@ __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const Cr
     sl[32 * w + m] = t0 < p.t1 ? acc.sum : -1.0f;            // -1: no states
   }
   __syncthreads();
-  const int row = threadIdx.x >> 3, part = threadIdx.x & 7;   // eight threads to a row
+  const int row = threadIdx.x / SHARE, part = threadIdx.x % SHARE;
   if (row >= a.rows) return;
-  float top = kLowest, sum = 0.0f, f[4];
+  float top = kLowest, sum = 0.0f, f[W];
   bool some = false;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < W; ++i) {
     const bool in = sl[32 * i + row] != -1.0f;
     some = some || in;
     if (in) top = fmaxf(top, sm[32 * i + row]);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < W; ++i) {
     const bool in = sl[32 * i + row] != -1.0f;
     f[i] = in ? __builtin_amdgcn_exp2f(sm[32 * i + row] - top) : 0.0f;
     sum = in ? __builtin_fmaf(f[i], sl[32 * i + row], sum) : sum;
@@ -728,11 +728,11 @@ __global__ __launch_bounds__(256, DB > 2 ? 1 : 2) void cross_few_kernel(const Cr
     a.ml[2 * at + 1] = some ? sum : -1.0f;
   }
 #pragma unroll
-  for (int c = 4 * part; c < 32 * DB; c += 32) {
+  for (int c = 4 * part; c < 32 * DB; c += 4 * SHARE) {
     if (c >= a.D) break;
     v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W; ++i) {
       const v4f x = *reinterpret_cast<const v4f *>(so + (32 * i + row) * PITCH + c);
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(f[i], x[e], y[e]);
@@ -912,20 +912,20 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
       else hipLaunchKernelGGL((cross_near_kernel<DB, CAP, false, false>), grid, dim3(512), 0, stream, a);      \
     }                                                                                     \
   } while (0)
-#define CROSS_FEW(DB)                                                                     \
+#define CROSS_FEW(DB, W)                                                                     \
   do {                                                                                    \
     if (dtype == SVDQ_FP16) {                                                             \
-      if (list) hipLaunchKernelGGL((cross_few_kernel<DB, true, true>), grid, dim3(256), 0, stream, a);   \
-      else hipLaunchKernelGGL((cross_few_kernel<DB, true, false>), grid, dim3(256), 0, stream, a);       \
+      if (list) hipLaunchKernelGGL((cross_few_kernel<DB, W, true, true>), grid, dim3(64 * W), 0, stream, a);   \
+      else hipLaunchKernelGGL((cross_few_kernel<DB, W, true, false>), grid, dim3(64 * W), 0, stream, a);       \
     } else {                                                                              \
-      if (list) hipLaunchKernelGGL((cross_few_kernel<DB, false, true>), grid, dim3(256), 0, stream, a);  \
-      else hipLaunchKernelGGL((cross_few_kernel<DB, false, false>), grid, dim3(256), 0, stream, a);      \
+      if (list) hipLaunchKernelGGL((cross_few_kernel<DB, W, false, true>), grid, dim3(64 * W), 0, stream, a);  \
+      else hipLaunchKernelGGL((cross_few_kernel<DB, W, false, false>), grid, dim3(64 * W), 0, stream, a);      \
     }                                                                                     \
   } while (0)
   switch (p.blocks) {
-    case 2: if (p.own) CROSS_FEW(2); else if (p.near) CROSS_NEAR(2); else CROSS_MANY(2, 64); break;
-    case 3: if (p.own) CROSS_FEW(3); else if (p.near) CROSS_NEAR(3); else CROSS_MANY(3, 64); break;
-    case 4: if (p.own) CROSS_FEW(4); else if (p.near) CROSS_NEAR(4); else CROSS_MANY(4, 64); break;
+    case 2: if (p.wide) CROSS_FEW(2, 8); else if (p.own) CROSS_FEW(2, 4); else if (p.near) CROSS_NEAR(2); else CROSS_MANY(2, 64); break;
+    case 3: if (p.own) CROSS_FEW(3, 4); else if (p.near) CROSS_NEAR(3); else CROSS_MANY(3, 64); break;
+    case 4: if (p.own) CROSS_FEW(4, 4); else if (p.near) CROSS_NEAR(4); else CROSS_MANY(4, 64); break;
     case 5: CROSS_MANY(5, 32); break;
     default: CROSS_MANY(8, 32); break;
   }

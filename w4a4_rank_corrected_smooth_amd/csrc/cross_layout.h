@@ -25,6 +25,7 @@ struct CrossPlan {
   int blocks = 0;         // blocks of 32 channels that the kernel is built for
   bool near = false;      // all states in LDS, many rows
   bool own = false;       // each wavefront has states of its own (few rows), not rows of its own
+  bool wide = false;      // own: eight wavefronts, not four
   int least = 1;          // tiles of a part, for that the parts' sums are not most of the work
   int tile_keys = 0;      // states that a workgroup (own: a wavefront) takes at a time
   int64_t tiles = 0;      // workgroups that share the rows of a (batch row, key/value head)
@@ -57,7 +58,12 @@ inline CrossPlan cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64
   // the form for few rows needs most of the LDS, two elsewhere): as many as fit in one round, of `least` tiles
   // (many rows: 256 over 1500 states, 16 heads of 64, with 4, 6, 8 and 12 take 14.7, 15.3, 17.1 and 19.4 us, 512 over 4096, 8
   // heads of 64, 22.9, 21.4, 19.2 and 21.8; 256 rows over 15804 states of 6 batch rows 33.4, 32.5, 32.3 and 41.8).
-  const int64_t places = p.own && p.blocks > 2 ? 256 : 512;
+  // Few rows of 64 channels or less: eight wavefronts, and no join, where a workgroup to a head nearly fills the CUs
+  // (160 heads over 1500 states 15.1 us, two workgroups of four to a CU and a join 16.7; 240 18.6 and 21.5, with a mask
+  // 21.5 and 24.5; 256 over 448 7.5 and 11.0; but 80 over 1500 11.9 and 11.4, 320 28.8 and 25.3).  Longer states are
+  // shared out by their lengths.
+  p.wide = p.own && p.blocks == 2 && work > 128 && work <= 256 && Lk <= 2048;
+  const int64_t places = p.wide || (p.own && p.blocks > 2) ? 256 : 512;
   if (!p.near && work > 0 && work < places) {
     const int64_t want = places / work, most = key_tiles / p.least;
     p.parts = (int)(want < most ? want : most);
