@@ -967,7 +967,7 @@ def fp8_linear_forward(layer: Fp8Linear, x: torch.Tensor, gelu: bool = False, ou
     row = _fp8_rows(x, dev, layer.K)
     M = x.size(0)
     if out is None:
-        out = torch.empty((M, layer.N), dtype=out_dtype or x.dtype, device=dev)
+        out = x.new_empty((M, layer.N)) if out_dtype is None else x.new_empty((M, layer.N), dtype=out_dtype)
     else:
         _need_dense(out, "out", dev, out_dtype or out.dtype, (M, layer.N))
     if out.dtype not in _DT16:
@@ -1052,7 +1052,7 @@ def _rotary_rows(x, name: str, dev, T: int, D: int, dtype, out):
     """One of the two operands of svdq_rotary_apply, with its output."""
     H, row, head = _rotary_operand(x, name, dev, T, D, dtype)
     if out is None:
-        out = torch.empty((T, H, D), dtype=dtype, device=dev)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
         return out, (x.data_ptr(), row, head, H, out.data_ptr(), H * D, D)
     out_heads, out_row, out_head = _rotary_operand(out, name + "_out", dev, T, D, dtype)
     if out_heads != H:
