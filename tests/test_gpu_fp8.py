@@ -230,10 +230,10 @@ def test_fp8_linear_large(S):
         assert ((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + (7 * 2.0 ** -13 + (K / 8 + K / 128 + 2) * 2.0 ** -23) * size).all()
 
 
-@pytest.mark.parametrize("M,N", [(2100, 1000), (2900, 1500), (4500, 2700), (1500, 300)])
+@pytest.mark.parametrize("M,N", [(2100, 1000), (2900, 1500), (4100, 1500), (4500, 2700), (1500, 300)])
 @pytest.mark.parametrize("K", [8, 128, 136, 384, 504, 640])
 def test_fp8_linear_every_tile_form_short_k(S, M, N, K):
-    """Tiles of 128 x 128 with four stages and with two, of 256 x 256 and of 64 x 64, over fewer blocks of K than
+    """Tiles of 128 x 128 with four stages, of 192 x 128, of 128 x 128 with two, of 256 x 256 and of 64 x 64, over fewer blocks of K than
     stages and a few more: small integers, as above, so that the result is the exact one rounded once."""
     announce(f"fp8 linear of small integers M={M} N={N} K={K}")
     g = torch.Generator(device="cuda").manual_seed(M + K)

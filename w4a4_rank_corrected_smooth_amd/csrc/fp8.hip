@@ -180,8 +180,7 @@ __device__ __forceinline__ v4f finish(const Fp8Args &a, v4f bias, v4f y) {
 // next copy, costs no read of its own.
 template <int TM, int TN, int WM, int WN, int ST, int OUT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args a) {
-  constexpr int XB = TM * WM, WB = TN * WN, WAVES = WM * WN, COPIES = (XB + WB) / WAVES;
-  static_assert((XB + WB) % WAVES == 0, "blocks dealt out evenly");
+  constexpr int XB = TM * WM, WB = TN * WN, WAVES = WM * WN, COPIES = (XB + WB + WAVES - 1) / WAVES;
   // a stage: the blocks of X and W, then their scales, 256 bytes to each (what a copy writes)
   constexpr int W_AT = XB * kFp8Block, XS_AT = W_AT + WB * kFp8Block, WS_AT = XS_AT + XB * 256;
   constexpr int STAGE = WS_AT + WB * 256;
@@ -197,13 +196,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args
   const int tm = 8 * band + in % high, tn = in / high;
 
   const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds);
-  // the blocks that this wavefront copies
+  // the blocks that this wavefront copies (the last one more than once where they do not come out even)
+  auto block_of = [&](int c) { return (XB + WB) % WAVES == 0 ? w + WAVES * c : min(w + WAVES * c, XB + WB - 1); };
   const uint8_t *from[COPIES], *scale[COPIES];
   uint32_t scale_lane[COPIES];
   int scale_step[COPIES];
 #pragma unroll
   for (int c = 0; c < COPIES; ++c) {
-    const int i = w + WAVES * c;
+    const int i = block_of(c);
     const bool is_x = i < XB;
     const int64_t at = (int64_t)(is_x ? min(tm * XB + i, a.m_blocks - 1) : min(tn * WB + i - XB, a.n_blocks - 1)) * a.blocks_k;
     from[c] = (is_x ? a.x : a.w) + at * kFp8Block;
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args
   constexpr int FETCHES = 5 * COPIES;
   int fetched = 0;
   auto fetch1 = [&](int stage, int f) {
-    const int c = f / 5, j = f % 5, i = w + WAVES * c;
+    const int c = f / 5, j = f % 5, i = block_of(c);
     const uint32_t at = lds_at + stage * STAGE;
     if (j < 4) {
       lds_dma16_s(from[c] + 1024 * j, 16 * lane, at + i * kFp8Block + 1024 * j);
@@ -544,6 +544,14 @@ __global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_few_kernel(const Fp8Ar
   a.out[(int64_t)m * a.N + n] = narrow<OUT>(y);
 }
 
+template <int TM, int TN, int WM, int WN, int ST, int OUT>
+void launch_tiles(Fp8Args &a, hipStream_t stream) {
+  a.tiles_m = (a.M + 32 * TM * WM - 1) / (32 * TM * WM);
+  a.tiles_n = (a.N + 32 * TN * WN - 1) / (32 * TN * WN);
+  const dim3 grid((unsigned)((a.tiles_m * a.tiles_n + 7) / 8 * 8));
+  hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, ST, OUT>), grid, dim3(64 * WM * WN), 0, stream, a);
+}
+
 template <int OUT>
 void launch_product(const Fp8Plan &p, Fp8Args &a, bool f16, hipStream_t stream) {
   if (p.form == FP8_FEW) {
@@ -562,14 +570,13 @@ void launch_product(const Fp8Plan &p, Fp8Args &a, bool f16, hipStream_t stream) 
     else hipLaunchKernelGGL((fp8_rows_kernel<3, false, false, OUT>), grid, block, 0, stream, a);
     return;
   }
-  const int side = p.form == FP8_256 ? 256 : p.form == FP8_128 ? 128 : 64;
-  a.tiles_m = (a.M + side - 1) / side;
-  a.tiles_n = (a.N + side - 1) / side;
-  const dim3 grid((unsigned)((a.tiles_m * a.tiles_n + 7) / 8 * 8));
-  if (p.form == FP8_256) hipLaunchKernelGGL((fp8_tile_kernel<4, 2, 2, 4, 2, OUT>), grid, dim3(512), 0, stream, a);
-  else if (p.form == FP8_128 && p.deep) hipLaunchKernelGGL((fp8_tile_kernel<2, 1, 2, 4, 4, OUT>), grid, dim3(512), 0, stream, a);
-  else if (p.form == FP8_128) hipLaunchKernelGGL((fp8_tile_kernel<2, 2, 2, 2, 2, OUT>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((fp8_tile_kernel<1, 1, 2, 2, 4, OUT>), grid, dim3(256), 0, stream, a);
+  switch (p.form) {
+    case FP8_256: launch_tiles<4, 2, 2, 4, 2, OUT>(a, stream); break;
+    case FP8_192: launch_tiles<1, 2, 6, 2, 3, OUT>(a, stream); break;
+    case FP8_128_DEEP: launch_tiles<2, 1, 2, 4, 4, OUT>(a, stream); break;
+    case FP8_128: launch_tiles<2, 2, 2, 2, 2, OUT>(a, stream); break;
+    default: launch_tiles<1, 1, 2, 2, 4, OUT>(a, stream); break;
+  }
 }
 
 svdq_status_t rows_ok(const char *who, const void *x, int64_t x_row, svdq_dtype_t dtype) {

@@ -29,13 +29,13 @@ constexpr int64_t fp8_blocks(int64_t rows, int64_t K) { return fp8_up(rows, 32) 
 constexpr int64_t fp8_w_bytes(int64_t N, int64_t K) { return fp8_blocks(N, K) * (kFp8Block + kFp8WScales); }
 constexpr int64_t fp8_x_bytes(int64_t M, int64_t K) { return fp8_up(fp8_blocks(M, K) * (kFp8Block + kFp8XScales), 256); }
 
-// Which kernel multiplies: few rows, or tiles of 64, 128 or 256 rows and channels.
-enum Fp8Form { FP8_FEW, FP8_ROWS, FP8_64, FP8_128, FP8_256 };
+// Which kernel multiplies: few rows, or tiles of 64, 128 or 256 rows and channels, or of 192 rows by 128.
+// FP8_128_DEEP: four stages of the tiles in LDS, a workgroup to a CU, where FP8_128 has two and two.
+enum Fp8Form { FP8_FEW, FP8_ROWS, FP8_64, FP8_128_DEEP, FP8_192, FP8_128, FP8_256 };
 struct Fp8Plan {
   Fp8Form form = FP8_ROWS;
   bool inline_x = false;       // FP8_FEW, FP8_ROWS: each workgroup quantises the rows for itself
   int x_blocks = 1;            // FP8_ROWS: blocks of 32 rows
-  bool deep = false;           // FP8_128: four stages, a workgroup to a CU
   int64_t total = 0;           // bytes of workspace: the rows' blocks
 };
 
@@ -55,13 +55,16 @@ inline Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
     p.x_blocks = (int)((M + 31) / 32);
   } else {
     const int64_t t128 = (M + 127) / 128 * ((N + 127) / 128), t256 = (M + 255) / 256 * ((N + 255) / 256);
-    // Tiles of 256 x 256, a workgroup to a CU, take 1.4 times as long a round as tiles of 128 x 128 two to a CU (4096 x 4096 x
-    // 4096: 74 us in 1 round, 85 in 2; 2048 x 6144 x 4096: 64 and 70; 4096 x 2048 x 8192: 106 and 87); those keep
-    // four stages, one to a CU, where that makes one round (1024 x 4096 x 4096: 28.4 us, two stages 32.4, 64 x 64 tiles 41;
-    // 4095 x 1152 x 4608, 288 tiles: 49, 45 and 53); tiles of 64 x 64 fill the CUs where those do not (256 x
-    // 6144 x 4096, 96 tiles: 20.3 us, 128 x 128 21.6).
-    p.form = (t256 + 255) / 256 * 5120 <= 7 * t128 ? FP8_256 : t128 >= 128 ? FP8_128 : FP8_64;
-    p.deep = t128 <= 256;
+    // Tiles of 256 x 256, a workgroup to a CU, take 1.4 times as long a round as tiles of 128 x 128 two to a CU
+    // (4096 x 4096 x 4096: 74 us in 1 round, 85 in 2; 2048 x 6144 x 4096: 64 and 70; 4096 x 2048 x 8192: 106 and 87).
+    // Those keep four stages, one to a CU, where that makes one round (1024 x 4096 x 4096: 28.4 us, two stages 32.4,
+    // 64 x 64 tiles 41; 4095 x 1152 x 4608, 288 tiles: 49, 45 and 53), and are 192 high where that makes one round of them
+    // (twelve wavefronts, three stages; 4095 x 1152 x 4608: 45.6, two of 128 to a CU 48.3; 2304 x 2048 x 4096: 35.7 and
+    // 40.0; 160 or 256 high, and other shares of the wavefronts, were no better).  Tiles of 64 x 64 fill the CUs where
+    // those do not (256 x 6144 x 4096, 96 tiles: 20.3 us, 128 x 128 21.6).
+    const int64_t t192 = (M + 191) / 192 * ((N + 127) / 128);
+    p.form = (t256 + 255) / 256 * 5120 <= 7 * t128 ? FP8_256 : t128 < 128 ? FP8_64 : t128 <= 256 ? FP8_128_DEEP
+             : t192 <= 256 ? FP8_192 : FP8_128;
   }
   p.total = p.inline_x ? 0 : fp8_x_bytes(M, K);
   return p;
