@@ -141,6 +141,20 @@ def test_rotary_offsets_past_32_bits(S):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_rotary_of_65536_heads(S):
+    """A token's channels, and a workgroup's, past 2^24 and 2^31 if they were not cut: one pair of 256 channels."""
+    T, H, D = 300, 65536, 256
+    plan = S.RotaryPlan(D, [2], interleaved=False)
+    x = torch.randn(T, 1, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    positions = torch.arange(T, dtype=torch.int32, device="cuda")[:, None]
+    want, _ = S.rotary_apply(plan, x, None, positions)
+    out = torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda")
+    announce("rotary of 65536 heads of 256")
+    S.rotary_apply(plan, x.expand(T, H, D), None, positions, q_out=out)
+    for t in range(0, T, 50):
+        assert torch.equal(out[t:t + 50], want[t:t + 50].expand(-1, H, D))
+
+
 @pytest.mark.parametrize("Lq,Lk", [(3, 600), (20, 2600), (200, 600), (200, 2600), (66000, 300)])
 @pytest.mark.parametrize("mask", [False, True])
 def test_cross_attention_offsets_past_32_bits(S, Lq, Lk, mask):
