@@ -530,7 +530,9 @@ __device__ __forceinline__ void attend(Sums<DB, F16> &acc, const v4u (&q)[2 * DB
 // still (an instruction and 16 FMAs, from two wavefronts: 31 ns, 14 and 16 alone), so the kernel's time is the sum of
 // both: 16 instructions of 14 ns for 32 x 32 scores of 128 channels, and about 100 ns of maxima, exponentials and
 // conversions.  Ordering the two by hand, the next block's scores between this one's exponentials, was
-// slower than the compiler's order (564 against 539 us at 4096 x 16384, 16 heads).
+// slower than the compiler's order (564 against 539 us at 4096 x 16384, 16 heads).  Workgroups that go on to
+// the next row tile with its queries asked for ahead were no faster (32760 rows over 512 states, 12 heads: 146 us, this 142),
+// as the registers they need cost more.  4096 x 16384, 16 heads of 128: 520 us, 1.06 PFLOP/s.
 template <int DB, int KEYS, bool F16, bool LIST>
 __global__ __launch_bounds__(256, 2) void cross_many_kernel(const CrossArgs a) {
   typedef Rows<DB> L;
@@ -585,7 +587,9 @@ __global__ __launch_bounds__(256, 2) void cross_many_kernel(const CrossArgs a) {
 }
 
 // Many rows over few states: a workgroup keeps all of a key/value head's states in LDS (up to CAP), and its
-// eight wavefronts go through rows by 32, each by itself, without barriers.
+// eight wavefronts go through rows by 32, each by itself, without barriers.  2 x 4096 rows over 300 states, 16 heads of
+// 72: 27 us, of which 10 do not grow with the rows (launch, the states' way into LDS, last stores); the rest is
+// bound by the vector ALU as above.  The tiles of four wavefronts take 37.
 template <int DB, int CAP, bool F16, bool LIST>
 __global__ __launch_bounds__(512, 2) void cross_near_kernel(const CrossArgs a) {
   typedef Rows<DB> L;
@@ -637,7 +641,8 @@ __global__ __launch_bounds__(512, 2) void cross_near_kernel(const CrossArgs a) {
 }
 
 // Few rows (up to 32 of a key/value head): the wavefronts (four or eight) take tiles of 32 states of
-// their own, in LDS of their own, without barriers, two tiles in flight, and add up at the end.  Bound by memory.
+// their own, in LDS of their own, without barriers, two tiles in flight, and add up at the end.  Bound by memory
+// (8 x 20 heads of 64 over 1500 states, 61 MB: 15.2 us, 4.0 TB/s with a workgroup on 160 of the CUs).
 template <int DB, int W, bool F16, bool LIST>
 __global__ __launch_bounds__(64 * W, DB > 2 ? 1 : 2) void cross_few_kernel(const CrossArgs a) {
   typedef Rows<DB> L;
@@ -747,7 +752,7 @@ __global__ __launch_bounds__(64 * W, DB > 2 ? 1 : 2) void cross_few_kernel(const
 
 // A wavefront joins a row's pieces: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // LANES lanes hold a row's channels, four each; 64 / LANES pieces are read at a time, and four of
-// those in flight.
+// those in flight (about 40 pieces of 1024 rows of 128, 21 MB, to 6144 rows: 8 us, 2.6 TB/s).
 template <int LANES, bool F16>
 __global__ __launch_bounds__(256) void cross_join_kernel(const CrossArgs a, int keys) {
   const int lane = threadIdx.x & 63;

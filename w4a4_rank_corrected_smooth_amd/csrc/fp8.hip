@@ -83,7 +83,7 @@ __device__ __forceinline__ uint32_t quantize16(const uint16_t *src, int k, int K
   return (uint32_t)scale;
 }
 
-// A workgroup: 32 rows by one block.  CANON: codes [M, K] and scales [M, blocks] instead of operand blocks.
+// A workgroup: 32 rows by one block.  Bound by memory (4095 x 4608: 56 MB in 10.6 us, 5.3 TB/s).  CANON: codes [M, K] and scales [M, blocks] instead of operand blocks.
 template <bool F16, bool CANON>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(const uint16_t *__restrict__ x, int64_t x_row, int M, int K,
                                                            int blocks_k, uint8_t *__restrict__ out,
@@ -177,7 +177,8 @@ __device__ __forceinline__ v4f finish(const Fp8Args &a, v4f bias, v4f y) {
 // (alone, such an instruction takes 27 ns, with eight FMAs 31, and FMAs that wait for their own
 // tile's result cost their full 15 ns for eight).  Operands of the next block of K are read from LDS during the last row of
 // tiles, so that the barrier before it, which frees the stage just read for the
-// next copy, costs no read of its own.
+// next copy, costs no read of its own.  4608 x 16384 x 4096 in tiles of 256 x 256: 305 to 330 us with the quantiser and GELU,
+// by the card's clock under load, 2.0 PFLOP/s (with zeros for values 254 us); bound by the matrix core.
 template <int TM, int TN, int WM, int WN, int ST, int OUT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(const Fp8Args a) {
   constexpr int XB = TM * WM, WB = TN * WN, WAVES = WM * WN, COPIES = (XB + WB + WAVES - 1) / WAVES;
@@ -383,7 +384,8 @@ __device__ __forceinline__ void quantize_rows(const Fp8Args &a, uint8_t *xl, uin
 
 // Few rows.  A workgroup has 32 output channels; its eight wavefronts deal out
 // the blocks of K among themselves and add up in LDS.  Weights go from memory
-// straight into operands, AHEAD blocks of a wavefront in flight.  OWN: the
+// straight into operands, AHEAD blocks of a wavefront in flight (one row of 6144 x 4096: 6.9 us, 3.7 TB/s, most of the
+// rest the launch and the rows' quantising; 77 of 2121 x 1160: 8.2 with the quantiser's launch).  OWN: the
 // workgroup quantises the rows itself, into LDS (one block of 32 rows, up to 24576 values in all).
 template <int XB, bool OWN, bool F16, int OUT>
 __global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_rows_kernel(const Fp8Args a) {
@@ -470,8 +472,9 @@ __global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_rows_kernel(const Fp8A
 }
 
 // Up to 16 rows.  As above, with 16 output channels to a workgroup, so that few channels make more
-// workgroups, and more of a wavefront's part of K in flight.  The instruction takes a whole block of 128: lane l holds units 2
-// (l / 16) and 2 (l / 16) + 1 of channel (of row) l % 16, and its results are of row l % 16, channels 4 (l / 16) + [0, 4).
+// workgroups, and more of a wavefront's part of K in flight (one row of 4096 x 14336, 59 MB: 15.3 us, 3.8 TB/s).  The
+// instruction takes a whole block of 128: lane l holds units 2 (l / 16) and 2 (l / 16) + 1 of channel (of row) l % 16,
+// and its results are of row l % 16, channels 4 (l / 16) + [0, 4).
 constexpr int kFp8FewAhead = 8;
 template <bool OWN, bool F16, int OUT>
 __global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_few_kernel(const Fp8Args a) {
