@@ -1,6 +1,6 @@
 // Cross attention: queries over an encoder's states of another length.
 //
-//  cross_list_kernel     the visible states of each batch row, where there is a mask
+//  cross_list_kernel     the visible states of each batch row, where there is a mask over many
 //  cross_many_kernel     attention of a tile of rows over a piece of the states
 //  cross_near_kernel     the same over few states, all of them in LDS
 //  cross_few_kernel      the same for a handful of rows

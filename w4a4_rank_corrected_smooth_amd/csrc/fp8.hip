@@ -33,7 +33,7 @@ struct Fp8Args {
   int m_blocks, n_blocks;        // of 32
   int tiles_m, tiles_n;
   int gelu;
-  // FP8_ROWS with its own quantiser
+  // the forms for few rows that quantise them themselves
   const uint16_t *rows;
   int64_t rows_stride;
   int K;
