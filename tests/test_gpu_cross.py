@@ -354,3 +354,26 @@ def test_cross_attention_streams_graphs_and_two_at_once(S):
             g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(bufs[2], s[4][i]) for (g, bufs), s in zip(graphs, sets))
+
+
+@pytest.mark.parametrize("top", [125.0, 127.99])
+@pytest.mark.parametrize("B,Lq,Lk,Hq,Hkv,D,lens", [
+    (8, 1, 1500, 20, 20, 64, False), (1, 4, 1500, 2, 2, 64, False), (16, 3, 900, 16, 16, 96, False), (16, 3, 900, 16, 16, 128, False),
+    (1, 8, 20000, 8, 8, 96, False), (1, 200, 900, 2, 2, 128, False), (4, 150, 3001, 2, 1, 128, True), (1, 200, 900, 2, 2, 160, False),
+    (1, 200, 900, 2, 2, 256, False), (1, 4100, 300, 16, 16, 64, False), (2, 4097, 256, 8, 8, 128, False)])
+def test_cross_attention_large_values_behind_a_low_maximum(S, B, Lq, Lk, Hq, Hkv, D, lens, top):
+    """The last state's score is 7.9 (log2) above all others', which the running maximum need not follow, and its values are
+    next to the end of bfloat16's range: the result is finite."""
+    announce(f"cross of values 2^{top} B={B} Lq={Lq} Lk={Lk} Hq={Hq} Hkv={Hkv} D={D}")
+    r = np.random.default_rng(Lk)
+    q = torch.zeros(B, Lq, Hq, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    k = torch.zeros(B, Lk, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    v = rows(r, (B, Lk, Hkv, D), "bf16")
+    k[:, -1, :, 0] = 5.46875
+    v[:, -1] = (torch.rand(B, Hkv, D, device="cuda").sub(0.5).sign() * 2.0 ** (top - 7) * 2.0 ** 7).bfloat16()
+    n = torch.full((B,), Lk, dtype=torch.int32, device="cuda") if lens else None
+    got = S.cross_attention(q, k, v, scale=1.0, key_lens=n)
+    # all rows of a head are alike
+    assert torch.equal(got, got[:, :1].expand_as(got))
+    near(got[:, :1], q[:, :1], k, v, scale=1.0)

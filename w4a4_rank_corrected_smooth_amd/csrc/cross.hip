@@ -38,11 +38,14 @@ typedef short v4i16 __attribute__((ext_vector_type(4)));
 
 constexpr float kLowest = -3.0e38f;      // the maximum of a row that has met no score above -inf
 // How far (log2) scores may pass the running maximum before the sums are
-// rescaled: 2^8 more is no loss in float32, and nearly all tiles go without.
+// rescaled: nearly all tiles go without.
 constexpr float kSlack = 8.0f;
-// float16 weights are p 2^7, at most 2^15 with the slack: the type's smallest step is then at most
-// 2^-31 of the largest weight, so that many small ones do not vanish.
-constexpr float kShift16 = 7.0f;
+// Weights carry 2^shift, which the result's division takes off again.  Those of bfloat16 2^-8, for
+// that none passes 1, slack included: a product with a value of V is then no larger than that one, as far as float32 and
+// bfloat16 reach, and a weight is lost from 2^-118 down.  Those of float16 2^7, so at most 2^15: the type's smallest
+// step is then at most 2^-31 of the largest weight, so that many small ones do not vanish.
+template <bool F16>
+constexpr float kShift = F16 ? 7.0f : -kSlack;
 
 struct CrossArgs {
   const uint16_t *q, *k, *v;
@@ -513,7 +516,7 @@ __device__ __forceinline__ void attend(Sums<DB, F16> &acc, const v4u (&q)[2 * DB
 #pragma unroll
   for (int b = 1; b < KB; ++b) best = fmaxf(best, largest(s[b]));
   acc.raise(half_max(best) * c);
-  const float off = (F16 ? kShift16 : 0.0f) - acc.top;
+  const float off = kShift<F16> - acc.top;
 #pragma unroll
   for (int b = 0; b < KB; ++b) {
     v4u pw[2];
