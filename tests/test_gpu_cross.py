@@ -377,3 +377,25 @@ def test_cross_attention_large_values_behind_a_low_maximum(S, B, Lq, Lk, Hq, Hkv
     # all rows of a head are alike
     assert torch.equal(got, got[:, :1].expand_as(got))
     near(got[:, :1], q[:, :1], k, v, scale=1.0)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-45, 3e-39, -1e-38, 6e-38])
+@pytest.mark.parametrize("Lq,Lk,H,D,hide", [(2, 333, 2, 64, "none"), (40, 333, 2, 128, "none"), (40, 333, 2, 160, "lens"),
+                                            (4100, 300, 16, 72, "none"), (2, 333, 2, 64, "mask")])
+def test_cross_attention_smallest_scales_of_large_products(S, Lq, Lk, H, D, hide, scale):
+    """Products of 1e37 at scales that bring them to 0 (equal weights) and to scores below 1."""
+    announce(f"cross of products of 1e37, scale {scale}, Lq={Lq} D={D} {hide}")
+    scale = float(np.float32(scale))
+    r = np.random.default_rng(Lq)
+    q, k, v = (rows(r, (1, n, H, D), "bf16") for n in (Lq, Lk, Lk))
+    q[..., 3], k[..., 3] = 1e19, torch.from_numpy(r.uniform(-1e18, 1e18, (1, Lk, H))).cuda().bfloat16()
+    n = Lk - 30 if hide == "lens" else Lk
+    visible = np.arange(Lk)[None] < n
+    mask = None
+    if hide == "mask":
+        visible = r.random((1, Lk)) < 0.5
+        mask = torch.from_numpy(visible).cuda()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda") if hide == "lens" else None
+    got = S.cross_attention(q, k, v, scale=scale, key_lens=lens, mask=mask)
+    some = slice(0, None, 64) if Lq > 1000 else slice(None)
+    near(got[:, some], q[:, some], k, v, visible, scale=scale)
