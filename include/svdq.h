@@ -558,8 +558,9 @@ svdq_status_t svdq_rotary_apply(const svdq_rotary_t *plan, const void *q, int64_
  * strides multiples of 8 elements, not negative.  D a multiple of 8 up to 256, Hq a
  * multiple of Hkv, B <= 65536, Lk <= 2^30, B Lq Hq <= 2^28,
  * B Hkv <= 2^20, strides of k_token and v_token below 2^24, |scale| < 2^127.
- * Scores, softmax statistics and sums are float32; the weights p enter the
- * product in the inputs' type, bf16's at most 1 and the largest at least 2^-8, fp16's
+ * Scores, softmax statistics and sums are float32 (scores in units of log2: scale q . k log2(e) has to be
+ * in float32's range); the weights p enter the
+ * product in the inputs' type, bf16's at most 1 and the largest at least 2^-9, fp16's
  * at most 2^15 and the largest at least 2^7, so that its lower end is 2^-31 below them.  out is
  * rounded once.  Its sums are finite where Lk times the largest |v| is below 2^127.
  * The result does not depend on the order in which workgroups run.  One kernel, another

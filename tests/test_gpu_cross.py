@@ -399,3 +399,32 @@ def test_cross_attention_smallest_scales_of_large_products(S, Lq, Lk, H, D, hide
     got = S.cross_attention(q, k, v, scale=scale, key_lens=lens, mask=mask)
     some = slice(0, None, 64) if Lq > 1000 else slice(None)
     near(got[:, some], q[:, some], k, v, visible, scale=scale)
+
+
+@pytest.mark.parametrize("kind", ["alike", "rising", "negative"])
+@pytest.mark.parametrize("dtype,power", [("fp16", 12), ("fp16", 15), ("bf16", 15), ("bf16", 30), ("bf16", 58)])
+@pytest.mark.parametrize("B,Lq,Lk,Hq,Hkv,D", [
+    (8, 2, 1500, 20, 20, 64), (1, 4, 1, 2, 2, 64), (16, 3, 900, 16, 16, 96), (1, 8, 20000, 8, 8, 128), (1, 200, 900, 2, 2, 128),
+    (1, 200, 900, 2, 2, 160), (1, 200, 900, 2, 2, 256), (1, 4100, 300, 16, 16, 64)])
+def test_cross_attention_scores_far_from_zero(S, B, Lq, Lk, Hq, Hkv, D, dtype, power, kind):
+    """Scores of 2^24 to 2^122, where a step of float32 is many units of the exponent: those that are alike weigh the same,
+    and the others, lower by a sixteenth or more, nothing.  All products and their sums are exact (powers of two times up
+    to 16); a score's own rounding is the same for all that are alike.  Row 0 is an ordinary one among them."""
+    announce(f"cross of scores far from zero B={B} Lq={Lq} Lk={Lk} Hq={Hq} Hkv={Hkv} D={D} {dtype} 2^{power} {kind}")
+    r = np.random.default_rng(Lk + power)
+    q = rows(r, (B, Lq, Hq, D), dtype)
+    q[:, 1:] = 2.0 ** power
+    steps = {"alike": np.full(Lk, 13), "rising": 1 + 15 * np.arange(Lk) // max(1, Lk - 1), "negative": -16 + 14 * np.arange(Lk) // Lk}[kind]
+    steps = torch.from_numpy(steps).cuda()
+    k = (steps * 2.0 ** (power - 4))[None, :, None, None].expand(B, Lk, Hkv, D).to(DT[dtype])
+    v = rows(r, (B, Lk, Hkv, D), dtype)
+    best = steps == steps.max()
+    want, mean = (x[:, best].double().mean(1).repeat_interleave(Hq // Hkv, 1)[:, None] for x in (v, v.abs()))
+    u = torch.finfo(DT[dtype]).eps / 2
+    tol = u * want.abs() + (u + 2 * 2.0 ** -22 + 2 * Lk * 2.0 ** -23) * mean * (1 + 2.0 ** -6) + (2.0 ** -25 if dtype == "fp16" else 0)
+    for scale in (0.3, 0.11, 0.71, 0.0625):
+        got = S.cross_attention(q, k, v, scale=scale)
+        assert ((got[:, 1:].double() - want).abs() <= tol).all(), scale
+        q2 = q.clone()
+        q2[:, 1:] = 0.25
+        assert torch.equal(got[:, 0], S.cross_attention(q2, k, v, scale=scale)[:, 0], ), scale

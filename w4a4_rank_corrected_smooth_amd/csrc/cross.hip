@@ -38,16 +38,19 @@ namespace {
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 
-constexpr float kLowest = -3.0e38f;      // the maximum of a row that has met no score above -inf
+constexpr float kLowest = -0x1.fffffep127f;      // the maximum of a row that has met no score above -inf
 // How far (log2) scores may pass the running maximum before the sums are
 // rescaled: nearly all tiles go without.
 constexpr float kSlack = 8.0f;
-// Weights carry 2^shift, which the result's division takes off again.  Those of bfloat16 2^-8, for
-// that none passes 1, slack included: a product with a value of V is then no larger than that one, as far as float32 and
-// bfloat16 reach, and a weight is lost from 2^-118 down.  Those of float16 2^7, so at most 2^15: the type's smallest
-// step is then at most 2^-31 of the largest weight, so that many small ones do not vanish.
+// From this maximum on (log2) what rounding to float32 takes off it, up to half a step, is kept beside it: at
+// 2^24 that is one unit of the exponent, and soon more than the weights have room for.  Below it is 2^-9 at most.
+constexpr float kFar = 0x1p16f;
+// Weights carry 2^shift, which the result's division takes off again.  Those of bfloat16 2^-9, for
+// that none passes 1, slack and a maximum's rounding included: a product with a value of V is then no larger than that
+// one, as far as float32 and bfloat16 reach, and a weight is lost from 2^-117 down.  Those of float16 2^7, so at most
+// 2^15: the type's smallest step is then at most 2^-31 of the largest weight, so that many small ones do not vanish.
 template <bool F16>
-constexpr float kShift = F16 ? 7.0f : -kSlack;
+constexpr float kShift = F16 ? 7.0f : -kSlack - 1.0f;
 
 struct CrossArgs {
   const uint16_t *q, *k, *v;
@@ -57,6 +60,7 @@ struct CrossArgs {
   const int *index, *count;              // [B, Lk] the visible ones' numbers, and how many
   uint16_t *out;
   float *ml, *o;                         // pieces: [place][row] (m, l), and [..][D]
+  float *rest;                           // and what goes with an m from kFar on, elsewhere not written
   int B, Lq, Lk, Hq, Hkv, group, D, rows, tiles, parts;
   int run, work;                         // pieces of work; how many go to one XCD together
   int line, least;                       // parts of all batch rows together, shared out by their lengths (0: `parts` each); tiles of one
@@ -381,17 +385,23 @@ struct Reader {
 template <int DB, bool F16>
 struct Sums {
   v16f o[DB];
-  float top = kLowest, sum = 0.0f;       // `sum`: of this lane's half; the halves' are added at the end
+  float top = kLowest, rest = 0.0f;      // the weights' reference: rest is 0 below kFar
+  float sum = 0.0f;                      // of this lane's half; the halves' are added at the end
+  bool far = false;                      // some row of the wavefront has a rest
   __device__ __forceinline__ Sums() {
 #pragma unroll
     for (int d = 0; d < DB; ++d) o[d] = zero16();
   }
-  // makes room for scores whose largest is `best` (times c)
-  __device__ __forceinline__ void raise(float best) {
-    if (__any(best > top + kSlack)) {
-      const float to = best > top + kSlack ? best : top;
-      const float r = __builtin_amdgcn_exp2f(top - to);
+  // makes room for scores whose largest is `best` times c
+  __device__ __forceinline__ void raise(float best, float c) {
+    const bool up = __builtin_fmaf(best, c, -top) - rest > kSlack;
+    if (__any(up)) {
+      const float to = up ? best * c : top, size = fabsf(to);
+      const float left = !up ? rest : size >= kFar && size < __builtin_inff() ? __builtin_fmaf(best, c, -to) : 0.0f;
+      const float r = __builtin_amdgcn_exp2f((top - to) + (rest - left));
       top = to;
+      rest = left;
+      far = __any(rest != 0.0f);
       sum *= r;
 #pragma unroll
       for (int d = 0; d < DB; ++d)
@@ -407,6 +417,7 @@ struct Sums {
     if (h == 0) {
       a.ml[2 * at] = top;
       a.ml[2 * at + 1] = some ? sum : -1.0f;           // -1: a piece without states
+      if (fabsf(top) >= kFar) a.rest[at] = rest;
     }
     if (!some) return;
 #pragma unroll
@@ -517,8 +528,17 @@ __device__ __forceinline__ void attend(Sums<DB, F16> &acc, const v4u (&q)[2 * DB
   float best = largest(s[0]);
 #pragma unroll
   for (int b = 1; b < KB; ++b) best = fmaxf(best, largest(s[b]));
-  acc.raise(half_max(best) * c);
-  const float off = kShift<F16> - acc.top;
+  acc.raise(half_max(best), c);
+  float off = kShift<F16> - acc.top;
+  if (acc.far) {                         // such rows' scores less their maximum, whose rest would be lost in `off`
+    const bool apart = acc.rest != 0.0f;
+    const float inv = 1.0f / c;
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = apart ? (__builtin_fmaf(s[b][i], c, -acc.top) - acc.rest) * inv : s[b][i];
+    off = apart ? kShift<F16> : off;
+  }
 #pragma unroll
   for (int b = 0; b < KB; ++b) {
     v4u pw[2];
@@ -652,7 +672,7 @@ template <int DB, int W, bool F16, bool LIST>
 __global__ __launch_bounds__(64 * W, DB > 2 ? 1 : 2) void cross_few_kernel(const CrossArgs a) {
   typedef Rows<DB> L;
   constexpr int KEYS = 32, STEPS = 2 * DB, HALF = KEYS * L::ROW, PITCH = 32 * DB + 4;     // floats of a row of sums
-  constexpr int TILES = W * 4 * HALF, SUMS = W * 32 * (PITCH + 2) * 4, SHARE = 2 * W;     // threads to a row
+  constexpr int TILES = W * 4 * HALF, SUMS = W * 32 * (PITCH + 3) * 4, SHARE = 2 * W;     // threads to a row
   __shared__ __attribute__((aligned(1024))) uint8_t lds[TILES > SUMS ? TILES : SUMS];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   __shared__ int list[LIST ? kCrossOwnList : 1];
@@ -698,10 +718,10 @@ __global__ __launch_bounds__(64 * W, DB > 2 ? 1 : 2) void cross_few_kernel(const
       copy.look_up(t + 3 * W);
     }
   }
-  // The wavefronts' sums, [wavefront][row][channel], with their maxima and sums behind.
+  // The wavefronts' sums, [wavefront][row][channel], with their maxima, these' rests and sums behind.
   acc.sum = half_sum(acc.sum);
   __syncthreads();
-  float *so = reinterpret_cast<float *>(lds), *sm = so + W * 32 * PITCH, *sl = sm + W * 32;
+  float *so = reinterpret_cast<float *>(lds), *sm = so + W * 32 * PITCH, *sr = sm + W * 32, *sl = sr + W * 32;
   if (m < a.rows) {
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -710,23 +730,26 @@ __global__ __launch_bounds__(64 * W, DB > 2 ? 1 : 2) void cross_few_kernel(const
         *reinterpret_cast<v4f *>(so + (32 * w + m) * PITCH + 32 * d + 8 * j + 4 * h) =
             v4f{acc.o[d][4 * j], acc.o[d][4 * j + 1], acc.o[d][4 * j + 2], acc.o[d][4 * j + 3]};
     sm[32 * w + m] = acc.top;
+    sr[32 * w + m] = acc.rest;
     sl[32 * w + m] = t0 < p.t1 ? acc.sum : -1.0f;            // -1: no states
   }
   __syncthreads();
   const int row = threadIdx.x / SHARE, part = threadIdx.x % SHARE;
   if (row >= a.rows) return;
-  float top = kLowest, sum = 0.0f, f[W];
+  float top = kLowest, rest = 0.0f, sum = 0.0f, f[W];
   bool some = false;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     const bool in = sl[32 * i + row] != -1.0f;
+    const float x = sm[32 * i + row], y = sr[32 * i + row];
     some = some || in;
-    if (in) top = fmaxf(top, sm[32 * i + row]);
+    rest = !in || x < top ? rest : x > top ? y : fmaxf(rest, y);
+    if (in) top = fmaxf(top, x);
   }
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     const bool in = sl[32 * i + row] != -1.0f;
-    f[i] = in ? __builtin_amdgcn_exp2f(sm[32 * i + row] - top) : 0.0f;
+    f[i] = in ? __builtin_amdgcn_exp2f((sm[32 * i + row] - top) + (sr[32 * i + row] - rest)) : 0.0f;
     sum = in ? __builtin_fmaf(f[i], sl[32 * i + row], sum) : sum;
   }
   const Row at_row(a, p, row);
@@ -736,6 +759,7 @@ __global__ __launch_bounds__(64 * W, DB > 2 ? 1 : 2) void cross_few_kernel(const
   if (a.ml && part == 0) {
     a.ml[2 * at] = top;
     a.ml[2 * at + 1] = some ? sum : -1.0f;
+    if (fabsf(top) >= kFar) a.rest[at] = rest;
   }
 #pragma unroll
   for (int c = 4 * part; c < 32 * DB; c += 4 * SHARE) {
@@ -776,16 +800,28 @@ __global__ __launch_bounds__(256) void cross_join_kernel(const CrossArgs a, int 
   constexpr int GROUPS = 64 / LANES;
   const int g = lane / LANES, ch = 4 * (lane % LANES);
   const float2 *ml = reinterpret_cast<const float2 *>(a.ml);
-  float top = kLowest, sum = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float top = kLowest, rest = 0.0f, sum = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   bool some = false;
   // 64 pieces at a time, their maxima and sums a lane each
   for (int p0 = 0; p0 < pieces; p0 += 64) {
     const float2 x = p0 + lane < pieces ? ml[(p0 + lane) * all + at] : make_float2(kLowest, -1.0f);
     const bool in = x.y != -1.0f;
-    float to = in ? fmaxf(top, x.x) : top;
+    float to = in ? fmaxf(top, x.x) : top, r, f;
 #pragma unroll
     for (int i = 32; i > 0; i >>= 1) to = fmaxf(to, __shfl_xor(to, i));
-    const float r = __builtin_amdgcn_exp2f(top - to), f = in ? __builtin_amdgcn_exp2f(x.x - to) : 0.0f;
+    if (__any(in && fabsf(x.x) >= kFar) || rest != 0.0f) {
+      // maxima that are alike differ in their rests
+      const float mine = in && fabsf(x.x) >= kFar ? a.rest[(p0 + lane) * all + at] : 0.0f;
+      float left = fmaxf(in && x.x == to ? mine : -__builtin_inff(), top == to ? rest : -__builtin_inff());
+#pragma unroll
+      for (int i = 32; i > 0; i >>= 1) left = fmaxf(left, __shfl_xor(left, i));
+      r = __builtin_amdgcn_exp2f((top - to) + (rest - left));
+      f = in ? __builtin_amdgcn_exp2f((x.x - to) + (mine - left)) : 0.0f;
+      rest = left;
+    } else {
+      r = __builtin_amdgcn_exp2f(top - to);
+      f = in ? __builtin_amdgcn_exp2f(x.x - to) : 0.0f;
+    }
     some = some || __any(in);
     top = to;
     float add = in ? f * x.y : 0.0f;
@@ -876,6 +912,7 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
   a.least = p.least;
   if (p.parts > 1 || a.line) {
     a.ml = reinterpret_cast<float *>(ws + p.ml_off);
+    a.rest = reinterpret_cast<float *>(ws + p.rest_off);
     a.o = reinterpret_cast<float *>(ws + p.o_off);
   }
   a.lens = key_lens;

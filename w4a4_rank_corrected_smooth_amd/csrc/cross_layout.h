@@ -31,7 +31,7 @@ struct CrossPlan {
   int64_t tiles = 0;      // workgroups that share the rows of a (batch row, key/value head)
   int parts = 1;          // pieces that the states are cut into, over workgroups; or, where the lengths differ,
   int line = 0;           // pieces of all batch rows, shared out by their lengths (0: `parts` each)
-  int64_t index_off = 0, count_off = 0, ml_off = 0, o_off = 0, total = 0;
+  int64_t index_off = 0, count_off = 0, ml_off = 0, rest_off = 0, o_off = 0, total = 0;
 };
 
 constexpr int64_t cross_up(int64_t x) { return (x + 255) / 256 * 256; }
@@ -76,7 +76,8 @@ inline CrossPlan cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64
   p.count_off = lists ? cross_up(4 * B * Lk) : 0;
   const int64_t even = p.parts > 1 ? p.parts * heads : 0, shared = p.line ? (p.line + B) * Hkv : 0, pieces = even > shared ? even : shared;
   p.ml_off = p.count_off + (lists ? cross_up(4 * B) : 0);
-  p.o_off = p.ml_off + (pieces > 0 ? cross_up(8 * pieces * p.rows) : 0);
+  p.rest_off = p.ml_off + (pieces > 0 ? cross_up(8 * pieces * p.rows) : 0);
+  p.o_off = p.rest_off + (pieces > 0 ? cross_up(4 * pieces * p.rows) : 0);
   p.total = p.o_off + (pieces > 0 ? cross_up(4 * pieces * p.rows * D) : 0);
   return p;
 }
