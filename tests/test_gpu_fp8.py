@@ -309,3 +309,32 @@ def test_fp8_linear_streams_and_graphs(S):
             g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(bufs[1], s[2][i]) for (g, bufs), s in zip(graphs, sets))
+
+
+@pytest.mark.parametrize("M", [1, 16, 20, 50, 130, 700])
+def test_fp8_linear_scales_over_the_whole_range(S, M):
+    """Weight scales of zero, negative, subnormal and up to 2^127, under activations that bring the results back into
+    range: small integers times powers of two, so that every sum is exact and the result is rounded once."""
+    r = np.random.default_rng(M)
+    bases = np.array([0.0, -0.125, 2.0 ** -149, 2.0 ** -130, 2.0 ** -126, 2.0 ** 100, 2.0 ** 125])
+    N, K = 128 * len(bases), 264
+    xi, wi = r.integers(-3, 4, (M, K)).astype(float), r.integers(-3, 4, (N, K)).astype(float)
+    scales = (bases[:, None] * r.integers(1, 5, (len(bases), O.blocks(K)))).astype(np.float32)
+    scales[-1, -1] = 2.0 ** 127
+    w = wi * np.repeat(np.repeat(scales.astype(float), 128, 0), 128, 1)[:, :K]
+    layer = S.Fp8Linear(torch.from_numpy(wi).float().to(torch.float8_e4m3fn), scales)
+    reached = set()
+    for power in (-100, 0, 60, 110):
+        x = torch.from_numpy(xi * 2.0 ** power).bfloat16().cuda()
+        announce(f"fp8 linear of scales over the whole range, M={M}, rows of 2^{power}")
+        got = S.fp8_linear_forward(layer, x).cpu()
+        want = torch.from_numpy((xi * 2.0 ** power) @ w.T).bfloat16()
+        for i, b in enumerate(np.abs(bases)):
+            # 264 products of up to 9 by 4 times the base: below 2^14 times it; at the other end the instruction's
+            # products are multiples of 2^power times a base's power of two, 2^-126 for subnormal ones
+            if b == 0 or (2.0 ** (power + 14) * b < 2.0 ** 127 and 2.0 ** power * max(b, 2.0 ** -126) >= 2.0 ** -126
+                          and 2.0 ** power * b >= 2.0 ** -126):
+                at = slice(128 * i, 128 * i + 128)
+                assert torch.equal(got[:, at], want[:, at]), (power, b)
+                reached.add(i)
+    assert reached == set(range(len(bases)))
