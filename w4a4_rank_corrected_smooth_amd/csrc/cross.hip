@@ -299,7 +299,7 @@ struct Copier {
         const uint64_t first = reinterpret_cast<uint64_t>(rows) + (uint64_t)(uint32_t)(t * KEYS + skip) * step;
         const uint64_t base = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(first >> 32)) << 32 |
                               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)first);
-        lds_dma16_s(reinterpret_cast<const void *>(base), (uint32_t)(row(j) - skip) * step + 16 * chunk(j), at);
+        lds_dma16_moved(reinterpret_cast<const void *>(base), (uint32_t)(row(j) - skip) * step + 16 * chunk(j), at);
       } else {                           // rows behind the last state repeat it
         const uint32_t key_at = LIST ? key[LIST ? j : 0] : (uint32_t)min(t * KEYS + row(j), n - 1);
         lds_dma16(rows + 16 * chunk(j) + (uint64_t)key_at * step, at);

@@ -40,19 +40,25 @@ __device__ __forceinline__ void lds_dma16(const void *gsrc, uint32_t lds_base) {
                :: "v"(gsrc), "s"(lds_base) : "memory");
 }
 // The same copy with a wave-uniform base address in scalar registers and a
-// 32-bit per-lane byte offset.  The vector ALU may have written the base just before (a
-// readfirstlane), and a memory instruction must not read such a register within 5 wait states, which the
-// compiler does not see to inside asm.  So the copy reads the base through a move by the scalar ALU, which waits by
-// itself; the move is also the wait state that the write of M0 needs.
+// 32-bit per-lane byte offset.  The base has to come from the scalar ALU (or from long before): a
+// memory instruction must not read a scalar register within 5 wait states of the vector ALU's write
+// (a readfirstlane), which the compiler does not see to inside asm.  tests/test_device_code.py looks
+// at what was built.
 __device__ __forceinline__ void lds_dma16_s(const void *sbase, uint32_t voff, uint32_t lds_base) {
-  uint64_t base;
-  asm volatile("s_mov_b32 m0, %3\n\ts_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
-               : "=&s"(base) : "v"(voff), "s"(sbase), "s"(lds_base) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds_base) : "memory");
 }
 // and of 4 bytes per lane: lane i writes LDS address lds_base + 4 i
 __device__ __forceinline__ void lds_dma4_s(const void *sbase, uint32_t voff, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds_base) : "memory");
+}
+// Of 16 bytes, with a base that a readfirstlane may have written just before: a move by the scalar ALU waits for it by
+// itself, and is the wait state that the write of M0 needs.  (In place of lds_dma16_s everywhere it cost the
+// 8-bit linear's tiles of 64 x 64 5 to 7%: 128 x 6144 x 4096 15.9 us and 15.1.)
+__device__ __forceinline__ void lds_dma16_moved(const void *sbase, uint32_t voff, uint32_t lds_base) {
   uint64_t base;
-  asm volatile("s_mov_b32 m0, %3\n\ts_mov_b64 %0, %2\n\tglobal_load_lds_dword %1, %0"
+  asm volatile("s_mov_b32 m0, %3\n\ts_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
                : "=&s"(base) : "v"(voff), "s"(sbase), "s"(lds_base) : "memory");
 }
 template <int N>
