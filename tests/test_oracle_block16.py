@@ -295,3 +295,44 @@ def test_fp8_wrapper_checks():
         S.fp8_quantize_activations([1])
     with pytest.raises(ValueError, match="32-bit"):
         layer.new_workspace((1 << 32) + 1)
+
+
+def test_outputs_that_overlap_inputs_are_found():
+    """Against the elements themselves, for dense outputs anywhere in a buffer and inputs of any strides."""
+    r = np.random.default_rng(7)
+    buf = torch.arange(4000, dtype=torch.int16)
+    seen = {True: 0, False: 0}
+    for _ in range(3000):
+        shape = tuple(int(n) for n in r.integers(1, 5, r.integers(1, 4))) + (int(r.integers(1, 9)),)
+        t = buf.as_strided(shape, tuple(int(s) for s in r.choice([0, 1, 8, 9, 24, 40, 130, 300], len(shape) - 1)) + (1,), int(r.integers(0, 400)))
+        out = buf[int(r.integers(0, 1900)):][:int(r.integers(1, 120))]
+        apart = not np.intersect1d(t.numpy(), out.numpy()).size
+        seen[apart] += 1
+        if apart:
+            S._need_apart(out, t, "t")
+        else:
+            with pytest.raises(ValueError, match="must not overlap t"):
+                S._need_apart(out, t, "t")
+    assert min(seen.values()) > 200
+    S._need_apart(buf, buf.clone(), "a copy")
+    S._need_apart(buf[:0], buf, "nothing")
+
+
+def test_wrappers_refuse_outputs_that_overlap_inputs():
+    layer = S.Fp8Linear.__new__(S.Fp8Linear)
+    layer.N, layer.K, layer.device = 136, 136, torch.device("cpu")
+    layer._ref = ctypes.byref(S.Fp8Weights(FAKE, None, 136, 136))
+    buf = torch.zeros(40, 136, dtype=torch.bfloat16)
+    for out in (buf[:5], buf[4:9], buf[:5].half().view(torch.bfloat16)):
+        apart = out.data_ptr() < buf.data_ptr() or out.data_ptr() >= buf.data_ptr() + buf.numel() * 2
+        with pytest.raises(ValueError, match="not on cpu" if apart else "overlap x"):
+            S.fp8_linear_forward(layer, buf[:5], out=out)
+    with pytest.raises(ValueError, match="not on cpu"):      # between the rows
+        S.fp8_linear_forward(layer, buf[::10][:2], out=buf[4:6])
+    q, kv = torch.zeros(2, 6, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 6, 8, 64, dtype=torch.bfloat16)
+    k, v = kv[:, :, :4], kv[:, :, 4:]
+    for args, out, why in (((q, k, v), q, "not on cpu"), ((q, q, v), q, "overlap k"), ((q, k, q), q, "overlap v"),
+                           ((k, q.clone(), v.clone()), kv.view(-1)[:q.numel()].view(q.shape), "overlap q"),
+                           ((q, k, v), kv.view(-1)[-q.numel():].view(q.shape), "overlap k")):
+        with pytest.raises(ValueError, match=why):
+            S.cross_attention(*args, out=out, workspace=torch.zeros(1, dtype=torch.uint8))

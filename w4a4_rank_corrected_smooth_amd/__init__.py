@@ -760,6 +760,30 @@ def _need_workspace(t, device) -> None:
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
 
 
+def _meets(lo: int, hi: int, at: int, row: int, dims) -> bool:
+    """Whether the bytes [lo, hi) meet rows of `row` bytes, at `at` and dims = [(count, stride)] from there, the largest
+    stride first."""
+    if not dims:
+        return lo < at + row and at < hi
+    (n, step), inner = dims[0], dims[1:]
+    span = row + sum((m - 1) * s for m, s in inner)
+    first = max(0, (lo - at - span) // step + 1) if step else 0
+    last = min(n - 1, (hi - at - 1) // step) if step else 0
+    if last - first > 1 and step >= span:          # one between two that reach [lo, hi) lies in it
+        return True
+    return any(_meets(lo, hi, at + i * step, row, inner) for i in range(first, last + 1))
+
+
+def _need_apart(out: torch.Tensor, t: torch.Tensor, name: str) -> None:
+    """Raises if a dense out shares memory with t, whose last dimension is dense."""
+    if out.untyped_storage()._cdata != t.untyped_storage()._cdata or not out.numel() or not t.numel():
+        return
+    lo, size = out.data_ptr(), t.element_size()
+    dims = sorted(((n, size * s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1), key=lambda d: -d[1])
+    if _meets(lo, lo + out.numel() * out.element_size(), t.data_ptr(), t.size(-1) * size, dims):
+        raise ValueError(f"out must not overlap {name}")
+
+
 def _call(device, f, *args) -> None:
     """A device entry point on `device`'s current stream."""
     i = device.index
@@ -962,7 +986,7 @@ def fp8_linear_forward(layer: Fp8Linear, x: torch.Tensor, gelu: bool = False, ou
                        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [M, K] (bf16 or fp16, any row stride that is a multiple of 8) through the layer, with
     its bias and, if `gelu`, the tanh GELU: [M, N] of x's type, or out_dtype (bf16 or fp16).
-    The rows are quantised to e4m3 with a power of two for each 128 channels."""
+    The rows are quantised to e4m3 with a power of two for each 128 channels.  out must not overlap x."""
     dev = layer.device
     row = _fp8_rows(x, dev, layer.K)
     M = x.size(0)
@@ -970,6 +994,7 @@ def fp8_linear_forward(layer: Fp8Linear, x: torch.Tensor, gelu: bool = False, ou
         out = x.new_empty((M, layer.N)) if out_dtype is None else x.new_empty((M, layer.N), dtype=out_dtype)
     else:
         _need_dense(out, "out", dev, out_dtype or out.dtype, (M, layer.N))
+        _need_apart(out, x, "x")
     if out.dtype not in _DT16:
         raise ValueError(f"out must be bfloat16 or float16, not {out.dtype}")
     if workspace is None:
@@ -1109,7 +1134,7 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_lens:
     length (bf16 or fp16; any strides that are multiples of 8, channels adjacent; Hq a multiple
     of Hkv).  Batch row b sees the states before key_lens[b] (int32 [B]) whose mask[b, t]
     (bool [B, Lk]) is true; what the others hold is not looked at, and a row that sees none gives
-    zeros.  Returns [B, Lq, Hq, D], in `out` if given, which may be a dense q.  scale: 1 / sqrt(D) if not given."""
+    zeros.  Returns [B, Lq, Hq, D], in `out` if given, which may be a dense q and overlaps nothing else.  scale: 1 / sqrt(D) if not given."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     dev = q.device
@@ -1134,6 +1159,10 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_lens:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _need_dense(out, "out", dev, q.dtype, (B, Lq, Hq, D))
+        for t, name in ((k, "k"), (v, "v")):
+            _need_apart(out, t, name)
+        if out.data_ptr() != q.data_ptr() or not q.is_contiguous():
+            _need_apart(out, q, "q")
     if workspace is None:
         workspace = cross_attention_workspace(q, k, mask is not None)
     else:
