@@ -456,7 +456,8 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
  * projections that 4 bits hurt.  A weight is its code times the float32 scale of its 128 x 128
  * block; 128 consecutive channels of a row of X share the smallest power of
  * two s with max |x| <= 448 s (at least 2^-127), and x / s, which is exact, is
- * rounded to e4m3 once, ties to even.  So
+ * rounded to e4m3 once, ties to even.  (A checkpoint whose activations were scaled by max |x| / 448 in
+ * float32 meets slightly different codes here: its scale is up to two times smaller.)  So
  *   Y[m, n] = sum_b sw[n / 128, b] sx[m, b] sum_{k in block b} a[m, k] w[n, k]  (+ bias[n]).
  * Blocks are summed in float32.  Inside a block the matrix instruction adds
  * groups of eight neighbouring channels' products with each cut off below 2^-13 of the group's largest
@@ -558,9 +559,8 @@ svdq_status_t svdq_rotary_apply(const svdq_rotary_t *plan, const void *q, int64_
  * strides multiples of 8 elements, not negative.  D a multiple of 8 up to 256, Hq a
  * multiple of Hkv, B <= 65536, Lk <= 2^30, B Lq Hq <= 2^28,
  * B Hkv <= 2^20, strides of k_token and v_token below 2^24, |scale| < 2^127.
- * Scores, softmax statistics and sums are float32 (scores in units of log2: scale q . k log2(e) has to be
- * in float32's range); the weights p enter the
- * product in the inputs' type, bf16's at most 1 and the largest at least 2^-9, fp16's
+ * Scores, softmax statistics and sums are float32 (scores in units of log2: scale q . k log2(e) has to
+ * be in float32's range); the weights p enter the product in the inputs' type, bf16's at most 1 and the largest at least 2^-9, fp16's
  * at most 2^15 and the largest at least 2^7, so that its lower end is 2^-31 below them.  out is
  * rounded once.  Its sums are finite where Lk times the largest |v| is below 2^127.
  * The result does not depend on the order in which workgroups run.  One kernel, another

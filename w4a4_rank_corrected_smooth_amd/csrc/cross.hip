@@ -551,13 +551,18 @@ __device__ __forceinline__ void attend(Sums<DB, F16> &acc, const v4u (&q)[2 * DB
 }
 
 // Many rows: each of the four wavefronts has 32, and all read the same tiles of
-// KEYS states, two in LDS.  While a 16-bit matrix instruction runs, the SIMD's vector ALU stands nearly
-// still (an instruction and 16 FMAs, from two wavefronts: 31 ns, 14 and 16 alone), so the kernel's time is the sum of
-// both: 16 instructions of 14 ns for 32 x 32 scores of 128 channels, and about 100 ns of maxima, exponentials and
-// conversions.  Ordering the two by hand, the next block's scores between this one's exponentials, was
-// slower than the compiler's order (564 against 539 us at 4096 x 16384, 16 heads).  Workgroups that go on to
+// KEYS states, two in LDS.  A block of 32 x 32 scores of 128 channels is 16 matrix instructions, 512 cycles, 80
+// vector instructions, 16 of them exponentials, and 24 LDS reads, 16 KB.  In registers, two wavefronts to a SIMD
+// and none waiting for another's result, the matrix instructions take 222 ns, with 64 FMAs and 16 exponentials among
+// them 228, and with 16 KB from LDS besides 318; but with 128 and 256 FMAs 305 and 458, so the vector ALU is not
+// free.  The kernel takes 939 cycles a block, 505 ns at the clock it runs at: the matrix core is busy for 55% of
+// them and LDS for 27%.  What the units leave unused goes to each block's own order (products, maximum,
+// exponentials, products), which only two wavefronts of a SIMD cover.  Ordering it by hand, the next block's
+// scores between this one's exponentials, was slower than the compiler's order (564 against 539 us at
+// 4096 x 16384, 16 heads).  Workgroups that go on to
 // the next row tile with its queries asked for ahead were no faster (32760 rows over 512 states, 12 heads: 146 us, this 142),
-// as the registers they need cost more.  4096 x 16384, 16 heads of 128: 520 us, 1.06 PFLOP/s.
+// as the registers they need cost more.  4096 x 16384, 16 heads of 128: 520 us, 1.06 PFLOP/s; of 256 channels
+// 4096 x 4096 268 us, of 160 190.
 template <int DB, int KEYS, bool F16, bool LIST>
 __global__ __launch_bounds__(256, 2) void cross_many_kernel(const CrossArgs a) {
   typedef Rows<DB> L;
@@ -613,8 +618,8 @@ __global__ __launch_bounds__(256, 2) void cross_many_kernel(const CrossArgs a) {
 
 // Many rows over few states: a workgroup keeps all of a key/value head's states in LDS (up to CAP), and its
 // eight wavefronts go through rows by 32, each by itself, without barriers.  2 x 4096 rows over 300 states, 16 heads of
-// 72: 27 us, of which 10 do not grow with the rows (launch, the states' way into LDS, last stores); the rest is
-// bound by the vector ALU as above.  The tiles of four wavefronts take 37.
+// 72: 28 us, of which 10 do not grow with the rows (launch, the states' way into LDS, last stores); the rest is
+// the order of a block's steps as above.  The tiles of four wavefronts take 37.
 template <int DB, int CAP, bool F16, bool LIST>
 __global__ __launch_bounds__(512, 2) void cross_near_kernel(const CrossArgs a) {
   typedef Rows<DB> L;
@@ -667,7 +672,8 @@ __global__ __launch_bounds__(512, 2) void cross_near_kernel(const CrossArgs a) {
 
 // Few rows (up to 32 of a key/value head): the wavefronts (four or eight) take tiles of 32 states of
 // their own, in LDS of their own, without barriers, two tiles in flight, and add up at the end.  Bound by memory
-// (8 x 20 heads of 64 over 1500 states, 61 MB: 15.2 us, 4.0 TB/s with a workgroup on 160 of the CUs).
+// (8 x 20 heads of 64 over 1500 states, 61 MB: 15.6 us, 3.9 TB/s with a workgroup on 160 of the CUs; 32 rows over
+// 20000 states of 8 heads of 128, 82 MB: 26 us with its join; 8 x 20 heads of 72 over 1500, 69 MB: 24).
 template <int DB, int W, bool F16, bool LIST>
 __global__ __launch_bounds__(64 * W, DB > 2 ? 1 : 2) void cross_few_kernel(const CrossArgs a) {
   typedef Rows<DB> L;

@@ -46,7 +46,8 @@ inline CrossPlan cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64
   const int64_t heads = B * Hkv, blocks32 = (p.rows + 31) / 32;
   p.near = !p.own && Lk <= cross_near_states(p.blocks) && heads * blocks32 >= 8 * 256;
   if (p.near) {
-    // a workgroup to a CU, eight blocks of 32 rows to each at least
+    // a workgroup to a CU, eight blocks of 32 rows to each at least (a number of heads that is no part of 256 leaves CUs
+    // idle: 8 x 4096 rows over 77 states of 64 channels take 78 us for 20 heads, 160 workgroups, and 88 for 32, 256)
     p.tiles = heads < 256 ? 256 / heads : 1;
     if (p.tiles > (blocks32 + 7) / 8) p.tiles = (blocks32 + 7) / 8;
   } else {
@@ -61,7 +62,9 @@ inline CrossPlan cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64
   // Few rows of 64 channels or less: eight wavefronts, and no join, where a workgroup to a head nearly fills the CUs
   // (160 heads over 1500 states 15.1 us, two workgroups of four to a CU and a join 16.7; 240 18.6 and 21.5, with a mask
   // 21.5 and 24.5; 256 over 448 7.5 and 11.0; but 80 over 1500 11.9 and 11.4, 320 28.8 and 25.3).  Longer states are
-  // shared out by their lengths.
+  // shared out by their lengths.  From a round of workgroups on states are whole, also where the last round is part
+  // empty (over 16384 states of 128 channels: 4096 rows of 16 heads, 512 workgroups, 520 us; 4500 rows, 576, 762;
+  // 4608 of 24 heads, 864, 973).
   p.wide = p.own && p.blocks == 2 && work > 128 && work <= 256 && Lk <= 2048;
   const int64_t places = p.wide || (p.own && p.blocks > 2) ? 256 : 512;
   if (!p.near && work > 0 && work < places) {

@@ -49,7 +49,7 @@ __device__ __forceinline__ float widen(uint32_t h) {
 // Sixteen channels of a row (zeros past the end) to codes; the eight lanes of a block of 128
 // are neighbours.  With a = max |x| = 1.f 2^(E - 127), 448 = 1.75 2^8: the smallest e
 // with a <= 448 2^e is E - 135, or one more where f > 0.75, and at least -127.
-// x 2^-e is exact (16-bit values, at most 2^-133, times at most 2^127) and at most 448.
+// x 2^-e is exact (16-bit values are multiples of 2^-133, bfloat16's smallest, and 2^-e is 2^127 at most) and at most 448.
 template <bool F16>
 __device__ __forceinline__ uint32_t quantize16(const uint16_t *src, int k, int K, v4u &codes) {
   uint32_t in[8];
@@ -384,8 +384,8 @@ __device__ __forceinline__ void quantize_rows(const Fp8Args &a, uint8_t *xl, uin
 
 // Few rows.  A workgroup has 32 output channels; its eight wavefronts deal out
 // the blocks of K among themselves and add up in LDS.  Weights go from memory
-// straight into operands, AHEAD blocks of a wavefront in flight (one row of 6144 x 4096: 6.9 us, 3.7 TB/s, most of the
-// rest the launch and the rows' quantising; 77 of 2121 x 1160: 8.2 with the quantiser's launch).  OWN: the
+// straight into operands, AHEAD blocks of a wavefront in flight (one row of 6144 x 4096: 7.0 us, 3.7 TB/s, most of the
+// rest the launch and the rows' quantising; 8 rows 10.3, 64 12.9, 96 14.9; 77 of 2121 x 1160: 9.1 with the quantiser's launch).  OWN: the
 // workgroup quantises the rows itself, into LDS (one block of 32 rows, up to 24576 values in all).
 template <int XB, bool OWN, bool F16, int OUT>
 __global__ __launch_bounds__(64 * kFp8RowsWaves) void fp8_rows_kernel(const Fp8Args a) {

@@ -5,8 +5,10 @@
 // A workgroup takes a few tokens.  It first finds the sine and cosine of every
 // (token, pair), each once, in LDS, and then turns all heads of these tokens by them:
 // the float64 angles cost a pair's 40 instructions once for all its heads.
-// Bound by memory: every value is read and written once, 16 bytes a lane (32760 tokens of 24 heads of 128, 403 MB:
-// 80 us, 5.0 TB/s; a plain copy 4.95).  A decode step's launch (8 tokens, 40 heads) takes 3.2 us.
+// Bound by memory where a lane takes 16 bytes: every value is read and written once (32760 tokens of 24 heads of 128,
+// 403 MB: 80 us as neighbours, 82 as halves, 5.0 TB/s; a plain copy 4.95).  Halves whose pairs are no multiple of 8
+// go by 8 bytes (28 pairs of 128 channels, the same rows: 112 us) or, if none of 4, by single channels
+// (18 pairs of 72 channels in 48 heads, 453 MB: 328 us, where a copy takes 92).  A decode step's launch (8 tokens, 40 heads) takes 3.2 us.
 #include <hip/hip_runtime.h>
 
 #include "common.h"
