@@ -554,3 +554,26 @@ def test_attention_of_the_smallest_keys_and_values(S, Q, group):
     q = b.queries(Q, group, 2.0 ** 112)
     announce(f"kv4 attention of the smallest keys, {Q * group} rows")
     check(S.kv4_attention(b.cache, q, b.table, b.seq_lens, scale=2.0 ** 12), q, b, 2.0 ** 12)
+
+
+@pytest.mark.parametrize("scale", [0.0, 3e-39, -1e-38, 6e-38])
+def test_attention_of_smallest_scales_and_large_products(S, scale):
+    """Products of 1e37 at scales that bring them to 0 (equal weights) and to scores below 1."""
+    scale = float(np.float32(scale))
+    r = np.random.default_rng(98)
+    lens, D = [333, 40], 64
+    b = Batch(S, 99, lens, 1, D, 16, "bf16")
+    n = b.pages * 16
+    k = rows(r, (n, 1, D), "bf16")
+    k[..., 3] = torch.from_numpy(r.uniform(-1e18, 1e18, (n, 1))).to(k)
+    v = rows(r, (n, 1, D), "bf16")
+    S.kv4_append(b.cache, k, v, torch.arange(n, dtype=torch.int32, device="cuda"))
+    kv, vv = O.values(f64(k)), O.values(f64(v))
+    t = b.table.cpu().numpy()
+    for s, m in enumerate(lens):
+        at = t[s, np.arange(m) // 16] * 16 + np.arange(m) % 16
+        b.k[s], b.v[s] = kv[at], vv[at]
+    q = b.queries(2, 4)
+    q[..., 3] = 1e19
+    announce(f"kv4 attention of products of 1e37, scale {scale}")
+    check(S.kv4_attention(b.cache, q, b.table, b.seq_lens, scale=scale), q, b, scale)

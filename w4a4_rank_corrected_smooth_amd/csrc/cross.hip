@@ -25,8 +25,6 @@
 // visible ones, so nothing else in the kernel knows of it.
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
-
 #include "common.h"
 #include "cross_layout.h"
 #include "device_util.h"
@@ -933,11 +931,8 @@ svdq_status_t svdq_cross_attention(const void *q, int64_t q_batch, int64_t q_tok
     a.index = index;
     a.count = count;
   }
-  // Maxima are taken of the bare products, so the scale's sign goes to the queries, and a scale of zero becomes
-  // float32's smallest number: it still hides the rows behind the last state, whose product is -inf, and brings no
-  // other product, all below 2^128, above 2^-21.  Subnormal bits are set by hand, as a host's thread may flush them.
-  const double c = fabs((double)scale) * 1.4426950408889634;
-  a.c = c < 0x1p-126 ? __builtin_bit_cast(float, std::max(1u, (uint32_t)(c * 0x1p149 + 0.5))) : (float)c;
+  // Maxima are taken of the bare products, so the scale's sign goes to the queries.
+  a.c = log2_scale(scale);
   a.flip = scale < 0.0f ? 0x80008000u : 0u;
   a.work = (int)(Hkv * p.tiles * (a.line ? a.line + B : B * (int64_t)p.parts));      // at most 2^28 / 128 + 2^20
   // Row tiles of a head that go to one XCD together: up to 32, as far as no XCD gets a sixteenth more

@@ -5,6 +5,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "common.h"
 
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -85,6 +87,14 @@ __device__ __forceinline__ float gelu_tanh_f32(float y) {
 
 // ------------------------------------------------------------ host side
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+// |scale| log2(e), for a softmax whose hidden scores are -inf before they are scaled.  A scale of zero becomes
+// float32's smallest number: -inf stays what it is, and no other product, all below 2^128, gets above 2^-21.
+// Subnormal bits are set by hand, as a host's thread may flush them.
+inline float log2_scale(float scale) {
+  const double c = fabs((double)scale) * 1.4426950408889634;
+  return c < 0x1p-126 ? __builtin_bit_cast(float, std::max(1u, (uint32_t)(c * 0x1p149 + 0.5))) : (float)c;
+}
 
 inline svdq_status_t launch_status(const char *what) {
   const hipError_t e = hipGetLastError();

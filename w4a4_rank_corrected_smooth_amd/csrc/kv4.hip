@@ -1047,9 +1047,8 @@ svdq_status_t svdq_kv4_attention(const svdq_kv4_cache_t *cache, const void *q, i
   a.rows = rows;
   a.row_blocks = row_blocks;
   a.block_rows = rows < block ? rows : block;
-  // Maxima are taken of the bare products, so the scale's sign goes to the
-  // queries, and a scale of zero becomes one that still hides masked scores.
-  a.scale = fmaxf((float)(fabs((double)scale) * 1.4426950408889634), 1e-37f);
+  // Maxima are taken of the bare products, so the scale's sign goes to the queries.
+  a.scale = log2_scale(scale);
   a.flip = scale < 0.0f ? 0x80008000u : 0u;
   a.out = static_cast<uint16_t *>(out);
   a.part = static_cast<float *>(workspace);
