@@ -577,3 +577,38 @@ def test_attention_of_smallest_scales_and_large_products(S, scale):
     q[..., 3] = 1e19
     announce(f"kv4 attention of products of 1e37, scale {scale}")
     check(S.kv4_attention(b.cache, q, b.table, b.seq_lens, scale=scale), q, b, scale)
+
+
+@pytest.mark.parametrize("kind", ["alike", "rising", "negative"])
+@pytest.mark.parametrize("lens,Q,Hq,H,D,page,dtype,power", [
+    ([700, 33], 1, 8, 2, 128, 16, "bf16", 40), ([700, 33], 3, 4, 1, 64, 32, "bf16", 56), ([20000], 1, 8, 1, 128, 256, "bf16", 30),
+    ([300], 1, 32, 2, 256, 64, "fp16", 15), ([1000, 5], 1, 17, 1, 128, 32, "bf16", 20)])
+def test_attention_of_scores_far_from_zero(S, lens, Q, Hq, H, D, page, dtype, power, kind):
+    """Scores of 2^30 to 2^118, where a step of float32 is many units of the exponent: those that are alike weigh the same,
+    and the others, lower by a sixteenth or more, nothing.  All products and their sums are exact."""
+    b = Batch(S, 120, lens, H, D, page, dtype)
+    top = max(power, 30)
+    announce(f"kv4 attention of scores far from zero, {lens} Q={Q} {Hq}/{H} D={D} {dtype} 2^{power} {kind}")
+    q = torch.full((len(lens), Q, Hq, D), 2.0 ** power, dtype=DT[dtype], device="cuda")
+    n = b.pages * page
+    k = torch.zeros(n, H, D, dtype=torch.bfloat16, device="cuda")
+    v = rows(b.r, (n, H, D), "bf16")
+    t = b.table.cpu().numpy()
+    slots = [t[s, np.arange(m) // page] * page + np.arange(m) % page for s, m in enumerate(lens)]
+    steps = {"alike": lambda i: np.full(len(i), 3.0), "rising": lambda i: np.array([0.5, 1, 1.5, 2, 3, 4, 6])[7 * i // len(i)],
+             "negative": lambda i: -np.array([6, 4, 3, 2, 1.5, 1, 0.5])[7 * i // len(i)]}[kind]
+    for at in slots:
+        k[torch.from_numpy(at).long().cuda()] = torch.from_numpy(steps(np.arange(len(at))) * 2.0 ** (top - 2))[:, None, None].to(k)
+    S.kv4_append(b.cache, k, v, torch.arange(n, dtype=torch.int32, device="cuda"))
+    vv = O.values(f64(v))
+    for scale in (0.3, 0.11, 0.71, 0.0625):
+        got = f64(S.kv4_attention(b.cache, q, b.table, b.seq_lens, scale=scale))
+        for s, m in enumerate(lens):
+            for i in range(Q):
+                seen = m - Q + i + 1
+                x = steps(np.arange(m))[:seen]
+                best = vv[slots[s][:seen][x == x.max()]]
+                want, mean = (np.repeat(y.mean(0), Hq // H, 0) for y in (best, np.abs(best)))
+                # the weights are all 1, the sums over them as above, and the result is rounded
+                tol = torch.finfo(DT[dtype]).eps / 2 * np.abs(want) * (1 + 2.0 ** -6) + (2.0 ** -20 + 2 * m * 2.0 ** -24) * mean
+                assert (np.abs(got[s, i] - want) <= tol).all(), (scale, s, i)

@@ -680,14 +680,16 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[x][i][e] *= g;
         }
-        const float ref = m[x] == -__builtin_inff() ? 0.0f : m[x] * a.scale;
+        // Differences are taken of the bare products: of scaled ones a fused product would hold
+        // the rounding of the maximum, many units of the exponent where scores are far from zero.
+        const float ref = m[x] == -__builtin_inff() ? 0.0f : m[x];
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][g][2 * i], a.scale, -ref));
-            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][g][2 * i + 1], a.scale, -ref));
+            const float p0 = __builtin_amdgcn_exp2f((s[x][g][2 * i] - ref) * a.scale);
+            const float p1 = __builtin_amdgcn_exp2f((s[x][g][2 * i + 1] - ref) * a.scale);
             l[x] += p0 + p1;
             const uint32_t pk = pack_bf16(p0, p1);
             hi[2 * g + i] = pk;
@@ -781,7 +783,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
       l[x] += __shfl_xor(l[x], 32);
       const bool mine = !second;
       if (mine && c4 == 0) {
-        sm[w][16 * x + col] = m[x] == -kLargest ? m[x] : m[x] * a.scale;
+        sm[w][16 * x + col] = m[x];
         sl[w][16 * x + col] = l[x];
       }
 #pragma unroll
@@ -802,7 +804,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kv4_waves(D
       const float ref = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        f[k] = __builtin_amdgcn_exp2f(sm[k][c] - ref);
+        f[k] = __builtin_amdgcn_exp2f((sm[k][c] - ref) * a.scale);
         sum = __builtin_fmaf(sl[k][c], f[k], sum);
       }
       const bool done = ch0 == 0 && ch1 == n;
@@ -891,7 +893,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(AttendArgs a) {
 #pragma unroll 4
   for (int p = WIDE ? w : 0; p < pieces; p += STEP) {
     const int64_t at = place(p);
-    const float f = __builtin_amdgcn_exp2f(ml[at * 2] - ref);
+    const float f = __builtin_amdgcn_exp2f((ml[at * 2] - ref) * a.scale);
     l = __builtin_fmaf(ml[at * 2 + 1], f, l);
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = __builtin_fmaf(a.part[at * D + lane * V + e], f, acc[e]);
